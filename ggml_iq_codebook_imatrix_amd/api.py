@@ -1,4 +1,4 @@
-"""Thin Python binding of libiq.so (see include/iq.h).
+"""Thin Python binding of libiq.so (see include/iq.h and include/iq_run.h).
 
 Argument marshalling only: every step runs in the HIP library.  Each wrapper
 checks the shape, dtype and device of every tensor it is given (IQError before
@@ -22,6 +22,7 @@ FMT = {n: i for i, n in enumerate(FORMATS)}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 STATUS_NONFINITE, STATUS_OVERFLOW, STATUS_BADCHOICE, STATUS_BADIMP, STATUS_BADID = 1, 2, 4, 8, 16
+STATUS_ROUNDED = 32  # linear, moe: a codebook value times a multiplier is not exact in fp16
 ERRORS = {-1: "IQ_ERR_FMT", -2: "IQ_ERR_DTYPE", -3: "IQ_ERR_NULL", -4: "IQ_ERR_SHAPE", -5: "IQ_ERR_ARG",
           -6: "IQ_ERR_HIP", -7: "IQ_ERR_WORKSPACE"}
 
@@ -44,6 +45,12 @@ SIGNATURES = {
     "iq_choice_search": ([_I, _P, _I, _I64, _I64, _I64, _P, _P, _P, _F, _P, _P, _P, _SZ, _P, _P], _I),
     "iq_dequantize": ([_I, _P, _I64, _I64, _P, _P, _I, _P], _I),
     "iq_error_string": ([_I], ctypes.c_char_p),
+    # include/iq_run.h
+    "iq_linear_workspace_size": ([_I, _I64, _I64, _I, _I64, _I, _P], _I),
+    "iq_linear": ([_I, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _P, _I, _I, _P, _P, _SZ, _P, _P], _I),
+    "iq_moe_workspace_size": ([_I, _I, _I64, _I64, _I, _I, _I64, _I, _P], _I),
+    "iq_moe": ([_I, _I, _P, _P, _P, _I64, _I64, _I, _P, _P, _P, _I, _I64, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P,
+                _P], _I),
 }
 
 
@@ -457,3 +464,125 @@ def dequantize(fmt, packed: torch.Tensor, grid: torch.Tensor, dtype=torch.float3
                              _ptr(out, "out", dev), DTYPE[out.dtype], _stream())
     _check(rc, "iq_dequantize")
     return out
+
+
+# --------------------------------------------------------------------------
+# Tokens through encoded weights (include/iq_run.h)
+# --------------------------------------------------------------------------
+def linear_workspace_size(fmt, rows: int, cols: int, dtype, T: int, rank: int = 0) -> int:
+    if dtype not in DTYPE:
+        raise IQError(f"unsupported dtype {dtype}")
+    return _size_query("iq_linear_workspace_size", _fmt(fmt), int(rows), int(cols), DTYPE[dtype], int(T), int(rank))
+
+
+def moe_workspace_size(fmt, hidden: int, inter: int, num_experts: int, dtype, T: int, top_k: int,
+                       down_fmt=None) -> int:
+    if dtype not in DTYPE:
+        raise IQError(f"unsupported dtype {dtype}")
+    f = _fmt(fmt)
+    return _size_query("iq_moe_workspace_size", f, f if down_fmt is None else _fmt(down_fmt), int(hidden), int(inter),
+                       int(num_experts), DTYPE[dtype], int(T), int(top_k))
+
+
+def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_a: torch.Tensor | None = None,
+           lora_b: torch.Tensor | None = None, lora_scale: torch.Tensor | None = None,
+           lora_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
+           status: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Tokens x [T, cols] through the encoded weight packed [rows, cols/256, block_bytes] -> [T, rows], of x's dtype.
+    With lora_a [N, r, cols], lora_b [N, rows, r] (x's dtype) and lora_ids [T] int32 (-1: none), token t also gets
+    lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones)."""
+    f = _fmt(fmt)
+    info = format_info(f)
+    _need(packed, "packed", (None, None, info["block_bytes"]), torch.uint8)
+    rows, nb = packed.shape[0], packed.shape[1]
+    cols = nb * 256
+    _need(grid, "grid", (info["grid_size"], 8), torch.float32)
+    _need(x, "x", (None, cols), tuple(DTYPE))
+    T, N, rank = x.shape[0], 0, 0
+    if lora_a is not None:
+        _need(lora_a, "lora_a", (None, None, cols), x.dtype)
+        N, rank = lora_a.shape[0], lora_a.shape[1]
+        if N < 1 or rank < 1:
+            raise IQError("lora_a holds no adapter")
+        _need(lora_b, "lora_b", (N, rows, rank), x.dtype)
+        if lora_scale is not None:
+            _need(lora_scale, "lora_scale", (N,), torch.float32)
+        _need(lora_ids, "lora_ids", (T,), torch.int32)
+    elif lora_b is not None or lora_scale is not None or lora_ids is not None:
+        raise IQError("lora_b, lora_scale and lora_ids need lora_a")
+    if out is not None:
+        _need(out, "out", (T, rows), x.dtype)
+    _status_ok(status)
+    dev = _device_of(x)
+    if out is None:
+        out = torch.empty((T, rows), dtype=x.dtype, device=dev)
+    ws, wp, wn = _workspace(linear_workspace_size(f, rows, cols, x.dtype, T, rank), dev, workspace)
+    rc = lib().iq_linear(f, _ptr(packed, "packed", dev), rows, cols, _ptr(grid, "grid", dev), _ptr(x, "x", dev),
+                         DTYPE[x.dtype], T, _ptr(lora_a, "lora_a", dev), _ptr(lora_b, "lora_b", dev),
+                         _ptr(lora_scale, "lora_scale", dev), _ptr(lora_ids, "lora_ids", dev), N, rank,
+                         _ptr(out, "out", dev), wp, wn, _ptr(status, "status", dev), _stream())
+    _check(rc, "iq_linear")
+    return out
+
+
+def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: torch.Tensor, x: torch.Tensor,
+        num_experts: int, router: torch.Tensor | None = None, top_k: int | None = None, renormalize: bool = True,
+        ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, down_fmt=None,
+        down_grid: torch.Tensor | None = None, out: torch.Tensor | None = None,
+        status: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """A mixture-of-experts layer on encoded experts: gate, up [E*inter, hidden/256, bytes], down
+    [E*hidden, inter/256, bytes] (down_fmt and down_grid where they differ), x [T, hidden].
+    With router [E, hidden] and top_k the layer routes its tokens (ids and weights, where given, are filled);
+    without, ids [T, top_k] int32 and weights [T, top_k] f32 are the caller's.  Returns (y, ids, weights)."""
+    f = _fmt(fmt)
+    fd = f if down_fmt is None else _fmt(down_fmt)
+    info, dinfo = format_info(f), format_info(fd)
+    E = int(num_experts)
+    if E < 1:
+        raise IQError("num_experts must be at least 1")
+    _need(x, "x", (None, None), tuple(DTYPE))
+    T, hidden = x.shape
+    if hidden % 256 or hidden == 0:
+        raise IQError(f"x has {hidden} columns, not a multiple of 256")
+    _need(gate, "gate", (None, hidden // 256, info["block_bytes"]), torch.uint8)
+    if gate.shape[0] % E or gate.shape[0] // E % 256 or gate.shape[0] == 0:
+        raise IQError(f"gate has {gate.shape[0]} rows, not a multiple of 256 for each of {E} experts")
+    inter = gate.shape[0] // E
+    _need(up, "up", tuple(gate.shape), torch.uint8)
+    _need(down, "down", (E * hidden, inter // 256, dinfo["block_bytes"]), torch.uint8)
+    _need(grid, "grid", (info["grid_size"], 8), torch.float32)
+    if down_grid is None:
+        if fd != f and dinfo["grid_size"] != info["grid_size"]:
+            raise IQError("down_grid is needed where down_fmt has another codebook")
+        down_grid = grid
+    else:
+        _need(down_grid, "down_grid", (dinfo["grid_size"], 8), torch.float32)
+    if router is not None:
+        _need(router, "router", (E, hidden), tuple(DTYPE))
+        if top_k is None or not 1 <= int(top_k) <= E:
+            raise IQError("top_k must lie in 1 .. num_experts with a router")
+    elif ids is None or weights is None:
+        raise IQError("either router or ids and weights must be given")
+    k = int(ids.shape[1] if top_k is None and ids is not None and ids.dim() == 2 else top_k or 0)
+    if ids is not None:
+        _need(ids, "ids", (T, k), torch.int32)
+    if weights is not None:
+        _need(weights, "weights", (T, k), torch.float32)
+    if out is not None:
+        _need(out, "out", (T, hidden), x.dtype)
+    _status_ok(status)
+    dev = _device_of(x)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    if out is None:
+        out = torch.empty((T, hidden), dtype=x.dtype, device=dev)
+    ws, wp, wn = _workspace(moe_workspace_size(f, hidden, inter, E, x.dtype, T, k, fd), dev, workspace)
+    rc = lib().iq_moe(f, fd, _ptr(gate, "gate", dev), _ptr(up, "up", dev), _ptr(down, "down", dev), hidden, inter, E,
+                      _ptr(grid, "grid", dev), _ptr(down_grid, "down_grid", dev), _ptr(x, "x", dev), DTYPE[x.dtype],
+                      T, _ptr(router, "router", dev), DTYPE[router.dtype] if router is not None else 0, k,
+                      int(bool(renormalize)), _ptr(ids, "ids", dev), _ptr(weights, "weights", dev),
+                      _ptr(out, "out", dev), wp, wn, _ptr(status, "status", dev), _stream())
+    _check(rc, "iq_moe")
+    return out, ids, weights
