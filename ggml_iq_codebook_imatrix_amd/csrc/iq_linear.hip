@@ -1,0 +1,360 @@
+// iq_linear.hip -- iq_linear: tokens through an encoded projection, with the
+// low-rank adapters of many requests beside it (include/iq_run.h).
+//
+// Two launches.  linear_prep_kernel brings the tokens into fp16 operand order,
+// converts the codebook, and forms the adapters' rank-wide products v = s A x.
+// The second kernel decodes the payload straight into matrix operands, and adds
+// B v to its sums before it stores them.
+
+#include "iq_run.hpp"
+
+namespace iq {
+namespace {
+
+struct Lora {
+  const void *a, *b;
+  const float *scale;
+  const int32_t *ids;
+  int n, rank, rpad;  // rpad: rank rounded up to 32, the width of v
+  float *v;           // [tokens rounded up to 16][rpad]
+};
+
+struct PrepArgs {
+  const void *x;
+  int dtype;
+  int64_t T, cols, nconv;  // nconv: workgroups that convert (two blocks of a tile each)
+  Tokens X;
+  Codebooks books;
+  Lora L;
+  int rtiles;  // tiles of 16 ranks
+  int32_t *status;
+};
+
+// The adapter of lane l < 16's token in tile tt (-1: none, or no such token).
+__device__ __forceinline__ int tile_adapter(const Lora &L, int64_t tt, int64_t T, int lane) {
+  const int64_t t = tt * 16 + lane;
+  if (lane >= 16 || t >= T) return -1;
+  const int a = L.ids[t];
+  return a >= 0 && a < L.n ? a : -1;
+}
+
+// v for the tokens of tile tt that share the adapter of token `slot`, 16 ranks:
+// the tile's 16 tokens (A) by the adapter's 16 rows (B), K split over the eight
+// waves; rows of other tokens are formed as well and dropped.
+__device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int rt, int slot, f32x4 *s_red) {
+  const Lora &L = P.L;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
+  const int mine = tile_adapter(L, tt, P.T, lane);
+  if (threadIdx.x < 16 && slot == 0 && rt == 0) {
+    const int64_t t = tt * 16 + lane;
+    if (t < P.T && mine < 0 && L.ids[t] != -1) raise_status(P.status, ST_BADID);
+  }
+  const int a = __builtin_amdgcn_readlane(mine, slot);
+  const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
+  if (a < 0 || (group & ((1u << slot) - 1u))) return;  // an earlier token's workgroup does it
+  const int64_t t = min(tt * 16 + n, P.T - 1);
+  const int j = min(rt * 16 + n, L.rank - 1);
+  const int64_t xr = t * P.cols + q * 8, ar = (static_cast<int64_t>(a) * L.rank + j) * P.cols + q * 8;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (P.dtype == 1) {
+#pragma unroll 8
+    for (int64_t k = wave * 32; k < P.cols; k += 256) {
+      const bf16x8 xa = ldu<bf16x8>(static_cast<const uint16_t *>(P.x) + xr + k);
+      const bf16x8 ab = ldu<bf16x8>(static_cast<const uint16_t *>(L.a) + ar + k);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, ab, acc, 0, 0, 0);
+    }
+  } else {
+#pragma unroll 4
+    for (int64_t k = wave * 32; k < P.cols; k += 256) {
+      float xa[8], ab[8];
+      load8u(P.x, 0, xr + k, xa);
+      load8u(L.a, 0, ar + k, ab);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xa[i], ab[i], acc, 0, 0, 0);
+    }
+  }
+  const float scale = L.scale ? L.scale[a] : 1.0f;
+  reduce_waves<1, 1>(&acc, s_red, 8, [&](int, int l, const f32x4 &s) {
+    const int jj = rt * 16 + (l & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = (l >> 4) * 4 + i;
+      if ((group >> tok) & 1u) L.v[(tt * 16 + tok) * L.rpad + jj] = jj < L.rank ? s[i] * scale : 0.0f;
+    }
+  });
+}
+
+template <int P>
+__global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
+  __shared__ f32x4 s_red[8 * 64];
+  int64_t w = blockIdx.x;
+  if (w < A.nconv) {
+    const int64_t nb = A.cols >> 8, i = w * 2 + (threadIdx.x >> 8);
+    if (i < nb * A.X.ntile) convert_tile<P>(A.x, A.dtype, A.T, A.cols, A.X, i % nb, i / nb, threadIdx.x & 255);
+    return;
+  }
+  w -= A.nconv;
+  if (w < A.books.wg[0]) {
+    convert_codebook(A.books, static_cast<int>(w));
+    return;
+  }
+  w -= A.books.wg[0];
+  const int slot = static_cast<int>(w & 15);
+  w >>= 4;
+  lora_shrink(A, w / A.rtiles, static_cast<int>(w % A.rtiles), slot, s_red);
+}
+
+// acc[r][c] += B v of the adapters that the tile's tokens name; wave w of nw
+// takes every nw-th adapter of a tile.  fp32 v is the sum of three bf16 values
+// beside a bf16 B (no rounding), and goes through the fp32 cores beside an fp32 B.
+template <int P, int C, int R>
+__device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t T, int64_t rows, int64_t row0,
+                                            int wave, int nw, f32x4 (&acc)[R][C]) {
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  int turn = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int mine = tile_adapter(L, tt0 + c, T, lane);
+    uint32_t todo = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xffffu;
+    while (todo) {
+      const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(todo));
+      const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
+      todo &= ~group;
+      if (turn++ % nw != wave) continue;
+      f32x4 d[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) d[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      // tokens past T or of other adapters: their rows of v may hold anything, and are dropped below
+      const float *v = L.v + (min((tt0 + c) * 16 + n, (T + 15) / 16 * 16 - 1)) * L.rpad;
+      if (P == 1) {
+        for (int j = q * 8; j < L.rpad; j += 32) {
+          float f[8];
+          load8u(v, 0, j, f);
+          bf16x8 part[3];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+              const uint32_t top = __float_as_uint(f[i]) & 0xffff0000u;
+              part[s][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
+              f[i] -= __uint_as_float(top);
+            }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int64_t row = min(row0 + r * 16 + n, rows - 1);
+            const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a) * rows + row) * L.rank;
+            bf16x8 w = {};
+            if (j + 8 <= L.rank) {
+              w = ldu<bf16x8>(b + j);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (j + i < L.rank) w[i] = __builtin_bit_cast(__bf16, b[j + i]);
+            }
+#pragma unroll
+            for (int s = 0; s < 3; ++s) d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[s], w, d[r], 0, 0, 0);
+          }
+        }
+      } else {
+        for (int j = q * 4; j < L.rpad; j += 16) {
+          const f32x4 f = *reinterpret_cast<const f32x4 *>(v + j);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int64_t row = min(row0 + r * 16 + n, rows - 1);
+            const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a) * rows + row) * L.rank;
+            f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (j + i < L.rank) w[i] = b[j + i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[i], w[i], d[r], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((group >> (q * 4 + k)) & 1u)
+#pragma unroll
+          for (int r = 0; r < R; ++r) acc[r][c][k] += d[r][k];
+    }
+  }
+}
+
+struct LinearArgs {
+  const uint8_t *packed;
+  int64_t rows, nb, T;
+  const _Float16 *tab;
+  Tokens X;
+  Lora L;
+  void *y;
+};
+
+// Few tokens: a workgroup takes R row tiles by C token tiles, its waves split
+// the blocks of a row between them and add up through LDS.
+template <int F, int P, int C, int R>
+__global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
+  constexpr int G = R * C < 4 ? R * C : 4;
+  constexpr int kTab = Geo<F>::N, kRed = 8 * G * 64;
+  __shared__ uint4 s_mem[kTab > kRed ? kTab : kRed];
+  load_table<F>(s_mem, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16 * R, tt0 = static_cast<int64_t>(blockIdx.y) * C;
+  const uint8_t *rp[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) rp[r] = A.packed + min(row0 + r * 16 + n, A.rows - 1) * A.nb * Geo<F>::BYTES;
+  const _Float16 *x0[C];
+  int64_t e0[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t t = min((tt0 + c) * 16 + n, A.T - 1);
+    x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
+    e0[c] = min((tt0 + c) * 16 + q * 4, A.X.ntile * 16 - 4);
+  }
+  f32x4 acc[R][C];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  Raw raw[R];
+  if (wave < A.nb) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r] + static_cast<int64_t>(wave) * Geo<F>::BYTES, q);
+  }
+  __syncthreads();
+  for (int64_t b = wave; b < A.nb; b += nw) {
+    Raw next[R];
+    const int64_t bn = min(b + nw, A.nb - 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+    const _Float16 *xp[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
+    f32x4 part[R][C];
+    block_mma<F, P, C, R>(raw, s_mem, xp, part);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + b * A.X.ntile * 16 + e0[c]);
+      const int ex[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int r = 0; r < R; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r] = next[r];
+  }
+  if (A.L.rank) lora_expand<P, C, R>(A.L, tt0, A.T, A.rows, row0, wave, nw, acc);
+  reduce_waves<R * C, G>(&acc[0][0], reinterpret_cast<f32x4 *>(s_mem), nw, [&](int tile, int l, const f32x4 &s) {
+    const int64_t row = row0 + (tile / C) * 16 + (l & 15);
+    if (row >= A.rows) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t t = (tt0 + tile % C) * 16 + (l >> 4) * 4 + k;
+      if (t < A.T) store1(A.y, P == 1, t * A.rows + row, s[k]);
+    }
+  });
+}
+
+struct LinearPlan {
+  TokensPlan x;
+  int rpad;
+  size_t tab, xo, eo, vo, bytes;
+};
+LinearPlan plan_linear(int fmt, int64_t cols, int dtype, int64_t T, int rank) {
+  LinearPlan p;
+  p.x = plan_tokens(T, cols, dtype);
+  p.rpad = (rank + 31) / 32 * 32;
+  p.tab = 0;
+  p.xo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
+  p.eo = p.xo + ws_up(p.x.xbytes);
+  p.vo = p.eo + ws_up(p.x.ebytes);
+  p.bytes = p.vo + ws_up(static_cast<size_t>(p.x.ntile) * 16 * p.rpad * 4) + kWsAlign;
+  return p;
+}
+
+int check_linear(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int rank) {
+  if (run_bad_fmt(fmt)) return IQ_ERR_FMT;
+  if (run_bad_dtype(dtype)) return IQ_ERR_DTYPE;
+  if (rows < 0 || T < 0 || cols <= 0 || cols % 256 != 0) return IQ_ERR_SHAPE;
+  if (rows > (int64_t(1) << 31) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
+  if (rank < 0 || rank > 1024) return IQ_ERR_ARG;
+  const int64_t ntile = (T + 15) / 16;
+  // the preparing launch: conversion, codebook, adapters
+  if (ntile * (cols / 256) / 2 + 8 + ntile * 16 * ((rank + 31) / 32 * 2) >= kMaxWG) return IQ_ERR_SHAPE;
+  if (ntile > 4 * 65535) return IQ_ERR_SHAPE;
+  return IQ_OK;
+}
+
+template <int F, int P, int C, int R>
+void launch_few(const LinearArgs &A, hipStream_t stream) {
+  int nw = 1;  // waves: a power of two, no more than a row has blocks
+  while (nw < 8 && nw < A.nb) nw *= 2;
+  const dim3 grid(static_cast<unsigned>((A.rows + 16 * R - 1) / (16 * R)),
+                  static_cast<unsigned>((A.X.ntile + C - 1) / C));
+  hipLaunchKernelGGL((linear_few_kernel<F, P, C, R>), grid, dim3(64 * nw), 0, stream, A);
+}
+
+template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
+  if (A.X.ntile == 1)
+    launch_few<F, P, 1, 1>(A, stream);
+  else if (A.X.ntile == 2)
+    launch_few<F, P, 2, 2>(A, stream);
+  else
+    launch_few<F, P, 4, 2>(A, stream);
+}
+
+}  // namespace
+}  // namespace iq
+
+extern "C" {
+
+int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int rank, size_t *bytes) {
+  const int rc = iq::check_linear(fmt, rows, cols, dtype, T, rank);
+  if (rc != IQ_OK) return rc;
+  if (!bytes) return IQ_ERR_NULL;
+  *bytes = rows && T ? iq::plan_linear(fmt, cols, dtype, T, rank).bytes : 0;
+  return IQ_OK;
+}
+
+int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const float *grid, const void *x,
+              int dtype, int64_t T, const void *lora_a, const void *lora_b, const float *lora_scale,
+              const int32_t *lora_ids, int num_adapters, int rank, void *y, void *workspace,
+              size_t workspace_bytes, int32_t *status, hipStream_t stream) {
+  using namespace iq;
+  int rc = check_linear(fmt, rows, cols, dtype, T, rank);
+  if (rc != IQ_OK) return rc;
+  const bool empty = rows == 0 || T == 0;
+  if (!grid || (!empty && (!packed || !x || !y || (rank && (!lora_a || !lora_b || !lora_ids))))) return IQ_ERR_NULL;
+  if (rank && num_adapters < 1) return IQ_ERR_ARG;
+  if (empty) return IQ_OK;
+  const LinearPlan P = plan_linear(fmt, cols, dtype, T, rank);
+  if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
+  char *base = ws_base(workspace);
+  _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab);
+  const Tokens X{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile};
+  const Lora L{lora_a, lora_b, lora_scale, lora_ids, num_adapters, rank, P.rpad,
+               reinterpret_cast<float *>(base + P.vo)};
+  PrepArgs A{};
+  A.x = x;
+  A.dtype = dtype;
+  A.T = T;
+  A.cols = cols;
+  A.nconv = (P.x.ntile * (cols / 256) + 1) / 2;
+  A.X = X;
+  A.books = one_codebook(fmt, grid, tab, status);
+  A.L = L;
+  A.rtiles = P.rpad / 16;
+  A.status = status;
+  const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + P.x.ntile * 16 * A.rtiles));
+  if (dtype == IQ_DTYPE_F32)
+    hipLaunchKernelGGL(linear_prep_kernel<2>, wgs, dim3(512), 0, stream, A);
+  else
+    hipLaunchKernelGGL(linear_prep_kernel<1>, wgs, dim3(512), 0, stream, A);
+  if (!run_launched()) return IQ_ERR_HIP;
+  const LinearArgs M{packed, rows, cols / 256, T, tab, X, L, y};
+#define CALL(F) dtype == IQ_DTYPE_F32 ? launch_linear<F, 2>(M, stream) : launch_linear<F, 1>(M, stream)
+  IQ_BY_FMT(fmt, CALL)
+#undef CALL
+  return run_launched() ? IQ_OK : IQ_ERR_HIP;
+}
+
+}  // extern "C"

@@ -239,36 +239,6 @@ __global__ void __launch_bounds__(256) run_prep_kernel(PrepArgs P) {
   store_block(P.X, t, b, lane, v);
 }
 
-// ---------------------------------------------------------------------------
-// Low-rank adapters, first half: v[t][j] = scale * sum_k A[a][j][k] x[t][k], one wave each.
-// ---------------------------------------------------------------------------
-struct LoraArgs {
-  const void *a, *b;
-  const float *scale;
-  const int32_t *ids;
-  int n, rank;
-  float *v;
-};
-
-__global__ void __launch_bounds__(256) lora_shrink_kernel(LoraArgs L, const void *x, int dtype, int64_t T,
-                                                           int64_t cols, int32_t *status) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (i >= T * L.rank) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = i / L.rank, j = i - t * L.rank;
-  const int a = L.ids[t];
-  if (a < 0 || a >= L.n) {
-    if (lane == 0 && a != -1) raise_status(status, ST_BADID);
-    return;
-  }
-  float s = 0.0f;
-  for (int64_t k = lane; k < cols; k += 64)
-    s = fmaf(load1(L.a, dtype, (static_cast<int64_t>(a) * L.rank + j) * cols + k), load1(x, dtype, t * cols + k), s);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
-  if (lane == 0) L.v[i] = s * (L.scale ? L.scale[a] : 1.0f);
-}
-
 template <int F> __device__ __forceinline__ void load_table(uint4 *s_tab, const _Float16 *tab) {
   for (int i = threadIdx.x; i < Geo<F>::N; i += blockDim.x) s_tab[i] = reinterpret_cast<const uint4 *>(tab)[i];
 }
@@ -292,46 +262,6 @@ __device__ __forceinline__ void block_product(const uint8_t *blk, const uint4 *s
   const float d = block_scale<F>(r);
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] += ldexpf(d * part[k], ex[k]);
-}
-
-// One wave: 16 rows by 16 tokens.
-template <int F>
-__global__ void __launch_bounds__(256) linear_kernel(const uint8_t *packed, int64_t rows, int64_t nb,
-                                                      const _Float16 *tab, Tokens X, int64_t T, int dtype, LoraArgs L,
-                                                      void *y) {
-  __shared__ uint4 s_tab[Geo<F>::N];
-  load_table<F>(s_tab, tab);
-  __syncthreads();
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t rt = w / X.ntile, tt = w - rt * X.ntile;
-  if (rt * 16 >= rows) return;
-  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int64_t row = rt * 16 + n;
-  const uint8_t *rowp = packed + min(row, rows - 1) * nb * Geo<F>::BYTES;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t b = 0; b < nb; ++b) {
-    int ex[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) ex[k] = X.ex[b * X.ntile * 16 + tt * 16 + q * 4 + k];
-    block_product<F>(rowp + b * Geo<F>::BYTES, s_tab, X, b, tt, n, q, acc, ex);
-  }
-  if (row >= rows) return;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t t = tt * 16 + q * 4 + k;
-    if (t >= T) break;
-    float s = acc[k];
-    if (L.rank) {
-      const int a = L.ids[t];
-      if (a >= 0 && a < L.n) {
-        float l = 0.0f;
-        for (int j = 0; j < L.rank; ++j)
-          l = fmaf(L.v[t * L.rank + j], load1(L.b, dtype, (static_cast<int64_t>(a) * rows + row) * L.rank + j), l);
-        s += l;
-      }
-    }
-    store1(y, dtype, t * rows + row, s);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -484,21 +414,6 @@ TokensPlan plan_tokens(int64_t T, int64_t cols, int dtype) {
   return p;
 }
 
-struct LinearPlan {
-  TokensPlan x;
-  size_t tab, xo, eo, vo, bytes;
-};
-LinearPlan plan_linear(int fmt, int64_t cols, int dtype, int64_t T, int rank) {
-  LinearPlan p;
-  p.x = plan_tokens(T, cols, dtype);
-  p.tab = 0;
-  p.xo = ws_up(static_cast<size_t>(kGridN[fmt]) * 16);
-  p.eo = p.xo + ws_up(p.x.xbytes);
-  p.vo = p.eo + ws_up(p.x.ebytes);
-  p.bytes = p.vo + ws_up(static_cast<size_t>(T) * rank * 4) + kWsAlign;
-  return p;
-}
-
 struct MoePlan {
   TokensPlan x, h;
   size_t tab, tab2, xo, eo, lo, ho, hxo, heo, bytes;
@@ -521,18 +436,6 @@ MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, in
 
 bool bad_fmt(int f) { return f < 0 || f > 4; }
 bool bad_dtype(int d) { return d != IQ_DTYPE_F32 && d != IQ_DTYPE_BF16; }
-
-int check_linear(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int rank) {
-  if (bad_fmt(fmt)) return IQ_ERR_FMT;
-  if (bad_dtype(dtype)) return IQ_ERR_DTYPE;
-  if (rows < 0 || T < 0 || cols <= 0 || cols % 256 != 0) return IQ_ERR_SHAPE;
-  if (rows > (int64_t(1) << 31) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 31)) return IQ_ERR_SHAPE;
-  if (T * (cols / 256) / 4 >= kMaxGrid - 2 || ((rows + 15) / 16) * ((T + 15) / 16) / 4 >= kMaxGrid)
-    return IQ_ERR_SHAPE;
-  if (rank < 0 || rank > 1024) return IQ_ERR_ARG;
-  if (T * rank / 4 >= kMaxGrid) return IQ_ERR_SHAPE;
-  return IQ_OK;
-}
 
 int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int dtype, int64_t T, int top_k) {
   if (bad_fmt(fmt) || bad_fmt(down_fmt)) return IQ_ERR_FMT;
@@ -588,46 +491,6 @@ int launch_prep(const void *x, int dtype, int64_t T, int64_t cols, const Tokens 
 }  // namespace iq
 
 extern "C" {
-
-int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int rank, size_t *bytes) {
-  const int rc = iq::check_linear(fmt, rows, cols, dtype, T, rank);
-  if (rc != IQ_OK) return rc;
-  if (!bytes) return IQ_ERR_NULL;
-  *bytes = rows && T ? iq::plan_linear(fmt, cols, dtype, T, rank).bytes : 0;
-  return IQ_OK;
-}
-
-int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const float *grid, const void *x,
-              int dtype, int64_t T, const void *lora_a, const void *lora_b, const float *lora_scale,
-              const int32_t *lora_ids, int num_adapters, int rank, void *y, void *workspace,
-              size_t workspace_bytes, int32_t *status, hipStream_t stream) {
-  using namespace iq;
-  int rc = check_linear(fmt, rows, cols, dtype, T, rank);
-  if (rc != IQ_OK) return rc;
-  const bool empty = rows == 0 || T == 0;
-  if (!grid || (!empty && (!packed || !x || !y || (rank && (!lora_a || !lora_b || !lora_ids))))) return IQ_ERR_NULL;
-  if (rank && num_adapters < 1) return IQ_ERR_ARG;
-  if (empty) return IQ_OK;
-  const LinearPlan P = plan_linear(fmt, cols, dtype, T, rank);
-  if ((rc = check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
-  char *base = ws_base(workspace);
-  _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab);
-  const Tokens X{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile,
-                 P.x.parts};
-  const LoraArgs L{lora_a, lora_b, lora_scale, lora_ids, num_adapters, rank, reinterpret_cast<float *>(base + P.vo)};
-  if ((rc = launch_prep(x, dtype, T, cols, X, grid, tab, fmt, nullptr, nullptr, 0, status, stream)) != IQ_OK)
-    return rc;
-  if (rank) {
-    hipLaunchKernelGGL(lora_shrink_kernel, waves4(T * rank), dim3(256), 0, stream, L, x, dtype, T, cols, status);
-    if (!launched_ok()) return IQ_ERR_HIP;
-  }
-#define CALL(F)                                                                                                  \
-  hipLaunchKernelGGL(linear_kernel<F>, waves4(((rows + 15) / 16) * X.ntile), dim3(256), 0, stream, packed, rows, \
-                     cols / 256, tab, X, T, dtype, L, y)
-  IQ_BY_FMT(fmt, CALL)
-#undef CALL
-  return launched_ok() ? IQ_OK : IQ_ERR_HIP;
-}
 
 int iq_moe_workspace_size(int fmt, int down_fmt, int64_t hidden, int64_t inter, int num_experts, int dtype,
                           int64_t T, int top_k, size_t *bytes) {

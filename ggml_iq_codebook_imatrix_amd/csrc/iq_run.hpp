@@ -1,0 +1,364 @@
+// iq_run.hpp -- what iq_linear (iq_linear.hip) and iq_moe (iq_moe.hip) share:
+// payload fields to fp16 matrix operands, tokens in operand order, and the
+// products of one 256-column block.  Declared in include/iq_run.h.
+//
+// A weight is d * m * v: d the block's fp16 scale, m the group's odd multiplier,
+// v its signed codebook value.  The products run on the fp16 matrix cores:
+// m * v is formed in packed fp16 (exact for the layouts' codebooks: at most 11
+// bits), d and the tokens' power-of-two block scales are applied in fp32 to
+// each 256-column block's sum.
+//
+// Operand layout (v_mfma_f32_16x16x32_f16): the weights are B, lane l holding
+// eight consecutive k of row n = l % 16; the tokens are A, lane l holding the
+// same k of token m = l % 16; D has lane l hold row n = l % 16 and tokens
+// 4 (l / 16) + 0..3, so a block's d, known to the lane that decodes row n,
+// scales that lane's own sums.  The order of k is free as long as both operands
+// use it: lane quarter q = l / 16 takes the block's 64 columns from 64 q on,
+// eight at a step, so that a lane's share of the payload is contiguous (two or
+// three wide loads a block) and a step's eight values are one codebook entry.
+#pragma once
+
+#include "iq_common.hpp"
+#include "iq_internal.hpp"
+#include "iq_run.h"
+
+namespace iq {
+
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int ST_ROUNDED = IQ_STATUS_ROUNDED;
+constexpr int kCodebook[5] = {256, 512, 1024, 2048, 2048};
+constexpr int64_t kMaxWG = (int64_t(1) << 31) - 1;  // workgroups in one grid dimension
+
+inline bool run_launched() { return hipGetLastError() == hipSuccess; }
+inline bool run_bad_fmt(int f) { return f < 0 || f > 4; }
+inline bool run_bad_dtype(int d) { return d != IQ_DTYPE_F32 && d != IQ_DTYPE_BF16; }
+inline int run_check_ws(size_t need, const void *ws, size_t have) {
+  if (!ws) return IQ_ERR_NULL;
+  return have < need ? IQ_ERR_WORKSPACE : IQ_OK;
+}
+
+// Tokens in fp16: x16 [block][tile of 16 tokens][part][step 0..7][lane][8], the
+// A operand of a step as 1 KiB of consecutive memory; ex [block][tokens]: the
+// power of two that undoes the block's scaling.  What lies past the last token
+// is left unwritten and not read.
+struct Tokens {
+  _Float16 *x16;
+  int32_t *ex;
+  int64_t ntile;  // tiles of 16 tokens
+};
+struct TokensPlan {
+  int64_t ntile;
+  int parts;
+  size_t xbytes, ebytes;
+};
+inline TokensPlan plan_tokens(int64_t T, int64_t cols, int dtype) {
+  TokensPlan p;
+  p.ntile = (T + 15) / 16;
+  p.parts = dtype == IQ_DTYPE_F32 ? 2 : 1;
+  p.xbytes = static_cast<size_t>(cols / 256) * p.ntile * p.parts * 8192;
+  p.ebytes = static_cast<size_t>(cols / 256) * p.ntile * 64;
+  return p;
+}
+
+// Codebooks to convert: up to two, 512 entries a workgroup of 512 threads.
+struct Codebooks {
+  const float *grid[2];
+  _Float16 *tab[2];
+  int n[2], iq1[2], wg[2];
+  int32_t *status;
+};
+inline Codebooks one_codebook(int fmt, const float *grid, _Float16 *tab, int32_t *status) {
+  Codebooks c{};
+  c.grid[0] = grid;
+  c.tab[0] = tab;
+  c.n[0] = kCodebook[fmt];
+  c.iq1[0] = fmt >= IQ1_S;
+  c.wg[0] = (kCodebook[fmt] + 511) / 512;
+  c.status = status;
+  return c;
+}
+
+#define IQ_BY_FMT(fmt, CALL)            \
+  switch (fmt) {                        \
+    case IQ2_XXS: CALL(IQ2_XXS); break; \
+    case IQ2_XS: CALL(IQ2_XS); break;   \
+    case IQ2_S: CALL(IQ2_S); break;     \
+    case IQ1_S: CALL(IQ1_S); break;     \
+    default: CALL(IQ1_M); break;        \
+  }
+
+#ifdef __HIPCC__
+
+template <class V> __device__ __forceinline__ V ldu(const void *p) {  // any alignment
+  V v;
+  __builtin_memcpy(&v, p, sizeof(V));
+  return v;
+}
+
+__device__ __forceinline__ float load1(const void *x, int dtype, int64_t i) {
+  return dtype == 1 ? bf16_to_f32(static_cast<const uint16_t *>(x)[i]) : static_cast<const float *>(x)[i];
+}
+__device__ __forceinline__ void store1(void *y, int dtype, int64_t i, float v) {
+  if (dtype == 1)
+    static_cast<uint16_t *>(y)[i] = f32_to_bf16(v);
+  else
+    static_cast<float *>(y)[i] = v;
+}
+
+// Eight consecutive values from any address.
+__device__ __forceinline__ void load8u(const void *base, int dtype, int64_t idx, float v[8]) {
+  if (dtype == 1) {
+    const uint4 u = ldu<uint4>(static_cast<const uint16_t *>(base) + idx);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = ldu<float4>(static_cast<const float *>(base) + idx);
+    const float4 b = ldu<float4>(static_cast<const float *>(base) + idx + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Payload fields
+// ---------------------------------------------------------------------------
+// One lane's share of a block: the fields of groups 8q .. 8q + 7.
+struct Raw {
+  uint32_t a[4];
+  uint32_t s;
+  uint32_t d16;
+};
+
+template <int F> __device__ __forceinline__ Raw load_raw(const uint8_t *blk, int q) {
+  Raw r;
+  if (F == IQ2_XXS || F == IQ2_XS) {
+    const uint4 v = ldu<uint4>(blk + 2 + 16 * q);
+    r.a[0] = v.x; r.a[1] = v.y; r.a[2] = v.z; r.a[3] = v.w;
+    r.s = F == IQ2_XS ? ldu<uint16_t>(blk + 66 + 2 * q) : 0;
+    r.d16 = ldu<uint16_t>(blk);
+  } else if (F == IQ2_S) {
+    const uint2 k = ldu<uint2>(blk + 2 + 8 * q), m = ldu<uint2>(blk + 34 + 8 * q);
+    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = m.x; r.a[3] = m.y;
+    r.s = ldu<uint16_t>(blk + 66 + 2 * q) | (static_cast<uint32_t>(ldu<uint16_t>(blk + 74 + 2 * q)) << 16);
+    r.d16 = ldu<uint16_t>(blk);
+  } else if (F == IQ1_S) {
+    const uint2 k = ldu<uint2>(blk + 2 + 8 * q);
+    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = ldu<uint32_t>(blk + 34 + 4 * q);
+    r.a[3] = r.s = 0;
+    r.d16 = ldu<uint16_t>(blk);
+  } else {
+    const uint2 k = ldu<uint2>(blk + 8 * q), w = ldu<uint2>(blk + 48);
+    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = ldu<uint32_t>(blk + 32 + 4 * q);
+    r.a[3] = 0;
+    r.s = ((q & 2) ? w.y : w.x) >> ((q & 1) * 16);  // scale word q
+    r.d16 = ((w.x >> 12) & 15u) | ((w.x >> 28) << 4) | (((w.y >> 12) & 15u) << 8) | ((w.y >> 28) << 12);
+  }
+  return r;
+}
+
+template <int F> __device__ __forceinline__ float block_scale(const Raw &r) {
+  const float d = f16_bits_to_f32(static_cast<uint16_t>(r.d16));
+  return Geo<F>::IQ1 ? d : d * 0.125f;  // exact: a power of two
+}
+
+// m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16).
+template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab) {
+  uint32_t k, ls, mask = 0, h = 0;
+  if (F == IQ2_XXS) {
+    const uint32_t word = r.a[2 * (i >> 2) + 1];
+    k = (r.a[2 * (i >> 2)] >> (8 * (i & 3))) & 255u;
+    mask = (word >> (7 * (i & 3))) & 127u;
+    ls = word >> 28;
+  } else if (F == IQ2_XS) {
+    const uint32_t v = r.a[i >> 1] >> (16 * (i & 1));
+    k = v & 511u;
+    mask = (v >> 9) & 127u;
+    ls = (r.s >> (4 * (i >> 1))) & 15u;
+  } else if (F == IQ2_S) {
+    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((r.s >> (2 * i)) & 3u) << 8);
+    mask = (r.a[2 + (i >> 2)] >> (8 * (i & 3))) & 255u;
+    ls = (r.s >> (16 + 4 * (i >> 1))) & 15u;
+  } else if (F == IQ1_S) {
+    const uint32_t w = r.a[2] >> (16 * (i >> 2));
+    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((w >> (3 * (i & 3))) & 7u) << 8);
+    ls = (w >> 12) & 7u;
+    h = (w >> 15) & 1u;
+  } else {
+    const uint32_t nib = r.a[2] >> (4 * i);
+    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | ((nib & 7u) << 8);
+    h = (nib >> 3) & 1u;
+    ls = (r.s >> (3 * (i >> 1))) & 7u;
+  }
+  const uint4 e = tab[k];
+  const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * ls + 1));
+  const half2v m2 = {m, m};
+  uint32_t o[4] = {e.x, e.y, e.z, e.w};
+  if (Geo<F>::IQ1) {
+    const half2v up = m2 * static_cast<_Float16>(0.125f);
+    const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (h * 0x80008000u));
+#pragma unroll
+    for (int p = 0; p < 4; ++p)  // m g + m delta, rounded once
+      o[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
+  } else {
+    // The eighth sign is the parity of the seven (IQ2_S holds it).  Bit 2p of
+    // the mask to 2p and bit 2p + 1 to 2p + 16, so that one shift brings a
+    // pair's signs home; what else the two shifts leave behind is masked there.
+    if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
+    uint32_t sp = mask | (mask << 15);
+    asm("" : "+v"(sp));  // keeps shifts from being merged into multiplications by constants (a quarter of the rate)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
+      o[p] = __builtin_bit_cast(uint32_t, v) ^ ((sp << (15 - 2 * p)) & 0x80008000u);
+    }
+  }
+  return __builtin_bit_cast(half8v, make_uint4(o[0], o[1], o[2], o[3]));
+}
+
+template <int F> __device__ __forceinline__ void load_table(uint4 *s_tab, const _Float16 *tab) {
+  for (int i = threadIdx.x; i < Geo<F>::N; i += blockDim.x) s_tab[i] = reinterpret_cast<const uint4 *>(tab)[i];
+}
+
+// part[r][c] = one block of R row tiles by C token tiles; xp[c]: the lane's
+// share of the block's token operand (P parts: fp32 tokens are the sum of two).
+template <int F, int P, int C, int R>
+__device__ __forceinline__ void block_mma(const Raw (&raw)[R], const uint4 *tab, const _Float16 *const (&xp)[C],
+                                          f32x4 (&part)[R][C]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    half8v x[C][P];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int p = 0; p < P; ++p) x[c][p] = *reinterpret_cast<const half8v *>(xp[c] + p * 4096 + i * 512);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const half8v w = group_half8<F>(raw[r], i, tab);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          part[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[c][p], w, part[r][c], 0, 0, 0);
+    }
+  }
+}
+
+// acc += 2^ex * d * part
+__device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d, const int ex[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] += ldexpf(d * part[k], ex[k]);
+}
+
+// ---------------------------------------------------------------------------
+// Tokens to fp16
+// ---------------------------------------------------------------------------
+// The exponent field of the largest finite magnitude seen so far (at least 1).
+__device__ __forceinline__ uint32_t max_exponent(uint32_t e, float v) {
+  const uint32_t u = (__float_as_uint(v) >> 23) & 255u;
+  return max(e, u == 255u ? 1u : u);
+}
+// 2^n with n = 141 - e brings that magnitude under 2^15; infinities and NaN pass
+__device__ __forceinline__ void to_parts(float v, int n, _Float16 &hi, _Float16 &lo) {
+  const float f = ldexpf(v, n);
+  hi = static_cast<_Float16>(f);
+  lo = finite_f(f) ? static_cast<_Float16>(f - static_cast<float>(hi)) : static_cast<_Float16>(0.0f);
+}
+
+// 256 threads convert one block of one tile of 16 tokens: thread = (token,
+// sixteenth of the block), so that 16 neighbouring lanes hold one token.
+template <int P>
+__device__ __forceinline__ void convert_tile(const void *x, int dtype, int64_t T, int64_t cols, const Tokens &X,
+                                             int64_t b, int64_t tile, int tid) {
+  const int tok = tid >> 4, c = tid & 15;
+  const int64_t t = tile * 16 + tok;
+  if (t >= T) return;  // whole groups of 16 lanes
+  float v[16];
+  load8u(x, dtype, t * cols + b * 256 + c * 16, v);
+  load8u(x, dtype, t * cols + b * 256 + c * 16 + 8, v + 8);
+  uint32_t e = 1;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) e = max_exponent(e, v[j]);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) e = max(e, static_cast<uint32_t>(__shfl_xor(static_cast<int>(e), o, 64)));
+  const int n = 141 - static_cast<int>(e);
+  _Float16 *p = X.x16 + (b * X.ntile + tile) * P * 4096;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {  // group 2c + g of the block: quarter c / 4, step 2 (c % 4) + g
+    half8v hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      _Float16 a, b2;
+      to_parts(v[8 * g + j], n, a, b2);
+      hi[j] = a;
+      lo[j] = b2;
+    }
+    const int at = ((2 * (c & 3) + g) * 64 + (c >> 2) * 16 + tok) * 8;
+    *reinterpret_cast<half8v *>(p + at) = hi;
+    if (P == 2) *reinterpret_cast<half8v *>(p + 4096 + at) = lo;
+  }
+  if (c == 0) X.ex[b * X.ntile * 16 + t] = -n;
+}
+
+// One codebook entry per thread.  Every product with a multiplier is exact in
+// fp16 if that with the largest is: products of odd numbers are odd, so the
+// largest has the most bits.
+__device__ __forceinline__ void convert_codebook(const Codebooks &B, int wg) {
+  const int which = wg >= B.wg[0] ? 1 : 0;
+  const int i = (which ? wg - B.wg[0] : wg) * 512 + static_cast<int>(threadIdx.x);
+  if (i >= B.n[which]) return;
+  float g[8];
+  load8u(B.grid[which], 0, static_cast<int64_t>(i) * 8, g);
+  half8v o;
+  bool inexact = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const auto check = [&](float f) { inexact |= static_cast<float>(static_cast<_Float16>(f)) != f; };
+    o[j] = static_cast<_Float16>(g[j]);
+    check(g[j]);
+    if (B.iq1[which]) {
+      check(15.0f * (g[j] + 0.125f));
+      check(15.0f * (g[j] - 0.125f));
+    } else {
+      check(31.0f * g[j]);
+    }
+  }
+  reinterpret_cast<half8v *>(B.tab[which])[i] = o;
+  if (inexact) raise_status(B.status, ST_ROUNDED);
+}
+
+// ---------------------------------------------------------------------------
+// Sum of the waves' accumulators through LDS, in wave order, G tiles at a time;
+// then f(tile, lane, sum) on one thread per lane.  red: nw * G * 64 f32x4.
+// ---------------------------------------------------------------------------
+template <int N, int G, class Fn>
+__device__ __forceinline__ void reduce_waves(const f32x4 *acc, f32x4 *red, int nw, Fn f) {
+  const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
+#pragma unroll
+  for (int g = 0; g < N; g += G) {
+    __syncthreads();  // the table (first) or the sums before (later) are no longer read
+#pragma unroll
+    for (int j = 0; j < G; ++j) red[(wave * G + j) * 64 + lane] = acc[g + j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * 64; i += blockDim.x) {
+      f32x4 s = red[i];
+      for (int w = 1; w < nw; ++w) s += red[w * G * 64 + i];
+      f(g + (i >> 6), i & 63, s);
+    }
+  }
+}
+
+#endif  // __HIPCC__
+
+}  // namespace iq

@@ -80,11 +80,14 @@ def exact_linear(orc, fmt, rows, nb, T, N, r, seed):
     b = g.integers(-2, 3, (N, rows, r)).astype(np.float32)
     scale = 2.0 ** g.integers(-2, 3, N).astype(np.float32)
     ids = g.integers(-1, max(N, 1), T).astype(np.int32)
-    y = x.astype(np.float64) @ decoded(orc, fmt, p, grid).T
+    w = decoded(orc, fmt, p, grid)
+    y, size = x.astype(np.float64) @ w.T, np.abs(x).astype(np.float64) @ np.abs(w).T
     for n in range(N):
         at = ids == n
-        y[at] += scale[n] * ((x[at].astype(np.float64) @ a[n].T) @ b[n].T)
-    return grid, p, x, a, b, scale.astype(np.float32), ids, y
+        more = scale[n] * ((x[at].astype(np.float64) @ a[n].T) @ b[n].T)
+        y[at] += more
+        size[at] += np.abs(more)
+    return grid, p, x, a, b, scale.astype(np.float32), ids, y, size
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -92,13 +95,19 @@ def exact_linear(orc, fmt, rows, nb, T, N, r, seed):
 def test_linear_exact(api, orc, fmt, dtype):
     for i, (rows, nb, T, N, r) in enumerate(SHAPES):
         print("[case] linear exact", fmt, dtype, rows, nb, T, N, r, flush=True)
-        grid, p, x, a, b, scale, ids, y = exact_linear(orc, fmt, rows, nb, T, N, r, 20 + i)
-        # every partial sum is a multiple of 2^-13 below 2^11, so float32 holds each exactly
+        grid, p, x, a, b, scale, ids, y, size = exact_linear(orc, fmt, rows, nb, T, N, r, 20 + i)
+        # Weights are multiples of 2^-11, adapters' products of 2^-2.  `size`, the sum of |x w| and of the adapter's
+        # product, bounds every partial sum: below 2^13 a float32 holds each exactly.  Above it (adapters reach 2^14)
+        # the at most 10 additions of 8 waves' sums and the adapter's product round by 2^-24 of at most `size` each.
         lora = dict(lora_a=dev(a, dtype), lora_b=dev(b, dtype), lora_scale=dev(scale), lora_ids=dev(ids)) if N else {}
         st = api.new_status()
         got = api.linear(fmt, dev(p), dev(grid), dev(x, dtype), status=st, **lora)
         assert got.dtype == dtype and got.shape == (T, rows)
-        assert np.array_equal(f64(got), round_to(y, dtype)), (rows, nb, T, N, r)
+        sure = size < 2.0 ** 13
+        assert sure.mean() > 0.5
+        assert np.array_equal(f64(got)[sure], round_to(y, dtype)[sure]), (rows, nb, T, N, r)
+        near = np.abs(f64(got) - y) <= 10 * U * size + np.abs(y) * (2.0 ** -8 if dtype == torch.bfloat16 else U)
+        assert near.all(), (rows, nb, T, N, r)
         assert api.read_status(st) == 0
 
 
