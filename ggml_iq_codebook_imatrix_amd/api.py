@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -467,12 +468,46 @@ def dequantize(fmt, packed: torch.Tensor, grid: torch.Tensor, dtype=torch.float3
 
 
 # --------------------------------------------------------------------------
-# Tokens through encoded weights (include/iq_run.h)
+# Tokens through encoded weights (include/iq_run.h).  These calls sit in serving
+# loops, where a launch takes microseconds: the checks below compare whole
+# shapes first and spell out what is wrong only when something is, and the
+# answers of the (pure) size and format queries are kept.
 # --------------------------------------------------------------------------
+@functools.lru_cache(maxsize=None)
+def _geometry(f: int):
+    info = format_info(f)
+    return info["grid_size"], info["block_bytes"]
+
+
+@functools.lru_cache(maxsize=4096)
+def _run_size(fn: str, *args) -> int:
+    return _size_query(fn, *args)
+
+
+def _is(t, name: str, shape, dtype):
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype:
+        _need(t, name, shape, dtype)
+
+
+def _addr(t, name: str, device):
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous():
+        _ptr(t, name, device)
+    return t.data_ptr()
+
+
+def _scratch(nbytes: int, device, workspace):
+    if workspace is None and nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    return _workspace(nbytes, device, workspace)
+
+
 def linear_workspace_size(fmt, rows: int, cols: int, dtype, T: int, rank: int = 0) -> int:
     if dtype not in DTYPE:
         raise IQError(f"unsupported dtype {dtype}")
-    return _size_query("iq_linear_workspace_size", _fmt(fmt), int(rows), int(cols), DTYPE[dtype], int(T), int(rank))
+    return _run_size("iq_linear_workspace_size", _fmt(fmt), int(rows), int(cols), DTYPE[dtype], int(T), int(rank))
 
 
 def moe_workspace_size(fmt, hidden: int, inter: int, num_experts: int, dtype, T: int, top_k: int,
@@ -480,8 +515,8 @@ def moe_workspace_size(fmt, hidden: int, inter: int, num_experts: int, dtype, T:
     if dtype not in DTYPE:
         raise IQError(f"unsupported dtype {dtype}")
     f = _fmt(fmt)
-    return _size_query("iq_moe_workspace_size", f, f if down_fmt is None else _fmt(down_fmt), int(hidden), int(inter),
-                       int(num_experts), DTYPE[dtype], int(T), int(top_k))
+    return _run_size("iq_moe_workspace_size", f, f if down_fmt is None else _fmt(down_fmt), int(hidden), int(inter),
+                     int(num_experts), DTYPE[dtype], int(T), int(top_k))
 
 
 def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_a: torch.Tensor | None = None,
@@ -492,36 +527,41 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
     With lora_a [N, r, cols], lora_b [N, rows, r] (x's dtype) and lora_ids [T] int32 (-1: none), token t also gets
     lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones)."""
     f = _fmt(fmt)
-    info = format_info(f)
-    _need(packed, "packed", (None, None, info["block_bytes"]), torch.uint8)
-    rows, nb = packed.shape[0], packed.shape[1]
+    entries, nbytes = _geometry(f)
+    _need(packed, "packed", (None, None, nbytes), torch.uint8)
+    rows, nb, _ = packed.shape
     cols = nb * 256
-    _need(grid, "grid", (info["grid_size"], 8), torch.float32)
+    _is(grid, "grid", (entries, 8), torch.float32)
     _need(x, "x", (None, cols), tuple(DTYPE))
-    T, N, rank = x.shape[0], 0, 0
+    T, dtype = x.shape[0], x.dtype
+    N = rank = 0
     if lora_a is not None:
-        _need(lora_a, "lora_a", (None, None, cols), x.dtype)
-        N, rank = lora_a.shape[0], lora_a.shape[1]
+        _need(lora_a, "lora_a", (None, None, cols), dtype)
+        N, rank, _ = lora_a.shape
         if N < 1 or rank < 1:
             raise IQError("lora_a holds no adapter")
-        _need(lora_b, "lora_b", (N, rows, rank), x.dtype)
+        _is(lora_b, "lora_b", (N, rows, rank), dtype)
         if lora_scale is not None:
-            _need(lora_scale, "lora_scale", (N,), torch.float32)
-        _need(lora_ids, "lora_ids", (T,), torch.int32)
+            _is(lora_scale, "lora_scale", (N,), torch.float32)
+        _is(lora_ids, "lora_ids", (T,), torch.int32)
     elif lora_b is not None or lora_scale is not None or lora_ids is not None:
         raise IQError("lora_b, lora_scale and lora_ids need lora_a")
     if out is not None:
-        _need(out, "out", (T, rows), x.dtype)
-    _status_ok(status)
+        _is(out, "out", (T, rows), dtype)
+    if status is not None:
+        _status_ok(status)
     dev = _device_of(x)
     if out is None:
-        out = torch.empty((T, rows), dtype=x.dtype, device=dev)
-    ws, wp, wn = _workspace(linear_workspace_size(f, rows, cols, x.dtype, T, rank), dev, workspace)
-    rc = lib().iq_linear(f, _ptr(packed, "packed", dev), rows, cols, _ptr(grid, "grid", dev), _ptr(x, "x", dev),
-                         DTYPE[x.dtype], T, _ptr(lora_a, "lora_a", dev), _ptr(lora_b, "lora_b", dev),
-                         _ptr(lora_scale, "lora_scale", dev), _ptr(lora_ids, "lora_ids", dev), N, rank,
-                         _ptr(out, "out", dev), wp, wn, _ptr(status, "status", dev), _stream())
-    _check(rc, "iq_linear")
+        out = torch.empty((T, rows), dtype=dtype, device=dev)
+    dt = DTYPE[dtype]
+    ws, wp, wn = _scratch(_run_size("iq_linear_workspace_size", f, rows, cols, dt, T, rank), dev, workspace)
+    rc = lib().iq_linear(f, _addr(packed, "packed", dev), rows, cols, _addr(grid, "grid", dev), _addr(x, "x", dev),
+                         dt, T, _addr(lora_a, "lora_a", dev), _addr(lora_b, "lora_b", dev),
+                         _addr(lora_scale, "lora_scale", dev), _addr(lora_ids, "lora_ids", dev), N, rank,
+                         _addr(out, "out", dev), wp, wn, _addr(status, "status", dev),
+                         torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "iq_linear")
     return out
 
 
@@ -536,27 +576,27 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     without, ids [T, top_k] int32 and weights [T, top_k] f32 are the caller's.  Returns (y, ids, weights)."""
     f = _fmt(fmt)
     fd = f if down_fmt is None else _fmt(down_fmt)
-    info, dinfo = format_info(f), format_info(fd)
+    (entries, nbytes), (dentries, dbytes) = _geometry(f), _geometry(fd)
     E = int(num_experts)
     if E < 1:
         raise IQError("num_experts must be at least 1")
     _need(x, "x", (None, None), tuple(DTYPE))
-    T, hidden = x.shape
+    (T, hidden), dtype = x.shape, x.dtype
     if hidden % 256 or hidden == 0:
         raise IQError(f"x has {hidden} columns, not a multiple of 256")
-    _need(gate, "gate", (None, hidden // 256, info["block_bytes"]), torch.uint8)
+    _need(gate, "gate", (None, hidden // 256, nbytes), torch.uint8)
     if gate.shape[0] % E or gate.shape[0] // E % 256 or gate.shape[0] == 0:
         raise IQError(f"gate has {gate.shape[0]} rows, not a multiple of 256 for each of {E} experts")
     inter = gate.shape[0] // E
-    _need(up, "up", tuple(gate.shape), torch.uint8)
-    _need(down, "down", (E * hidden, inter // 256, dinfo["block_bytes"]), torch.uint8)
-    _need(grid, "grid", (info["grid_size"], 8), torch.float32)
+    _is(up, "up", (E * inter, hidden // 256, nbytes), torch.uint8)
+    _is(down, "down", (E * hidden, inter // 256, dbytes), torch.uint8)
+    _is(grid, "grid", (entries, 8), torch.float32)
     if down_grid is None:
-        if fd != f and dinfo["grid_size"] != info["grid_size"]:
+        if fd != f and dentries != entries:
             raise IQError("down_grid is needed where down_fmt has another codebook")
         down_grid = grid
     else:
-        _need(down_grid, "down_grid", (dinfo["grid_size"], 8), torch.float32)
+        _is(down_grid, "down_grid", (dentries, 8), torch.float32)
     if router is not None:
         _need(router, "router", (E, hidden), tuple(DTYPE))
         if top_k is None or not 1 <= int(top_k) <= E:
@@ -565,24 +605,28 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
         raise IQError("either router or ids and weights must be given")
     k = int(ids.shape[1] if top_k is None and ids is not None and ids.dim() == 2 else top_k or 0)
     if ids is not None:
-        _need(ids, "ids", (T, k), torch.int32)
+        _is(ids, "ids", (T, k), torch.int32)
     if weights is not None:
-        _need(weights, "weights", (T, k), torch.float32)
+        _is(weights, "weights", (T, k), torch.float32)
     if out is not None:
-        _need(out, "out", (T, hidden), x.dtype)
-    _status_ok(status)
+        _is(out, "out", (T, hidden), dtype)
+    if status is not None:
+        _status_ok(status)
     dev = _device_of(x)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     if out is None:
-        out = torch.empty((T, hidden), dtype=x.dtype, device=dev)
-    ws, wp, wn = _workspace(moe_workspace_size(f, hidden, inter, E, x.dtype, T, k, fd), dev, workspace)
-    rc = lib().iq_moe(f, fd, _ptr(gate, "gate", dev), _ptr(up, "up", dev), _ptr(down, "down", dev), hidden, inter, E,
-                      _ptr(grid, "grid", dev), _ptr(down_grid, "down_grid", dev), _ptr(x, "x", dev), DTYPE[x.dtype],
-                      T, _ptr(router, "router", dev), DTYPE[router.dtype] if router is not None else 0, k,
-                      int(bool(renormalize)), _ptr(ids, "ids", dev), _ptr(weights, "weights", dev),
-                      _ptr(out, "out", dev), wp, wn, _ptr(status, "status", dev), _stream())
-    _check(rc, "iq_moe")
+        out = torch.empty((T, hidden), dtype=dtype, device=dev)
+    dt = DTYPE[dtype]
+    ws, wp, wn = _scratch(_run_size("iq_moe_workspace_size", f, fd, hidden, inter, E, dt, T, k), dev, workspace)
+    rc = lib().iq_moe(f, fd, _addr(gate, "gate", dev), _addr(up, "up", dev), _addr(down, "down", dev), hidden, inter,
+                      E, _addr(grid, "grid", dev), _addr(down_grid, "down_grid", dev), _addr(x, "x", dev), dt, T,
+                      _addr(router, "router", dev), 0 if router is None else DTYPE[router.dtype], k,
+                      int(bool(renormalize)), _addr(ids, "ids", dev), _addr(weights, "weights", dev),
+                      _addr(out, "out", dev), wp, wn, _addr(status, "status", dev),
+                      torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "iq_moe")
     return out, ids, weights

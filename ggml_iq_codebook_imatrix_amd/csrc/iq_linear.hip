@@ -43,7 +43,8 @@ __device__ __forceinline__ int tile_adapter(const Lora &L, int64_t tt, int64_t T
 // waves; rows of other tokens are formed as well and dropped.
 __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int rt, int slot, f32x4 *s_red) {
   const Lora &L = P.L;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, q = lane >> 4;
   const int mine = tile_adapter(L, tt, P.T, lane);
   if (threadIdx.x < 16 && slot == 0 && rt == 0) {
     const int64_t t = tt * 16 + lane;
@@ -56,21 +57,37 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
   const int j = min(rt * 16 + n, L.rank - 1);
   const int64_t xr = t * P.cols + q * 8, ar = (static_cast<int64_t>(a) * L.rank + j) * P.cols + q * 8;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int nb = static_cast<int>(P.cols >> 8), k0 = wave * 32;  // 32 of each 256 columns; U loads in flight
   if (P.dtype == 1) {
-#pragma unroll 8
-    for (int64_t k = wave * 32; k < P.cols; k += 256) {
-      const bf16x8 xa = ldu<bf16x8>(static_cast<const uint16_t *>(P.x) + xr + k);
-      const bf16x8 ab = ldu<bf16x8>(static_cast<const uint16_t *>(L.a) + ar + k);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, ab, acc, 0, 0, 0);
+    constexpr int U = 8;
+    const uint16_t *xp = static_cast<const uint16_t *>(P.x) + xr + k0, *ap = static_cast<const uint16_t *>(L.a) + ar + k0;
+    for (int b = 0; b < nb; b += U) {
+      bf16x8 xa[U], ab[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = min(b + u, nb - 1) * 256;
+        xa[u] = ldu<bf16x8>(xp + at);
+        ab[u] = ldu<bf16x8>(ap + at);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (b + u < nb) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[u], ab[u], acc, 0, 0, 0);
     }
   } else {
-#pragma unroll 4
-    for (int64_t k = wave * 32; k < P.cols; k += 256) {
-      float xa[8], ab[8];
-      load8u(P.x, 0, xr + k, xa);
-      load8u(L.a, 0, ar + k, ab);
+    constexpr int U = 4;
+    for (int b = 0; b < nb; b += U) {
+      float xa[U][8], ab[U][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xa[i], ab[i], acc, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const int at = min(b + u, nb - 1) * 256 + k0;
+        load8u(P.x, 0, xr + at, xa[u]);
+        load8u(L.a, 0, ar + at, ab[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (b + u < nb)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xa[u][i], ab[u][i], acc, 0, 0, 0);
     }
   }
   const float scale = L.scale ? L.scale[a] : 1.0f;
@@ -79,7 +96,10 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = (l >> 4) * 4 + i;
-      if ((group >> tok) & 1u) L.v[(tt * 16 + tok) * L.rpad + jj] = jj < L.rank ? s[i] * scale : 0.0f;
+      if (!((group >> tok) & 1u)) continue;
+      float *v = L.v + (tt * 16 + tok) * L.rpad + jj;
+      *v = jj < L.rank ? s[i] * scale : 0.0f;
+      if (rt + 1 == P.rtiles && L.rpad > P.rtiles * 16) v[16] = 0.0f;  // the rest of the last 32 ranks
     }
   });
 }
@@ -342,7 +362,7 @@ int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const 
   A.X = X;
   A.books = one_codebook(fmt, grid, tab, status);
   A.L = L;
-  A.rtiles = P.rpad / 16;
+  A.rtiles = (rank + 15) / 16;
   A.status = status;
   const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + P.x.ntile * 16 * A.rtiles));
   if (dtype == IQ_DTYPE_F32)
