@@ -119,8 +119,11 @@ __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
     return;
   }
   w -= A.books.wg[0];
-  const int slot = static_cast<int>(w & 15);
-  w >>= 4;
+  // slots last: where one adapter serves a whole tile, only slot 0 has work, and
+  // consecutive workgroups go to different XCDs (16 apart all went to one: 8x slower)
+  const int64_t tiles = A.X.ntile * A.rtiles;
+  const int slot = static_cast<int>(w / tiles);
+  w -= slot * tiles;
   lora_shrink(A, w / A.rtiles, static_cast<int>(w % A.rtiles), slot, s_red);
 }
 

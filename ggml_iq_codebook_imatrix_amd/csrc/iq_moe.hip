@@ -1,335 +1,174 @@
-// iq_run.hip -- tokens through encoded weights: iq_linear (a projection with the
-// low-rank adapters of many requests) and iq_moe (a mixture-of-experts layer),
-// declared in include/iq_run.h.
+// iq_moe.hip -- iq_moe: a mixture-of-experts layer on encoded experts
+// (include/iq_run.h).
 //
-// A weight is d * m * v: d the block's fp16 scale, m the group's odd multiplier,
-// v its signed codebook value.  The products run on the fp16 matrix cores:
-// m * v is formed in packed fp16 (exact for the layouts' codebooks: at most 11
-// bits), d and the tokens' power-of-two block scales are applied in fp32 to
-// each 256-column block's sum.
-//
-// Operand layout (v_mfma_f32_16x16x32_f16): the weights are B, lane l holding
-// eight consecutive k of row n = l % 16; the tokens are A, lane l holding the
-// same k of token m = l % 16; D has lane l hold row n = l % 16 and tokens
-// 4 (l / 16) + 0..3.  The order of k is free as long as both operands use it:
-// lane quarter q = l / 16 takes the block's 64 columns from 64 q on, eight at a
-// step, so that a lane's share of the payload is contiguous (two to three wide
-// loads a block) and one group of eight values is one codebook entry.
+// route_kernel brings the tokens into operand order, converts the codebooks and
+// forms the router's logits in fp64.  Then, by the number of tokens:
+//  few   up to 16 tokens (and 256 experts).  Launches cost more than arithmetic,
+//        so every workgroup of the next kernel picks the top_k itself, and there
+//        are three in all: few_up_kernel (16 rows of gate and up of one expert,
+//        blocks split over the waves) writes h in fp32, few_down_kernel (16
+//        columns of y, the chosen experts' blocks split over the waves) converts
+//        the h it needs and adds over experts in its accumulators.
+//  many  the choice is a launch of its own.  A workgroup takes 256 rows of one
+//        expert for up to 32 of the pairs routed to it, so that h leaves in
+//        operand order; the down projections leave one row per pair, and a last
+//        kernel adds each token's rows in the order of its ids.
 
-#include "iq_run.h"
-#include "iq_common.hpp"
-#include "iq_internal.hpp"
+#include "iq_run.hpp"
 
 namespace iq {
 namespace {
 
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef _Float16 half8v __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+constexpr int kFewTokens = 16, kFewExperts = 256, kMaxTopK = 64;
 
-constexpr int ST_ROUNDED = 32;
-constexpr int kGridN[5] = {256, 512, 1024, 2048, 2048};
-
-bool launched_ok() { return hipGetLastError() == hipSuccess; }
-
-// ---------------------------------------------------------------------------
-// Payload fields
-// ---------------------------------------------------------------------------
-template <class T> __device__ __forceinline__ T ldu(const uint8_t *p) {  // any alignment
-  T v;
-  __builtin_memcpy(&v, p, sizeof(T));
-  return v;
-}
-
-// One lane's share of a block: the fields of groups 8q .. 8q + 7.
-struct Raw {
-  uint32_t a[4];
-  uint32_t s;
-  uint32_t d16;
-};
-
-template <int F> __device__ __forceinline__ Raw load_raw(const uint8_t *blk, int q) {
-  Raw r;
-  if (F == IQ2_XXS || F == IQ2_XS) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.a[i] = ldu<uint32_t>(blk + 2 + 16 * q + 4 * i);
-    r.s = F == IQ2_XS ? ldu<uint16_t>(blk + 66 + 2 * q) : 0;
-    r.d16 = ldu<uint16_t>(blk);
-  } else if (F == IQ2_S) {
-    r.a[0] = ldu<uint32_t>(blk + 2 + 8 * q);
-    r.a[1] = ldu<uint32_t>(blk + 6 + 8 * q);
-    r.a[2] = ldu<uint32_t>(blk + 34 + 8 * q);
-    r.a[3] = ldu<uint32_t>(blk + 38 + 8 * q);
-    r.s = ldu<uint16_t>(blk + 66 + 2 * q) | (static_cast<uint32_t>(ldu<uint16_t>(blk + 74 + 2 * q)) << 16);
-    r.d16 = ldu<uint16_t>(blk);
-  } else if (F == IQ1_S) {
-    r.a[0] = ldu<uint32_t>(blk + 2 + 8 * q);
-    r.a[1] = ldu<uint32_t>(blk + 6 + 8 * q);
-    r.a[2] = ldu<uint32_t>(blk + 34 + 4 * q);
-    r.a[3] = r.s = 0;
-    r.d16 = ldu<uint16_t>(blk);
-  } else {
-    r.a[0] = ldu<uint32_t>(blk + 8 * q);
-    r.a[1] = ldu<uint32_t>(blk + 8 * q + 4);
-    r.a[2] = ldu<uint32_t>(blk + 32 + 4 * q);
-    r.a[3] = 0;
-    r.s = ldu<uint16_t>(blk + 48 + 2 * q);
-    const uint32_t w0 = ldu<uint32_t>(blk + 48), w1 = ldu<uint32_t>(blk + 52);
-    r.d16 = ((w0 >> 12) & 15u) | ((w0 >> 28) << 4) | (((w1 >> 12) & 15u) << 8) | ((w1 >> 28) << 12);
-  }
-  return r;
-}
-
-template <int F> __device__ __forceinline__ float block_scale(const Raw &r) {
-  const float d = f16_bits_to_f32(static_cast<uint16_t>(r.d16));
-  return Geo<F>::IQ1 ? d : d * 0.125f;  // exact: a power of two
-}
-
-// m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16).
-template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab) {
-  uint32_t k, ls, mask = 0, h = 0;
-  if (F == IQ2_XXS) {
-    const uint32_t word = r.a[2 * (i >> 2) + 1];
-    k = (r.a[2 * (i >> 2)] >> (8 * (i & 3))) & 255u;
-    mask = (word >> (7 * (i & 3))) & 127u;
-    ls = word >> 28;
-  } else if (F == IQ2_XS) {
-    const uint32_t v = (r.a[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-    k = v & 511u;
-    mask = v >> 9;
-    ls = (r.s >> (4 * (i >> 1))) & 15u;
-  } else if (F == IQ2_S) {
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((r.s >> (2 * i)) & 3u) << 8);
-    mask = (r.a[2 + (i >> 2)] >> (8 * (i & 3))) & 255u;
-    ls = (r.s >> (16 + 4 * (i >> 1))) & 15u;
-  } else if (F == IQ1_S) {
-    const uint32_t w = (r.a[2] >> (16 * (i >> 2))) & 0xffffu;
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((w >> (3 * (i & 3))) & 7u) << 8);
-    ls = (w >> 12) & 7u;
-    h = w >> 15;
-  } else {
-    const uint32_t nib = (r.a[2] >> (4 * i)) & 15u;
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | ((nib & 7u) << 8);
-    h = nib >> 3;
-    ls = (r.s >> (3 * (i >> 1))) & 7u;
-  }
-  const uint4 e = tab[k];
-  const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * ls + 1));
-  const half2v m2 = {m, m};
-  uint32_t o[4] = {e.x, e.y, e.z, e.w};
-  if (Geo<F>::IQ1) {
-    const half2v c2 = m2 * (h ? static_cast<_Float16>(-0.125f) : static_cast<_Float16>(0.125f));
-#pragma unroll
-    for (int p = 0; p < 4; ++p)  // m g + m delta, rounded once
-      o[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
-  } else {
-    // the eighth sign is the parity of the seven (IQ2_S holds it); then bit 2p
-    // to 2p and bit 2p + 1 to 2p + 16, so one shift brings a pair's signs home
-    if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
-    const uint32_t sp = (mask & 0x55u) | ((mask & 0xaau) << 15);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
-      o[p] = __builtin_bit_cast(uint32_t, v) ^ ((sp << (15 - 2 * p)) & 0x80008000u);
-    }
-  }
-  return __builtin_bit_cast(half8v, make_uint4(o[0], o[1], o[2], o[3]));
-}
-
-// ---------------------------------------------------------------------------
-// Tokens in fp16: x16 [block][tile of 16 tokens][part][step 0..7][lane][8], the
-// A operand of step i as 1 KiB of consecutive memory; ex [block][tokens]: the
-// power of two that undoes the block's scaling.  Tokens past T are left
-// unwritten: they only reach outputs that are not stored.
-// ---------------------------------------------------------------------------
-struct Tokens {
-  _Float16 *x16;
-  int32_t *ex;
-  int64_t ntile;  // tiles of 16 tokens
-  int parts;
-};
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o, 64)));
-  return v;
-}
-
-// One wave: token t's block b (lane: columns 4 lane .. + 3, given in v).
-__device__ __forceinline__ void store_block(const Tokens &X, int64_t t, int64_t b, int lane, const float v[4]) {
-  uint32_t e = 1;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t u = (__float_as_uint(v[j]) >> 23) & 255u;
-    e = max(e, u == 255u ? 1u : u);
-  }
-  const int n = 141 - static_cast<int>(wave_max(e));  // 14 - (e - 127): |x 2^n| < 2^15
-  _Float16 hi[4], lo[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float f = ldexpf(v[j], n);
-    hi[j] = static_cast<_Float16>(f);
-    lo[j] = finite_f(f) ? static_cast<_Float16>(f - static_cast<float>(hi[j])) : static_cast<_Float16>(0.0f);
-  }
-  const int q = lane >> 4, i = (lane & 15) >> 1;
-  const int64_t tile = b * X.ntile + (t >> 4);
-  const int64_t at = (static_cast<int64_t>(i) * 64 + q * 16 + (t & 15)) * 8 + (lane & 1) * 4;
-  _Float16 *p = X.x16 + tile * X.parts * 4096 + at;
-  *reinterpret_cast<uint2 *>(p) = __builtin_bit_cast(uint2, hi);
-  if (X.parts == 2) *reinterpret_cast<uint2 *>(p + 4096) = __builtin_bit_cast(uint2, lo);
-  if (lane == 0) X.ex[b * X.ntile * 16 + t] = -n;
-}
-
-__device__ __forceinline__ float load1(const void *x, int dtype, int64_t i) {
-  return dtype == 1 ? bf16_to_f32(static_cast<const uint16_t *>(x)[i]) : static_cast<const float *>(x)[i];
-}
-
-__device__ __forceinline__ void store1(void *y, int dtype, int64_t i, float v) {
-  if (dtype == 1)
-    static_cast<uint16_t *>(y)[i] = f32_to_bf16(v);
-  else
-    static_cast<float *>(y)[i] = v;
-}
-
-// Workgroups 0 .. nconv - 1 convert tokens (four blocks each), the one after
-// them the codebook, and one more a second codebook if there is one.
-struct PrepArgs {
-  const void *x;
-  int dtype;
-  int64_t T, cols, nconv;
-  Tokens X;
-  const float *grid[2];
-  _Float16 *tab[2];
-  int n[2], iq1[2];
+struct MoeArgs {
+  const uint8_t *gate, *up, *down;
+  int64_t hidden, inter;
+  int E, top_k, renorm, routed;
+  int64_t T, npair;
+  const void *x, *router;
+  int dtype, rdtype;
+  Tokens X, H;             // tokens; h of the pairs (many)
+  const _Float16 *tab, *dtab;
+  double *logits;          // [T, E]
+  int32_t *ids;
+  float *weights;
+  float *h;                // few: [pairs, inter] f32
+  float *z;                // many: [pairs, hidden] f32
+  void *y;
   int32_t *status;
+  Codebooks books;
+  int64_t nconv;
 };
 
-__device__ void convert_codebook(const float *grid, _Float16 *tab, int n, bool iq1, int32_t *status) {
-  bool inexact = false;
-  for (int i = threadIdx.x; i < n * 8; i += blockDim.x) {
-    const float g = grid[i];
-    tab[i] = static_cast<_Float16>(g);
-    for (int m = 1; m < (iq1 ? 16 : 32); m += 2) {
-      const float f = static_cast<float>(m);
-      if (iq1) {
-        inexact |= static_cast<float>(static_cast<_Float16>(f * (g + 0.125f))) != f * (g + 0.125f);
-        inexact |= static_cast<float>(static_cast<_Float16>(f * (g - 0.125f))) != f * (g - 0.125f);
-      } else {
-        inexact |= static_cast<float>(static_cast<_Float16>(f * g)) != f * g;
-      }
+// ---------------------------------------------------------------------------
+// Routing
+// ---------------------------------------------------------------------------
+constexpr int kRouteTokens = 4;  // tokens a wave carries past one row of the router
+
+// One wave: the logits of one expert for four tokens.  Summed in fp64, so that
+// no order of summation can swap neighbours in the ranking.
+__device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t ne = (A.E + 7) / 8, t0 = (w / ne) * kRouteTokens, e = (w % ne) * 8 + wave;
+  if (e >= A.E) return;
+  double s[kRouteTokens] = {};
+  for (int64_t k = lane * 8; k < A.hidden; k += 512) {
+    float r[8], x[kRouteTokens][8];
+    load8u(A.router, A.rdtype, e * A.hidden + k, r);
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i) load8u(A.x, A.dtype, min(t0 + i, A.T - 1) * A.hidden + k, x[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double rd = static_cast<double>(r[j]);
+#pragma unroll
+      for (int i = 0; i < kRouteTokens; ++i)
+        if (t0 + i < A.T) s[i] = fma(rd, static_cast<double>(x[i][j]), s[i]);
     }
-    inexact |= static_cast<float>(tab[i]) != g;
   }
-  if (inexact) raise_status(status, ST_ROUNDED);
+#pragma unroll
+  for (int i = 0; i < kRouteTokens; ++i) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s[i] += __shfl_xor(s[i], o, 64);
+    if (lane == 0 && t0 + i < A.T) A.logits[(t0 + i) * A.E + e] = s[i];
+  }
 }
 
-__global__ void __launch_bounds__(256) run_prep_kernel(PrepArgs P) {
-  if (blockIdx.x >= P.nconv) {
-    const int w = static_cast<int>(blockIdx.x - P.nconv);
-    convert_codebook(P.grid[w], P.tab[w], P.n[w], P.iq1[w], P.status);
+template <int P>
+__global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
+  int64_t w = blockIdx.x;
+  if (w < A.nconv) {
+    const int64_t nb = A.hidden >> 8, i = w * 2 + (threadIdx.x >> 8);
+    if (i < nb * A.X.ntile) convert_tile<P>(A.x, A.dtype, A.T, A.hidden, A.X, i % nb, i / nb, threadIdx.x & 255);
     return;
   }
-  const int64_t nb = P.cols >> 8, i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (i >= P.T * nb) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = i / nb, b = i - t * nb;
-  float v[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = load1(P.x, P.dtype, t * P.cols + b * 256 + lane * 4 + j);
-  store_block(P.X, t, b, lane, v);
-}
-
-template <int F> __device__ __forceinline__ void load_table(uint4 *s_tab, const _Float16 *tab) {
-  for (int i = threadIdx.x; i < Geo<F>::N; i += blockDim.x) s_tab[i] = reinterpret_cast<const uint4 *>(tab)[i];
-}
-
-// acc += one block of a 16-row by 16-token product.  rowp: the lane's row in
-// the payload; xlane: which of the tile's tokens the lane feeds.
-template <int F>
-__device__ __forceinline__ void block_product(const uint8_t *blk, const uint4 *s_tab, const Tokens &X, int64_t b,
-                                              int64_t tile, int xlane, int q, f32x4 &acc, const int ex[4]) {
-  const Raw r = load_raw<F>(blk, q);
-  f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-  const _Float16 *xp = X.x16 + (b * X.ntile + tile) * X.parts * 4096 + (q * 16 + xlane) * 8;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const half8v w = group_half8<F>(r, i, s_tab);
-    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const half8v *>(xp + i * 512), w, part, 0, 0, 0);
-    if (X.parts == 2)
-      part = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const half8v *>(xp + 4096 + i * 512), w, part,
-                                                    0, 0, 0);
+  w -= A.nconv;
+  if (w < A.books.wg[0] + A.books.wg[1]) {
+    convert_codebook(A.books, static_cast<int>(w));
+    return;
   }
-  const float d = block_scale<F>(r);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] += ldexpf(d * part[k], ex[k]);
+  route_logits(A, w - A.books.wg[0] - A.books.wg[1]);
 }
 
-// ---------------------------------------------------------------------------
-// Mixture of experts
-// ---------------------------------------------------------------------------
-// logits[t][e] in fp64, one wave each
-__global__ void __launch_bounds__(256) router_kernel(const void *x, int dtype, const void *router, int rdtype,
-                                                      int64_t T, int64_t K, int E, double *logits) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (i >= T * E) return;
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xf,
+                                                                  0xf, false)));
+}
+// maximum over the wave, the same in every lane: prefixes within rows of 16, then across the rows
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max<0x111>(v);
+  v = dpp_max<0x112>(v);
+  v = dpp_max<0x114>(v);
+  v = dpp_max<0x118>(v);
+  v = dpp_max<0x142>(v);
+  v = dpp_max<0x143>(v);
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// fp64 as a whole number of the same order, from 1 (NaN) up; 0: taken
+__device__ __forceinline__ uint64_t order_key(double v) {
+  if (v != v) return 1;
+  const int64_t b = __builtin_bit_cast(int64_t, v + 0.0);  // -0 as 0
+  return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+  if (k == 1) return __builtin_nan("");
+  return __builtin_bit_cast(double, (k >> 63) ? k & ~(uint64_t(1) << 63) : ~k);
+}
+
+// One wave picks a token's top_k (at most 64): largest logit first, equal ones
+// by id, NaN last.  Lane l holds experts l + 64 j; a round finds the largest
+// upper half by register permutes and looks at lower halves and ids only where
+// several lanes tie.  ids, weights: where the token's choice goes.
+template <int KPL>
+__device__ __forceinline__ void pick_top(const double *l, int E, int top_k, int renorm, int32_t *ids, float *weights) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = i / E, e = i - t * E;
-  double s = 0.0;
-  for (int64_t k = lane; k < K; k += 64)
-    s = fma(static_cast<double>(load1(router, rdtype, e * K + k)), static_cast<double>(load1(x, dtype, t * K + k)), s);
+  uint64_t key[KPL];
 #pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
-  if (lane == 0) logits[i] = s;
-}
-
-// one wave per token: the top_k largest logits, ties to the lower id, NaN last
-__global__ void __launch_bounds__(64) topk_kernel(const double *logits, int E, int top_k, int renorm, int32_t *ids,
-                                                   float *weights) {
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x;
-  const double *l = logits + t * E;
+  for (int j = 0; j < KPL; ++j) {
+    const int e = lane + 64 * j;
+    key[j] = e < E ? order_key(l[e]) : 0;
+  }
   double top = 0.0;
-  float sum = 0.0f, mine = 0.0f;
-  double last = 0.0;
-  int last_id = -1;
-  bool last_nan = false;
+  float mine = 0.0f, sum = 0.0f;
+  int my_id = 0;
   for (int s = 0; s < top_k; ++s) {
-    // the largest (value, lower id) after (last, last_id) in the order
-    double bv = 0.0;
-    int bi = -1;
-    bool bn = false;
-    for (int e = lane; e < E; e += 64) {
-      const double v = l[e];
-      const bool nan = v != v;
-      const bool after = last_id < 0 || (nan ? (!last_nan || e > last_id)
-                                             : (!last_nan && (v < last || (v == last && e > last_id))));
-      if (!after) continue;
-      if (bi < 0 || (bn && !nan) || (!bn && !nan && v > bv)) {
-        bv = v;
-        bi = e;
-        bn = nan;
-      }
-    }
+    uint64_t best = key[0];
+    int bj = 0;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      const double ov = __shfl_xor(bv, o, 64);
-      const int oi = __shfl_xor(bi, o, 64);
-      const bool on = __shfl_xor(static_cast<int>(bn), o, 64) != 0;
-      const bool take = oi >= 0 && (bi < 0 || (bn != on ? bn : (!bn && ov != bv ? ov > bv : oi < bi)));
-      if (take) {
-        bv = ov;
-        bi = oi;
-        bn = on;
+    for (int j = 1; j < KPL; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        bj = j;
+      }
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+    const uint32_t mhi = wave_max_u32(hi);
+    uint64_t who = __ballot(hi == mhi);
+    if (who & (who - 1)) {
+      const uint32_t mlo = wave_max_u32(hi == mhi ? lo : 0u);
+      const bool tied = hi == mhi && lo == mlo;
+      who = __ballot(tied);
+      if (who & (who - 1)) {  // the lowest id: the largest 4095 - id
+        const uint32_t id = 4095u - static_cast<uint32_t>(lane + 64 * bj);
+        const uint32_t mid = wave_max_u32(tied ? id : 0u);
+        who = __ballot(tied && id == mid);
       }
     }
-    last = bv;
-    last_id = bi;
-    last_nan = bn;
-    if (s == 0) top = bv;
-    const float p = expf(static_cast<float>(bv - top));
+    const int from = static_cast<int>(__builtin_ctzll(who));
+    const uint64_t won = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(hi), from)) << 32) |
+                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(lo), from));
+    const int wj = __builtin_amdgcn_readlane(bj, from);
+#pragma unroll
+    for (int j = 0; j < KPL; ++j)
+      if (lane == from && j == wj) key[j] = 0;
+    const double v = key_value(won);
+    if (s == 0) top = v;
+    const float p = expf(static_cast<float>(v - top));
     sum += p;
-    if (lane == s) mine = p;
-    if (lane == 0) ids[t * top_k + s] = bi;
+    if (lane == s) {
+      mine = p;
+      my_id = from + 64 * wj;
+    }
   }
   if (!renorm) {
     sum = 0.0f;
@@ -337,155 +176,509 @@ __global__ void __launch_bounds__(64) topk_kernel(const double *logits, int E, i
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
   }
-  if (lane < top_k) weights[t * top_k + lane] = mine / sum;
+  if (lane < top_k) {
+    ids[lane] = my_id;
+    weights[lane] = mine / sum;
+  }
 }
 
-// One wave: 16 rows of gate and up for one (token, slot) pair; h = weight *
-// silu(g) * u.  Every row of the A operand is the pair's token.
-template <int F>
-__global__ void __launch_bounds__(256) gate_up_kernel(const uint8_t *gate, const uint8_t *up, int64_t inter,
-                                                       int64_t nb, int E, const _Float16 *tab, Tokens X,
-                                                       int64_t npair, int top_k, const int32_t *ids,
-                                                       const float *weights, float *h, int32_t *status) {
-  __shared__ uint4 s_tab[Geo<F>::N];
-  load_table<F>(s_tab, tab);
-  __syncthreads();
-  const int64_t nrt = inter / 16, w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t p = w / nrt, rt = w - p * nrt;
-  if (p >= npair) return;
-  const int e = ids[p];
-  if (e < 0 || e >= E) {
-    raise_status(status, ST_BADID);
-    return;
-  }
-  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int64_t t = p / top_k, row = e * inter + rt * 16 + n;
-  f32x4 ag = {0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
-  for (int64_t b = 0; b < nb; ++b) {
-    const int x = X.ex[b * X.ntile * 16 + t], ex[4] = {x, x, x, x};
-    block_product<F>(gate + (row * nb + b) * Geo<F>::BYTES, s_tab, X, b, t >> 4, t & 15, q, ag, ex);
-    block_product<F>(up + (row * nb + b) * Geo<F>::BYTES, s_tab, X, b, t >> 4, t & 15, q, au, ex);
-  }
-  if (q == 0) h[p * inter + rt * 16 + n] = ag[0] / (1.0f + expf(-ag[0])) * au[0] * weights[p];
+__global__ void __launch_bounds__(64) topk_kernel(MoeArgs A) {
+  const int64_t t = blockIdx.x;
+  if (A.E <= 256)
+    pick_top<4>(A.logits + t * A.E, A.E, A.top_k, A.renorm, A.ids + t * A.top_k, A.weights + t * A.top_k);
+  else
+    pick_top<64>(A.logits + t * A.E, A.E, A.top_k, A.renorm, A.ids + t * A.top_k, A.weights + t * A.top_k);
 }
 
-// One wave: 16 output columns of one token, over the token's experts.
-template <int F>
-__global__ void __launch_bounds__(256) down_kernel(const uint8_t *down, int64_t hidden, int64_t nb, int E,
-                                                    const _Float16 *tab, Tokens H, int64_t T, int top_k,
-                                                    const int32_t *ids, int dtype, void *y) {
-  __shared__ uint4 s_tab[Geo<F>::N];
-  load_table<F>(s_tab, tab);
+__device__ __forceinline__ float gated(float g, float u, float w) { return g / (1.0f + expf(-g)) * u * w; }
+
+// ---------------------------------------------------------------------------
+// Few tokens
+// ---------------------------------------------------------------------------
+// The pairs' experts in LDS (-1: none), and which experts occur.
+__device__ __forceinline__ void few_active(const int *s_ids, int np, uint32_t *s_bits) {
+  if (threadIdx.x < kFewExperts / 32) s_bits[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t nrt = hidden / 16, w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t t = w / nrt, rt = w - t * nrt;
-  if (t >= T) return;
-  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < top_k; ++s) {
-    const int64_t p = t * top_k + s;
-    const int e = ids[p];
-    if (e < 0 || e >= E) continue;
-    const int64_t row = e * hidden + rt * 16 + n;
-    for (int64_t b = 0; b < nb; ++b) {
-      const int x = H.ex[b * H.ntile * 16 + p], ex[4] = {x, x, x, x};
-      block_product<F>(down + (row * nb + b) * Geo<F>::BYTES, s_tab, H, b, p >> 4, p & 15, q, acc, ex);
+  for (int p = threadIdx.x; p < np; p += blockDim.x)
+    if (s_ids[p] >= 0) atomicOr(&s_bits[s_ids[p] >> 5], 1u << (s_ids[p] & 31));
+  __syncthreads();
+}
+
+template <int F, int P>
+__global__ void __launch_bounds__(512) few_up_kernel(MoeArgs A) {
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ f32x4 s_red[8 * 2 * 64];
+  __shared__ int s_ids[kFewTokens * kMaxTopK], s_list[kFewTokens * kMaxTopK];
+  __shared__ float s_w[kFewTokens * kMaxTopK];
+  __shared__ uint32_t s_bits[kFewExperts / 32];
+  __shared__ int s_n;
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6, np = static_cast<int>(A.npair);
+  if (A.routed) {
+    for (int t = wave; t < A.T; t += nw)
+      pick_top<4>(A.logits + static_cast<int64_t>(t) * A.E, A.E, A.top_k, A.renorm, s_ids + t * A.top_k,
+                  s_w + t * A.top_k);
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int p = threadIdx.x; p < np; p += blockDim.x) {
+        A.ids[p] = s_ids[p];
+        A.weights[p] = s_w[p];
+      }
+  } else {
+    for (int p = threadIdx.x; p < np; p += blockDim.x) {
+      const int e = A.ids[p];
+      const bool bad = e < 0 || e >= A.E;
+      if (bad && blockIdx.x == 0) raise_status(A.status, ST_BADID);
+      s_ids[p] = bad ? -1 : e;
+      s_w[p] = A.weights[p];
     }
   }
-  if (q == 0) store1(y, dtype, t * hidden + rt * 16 + n, acc[0]);
+  few_active(s_ids, np, s_bits);
+  // this workgroup's expert: the one of rank `slot` among those that occur
+  const int64_t nrt = A.inter / 16;
+  int slot = static_cast<int>(blockIdx.x / nrt), e = -1;
+  const int64_t rt = blockIdx.x % nrt;
+#pragma unroll
+  for (int i = 0; i < kFewExperts / 32; ++i) {
+    uint32_t bits = __builtin_amdgcn_readfirstlane(s_bits[i]);
+    const int c = __builtin_popcount(bits);
+    if (e < 0 && slot < c) {
+      for (int k = 0; k < slot; ++k) bits &= bits - 1;
+      e = i * 32 + __builtin_ctz(bits);
+    }
+    if (e < 0) slot -= c;
+  }
+  if (e < 0) return;
+  if (wave == 0) {
+    int n = 0;
+    for (int p0 = 0; p0 < np; p0 += 64) {
+      const bool hit = p0 + lane < np && s_ids[p0 + lane] == e;
+      const uint64_t b = __ballot(hit);
+      if (hit) s_list[n + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = p0 + lane;
+      n += __builtin_popcountll(b);
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int count = s_n, n = lane & 15, q = lane >> 4;
+  const int64_t nb = A.hidden >> 8, row = e * A.inter + rt * 16 + n;
+  const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
+  for (int c0 = 0; c0 < count; c0 += 16) {
+    const int t = s_list[min(c0 + n, count - 1)] / A.top_k;
+    const _Float16 *x0 = A.X.x16 + (q * 16 + t) * 8;  // one tile of tokens
+    int et[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) et[k] = s_list[min(c0 + q * 4 + k, count - 1)] / A.top_k;
+    f32x4 acc[2] = {};
+    for (int64_t b = wave; b < nb; b += nw) {
+      Raw raw[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r] + b * Geo<F>::BYTES, q);
+      int ex[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * 16 + et[k]];
+      const _Float16 *const xp[1] = {x0 + b * P * 4096};
+      f32x4 part[2][1];
+      block_mma<F, P, 1, 2>(raw, s_tab, xp, part);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) scale_add(acc[r], part[r][0], block_scale<F>(raw[r]), ex);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) s_red[(wave * 2 + r) * 64 + lane] = acc[r];
+    __syncthreads();
+    if (wave == 0) {
+      f32x4 g = s_red[lane], u = s_red[64 + lane];
+      for (int w = 1; w < nw; ++w) {
+        g += s_red[w * 128 + lane];
+        u += s_red[w * 128 + 64 + lane];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + q * 4 + k < count) {
+          const int p = s_list[c0 + q * 4 + k];
+          A.h[p * A.inter + rt * 16 + n] = gated(g[k], u[k], s_w[p]);
+        }
+    }
+  }
+}
+
+// Waves split (expert, block of inter): each stages its tokens' h of that block
+// as the A operand (rows: tokens; absent ones zero) in LDS of its own.
+constexpr int few_down_waves(int parts) { return parts == 2 ? 4 : 8; }  // 8 KiB of LDS a part and wave
+template <int F, int P>
+__global__ void __launch_bounds__(64 * few_down_waves(P)) few_down_kernel(MoeArgs A) {
+  constexpr int NW = few_down_waves(P);
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ uint4 s_x[NW][P * 512];  // also the sums over the waves
+  __shared__ int s_ids[kFewTokens * kMaxTopK], s_ex[NW][16], s_active[kFewExperts];
+  __shared__ uint32_t s_bits[kFewExperts / 32];
+  load_table<F>(s_tab, A.dtab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int np = static_cast<int>(A.npair), n = lane & 15, q = lane >> 4;
+  for (int p = threadIdx.x; p < np; p += blockDim.x) {
+    const int e = A.ids[p];
+    s_ids[p] = e >= 0 && e < A.E ? e : -1;
+  }
+  for (int i = lane; i < P * 512; i += 64) s_x[wave][i] = make_uint4(0, 0, 0, 0);
+  if (lane < 16) s_ex[wave][lane] = 0;
+  __syncthreads();
+  few_active(s_ids, np, s_bits);
+  int na = 0;
+#pragma unroll
+  for (int i = 0; i < kFewExperts / 32; ++i) {
+    const uint32_t bits = __builtin_amdgcn_readfirstlane(s_bits[i]);
+    if (wave == 0 && lane < 32 && ((bits >> lane) & 1u))
+      s_active[na + __builtin_popcount(bits & ((1u << lane) - 1u))] = i * 32 + lane;
+    na += __builtin_popcount(bits);
+  }
+  __syncthreads();
+  const int nb = static_cast<int>(A.inter >> 8);
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 16;
+  _Float16 *xs = reinterpret_cast<_Float16 *>(&s_x[wave][0]);
+  const int at = (((lane & 15) >> 1) * 64 + q * 16) * 8 + (lane & 1) * 4;  // where columns 4 lane .. + 3 go, token 0
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int task = wave; task < na * nb; task += NW) {
+    const int e = __builtin_amdgcn_readfirstlane(s_active[task / nb]), b = task % nb;
+    Raw raw[1];
+    raw[0] = load_raw<F>(A.down + ((e * A.hidden + col0 + n) * nb + b) * Geo<F>::BYTES, q);
+    uint32_t present = 0;
+    const auto stage = [&](int t, const float *v) {  // token t's h: one wave, four columns a lane
+      uint32_t x = 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x = max_exponent(x, v[j]);
+      const int up = 141 - static_cast<int>(wave_max_u32(x));
+      _Float16 hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to_parts(v[j], up, hi[j], lo[j]);
+      *reinterpret_cast<uint2 *>(xs + at + t * 8) = __builtin_bit_cast(uint2, hi);
+      if (P == 2) *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = __builtin_bit_cast(uint2, lo);
+      if (lane == 0) s_ex[wave][t] = -up;
+      present |= 1u << t;
+    };
+    float v[4] = {};
+    int token = -1;
+    for (int p0 = 0; p0 < np; p0 += 64) {
+      uint64_t hits = __ballot(p0 + lane < np && s_ids[p0 + lane] == e);
+      while (hits) {
+        const int p = p0 + static_cast<int>(__builtin_ctzll(hits));
+        hits &= hits - 1;
+        const int t = p / A.top_k;
+        if (t != token) {  // an expert named twice by a token: its rows are added
+          if (token >= 0) stage(token, v);
+          token = t;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = 0.0f;
+        }
+        const float4 f = *reinterpret_cast<const float4 *>(A.h + p * A.inter + b * 256 + lane * 4);
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+      }
+    }
+    stage(token, v);
+    const _Float16 *const xp[1] = {xs + lane * 8};
+    f32x4 part[1][1];
+    block_mma<F, P, 1, 1>(raw, s_tab, xp, part);
+    const float d = block_scale<F>(raw[0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((present >> (q * 4 + k)) & 1u) acc[k] += ldexpf(d * part[0][0][k], s_ex[wave][q * 4 + k]);
+    for (uint32_t m = present; m; m &= m - 1) {  // leave the rows zero again
+      const int t = __builtin_ctz(m);
+      *reinterpret_cast<uint2 *>(xs + at + t * 8) = make_uint2(0, 0);
+      if (P == 2) *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = make_uint2(0, 0);
+    }
+  }
+  reduce_waves<1, 1>(&acc, reinterpret_cast<f32x4 *>(&s_x[0][0]), NW, [&](int, int l, const f32x4 &s) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = (l >> 4) * 4 + k;
+      if (t < A.T) store1(A.y, P == 1, t * A.hidden + col0 + (l & 15), s[k]);
+    }
+  });
 }
 
 // ---------------------------------------------------------------------------
-// Workspaces
+// Many tokens
 // ---------------------------------------------------------------------------
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
-
-struct TokensPlan {
-  int64_t ntile;
-  int parts;
-  size_t xbytes, ebytes;
-};
-TokensPlan plan_tokens(int64_t T, int64_t cols, int dtype) {
-  TokensPlan p;
-  p.ntile = (T + 15) / 16;
-  p.parts = dtype == IQ_DTYPE_F32 ? 2 : 1;
-  p.xbytes = static_cast<size_t>(cols / 256) * p.ntile * p.parts * 8192;
-  p.ebytes = static_cast<size_t>(cols / 256) * p.ntile * 64;
-  return p;
+// Walks the pairs of one expert in ascending order, N at a time: f(list, count).
+template <int N, class Fn>
+__device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, int *s_list, int *s_cnt, Fn f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int have = 0;
+  for (int64_t p0 = 0; p0 < A.npair; p0 += 512) {
+    const int64_t p = p0 + threadIdx.x;
+    const bool hit = p < A.npair && A.ids[p] == e;
+    const uint64_t b = __ballot(hit);
+    if (lane == 0) s_cnt[wave] = __builtin_popcountll(b);
+    __syncthreads();
+    int at = have, total = 0;
+    for (int w = 0; w < 8; ++w) {
+      const int c = s_cnt[w];
+      if (w < wave) at += c;
+      total += c;
+    }
+    if (hit) s_list[at + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = static_cast<int>(p);
+    have += total;
+    __syncthreads();
+    const bool last = p0 + 512 >= A.npair;
+    int head = 0;
+    while (have - head >= N || (last && have > head)) {
+      f(s_list + head, min(N, have - head));
+      head += min(N, have - head);
+    }
+    if (head) {  // what is left moves to the front
+      const int rest = have - head;
+      int keep = 0;
+      if (static_cast<int>(threadIdx.x) < rest) keep = s_list[head + threadIdx.x];
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < rest) s_list[threadIdx.x] = keep;
+      have = rest;
+      __syncthreads();
+    }
+  }
 }
+
+template <int F, int P, int C>
+__global__ void __launch_bounds__(512) many_up_kernel(MoeArgs A) {
+  constexpr int N = 16 * C;
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ int s_list[512 + N], s_cnt[8];
+  __shared__ uint32_t s_max[16][N];
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
+  const int64_t nb = A.hidden >> 8, nblk = A.inter >> 8;
+  const int e = static_cast<int>(blockIdx.x / nblk);
+  const int64_t blk = blockIdx.x % nblk;
+  for_pairs<N>(A, e, s_list, s_cnt, [&](const int *list, int count) {
+    const _Float16 *x0[C];
+    int64_t e0[C][4];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t t = list[min(c * 16 + n, count - 1)] / A.top_k;
+      x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)] / A.top_k;
+    }
+    float h[2][C][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t row = e * A.inter + blk * 256 + (half * 8 + wave) * 16 + n;
+      const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
+      f32x4 acc[2][C] = {};
+      Raw raw[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
+      for (int64_t b = 0; b < nb; ++b) {
+        Raw next[2];
+        const int64_t bn = min(b + 1, nb - 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+        const _Float16 *xp[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
+        f32x4 part[2][C];
+        block_mma<F, P, C, 2>(raw, s_tab, xp, part);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          int ex[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[r] = next[r];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float w = A.weights[list[min(c * 16 + q * 4 + k, count - 1)]];
+          h[half][c][k] = gated(acc[0][c][k], acc[1][c][k], w);
+          uint32_t m = max_exponent(1, h[half][c][k]);
+#pragma unroll
+          for (int o = 8; o; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
+          if (n == 0) s_max[half * 8 + wave][c * 16 + q * 4 + k] = m;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = c * 16 + q * 4 + k;
+        uint32_t m = 1;
+        for (int w = 0; w < 16; ++w) m = max(m, s_max[w][i]);
+        if (i >= count) continue;
+        const int64_t p = list[i];
+        const int up = 141 - static_cast<int>(m);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int col = (half * 8 + wave) * 16 + n;
+          _Float16 hi, lo;
+          to_parts(h[half][c][k], up, hi, lo);
+          _Float16 *o = A.H.x16 + (blk * A.H.ntile + (p >> 4)) * P * 4096 +
+                        (((col & 63) >> 3) * 64 + (col >> 6) * 16 + (p & 15)) * 8 + (col & 7);
+          *o = hi;
+          if (P == 2) o[4096] = lo;
+        }
+        if (wave == 0 && n == 0) A.H.ex[blk * A.H.ntile * 16 + p] = -up;
+      }
+    __syncthreads();  // the list and the maxima are free again
+  });
+}
+
+template <int F, int P, int C>
+__global__ void __launch_bounds__(512) many_down_kernel(MoeArgs A) {
+  constexpr int N = 16 * C;
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ int s_list[512 + N], s_cnt[8];
+  load_table<F>(s_tab, A.dtab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
+  const int64_t nb = A.inter >> 8, nblk = A.hidden >> 8;
+  const int e = static_cast<int>(blockIdx.x / nblk);
+  const int64_t blk = blockIdx.x % nblk;
+  for_pairs<N>(A, e, s_list, s_cnt, [&](const int *list, int count) {
+    const _Float16 *x0[C];
+    int64_t e0[C][4];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t p = list[min(c * 16 + n, count - 1)];
+      x0[c] = A.H.x16 + (p >> 4) * P * 4096 + (q * 16 + (p & 15)) * 8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)];
+    }
+    const int64_t col = blk * 256 + wave * 32 + n;  // two row tiles a wave
+    const uint8_t *rp[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
+    f32x4 acc[2][C] = {};
+    Raw raw[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
+    for (int64_t b = 0; b < nb; ++b) {
+      Raw next[2];
+      const int64_t bn = min(b + 1, nb - 1);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+      const _Float16 *xp[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.H.ntile * P * 4096;
+      f32x4 part[2][C];
+      block_mma<F, P, C, 2>(raw, s_tab, xp, part);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        int ex[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ex[k] = A.H.ex[b * A.H.ntile * 16 + e0[c][k]];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) raw[r] = next[r];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c * 16 + q * 4 + k < count)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) A.z[e0[c][k] * A.hidden + col + r * 16] = acc[r][c][k];
+  });
+}
+
+// y[t] = the sum of its pairs' rows, in the order of its ids
+__global__ void __launch_bounds__(256) many_sum_kernel(MoeArgs A) {
+  const int64_t per = A.hidden / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= A.T * per) return;
+  const int64_t t = i / per, c = (i - t * per) * 4;
+  float s[4] = {};
+  for (int k = 0; k < A.top_k; ++k) {
+    const int e = A.ids[t * A.top_k + k];
+    if (e < 0 || e >= A.E) {
+      if (c == 0) raise_status(A.status, ST_BADID);
+      continue;
+    }
+    const float4 v = *reinterpret_cast<const float4 *>(A.z + (t * A.top_k + k) * A.hidden + c);
+    s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) store1(A.y, A.dtype, t * A.hidden + c + j, s[j]);
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+bool is_few(int64_t T, int E) { return T <= kFewTokens && E <= kFewExperts; }
 
 struct MoePlan {
   TokensPlan x, h;
-  size_t tab, tab2, xo, eo, lo, ho, hxo, heo, bytes;
+  size_t tab, dtab, xo, eo, lo, ho, hxo, heo, zo, bytes;
 };
 MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int dtype, int64_t T, int top_k) {
   MoePlan p;
+  const bool few = is_few(T, E);
+  const size_t np = static_cast<size_t>(T) * top_k;
   p.x = plan_tokens(T, hidden, dtype);
-  p.h = plan_tokens(T * top_k, inter, dtype);
+  p.h = plan_tokens(few ? 0 : T * top_k, inter, dtype);
   p.tab = 0;
-  p.tab2 = ws_up(static_cast<size_t>(kGridN[fmt]) * 16);
-  p.xo = p.tab2 + ws_up(static_cast<size_t>(kGridN[down_fmt]) * 16);
+  p.dtab = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
+  p.xo = p.dtab + ws_up(static_cast<size_t>(kCodebook[down_fmt]) * 16);
   p.eo = p.xo + ws_up(p.x.xbytes);
   p.lo = p.eo + ws_up(p.x.ebytes);
   p.ho = p.lo + ws_up(static_cast<size_t>(T) * E * 8);
-  p.hxo = p.ho + ws_up(static_cast<size_t>(T) * top_k * inter * 4);
+  p.hxo = p.ho + ws_up(few ? np * inter * 4 : 0);
   p.heo = p.hxo + ws_up(p.h.xbytes);
-  p.bytes = p.heo + ws_up(p.h.ebytes) + kWsAlign;
+  p.zo = p.heo + ws_up(p.h.ebytes);
+  p.bytes = p.zo + ws_up(few ? 0 : np * hidden * 4) + kWsAlign;
   return p;
 }
 
-bool bad_fmt(int f) { return f < 0 || f > 4; }
-bool bad_dtype(int d) { return d != IQ_DTYPE_F32 && d != IQ_DTYPE_BF16; }
-
 int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int dtype, int64_t T, int top_k) {
-  if (bad_fmt(fmt) || bad_fmt(down_fmt)) return IQ_ERR_FMT;
-  if (bad_dtype(dtype)) return IQ_ERR_DTYPE;
+  if (run_bad_fmt(fmt) || run_bad_fmt(down_fmt)) return IQ_ERR_FMT;
+  if (run_bad_dtype(dtype)) return IQ_ERR_DTYPE;
   if (T < 0 || hidden <= 0 || hidden % 256 != 0 || inter <= 0 || inter % 256 != 0) return IQ_ERR_SHAPE;
   if (hidden > (int64_t(1) << 24) || inter > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
-  if (E < 1 || E > 4096 || top_k < 1 || top_k > 64) return IQ_ERR_ARG;
-  const int64_t big = hidden > inter ? hidden : inter;
-  if (T > (int64_t(1) << 24) || T * top_k * (big / 16) >= kMaxGrid || T * E >= kMaxGrid) return IQ_ERR_SHAPE;
+  if (E < 1 || E > 4096 || top_k < 1 || top_k > kMaxTopK) return IQ_ERR_ARG;
+  const int64_t ntile = (T + 15) / 16, np = T * top_k;
+  if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
+  // the launches: routing, up, down, sum (pairs are counted in 32 bits)
+  if (ntile * (hidden / 256) / 2 + 8 + ((E + 7) / 8) * ((T + kRouteTokens - 1) / kRouteTokens) >= kMaxWG ||
+      np >= kMaxWG || np * (inter / 16) >= kMaxWG * (is_few(T, E) ? 1 : 16) || E * (inter / 256) >= kMaxWG ||
+      E * (hidden / 256) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
+    return IQ_ERR_SHAPE;
   return IQ_OK;
 }
 
-int check_ws(size_t need, const void *ws, size_t have) {
-  if (!ws) return IQ_ERR_NULL;
-  return have < need ? IQ_ERR_WORKSPACE : IQ_OK;
-}
-
-dim3 waves4(int64_t n) { return dim3(static_cast<unsigned>((n + 3) / 4)); }
-
-int launch_prep(const void *x, int dtype, int64_t T, int64_t cols, const Tokens &X, const float *g0, _Float16 *t0,
-                int f0, const float *g1, _Float16 *t1, int f1, int32_t *status, hipStream_t stream) {
-  PrepArgs P{};
-  P.x = x;
-  P.dtype = dtype;
-  P.T = T;
-  P.cols = cols;
-  P.nconv = (T * (cols / 256) + 3) / 4;
-  P.X = X;
-  P.grid[0] = g0;
-  P.grid[1] = g1;
-  P.tab[0] = t0;
-  P.tab[1] = t1;
-  P.n[0] = kGridN[f0];
-  P.n[1] = kGridN[f1];
-  P.iq1[0] = f0 >= IQ1_S;
-  P.iq1[1] = f1 >= IQ1_S;
-  P.status = status;
-  const int ntab = (g0 ? 1 : 0) + (g1 ? 1 : 0);
-  hipLaunchKernelGGL(run_prep_kernel, dim3(static_cast<unsigned>(P.nconv + ntab)), dim3(256), 0, stream, P);
-  return launched_ok() ? IQ_OK : IQ_ERR_HIP;
-}
-
-#define IQ_BY_FMT(fmt, CALL)                      \
-  switch (fmt) {                                  \
-    case IQ2_XXS: CALL(IQ2_XXS); break;           \
-    case IQ2_XS: CALL(IQ2_XS); break;             \
-    case IQ2_S: CALL(IQ2_S); break;               \
-    case IQ1_S: CALL(IQ1_S); break;               \
-    default: CALL(IQ1_M); break;                  \
+template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
+  if (is_few(A.T, A.E)) {
+    const int64_t nb = A.hidden / 256, experts = A.npair < A.E ? A.npair : A.E;
+    int nw = 1;
+    while (nw < 8 && nw < nb) nw *= 2;
+    hipLaunchKernelGGL((few_up_kernel<F, P>), dim3(static_cast<unsigned>(experts * (A.inter / 16))), dim3(64 * nw), 0,
+                       stream, A);
+    return;
   }
+  const dim3 grid(static_cast<unsigned>(A.E * (A.inter / 256)));
+  if (A.npair <= 8 * static_cast<int64_t>(A.E))
+    hipLaunchKernelGGL((many_up_kernel<F, P, 1>), grid, dim3(512), 0, stream, A);
+  else
+    hipLaunchKernelGGL((many_up_kernel<F, P, 2>), grid, dim3(512), 0, stream, A);
+}
+
+template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
+  if (is_few(A.T, A.E)) {
+    hipLaunchKernelGGL((few_down_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
+                       dim3(64 * few_down_waves(P)), 0, stream, A);
+    return;
+  }
+  const dim3 grid(static_cast<unsigned>(A.E * (A.hidden / 256)));
+  if (A.npair <= 8 * static_cast<int64_t>(A.E))
+    hipLaunchKernelGGL((many_down_kernel<F, P, 1>), grid, dim3(512), 0, stream, A);
+  else
+    hipLaunchKernelGGL((many_down_kernel<F, P, 2>), grid, dim3(512), 0, stream, A);
+}
 
 }  // namespace
 }  // namespace iq
@@ -508,48 +701,75 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   using namespace iq;
   int rc = check_moe(fmt, down_fmt, hidden, inter, num_experts, dtype, T, top_k);
   if (rc != IQ_OK) return rc;
-  if (router && bad_dtype(router_dtype)) return IQ_ERR_DTYPE;
+  if (router && run_bad_dtype(router_dtype)) return IQ_ERR_DTYPE;
   if (!grid || !down_grid || (T && (!gate || !up || !down || !x || !ids || !weights || !y))) return IQ_ERR_NULL;
   if (router && top_k > num_experts) return IQ_ERR_ARG;
   if (T == 0) return IQ_OK;
-  const int E = num_experts;
-  const MoePlan P = plan_moe(fmt, down_fmt, hidden, inter, E, dtype, T, top_k);
-  if ((rc = check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
+  const MoePlan P = plan_moe(fmt, down_fmt, hidden, inter, num_experts, dtype, T, top_k);
+  if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
   char *base = ws_base(workspace);
-  _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab), *tab2 = reinterpret_cast<_Float16 *>(base + P.tab2);
-  const Tokens X{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile,
-                 P.x.parts};
-  const Tokens H{reinterpret_cast<_Float16 *>(base + P.hxo), reinterpret_cast<int32_t *>(base + P.heo), P.h.ntile,
-                 P.h.parts};
-  double *logits = reinterpret_cast<double *>(base + P.lo);
-  float *h = reinterpret_cast<float *>(base + P.ho);
-  const int64_t np = T * top_k;
-  if ((rc = launch_prep(x, dtype, T, hidden, X, grid, tab, fmt, down_grid, tab2, down_fmt, status, stream)) != IQ_OK)
-    return rc;
-  if (router) {
-    hipLaunchKernelGGL(router_kernel, waves4(T * E), dim3(256), 0, stream, x, dtype, router, router_dtype, T, hidden,
-                       E, logits);
-    if (!launched_ok()) return IQ_ERR_HIP;
-    hipLaunchKernelGGL(topk_kernel, dim3(static_cast<unsigned>(T)), dim3(64), 0, stream,
-                       static_cast<const double *>(logits), E, top_k, renormalize, ids, weights);
-    if (!launched_ok()) return IQ_ERR_HIP;
+  MoeArgs A{};
+  A.gate = gate;
+  A.up = up;
+  A.down = down;
+  A.hidden = hidden;
+  A.inter = inter;
+  A.E = num_experts;
+  A.top_k = top_k;
+  A.renorm = renormalize;
+  A.routed = router != nullptr;
+  A.T = T;
+  A.npair = T * top_k;
+  A.x = x;
+  A.router = router;
+  A.dtype = dtype;
+  A.rdtype = router_dtype;
+  A.X = Tokens{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile};
+  A.H = Tokens{reinterpret_cast<_Float16 *>(base + P.hxo), reinterpret_cast<int32_t *>(base + P.heo), P.h.ntile};
+  _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab), *dtab = reinterpret_cast<_Float16 *>(base + P.dtab);
+  A.tab = tab;
+  A.dtab = dtab;
+  A.logits = reinterpret_cast<double *>(base + P.lo);
+  A.ids = ids;
+  A.weights = weights;
+  A.h = reinterpret_cast<float *>(base + P.ho);
+  A.z = reinterpret_cast<float *>(base + P.zo);
+  A.y = y;
+  A.status = status;
+  A.books = one_codebook(fmt, grid, tab, status);
+  const Codebooks second = one_codebook(down_fmt, down_grid, dtab, status);
+  A.books.grid[1] = second.grid[0];
+  A.books.tab[1] = second.tab[0];
+  A.books.n[1] = second.n[0];
+  A.books.iq1[1] = second.iq1[0];
+  A.books.wg[1] = second.wg[0];
+  A.nconv = (P.x.ntile * (hidden / 256) + 1) / 2;
+  const int64_t nroute = router ? ((num_experts + 7) / 8) * ((T + kRouteTokens - 1) / kRouteTokens) : 0;
+  const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + A.books.wg[1] + nroute));
+  if (dtype == IQ_DTYPE_F32)
+    hipLaunchKernelGGL(route_kernel<2>, wgs, dim3(512), 0, stream, A);
+  else
+    hipLaunchKernelGGL(route_kernel<1>, wgs, dim3(512), 0, stream, A);
+  if (!run_launched()) return IQ_ERR_HIP;
+  const bool few = is_few(T, num_experts);
+  if (router && !few) {
+    hipLaunchKernelGGL(topk_kernel, dim3(static_cast<unsigned>(T)), dim3(64), 0, stream, A);
+    if (!run_launched()) return IQ_ERR_HIP;
   }
-#define CALL(F)                                                                                                     \
-  hipLaunchKernelGGL(gate_up_kernel<F>, waves4(np * (inter / 16)), dim3(256), 0, stream, gate, up, inter,           \
-                     hidden / 256, E, tab, X, np, top_k, static_cast<const int32_t *>(ids),                         \
-                     static_cast<const float *>(weights), h, status)
+#define CALL(F) dtype == IQ_DTYPE_F32 ? launch_up<F, 2>(A, stream) : launch_up<F, 1>(A, stream)
   IQ_BY_FMT(fmt, CALL)
 #undef CALL
-  if (!launched_ok()) return IQ_ERR_HIP;
-  if ((rc = launch_prep(h, IQ_DTYPE_F32, np, inter, H, nullptr, nullptr, 0, nullptr, nullptr, 0, status, stream)) !=
-      IQ_OK)
-    return rc;
-#define CALL(F)                                                                                                    \
-  hipLaunchKernelGGL(down_kernel<F>, waves4(T * (hidden / 16)), dim3(256), 0, stream, down, hidden, inter / 256, E, \
-                     tab2, H, T, top_k, static_cast<const int32_t *>(ids), dtype, y)
+  if (!run_launched()) return IQ_ERR_HIP;
+#define CALL(F) dtype == IQ_DTYPE_F32 ? launch_down<F, 2>(A, stream) : launch_down<F, 1>(A, stream)
   IQ_BY_FMT(down_fmt, CALL)
 #undef CALL
-  return launched_ok() ? IQ_OK : IQ_ERR_HIP;
+  if (!run_launched()) return IQ_ERR_HIP;
+  if (!few) {
+    hipLaunchKernelGGL(many_sum_kernel, dim3(static_cast<unsigned>((T * (hidden / 4) + 255) / 256)), dim3(256), 0,
+                       stream, A);
+    if (!run_launched()) return IQ_ERR_HIP;
+  }
+  return IQ_OK;
 }
 
 }  // extern "C"
