@@ -2,17 +2,24 @@
 // (include/iq_run.h).
 //
 // route_kernel brings the tokens into operand order, converts the codebooks and
-// forms the router's logits in fp64.  Then, by the number of tokens:
-//  few   up to 16 tokens (and 256 experts).  Launches cost more than arithmetic,
-//        so every workgroup of the next kernel picks the top_k itself, and there
-//        are three in all: few_up_kernel (16 rows of gate and up of one expert,
-//        blocks split over the waves) writes h in fp32, few_down_kernel (16
-//        columns of y, the chosen experts' blocks split over the waves) converts
-//        the h it needs and adds over experts in its accumulators.
-//  many  the choice is a launch of its own.  A workgroup takes 256 rows of one
-//        expert for up to 32 of the pairs routed to it, so that h leaves in
-//        operand order; the down projections leave one row per pair, and a last
-//        kernel adds each token's rows in the order of its ids.
+// forms the router's logits in fp64.  For up to 16 tokens (and 256 experts) a
+// launch costs more than picking the top_k does, so every workgroup of the next
+// kernel picks them itself and takes the expert of its rank among the chosen
+// ones; for more, the choice is a launch of its own and a workgroup is given an
+// expert, whose pairs it gathers from the ids.
+//
+// Gate and up (h in fp32, one row per pair):
+//  up_split_kernel  16 rows of gate and up, the blocks of K split over the waves:
+//                   where the chosen experts' rows alone would not fill the chip.
+//  up_rows_kernel   128 rows, each wave 16 of them over the whole of K.
+// Down:
+//  down_split_kernel  16 columns of y; the (expert, block) pairs split over the
+//                   waves, experts added up in the accumulators: no further launch.
+//  down_rows_kernel 256 columns of one expert for the pairs routed to it, h
+//                   converted once into LDS; sum_kernel adds each token's rows in
+//                   the order of its ids.
+
+#include <type_traits>
 
 #include "iq_run.hpp"
 
@@ -28,13 +35,13 @@ struct MoeArgs {
   int64_t T, npair;
   const void *x, *router;
   int dtype, rdtype;
-  Tokens X, H;             // tokens; h of the pairs (many)
+  Tokens X;
   const _Float16 *tab, *dtab;
   double *logits;          // [T, E]
   int32_t *ids;
   float *weights;
-  float *h;                // few: [pairs, inter] f32
-  float *z;                // many: [pairs, hidden] f32
+  float *h;                // [pairs, inter]
+  float *z;                // [pairs, hidden] (down_rows_kernel)
   void *y;
   int32_t *status;
   Codebooks books;
@@ -53,6 +60,7 @@ __device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w) {
   const int64_t ne = (A.E + 7) / 8, t0 = (w / ne) * kRouteTokens, e = (w % ne) * 8 + wave;
   if (e >= A.E) return;
   double s[kRouteTokens] = {};
+#pragma unroll 4
   for (int64_t k = lane * 8; k < A.hidden; k += 512) {
     float r[8], x[kRouteTokens][8];
     load8u(A.router, A.rdtype, e * A.hidden + k, r);
@@ -193,55 +201,53 @@ __global__ void __launch_bounds__(64) topk_kernel(MoeArgs A) {
 __device__ __forceinline__ float gated(float g, float u, float w) { return g / (1.0f + expf(-g)) * u * w; }
 
 // ---------------------------------------------------------------------------
-// Few tokens
+// The pairs of an expert
 // ---------------------------------------------------------------------------
-// The pairs' experts in LDS (-1: none), and which experts occur.
-__device__ __forceinline__ void few_active(const int *s_ids, int np, uint32_t *s_bits) {
-  if (threadIdx.x < kFewExperts / 32) s_bits[threadIdx.x] = 0;
-  __syncthreads();
-  for (int p = threadIdx.x; p < np; p += blockDim.x)
-    if (s_ids[p] >= 0) atomicOr(&s_bits[s_ids[p] >> 5], 1u << (s_ids[p] & 31));
-  __syncthreads();
-}
+// What a workgroup knows of the routing of few tokens.
+struct FewPairs {
+  int ids[kFewTokens * kMaxTopK];   // the pairs' experts (-1: none)
+  int list[kFewTokens * kMaxTopK];  // the pairs of this workgroup's expert, ascending
+  float w[kFewTokens * kMaxTopK];
+  uint32_t bits[kFewExperts / 32];  // the experts that occur
+  int n;
+};
 
-template <int F, int P>
-__global__ void __launch_bounds__(512) few_up_kernel(MoeArgs A) {
-  __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ f32x4 s_red[8 * 2 * 64];
-  __shared__ int s_ids[kFewTokens * kMaxTopK], s_list[kFewTokens * kMaxTopK];
-  __shared__ float s_w[kFewTokens * kMaxTopK];
-  __shared__ uint32_t s_bits[kFewExperts / 32];
-  __shared__ int s_n;
-  load_table<F>(s_tab, A.tab);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nw = blockDim.x >> 6, np = static_cast<int>(A.npair);
-  if (A.routed) {
+// The pairs' experts into LDS: picked here from the logits, or read.
+__device__ __forceinline__ void few_ids(const MoeArgs &A, FewPairs &S, bool pick) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int np = static_cast<int>(A.npair);
+  if (threadIdx.x < kFewExperts / 32) S.bits[threadIdx.x] = 0;
+  if (pick) {
     for (int t = wave; t < A.T; t += nw)
-      pick_top<4>(A.logits + static_cast<int64_t>(t) * A.E, A.E, A.top_k, A.renorm, s_ids + t * A.top_k,
-                  s_w + t * A.top_k);
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int p = threadIdx.x; p < np; p += blockDim.x) {
-        A.ids[p] = s_ids[p];
-        A.weights[p] = s_w[p];
-      }
+      pick_top<4>(A.logits + static_cast<int64_t>(t) * A.E, A.E, A.top_k, A.renorm, S.ids + t * A.top_k,
+                  S.w + t * A.top_k);
   } else {
     for (int p = threadIdx.x; p < np; p += blockDim.x) {
       const int e = A.ids[p];
       const bool bad = e < 0 || e >= A.E;
       if (bad && blockIdx.x == 0) raise_status(A.status, ST_BADID);
-      s_ids[p] = bad ? -1 : e;
-      s_w[p] = A.weights[p];
+      S.ids[p] = bad ? -1 : e;
+      S.w[p] = A.weights[p];
     }
   }
-  few_active(s_ids, np, s_bits);
-  // this workgroup's expert: the one of rank `slot` among those that occur
-  const int64_t nrt = A.inter / 16;
-  int slot = static_cast<int>(blockIdx.x / nrt), e = -1;
-  const int64_t rt = blockIdx.x % nrt;
+  __syncthreads();
+  for (int p = threadIdx.x; p < np; p += blockDim.x) {
+    if (pick && blockIdx.x == 0) {
+      A.ids[p] = S.ids[p];
+      A.weights[p] = S.w[p];
+    }
+    if (S.ids[p] >= 0) atomicOr(&S.bits[S.ids[p] >> 5], 1u << (S.ids[p] & 31));
+  }
+  __syncthreads();
+}
+
+// The expert of rank `slot` among those that occur, and its pairs; -1: there are not as many.
+__device__ __forceinline__ int few_expert(const MoeArgs &A, FewPairs &S, int slot) {
+  const int lane = threadIdx.x & 63, np = static_cast<int>(A.npair);
+  int e = -1;
 #pragma unroll
   for (int i = 0; i < kFewExperts / 32; ++i) {
-    uint32_t bits = __builtin_amdgcn_readfirstlane(s_bits[i]);
+    uint32_t bits = __builtin_amdgcn_readfirstlane(S.bits[i]);
     const int c = __builtin_popcount(bits);
     if (e < 0 && slot < c) {
       for (int k = 0; k < slot; ++k) bits &= bits - 1;
@@ -249,27 +255,41 @@ __global__ void __launch_bounds__(512) few_up_kernel(MoeArgs A) {
     }
     if (e < 0) slot -= c;
   }
-  if (e < 0) return;
-  if (wave == 0) {
+  if (e < 0) return -1;
+  if (threadIdx.x < 64) {
     int n = 0;
     for (int p0 = 0; p0 < np; p0 += 64) {
-      const bool hit = p0 + lane < np && s_ids[p0 + lane] == e;
+      const bool hit = p0 + lane < np && S.ids[p0 + lane] == e;
       const uint64_t b = __ballot(hit);
-      if (hit) s_list[n + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = p0 + lane;
+      if (hit) S.list[n + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = p0 + lane;
       n += __builtin_popcountll(b);
     }
-    if (lane == 0) s_n = n;
+    if (lane == 0) S.n = n;
   }
   __syncthreads();
-  const int count = s_n, n = lane & 15, q = lane >> 4;
+  return e;
+}
+
+template <int F, int P>
+__global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ f32x4 s_red[8 * 2 * 64];
+  __shared__ FewPairs S;
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  few_ids(A, S, A.routed);
+  const int64_t nrt = A.inter / 16, rt = blockIdx.x % nrt;
+  const int e = few_expert(A, S, static_cast<int>(blockIdx.x / nrt));
+  if (e < 0) return;
+  const int count = S.n, n = lane & 15, q = lane >> 4;
   const int64_t nb = A.hidden >> 8, row = e * A.inter + rt * 16 + n;
   const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
   for (int c0 = 0; c0 < count; c0 += 16) {
-    const int t = s_list[min(c0 + n, count - 1)] / A.top_k;
+    const int t = S.list[min(c0 + n, count - 1)] / A.top_k;
     const _Float16 *x0 = A.X.x16 + (q * 16 + t) * 8;  // one tile of tokens
     int et[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) et[k] = s_list[min(c0 + q * 4 + k, count - 1)] / A.top_k;
+    for (int k = 0; k < 4; ++k) et[k] = S.list[min(c0 + q * 4 + k, count - 1)] / A.top_k;
     f32x4 acc[2] = {};
     for (int64_t b = wave; b < nb; b += nw) {
       Raw raw[2];
@@ -297,8 +317,8 @@ __global__ void __launch_bounds__(512) few_up_kernel(MoeArgs A) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (c0 + q * 4 + k < count) {
-          const int p = s_list[c0 + q * 4 + k];
-          A.h[p * A.inter + rt * 16 + n] = gated(g[k], u[k], s_w[p]);
+          const int p = S.list[c0 + q * 4 + k];
+          A.h[p * A.inter + rt * 16 + n] = gated(g[k], u[k], S.w[p]);
         }
     }
   }
@@ -306,29 +326,24 @@ __global__ void __launch_bounds__(512) few_up_kernel(MoeArgs A) {
 
 // Waves split (expert, block of inter): each stages its tokens' h of that block
 // as the A operand (rows: tokens; absent ones zero) in LDS of its own.
-constexpr int few_down_waves(int parts) { return parts == 2 ? 4 : 8; }  // 8 KiB of LDS a part and wave
+constexpr int down_split_waves(int parts) { return parts == 2 ? 4 : 8; }  // 8 KiB of LDS a part and wave
 template <int F, int P>
-__global__ void __launch_bounds__(64 * few_down_waves(P)) few_down_kernel(MoeArgs A) {
-  constexpr int NW = few_down_waves(P);
+__global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(MoeArgs A) {
+  constexpr int NW = down_split_waves(P);
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ uint4 s_x[NW][P * 512];  // also the sums over the waves
-  __shared__ int s_ids[kFewTokens * kMaxTopK], s_ex[NW][16], s_active[kFewExperts];
-  __shared__ uint32_t s_bits[kFewExperts / 32];
+  __shared__ int s_ex[NW][16], s_active[kFewExperts];
+  __shared__ FewPairs S;
   load_table<F>(s_tab, A.dtab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int np = static_cast<int>(A.npair), n = lane & 15, q = lane >> 4;
-  for (int p = threadIdx.x; p < np; p += blockDim.x) {
-    const int e = A.ids[p];
-    s_ids[p] = e >= 0 && e < A.E ? e : -1;
-  }
   for (int i = lane; i < P * 512; i += 64) s_x[wave][i] = make_uint4(0, 0, 0, 0);
   if (lane < 16) s_ex[wave][lane] = 0;
-  __syncthreads();
-  few_active(s_ids, np, s_bits);
+  few_ids(A, S, false);
   int na = 0;
 #pragma unroll
   for (int i = 0; i < kFewExperts / 32; ++i) {
-    const uint32_t bits = __builtin_amdgcn_readfirstlane(s_bits[i]);
+    const uint32_t bits = __builtin_amdgcn_readfirstlane(S.bits[i]);
     if (wave == 0 && lane < 32 && ((bits >> lane) & 1u))
       s_active[na + __builtin_popcount(bits & ((1u << lane) - 1u))] = i * 32 + lane;
     na += __builtin_popcount(bits);
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(64 * few_down_waves(P)) few_down_kernel(MoeArg
     float v[4] = {};
     int token = -1;
     for (int p0 = 0; p0 < np; p0 += 64) {
-      uint64_t hits = __ballot(p0 + lane < np && s_ids[p0 + lane] == e);
+      uint64_t hits = __ballot(p0 + lane < np && S.ids[p0 + lane] == e);
       while (hits) {
         const int p = p0 + static_cast<int>(__builtin_ctzll(hits));
         hits &= hits - 1;
@@ -398,59 +413,66 @@ __global__ void __launch_bounds__(64 * few_down_waves(P)) few_down_kernel(MoeArg
   });
 }
 
-// ---------------------------------------------------------------------------
-// Many tokens
-// ---------------------------------------------------------------------------
 // Walks the pairs of one expert in ascending order, N at a time: f(list, count).
+// Few tokens: they are in LDS already; otherwise the ids are searched, 512 at a time.
+template <int N> struct PairWalk {
+  int list[512 + N], cnt[8];
+};
 template <int N, class Fn>
-__device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, int *s_list, int *s_cnt, Fn f) {
+__device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &S, Fn f) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int have = 0;
   for (int64_t p0 = 0; p0 < A.npair; p0 += 512) {
     const int64_t p = p0 + threadIdx.x;
     const bool hit = p < A.npair && A.ids[p] == e;
     const uint64_t b = __ballot(hit);
-    if (lane == 0) s_cnt[wave] = __builtin_popcountll(b);
+    if (lane == 0) S.cnt[wave] = __builtin_popcountll(b);
     __syncthreads();
     int at = have, total = 0;
     for (int w = 0; w < 8; ++w) {
-      const int c = s_cnt[w];
+      const int c = S.cnt[w];
       if (w < wave) at += c;
       total += c;
     }
-    if (hit) s_list[at + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = static_cast<int>(p);
+    if (hit) S.list[at + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = static_cast<int>(p);
     have += total;
     __syncthreads();
     const bool last = p0 + 512 >= A.npair;
     int head = 0;
     while (have - head >= N || (last && have > head)) {
-      f(s_list + head, min(N, have - head));
+      f(S.list + head, min(N, have - head));
       head += min(N, have - head);
     }
     if (head) {  // what is left moves to the front
       const int rest = have - head;
       int keep = 0;
-      if (static_cast<int>(threadIdx.x) < rest) keep = s_list[head + threadIdx.x];
+      if (static_cast<int>(threadIdx.x) < rest) keep = S.list[head + threadIdx.x];
       __syncthreads();
-      if (static_cast<int>(threadIdx.x) < rest) s_list[threadIdx.x] = keep;
+      if (static_cast<int>(threadIdx.x) < rest) S.list[threadIdx.x] = keep;
       have = rest;
       __syncthreads();
     }
   }
 }
 
-template <int F, int P, int C>
-__global__ void __launch_bounds__(512) many_up_kernel(MoeArgs A) {
+// 128 rows of gate and up of one expert: eight waves, 16 rows each.
+template <int F, int P, int C, bool FEW>
+__global__ void __launch_bounds__(512) up_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ int s_list[512 + N], s_cnt[8];
-  __shared__ uint32_t s_max[16][N];
+  __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.hidden >> 8, nblk = A.inter >> 8;
-  const int e = static_cast<int>(blockIdx.x / nblk);
-  const int64_t blk = blockIdx.x % nblk;
-  for_pairs<N>(A, e, s_list, s_cnt, [&](const int *list, int count) {
+  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per;
+  int e = static_cast<int>(blockIdx.x / per);
+  if constexpr (FEW) {
+    few_ids(A, S, A.routed);
+    e = few_expert(A, S, e);
+    if (e < 0) return;
+  }
+  const int64_t col = part * 128 + wave * 16 + n, row = e * A.inter + col;
+  const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
+  const auto body = [&](const int *list, int count) {
     const _Float16 *x0[C];
     int64_t e0[C][4];
 #pragma unroll
@@ -460,99 +482,6 @@ __global__ void __launch_bounds__(512) many_up_kernel(MoeArgs A) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)] / A.top_k;
     }
-    float h[2][C][4];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t row = e * A.inter + blk * 256 + (half * 8 + wave) * 16 + n;
-      const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
-      f32x4 acc[2][C] = {};
-      Raw raw[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
-      for (int64_t b = 0; b < nb; ++b) {
-        Raw next[2];
-        const int64_t bn = min(b + 1, nb - 1);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-        const _Float16 *xp[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
-        f32x4 part[2][C];
-        block_mma<F, P, C, 2>(raw, s_tab, xp, part);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          int ex[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) raw[r] = next[r];
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float w = A.weights[list[min(c * 16 + q * 4 + k, count - 1)]];
-          h[half][c][k] = gated(acc[0][c][k], acc[1][c][k], w);
-          uint32_t m = max_exponent(1, h[half][c][k]);
-#pragma unroll
-          for (int o = 8; o; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
-          if (n == 0) s_max[half * 8 + wave][c * 16 + q * 4 + k] = m;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = c * 16 + q * 4 + k;
-        uint32_t m = 1;
-        for (int w = 0; w < 16; ++w) m = max(m, s_max[w][i]);
-        if (i >= count) continue;
-        const int64_t p = list[i];
-        const int up = 141 - static_cast<int>(m);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int col = (half * 8 + wave) * 16 + n;
-          _Float16 hi, lo;
-          to_parts(h[half][c][k], up, hi, lo);
-          _Float16 *o = A.H.x16 + (blk * A.H.ntile + (p >> 4)) * P * 4096 +
-                        (((col & 63) >> 3) * 64 + (col >> 6) * 16 + (p & 15)) * 8 + (col & 7);
-          *o = hi;
-          if (P == 2) o[4096] = lo;
-        }
-        if (wave == 0 && n == 0) A.H.ex[blk * A.H.ntile * 16 + p] = -up;
-      }
-    __syncthreads();  // the list and the maxima are free again
-  });
-}
-
-template <int F, int P, int C>
-__global__ void __launch_bounds__(512) many_down_kernel(MoeArgs A) {
-  constexpr int N = 16 * C;
-  __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ int s_list[512 + N], s_cnt[8];
-  load_table<F>(s_tab, A.dtab);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.inter >> 8, nblk = A.hidden >> 8;
-  const int e = static_cast<int>(blockIdx.x / nblk);
-  const int64_t blk = blockIdx.x % nblk;
-  for_pairs<N>(A, e, s_list, s_cnt, [&](const int *list, int count) {
-    const _Float16 *x0[C];
-    int64_t e0[C][4];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t p = list[min(c * 16 + n, count - 1)];
-      x0[c] = A.H.x16 + (p >> 4) * P * 4096 + (q * 16 + (p & 15)) * 8;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)];
-    }
-    const int64_t col = blk * 256 + wave * 32 + n;  // two row tiles a wave
-    const uint8_t *rp[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
     f32x4 acc[2][C] = {};
     Raw raw[2];
 #pragma unroll
@@ -564,16 +493,16 @@ __global__ void __launch_bounds__(512) many_down_kernel(MoeArgs A) {
       for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
       const _Float16 *xp[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.H.ntile * P * 4096;
-      f32x4 part[2][C];
-      block_mma<F, P, C, 2>(raw, s_tab, xp, part);
+      for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
+      f32x4 sum[2][C];
+      block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         int ex[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ex[k] = A.H.ex[b * A.H.ntile * 16 + e0[c][k]];
+        for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex);
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) raw[r] = next[r];
@@ -581,15 +510,118 @@ __global__ void __launch_bounds__(512) many_down_kernel(MoeArgs A) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c * 16 + q * 4 + k < count)
+      for (int k = 0; k < 4; ++k) {
+        const int i = c * 16 + q * 4 + k;
+        if (i >= count) continue;
+        const int64_t p = list[i];
+        float w;
+        if constexpr (FEW)
+          w = S.w[p];
+        else
+          w = A.weights[p];
+        A.h[p * A.inter + col] = gated(acc[0][c][k], acc[1][c][k], w);
+      }
+  };
+  if constexpr (FEW) {
+    for (int c0 = 0; c0 < S.n; c0 += N) body(S.list + c0, min(N, S.n - c0));
+  } else {
+    for_pairs<N>(A, e, S, body);
+  }
+}
+
+// 256 columns of y of one expert: eight waves, 32 columns each.  The pairs' h
+// goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
+// block, so the conversion is repeated only by the hidden / 256 workgroups of an
+// expert.  z: one row per pair.
+template <int F, int P, int C, bool FEW>
+__global__ void __launch_bounds__(512) down_rows_kernel(MoeArgs A) {
+  constexpr int N = 16 * C, KB = 4 / P;
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ _Float16 s_h[KB][C][P * 4096];
+  __shared__ int s_ex[KB][N];
+  __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
+  load_table<F>(s_tab, A.dtab);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
+  const int nb = static_cast<int>(A.inter >> 8);
+  const int64_t per = A.hidden >> 8, part = blockIdx.x % per;
+  int e = static_cast<int>(blockIdx.x / per);
+  if constexpr (FEW) {
+    few_ids(A, S, false);
+    e = few_expert(A, S, e);
+    if (e < 0) return;
+  }
+  const int64_t col = part * 256 + wave * 32 + n;
+  const uint8_t *rp[2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) A.z[e0[c][k] * A.hidden + col + r * 16] = acc[r][c][k];
-  });
+  for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
+  const auto body = [&](const int *list, int count) {
+    f32x4 acc[2][C] = {};
+    Raw raw[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
+    for (int b0 = 0; b0 < nb; b0 += KB) {
+      const int kb = min(KB, nb - b0);
+      if (b0) __syncthreads();  // the blocks before are read
+      for (int i = wave; i < count * kb; i += 8) {
+        const int m = i / kb, j = i - m * kb;
+        const float4 f = *reinterpret_cast<const float4 *>(A.h + list[m] * A.inter + (b0 + j) * 256 + lane * 4);
+        const float v[4] = {f.x, f.y, f.z, f.w};
+        uint32_t x = 1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x = max_exponent(x, v[k]);
+        const int up = 141 - static_cast<int>(wave_max_u32(x));
+        _Float16 hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to_parts(v[k], up, hi[k], lo[k]);
+        _Float16 *o = &s_h[j][m >> 4][((n >> 1) * 64 + q * 16 + (m & 15)) * 8 + (n & 1) * 4];
+        *reinterpret_cast<uint2 *>(o) = __builtin_bit_cast(uint2, hi);
+        if (P == 2) *reinterpret_cast<uint2 *>(o + 4096) = __builtin_bit_cast(uint2, lo);
+        if (lane == 0) s_ex[j][m] = -up;
+      }
+      __syncthreads();
+      for (int j = 0; j < kb; ++j) {
+        Raw next[2];
+        const int bn = min(b0 + j + 1, nb - 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+        const _Float16 *xp[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
+        f32x4 sum[2][C];
+        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          int ex[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ex[k] = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
+#pragma unroll
+          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[r] = next[r];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = c * 16 + q * 4 + k;
+        if (i >= count) continue;
+        const int64_t p = list[i];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) A.z[p * A.hidden + col + r * 16] = acc[r][c][k];
+      }
+    __syncthreads();  // s_h is free again
+  };
+  if constexpr (FEW) {
+    for (int c0 = 0; c0 < S.n; c0 += N) body(S.list + c0, min(N, S.n - c0));
+  } else {
+    for_pairs<N>(A, e, S, body);
+  }
 }
 
 // y[t] = the sum of its pairs' rows, in the order of its ids
-__global__ void __launch_bounds__(256) many_sum_kernel(MoeArgs A) {
+__global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
   const int64_t per = A.hidden / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= A.T * per) return;
   const int64_t t = i / per, c = (i - t * per) * 4;
@@ -611,27 +643,28 @@ __global__ void __launch_bounds__(256) many_sum_kernel(MoeArgs A) {
 // Host
 // ---------------------------------------------------------------------------
 bool is_few(int64_t T, int E) { return T <= kFewTokens && E <= kFewExperts; }
+// Experts that np pairs reach at most.
+int64_t reached(int64_t np, int E) { return np < E ? np : E; }
+// K is split where whole rows would leave SIMDs without a wave (1,024 of them).
+bool split_up(const MoeArgs &A) { return is_few(A.T, A.E) && reached(A.npair, A.E) * (A.inter / 16) < 1024; }
+bool split_down(int64_t T, int E) { return T <= 2 && E <= kFewExperts; }
 
 struct MoePlan {
-  TokensPlan x, h;
-  size_t tab, dtab, xo, eo, lo, ho, hxo, heo, zo, bytes;
+  TokensPlan x;
+  size_t tab, dtab, xo, eo, lo, ho, zo, bytes;
 };
 MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int dtype, int64_t T, int top_k) {
   MoePlan p;
-  const bool few = is_few(T, E);
   const size_t np = static_cast<size_t>(T) * top_k;
   p.x = plan_tokens(T, hidden, dtype);
-  p.h = plan_tokens(few ? 0 : T * top_k, inter, dtype);
   p.tab = 0;
   p.dtab = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
   p.xo = p.dtab + ws_up(static_cast<size_t>(kCodebook[down_fmt]) * 16);
   p.eo = p.xo + ws_up(p.x.xbytes);
   p.lo = p.eo + ws_up(p.x.ebytes);
   p.ho = p.lo + ws_up(static_cast<size_t>(T) * E * 8);
-  p.hxo = p.ho + ws_up(few ? np * inter * 4 : 0);
-  p.heo = p.hxo + ws_up(p.h.xbytes);
-  p.zo = p.heo + ws_up(p.h.ebytes);
-  p.bytes = p.zo + ws_up(few ? 0 : np * hidden * 4) + kWsAlign;
+  p.zo = p.ho + ws_up(np * inter * 4);
+  p.bytes = p.zo + ws_up(split_down(T, E) ? 0 : np * hidden * 4) + kWsAlign;
   return p;
 }
 
@@ -645,39 +678,45 @@ int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int d
   if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   // the launches: routing, up, down, sum (pairs are counted in 32 bits)
   if (ntile * (hidden / 256) / 2 + 8 + ((E + 7) / 8) * ((T + kRouteTokens - 1) / kRouteTokens) >= kMaxWG ||
-      np >= kMaxWG || np * (inter / 16) >= kMaxWG * (is_few(T, E) ? 1 : 16) || E * (inter / 256) >= kMaxWG ||
-      E * (hidden / 256) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
+      np >= kMaxWG || E * (inter / 16) >= kMaxWG || E * (hidden / 16) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
     return IQ_ERR_SHAPE;
   return IQ_OK;
 }
 
 template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
-  if (is_few(A.T, A.E)) {
-    const int64_t nb = A.hidden / 256, experts = A.npair < A.E ? A.npair : A.E;
+  const int64_t experts = reached(A.npair, A.E);
+  if (split_up(A)) {
+    const int64_t nb = A.hidden / 256;
     int nw = 1;
     while (nw < 8 && nw < nb) nw *= 2;
-    hipLaunchKernelGGL((few_up_kernel<F, P>), dim3(static_cast<unsigned>(experts * (A.inter / 16))), dim3(64 * nw), 0,
-                       stream, A);
+    hipLaunchKernelGGL((up_split_kernel<F, P>), dim3(static_cast<unsigned>(experts * (A.inter / 16))), dim3(64 * nw),
+                       0, stream, A);
     return;
   }
-  const dim3 grid(static_cast<unsigned>(A.E * (A.inter / 256)));
-  if (A.npair <= 8 * static_cast<int64_t>(A.E))
-    hipLaunchKernelGGL((many_up_kernel<F, P, 1>), grid, dim3(512), 0, stream, A);
+  const unsigned per = static_cast<unsigned>(A.inter / 128);
+  if (is_few(A.T, A.E))
+    hipLaunchKernelGGL((up_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(experts) * per), dim3(512), 0,
+                       stream, A);
+  else if (A.npair <= 8 * static_cast<int64_t>(A.E))  // 8 pairs an expert on average: few have more than 16
+    hipLaunchKernelGGL((up_rows_kernel<F, P, 1, false>), dim3(A.E * per), dim3(512), 0, stream, A);
   else
-    hipLaunchKernelGGL((many_up_kernel<F, P, 2>), grid, dim3(512), 0, stream, A);
+    hipLaunchKernelGGL((up_rows_kernel<F, P, 2, false>), dim3(A.E * per), dim3(512), 0, stream, A);
 }
 
 template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
-  if (is_few(A.T, A.E)) {
-    hipLaunchKernelGGL((few_down_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
-                       dim3(64 * few_down_waves(P)), 0, stream, A);
+  if (split_down(A.T, A.E)) {
+    hipLaunchKernelGGL((down_split_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
+                       dim3(64 * down_split_waves(P)), 0, stream, A);
     return;
   }
-  const dim3 grid(static_cast<unsigned>(A.E * (A.hidden / 256)));
-  if (A.npair <= 8 * static_cast<int64_t>(A.E))
-    hipLaunchKernelGGL((many_down_kernel<F, P, 1>), grid, dim3(512), 0, stream, A);
+  const unsigned per = static_cast<unsigned>(A.hidden / 256);
+  if (is_few(A.T, A.E))
+    hipLaunchKernelGGL((down_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(reached(A.npair, A.E)) * per),
+                       dim3(512), 0, stream, A);
+  else if (A.npair <= 8 * static_cast<int64_t>(A.E))
+    hipLaunchKernelGGL((down_rows_kernel<F, P, 1, false>), dim3(A.E * per), dim3(512), 0, stream, A);
   else
-    hipLaunchKernelGGL((many_down_kernel<F, P, 2>), grid, dim3(512), 0, stream, A);
+    hipLaunchKernelGGL((down_rows_kernel<F, P, 2, false>), dim3(A.E * per), dim3(512), 0, stream, A);
 }
 
 }  // namespace
@@ -725,7 +764,6 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.dtype = dtype;
   A.rdtype = router_dtype;
   A.X = Tokens{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile};
-  A.H = Tokens{reinterpret_cast<_Float16 *>(base + P.hxo), reinterpret_cast<int32_t *>(base + P.heo), P.h.ntile};
   _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab), *dtab = reinterpret_cast<_Float16 *>(base + P.dtab);
   A.tab = tab;
   A.dtab = dtab;
@@ -751,8 +789,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   else
     hipLaunchKernelGGL(route_kernel<1>, wgs, dim3(512), 0, stream, A);
   if (!run_launched()) return IQ_ERR_HIP;
-  const bool few = is_few(T, num_experts);
-  if (router && !few) {
+  if (router && !is_few(T, num_experts)) {
     hipLaunchKernelGGL(topk_kernel, dim3(static_cast<unsigned>(T)), dim3(64), 0, stream, A);
     if (!run_launched()) return IQ_ERR_HIP;
   }
@@ -764,8 +801,8 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   IQ_BY_FMT(down_fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-  if (!few) {
-    hipLaunchKernelGGL(many_sum_kernel, dim3(static_cast<unsigned>((T * (hidden / 4) + 255) / 256)), dim3(256), 0,
+  if (!split_down(T, num_experts)) {
+    hipLaunchKernelGGL(sum_kernel, dim3(static_cast<unsigned>((T * (hidden / 4) + 255) / 256)), dim3(256), 0,
                        stream, A);
     if (!run_launched()) return IQ_ERR_HIP;
   }
