@@ -15,9 +15,12 @@ struct Lora {
   const void *a, *b;
   const float *scale;
   const int32_t *ids;
-  int n, rank, rpad;  // rpad: rank rounded up to 32, the width of v
-  float *v;           // [tokens rounded up to 16][rpad]
+  int n, rank, chunks;  // chunks of 32 ranks (bf16) or 16 (float32)
+  // v in operand order, [tile of 16 tokens][chunk]: bf16 the three bf16 values
+  // that add up to it, [3][lane][8]; float32 [lane][4]
+  void *v;
 };
+constexpr int kChunkBytes[2] = {3 * 1024, 1024};  // bf16, float32
 
 struct PrepArgs {
   const void *x;
@@ -97,9 +100,21 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
     for (int i = 0; i < 4; ++i) {
       const int tok = (l >> 4) * 4 + i;
       if (!((group >> tok) & 1u)) continue;
-      float *v = L.v + (tt * 16 + tok) * L.rpad + jj;
-      *v = jj < L.rank ? s[i] * scale : 0.0f;
-      if (rt + 1 == P.rtiles && L.rpad > P.rtiles * 16) v[16] = 0.0f;  // the rest of the last 32 ranks
+      float f = jj < L.rank ? s[i] * scale : 0.0f;
+      if (P.dtype == 1) {
+        uint16_t *v = static_cast<uint16_t *>(L.v) + (tt * L.chunks + (jj >> 5)) * 1536 +
+                      (((jj & 31) >> 3) * 16 + tok) * 8 + (jj & 7);
+        const bool pad = rt + 1 == P.rtiles && !(rt & 1);  // the upper half of the last 32 ranks is nobody's
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t top = __float_as_uint(f) & 0xffff0000u;
+          v[k * 512] = static_cast<uint16_t>(top >> 16);
+          if (pad) v[k * 512 + 256] = 0;
+          f -= __uint_as_float(top);
+        }
+      } else {
+        static_cast<float *>(L.v)[(tt * L.chunks + rt) * 256 + (((jj & 15) >> 2) * 16 + tok) * 4 + (jj & 3)] = f;
+      }
     }
   });
 }
@@ -127,79 +142,114 @@ __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
   lora_shrink(A, w / A.rtiles, static_cast<int>(w % A.rtiles), slot, s_red);
 }
 
-// acc[r][c] += B v of the adapters that the tile's tokens name; wave w of nw
-// takes every nw-th adapter of a tile.  fp32 v is the sum of three bf16 values
-// beside a bf16 B (no rounding), and goes through the fp32 cores beside an fp32 B.
+// acc[r][c] += B v of the adapters that the tiles' tokens name.  Of tile c, wave
+// w of nw takes the adapters whose turn t (in order of first use) has
+// (t + c) % nw == w; a round fetches one adapter for each of the C tiles before it
+// multiplies.  fp32 v is the sum of three bf16 values beside a bf16 B (no
+// rounding), and goes through the fp32 cores beside an fp32 B.  Rows of v of
+// other tokens hold anything; what they give is dropped.
 template <int P, int C, int R>
 __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t T, int64_t rows, int64_t row0,
                                             int wave, int nw, f32x4 (&acc)[R][C]) {
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  int turn = 0;
+  int mine[C], turn[C];
+  uint32_t todo[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int mine = tile_adapter(L, tt0 + c, T, lane);
-    uint32_t todo = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xffffu;
-    while (todo) {
-      const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(todo));
-      const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
-      todo &= ~group;
-      if (turn++ % nw != wave) continue;
-      f32x4 d[R];
+    mine[c] = tile_adapter(L, tt0 + c, T, lane);
+    todo[c] = static_cast<uint32_t>(__ballot(mine[c] >= 0)) & 0xffffu;
+    turn[c] = c;
+  }
+  for (;;) {
+    int a[C];
+    uint32_t group[C], any = 0;
 #pragma unroll
-      for (int r = 0; r < R; ++r) d[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      // tokens past T or of other adapters: their rows of v may hold anything, and are dropped below
-      const float *v = L.v + (min((tt0 + c) * 16 + n, (T + 15) / 16 * 16 - 1)) * L.rpad;
+    for (int c = 0; c < C; ++c) {
+      a[c] = 0;
+      group[c] = 0;
+      while (todo[c] && !group[c]) {
+        a[c] = __builtin_amdgcn_readlane(mine[c], __builtin_ctz(todo[c]));
+        const uint32_t g = static_cast<uint32_t>(__ballot(mine[c] == a[c])) & 0xffffu;
+        todo[c] &= ~g;
+        if (turn[c]++ % nw == wave) group[c] = g;
+      }
+      any |= group[c];
+    }
+    if (!any) return;
+    f32x4 d[R][C];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) d[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ch = 0; ch < L.chunks; ++ch) {
       if (P == 1) {
-        for (int j = q * 8; j < L.rpad; j += 32) {
-          float f[8];
-          load8u(v, 0, j, f);
-          bf16x8 part[3];
+        bf16x8 v[C][3], w[C][R];
+        const int j = ch * 32 + q * 8;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+        for (int c = 0; c < C; ++c) {
+          if (!group[c]) continue;
+          const uint16_t *vp = static_cast<const uint16_t *>(L.v) + ((tt0 + c) * L.chunks + ch) * 1536 + lane * 8;
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-              const uint32_t top = __float_as_uint(f[i]) & 0xffff0000u;
-              part[s][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
-              f[i] -= __uint_as_float(top);
-            }
+          for (int s = 0; s < 3; ++s) v[c][s] = *reinterpret_cast<const bf16x8 *>(vp + s * 512);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const int64_t row = min(row0 + r * 16 + n, rows - 1);
-            const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a) * rows + row) * L.rank;
-            bf16x8 w = {};
+            const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+            w[c][r] = bf16x8{};
             if (j + 8 <= L.rank) {
-              w = ldu<bf16x8>(b + j);
+              w[c][r] = ldu<bf16x8>(b + j);
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (j + i < L.rank) w[i] = __builtin_bit_cast(__bf16, b[j + i]);
+                if (j + i < L.rank) w[c][r][i] = __builtin_bit_cast(__bf16, b[j + i]);
             }
-#pragma unroll
-            for (int s = 0; s < 3; ++s) d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[s], w, d[r], 0, 0, 0);
           }
         }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (!group[c]) continue;
+#pragma unroll
+          for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              d[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c][s], w[c][r], d[r][c], 0, 0, 0);
+        }
       } else {
-        for (int j = q * 4; j < L.rpad; j += 16) {
-          const f32x4 f = *reinterpret_cast<const f32x4 *>(v + j);
+        f32x4 v[C], w[C][R];
+        const int j = ch * 16 + q * 4;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (!group[c]) continue;
+          v[c] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(L.v) +
+                                                  ((tt0 + c) * L.chunks + ch) * 256 + lane * 4);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const int64_t row = min(row0 + r * 16 + n, rows - 1);
-            const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a) * rows + row) * L.rank;
-            f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+            w[c][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (j + i < L.rank) w[i] = b[j + i];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[i], w[i], d[r], 0, 0, 0);
+              if (j + i < L.rank) w[c][r][i] = b[j + i];
           }
         }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (!group[c]) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              d[r][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[c][i], w[c][r][i], d[r][c], 0, 0, 0);
+        }
       }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if ((group >> (q * 4 + k)) & 1u)
+        if ((group[c] >> (q * 4 + k)) & 1u)
 #pragma unroll
-          for (int r = 0; r < R; ++r) acc[r][c][k] += d[r][k];
-    }
+          for (int r = 0; r < R; ++r) acc[r][c][k] += d[r][c][k];
   }
 }
 
@@ -239,28 +289,38 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t stride = A.X.ntile * P * 4096;  // between blocks of the token operand
+  const int64_t first = min(static_cast<int64_t>(wave), A.nb - 1);
   Raw raw[R];
-  if (wave < A.nb) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r] + static_cast<int64_t>(wave) * Geo<F>::BYTES, q);
-  }
+  for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r] + first * Geo<F>::BYTES, q);
+  Steps<P, C> x;
+  const _Float16 *xp[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) xp[c] = x0[c] + first * stride;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
   __syncthreads();
   for (int64_t b = wave; b < A.nb; b += nw) {
+    int4 e[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) e[c] = *reinterpret_cast<const int4 *>(A.X.ex + b * A.X.ntile * 16 + e0[c]);
     Raw next[R];
     const int64_t bn = min(b + nw, A.nb - 1);
 #pragma unroll
     for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-    const _Float16 *xp[C];
+    const _Float16 *xn[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
+    for (int c = 0; c < C; ++c) xn[c] = x0[c] + bn * stride;
+    __builtin_amdgcn_sched_barrier(0x38f);
     f32x4 part[R][C];
-    block_mma<F, P, C, R>(raw, s_mem, xp, part);
+    block_mma_ahead<F, P, C, R>(raw, s_mem, xp, xn, x, part);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + b * A.X.ntile * 16 + e0[c]);
-      const int ex[4] = {e.x, e.y, e.z, e.w};
+      const int ex[4] = {e[c].x, e[c].y, e[c].z, e[c].w};
 #pragma unroll
       for (int r = 0; r < R; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+      xp[c] = xn[c];
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) raw[r] = next[r];
@@ -279,18 +339,18 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
 
 struct LinearPlan {
   TokensPlan x;
-  int rpad;
+  int chunks;
   size_t tab, xo, eo, vo, bytes;
 };
 LinearPlan plan_linear(int fmt, int64_t cols, int dtype, int64_t T, int rank) {
   LinearPlan p;
   p.x = plan_tokens(T, cols, dtype);
-  p.rpad = (rank + 31) / 32 * 32;
+  p.chunks = dtype == IQ_DTYPE_F32 ? (rank + 15) / 16 : (rank + 31) / 32;
   p.tab = 0;
   p.xo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
   p.eo = p.xo + ws_up(p.x.xbytes);
   p.vo = p.eo + ws_up(p.x.ebytes);
-  p.bytes = p.vo + ws_up(static_cast<size_t>(p.x.ntile) * 16 * p.rpad * 4) + kWsAlign;
+  p.bytes = p.vo + ws_up(static_cast<size_t>(p.x.ntile) * p.chunks * kChunkBytes[dtype == IQ_DTYPE_F32]) + kWsAlign;
   return p;
 }
 
@@ -354,8 +414,7 @@ int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const 
   char *base = ws_base(workspace);
   _Float16 *tab = reinterpret_cast<_Float16 *>(base + P.tab);
   const Tokens X{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile};
-  const Lora L{lora_a, lora_b, lora_scale, lora_ids, num_adapters, rank, P.rpad,
-               reinterpret_cast<float *>(base + P.vo)};
+  const Lora L{lora_a, lora_b, lora_scale, lora_ids, num_adapters, rank, P.chunks, base + P.vo};
   PrepArgs A{};
   A.x = x;
   A.dtype = dtype;

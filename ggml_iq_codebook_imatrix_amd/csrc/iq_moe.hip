@@ -2,11 +2,11 @@
 // (include/iq_run.h).
 //
 // route_kernel brings the tokens into operand order, converts the codebooks and
-// forms the router's logits in fp64.  For up to 16 tokens (and 256 experts) a
+// forms the router's logits in fp64.  For up to 8 tokens (and 256 experts) a
 // launch costs more than picking the top_k does, so every workgroup of the next
-// kernel picks them itself and takes the expert of its rank among the chosen
-// ones; for more, the choice is a launch of its own and a workgroup is given an
-// expert, whose pairs it gathers from the ids.
+// kernel picks them itself; for more, the choice is a launch of its own.  Up to
+// 16 tokens a workgroup takes the expert of its rank among the chosen ones; for
+// more it is given an expert, whose pairs it gathers from the ids.
 //
 // Gate and up (h in fp32, one row per pair):
 //  up_split_kernel  16 rows of gate and up, the blocks of K split over the waves:
@@ -31,7 +31,7 @@ constexpr int kFewTokens = 16, kFewExperts = 256, kMaxTopK = 64;
 struct MoeArgs {
   const uint8_t *gate, *up, *down;
   int64_t hidden, inter;
-  int E, top_k, renorm, routed;
+  int E, top_k, renorm, pick;  // pick: few tokens' top_k is picked by the up kernel
   int64_t T, npair;
   const void *x, *router;
   int dtype, rdtype;
@@ -51,39 +51,53 @@ struct MoeArgs {
 // ---------------------------------------------------------------------------
 // Routing
 // ---------------------------------------------------------------------------
-constexpr int kRouteTokens = 4;  // tokens a wave carries past one row of the router
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-// One wave: the logits of one expert for four tokens.  Summed in fp64, so that
-// no order of summation can swap neighbours in the ranking.
-__device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t ne = (A.E + 7) / 8, t0 = (w / ne) * kRouteTokens, e = (w % ne) * 8 + wave;
-  if (e >= A.E) return;
-  double s[kRouteTokens] = {};
-#pragma unroll 4
-  for (int64_t k = lane * 8; k < A.hidden; k += 512) {
-    float r[8], x[kRouteTokens][8];
-    load8u(A.router, A.rdtype, e * A.hidden + k, r);
+// The logits of 16 tokens and 16 experts on the fp64 matrix cores, K split over
+// the eight waves.  In fp64, so that no order of summation can swap neighbours in
+// the ranking.  v_mfma_f64_16x16x4: lane l holds k = l / 16 of token (A) and
+// expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
+template <int P>
+__device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w, double *s_red) {
+  constexpr int U = 4;  // loads in flight
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ne = (A.E + 15) / 16, nb = static_cast<int>(A.hidden >> 8);
+  const int64_t t0 = w / ne * 16, e0 = w % ne * 16;
+  const int64_t k0 = wave * 32 + (lane >> 4) * 8;  // 32 of each 256 columns
+  const int64_t xr = min(t0 + (lane & 15), A.T - 1) * A.hidden + k0;
+  const int64_t rr = min(e0 + (lane & 15), static_cast<int64_t>(A.E) - 1) * A.hidden + k0;
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+  for (int b = 0; b < nb; b += U) {
+    float x[U][8], r[U][8];
 #pragma unroll
-    for (int i = 0; i < kRouteTokens; ++i) load8u(A.x, A.dtype, min(t0 + i, A.T - 1) * A.hidden + k, x[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double rd = static_cast<double>(r[j]);
-#pragma unroll
-      for (int i = 0; i < kRouteTokens; ++i)
-        if (t0 + i < A.T) s[i] = fma(rd, static_cast<double>(x[i][j]), s[i]);
+    for (int u = 0; u < U; ++u) {
+      const int at = min(b + u, nb - 1) * 256;
+      load8u(A.x, P == 1, xr + at, x[u]);
+      load8u(A.router, A.rdtype, rr + at, r[u]);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u < nb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(x[u][i]), static_cast<double>(r[u][i]), acc,
+                                                     0, 0, 0);
   }
 #pragma unroll
-  for (int i = 0; i < kRouteTokens; ++i) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) s[i] += __shfl_xor(s[i], o, 64);
-    if (lane == 0 && t0 + i < A.T) A.logits[(t0 + i) * A.E + e] = s[i];
+  for (int i = 0; i < 4; ++i) s_red[(wave * 4 + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    const int i = threadIdx.x >> 6;
+    double s = s_red[i * 64 + lane];
+    for (int v = 1; v < 8; ++v) s += s_red[(v * 4 + i) * 64 + lane];
+    const int64_t t = t0 + (lane >> 4) + 4 * i, e = e0 + (lane & 15);
+    if (t < A.T && e < A.E) A.logits[t * A.E + e] = s;
   }
 }
 
 template <int P>
 __global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
+  __shared__ double s_red[8 * 4 * 64];
   int64_t w = blockIdx.x;
   if (w < A.nconv) {
     const int64_t nb = A.hidden >> 8, i = w * 2 + (threadIdx.x >> 8);
@@ -95,7 +109,7 @@ __global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
     convert_codebook(A.books, static_cast<int>(w));
     return;
   }
-  route_logits(A, w - A.books.wg[0] - A.books.wg[1]);
+  route_logits<P>(A, w - A.books.wg[0] - A.books.wg[1], s_red);
 }
 
 template <int CTRL> __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
   __shared__ FewPairs S;
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  few_ids(A, S, A.routed);
+  few_ids(A, S, A.pick);
   const int64_t nrt = A.inter / 16, rt = blockIdx.x % nrt;
   const int e = few_expert(A, S, static_cast<int>(blockIdx.x / nrt));
   if (e < 0) return;
@@ -457,7 +471,7 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
 
 // 128 rows of gate and up of one expert: eight waves, 16 rows each.
 template <int F, int P, int C, bool FEW>
-__global__ void __launch_bounds__(512) up_rows_kernel(MoeArgs A) {
+__global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
@@ -466,7 +480,7 @@ __global__ void __launch_bounds__(512) up_rows_kernel(MoeArgs A) {
   const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
   if constexpr (FEW) {
-    few_ids(A, S, A.routed);
+    few_ids(A, S, A.pick);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
@@ -482,27 +496,38 @@ __global__ void __launch_bounds__(512) up_rows_kernel(MoeArgs A) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)] / A.top_k;
     }
+    const int64_t stride = A.X.ntile * P * 4096;  // between blocks of the token operand
     f32x4 acc[2][C] = {};
     Raw raw[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
+    Steps<P, C> x;
+    const _Float16 *xp[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) xp[c] = x0[c];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
     for (int64_t b = 0; b < nb; ++b) {
+      int ex[C][4];
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ex[c][k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
       Raw next[2];
       const int64_t bn = min(b + 1, nb - 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-      const _Float16 *xp[C];
+      const _Float16 *xn[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * A.X.ntile * P * 4096;
+      for (int c = 0; c < C; ++c) xn[c] = x0[c] + bn * stride;
+      __builtin_amdgcn_sched_barrier(0x38f);
       f32x4 sum[2][C];
-      block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
+      block_mma_ahead<F, P, C, 2>(raw, s_tab, xp, xn, x, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        int ex[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex);
+        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex[c]);
+        xp[c] = xn[c];
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) raw[r] = next[r];
@@ -534,7 +559,7 @@ __global__ void __launch_bounds__(512) up_rows_kernel(MoeArgs A) {
 // block, so the conversion is repeated only by the hidden / 256 workgroups of an
 // expert.  z: one row per pair.
 template <int F, int P, int C, bool FEW>
-__global__ void __launch_bounds__(512) down_rows_kernel(MoeArgs A) {
+__global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C, KB = 4 / P;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ _Float16 s_h[KB][C][P * 4096];
@@ -626,14 +651,25 @@ __global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
   if (i >= A.T * per) return;
   const int64_t t = i / per, c = (i - t * per) * 4;
   float s[4] = {};
-  for (int k = 0; k < A.top_k; ++k) {
-    const int e = A.ids[t * A.top_k + k];
-    if (e < 0 || e >= A.E) {
-      if (c == 0) raise_status(A.status, ST_BADID);
-      continue;
+  for (int k0 = 0; k0 < A.top_k; k0 += 8) {  // eight rows in flight
+    float4 v[8];
+    bool ok[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t p = t * A.top_k + min(k0 + k, A.top_k - 1);
+      v[k] = *reinterpret_cast<const float4 *>(A.z + p * A.hidden + c);
+      const int e = A.ids[p];
+      ok[k] = e >= 0 && e < A.E;  // a pair without an expert has no row
+      if (!ok[k] && c == 0) raise_status(A.status, ST_BADID);
+      ok[k] = ok[k] && k0 + k < A.top_k;
     }
-    const float4 v = *reinterpret_cast<const float4 *>(A.z + (t * A.top_k + k) * A.hidden + c);
-    s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s[0] += ok[k] ? v[k].x : 0.0f;
+      s[1] += ok[k] ? v[k].y : 0.0f;
+      s[2] += ok[k] ? v[k].z : 0.0f;
+      s[3] += ok[k] ? v[k].w : 0.0f;
+    }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) store1(A.y, A.dtype, t * A.hidden + c + j, s[j]);
@@ -643,6 +679,9 @@ __global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
 // Host
 // ---------------------------------------------------------------------------
 bool is_few(int64_t T, int E) { return T <= kFewTokens && E <= kFewExperts; }
+// A wave picks a token's experts in 2 us (of 128), a launch for it takes 4 to 5:
+// picked in the next kernel while its eight waves do it in one go.
+bool is_pick(int64_t T, int E) { return T <= 8 && E <= kFewExperts; }
 // Experts that np pairs reach at most.
 int64_t reached(int64_t np, int E) { return np < E ? np : E; }
 // K is split where whole rows would leave SIMDs without a wave (1,024 of them).
@@ -677,7 +716,7 @@ int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int d
   const int64_t ntile = (T + 15) / 16, np = T * top_k;
   if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   // the launches: routing, up, down, sum (pairs are counted in 32 bits)
-  if (ntile * (hidden / 256) / 2 + 8 + ((E + 7) / 8) * ((T + kRouteTokens - 1) / kRouteTokens) >= kMaxWG ||
+  if (ntile * (hidden / 256) / 2 + 8 + ((E + 15) / 16) * ntile >= kMaxWG ||
       np >= kMaxWG || E * (inter / 16) >= kMaxWG || E * (hidden / 16) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
     return IQ_ERR_SHAPE;
   return IQ_OK;
@@ -756,7 +795,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.E = num_experts;
   A.top_k = top_k;
   A.renorm = renormalize;
-  A.routed = router != nullptr;
+  A.pick = router != nullptr && is_pick(T, num_experts);
   A.T = T;
   A.npair = T * top_k;
   A.x = x;
@@ -782,14 +821,14 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.books.iq1[1] = second.iq1[0];
   A.books.wg[1] = second.wg[0];
   A.nconv = (P.x.ntile * (hidden / 256) + 1) / 2;
-  const int64_t nroute = router ? ((num_experts + 7) / 8) * ((T + kRouteTokens - 1) / kRouteTokens) : 0;
+  const int64_t nroute = router ? ((num_experts + 15) / 16) * P.x.ntile : 0;
   const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + A.books.wg[1] + nroute));
   if (dtype == IQ_DTYPE_F32)
     hipLaunchKernelGGL(route_kernel<2>, wgs, dim3(512), 0, stream, A);
   else
     hipLaunchKernelGGL(route_kernel<1>, wgs, dim3(512), 0, stream, A);
   if (!run_launched()) return IQ_ERR_HIP;
-  if (router && !is_few(T, num_experts)) {
+  if (router && !A.pick) {
     hipLaunchKernelGGL(topk_kernel, dim3(static_cast<unsigned>(T)), dim3(64), 0, stream, A);
     if (!run_launched()) return IQ_ERR_HIP;
   }

@@ -255,6 +255,48 @@ __device__ __forceinline__ void block_mma(const Raw (&raw)[R], const uint4 *tab,
   }
 }
 
+// The same with the token operand read ahead in global memory.  Loads return in
+// order, so a step's operand asked for after the next block's payload waits for
+// that as well, which comes from HBM: operands are therefore asked for four
+// steps ahead (x holds four), and the payload of the next block right before
+// this block's steps, half a block before anything waits behind it.
+template <int P, int C> struct Steps {
+  half8v v[4][C][P];
+};
+template <int P, int C>
+__device__ __forceinline__ void load_step(Steps<P, C> &x, int i, const _Float16 *const (&xp)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int p = 0; p < P; ++p) x.v[i & 3][c][p] = *reinterpret_cast<const half8v *>(xp[c] + p * 4096 + i * 512);
+}
+template <int F, int P, int C, int R>
+__device__ __forceinline__ void block_mma_ahead(const Raw (&raw)[R], const uint4 *tab, const _Float16 *const (&xp)[C],
+                                                const _Float16 *const (&xn)[C], Steps<P, C> &x,
+                                                f32x4 (&part)[R][C]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const half8v w = group_half8<F>(raw[r], i, tab);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          part[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.v[i & 3][c][p], w, part[r][c], 0, 0, 0);
+    }
+    if (i < 4)
+      load_step<P, C>(x, i + 4, xp);
+    else
+      load_step<P, C>(x, i - 4, xn);
+    __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
+  }
+}
+
 // acc += 2^ex * d * part
 __device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d, const int ex[4]) {
 #pragma unroll
