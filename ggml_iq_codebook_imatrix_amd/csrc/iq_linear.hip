@@ -25,7 +25,7 @@ constexpr int kChunkBytes[2] = {3 * 1024, 1024};  // bf16, float32
 struct PrepArgs {
   const void *x;
   int dtype;
-  int64_t T, cols, nconv;  // nconv: workgroups that convert (two blocks of a tile each)
+  int64_t T, cols, nconv;  // nconv: workgroups that convert (eight tokens each)
   Tokens X;
   Codebooks books;
   Lora L;
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
   __shared__ f32x4 s_red[8 * 64];
   int64_t w = blockIdx.x;
   if (w < A.nconv) {
-    const int64_t nb = A.cols >> 8, i = w * 2 + (threadIdx.x >> 8);
-    if (i < nb * A.X.ntile) convert_tile<P>(A.x, A.dtype, A.T, A.cols, A.X, i % nb, i / nb, threadIdx.x & 255);
+    const int64_t t = w * 8 + (threadIdx.x >> 6);
+    if (t < A.T) convert_token<P>(A.x, A.dtype, A.cols, A.X, t, threadIdx.x & 63);
     return;
   }
   w -= A.nconv;
@@ -302,9 +302,6 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
   for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
   __syncthreads();
   for (int64_t b = wave; b < A.nb; b += nw) {
-    int4 e[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) e[c] = *reinterpret_cast<const int4 *>(A.X.ex + b * A.X.ntile * 16 + e0[c]);
     Raw next[R];
     const int64_t bn = min(b + nw, A.nb - 1);
 #pragma unroll
@@ -317,13 +314,20 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
     block_mma_ahead<F, P, C, R>(raw, s_mem, xp, xn, x, part);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int ex[4] = {e[c].x, e[c].y, e[c].z, e[c].w};
 #pragma unroll
-      for (int r = 0; r < R; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]), ex);
+      for (int r = 0; r < R; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]));
       xp[c] = xn[c];
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) raw[r] = next[r];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + e0[c]);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      acc[r][c] = f32x4{ldexpf(acc[r][c][0], e.x), ldexpf(acc[r][c][1], e.y), ldexpf(acc[r][c][2], e.z),
+                        ldexpf(acc[r][c][3], e.w)};
   }
   if (A.L.rank) lora_expand<P, C, R>(A.L, tt0, A.T, A.rows, row0, wave, nw, acc);
   reduce_waves<R * C, G>(&acc[0][0], reinterpret_cast<f32x4 *>(s_mem), nw, [&](int tile, int l, const f32x4 &s) {
@@ -362,7 +366,7 @@ int check_linear(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int 
   if (rank < 0 || rank > 1024) return IQ_ERR_ARG;
   const int64_t ntile = (T + 15) / 16;
   // the preparing launch: conversion, codebook, adapters
-  if (ntile * (cols / 256) / 2 + 8 + ntile * 16 * ((rank + 31) / 32 * 2) >= kMaxWG) return IQ_ERR_SHAPE;
+  if ((T + 7) / 8 + 8 + ntile * 16 * ((rank + 15) / 16) >= kMaxWG) return IQ_ERR_SHAPE;
   if (ntile > 4 * 65535) return IQ_ERR_SHAPE;
   return IQ_OK;
 }
@@ -420,7 +424,7 @@ int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const 
   A.dtype = dtype;
   A.T = T;
   A.cols = cols;
-  A.nconv = (P.x.ntile * (cols / 256) + 1) / 2;
+  A.nconv = (T + 7) / 8;
   A.X = X;
   A.books = one_codebook(fmt, grid, tab, status);
   A.L = L;

@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
   __shared__ double s_red[8 * 4 * 64];
   int64_t w = blockIdx.x;
   if (w < A.nconv) {
-    const int64_t nb = A.hidden >> 8, i = w * 2 + (threadIdx.x >> 8);
-    if (i < nb * A.X.ntile) convert_tile<P>(A.x, A.dtype, A.T, A.hidden, A.X, i % nb, i / nb, threadIdx.x & 255);
+    const int64_t t = w * 8 + (threadIdx.x >> 6);
+    if (t < A.T) convert_token<P>(A.x, A.dtype, A.hidden, A.X, t, threadIdx.x & 63);
     return;
   }
   w -= A.nconv;
@@ -212,6 +212,17 @@ __global__ void __launch_bounds__(64) topk_kernel(MoeArgs A) {
     pick_top<64>(A.logits + t * A.E, A.E, A.top_k, A.renorm, A.ids + t * A.top_k, A.weights + t * A.top_k);
 }
 
+// The four of a block's values whose place in the operand is the lane's: elements
+// 4 (lane % 2) .. + 3 of group lane / 2.
+__device__ __forceinline__ void load_h(const float *h, int lane, float v[4]) {
+  const float *p = h + (lane >> 1) * 8 + (lane & 1) * 2;
+  const float2 a = *reinterpret_cast<const float2 *>(p), b = *reinterpret_cast<const float2 *>(p + 4);
+  v[0] = a.x;
+  v[1] = b.x;
+  v[2] = a.y;
+  v[3] = b.y;
+}
+
 __device__ __forceinline__ float gated(float g, float u, float w) { return g / (1.0f + expf(-g)) * u * w; }
 
 // ---------------------------------------------------------------------------
@@ -301,22 +312,16 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
   for (int c0 = 0; c0 < count; c0 += 16) {
     const int t = S.list[min(c0 + n, count - 1)] / A.top_k;
     const _Float16 *x0 = A.X.x16 + (q * 16 + t) * 8;  // one tile of tokens
-    int et[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) et[k] = S.list[min(c0 + q * 4 + k, count - 1)] / A.top_k;
     f32x4 acc[2] = {};
     for (int64_t b = wave; b < nb; b += nw) {
       Raw raw[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r] + b * Geo<F>::BYTES, q);
-      int ex[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ex[k] = A.X.ex[b * 16 + et[k]];
       const _Float16 *const xp[1] = {x0 + b * P * 4096};
       f32x4 part[2][1];
       block_mma<F, P, 1, 2>(raw, s_tab, xp, part);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) scale_add(acc[r], part[r][0], block_scale<F>(raw[r]), ex);
+      for (int r = 0; r < 2; ++r) scale_add(acc[r], part[r][0], block_scale<F>(raw[r]));
     }
     __syncthreads();
 #pragma unroll
@@ -331,8 +336,8 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (c0 + q * 4 + k < count) {
-          const int p = S.list[c0 + q * 4 + k];
-          A.h[p * A.inter + rt * 16 + n] = gated(g[k], u[k], S.w[p]);
+          const int p = S.list[c0 + q * 4 + k], ex = A.X.ex[p / A.top_k];
+          A.h[p * A.inter + rt * 16 + n] = gated(ldexpf(g[k], ex), ldexpf(u[k], ex), S.w[p]);
         }
     }
   }
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
   const int nb = static_cast<int>(A.inter >> 8);
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 16;
   _Float16 *xs = reinterpret_cast<_Float16 *>(&s_x[wave][0]);
-  const int at = (((lane & 15) >> 1) * 64 + q * 16) * 8 + (lane & 1) * 4;  // where columns 4 lane .. + 3 go, token 0
+  const int at = (((lane & 15) >> 1) * 64 + q * 16) * 8 + (lane & 1) * 4;  // the lane's place, token 0
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int task = wave; task < na * nb; task += NW) {
     const int e = __builtin_amdgcn_readfirstlane(s_active[task / nb]), b = task % nb;
@@ -400,8 +405,10 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = 0.0f;
         }
-        const float4 f = *reinterpret_cast<const float4 *>(A.h + p * A.inter + b * 256 + lane * 4);
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        float f[4];
+        load_h(A.h + p * A.inter + b * 256, lane, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += f[j];
       }
     }
     stage(token, v);
@@ -488,13 +495,10 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
   const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
   const auto body = [&](const int *list, int count) {
     const _Float16 *x0[C];
-    int64_t e0[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t t = list[min(c * 16 + n, count - 1)] / A.top_k;
       x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e0[c][k] = list[min(c * 16 + q * 4 + k, count - 1)] / A.top_k;
     }
     const int64_t stride = A.X.ntile * P * 4096;  // between blocks of the token operand
     f32x4 acc[2][C] = {};
@@ -508,11 +512,6 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
     for (int64_t b = 0; b < nb; ++b) {
-      int ex[C][4];
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ex[c][k] = A.X.ex[b * A.X.ntile * 16 + e0[c][k]];
       Raw next[2];
       const int64_t bn = min(b + 1, nb - 1);
 #pragma unroll
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex[c]);
+        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]));
         xp[c] = xn[c];
       }
 #pragma unroll
@@ -544,7 +543,8 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
           w = S.w[p];
         else
           w = A.weights[p];
-        A.h[p * A.inter + col] = gated(acc[0][c][k], acc[1][c][k], w);
+        const int ex = A.X.ex[p / A.top_k];
+        A.h[p * A.inter + col] = gated(ldexpf(acc[0][c][k], ex), ldexpf(acc[1][c][k], ex), w);
       }
   };
   if constexpr (FEW) {
@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
       if (b0) __syncthreads();  // the blocks before are read
       for (int i = wave; i < count * kb; i += 8) {
         const int m = i / kb, j = i - m * kb;
-        const float4 f = *reinterpret_cast<const float4 *>(A.h + list[m] * A.inter + (b0 + j) * 256 + lane * 4);
-        const float v[4] = {f.x, f.y, f.z, f.w};
+        float v[4];
+        load_h(A.h + list[m] * A.inter + (b0 + j) * 256, lane, v);
         uint32_t x = 1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x = max_exponent(x, v[k]);
@@ -616,11 +616,12 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
         block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          int ex[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ex[k] = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
+          for (int k = 0; k < 4; ++k) {
+            const int ex = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
 #pragma unroll
-          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]), ex);
+            for (int r = 0; r < 2; ++r) acc[r][c][k] += ldexpf(block_scale<F>(raw[r]) * sum[r][c][k], ex);
+          }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) raw[r] = next[r];
@@ -716,7 +717,7 @@ int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int d
   const int64_t ntile = (T + 15) / 16, np = T * top_k;
   if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   // the launches: routing, up, down, sum (pairs are counted in 32 bits)
-  if (ntile * (hidden / 256) / 2 + 8 + ((E + 15) / 16) * ntile >= kMaxWG ||
+  if ((T + 7) / 8 + 8 + ((E + 15) / 16) * ntile >= kMaxWG ||
       np >= kMaxWG || E * (inter / 16) >= kMaxWG || E * (hidden / 16) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
     return IQ_ERR_SHAPE;
   return IQ_OK;
@@ -820,7 +821,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.books.n[1] = second.n[0];
   A.books.iq1[1] = second.iq1[0];
   A.books.wg[1] = second.wg[0];
-  A.nconv = (P.x.ntile * (hidden / 256) + 1) / 2;
+  A.nconv = (T + 7) / 8;
   const int64_t nroute = router ? ((num_experts + 15) / 16) * P.x.ntile : 0;
   const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + A.books.wg[1] + nroute));
   if (dtype == IQ_DTYPE_F32)

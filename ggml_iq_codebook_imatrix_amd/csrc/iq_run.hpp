@@ -5,8 +5,8 @@
 // A weight is d * m * v: d the block's fp16 scale, m the group's odd multiplier,
 // v its signed codebook value.  The products run on the fp16 matrix cores:
 // m * v is formed in packed fp16 (exact for the layouts' codebooks: at most 11
-// bits), d and the tokens' power-of-two block scales are applied in fp32 to
-// each 256-column block's sum.
+// bits), d is applied in fp32 to each 256-column block's sum, and the token's
+// power-of-two scale to the whole sum.
 //
 // Operand layout (v_mfma_f32_16x16x32_f16): the weights are B, lane l holding
 // eight consecutive k of row n = l % 16; the tokens are A, lane l holding the
@@ -16,6 +16,9 @@
 // use it: lane quarter q = l / 16 takes the block's 64 columns from 64 q on,
 // eight at a step, so that a lane's share of the payload is contiguous (two or
 // three wide loads a block) and a step's eight values are one codebook entry.
+// Within the eight, value j and value j + 4 share a register (kept_at): the signs
+// of the four pairs are then one bit apart, and bringing them to the sign places
+// is an addition (x + x), which issues at twice the rate of a shift.
 #pragma once
 
 #include "iq_common.hpp"
@@ -42,9 +45,9 @@ inline int run_check_ws(size_t need, const void *ws, size_t have) {
 }
 
 // Tokens in fp16: x16 [block][tile of 16 tokens][part][step 0..7][lane][8], the
-// A operand of a step as 1 KiB of consecutive memory; ex [block][tokens]: the
-// power of two that undoes the block's scaling.  What lies past the last token
-// is left unwritten and not read.
+// A operand of a step as 1 KiB of consecutive memory; ex [tokens]: the power of
+// two that undoes a token's scaling.  What lies past the last token is left
+// unwritten and not read.
 struct Tokens {
   _Float16 *x16;
   int32_t *ex;
@@ -60,7 +63,7 @@ inline TokensPlan plan_tokens(int64_t T, int64_t cols, int dtype) {
   p.ntile = (T + 15) / 16;
   p.parts = dtype == IQ_DTYPE_F32 ? 2 : 1;
   p.xbytes = static_cast<size_t>(cols / 256) * p.ntile * p.parts * 8192;
-  p.ebytes = static_cast<size_t>(cols / 256) * p.ntile * 64;
+  p.ebytes = static_cast<size_t>(p.ntile) * 64;
   return p;
 }
 
@@ -169,6 +172,9 @@ template <int F> __device__ __forceinline__ float block_scale(const Raw &r) {
   return Geo<F>::IQ1 ? d : d * 0.125f;  // exact: a power of two
 }
 
+// Which of a group's eight values the operands' element h holds.
+__device__ constexpr int kept_at(int h) { return (h >> 1) + 4 * (h & 1); }
+
 // m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16).
 template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab) {
   uint32_t k, ls, mask = 0, h = 0;
@@ -208,16 +214,17 @@ template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int
     for (int p = 0; p < 4; ++p)  // m g + m delta, rounded once
       o[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
   } else {
-    // The eighth sign is the parity of the seven (IQ2_S holds it).  Bit 2p of
-    // the mask to 2p and bit 2p + 1 to 2p + 16, so that one shift brings a
-    // pair's signs home; what else the two shifts leave behind is masked there.
+    // The eighth sign is the parity of the seven (IQ2_S holds it).  Signs 3 and
+    // 7 to bits 15 and 31, the places of the last register's pair; each doubling
+    // brings the pair before it there.
     if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
-    uint32_t sp = mask | (mask << 15);
-    asm("" : "+v"(sp));  // keeps shifts from being merged into multiplications by constants (a quarter of the rate)
+    uint32_t t = mask * 0x1001000u;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 3; p >= 0; --p) {
       const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
-      o[p] = __builtin_bit_cast(uint32_t, v) ^ ((sp << (15 - 2 * p)) & 0x80008000u);
+      o[p] = __builtin_bit_cast(uint32_t, v) ^ (t & 0x80008000u);
+      asm("" : "+v"(t));  // keeps the doublings from being merged into shifts or multiplications
+      t += t;
     }
   }
   return __builtin_bit_cast(half8v, make_uint4(o[0], o[1], o[2], o[3]));
@@ -297,10 +304,10 @@ __device__ __forceinline__ void block_mma_ahead(const Raw (&raw)[R], const uint4
   }
 }
 
-// acc += 2^ex * d * part
-__device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d, const int ex[4]) {
+// acc += d * part
+__device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] += ldexpf(d * part[k], ex[k]);
+  for (int k = 0; k < 4; ++k) acc[k] = fmaf(d, part[k], acc[k]);
 }
 
 // ---------------------------------------------------------------------------
@@ -318,39 +325,56 @@ __device__ __forceinline__ void to_parts(float v, int n, _Float16 &hi, _Float16 
   lo = finite_f(f) ? static_cast<_Float16>(f - static_cast<float>(hi)) : static_cast<_Float16>(0.0f);
 }
 
-// 256 threads convert one block of one tile of 16 tokens: thread = (token,
-// sixteenth of the block), so that 16 neighbouring lanes hold one token.
+// One wave converts one token: its largest exponent, then its values (read
+// again, from cache).  The tile's other tokens are neighbouring waves', so that
+// the 16-byte pieces of a line are written at about the same time.
 template <int P>
-__device__ __forceinline__ void convert_tile(const void *x, int dtype, int64_t T, int64_t cols, const Tokens &X,
-                                             int64_t b, int64_t tile, int tid) {
-  const int tok = tid >> 4, c = tid & 15;
-  const int64_t t = tile * 16 + tok;
-  if (t >= T) return;  // whole groups of 16 lanes
-  float v[16];
-  load8u(x, dtype, t * cols + b * 256 + c * 16, v);
-  load8u(x, dtype, t * cols + b * 256 + c * 16 + 8, v + 8);
+__device__ __forceinline__ void convert_token(const void *x, int dtype, int64_t cols, const Tokens &X, int64_t t,
+                                              int lane) {
+  constexpr int U = 4;  // loads in flight, 512 columns each
   uint32_t e = 1;
+  for (int64_t k = 0; k < cols; k += 512 * U) {
+    float v[U][8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) e = max_exponent(e, v[j]);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) e = max(e, static_cast<uint32_t>(__shfl_xor(static_cast<int>(e), o, 64)));
-  const int n = 141 - static_cast<int>(e);
-  _Float16 *p = X.x16 + (b * X.ntile + tile) * P * 4096;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {  // group 2c + g of the block: quarter c / 4, step 2 (c % 4) + g
-    half8v hi, lo;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      _Float16 a, b2;
-      to_parts(v[8 * g + j], n, a, b2);
-      hi[j] = a;
-      lo[j] = b2;
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = k + u * 512 + lane * 8;
+      load8u(x, dtype, t * cols + (col < cols ? col : 0), v[u]);  // past the row: its first values again
     }
-    const int at = ((2 * (c & 3) + g) * 64 + (c >> 2) * 16 + tok) * 8;
-    *reinterpret_cast<half8v *>(p + at) = hi;
-    if (P == 2) *reinterpret_cast<half8v *>(p + 4096 + at) = lo;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e = max_exponent(e, v[u][j]);
   }
-  if (c == 0) X.ex[b * X.ntile * 16 + t] = -n;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) e = max(e, static_cast<uint32_t>(__shfl_xor(static_cast<int>(e), o, 64)));
+  const int n = 141 - static_cast<int>(e);
+  for (int64_t k = 0; k < cols; k += 512 * U) {
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = k + u * 512 + lane * 8;
+      load8u(x, dtype, t * cols + (col < cols ? col : 0), v[u]);  // past the row: its first values again
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = k + u * 512 + lane * 8;
+      if (col >= cols) continue;
+      const int g = static_cast<int>(col & 255) >> 3;  // group of the block: quarter g / 8, step g % 8
+      half8v hi, lo;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        _Float16 a, b;
+        to_parts(v[u][kept_at(h)], n, a, b);
+        hi[h] = a;
+        lo[h] = b;
+      }
+      _Float16 *p = X.x16 + ((col >> 8) * X.ntile + (t >> 4)) * P * 4096 +
+                    ((g & 7) * 64 + (g >> 3) * 16 + (t & 15)) * 8;
+      *reinterpret_cast<half8v *>(p) = hi;
+      if (P == 2) *reinterpret_cast<half8v *>(p + 4096) = lo;
+    }
+  }
+  if (lane == 0) X.ex[t] = -n;
 }
 
 // One codebook entry per thread.  Every product with a multiplier is exact in
@@ -367,7 +391,7 @@ __device__ __forceinline__ void convert_codebook(const Codebooks &B, int wg) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const auto check = [&](float f) { inexact |= static_cast<float>(static_cast<_Float16>(f)) != f; };
-    o[j] = static_cast<_Float16>(g[j]);
+    o[j] = static_cast<_Float16>(g[kept_at(j)]);
     check(g[j]);
     if (B.iq1[which]) {
       check(15.0f * (g[j] + 0.125f));

@@ -16,13 +16,13 @@
  *    most 6 significant bits (IQ2; IQ1: value +- 1/8 at most 7), as {1,3,5} and
  *    {-1,0,1} have; any other codebook is rounded to fp16, and the product again
  *    (relative 2^-11 each), and IQ_STATUS_ROUNDED is raised.
- *  - each token's 256-column block is scaled by the power of two that brings its
- *    largest finite magnitude under 2^15 and held in fp16: exact for bf16 tokens
- *    (what lies 2^-29 or more below the block's largest value is rounded by less
- *    than 2^-39 of it); fp32 tokens are held as the sum of two fp16 values
- *    (relative 2^-22 of the value).
- *  - the block scale d and the power of two are applied in fp32 to each block's
- *    fp32 sum, and blocks are added in fp32.
+ *  - each token is scaled by the power of two that brings its largest finite
+ *    magnitude under 2^15 and held in fp16: exact for bf16 tokens (what lies 2^-29
+ *    or more below the token's largest value is rounded by less than 2^-39 of it);
+ *    fp32 tokens are held as the sum of two fp16 values (relative 2^-22 of the
+ *    value).
+ *  - the block scale d is applied in fp32 to each 256-column block's fp32 sum,
+ *    blocks are added in fp32, and the power of two is taken back at the end.
  * Infinities and NaN in a token reach that token's outputs only.
  */
 #ifndef IQ_RUN_H
