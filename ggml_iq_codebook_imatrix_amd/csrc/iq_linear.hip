@@ -341,6 +341,133 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
   });
 }
 
+// More tokens: the eight waves are KG groups that take every KG-th block and
+// 8 / KG groups that take 16 R rows each; the C token tiles of a chunk of KG
+// blocks lie in LDS for all of them (64 KiB), the next chunk's on their way in
+// registers.
+template <int F, int P, int C, int R, int KG>
+__global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
+  constexpr int RG = 8 / KG, XU = KG * C * P, G = 4, kTab = Geo<F>::N;
+  typedef Payload<F, R, 1> Pay;
+  __shared__ uint4 s_tab[kTab];
+  __shared__ u32x4 s_x[XU * 512];
+  __shared__ u32x4 s_pay[8][Pay::kUnits];
+  static_assert(KG == 1 || XU * 512 >= 8 * G * 64, "the sums over the waves fit");
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / RG;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * RG + wave % RG) * 16 * R;
+  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * C, rowbytes = A.nb * Geo<F>::BYTES;
+  const uint8_t *end = A.packed + A.rows * rowbytes;
+  Pay pay;
+  pay.init([&](int i) { return A.packed + min(row0 + i, A.rows - 1) * rowbytes; });
+  u32x4 xr[XU];
+  // chunk ch of the token operand: 512 threads, XU units of 16 bytes each
+  const auto load_x = [&](int64_t ch) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XU; ++i) {
+      const int64_t b = min(ch * KG + i / (C * P), A.nb - 1);
+      const int64_t tile = min(tt0 + i / P % C, A.X.ntile - 1);
+      xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[((b * A.X.ntile + tile) * P + i % P) * 512 + threadIdx.x];
+    }
+  };
+  const auto store_x = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XU; ++i) s_x[i * 512 + threadIdx.x] = xr[i];
+  };
+  f32x4 acc[R][C];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t chunks = (A.nb + KG - 1) / KG;
+  pay.load(min(static_cast<int64_t>(kg), A.nb - 1), end);
+  load_x(0);
+  pay.store(s_pay[wave]);
+  store_x();
+  __syncthreads();
+  for (int64_t ch = 0; ch < chunks; ++ch) {
+    if (ch + 1 < chunks) {
+      pay.load(min((ch + 1) * KG + kg, A.nb - 1), end);
+      load_x(ch + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0x38f);
+    if (ch * KG + kg < A.nb) {
+      Raw raw[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) raw[r] = Pay::raw(s_pay[wave], r, 0);
+      const _Float16 *xp[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) xp[c] = reinterpret_cast<const _Float16 *>(s_x + (kg * C + c) * P * 512 + lane);
+      f32x4 part[R][C];
+      block_mma<F, P, C, R>(raw, s_tab, xp, part);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]));
+    }
+    if (ch + 1 < chunks) {
+      __syncthreads();  // the chunk is read
+      pay.store(s_pay[wave]);
+      store_x();
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + min((tt0 + c) * 16 + q * 4, A.X.ntile * 16 - 4));
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      acc[r][c] = f32x4{ldexpf(acc[r][c][0], e.x), ldexpf(acc[r][c][1], e.y), ldexpf(acc[r][c][2], e.z),
+                        ldexpf(acc[r][c][3], e.w)};
+  }
+  if (A.L.rank) {  // four token tiles at a time: what a round fetches is held in registers
+    constexpr int CB = C < 4 ? C : 4;
+#pragma unroll
+    for (int c0 = 0; c0 < C; c0 += CB) {
+      f32x4 a[R][CB];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) a[r][c] = acc[r][c0 + c];
+      lora_expand<P, CB, R>(A.L, tt0 + c0, A.T, A.rows, row0, kg, KG, a);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) acc[r][c0 + c] = a[r][c];
+    }
+  }
+  const auto put = [&](int64_t r0, int tile, int l, const f32x4 &s) {
+    const int64_t row = r0 + (tile / C) * 16 + (l & 15);
+    if (row >= A.rows) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t t = (tt0 + tile % C) * 16 + (l >> 4) * 4 + k;
+      if (t < A.T) store1(A.y, P == 1, t * A.rows + row, s[k]);
+    }
+  };
+  if constexpr (KG == 1) {
+#pragma unroll
+    for (int i = 0; i < R * C; ++i) put(row0, i, lane, acc[i / C][i % C]);
+  } else {  // the KG groups' sums, in their order
+    f32x4 *red = reinterpret_cast<f32x4 *>(s_x);
+#pragma unroll
+    for (int g = 0; g < R * C; g += G) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < G; ++j) red[(wave * G + j) * 64 + lane] = acc[(g + j) / C][(g + j) % C];
+      __syncthreads();
+      for (int i = threadIdx.x; i < RG * G * 64; i += 512) {
+        const int rg = i / (G * 64), rest = i % (G * 64);
+        f32x4 s = red[rg * G * 64 + rest];
+#pragma unroll
+        for (int k = 1; k < KG; ++k) s += red[(k * RG + rg) * G * 64 + rest];
+        put((static_cast<int64_t>(blockIdx.x) * RG + rg) * 16 * R, g + rest / 64, rest & 63, s);
+      }
+    }
+  }
+}
+
 struct LinearPlan {
   TokensPlan x;
   int chunks;
@@ -380,13 +507,24 @@ void launch_few(const LinearArgs &A, hipStream_t stream) {
   hipLaunchKernelGGL((linear_few_kernel<F, P, C, R>), grid, dim3(64 * nw), 0, stream, A);
 }
 
+template <int F, int P, int C, int R, int KG>
+void launch_tile(const LinearArgs &A, hipStream_t stream) {
+  const int64_t rows = 8 / KG * 16 * R;
+  hipLaunchKernelGGL((linear_tile_kernel<F, P, C, R, KG>),
+                     dim3(static_cast<unsigned>((A.rows + rows - 1) / rows),
+                          static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+                     dim3(512), 0, stream, A);
+}
+
 template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
   if (A.X.ntile == 1)
     launch_few<F, P, 1, 1>(A, stream);
   else if (A.X.ntile == 2)
-    launch_few<F, P, 2, 2>(A, stream);
+    launch_tile<F, P, 2, 2, 4 / P>(A, stream);
+  else if (P == 2 || A.X.ntile <= 4)
+    launch_tile<F, P, 4, 2, 2 / P>(A, stream);
   else
-    launch_few<F, P, 4, 2>(A, stream);
+    launch_tile<F, P, P == 2 ? 4 : 8, 2, 1>(A, stream);
 }
 
 }  // namespace

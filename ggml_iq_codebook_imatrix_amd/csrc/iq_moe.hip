@@ -476,60 +476,94 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
   }
 }
 
-// 128 rows of gate and up of one expert: eight waves, 16 rows each.
+// 128 rows of gate and up of one expert: eight waves, 16 rows each.  The pairs'
+// tokens lie in LDS for all of them, two blocks at a time, the next two on their
+// way in registers.
 template <int F, int P, int C, bool FEW>
 __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C;
+  constexpr int N = 16 * C, KC = 2, XU = KC * C * P;
+  typedef Payload<F, 2, KC> Pay;
   __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ u32x4 s_x[XU * 512];
+  __shared__ u32x4 s_pay[8][Pay::kUnits];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per;
+  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per, rowbytes = nb * Geo<F>::BYTES;
   int e = static_cast<int>(blockIdx.x / per);
   if constexpr (FEW) {
     few_ids(A, S, A.pick);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col = part * 128 + wave * 16 + n, row = e * A.inter + col;
-  const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
-  const auto body = [&](const int *list, int count) {
-    const _Float16 *x0[C];
+  const int64_t col = part * 128 + wave * 16 + n, row0 = e * A.inter + part * 128 + wave * 16;
+  const int64_t size = A.E * A.inter * rowbytes;
+  const uint8_t *gend = A.gate + size, *uend = A.up + size;
+  Pay pay;
+  pay.init([&](int i) { return (i < 16 ? A.gate : A.up) + (row0 + (i & 15)) * rowbytes; });
+  // the units of rows 0 .. 15 are gate's: a lane's unit ends with its matrix
+  const auto load_pay = [&](int64_t b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t t = list[min(c * 16 + n, count - 1)] / A.top_k;
-      x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
+    for (int i = 0; i < Pay::kPer; ++i) {
+      const uint8_t *p = pay.at[i] + b * Geo<F>::BYTES;
+      const uint8_t *end = i * 64 + lane < 16 * Pay::U ? gend : uend;
+      pay.v[i] = load_unit(p, end);
     }
-    const int64_t stride = A.X.ntile * P * 4096;  // between blocks of the token operand
-    f32x4 acc[2][C] = {};
-    Raw raw[2];
+  };
+  const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
+    const int m = threadIdx.x & 15;  // a thread copies the same row of every tile
+    u32x4 xr[XU];
+    const auto load_x = [&](int64_t b0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
-    Steps<P, C> x;
-    const _Float16 *xp[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) xp[c] = x0[c];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
-    for (int64_t b = 0; b < nb; ++b) {
-      Raw next[2];
-      const int64_t bn = min(b + 1, nb - 1);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-      const _Float16 *xn[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) xn[c] = x0[c] + bn * stride;
-      __builtin_amdgcn_sched_barrier(0x38f);
-      f32x4 sum[2][C];
-      block_mma_ahead<F, P, C, 2>(raw, s_tab, xp, xn, x, sum);
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]));
-        xp[c] = xn[c];
+      for (int i = 0; i < XU; ++i) {
+        const int c = i / P % C, slot = c * 16 + m;
+        if (slot < count) {
+          const int64_t b = min(b0 + i / (C * P), nb - 1), t = list[slot] / A.top_k;
+          const int64_t at = ((b * A.X.ntile + (t >> 4)) * P + i % P) * 512 + (threadIdx.x & ~15) + (t & 15);
+          xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[at];
+        }
       }
+    };
+    const auto store_x = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) raw[r] = next[r];
+      for (int i = 0; i < XU; ++i)
+        if (i / P % C * 16 + m < count) s_x[i * 512 + threadIdx.x] = xr[i];
+    };
+    f32x4 acc[2][C] = {};
+    load_pay(0);
+    load_x(0);
+    pay.store(s_pay[wave]);
+    store_x();
+    __syncthreads();
+    for (int64_t b0 = 0; b0 < nb; b0 += KC) {
+      const bool more = b0 + KC < nb;
+      if (more) {
+        load_pay(b0 + KC);
+        load_x(b0 + KC);
+      }
+      __builtin_amdgcn_sched_barrier(0x38f);
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        if (b0 + k >= nb) break;
+        Raw raw[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[r] = Pay::raw(s_pay[wave], r, k);
+        const _Float16 *xp[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xp[c] = reinterpret_cast<const _Float16 *>(s_x + (k * C + c) * P * 512 + lane);
+        f32x4 sum[2][C];
+        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]));
+      }
+      __syncthreads();  // the blocks are read (and, at the end, free for the next pairs)
+      if (more) {
+        pay.store(s_pay[wave]);
+        store_x();
+        __syncthreads();
+      }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -554,36 +588,36 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
   }
 }
 
-// 256 columns of y of one expert: eight waves, 32 columns each.  The pairs' h
+// 128 columns of y of one expert: eight waves, 16 columns each.  The pairs' h
 // goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
-// block, so the conversion is repeated only by the hidden / 256 workgroups of an
+// block, so the conversion is repeated only by the hidden / 128 workgroups of an
 // expert.  z: one row per pair.
 template <int F, int P, int C, bool FEW>
 __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KB = 4 / P;
+  constexpr int N = 16 * C, KC = 2, KB = 4 / P;
+  typedef Payload<F, 1, KC> Pay;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ _Float16 s_h[KB][C][P * 4096];
+  __shared__ u32x4 s_pay[8][Pay::kUnits];
   __shared__ int s_ex[KB][N];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.dtab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
   const int nb = static_cast<int>(A.inter >> 8);
-  const int64_t per = A.hidden >> 8, part = blockIdx.x % per;
+  const int64_t per = A.hidden >> 7, part = blockIdx.x % per, rowbytes = static_cast<int64_t>(nb) * Geo<F>::BYTES;
   int e = static_cast<int>(blockIdx.x / per);
   if constexpr (FEW) {
     few_ids(A, S, false);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col = part * 256 + wave * 32 + n;
-  const uint8_t *rp[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
-  const auto body = [&](const int *list, int count) {
-    f32x4 acc[2][C] = {};
-    Raw raw[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r], q);
+  const int64_t col0 = part * 128 + wave * 16;
+  const uint8_t *end = A.down + A.E * A.hidden * rowbytes;
+  Pay pay;
+  pay.init([&](int i) { return A.down + (e * A.hidden + col0 + i) * rowbytes; });
+  const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
+    f32x4 acc[C] = {};
+    pay.load(0, end);
     for (int b0 = 0; b0 < nb; b0 += KB) {
       const int kb = min(KB, nb - b0);
       if (b0) __syncthreads();  // the blocks before are read
@@ -604,27 +638,28 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
         if (lane == 0) s_ex[j][m] = -up;
       }
       __syncthreads();
-      for (int j = 0; j < kb; ++j) {
-        Raw next[2];
-        const int bn = min(b0 + j + 1, nb - 1);
+      for (int j0 = 0; j0 < kb; j0 += KC) {
+        pay.store(s_pay[wave]);  // read by this wave alone
+        if (b0 + j0 + KC < nb) pay.load(b0 + j0 + KC, end);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-        const _Float16 *xp[C];
+        for (int k = 0; k < KC; ++k) {
+          const int j = j0 + k;
+          if (j >= kb) break;
+          Raw raw[1];
+          raw[0] = Pay::raw(s_pay[wave], 0, k);
+          const _Float16 *xp[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
-        f32x4 sum[2][C];
-        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
+          for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
+          f32x4 sum[1][C];
+          block_mma<F, P, C, 1>(raw, s_tab, xp, sum);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+          for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int ex = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
-#pragma unroll
-            for (int r = 0; r < 2; ++r) acc[r][c][k] += ldexpf(block_scale<F>(raw[r]) * sum[r][c][k], ex);
-          }
+            for (int i = 0; i < 4; ++i) {
+              const int ex = s_ex[j][c * 16 + q * 4 + i];  // past count: of rows not stored
+              acc[c][i] += ldexpf(block_scale<F>(raw[0]) * sum[0][c][i], ex);
+            }
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) raw[r] = next[r];
       }
     }
 #pragma unroll
@@ -632,10 +667,7 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = c * 16 + q * 4 + k;
-        if (i >= count) continue;
-        const int64_t p = list[i];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) A.z[p * A.hidden + col + r * 16] = acc[r][c][k];
+        if (i < count) A.z[list[i] * A.hidden + col0 + n] = acc[c][k];
       }
     __syncthreads();  // s_h is free again
   };
@@ -749,7 +781,7 @@ template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
                        dim3(64 * down_split_waves(P)), 0, stream, A);
     return;
   }
-  const unsigned per = static_cast<unsigned>(A.hidden / 256);
+  const unsigned per = static_cast<unsigned>(A.hidden / 128);
   if (is_few(A.T, A.E))
     hipLaunchKernelGGL((down_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(reached(A.npair, A.E)) * per),
                        dim3(512), 0, stream, A);

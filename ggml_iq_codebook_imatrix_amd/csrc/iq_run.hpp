@@ -31,6 +31,7 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // arrays of it stay in registers, of uint4 they did not
 
 constexpr int ST_ROUNDED = IQ_STATUS_ROUNDED;
 constexpr int kCodebook[5] = {256, 512, 1024, 2048, 2048};
@@ -309,6 +310,59 @@ __device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = fmaf(d, part[k], acc[k]);
 }
+
+// 16 bytes of a payload that ends at `end`.  A row's last unit may reach into the
+// next row, but not past the end: there the bytes come one by one.
+__device__ __forceinline__ u32x4 load_unit(const uint8_t *p, const uint8_t *end) {
+  if (p + 16 <= end) return ldu<u32x4>(p);
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j)
+    if (p + j < end) {
+      const uint32_t v = static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] |= (j >> 2) == k ? v : 0u;
+    }
+  return w;
+}
+
+// A wave's payload through LDS of its own.  Read straight into operands, a
+// block's fields touch 16 rows in pieces of 64 bytes and less, and every line is
+// asked for two to three times: the requests, not the bytes, then bound the
+// kernels.  Here KC blocks of 16 R rows come in as consecutive 16-byte units (U a
+// row, from any address), are kept in registers while the blocks before are
+// multiplied, and the fields are read back from LDS (which takes any alignment).
+template <int F, int R, int KC> struct Payload {
+  static constexpr int U = (KC * Geo<F>::BYTES + 15) / 16, kUnits = R * 16 * U, kPer = (kUnits + 63) / 64;
+  const uint8_t *at[kPer];
+  u32x4 v[kPer];
+  // rowp(i): row i of the wave's 16 R
+  template <class Fn> __device__ __forceinline__ void init(Fn rowp) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = min(i * 64 + lane, kUnits - 1);
+      at[i] = rowp(u / U) + (u % U) * 16;
+    }
+  }
+  // blocks b .. b + KC - 1; end: the payload's
+  __device__ __forceinline__ void load(int64_t b, const uint8_t *end) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = load_unit(at[i] + b * Geo<F>::BYTES, end);
+  }
+  __device__ __forceinline__ void store(u32x4 *lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i * 64 + lane < kUnits) lds[i * 64 + lane] = v[i];
+  }
+  // the lane's fields of block k of the KC, row tile r
+  static __device__ __forceinline__ Raw raw(const u32x4 *lds, int r, int k) {
+    const int lane = threadIdx.x & 63;
+    return load_raw<F>(reinterpret_cast<const uint8_t *>(lds + (r * 16 + (lane & 15)) * U) + k * Geo<F>::BYTES,
+                       lane >> 4);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Tokens to fp16
