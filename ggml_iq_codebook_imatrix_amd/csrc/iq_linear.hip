@@ -94,7 +94,8 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
     }
   }
   const float scale = L.scale ? L.scale[a] : 1.0f;
-  reduce_waves<1, 1>(&acc, s_red, 8, [&](int, int l, const f32x4 &s) {
+  const Split S{8, 1, wave, 0};
+  reduce_split<1, 1>(&acc, s_red, S, [&](int, int, int l, const f32x4 &s) {
     const int jj = rt * 16 + (l & 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -262,20 +263,18 @@ struct LinearArgs {
   void *y;
 };
 
-// Few tokens: a workgroup takes R row tiles by C token tiles, its waves split
-// the blocks of a row between them and add up through LDS.
-template <int F, int P, int C, int R>
-__global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
-  constexpr int G = R * C < 4 ? R * C : 4;
+// Few tokens: waves split K (split_blocks), RT row tiles each by C token tiles.
+template <int F, int P, int C, int RT>
+__global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
+  constexpr int G = RT * C < 4 ? RT * C : 4;
   constexpr int kTab = Geo<F>::N, kRed = 8 * G * 64;
   __shared__ uint4 s_mem[kTab > kRed ? kTab : kRed];
   load_table<F>(s_mem, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16 * R, tt0 = static_cast<int64_t>(blockIdx.y) * C;
-  const uint8_t *rp[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) rp[r] = A.packed + min(row0 + r * 16 + n, A.rows - 1) * A.nb * Geo<F>::BYTES;
+  const Split S = split_of(A.nb);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * S.rw + S.rg) * 16 * RT;
+  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * C;
+  const int64_t rowbytes = A.nb * Geo<F>::BYTES, stride = A.X.ntile * P * 4096;
   const _Float16 *x0[C];
   int64_t e0[C];
 #pragma unroll
@@ -284,54 +283,29 @@ __global__ void __launch_bounds__(512) linear_few_kernel(LinearArgs A) {
     x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
     e0[c] = min((tt0 + c) * 16 + q * 4, A.X.ntile * 16 - 4);
   }
-  f32x4 acc[R][C];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t stride = A.X.ntile * P * 4096;  // between blocks of the token operand
-  const int64_t first = min(static_cast<int64_t>(wave), A.nb - 1);
-  Raw raw[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r] + first * Geo<F>::BYTES, q);
-  Steps<P, C> x;
-  const _Float16 *xp[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) xp[c] = x0[c] + first * stride;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load_step<P, C>(x, i, xp);
+  f32x4 acc[RT][1][C] = {};
   __syncthreads();
-  for (int64_t b = wave; b < A.nb; b += nw) {
-    Raw next[R];
-    const int64_t bn = min(b + nw, A.nb - 1);
+  split_blocks<F, P, C, RT, 1>(
+      A.nb, S, s_mem, [&](int, int rt) { return A.packed + min(row0 + rt * 16 + n, A.rows - 1) * rowbytes; },
+      [&](int64_t b, Operand<P, C> &x) __attribute__((always_inline)) {
+        const _Float16 *xp[C];
 #pragma unroll
-    for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-    const _Float16 *xn[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) xn[c] = x0[c] + bn * stride;
-    __builtin_amdgcn_sched_barrier(0x38f);
-    f32x4 part[R][C];
-    block_mma_ahead<F, P, C, R>(raw, s_mem, xp, xn, x, part);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) scale_add(acc[r][c], part[r][c], block_scale<F>(raw[r]));
-      xp[c] = xn[c];
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) raw[r] = next[r];
-  }
+        for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * stride;
+        load_operand<P, C>(x, xp);
+      },
+      [](f32x4 &a, const f32x4 &part, float d, int) { scale_add(a, part, d); }, acc);
+  f32x4 sum[RT][C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + e0[c]);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      acc[r][c] = f32x4{ldexpf(acc[r][c][0], e.x), ldexpf(acc[r][c][1], e.y), ldexpf(acc[r][c][2], e.z),
-                        ldexpf(acc[r][c][3], e.w)};
+    for (int r = 0; r < RT; ++r)
+      sum[r][c] = f32x4{ldexpf(acc[r][0][c][0], e.x), ldexpf(acc[r][0][c][1], e.y), ldexpf(acc[r][0][c][2], e.z),
+                        ldexpf(acc[r][0][c][3], e.w)};
   }
-  if (A.L.rank) lora_expand<P, C, R>(A.L, tt0, A.T, A.rows, row0, wave, nw, acc);
-  reduce_waves<R * C, G>(&acc[0][0], reinterpret_cast<f32x4 *>(s_mem), nw, [&](int tile, int l, const f32x4 &s) {
-    const int64_t row = row0 + (tile / C) * 16 + (l & 15);
+  if (A.L.rank) lora_expand<P, C, RT>(A.L, tt0, A.T, A.rows, row0, S.kg, S.kw, sum);
+  reduce_split<RT * C, G>(&sum[0][0], reinterpret_cast<f32x4 *>(s_mem), S, [&](int rg, int tile, int l, const f32x4 &s) {
+    const int64_t row = ((static_cast<int64_t>(blockIdx.x) * S.rw + rg) * RT + tile / C) * 16 + (l & 15);
     if (row >= A.rows) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -498,13 +472,13 @@ int check_linear(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int 
   return IQ_OK;
 }
 
-template <int F, int P, int C, int R>
-void launch_few(const LinearArgs &A, hipStream_t stream) {
-  int nw = 1;  // waves: a power of two, no more than a row has blocks
-  while (nw < 8 && nw < A.nb) nw *= 2;
-  const dim3 grid(static_cast<unsigned>((A.rows + 16 * R - 1) / (16 * R)),
-                  static_cast<unsigned>((A.X.ntile + C - 1) / C));
-  hipLaunchKernelGGL((linear_few_kernel<F, P, C, R>), grid, dim3(64 * nw), 0, stream, A);
+template <int F, int P, int C, int RT>
+void launch_split(const LinearArgs &A, hipStream_t stream) {
+  const int64_t rw = split_rw(A.nb), rows = rw * 16 * RT;
+  hipLaunchKernelGGL((linear_split_kernel<F, P, C, RT>),
+                     dim3(static_cast<unsigned>((A.rows + rows - 1) / rows),
+                          static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+                     dim3(static_cast<unsigned>(64 * split_kw(A.nb) * rw)), 0, stream, A);
 }
 
 template <int F, int P, int C, int R, int KG>
@@ -517,14 +491,19 @@ void launch_tile(const LinearArgs &A, hipStream_t stream) {
 }
 
 template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
-  if (A.X.ntile == 1)
-    launch_few<F, P, 1, 1>(A, stream);
-  else if (A.X.ntile == 2)
-    launch_tile<F, P, 2, 2, 4 / P>(A, stream);
-  else if (P == 2 || A.X.ntile <= 4)
+  const int64_t tiles = (A.rows + 15) / 16 / split_rw(A.nb);  // row tiles, by the row groups of a workgroup
+  if (A.X.ntile == 1) {
+    if (tiles <= 768)
+      launch_split<F, P, 1, 1>(A, stream);
+    else
+      launch_split<F, P, 1, 4>(A, stream);
+  } else if (A.X.ntile == 2) {
+    launch_split<F, P, 2, 2>(A, stream);
+  } else if (P == 2 || A.X.ntile <= 4) {
     launch_tile<F, P, 4, 2, 2 / P>(A, stream);
-  else
+  } else {
     launch_tile<F, P, P == 2 ? 4 : 8, 2, 1>(A, stream);
+  }
 }
 
 }  // namespace

@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
       if (P == 2) *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = make_uint2(0, 0);
     }
   }
-  reduce_waves<1, 1>(&acc, reinterpret_cast<f32x4 *>(&s_x[0][0]), NW, [&](int, int l, const f32x4 &s) {
+  const Split W{NW, 1, wave, 0};
+  reduce_split<1, 1>(&acc, reinterpret_cast<f32x4 *>(&s_x[0][0]), W, [&](int, int, int l, const f32x4 &s) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int t = (l >> 4) * 4 + k;
@@ -476,94 +477,94 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
   }
 }
 
-// 128 rows of gate and up of one expert: eight waves, 16 rows each.  The pairs'
-// tokens lie in LDS for all of them, two blocks at a time, the next two on their
-// way in registers.
+// 128 rows of gate and up of one expert: eight waves, 16 rows each over the whole
+// of K.  The pairs' tokens come through LDS, KC blocks at a time for all waves;
+// a wave keeps the payload of the next two blocks on its way in registers (with
+// one, waiting for HBM was a third of the time).
 template <int F, int P, int C, bool FEW>
-__global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KC = 2, XU = KC * C * P;
-  typedef Payload<F, 2, KC> Pay;
+__global__ void __launch_bounds__(512, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
+  constexpr int N = 16 * C, KC = C * P == 4 ? 1 : 2, XU = KC * C * P;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ u32x4 s_x[XU * 512];
-  __shared__ u32x4 s_pay[8][Pay::kUnits];
+  __shared__ u32x4 s_x[2][XU * 512];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
-  load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per, rowbytes = nb * Geo<F>::BYTES;
+  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
+  load_table<F>(s_tab, A.tab);
   if constexpr (FEW) {
     few_ids(A, S, A.pick);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col = part * 128 + wave * 16 + n, row0 = e * A.inter + part * 128 + wave * 16;
-  const int64_t size = A.E * A.inter * rowbytes;
-  const uint8_t *gend = A.gate + size, *uend = A.up + size;
-  Pay pay;
-  pay.init([&](int i) { return (i < 16 ? A.gate : A.up) + (row0 + (i & 15)) * rowbytes; });
-  // the units of rows 0 .. 15 are gate's: a lane's unit ends with its matrix
-  const auto load_pay = [&](int64_t b) __attribute__((always_inline)) {
+  const int64_t col = part * 128 + wave * 16 + n, row = e * A.inter + col;
+  const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
+  Raw raw[3][2];  // the block in hand and the next two
 #pragma unroll
-    for (int i = 0; i < Pay::kPer; ++i) {
-      const uint8_t *p = pay.at[i] + b * Geo<F>::BYTES;
-      const uint8_t *end = i * 64 + lane < 16 * Pay::U ? gend : uend;
-      pay.v[i] = load_unit(p, end);
-    }
-  };
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
+  bool fresh = true;
   const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
+    if (!fresh) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          raw[k][r] = load_raw<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
+    }
+    fresh = false;
     const int m = threadIdx.x & 15;  // a thread copies the same row of every tile
+    int64_t from[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t t = list[min(c * 16 + m, count - 1)] / A.top_k;
+      from[c] = (t >> 4) * P * 512 + (threadIdx.x & ~15) + (t & 15);
+    }
     u32x4 xr[XU];
     const auto load_x = [&](int64_t b0) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < XU; ++i) {
-        const int c = i / P % C, slot = c * 16 + m;
-        if (slot < count) {
-          const int64_t b = min(b0 + i / (C * P), nb - 1), t = list[slot] / A.top_k;
-          const int64_t at = ((b * A.X.ntile + (t >> 4)) * P + i % P) * 512 + (threadIdx.x & ~15) + (t & 15);
-          xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[at];
-        }
+        const int c = i / P % C;
+        const int64_t b = min(b0 + i / (C * P), nb - 1);
+        if (c * 16 + m < count)
+          xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[b * A.X.ntile * P * 512 + i % P * 512 + from[c]];
       }
     };
-    const auto store_x = [&]() __attribute__((always_inline)) {
+    const auto store_x = [&](u32x4 *to) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < XU; ++i)
-        if (i / P % C * 16 + m < count) s_x[i * 512 + threadIdx.x] = xr[i];
+        if (i / P % C * 16 + m < count) to[i * 512 + threadIdx.x] = xr[i];
     };
     f32x4 acc[2][C] = {};
-    load_pay(0);
     load_x(0);
-    pay.store(s_pay[wave]);
-    store_x();
-    __syncthreads();
+    store_x(s_x[0]);
+    int cur = 0;
     for (int64_t b0 = 0; b0 < nb; b0 += KC) {
-      const bool more = b0 + KC < nb;
-      if (more) {
-        load_pay(b0 + KC);
-        load_x(b0 + KC);
-      }
-      __builtin_amdgcn_sched_barrier(0x38f);
+      __syncthreads();  // the chunk is there, and the one before read
+      if (b0 + KC < nb) load_x(b0 + KC);
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        if (b0 + k >= nb) break;
-        Raw raw[2];
+        const int64_t b = b0 + k;
+        if (b >= nb) break;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[r] = Pay::raw(s_pay[wave], r, k);
+        for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + min(b + 2, nb - 1) * Geo<F>::BYTES, q);
+        __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
         const _Float16 *xp[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) xp[c] = reinterpret_cast<const _Float16 *>(s_x + (k * C + c) * P * 512 + lane);
-        f32x4 sum[2][C];
-        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
-#pragma unroll
         for (int c = 0; c < C; ++c)
+          xp[c] = reinterpret_cast<const _Float16 *>(s_x[cur] + (k * C + c) * P * 512 + lane);
+        f32x4 sum[2][C];
+        block_mma<F, P, C, 2>(raw[0], s_tab, xp, sum);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]));
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[0][r]));
+          raw[0][r] = raw[1][r];
+          raw[1][r] = raw[2][r];
+        }
       }
-      __syncthreads();  // the blocks are read (and, at the end, free for the next pairs)
-      if (more) {
-        pay.store(s_pay[wave]);
-        store_x();
-        __syncthreads();
-      }
+      cur ^= 1;
+      if (b0 + KC < nb) store_x(s_x[cur]);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
         const int ex = A.X.ex[p / A.top_k];
         A.h[p * A.inter + col] = gated(ldexpf(acc[0][c][k], ex), ldexpf(acc[1][c][k], ex), w);
       }
+    __syncthreads();  // the tokens' memory and the list may change
   };
   if constexpr (FEW) {
     for (int c0 = 0; c0 < S.n; c0 += N) body(S.list + c0, min(N, S.n - c0));
@@ -588,36 +590,46 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A)
   }
 }
 
-// 128 columns of y of one expert: eight waves, 16 columns each.  The pairs' h
+// 256 columns of y of one expert: eight waves, 32 columns each.  The pairs' h
 // goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
-// block, so the conversion is repeated only by the hidden / 128 workgroups of an
+// block, so the conversion is repeated only by the hidden / 256 workgroups of an
 // expert.  z: one row per pair.
 template <int F, int P, int C, bool FEW>
 __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KC = 2, KB = 4 / P;
-  typedef Payload<F, 1, KC> Pay;
+  constexpr int N = 16 * C, KB = 4 / P;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ _Float16 s_h[KB][C][P * 4096];
-  __shared__ u32x4 s_pay[8][Pay::kUnits];
   __shared__ int s_ex[KB][N];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.dtab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
   const int nb = static_cast<int>(A.inter >> 8);
-  const int64_t per = A.hidden >> 7, part = blockIdx.x % per, rowbytes = static_cast<int64_t>(nb) * Geo<F>::BYTES;
+  const int64_t per = A.hidden >> 8, part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
   if constexpr (FEW) {
     few_ids(A, S, false);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col0 = part * 128 + wave * 16;
-  const uint8_t *end = A.down + A.E * A.hidden * rowbytes;
-  Pay pay;
-  pay.init([&](int i) { return A.down + (e * A.hidden + col0 + i) * rowbytes; });
+  const int64_t col = part * 256 + wave * 32 + n;
+  const uint8_t *rp[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
+  Raw raw[3][2];  // the block in hand and the next two
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
+  bool fresh = true;
   const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
-    f32x4 acc[C] = {};
-    pay.load(0, end);
+    f32x4 acc[2][C] = {};
+    if (!fresh) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
+    }
+    fresh = false;
     for (int b0 = 0; b0 < nb; b0 += KB) {
       const int kb = min(KB, nb - b0);
       if (b0) __syncthreads();  // the blocks before are read
@@ -638,27 +650,29 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
         if (lane == 0) s_ex[j][m] = -up;
       }
       __syncthreads();
-      for (int j0 = 0; j0 < kb; j0 += KC) {
-        pay.store(s_pay[wave]);  // read by this wave alone
-        if (b0 + j0 + KC < nb) pay.load(b0 + j0 + KC, end);
+      for (int j = 0; j < kb; ++j) {
+        const int bn = min(b0 + j + 2, nb - 1);
 #pragma unroll
-        for (int k = 0; k < KC; ++k) {
-          const int j = j0 + k;
-          if (j >= kb) break;
-          Raw raw[1];
-          raw[0] = Pay::raw(s_pay[wave], 0, k);
-          const _Float16 *xp[C];
+        for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+        __builtin_amdgcn_sched_barrier(0x38f);
+        const _Float16 *xp[C];
 #pragma unroll
-          for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
-          f32x4 sum[1][C];
-          block_mma<F, P, C, 1>(raw, s_tab, xp, sum);
+        for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
+        f32x4 sum[2][C];
+        block_mma<F, P, C, 2>(raw[0], s_tab, xp, sum);
 #pragma unroll
-          for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int ex = s_ex[j][c * 16 + q * 4 + i];  // past count: of rows not stored
-              acc[c][i] += ldexpf(block_scale<F>(raw[0]) * sum[0][c][i], ex);
-            }
+          for (int k = 0; k < 4; ++k) {
+            const int ex = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
+#pragma unroll
+            for (int r = 0; r < 2; ++r) acc[r][c][k] += ldexpf(block_scale<F>(raw[0][r]) * sum[r][c][k], ex);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          raw[0][r] = raw[1][r];
+          raw[1][r] = raw[2][r];
         }
       }
     }
@@ -667,7 +681,10 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = c * 16 + q * 4 + k;
-        if (i < count) A.z[list[i] * A.hidden + col0 + n] = acc[c][k];
+        if (i >= count) continue;
+        const int64_t p = list[i];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) A.z[p * A.hidden + col + r * 16] = acc[r][c][k];
       }
     __syncthreads();  // s_h is free again
   };
@@ -781,7 +798,7 @@ template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
                        dim3(64 * down_split_waves(P)), 0, stream, A);
     return;
   }
-  const unsigned per = static_cast<unsigned>(A.hidden / 128);
+  const unsigned per = static_cast<unsigned>(A.hidden / 256);
   if (is_few(A.T, A.E))
     hipLaunchKernelGGL((down_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(reached(A.npair, A.E)) * per),
                        dim3(512), 0, stream, A);

@@ -263,48 +263,6 @@ __device__ __forceinline__ void block_mma(const Raw (&raw)[R], const uint4 *tab,
   }
 }
 
-// The same with the token operand read ahead in global memory.  Loads return in
-// order, so a step's operand asked for after the next block's payload waits for
-// that as well, which comes from HBM: operands are therefore asked for four
-// steps ahead (x holds four), and the payload of the next block right before
-// this block's steps, half a block before anything waits behind it.
-template <int P, int C> struct Steps {
-  half8v v[4][C][P];
-};
-template <int P, int C>
-__device__ __forceinline__ void load_step(Steps<P, C> &x, int i, const _Float16 *const (&xp)[C]) {
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int p = 0; p < P; ++p) x.v[i & 3][c][p] = *reinterpret_cast<const half8v *>(xp[c] + p * 4096 + i * 512);
-}
-template <int F, int P, int C, int R>
-__device__ __forceinline__ void block_mma_ahead(const Raw (&raw)[R], const uint4 *tab, const _Float16 *const (&xp)[C],
-                                                const _Float16 *const (&xn)[C], Steps<P, C> &x,
-                                                f32x4 (&part)[R][C]) {
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < C; ++c) part[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const half8v w = group_half8<F>(raw[r], i, tab);
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          part[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.v[i & 3][c][p], w, part[r][c], 0, 0, 0);
-    }
-    if (i < 4)
-      load_step<P, C>(x, i + 4, xp);
-    else
-      load_step<P, C>(x, i - 4, xn);
-    __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
-  }
-}
-
 // acc += d * part
 __device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d) {
 #pragma unroll
@@ -459,22 +417,106 @@ __device__ __forceinline__ void convert_codebook(const Codebooks &B, int wg) {
 }
 
 // ---------------------------------------------------------------------------
-// Sum of the waves' accumulators through LDS, in wave order, G tiles at a time;
-// then f(tile, lane, sum) on one thread per lane.  red: nw * G * 64 f32x4.
+// Waves that split K.  A workgroup is kw x rw waves: wave (kg, rg) takes every
+// kw-th block of its row group's RT tiles of 16 rows.  The blocks of a row are
+// read by the workgroup at the same time, so that its lines, which hold nearly
+// two blocks, are fetched once (one wave walking along its rows found them gone
+// from L1 at every other block, and was bound by the requests); and a wave's
+// token operand, one block, stays in registers for all of its row tiles.
 // ---------------------------------------------------------------------------
+struct Split {
+  int kw, rw, kg, rg;
+};
+inline int split_kw(int64_t nb) { return nb < 8 ? static_cast<int>(nb) : 8; }
+inline int split_rw(int64_t nb) { return 8 / split_kw(nb); }
+__device__ __forceinline__ Split split_of(int64_t nb) {
+  Split s;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  s.kw = nb < 8 ? static_cast<int>(nb) : 8;
+  s.rw = static_cast<int>(blockDim.x >> 6) / s.kw;
+  s.kg = wave % s.kw;
+  s.rg = wave / s.kw;
+  return s;
+}
+
+template <int P, int C> struct Operand {
+  half8v v[8][C][P];
+};
+// xp[c]: the lane's share of the block
+template <int P, int C>
+__device__ __forceinline__ void load_operand(Operand<P, C> &x, const _Float16 *const (&xp)[C]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int p = 0; p < P; ++p) x.v[i][c][p] = *reinterpret_cast<const half8v *>(xp[c] + p * 4096 + i * 512);
+}
+
+// acc[rt][m][c] += the wave's blocks of M matrices.  rowp(m, rt): the lane's row;
+// loadx(b, x): the operand of block b; scale(c, f): applied to a block's sums
+// times d (a power of two of the block's own, or nothing).
+template <int F, int P, int C, int RT, int M, class RowP, class LoadX, class Add>
+__device__ __forceinline__ void split_blocks(int64_t nb, const Split &S, const uint4 *tab, RowP rowp, LoadX loadx,
+                                             Add add, f32x4 (&acc)[RT][M][C]) {
+  const int q = (threadIdx.x & 63) >> 4;
+  Operand<P, C> x;
+  Raw raw[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) raw[m] = load_raw<F>(rowp(m, 0) + static_cast<int64_t>(S.kg) * Geo<F>::BYTES, q);
+  for (int64_t b = S.kg; b < nb; b += S.kw) {
+    loadx(b, x);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      Raw next[M];  // the next row tile, or the first of the next block
+      const int64_t bn = rt + 1 < RT ? b : min(b + S.kw, nb - 1);
+#pragma unroll
+      for (int m = 0; m < M; ++m) next[m] = load_raw<F>(rowp(m, rt + 1 < RT ? rt + 1 : 0) + bn * Geo<F>::BYTES, q);
+      __builtin_amdgcn_sched_barrier(0);  // one row tile's work at a time: more costs registers, and with them waves
+      f32x4 part[M][C];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int c = 0; c < C; ++c) part[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const half8v w = group_half8<F>(raw[m], i, tab);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              part[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.v[i][c][p], w, part[m][c], 0, 0, 0);
+        }
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const float d = block_scale<F>(raw[m]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) add(acc[rt][m][c], part[m][c], d, c);
+        raw[m] = next[m];
+      }
+    }
+  }
+}
+
+// Sums over the kw waves of each row group through LDS, in their order, G tiles
+// of 16 x 16 at a time; then f(rg, tile, lane, sum).  red: 8 * G * 64 f32x4.
 template <int N, int G, class Fn>
-__device__ __forceinline__ void reduce_waves(const f32x4 *acc, f32x4 *red, int nw, Fn f) {
-  const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
+__device__ __forceinline__ void reduce_split(const f32x4 *acc, f32x4 *red, const Split &S, Fn f) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
 #pragma unroll
   for (int g = 0; g < N; g += G) {
-    __syncthreads();  // the table (first) or the sums before (later) are no longer read
+    __syncthreads();  // what the memory held before is read
 #pragma unroll
-    for (int j = 0; j < G; ++j) red[(wave * G + j) * 64 + lane] = acc[g + j];
+    for (int j = 0; j < G; ++j) red[((S.rg * S.kw + S.kg) * G + j) * 64 + lane] = acc[g + j];
     __syncthreads();
-    for (int i = threadIdx.x; i < G * 64; i += blockDim.x) {
-      f32x4 s = red[i];
-      for (int w = 1; w < nw; ++w) s += red[w * G * 64 + i];
-      f(g + (i >> 6), i & 63, s);
+    for (int i = threadIdx.x; i < S.rw * G * 64; i += blockDim.x) {
+      const int rg = i / (G * 64), rest = i % (G * 64);
+      const f32x4 *p = red + rg * S.kw * G * 64 + rest;
+      f32x4 s = p[0];
+      for (int k = 1; k < S.kw; ++k) s += p[k * G * 64];
+      f(rg, g + rest / 64, rest & 63, s);
     }
   }
 }
