@@ -37,7 +37,8 @@ struct MoeArgs {
   int dtype, rdtype;
   Tokens X;
   const _Float16 *tab, *dtab;
-  double *logits;          // [T, E]
+  double *logits;          // [ks][T, E], sums over parts of K
+  int ks;
   int32_t *ids;
   float *weights;
   float *h;                // [pairs, inter]
@@ -54,20 +55,22 @@ struct MoeArgs {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 // The logits of 16 tokens and 16 experts on the fp64 matrix cores, K split over
-// the eight waves.  In fp64, so that no order of summation can swap neighbours in
+// ks workgroups (whose sums the choice adds) and each one's eight waves.  In fp64, so that no order of summation can swap neighbours in
 // the ranking.  v_mfma_f64_16x16x4: lane l holds k = l / 16 of token (A) and
 // expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
 template <int P>
 __device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w, double *s_red) {
   constexpr int U = 4;  // loads in flight
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ne = (A.E + 15) / 16, nb = static_cast<int>(A.hidden >> 8);
+  const int ne = (A.E + 15) / 16, ks = static_cast<int>(w % A.ks);
+  const int b0 = static_cast<int>((A.hidden >> 8) * ks / A.ks), nb = static_cast<int>((A.hidden >> 8) * (ks + 1) / A.ks);
+  w /= A.ks;
   const int64_t t0 = w / ne * 16, e0 = w % ne * 16;
   const int64_t k0 = wave * 32 + (lane >> 4) * 8;  // 32 of each 256 columns
   const int64_t xr = min(t0 + (lane & 15), A.T - 1) * A.hidden + k0;
   const int64_t rr = min(e0 + (lane & 15), static_cast<int64_t>(A.E) - 1) * A.hidden + k0;
   f64x4 acc = {0.0, 0.0, 0.0, 0.0};
-  for (int b = 0; b < nb; b += U) {
+  for (int b = b0; b < nb; b += U) {
     float x[U][8], r[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -91,7 +94,7 @@ __device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w, double
     double s = s_red[i * 64 + lane];
     for (int v = 1; v < 8; ++v) s += s_red[(v * 4 + i) * 64 + lane];
     const int64_t t = t0 + (lane >> 4) + 4 * i, e = e0 + (lane & 15);
-    if (t < A.T && e < A.E) A.logits[t * A.E + e] = s;
+    if (t < A.T && e < A.E) A.logits[(ks * A.T + t) * A.E + e] = s;
   }
 }
 
@@ -143,13 +146,19 @@ __device__ __forceinline__ double key_value(uint64_t k) {
 // upper half by register permutes and looks at lower halves and ids only where
 // several lanes tie.  ids, weights: where the token's choice goes.
 template <int KPL>
-__device__ __forceinline__ void pick_top(const double *l, int E, int top_k, int renorm, int32_t *ids, float *weights) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void pick_top(const MoeArgs &A, int64_t t, int32_t *ids, float *weights) {
+  const int lane = threadIdx.x & 63, E = A.E, top_k = A.top_k;
+  const double *l = A.logits + t * E;
+  const auto logit = [&](int e) {
+    double s = l[e];
+    for (int k = 1; k < A.ks; ++k) s += l[k * A.T * E + e];
+    return s;
+  };
   uint64_t key[KPL];
 #pragma unroll
   for (int j = 0; j < KPL; ++j) {
     const int e = lane + 64 * j;
-    key[j] = e < E ? order_key(l[e]) : 0;
+    key[j] = e < E ? order_key(logit(e)) : 0;
   }
   double top = 0.0;
   float mine = 0.0f, sum = 0.0f;
@@ -192,9 +201,9 @@ __device__ __forceinline__ void pick_top(const double *l, int E, int top_k, int 
       my_id = from + 64 * wj;
     }
   }
-  if (!renorm) {
+  if (!A.renorm) {
     sum = 0.0f;
-    for (int e = lane; e < E; e += 64) sum += expf(static_cast<float>(l[e] - top));
+    for (int e = lane; e < E; e += 64) sum += expf(static_cast<float>(logit(e) - top));
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
   }
@@ -207,9 +216,9 @@ __device__ __forceinline__ void pick_top(const double *l, int E, int top_k, int 
 __global__ void __launch_bounds__(64) topk_kernel(MoeArgs A) {
   const int64_t t = blockIdx.x;
   if (A.E <= 256)
-    pick_top<4>(A.logits + t * A.E, A.E, A.top_k, A.renorm, A.ids + t * A.top_k, A.weights + t * A.top_k);
+    pick_top<4>(A, t, A.ids + t * A.top_k, A.weights + t * A.top_k);
   else
-    pick_top<64>(A.logits + t * A.E, A.E, A.top_k, A.renorm, A.ids + t * A.top_k, A.weights + t * A.top_k);
+    pick_top<64>(A, t, A.ids + t * A.top_k, A.weights + t * A.top_k);
 }
 
 // The four of a block's values whose place in the operand is the lane's: elements
@@ -244,8 +253,7 @@ __device__ __forceinline__ void few_ids(const MoeArgs &A, FewPairs &S, bool pick
   if (threadIdx.x < kFewExperts / 32) S.bits[threadIdx.x] = 0;
   if (pick) {
     for (int t = wave; t < A.T; t += nw)
-      pick_top<4>(A.logits + static_cast<int64_t>(t) * A.E, A.E, A.top_k, A.renorm, S.ids + t * A.top_k,
-                  S.w + t * A.top_k);
+      pick_top<4>(A, t, S.ids + t * A.top_k, S.w + t * A.top_k);
   } else {
     for (int p = threadIdx.x; p < np; p += blockDim.x) {
       const int e = A.ids[p];
@@ -436,22 +444,22 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
 }
 
 // Walks the pairs of one expert in ascending order, N at a time: f(list, count).
-// Few tokens: they are in LDS already; otherwise the ids are searched, 512 at a time.
+// Few tokens: they are in LDS already; otherwise the ids are searched, a workgroup's width at a time.
 template <int N> struct PairWalk {
-  int list[512 + N], cnt[8];
+  int list[512 + N], cnt[8];  // up to eight waves
 };
 template <int N, class Fn>
 __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &S, Fn f) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   int have = 0;
-  for (int64_t p0 = 0; p0 < A.npair; p0 += 512) {
+  for (int64_t p0 = 0; p0 < A.npair; p0 += blockDim.x) {
     const int64_t p = p0 + threadIdx.x;
     const bool hit = p < A.npair && A.ids[p] == e;
     const uint64_t b = __ballot(hit);
     if (lane == 0) S.cnt[wave] = __builtin_popcountll(b);
     __syncthreads();
     int at = have, total = 0;
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < nw; ++w) {
       const int c = S.cnt[w];
       if (w < wave) at += c;
       total += c;
@@ -459,7 +467,7 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
     if (hit) S.list[at + __builtin_popcountll(b & ((uint64_t(1) << lane) - 1))] = static_cast<int>(p);
     have += total;
     __syncthreads();
-    const bool last = p0 + 512 >= A.npair;
+    const bool last = p0 + blockDim.x >= A.npair;
     int head = 0;
     while (have - head >= N || (last && have > head)) {
       f(S.list + head, min(N, have - head));
@@ -477,18 +485,18 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
   }
 }
 
-// 128 rows of gate and up of one expert: eight waves, 16 rows each over the whole
+// 16 NW rows of gate and up of one expert: NW waves, 16 rows each over the whole
 // of K.  The pairs' tokens come through LDS, KC blocks at a time for all waves;
 // a wave keeps the payload of the next two blocks on its way in registers (with
 // one, waiting for HBM was a third of the time).
-template <int F, int P, int C, bool FEW>
-__global__ void __launch_bounds__(512, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KC = C * P == 4 ? 1 : 2, XU = KC * C * P;
+template <int F, int P, int C, int NW, bool FEW>
+__global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
+  constexpr int N = 16 * C, KC = C * P == 4 ? 1 : 2, kUnits = 512 / (64 * NW), XU = KC * C * P * kUnits;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ u32x4 s_x[2][XU * 512];
+  __shared__ u32x4 s_x[2][XU * 64 * NW];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.hidden >> 8, per = A.inter >> 7, part = blockIdx.x % per;
+  const int64_t nb = A.hidden >> 8, per = A.inter / (16 * NW), part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
   load_table<F>(s_tab, A.tab);
   if constexpr (FEW) {
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(512, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArg
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col = part * 128 + wave * 16 + n, row = e * A.inter + col;
+  const int64_t col = part * 16 * NW + wave * 16 + n, row = e * A.inter + col;
   const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
   Raw raw[3][2];  // the block in hand and the next two
 #pragma unroll
@@ -521,19 +529,21 @@ __global__ void __launch_bounds__(512, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArg
       from[c] = (t >> 4) * P * 512 + (threadIdx.x & ~15) + (t & 15);
     }
     u32x4 xr[XU];
+    // unit i: part i / kUnits of the chunk's [block][tile][part] 8 KiB pieces
     const auto load_x = [&](int64_t b0) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < XU; ++i) {
-        const int c = i / P % C;
-        const int64_t b = min(b0 + i / (C * P), nb - 1);
+        const int piece = i / kUnits, c = piece / P % C;
+        const int64_t b = min(b0 + piece / (C * P), nb - 1);
         if (c * 16 + m < count)
-          xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[b * A.X.ntile * P * 512 + i % P * 512 + from[c]];
+          xr[i] = reinterpret_cast<const u32x4 *>(
+              A.X.x16)[b * A.X.ntile * P * 512 + piece % P * 512 + i % kUnits * (64 * NW) + from[c]];
       }
     };
     const auto store_x = [&](u32x4 *to) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < XU; ++i)
-        if (i / P % C * 16 + m < count) to[i * 512 + threadIdx.x] = xr[i];
+        if (i / kUnits / P % C * 16 + m < count) to[i * 64 * NW + threadIdx.x] = xr[i];
     };
     f32x4 acc[2][C] = {};
     load_x(0);
@@ -590,12 +600,12 @@ __global__ void __launch_bounds__(512, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArg
   }
 }
 
-// 256 columns of y of one expert: eight waves, 32 columns each.  The pairs' h
+// 32 NW columns of y of one expert: NW waves, 32 columns each.  The pairs' h
 // goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
-// block, so the conversion is repeated only by the hidden / 256 workgroups of an
-// expert.  z: one row per pair.
-template <int F, int P, int C, bool FEW>
-__global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
+// block, so the conversion is repeated only by an expert's hidden / (32 NW)
+// workgroups.  z: one row per pair.
+template <int F, int P, int C, int NW, bool FEW>
+__global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C, KB = 4 / P;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ _Float16 s_h[KB][C][P * 4096];
@@ -604,14 +614,14 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
   load_table<F>(s_tab, A.dtab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
   const int nb = static_cast<int>(A.inter >> 8);
-  const int64_t per = A.hidden >> 8, part = blockIdx.x % per;
+  const int64_t per = A.hidden / (32 * NW), part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
   if constexpr (FEW) {
     few_ids(A, S, false);
     e = few_expert(A, S, e);
     if (e < 0) return;
   }
-  const int64_t col = part * 256 + wave * 32 + n;
+  const int64_t col = part * 32 * NW + wave * 32 + n;
   const uint8_t *rp[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(512, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs 
     for (int b0 = 0; b0 < nb; b0 += KB) {
       const int kb = min(KB, nb - b0);
       if (b0) __syncthreads();  // the blocks before are read
-      for (int i = wave; i < count * kb; i += 8) {
+      for (int i = wave; i < count * kb; i += NW) {
         const int m = i / kb, j = i - m * kb;
         float v[4];
         load_h(A.h + list[m] * A.inter + (b0 + j) * 256, lane, v);
@@ -740,6 +750,7 @@ bool split_down(int64_t T, int E) { return T <= 2 && E <= kFewExperts; }
 
 struct MoePlan {
   TokensPlan x;
+  int ks;
   size_t tab, dtab, xo, eo, lo, ho, zo, bytes;
 };
 MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int dtype, int64_t T, int top_k) {
@@ -751,7 +762,8 @@ MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, in
   p.xo = p.dtab + ws_up(static_cast<size_t>(kCodebook[down_fmt]) * 16);
   p.eo = p.xo + ws_up(p.x.xbytes);
   p.lo = p.eo + ws_up(p.x.ebytes);
-  p.ho = p.lo + ws_up(static_cast<size_t>(T) * E * 8);
+  p.ks = hidden >= 4 * 256 ? 4 : 1;  // 8 workgroups would route 16 tokens to 128 experts: 4 us more
+  p.ho = p.lo + ws_up(static_cast<size_t>(p.ks) * T * E * 8);
   p.zo = p.ho + ws_up(np * inter * 4);
   p.bytes = p.zo + ws_up(split_down(T, E) ? 0 : np * hidden * 4) + kWsAlign;
   return p;
@@ -766,12 +778,22 @@ int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int d
   const int64_t ntile = (T + 15) / 16, np = T * top_k;
   if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   // the launches: routing, up, down, sum (pairs are counted in 32 bits)
-  if ((T + 7) / 8 + 8 + ((E + 15) / 16) * ntile >= kMaxWG ||
+  if ((T + 7) / 8 + 8 + ((E + 15) / 16) * ntile * 4 >= kMaxWG ||
       np >= kMaxWG || E * (inter / 16) >= kMaxWG || E * (hidden / 16) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
     return IQ_ERR_SHAPE;
   return IQ_OK;
 }
 
+template <int F, int P, int C, int NW, bool FEW>
+void launch_up_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
+  hipLaunchKernelGGL((up_rows_kernel<F, P, C, NW, FEW>), dim3(static_cast<unsigned>(experts * (A.inter / (16 * NW)))),
+                     dim3(64 * NW), 0, stream, A);
+}
+template <int F, int P, int C, int NW, bool FEW>
+void launch_down_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
+  hipLaunchKernelGGL((down_rows_kernel<F, P, C, NW, FEW>),
+                     dim3(static_cast<unsigned>(experts * (A.hidden / (32 * NW)))), dim3(64 * NW), 0, stream, A);
+}
 template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
   const int64_t experts = reached(A.npair, A.E);
   if (split_up(A)) {
@@ -782,14 +804,12 @@ template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
                        0, stream, A);
     return;
   }
-  const unsigned per = static_cast<unsigned>(A.inter / 128);
   if (is_few(A.T, A.E))
-    hipLaunchKernelGGL((up_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(experts) * per), dim3(512), 0,
-                       stream, A);
+    launch_up_rows<F, P, 1, 4, true>(A, experts, stream);
   else if (A.npair <= 8 * static_cast<int64_t>(A.E))  // 8 pairs an expert on average: few have more than 16
-    hipLaunchKernelGGL((up_rows_kernel<F, P, 1, false>), dim3(A.E * per), dim3(512), 0, stream, A);
+    launch_up_rows<F, P, 1, 8, false>(A, A.E, stream);
   else
-    hipLaunchKernelGGL((up_rows_kernel<F, P, 2, false>), dim3(A.E * per), dim3(512), 0, stream, A);
+    launch_up_rows<F, P, 2, 8, false>(A, A.E, stream);
 }
 
 template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
@@ -798,14 +818,12 @@ template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
                        dim3(64 * down_split_waves(P)), 0, stream, A);
     return;
   }
-  const unsigned per = static_cast<unsigned>(A.hidden / 256);
   if (is_few(A.T, A.E))
-    hipLaunchKernelGGL((down_rows_kernel<F, P, 1, true>), dim3(static_cast<unsigned>(reached(A.npair, A.E)) * per),
-                       dim3(512), 0, stream, A);
+    launch_down_rows<F, P, 1, 8, true>(A, reached(A.npair, A.E), stream);
   else if (A.npair <= 8 * static_cast<int64_t>(A.E))
-    hipLaunchKernelGGL((down_rows_kernel<F, P, 1, false>), dim3(A.E * per), dim3(512), 0, stream, A);
+    launch_down_rows<F, P, 1, 8, false>(A, A.E, stream);
   else
-    hipLaunchKernelGGL((down_rows_kernel<F, P, 2, false>), dim3(A.E * per), dim3(512), 0, stream, A);
+    launch_down_rows<F, P, 2, 8, false>(A, A.E, stream);
 }
 
 }  // namespace
@@ -857,6 +875,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.tab = tab;
   A.dtab = dtab;
   A.logits = reinterpret_cast<double *>(base + P.lo);
+  A.ks = P.ks;
   A.ids = ids;
   A.weights = weights;
   A.h = reinterpret_cast<float *>(base + P.ho);
@@ -871,7 +890,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   A.books.iq1[1] = second.iq1[0];
   A.books.wg[1] = second.wg[0];
   A.nconv = (T + 7) / 8;
-  const int64_t nroute = router ? ((num_experts + 15) / 16) * P.x.ntile : 0;
+  const int64_t nroute = router ? ((num_experts + 15) / 16) * P.x.ntile * P.ks : 0;
   const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + A.books.wg[1] + nroute));
   if (dtype == IQ_DTYPE_F32)
     hipLaunchKernelGGL(route_kernel<2>, wgs, dim3(512), 0, stream, A);
