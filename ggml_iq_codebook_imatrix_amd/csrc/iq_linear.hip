@@ -442,6 +442,130 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
   }
 }
 
+// Prompts (bf16): eight waves of 64 rows each by C token tiles.  What bounds it is
+// balanced: a step of a wave is four codebook entries and C token operands from
+// LDS, 80 vector instructions and 4 C matrix instructions.  Registers decide the
+// tile, so there are no sums apart from the accumulators: these are kept in units
+// of the block's d, and rescaled by the ratio of two blocks' d in between (one
+// more rounding of 2^-24 a block, bf16 outputs round by 2^-9).  A block of d = 0
+// counts with zero weights instead.  Token operands go from memory to LDS
+// directly, half a block ahead.
+template <int F, int C>
+__global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
+  constexpr int R = 4, kHalf = C * 256;  // 16-byte units of half a block: C tiles of 4 KiB
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ u32x4 s_x[2][kHalf];
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * 8 + wave) * 16 * R;
+  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * C, rowbytes = A.nb * Geo<F>::BYTES;
+  const uint8_t *rp[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) rp[r] = A.packed + min(row0 + r * 16 + n, A.rows - 1) * rowbytes;
+  // half h of the token operand into buffer h % 2: piece i (1 KiB) by wave i % 8,
+  // tile i / 4, its steps' lanes in order
+  const auto fetch = [&](int64_t h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i0 = 0; i0 < C * 4; i0 += 8) {
+      const int i = i0 + wave;
+      if (i < C * 4) {
+        const int64_t tile = min(tt0 + i / 4, A.X.ntile - 1);
+        const u32x4 *from = reinterpret_cast<const u32x4 *>(A.X.x16) + ((h >> 1) * A.X.ntile + tile) * 512 +
+                            (h & 1) * 256 + (i & 3) * 64 + lane;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                         (__attribute__((address_space(3))) void *)&s_x[h & 1][i * 64], 16, 0, 0);
+      }
+    }
+  };
+  f32x4 acc[R][C];
+  float unit[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    unit[r] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  Raw raw[R], next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r], q);
+  fetch(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the barrier does not wait for loads into LDS
+  __syncthreads();
+  for (int64_t b = 0; b < A.nb; ++b) {
+    uint32_t keep[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float d = block_scale<F>(raw[r]);
+      keep[r] = d != 0.0f ? ~0u : 0u;
+      const float ratio = keep[r] ? unit[r] / d : 1.0f;
+      unit[r] = keep[r] ? d : unit[r];
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[r][c] *= ratio;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t h = 2 * b + half;
+      if (h + 1 < 2 * A.nb) fetch(h + 1);
+      if (half == 0) {
+        const int64_t bn = min(b + 1, A.nb - 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+      }
+      __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        half8v x[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = __builtin_bit_cast(half8v, s_x[half][c * 256 + i * 64 + lane]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const half8v w = group_half8<F>(raw[r], half * 4 + i, s_tab, keep[r]);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[c], w, acc[r][c], 0, 0, 0);
+        }
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // the next half is there, this one free
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r] = next[r];
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int4 e = *reinterpret_cast<const int4 *>(A.X.ex + min((tt0 + c) * 16 + q * 4, A.X.ntile * 16 - 4));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const f32x4 s = acc[r][c] * unit[r];
+      acc[r][c] = f32x4{ldexpf(s[0], e.x), ldexpf(s[1], e.y), ldexpf(s[2], e.z), ldexpf(s[3], e.w)};
+    }
+  }
+  if (A.L.rank) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      f32x4 a[R][1];
+#pragma unroll
+      for (int r = 0; r < R; ++r) a[r][0] = acc[r][c];
+      lora_expand<1, 1, R>(A.L, tt0 + c, A.T, A.rows, row0, 0, 1, a);
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r][c] = a[r][0];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = row0 + r * 16 + n;
+    if (row >= A.rows) continue;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t t = (tt0 + c) * 16 + q * 4 + k;
+        if (t < A.T) store1(A.y, 1, t * A.rows + row, acc[r][c][k]);
+      }
+  }
+}
+
 struct LinearPlan {
   TokensPlan x;
   int chunks;
@@ -490,6 +614,12 @@ void launch_tile(const LinearArgs &A, hipStream_t stream) {
                      dim3(512), 0, stream, A);
 }
 
+template <int F, int C> void launch_prompt(const LinearArgs &A, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_prompt_kernel<F, C>),
+                     dim3(static_cast<unsigned>((A.rows + 511) / 512), static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+                     dim3(512), 0, stream, A);
+}
+
 template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
   const int64_t tiles = (A.rows + 15) / 16 / split_rw(A.nb);  // row tiles, by the row groups of a workgroup
   if (A.X.ntile == 1) {
@@ -502,7 +632,15 @@ template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stre
   } else if (P == 2 || A.X.ntile <= 4) {
     launch_tile<F, P, 4, 2, 2 / P>(A, stream);
   } else {
-    launch_tile<F, P, P == 2 ? 4 : 8, 2, 1>(A, stream);
+    // one workgroup a CU: the tile whose rounds over 256 CUs cost least
+    const auto cost = [&](int64_t C) {
+      const int64_t wgs = (A.rows + 511) / 512 * ((A.X.ntile + C - 1) / C);
+      return (wgs + 255) / 256 * C;
+    };
+    if (cost(6) <= cost(4))
+      launch_prompt<F, 6>(A, stream);
+    else
+      launch_prompt<F, 4>(A, stream);
   }
 }
 

@@ -176,8 +176,10 @@ template <int F> __device__ __forceinline__ float block_scale(const Raw &r) {
 // Which of a group's eight values the operands' element h holds.
 __device__ constexpr int kept_at(int h) { return (h >> 1) + 4 * (h & 1); }
 
-// m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16).
-template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab) {
+// m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16); zeros
+// where keep is 0 instead of all ones.
+template <int F>
+__device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab, uint32_t keep = ~0u) {
   uint32_t k, ls, mask = 0, h = 0;
   if (F == IQ2_XXS) {
     const uint32_t word = r.a[2 * (i >> 2) + 1];
@@ -206,7 +208,7 @@ template <int F> __device__ __forceinline__ half8v group_half8(const Raw &r, int
   }
   const uint4 e = tab[k];
   const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * ls + 1));
-  const half2v m2 = {m, m};
+  const half2v m2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, half2v{m, m}) & keep);
   uint32_t o[4] = {e.x, e.y, e.z, e.w};
   if (Geo<F>::IQ1) {
     const half2v up = m2 * static_cast<_Float16>(0.125f);
