@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
       pay.load(min((ch + 1) * KG + kg, A.nb - 1), end);
       load_x(ch + 1);
     }
-    __builtin_amdgcn_sched_barrier(0x38f);
+    __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
     if (ch * KG + kg < A.nb) {
       Raw raw[R];
 #pragma unroll
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
 #pragma unroll
         for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
       }
-      __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
+      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         half8v x[C];

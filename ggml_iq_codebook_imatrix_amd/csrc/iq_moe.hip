@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
         if (b >= nb) break;
 #pragma unroll
         for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + min(b + 2, nb - 1) * Geo<F>::BYTES, q);
-        __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory may pass
+        __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
         const _Float16 *xp[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
         const int bn = min(b0 + j + 2, nb - 1);
 #pragma unroll
         for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
-        __builtin_amdgcn_sched_barrier(0x38f);
+        __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
         const _Float16 *xp[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
