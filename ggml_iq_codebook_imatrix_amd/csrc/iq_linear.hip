@@ -322,19 +322,17 @@ __global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
 template <int F, int P, int C, int R, int KG>
 __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
   constexpr int RG = 8 / KG, XU = KG * C * P, G = 4, kTab = Geo<F>::N;
-  typedef Payload<F, R, 1> Pay;
   __shared__ uint4 s_tab[kTab];
   __shared__ u32x4 s_x[XU * 512];
-  __shared__ u32x4 s_pay[8][Pay::kUnits];
   static_assert(KG == 1 || XU * 512 >= 8 * G * 64, "the sums over the waves fit");
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / RG;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * RG + wave % RG) * 16 * R;
   const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * C, rowbytes = A.nb * Geo<F>::BYTES;
-  const uint8_t *end = A.packed + A.rows * rowbytes;
-  Pay pay;
-  pay.init([&](int i) { return A.packed + min(row0 + i, A.rows - 1) * rowbytes; });
+  const uint8_t *rp[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) rp[r] = A.packed + min(row0 + r * 16 + n, A.rows - 1) * rowbytes;
   u32x4 xr[XU];
   // chunk ch of the token operand: 512 threads, XU units of 16 bytes each
   const auto load_x = [&](int64_t ch) __attribute__((always_inline)) {
@@ -355,21 +353,24 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int64_t chunks = (A.nb + KG - 1) / KG;
-  pay.load(min(static_cast<int64_t>(kg), A.nb - 1), end);
+  Words words[R], next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) words[r] = load_words<F>(rp[r] + min(static_cast<int64_t>(kg), A.nb - 1) * Geo<F>::BYTES, q);
   load_x(0);
-  pay.store(s_pay[wave]);
   store_x();
   __syncthreads();
   for (int64_t ch = 0; ch < chunks; ++ch) {
     if (ch + 1 < chunks) {
-      pay.load(min((ch + 1) * KG + kg, A.nb - 1), end);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        next[r] = load_words<F>(rp[r] + min((ch + 1) * KG + kg, A.nb - 1) * Geo<F>::BYTES, q);
       load_x(ch + 1);
     }
     __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
     if (ch * KG + kg < A.nb) {
       Raw raw[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) raw[r] = Pay::raw(s_pay[wave], r, 0);
+      for (int r = 0; r < R; ++r) raw[r] = unpack<F>(words[r], q);
       const _Float16 *xp[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) xp[c] = reinterpret_cast<const _Float16 *>(s_x + (kg * C + c) * P * 512 + lane);
@@ -382,8 +383,9 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
     }
     if (ch + 1 < chunks) {
       __syncthreads();  // the chunk is read
-      pay.store(s_pay[wave]);
       store_x();
+#pragma unroll
+      for (int r = 0; r < R; ++r) words[r] = next[r];
       __syncthreads();
     }
   }
@@ -486,16 +488,18 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  Raw raw[R], next[R];
+  Words words[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) raw[r] = load_raw<F>(rp[r], q);
+  for (int r = 0; r < R; ++r) words[r] = load_words<F>(rp[r], q);
   fetch(0);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the barrier does not wait for loads into LDS
   __syncthreads();
   for (int64_t b = 0; b < A.nb; ++b) {
     uint32_t keep[R];
+    Raw raw[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      raw[r] = unpack<F>(words[r], q);
       const float d = block_scale<F>(raw[r]);
       keep[r] = d != 0.0f ? ~0u : 0u;
       const float ratio = keep[r] ? unit[r] / d : 1.0f;
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
       if (half == 0) {
         const int64_t bn = min(b + 1, A.nb - 1);
 #pragma unroll
-        for (int r = 0; r < R; ++r) next[r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+        for (int r = 0; r < R; ++r) words[r] = load_words<F>(rp[r] + bn * Geo<F>::BYTES, q);
       }
       __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
 #pragma unroll
@@ -529,8 +533,6 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // the next half is there, this one free
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r) raw[r] = next[r];
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -668,6 +670,7 @@ int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const 
   if (!grid || (!empty && (!packed || !x || !y || (rank && (!lora_a || !lora_b || !lora_ids))))) return IQ_ERR_NULL;
   if (rank && num_adapters < 1) return IQ_ERR_ARG;
   if (empty) return IQ_OK;
+  if (reinterpret_cast<uintptr_t>(packed) & 1) return IQ_ERR_ARG;
   const LinearPlan P = plan_linear(fmt, cols, dtype, T, rank);
   if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
   char *base = ws_base(workspace);

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
     for (int64_t b = wave; b < nb; b += nw) {
       Raw raw[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) raw[r] = load_raw<F>(rp[r] + b * Geo<F>::BYTES, q);
+      for (int r = 0; r < 2; ++r) raw[r] = unpack<F>(load_words<F>(rp[r] + b * Geo<F>::BYTES, q), q);
       const _Float16 *const xp[1] = {x0 + b * P * 4096};
       f32x4 part[2][1];
       block_mma<F, P, 1, 2>(raw, s_tab, xp, part);
@@ -383,8 +383,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int task = wave; task < na * nb; task += NW) {
     const int e = __builtin_amdgcn_readfirstlane(s_active[task / nb]), b = task % nb;
-    Raw raw[1];
-    raw[0] = load_raw<F>(A.down + ((e * A.hidden + col0 + n) * nb + b) * Geo<F>::BYTES, q);
+    const Words words = load_words<F>(A.down + ((e * A.hidden + col0 + n) * nb + b) * Geo<F>::BYTES, q);
     uint32_t present = 0;
     const auto stage = [&](int t, const float *v) {  // token t's h: one wave, four columns a lane
       uint32_t x = 1;
@@ -421,6 +420,8 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
     }
     stage(token, v);
     const _Float16 *const xp[1] = {xs + lane * 8};
+    Raw raw[1];
+    raw[0] = unpack<F>(words, q);
     f32x4 part[1][1];
     block_mma<F, P, 1, 1>(raw, s_tab, xp, part);
     const float d = block_scale<F>(raw[0]);
@@ -506,11 +507,11 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
   }
   const int64_t col = part * 16 * NW + wave * 16 + n, row = e * A.inter + col;
   const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
-  Raw raw[3][2];  // the block in hand and the next two
+  Words words[3][2];  // the block in hand and the next two
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
+    for (int r = 0; r < 2; ++r) words[k][r] = load_words<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
   bool fresh = true;
   const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
     if (!fresh) {
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          raw[k][r] = load_raw<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
+          words[k][r] = load_words<F>(rp[r] + min(static_cast<int64_t>(k), nb - 1) * Geo<F>::BYTES, q);
     }
     fresh = false;
     const int m = threadIdx.x & 15;  // a thread copies the same row of every tile
@@ -557,20 +558,23 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
         const int64_t b = b0 + k;
         if (b >= nb) break;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + min(b + 2, nb - 1) * Geo<F>::BYTES, q);
+        for (int r = 0; r < 2; ++r) words[2][r] = load_words<F>(rp[r] + min(b + 2, nb - 1) * Geo<F>::BYTES, q);
         __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
         const _Float16 *xp[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
           xp[c] = reinterpret_cast<const _Float16 *>(s_x[cur] + (k * C + c) * P * 512 + lane);
         f32x4 sum[2][C];
-        block_mma<F, P, C, 2>(raw[0], s_tab, xp, sum);
+        Raw raw[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[r] = unpack<F>(words[0][r], q);
+        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[0][r]));
-          raw[0][r] = raw[1][r];
-          raw[1][r] = raw[2][r];
+          for (int c = 0; c < C; ++c) scale_add(acc[r][c], sum[r][c], block_scale<F>(raw[r]));
+          words[0][r] = words[1][r];
+          words[1][r] = words[2][r];
         }
       }
       cur ^= 1;
@@ -625,11 +629,11 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
   const uint8_t *rp[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) rp[r] = A.down + (e * A.hidden + col + r * 16) * nb * Geo<F>::BYTES;
-  Raw raw[3][2];  // the block in hand and the next two
+  Words words[3][2];  // the block in hand and the next two
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
+    for (int r = 0; r < 2; ++r) words[k][r] = load_words<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
   bool fresh = true;
   const auto body = [&](const int *list, int count) __attribute__((always_inline)) {
     f32x4 acc[2][C] = {};
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[k][r] = load_raw<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
+        for (int r = 0; r < 2; ++r) words[k][r] = load_words<F>(rp[r] + min(k, nb - 1) * Geo<F>::BYTES, q);
     }
     fresh = false;
     for (int b0 = 0; b0 < nb; b0 += KB) {
@@ -663,26 +667,29 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
       for (int j = 0; j < kb; ++j) {
         const int bn = min(b0 + j + 2, nb - 1);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) raw[2][r] = load_raw<F>(rp[r] + bn * Geo<F>::BYTES, q);
+        for (int r = 0; r < 2; ++r) words[2][r] = load_words<F>(rp[r] + bn * Geo<F>::BYTES, q);
         __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
         const _Float16 *xp[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) xp[c] = &s_h[j][c][lane * 8];
         f32x4 sum[2][C];
-        block_mma<F, P, C, 2>(raw[0], s_tab, xp, sum);
+        Raw raw[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw[r] = unpack<F>(words[0][r], q);
+        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int ex = s_ex[j][c * 16 + q * 4 + k];  // past count: of rows not stored
 #pragma unroll
-            for (int r = 0; r < 2; ++r) acc[r][c][k] += ldexpf(block_scale<F>(raw[0][r]) * sum[r][c][k], ex);
+            for (int r = 0; r < 2; ++r) acc[r][c][k] += ldexpf(block_scale<F>(raw[r]) * sum[r][c][k], ex);
           }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          raw[0][r] = raw[1][r];
-          raw[1][r] = raw[2][r];
+          words[0][r] = words[1][r];
+          words[1][r] = words[2][r];
         }
       }
     }
@@ -851,6 +858,8 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   if (!grid || !down_grid || (T && (!gate || !up || !down || !x || !ids || !weights || !y))) return IQ_ERR_NULL;
   if (router && top_k > num_experts) return IQ_ERR_ARG;
   if (T == 0) return IQ_OK;
+  if ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) | reinterpret_cast<uintptr_t>(down)) & 1)
+    return IQ_ERR_ARG;
   const MoePlan P = plan_moe(fmt, down_fmt, hidden, inter, num_experts, dtype, T, top_k);
   if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
   char *base = ws_base(workspace);

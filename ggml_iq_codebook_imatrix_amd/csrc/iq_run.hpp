@@ -141,29 +141,94 @@ struct Raw {
   uint32_t d16;
 };
 
-template <int F> __device__ __forceinline__ Raw load_raw(const uint8_t *blk, int q) {
-  Raw r;
+// The words that hold them, as loaded.  Payload addresses are even, and blocks of
+// 66, 74, 82 and 50 bytes put every other one across 4-byte words.  Measured on
+// one CU, 16 bytes from each of 16 rows four times: 35 cycles at 4-byte aligned
+// addresses, 125 at others (2 and 4 bytes 37 at any, 8 bytes 33 and 64).  So
+// whole aligned words are loaded, and the fields moved into place by a byte
+// permutation when the block's turn comes; d, which lies before the first
+// quarter's fields, comes with that quarter's words.
+struct Words {
+  uint32_t w[9];
+  uint32_t sel;  // the permutation: bytes 2.. or 4.. of a pair of words
+};
+
+template <class V> __device__ __forceinline__ V ldw(uintptr_t p) {  // 4-byte aligned
+  V v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(reinterpret_cast<const void *>(p), 4), sizeof(V));
+  return v;
+}
+struct Words3 {
+  uint32_t x, y, z;
+};
+
+template <int F> __device__ __forceinline__ Words load_words(const uint8_t *blk, int q) {
+  Words r;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(blk) & ~uintptr_t(3);
+  r.sel = (reinterpret_cast<uintptr_t>(blk) & 2) ? 0x07060504u : 0x05040302u;
   if (F == IQ2_XXS || F == IQ2_XS) {
-    const uint4 v = ldu<uint4>(blk + 2 + 16 * q);
-    r.a[0] = v.x; r.a[1] = v.y; r.a[2] = v.z; r.a[3] = v.w;
-    r.s = F == IQ2_XS ? ldu<uint16_t>(blk + 66 + 2 * q) : 0;
-    r.d16 = ldu<uint16_t>(blk);
+    const u32x4 v = ldw<u32x4>(a + 16 * q);
+    r.w[0] = v[0]; r.w[1] = v[1]; r.w[2] = v[2]; r.w[3] = v[3];
+    if (F == IQ2_XXS) {
+      r.w[4] = ldw<uint32_t>(a + 16 * q + 16);
+    } else {  // the last fields and the scales; the fifth word of other quarters is their neighbour's first
+      const Words3 t = ldw<Words3>(a + 64);
+      r.w[4] = t.x; r.w[5] = t.y; r.w[6] = t.z;
+    }
   } else if (F == IQ2_S) {
-    const uint2 k = ldu<uint2>(blk + 2 + 8 * q), m = ldu<uint2>(blk + 34 + 8 * q);
-    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = m.x; r.a[3] = m.y;
-    r.s = ldu<uint16_t>(blk + 66 + 2 * q) | (static_cast<uint32_t>(ldu<uint16_t>(blk + 74 + 2 * q)) << 16);
-    r.d16 = ldu<uint16_t>(blk);
+    const Words3 k = ldw<Words3>(a + 8 * q), m = ldw<Words3>(a + 32 + 8 * q);
+    const uintptr_t t = reinterpret_cast<uintptr_t>(blk) + 66 + 2 * q;
+    const Words3 e = ldw<Words3>(t & ~uintptr_t(3));
+    r.w[0] = k.x; r.w[1] = k.y; r.w[2] = k.z;
+    r.w[3] = m.x; r.w[4] = m.y; r.w[5] = m.z;
+    r.w[6] = e.x; r.w[8] = e.z;
+    r.w[7] = (t & 2) ? 0x07060302u : 0x05040100u;
   } else if (F == IQ1_S) {
-    const uint2 k = ldu<uint2>(blk + 2 + 8 * q);
-    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = ldu<uint32_t>(blk + 34 + 4 * q);
-    r.a[3] = r.s = 0;
-    r.d16 = ldu<uint16_t>(blk);
+    const Words3 k = ldw<Words3>(a + 8 * q);
+    r.w[0] = k.x; r.w[1] = k.y; r.w[2] = k.z;
+    r.w[3] = ldu<uint32_t>(blk + 34 + 4 * q);
   } else {
     const uint2 k = ldu<uint2>(blk + 8 * q), w = ldu<uint2>(blk + 48);
-    r.a[0] = k.x; r.a[1] = k.y; r.a[2] = ldu<uint32_t>(blk + 32 + 4 * q);
-    r.a[3] = 0;
-    r.s = ((q & 2) ? w.y : w.x) >> ((q & 1) * 16);  // scale word q
-    r.d16 = ((w.x >> 12) & 15u) | ((w.x >> 28) << 4) | (((w.y >> 12) & 15u) << 8) | ((w.y >> 28) << 12);
+    r.w[0] = k.x; r.w[1] = k.y; r.w[2] = ldu<uint32_t>(blk + 32 + 4 * q);
+    r.w[3] = w.x; r.w[4] = w.y;
+  }
+  return r;
+}
+
+// All lanes of the wave take part (words are passed between the quarters).
+template <int F> __device__ __forceinline__ Raw unpack(const Words &v, int q) {
+  Raw r;
+  const int lane = threadIdx.x & 63;
+  r.a[2] = r.a[3] = r.s = 0;
+  if (F == IQ1_M) {
+    r.a[0] = v.w[0]; r.a[1] = v.w[1]; r.a[2] = v.w[2];
+    r.s = ((q & 2) ? v.w[4] : v.w[3]) >> ((q & 1) * 16);  // scale word q
+    r.d16 = ((v.w[3] >> 12) & 15u) | ((v.w[3] >> 28) << 4) | (((v.w[4] >> 12) & 15u) << 8) | ((v.w[4] >> 28) << 12);
+    return r;
+  }
+  const auto pair = [&](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, v.sel); };
+  // d: the two bytes before the fields, in the first quarter's first word
+  const uint32_t first = v.sel == 0x07060504u ? v.w[0] >> 16 : v.w[0] & 0xffffu;
+  r.d16 = static_cast<uint32_t>(__shfl(static_cast<int>(first), lane & 15, 64));
+  r.a[0] = pair(v.w[0], v.w[1]);
+  r.a[1] = pair(v.w[1], v.w[2]);
+  if (F == IQ2_XXS || F == IQ2_XS) {
+    uint32_t fifth = v.w[4];
+    if (F == IQ2_XS) {
+      const uint32_t other = static_cast<uint32_t>(__shfl(static_cast<int>(v.w[0]), lane + 16, 64));
+      fifth = q == 3 ? v.w[4] : other;
+      // the scales' bytes 2q and 2q + 1 lie 2 + 2q bytes into the words, or 4 + 2q
+      const uint32_t lo = pair(v.w[4], v.w[5]), hi = pair(v.w[5], v.w[6]);
+      r.s = ((q & 2) ? hi : lo) >> ((q & 1) * 16);
+    }
+    r.a[2] = pair(v.w[2], v.w[3]);
+    r.a[3] = pair(v.w[3], fifth);
+  } else if (F == IQ2_S) {
+    r.a[2] = pair(v.w[3], v.w[4]);
+    r.a[3] = pair(v.w[4], v.w[5]);
+    r.s = __builtin_amdgcn_perm(v.w[8], v.w[6], v.w[7]);
+  } else {
+    r.a[2] = v.w[3];
   }
   return r;
 }
@@ -270,59 +335,6 @@ __device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = fmaf(d, part[k], acc[k]);
 }
-
-// 16 bytes of a payload that ends at `end`.  A row's last unit may reach into the
-// next row, but not past the end: there the bytes come one by one.
-__device__ __forceinline__ u32x4 load_unit(const uint8_t *p, const uint8_t *end) {
-  if (p + 16 <= end) return ldu<u32x4>(p);
-  u32x4 w = {0, 0, 0, 0};
-#pragma unroll 1
-  for (int j = 0; j < 16; ++j)
-    if (p + j < end) {
-      const uint32_t v = static_cast<uint32_t>(p[j]) << (8 * (j & 3));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] |= (j >> 2) == k ? v : 0u;
-    }
-  return w;
-}
-
-// A wave's payload through LDS of its own.  Read straight into operands, a
-// block's fields touch 16 rows in pieces of 64 bytes and less, and every line is
-// asked for two to three times: the requests, not the bytes, then bound the
-// kernels.  Here KC blocks of 16 R rows come in as consecutive 16-byte units (U a
-// row, from any address), are kept in registers while the blocks before are
-// multiplied, and the fields are read back from LDS (which takes any alignment).
-template <int F, int R, int KC> struct Payload {
-  static constexpr int U = (KC * Geo<F>::BYTES + 15) / 16, kUnits = R * 16 * U, kPer = (kUnits + 63) / 64;
-  const uint8_t *at[kPer];
-  u32x4 v[kPer];
-  // rowp(i): row i of the wave's 16 R
-  template <class Fn> __device__ __forceinline__ void init(Fn rowp) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int u = min(i * 64 + lane, kUnits - 1);
-      at[i] = rowp(u / U) + (u % U) * 16;
-    }
-  }
-  // blocks b .. b + KC - 1; end: the payload's
-  __device__ __forceinline__ void load(int64_t b, const uint8_t *end) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = load_unit(at[i] + b * Geo<F>::BYTES, end);
-  }
-  __device__ __forceinline__ void store(u32x4 *lds) const {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i * 64 + lane < kUnits) lds[i * 64 + lane] = v[i];
-  }
-  // the lane's fields of block k of the KC, row tile r
-  static __device__ __forceinline__ Raw raw(const u32x4 *lds, int r, int k) {
-    const int lane = threadIdx.x & 63;
-    return load_raw<F>(reinterpret_cast<const uint8_t *>(lds + (r * 16 + (lane & 15)) * U) + k * Geo<F>::BYTES,
-                       lane >> 4);
-  }
-};
 
 // ---------------------------------------------------------------------------
 // Tokens to fp16
@@ -463,23 +475,26 @@ __device__ __forceinline__ void split_blocks(int64_t nb, const Split &S, const u
                                              Add add, f32x4 (&acc)[RT][M][C]) {
   const int q = (threadIdx.x & 63) >> 4;
   Operand<P, C> x;
-  Raw raw[M];
+  Words words[M];
 #pragma unroll
-  for (int m = 0; m < M; ++m) raw[m] = load_raw<F>(rowp(m, 0) + static_cast<int64_t>(S.kg) * Geo<F>::BYTES, q);
+  for (int m = 0; m < M; ++m) words[m] = load_words<F>(rowp(m, 0) + static_cast<int64_t>(S.kg) * Geo<F>::BYTES, q);
   for (int64_t b = S.kg; b < nb; b += S.kw) {
     loadx(b, x);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      Raw next[M];  // the next row tile, or the first of the next block
+      Words next[M];  // the next row tile, or the first of the next block
       const int64_t bn = rt + 1 < RT ? b : min(b + S.kw, nb - 1);
 #pragma unroll
-      for (int m = 0; m < M; ++m) next[m] = load_raw<F>(rowp(m, rt + 1 < RT ? rt + 1 : 0) + bn * Geo<F>::BYTES, q);
+      for (int m = 0; m < M; ++m) next[m] = load_words<F>(rowp(m, rt + 1 < RT ? rt + 1 : 0) + bn * Geo<F>::BYTES, q);
       __builtin_amdgcn_sched_barrier(0);  // one row tile's work at a time: more costs registers, and with them waves
       f32x4 part[M][C];
+      Raw raw[M];
 #pragma unroll
-      for (int m = 0; m < M; ++m)
+      for (int m = 0; m < M; ++m) {
+        raw[m] = unpack<F>(words[m], q);
 #pragma unroll
         for (int c = 0; c < C; ++c) part[m][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -496,7 +511,7 @@ __device__ __forceinline__ void split_blocks(int64_t nb, const Split &S, const u
         const float d = block_scale<F>(raw[m]);
 #pragma unroll
         for (int c = 0; c < C; ++c) add(acc[rt][m][c], part[m][c], d, c);
-        raw[m] = next[m];
+        words[m] = next[m];
       }
     }
   }

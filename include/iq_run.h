@@ -45,7 +45,9 @@ extern "C" {
  * W the weight iq_dequantize returns for `packed`.  Without adapters (rank 0)
  * the second term is absent.
  *
- *  packed   (device) [rows, cols/256, block_bytes] payload; any alignment.
+ *  packed   (device) [rows, cols/256, block_bytes] payload, at an even address.
+ *           Whole aligned 4-byte words are read: of the words that hold its first
+ *           and last bytes, the bytes outside the payload as well (and unused).
  *  grid     (device) [grid_size, 8] f32 codebook the payload was encoded with.
  *  x        (device) [T, cols] tokens, dtype f32 or bf16.
  *  lora_a   (device) [num_adapters, rank, cols], lora_b (device) [num_adapters,
@@ -64,7 +66,8 @@ extern "C" {
  * Errors: IQ_ERR_FMT, IQ_ERR_DTYPE, IQ_ERR_NULL (grid, packed, x, y; with
  * adapters lora_a, lora_b, lora_ids; a needed workspace), IQ_ERR_SHAPE (rows or
  * T negative, cols <= 0 or % 256, sizes whose launches would not fit a grid),
- * IQ_ERR_ARG (rank outside [0, 1024], num_adapters < 1 with a rank),
+ * IQ_ERR_ARG (rank outside [0, 1024], num_adapters < 1 with a rank, packed at an
+ * odd address),
  * IQ_ERR_WORKSPACE, IQ_ERR_HIP. */
 int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const float *grid, const void *x,
               int dtype, int64_t T, const void *lora_a, const void *lora_b, const float *lora_scale,
@@ -84,7 +87,7 @@ int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int
  *
  *  gate, up (device) [num_experts * inter, hidden/256, block_bytes(fmt)] payloads:
  *           expert e's rows are e * inter ... (the fused layout iq_quantize
- *           encodes with rows_per_expert = inter).
+ *           encodes with rows_per_expert = inter).  Payloads as in iq_linear.
  *  down     (device) [num_experts * hidden, inter/256, block_bytes(down_fmt)].
  *  grid, down_grid  (device) the codebooks of fmt and down_fmt (the same pointer
  *           where both are the same).
@@ -107,7 +110,7 @@ int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int
  * Errors: IQ_ERR_FMT, IQ_ERR_DTYPE, IQ_ERR_NULL, IQ_ERR_SHAPE (T negative, hidden
  * or inter <= 0 or % 256, sizes whose launches would not fit a grid), IQ_ERR_ARG
  * (num_experts outside [1, 4096], top_k outside [1, 64], top_k > num_experts with
- * a router), IQ_ERR_WORKSPACE, IQ_ERR_HIP. */
+ * a router, a payload at an odd address), IQ_ERR_WORKSPACE, IQ_ERR_HIP. */
 int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const uint8_t *down, int64_t hidden,
            int64_t inter, int num_experts, const float *grid, const float *down_grid, const void *x, int dtype,
            int64_t T, const void *router, int router_dtype, int top_k, int renormalize, int32_t *ids,

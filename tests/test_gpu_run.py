@@ -62,6 +62,17 @@ def round_to(v, dtype):
     return torch.from_numpy(v).to(torch.float32).to(dtype).double().numpy()
 
 
+def shifted(t, by):
+    """The same values, `by` elements into a buffer of their own."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+    buf[by:] = t.reshape(-1)
+    return buf[by:].view(t.shape)
+
+
+def odd(t):
+    return shifted(t, 1)
+
+
 # --------------------------------------------------------------------------
 # iq_linear
 # --------------------------------------------------------------------------
@@ -238,9 +249,18 @@ def test_linear_codebook_rounding_is_reported(api, orc):
 
 @pytest.mark.parametrize("T", [1, 20, 200])
 def test_linear_views_guards_and_empty(api, T):
-    """Odd addresses of payload and tokens, caller buffers, memory behind every output, empty calls."""
+    """Every even address of the payload, odd ones of the rest, caller buffers, memory behind every output, empty calls."""
     print("[case] linear views", T, flush=True)
-    fmt, rows, nb, N, r = "IQ2_XXS", 37, 3, 2, 3
+    rows, nb, N, r = 37, 3, 2, 3
+    for fmt in FORMATS:
+        grid, pay = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
+        x = dev(inputs.activations(T, nb * 256, 7, 8)).bfloat16()
+        want = api.linear(fmt, pay, grid, x)
+        for by in (2, 4, 6, 14):
+            assert torch.equal(api.linear(fmt, shifted(pay, by), grid, x), want), (fmt, by)
+        with pytest.raises(api.IQError):
+            api.linear(fmt, odd(pay), grid, x)
+    fmt = "IQ2_XXS"
     grid, pay = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
     x = dev(inputs.activations(T, nb * 256, 7, 8)).bfloat16()
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -249,14 +269,10 @@ def test_linear_views_guards_and_empty(api, T):
     ids = (torch.arange(T, device="cuda") % N).int()
     want = api.linear(fmt, pay, grid, x, a, b, None, ids)
 
-    def odd(t):
-        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
-        buf[1:] = t.reshape(-1)
-        return buf[1:].view(t.shape)
     need = api.linear_workspace_size(fmt, rows, nb * 256, x.dtype, T, r)
     ws = torch.full((need + 100,), 7, dtype=torch.uint8, device="cuda")
     out = torch.full((T + 2, rows), 7.0, dtype=x.dtype, device="cuda")
-    got = api.linear(fmt, odd(pay), odd(grid), odd(x), odd(a), odd(b), None, ids, out=out[1:T + 1],
+    got = api.linear(fmt, shifted(pay, 2), odd(grid), odd(x), odd(a), odd(b), None, ids, out=out[1:T + 1],
                      workspace=ws[1:need + 1])
     assert got.data_ptr() == out[1].data_ptr() and torch.equal(got, want)
     assert bool((out[0] == 7).all()) and bool((out[T + 1] == 7).all())
@@ -402,16 +418,13 @@ def test_moe_views_and_guards(api, T):
     kw = dict(down_fmt=dfmt, down_grid=dev(dgrid), top_k=k)
     want, wi, ww = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, router=router, **kw)
 
-    def odd(t):
-        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
-        buf[1:] = t.reshape(-1)
-        return buf[1:].view(t.shape)
     need = api.moe_workspace_size(fmt, H, I, E, x.dtype, T, k, dfmt)
     ws = torch.full((need + 100,), 7, dtype=torch.uint8, device="cuda")
     out = torch.full((T + 2, H), 7.0, dtype=x.dtype, device="cuda")
     ids = torch.full((T + 2, k), 7, dtype=torch.int32, device="cuda")
     weights = torch.full((T + 2, k), 7.0, device="cuda")
-    api.moe(fmt, odd(dev(gate)), odd(dev(up)), odd(dev(down)), odd(dev(grid)), odd(x), E, router=odd(router), **kw,
+    api.moe(fmt, shifted(dev(gate), 2), shifted(dev(up), 6), shifted(dev(down), 2), odd(dev(grid)), odd(x), E,
+            router=odd(router), **kw,
             ids=ids[1:T + 1], weights=weights[1:T + 1], out=out[1:T + 1], workspace=ws[1:need + 1])
     assert torch.equal(out[1:T + 1], want) and torch.equal(ids[1:T + 1], wi) and torch.equal(weights[1:T + 1], ww)
     for t in (out, ids, weights):

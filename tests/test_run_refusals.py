@@ -65,14 +65,16 @@ LINEAR_BAD = [
     (dict(x=None), -3), (dict(y=None), -3), (dict(a=None), -3), (dict(b=None), -3), (dict(ids=None), -3),
     (dict(ws=None), -3), (dict(cols=300), -4), (dict(cols=0), -4), (dict(rows=-1), -4), (dict(T=-1), -4),
     (dict(rows=1 << 40), -4), (dict(T=1 << 40), -4), (dict(cols=1 << 40), -4), (dict(rank=-1), -5),
-    (dict(rank=1025), -5), (dict(N=0), -5), (dict(wn=64), -7),
+    (dict(rank=1025), -5), (dict(N=0), -5), (dict(packed=ctypes.c_void_p(0x100001)), -5), (dict(wn=64), -7),
 ]
 MOE_BAD = [
     (dict(fmt=5), -1), (dict(down_fmt=9), -1), (dict(dtype=3), -2), (dict(rdtype=7), -2), (dict(grid=None), -3),
     (dict(dgrid=None), -3), (dict(gate=None), -3), (dict(up=None), -3), (dict(down=None), -3), (dict(x=None), -3),
     (dict(ids=None), -3), (dict(weights=None), -3), (dict(y=None), -3), (dict(ws=None), -3), (dict(hidden=500), -4),
     (dict(inter=128), -4), (dict(inter=0), -4), (dict(T=-3), -4), (dict(T=1 << 40), -4), (dict(hidden=1 << 30), -4),
-    (dict(E=0), -5), (dict(E=4097), -5), (dict(k=0), -5), (dict(k=65), -5), (dict(k=9), -5), (dict(wn=100), -7),
+    (dict(E=0), -5), (dict(E=4097), -5), (dict(k=0), -5), (dict(k=65), -5), (dict(k=9), -5),
+    (dict(gate=ctypes.c_void_p(0x100001)), -5), (dict(up=ctypes.c_void_p(0x100003)), -5),
+    (dict(down=ctypes.c_void_p(0x100001)), -5), (dict(wn=100), -7),
 ]
 
 
