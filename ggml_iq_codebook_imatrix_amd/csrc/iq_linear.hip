@@ -42,8 +42,8 @@ __device__ __forceinline__ int tile_adapter(const Lora &L, int64_t tt, int64_t T
 }
 
 // v for the tokens of tile tt that share the adapter of token `slot`, 16 ranks:
-// the tile's 16 tokens (A) by the adapter's 16 rows (B), K split over the eight
-// waves; rows of other tokens are formed as well and dropped.
+// 16 tokens (A) by the adapter's 16 rows (B), K split over the eight waves; the
+// rows of tokens with other adapters are dropped.
 __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int rt, int slot, f32x4 *s_red) {
   const Lora &L = P.L;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -56,7 +56,8 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
   const int a = __builtin_amdgcn_readlane(mine, slot);
   const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
   if (a < 0 || (group & ((1u << slot) - 1u))) return;  // an earlier token's workgroup does it
-  const int64_t t = min(tt * 16 + n, P.T - 1);
+  // rows of other tokens read this one's: fewer lines
+  const int64_t t = tt * 16 + (((group >> n) & 1u) ? n : slot);
   const int j = min(rt * 16 + n, L.rank - 1);
   const int64_t xr = t * P.cols + q * 8, ar = (static_cast<int64_t>(a) * L.rank + j) * P.cols + q * 8;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -145,15 +146,64 @@ __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
 
 // acc[r][c] += B v of the adapters that the tiles' tokens name.  Of tile c, wave
 // w of nw takes the adapters whose turn t (in order of first use) has
-// (t + c) % nw == w; a round fetches one adapter for each of the C tiles before it
+// (t + c) % nw == w; a round takes one adapter of each of the C tiles, 32 ranks
+// (bf16) or 16 at a time, and what the next one needs is fetched before this one
 // multiplies.  fp32 v is the sum of three bf16 values beside a bf16 B (no
 // rounding), and goes through the fp32 cores beside an fp32 B.  Rows of v of
 // other tokens hold anything; what they give is dropped.
+template <int P, int C, int R> struct LoraStep {
+  bf16x8 v[C][3], w[C][R];   // bf16
+  f32x4 vf[C], wf[C][R];     // float32
+  uint32_t group[C];         // tokens of the tile
+};
+
+template <int P, int C, int R>
+__device__ __forceinline__ void lora_fetch(const Lora &L, int64_t tt0, int64_t rows, int64_t row0, int ch,
+                                           const int (&a)[C], LoraStep<P, C, R> &s) {
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (!s.group[c]) continue;
+    if (P == 1) {
+      const int j = ch * 32 + q * 8;
+      const uint16_t *vp = static_cast<const uint16_t *>(L.v) + ((tt0 + c) * L.chunks + ch) * 1536 + lane * 8;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) s.v[c][k] = *reinterpret_cast<const bf16x8 *>(vp + k * 512);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t row = min(row0 + r * 16 + n, rows - 1);
+        const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+        if ((L.rank & 7) == 0) {  // whole eights; past the rank v is zero, and the last eight will do
+          s.w[c][r] = ldu<bf16x8>(b + min(j, L.rank - 8));
+        } else {
+          s.w[c][r] = bf16x8{};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (j + i < L.rank) s.w[c][r][i] = __builtin_bit_cast(__bf16, b[j + i]);
+        }
+      }
+    } else {
+      const int j = ch * 16 + q * 4;
+      s.vf[c] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(L.v) + ((tt0 + c) * L.chunks + ch) * 256 +
+                                                 lane * 4);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t row = min(row0 + r * 16 + n, rows - 1);
+        const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+        s.wf[c][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < L.rank) s.wf[c][r][i] = b[j + i];
+      }
+    }
+  }
+}
+
 template <int P, int C, int R>
 __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t T, int64_t rows, int64_t row0,
                                             int wave, int nw, f32x4 (&acc)[R][C]) {
-  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  int mine[C], turn[C];
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  int mine[C], turn[C], a[C];
   uint32_t todo[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -161,12 +211,11 @@ __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t 
     todo[c] = static_cast<uint32_t>(__ballot(mine[c] >= 0)) & 0xffffu;
     turn[c] = c;
   }
-  for (;;) {
-    int a[C];
-    uint32_t group[C], any = 0;
+  // the wave's next adapter of each tile; 0: none is left
+  const auto next_round = [&](uint32_t (&group)[C]) __attribute__((always_inline)) {
+    uint32_t any = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      a[c] = 0;
       group[c] = 0;
       while (todo[c] && !group[c]) {
         a[c] = __builtin_amdgcn_readlane(mine[c], __builtin_ctz(todo[c]));
@@ -176,81 +225,44 @@ __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t 
       }
       any |= group[c];
     }
-    if (!any) return;
-    f32x4 d[R][C];
+    return any;
+  };
+  LoraStep<P, C, R> now, then;
+  if (!next_round(now.group)) return;
+  int ch = 0;
+  lora_fetch<P, C, R>(L, tt0, rows, row0, 0, a, now);
+  for (;;) {
+    uint32_t more = 1;
+    if (++ch < L.chunks) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int c = 0; c < C; ++c) then.group[c] = now.group[c];
+    } else {
+      ch = 0;
+      more = next_round(then.group);
+    }
+    if (more) lora_fetch<P, C, R>(L, tt0, rows, row0, ch, a, then);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < C; ++c) d[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int ch = 0; ch < L.chunks; ++ch) {
-      if (P == 1) {
-        bf16x8 v[C][3], w[C][R];
-        const int j = ch * 32 + q * 8;
+    for (int c = 0; c < C; ++c) {
+      if (!now.group[c]) continue;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (!group[c]) continue;
-          const uint16_t *vp = static_cast<const uint16_t *>(L.v) + ((tt0 + c) * L.chunks + ch) * 1536 + lane * 8;
+      for (int r = 0; r < R; ++r) {
+        f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (P == 1) {
 #pragma unroll
-          for (int s = 0; s < 3; ++s) v[c][s] = *reinterpret_cast<const bf16x8 *>(vp + s * 512);
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int64_t row = min(row0 + r * 16 + n, rows - 1);
-            const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
-            w[c][r] = bf16x8{};
-            if (j + 8 <= L.rank) {
-              w[c][r] = ldu<bf16x8>(b + j);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (j + i < L.rank) w[c][r][i] = __builtin_bit_cast(__bf16, b[j + i]);
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (!group[c]) continue;
-#pragma unroll
-          for (int s = 0; s < 3; ++s)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-              d[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c][s], w[c][r], d[r][c], 0, 0, 0);
-        }
-      } else {
-        f32x4 v[C], w[C][R];
-        const int j = ch * 16 + q * 4;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (!group[c]) continue;
-          v[c] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(L.v) +
-                                                  ((tt0 + c) * L.chunks + ch) * 256 + lane * 4);
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int64_t row = min(row0 + r * 16 + n, rows - 1);
-            const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
-            w[c][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (j + i < L.rank) w[c][r][i] = b[j + i];
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (!group[c]) continue;
+          for (int k = 0; k < 3; ++k) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.v[c][k], now.w[c][r], d, 0, 0, 0);
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-              d[r][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[c][i], w[c][r][i], d[r][c], 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_16x16x4f32(now.vf[c][i], now.wf[c][r][i], d, 0, 0, 0);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((now.group[c] >> (q * 4 + k)) & 1u) acc[r][c][k] += d[k];
       }
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if ((group[c] >> (q * 4 + k)) & 1u)
-#pragma unroll
-          for (int r = 0; r < R; ++r) acc[r][c][k] += d[r][c][k];
+    if (!more) return;
+    now = then;
   }
 }
 
@@ -545,13 +557,17 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
   }
   if (A.L.rank) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      f32x4 a[R][1];
+    for (int c = 0; c < C; c += 2) {
+      f32x4 a[R][2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) a[r][0] = acc[r][c];
-      lora_expand<1, 1, R>(A.L, tt0 + c, A.T, A.rows, row0, 0, 1, a);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int r = 0; r < R; ++r) acc[r][c] = a[r][0];
+        for (int k = 0; k < 2; ++k) a[r][k] = acc[r][c + k];
+      lora_expand<1, 2, R>(A.L, tt0 + c, A.T, A.rows, row0, 0, 1, a);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc[r][c + k] = a[r][k];
     }
   }
 #pragma unroll

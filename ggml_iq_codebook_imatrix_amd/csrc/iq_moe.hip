@@ -160,8 +160,7 @@ __device__ __forceinline__ void pick_top(const MoeArgs &A, int64_t t, int32_t *i
     const int e = lane + 64 * j;
     key[j] = e < E ? order_key(logit(e)) : 0;
   }
-  double top = 0.0;
-  float mine = 0.0f, sum = 0.0f;
+  double top = 0.0, mine = 0.0;
   int my_id = 0;
   for (int s = 0; s < top_k; ++s) {
     uint64_t best = key[0];
@@ -194,28 +193,30 @@ __device__ __forceinline__ void pick_top(const MoeArgs &A, int64_t t, int32_t *i
       if (lane == from && j == wj) key[j] = 0;
     const double v = key_value(won);
     if (s == 0) top = v;
-    const float p = expf(static_cast<float>(v - top));
-    sum += p;
     if (lane == s) {
-      mine = p;
+      mine = v;
       my_id = from + 64 * wj;
     }
   }
+  const float p = lane < top_k ? expf(static_cast<float>(mine - top)) : 0.0f;
+  float sum = p;
   if (!A.renorm) {
     sum = 0.0f;
     for (int e = lane; e < E; e += 64) sum += expf(static_cast<float>(logit(e) - top));
-#pragma unroll
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
   }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if (lane < top_k) {
     ids[lane] = my_id;
-    weights[lane] = mine / sum;
+    weights[lane] = p / sum;
   }
 }
 
 __global__ void __launch_bounds__(64) topk_kernel(MoeArgs A) {
   const int64_t t = blockIdx.x;
-  if (A.E <= 256)
+  if (A.E <= 128)
+    pick_top<2>(A, t, A.ids + t * A.top_k, A.weights + t * A.top_k);
+  else if (A.E <= 256)
     pick_top<4>(A, t, A.ids + t * A.top_k, A.weights + t * A.top_k);
   else
     pick_top<64>(A, t, A.ids + t * A.top_k, A.weights + t * A.top_k);
@@ -252,8 +253,12 @@ __device__ __forceinline__ void few_ids(const MoeArgs &A, FewPairs &S, bool pick
   const int np = static_cast<int>(A.npair);
   if (threadIdx.x < kFewExperts / 32) S.bits[threadIdx.x] = 0;
   if (pick) {
-    for (int t = wave; t < A.T; t += nw)
-      pick_top<4>(A, t, S.ids + t * A.top_k, S.w + t * A.top_k);
+    for (int t = wave; t < A.T; t += nw) {
+      if (A.E <= 128)
+        pick_top<2>(A, t, S.ids + t * A.top_k, S.w + t * A.top_k);
+      else
+        pick_top<4>(A, t, S.ids + t * A.top_k, S.w + t * A.top_k);
+    }
   } else {
     for (int p = threadIdx.x; p < np; p += blockDim.x) {
       const int e = A.ids[p];

@@ -291,8 +291,7 @@ __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *
     for (int p = 3; p >= 0; --p) {
       const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
       o[p] = __builtin_bit_cast(uint32_t, v) ^ (t & 0x80008000u);
-      asm("" : "+v"(t));  // keeps the doublings from being merged into shifts or multiplications
-      t += t;
+      asm("v_add_u32 %0, %0, %0" : "+v"(t));  // t + t in C becomes a shift, at half the rate
     }
   }
   return __builtin_bit_cast(half8v, make_uint4(o[0], o[1], o[2], o[3]));

@@ -95,9 +95,9 @@ def exact_linear(orc, fmt, rows, nb, T, N, r, seed):
     y, size = x.astype(np.float64) @ w.T, np.abs(x).astype(np.float64) @ np.abs(w).T
     for n in range(N):
         at = ids == n
-        more = scale[n] * ((x[at].astype(np.float64) @ a[n].T) @ b[n].T)
-        y[at] += more
-        size[at] += np.abs(more)
+        v = x[at].astype(np.float64) @ a[n].T
+        y[at] += scale[n] * (v @ b[n].T)
+        size[at] += scale[n] * (np.abs(v) @ np.abs(b[n]).T)
     return grid, p, x, a, b, scale.astype(np.float32), ids, y, size
 
 
@@ -107,17 +107,18 @@ def test_linear_exact(api, orc, fmt, dtype):
     for i, (rows, nb, T, N, r) in enumerate(SHAPES):
         print("[case] linear exact", fmt, dtype, rows, nb, T, N, r, flush=True)
         grid, p, x, a, b, scale, ids, y, size = exact_linear(orc, fmt, rows, nb, T, N, r, 20 + i)
-        # Weights are multiples of 2^-11, adapters' products of 2^-2.  `size`, the sum of |x w| and of the adapter's
-        # product, bounds every partial sum: below 2^13 a float32 holds each exactly.  Above it (adapters reach 2^14)
-        # the at most 10 additions of 8 waves' sums and the adapter's product round by 2^-24 of at most `size` each.
+        # Weights are multiples of 2^-11, adapters' products of 2^-2.  `size`, the sum of |x w| and of scale |v b| over
+        # the ranks, bounds every partial sum in any order: below 2^13 a float32 holds each exactly.  Above it (adapters
+        # of large rank) no output takes more than 8 + 64 / 16 + 2 additions of sums that are themselves exact (blocks
+        # alone stay below 2^13), each off by 2^-24 of at most `size`.
         lora = dict(lora_a=dev(a, dtype), lora_b=dev(b, dtype), lora_scale=dev(scale), lora_ids=dev(ids)) if N else {}
         st = api.new_status()
         got = api.linear(fmt, dev(p), dev(grid), dev(x, dtype), status=st, **lora)
         assert got.dtype == dtype and got.shape == (T, rows)
         sure = size < 2.0 ** 13
-        assert sure.mean() > 0.5
+        assert sure.mean() > (0.5 if r < 64 else 0.1)
         assert np.array_equal(f64(got)[sure], round_to(y, dtype)[sure]), (rows, nb, T, N, r)
-        near = np.abs(f64(got) - y) <= 10 * U * size + np.abs(y) * (2.0 ** -8 if dtype == torch.bfloat16 else U)
+        near = np.abs(f64(got) - y) <= 14 * U * size + np.abs(y) * (2.0 ** -8 if dtype == torch.bfloat16 else U)
         assert near.all(), (rows, nb, T, N, r)
         assert api.read_status(st) == 0
 
