@@ -464,9 +464,9 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
 // more rounding of 2^-24 a block, bf16 outputs round by 2^-9).  A block of d = 0
 // counts with zero weights instead.  Token operands go from memory to LDS
 // directly, half a block ahead.
-template <int F, int C>
+template <int F, int C, int R>
 __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
-  constexpr int R = 4, kHalf = C * 256;  // 16-byte units of half a block: C tiles of 4 KiB
+  constexpr int kHalf = C * 256;  // 16-byte units of half a block: C tiles of 4 KiB
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ u32x4 s_x[2][kHalf];
   load_table<F>(s_tab, A.tab);
@@ -632,33 +632,51 @@ void launch_tile(const LinearArgs &A, hipStream_t stream) {
                      dim3(512), 0, stream, A);
 }
 
-template <int F, int C> void launch_prompt(const LinearArgs &A, hipStream_t stream) {
-  hipLaunchKernelGGL((linear_prompt_kernel<F, C>),
-                     dim3(static_cast<unsigned>((A.rows + 511) / 512), static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+template <int F, int C, int R> void launch_prompt(const LinearArgs &A, hipStream_t stream) {
+  constexpr int rows = 8 * 16 * R;
+  hipLaunchKernelGGL((linear_prompt_kernel<F, C, R>),
+                     dim3(static_cast<unsigned>((A.rows + rows - 1) / rows),
+                          static_cast<unsigned>((A.X.ntile + C - 1) / C)),
                      dim3(512), 0, stream, A);
 }
 
+// What a kernel takes of a large launch: rows and token tiles of a workgroup, one
+// workgroup a CU, and the cost of the first round over 256 CUs and of each further
+// one (us at 4,096 columns).
+struct TileCost {
+  int rows, C, first, more;
+};
+inline int64_t tile_cost(const TileCost &k, int64_t rows, int64_t ntile) {
+  const int64_t wgs = (rows + k.rows - 1) / k.rows * ((ntile + k.C - 1) / k.C);
+  return k.first + ((wgs + 255) / 256 - 1) * k.more;
+}
+
 template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
-  const int64_t tiles = (A.rows + 15) / 16 / split_rw(A.nb);  // row tiles, by the row groups of a workgroup
-  if (A.X.ntile == 1) {
-    if (tiles <= 768)
+  const int64_t ntile = A.X.ntile, rtiles = (A.rows + 15) / 16, pairs = rtiles * ntile;
+  if (ntile == 1) {
+    if (rtiles / split_rw(A.nb) <= 768)
       launch_split<F, P, 1, 1>(A, stream);
     else
       launch_split<F, P, 1, 4>(A, stream);
-  } else if (A.X.ntile == 2) {
-    launch_split<F, P, 2, 2>(A, stream);
-  } else if (P == 2 || A.X.ntile <= 4) {
-    launch_tile<F, P, 4, 2, 2 / P>(A, stream);
-  } else {
-    // one workgroup a CU: the tile whose rounds over 256 CUs cost least
-    const auto cost = [&](int64_t C) {
-      const int64_t wgs = (A.rows + 511) / 512 * ((A.X.ntile + C - 1) / C);
-      return (wgs + 255) / 256 * C;
-    };
-    if (cost(6) <= cost(4))
-      launch_prompt<F, 6>(A, stream);
-    else
-      launch_prompt<F, 4>(A, stream);
+    return;
+  }
+  // Measured at 4,096 columns, bf16 (float32): 512 tile pairs 16.5 us with one row
+  // tile a wave and 18.4 with two (26.1, 27.7), 1,024 pairs 22.5 and 21.5 (34.0,
+  // 28.1).  2,048 pairs take 31 us with two and 38 in tiles (4,096: 59 and 70); two
+  // token tiles would leave half of a tile empty.
+  if (pairs <= 512) return launch_split<F, P, 2, 1>(A, stream);
+  if (ntile == 2 || pairs <= 2048 * P) return launch_split<F, P, 2, 2>(A, stream);
+  const TileCost costs[2][5] = {{{64, 4, 37, 21}, {128, 4, 47, 31}, {128, 8, 56, 46}, {256, 8, 80, 74}, {256, 10, 92, 90}},
+                                {{128, 4, 70, 47}, {256, 4, 90, 76}}};
+  int best = 0;
+  for (int i = 1; i < (P == 1 ? 5 : 2); ++i)
+    if (tile_cost(costs[P - 1][i], A.rows, ntile) < tile_cost(costs[P - 1][best], A.rows, ntile)) best = i;
+  if (best == 0) return launch_tile<F, P, 4, 1, 2 / P>(A, stream);
+  if (best == 1) return launch_tile<F, P, 4, 2, 2 / P>(A, stream);
+  if constexpr (P == 1) {
+    if (best == 2) return launch_prompt<F, 8, 1>(A, stream);
+    if (best == 3) return launch_prompt<F, 8, 2>(A, stream);
+    launch_prompt<F, 10, 2>(A, stream);
   }
 }
 
