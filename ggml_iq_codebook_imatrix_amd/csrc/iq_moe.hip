@@ -308,51 +308,72 @@ __device__ __forceinline__ int few_expert(const MoeArgs &A, FewPairs &S, int slo
   return e;
 }
 
+// 16 rows of gate and up of one expert a row group, K split over its waves
+// (split_blocks); h of its pairs.  For few pairs.
 template <int F, int P>
 __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
+  constexpr int C = 1, RT = 1, N = 16;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ f32x4 s_red[8 * 2 * 64];
+  __shared__ f32x4 s_red[8 * 2 * C * 64];
   __shared__ FewPairs S;
   load_table<F>(s_tab, A.tab);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int64_t nb = A.hidden >> 8, rowbytes = nb * Geo<F>::BYTES, stride = A.X.ntile * P * 4096;
+  const Split W = split_of(nb);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4, tiles = static_cast<int>(A.inter >> 4);
+  const int per = (tiles + W.rw * RT - 1) / (W.rw * RT), tile0 = static_cast<int>(blockIdx.x % per) * W.rw * RT;
   few_ids(A, S, A.pick);
-  const int64_t nrt = A.inter / 16, rt = blockIdx.x % nrt;
-  const int e = few_expert(A, S, static_cast<int>(blockIdx.x / nrt));
+  const int e = few_expert(A, S, static_cast<int>(blockIdx.x / per));
   if (e < 0) return;
-  const int count = S.n, n = lane & 15, q = lane >> 4;
-  const int64_t nb = A.hidden >> 8, row = e * A.inter + rt * 16 + n;
-  const uint8_t *rp[2] = {A.gate + row * nb * Geo<F>::BYTES, A.up + row * nb * Geo<F>::BYTES};
-  for (int c0 = 0; c0 < count; c0 += 16) {
-    const int t = S.list[min(c0 + n, count - 1)] / A.top_k;
-    const _Float16 *x0 = A.X.x16 + (q * 16 + t) * 8;  // one tile of tokens
-    f32x4 acc[2] = {};
-    for (int64_t b = wave; b < nb; b += nw) {
-      Raw raw[2];
+  for (int c0 = 0; c0 < S.n; c0 += N) {
+    const int *list = S.list + c0;
+    const int count = min(N, S.n - c0);
+    const _Float16 *x0[C];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) raw[r] = unpack<F>(load_words<F>(rp[r] + b * Geo<F>::BYTES, q), q);
-      const _Float16 *const xp[1] = {x0 + b * P * 4096};
-      f32x4 part[2][1];
-      block_mma<F, P, 1, 2>(raw, s_tab, xp, part);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) scale_add(acc[r], part[r][0], block_scale<F>(raw[r]));
+    for (int c = 0; c < C; ++c) {
+      const int64_t t = list[min(c * 16 + n, count - 1)] / A.top_k;
+      x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
     }
-    __syncthreads();
+    f32x4 acc[RT][2][C] = {};
+    split_blocks<F, P, C, RT, 2>(
+        nb, W, s_tab,
+        [&](int m, int rt) {
+          const int64_t row = e * A.inter + min(tile0 + W.rg * RT + rt, tiles - 1) * 16 + n;
+          return (m ? A.up : A.gate) + row * rowbytes;
+        },
+        [&](int64_t b, Operand<P, C> &x) __attribute__((always_inline)) {
+          const _Float16 *xp[C];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) s_red[(wave * 2 + r) * 64 + lane] = acc[r];
-    __syncthreads();
-    if (wave == 0) {
-      f32x4 g = s_red[lane], u = s_red[64 + lane];
-      for (int w = 1; w < nw; ++w) {
-        g += s_red[w * 128 + lane];
-        u += s_red[w * 128 + 64 + lane];
-      }
+          for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * stride;
+          load_operand<P, C>(x, xp);
+        },
+        [](f32x4 &a, const f32x4 &part, float d, int) { scale_add(a, part, d); }, acc);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c0 + q * 4 + k < count) {
-          const int p = S.list[c0 + q * 4 + k], ex = A.X.ex[p / A.top_k];
-          A.h[p * A.inter + rt * 16 + n] = gated(ldexpf(g[k], ex), ldexpf(u[k], ex), S.w[p]);
+    for (int rt = 0; rt < RT; ++rt) {  // the sums over a row group's waves, then h
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 2 * C; ++j) s_red[((W.rg * W.kw + W.kg) * 2 * C + j) * 64 + lane] = acc[rt][j / C][j % C];
+      __syncthreads();
+      for (int i = threadIdx.x; i < W.rw * C * 64; i += blockDim.x) {
+        const int rg = i / (C * 64), c = i / 64 % C, l = i & 63, tile = tile0 + rg * RT + rt;
+        if (tile >= tiles) continue;
+        const f32x4 *p = s_red + (rg * W.kw * 2 * C + c) * 64 + l;
+        f32x4 g = p[0], u = p[C * 64];
+        for (int k = 1; k < W.kw; ++k) {
+          g += p[k * 2 * C * 64];
+          u += p[(k * 2 + 1) * C * 64];
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = c * 16 + (l >> 4) * 4 + k;
+          if (at >= count) continue;
+          const int64_t pair = list[at];
+          const float w = S.w[pair];
+          const int ex = A.X.ex[pair / A.top_k];
+          A.h[pair * A.inter + tile * 16 + (l & 15)] = gated(ldexpf(g[k], ex), ldexpf(u[k], ex), w);
+        }
+      }
     }
+    __syncthreads();  // the sums' memory is free again
   }
 }
 
@@ -809,11 +830,9 @@ void launch_down_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
 template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
   const int64_t experts = reached(A.npair, A.E);
   if (split_up(A)) {
-    const int64_t nb = A.hidden / 256;
-    int nw = 1;
-    while (nw < 8 && nw < nb) nw *= 2;
-    hipLaunchKernelGGL((up_split_kernel<F, P>), dim3(static_cast<unsigned>(experts * (A.inter / 16))), dim3(64 * nw),
-                       0, stream, A);
+    const int64_t nb = A.hidden / 256, rows = split_rw(nb) * 16, per = (A.inter + rows - 1) / rows;
+    hipLaunchKernelGGL((up_split_kernel<F, P>), dim3(static_cast<unsigned>(experts * per)),
+                       dim3(static_cast<unsigned>(64 * split_kw(nb) * split_rw(nb))), 0, stream, A);
     return;
   }
   if (is_few(A.T, A.E))
