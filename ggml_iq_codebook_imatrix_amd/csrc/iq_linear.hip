@@ -30,6 +30,7 @@ struct PrepArgs {
   Codebooks books;
   Lora L;
   int rtiles;  // tiles of 16 ranks
+  int slots;   // workgroups of a token tile and rank tile, for its up to 16 adapters
   int32_t *status;
 };
 
@@ -125,23 +126,25 @@ template <int P>
 __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
   __shared__ f32x4 s_red[8 * 64];
   int64_t w = blockIdx.x;
+  // The shrink first, it takes longest.  Slots last: where one adapter serves a
+  // whole tile, only slot 0 has work, and consecutive workgroups go to different
+  // XCDs (16 apart all went to one: 8x slower).
+  const int64_t tiles = A.X.ntile * A.rtiles;
+  if (w < tiles * A.slots) {
+    const int first = static_cast<int>(w / tiles);
+    w -= first * tiles;
+    for (int slot = first; slot < 16; slot += A.slots)
+      lora_shrink(A, w / A.rtiles, static_cast<int>(w % A.rtiles), slot, s_red);
+    return;
+  }
+  w -= tiles * A.slots;
   if (w < A.nconv) {
     const int64_t t = w * 8 + (threadIdx.x >> 6);
-    if (t < A.T) convert_token<P>(A.x, A.dtype, A.cols, A.X, t, threadIdx.x & 63);
+    if (t < A.T) convert_token<P>(A.x, A.cols, A.X, t, threadIdx.x & 63);
     return;
   }
   w -= A.nconv;
-  if (w < A.books.wg[0]) {
-    convert_codebook(A.books, static_cast<int>(w));
-    return;
-  }
-  w -= A.books.wg[0];
-  // slots last: where one adapter serves a whole tile, only slot 0 has work, and
-  // consecutive workgroups go to different XCDs (16 apart all went to one: 8x slower)
-  const int64_t tiles = A.X.ntile * A.rtiles;
-  const int slot = static_cast<int>(w / tiles);
-  w -= slot * tiles;
-  lora_shrink(A, w / A.rtiles, static_cast<int>(w % A.rtiles), slot, s_red);
+  convert_codebook(A.books, static_cast<int>(w));
 }
 
 // acc[r][c] += B v of the adapters that the tiles' tokens name.  Of tile c, wave
@@ -721,8 +724,10 @@ int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const 
   A.books = one_codebook(fmt, grid, tab, status);
   A.L = L;
   A.rtiles = (rank + 15) / 16;
+  A.slots = 16;  // as many as are at work at once; more only wait (4,096 sorted tokens: 42 us, so 35)
+  while (A.slots > 1 && P.x.ntile * A.rtiles * A.slots > 512) A.slots /= 2;
   A.status = status;
-  const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + P.x.ntile * 16 * A.rtiles));
+  const dim3 wgs(static_cast<unsigned>(A.nconv + A.books.wg[0] + P.x.ntile * A.rtiles * A.slots));
   if (dtype == IQ_DTYPE_F32)
     hipLaunchKernelGGL(linear_prep_kernel<2>, wgs, dim3(512), 0, stream, A);
   else

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
   int64_t w = blockIdx.x;
   if (w < A.nconv) {
     const int64_t t = w * 8 + (threadIdx.x >> 6);
-    if (t < A.T) convert_token<P>(A.x, A.dtype, A.hidden, A.X, t, threadIdx.x & 63);
+    if (t < A.T) convert_token<P>(A.x, A.hidden, A.X, t, threadIdx.x & 63);
     return;
   }
   w -= A.nconv;
@@ -113,21 +113,6 @@ __global__ void __launch_bounds__(512) route_kernel(MoeArgs A) {
     return;
   }
   route_logits<P>(A, w - A.books.wg[0] - A.books.wg[1], s_red);
-}
-
-template <int CTRL> __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xf,
-                                                                  0xf, false)));
-}
-// maximum over the wave, the same in every lane: prefixes within rows of 16, then across the rows
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = dpp_max<0x111>(v);
-  v = dpp_max<0x112>(v);
-  v = dpp_max<0x114>(v);
-  v = dpp_max<0x118>(v);
-  v = dpp_max<0x142>(v);
-  v = dpp_max<0x143>(v);
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
 
 // fp64 as a whole number of the same order, from 1 (NaN) up; 0: taken

@@ -335,6 +335,21 @@ __device__ __forceinline__ void scale_add(f32x4 &acc, const f32x4 &part, float d
   for (int k = 0; k < 4; ++k) acc[k] = fmaf(d, part[k], acc[k]);
 }
 
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xf,
+                                                                  0xf, false)));
+}
+// maximum over the wave, the same in every lane: prefixes within rows of 16, then across the rows
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max<0x111>(v);
+  v = dpp_max<0x112>(v);
+  v = dpp_max<0x114>(v);
+  v = dpp_max<0x118>(v);
+  v = dpp_max<0x142>(v);
+  v = dpp_max<0x143>(v);
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
 // ---------------------------------------------------------------------------
 // Tokens to fp16
 // ---------------------------------------------------------------------------
@@ -350,46 +365,54 @@ __device__ __forceinline__ void to_parts(float v, int n, _Float16 &hi, _Float16 
   lo = finite_f(f) ? static_cast<_Float16>(f - static_cast<float>(hi)) : static_cast<_Float16>(0.0f);
 }
 
-// One wave converts one token: its largest exponent, then its values (read
-// again, from cache).  The tile's other tokens are neighbouring waves', so that
-// the 16-byte pieces of a line are written at about the same time.
+// One wave converts one token: its largest exponent, then its values, which it
+// holds in registers (or reads again: past 6,144 bf16 or 2,048 fp32 columns).  The
+// tile's other tokens are neighbouring waves', so that the 16-byte pieces of a
+// line are written at about the same time.
 template <int P>
-__device__ __forceinline__ void convert_token(const void *x, int dtype, int64_t cols, const Tokens &X, int64_t t,
-                                              int lane) {
-  constexpr int U = 4;  // loads in flight, 512 columns each
+__device__ __forceinline__ void convert_token(const void *x, int64_t cols, const Tokens &X, int64_t t, int lane) {
+  constexpr int U = P == 1 ? 12 : 4;  // loads in flight, 512 columns each
+  u32x4 raw[U][P];
+  const char *row = static_cast<const char *>(x) + t * cols * (2 * P);
+  const auto load = [&](int64_t k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + u * 512 >= cols) break;
+      const int64_t col = k + u * 512 + lane * 8;
+      const char *from = row + (col < cols ? col : 0) * (2 * P);  // past the row: its first values again
+#pragma unroll
+      for (int i = 0; i < P; ++i) raw[u][i] = ldu<u32x4>(from + 16 * i);
+    }
+  };
+  const auto value = [&](int u, int j) __attribute__((always_inline)) {
+    if (P == 2) return __uint_as_float(raw[u][j >> 2][j & 3]);
+    const uint32_t w = raw[u][0][j >> 1];
+    return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+  };
   uint32_t e = 1;
   for (int64_t k = 0; k < cols; k += 512 * U) {
-    float v[U][8];
+    load(k);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t col = k + u * 512 + lane * 8;
-      load8u(x, dtype, t * cols + (col < cols ? col : 0), v[u]);  // past the row: its first values again
+      if (k + u * 512 >= cols) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e = max_exponent(e, value(u, j));
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) e = max_exponent(e, v[u][j]);
   }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) e = max(e, static_cast<uint32_t>(__shfl_xor(static_cast<int>(e), o, 64)));
-  const int n = 141 - static_cast<int>(e);
+  const int n = 141 - static_cast<int>(wave_max_u32(e));
   for (int64_t k = 0; k < cols; k += 512 * U) {
-    float v[U][8];
+    if (cols > 512 * U) load(k);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t col = k + u * 512 + lane * 8;
-      load8u(x, dtype, t * cols + (col < cols ? col : 0), v[u]);  // past the row: its first values again
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t col = k + u * 512 + lane * 8;
+      if (k + u * 512 >= cols) break;
       if (col >= cols) continue;
       const int g = static_cast<int>(col & 255) >> 3;  // group of the block: quarter g / 8, step g % 8
       half8v hi, lo;
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
         _Float16 a, b;
-        to_parts(v[u][kept_at(h)], n, a, b);
+        to_parts(value(u, kept_at(h)), n, a, b);
         hi[h] = a;
         lo[h] = b;
       }
