@@ -149,33 +149,30 @@ __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
 
 // acc[r][c] += B v of the adapters that the tiles' tokens name.  Of tile c, wave
 // w of nw takes the adapters whose turn t (in order of first use) has
-// (t + c) % nw == w; a round takes one adapter of each of the C tiles, 32 ranks
-// (bf16) or 16 at a time, and what the next one needs is fetched before this one
-// multiplies.  fp32 v is the sum of three bf16 values beside a bf16 B (no
-// rounding), and goes through the fp32 cores beside an fp32 B.  Rows of v of
-// other tokens hold anything; what they give is dropped.
+// (t + c) % nw == w; a round takes one adapter of each of the C tiles, and the
+// next one's rows of B are fetched before this one multiplies.  32 ranks (bf16) or
+// 16 at a time, whose v, of all the tile's tokens, serves every adapter: what rows
+// of other tokens give is dropped.  fp32 v is the sum of three bf16 values beside a
+// bf16 B (no rounding), and goes through the fp32 cores beside an fp32 B.
 template <int P, int C, int R> struct LoraStep {
-  bf16x8 v[C][3], w[C][R];   // bf16
-  f32x4 vf[C], wf[C][R];     // float32
-  uint32_t group[C];         // tokens of the tile
+  bf16x8 w[C][R];     // bf16
+  f32x4 wf[C][R];     // float32
+  uint32_t group[C];  // tokens of the tile
 };
 
 template <int P, int C, int R>
-__device__ __forceinline__ void lora_fetch(const Lora &L, int64_t tt0, int64_t rows, int64_t row0, int ch,
-                                           const int (&a)[C], LoraStep<P, C, R> &s) {
+__device__ __forceinline__ void lora_fetch(const Lora &L, int64_t rows, int64_t row0, int ch, const int (&a)[C],
+                                           LoraStep<P, C, R> &s) {
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (!s.group[c]) continue;
-    if (P == 1) {
-      const int j = ch * 32 + q * 8;
-      const uint16_t *vp = static_cast<const uint16_t *>(L.v) + ((tt0 + c) * L.chunks + ch) * 1536 + lane * 8;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) s.v[c][k] = *reinterpret_cast<const bf16x8 *>(vp + k * 512);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int64_t row = min(row0 + r * 16 + n, rows - 1);
-        const uint16_t *b = static_cast<const uint16_t *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = min(row0 + r * 16 + n, rows - 1), at = (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+      if (P == 1) {
+        const int j = ch * 32 + q * 8;
+        const uint16_t *b = static_cast<const uint16_t *>(L.b) + at;
         if ((L.rank & 7) == 0) {  // whole eights; past the rank v is zero, and the last eight will do
           s.w[c][r] = ldu<bf16x8>(b + min(j, L.rank - 8));
         } else {
@@ -184,15 +181,9 @@ __device__ __forceinline__ void lora_fetch(const Lora &L, int64_t tt0, int64_t r
           for (int i = 0; i < 8; ++i)
             if (j + i < L.rank) s.w[c][r][i] = __builtin_bit_cast(__bf16, b[j + i]);
         }
-      }
-    } else {
-      const int j = ch * 16 + q * 4;
-      s.vf[c] = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(L.v) + ((tt0 + c) * L.chunks + ch) * 256 +
-                                                 lane * 4);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int64_t row = min(row0 + r * 16 + n, rows - 1);
-        const float *b = static_cast<const float *>(L.b) + (static_cast<int64_t>(a[c]) * rows + row) * L.rank;
+      } else {
+        const int j = ch * 16 + q * 4;
+        const float *b = static_cast<const float *>(L.b) + at;
         s.wf[c][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -209,11 +200,7 @@ __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t 
   int mine[C], turn[C], a[C];
   uint32_t todo[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    mine[c] = tile_adapter(L, tt0 + c, T, lane);
-    todo[c] = static_cast<uint32_t>(__ballot(mine[c] >= 0)) & 0xffffu;
-    turn[c] = c;
-  }
+  for (int c = 0; c < C; ++c) mine[c] = tile_adapter(L, tt0 + c, T, lane);
   // the wave's next adapter of each tile; 0: none is left
   const auto next_round = [&](uint32_t (&group)[C]) __attribute__((always_inline)) {
     uint32_t any = 0;
@@ -230,42 +217,50 @@ __device__ __forceinline__ void lora_expand(const Lora &L, int64_t tt0, int64_t 
     }
     return any;
   };
-  LoraStep<P, C, R> now, then;
-  if (!next_round(now.group)) return;
-  int ch = 0;
-  lora_fetch<P, C, R>(L, tt0, rows, row0, 0, a, now);
-  for (;;) {
-    uint32_t more = 1;
-    if (++ch < L.chunks) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) then.group[c] = now.group[c];
-    } else {
-      ch = 0;
-      more = next_round(then.group);
-    }
-    if (more) lora_fetch<P, C, R>(L, tt0, rows, row0, ch, a, then);
-    __builtin_amdgcn_sched_barrier(0);
+  for (int ch = 0; ch < L.chunks; ++ch) {
+    LoraStep<P, C, R> now, then;
+    bf16x8 v[C][3];
+    f32x4 vf[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (!now.group[c]) continue;
+      todo[c] = static_cast<uint32_t>(__ballot(mine[c] >= 0)) & 0xffffu;
+      turn[c] = c;
+      if (!todo[c]) continue;
+      const char *from = static_cast<const char *>(L.v) + ((tt0 + c) * L.chunks + ch) * kChunkBytes[P - 1] + lane * 16;
+      if (P == 1) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (P == 1) {
-#pragma unroll
-          for (int k = 0; k < 3; ++k) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.v[c][k], now.w[c][r], d, 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            d = __builtin_amdgcn_mfma_f32_16x16x4f32(now.vf[c][i], now.wf[c][r][i], d, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((now.group[c] >> (q * 4 + k)) & 1u) acc[r][c][k] += d[k];
+        for (int k = 0; k < 3; ++k) v[c][k] = *reinterpret_cast<const bf16x8 *>(from + k * 1024);
+      } else {
+        vf[c] = *reinterpret_cast<const f32x4 *>(from);
       }
     }
+    uint32_t more = next_round(now.group);
     if (!more) return;
-    now = then;
+    lora_fetch<P, C, R>(L, rows, row0, ch, a, now);
+    while (more) {
+      more = next_round(then.group);
+      if (more) lora_fetch<P, C, R>(L, rows, row0, ch, a, then);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (!now.group[c]) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (P == 1) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c][k], now.w[c][r], d, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[c][i], now.wf[c][r][i], d, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((now.group[c] >> (q * 4 + k)) & 1u) acc[r][c][k] += d[k];
+        }
+      }
+      now = then;
+    }
   }
 }
 
@@ -330,16 +325,16 @@ __global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
   });
 }
 
-// More tokens: the eight waves are KG groups that take every KG-th block and
-// 8 / KG groups that take 16 R rows each; the C token tiles of a chunk of KG
+// More tokens: the waves are KG groups that take every KG-th block and RG groups
+// that take 16 R rows each; the C token tiles of a chunk of KG
 // blocks lie in LDS for all of them (64 KiB), the next chunk's on their way in
 // registers.
-template <int F, int P, int C, int R, int KG>
-__global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
-  constexpr int RG = 8 / KG, XU = KG * C * P, G = 4, kTab = Geo<F>::N;
+template <int F, int P, int C, int R, int KG, int RG>
+__global__ void __launch_bounds__(64 * KG * RG, KG * RG / 4) linear_tile_kernel(LinearArgs A) {
+  constexpr int NT = 64 * KG * RG, kX = KG * C * P * 512, XU = (kX + NT - 1) / NT, G = 4, kTab = Geo<F>::N;
   __shared__ uint4 s_tab[kTab];
-  __shared__ u32x4 s_x[XU * 512];
-  static_assert(KG == 1 || XU * 512 >= 8 * G * 64, "the sums over the waves fit");
+  __shared__ u32x4 s_x[kX];
+  static_assert(KG == 1 || kX >= KG * RG * G * 64, "the sums over the waves fit");
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / RG;
@@ -349,18 +344,24 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
 #pragma unroll
   for (int r = 0; r < R; ++r) rp[r] = A.packed + min(row0 + r * 16 + n, A.rows - 1) * rowbytes;
   u32x4 xr[XU];
-  // chunk ch of the token operand: 512 threads, XU units of 16 bytes each
+  // chunk ch of the token operand: XU units of 16 bytes a thread, [block][tile][part] of 512
   const auto load_x = [&](int64_t ch) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < XU; ++i) {
-      const int64_t b = min(ch * KG + i / (C * P), A.nb - 1);
-      const int64_t tile = min(tt0 + i / P % C, A.X.ntile - 1);
-      xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[((b * A.X.ntile + tile) * P + i % P) * 512 + threadIdx.x];
+      const int u = i * NT + static_cast<int>(threadIdx.x), piece = u >> 9;
+      if (kX % NT && u >= kX) break;
+      const int64_t b = min(ch * KG + piece / (C * P), A.nb - 1);
+      const int64_t tile = min(tt0 + piece / P % C, A.X.ntile - 1);
+      xr[i] = reinterpret_cast<const u32x4 *>(A.X.x16)[((b * A.X.ntile + tile) * P + piece % P) * 512 + (u & 511)];
     }
   };
   const auto store_x = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < XU; ++i) s_x[i * 512 + threadIdx.x] = xr[i];
+    for (int i = 0; i < XU; ++i) {
+      const int u = i * NT + static_cast<int>(threadIdx.x);
+      if (kX % NT && u >= kX) break;
+      s_x[u] = xr[i];
+    }
   };
   f32x4 acc[R][C];
 #pragma unroll
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(512, 2) linear_tile_kernel(LinearArgs A) {
 #pragma unroll
       for (int j = 0; j < G; ++j) red[(wave * G + j) * 64 + lane] = acc[(g + j) / C][(g + j) % C];
       __syncthreads();
-      for (int i = threadIdx.x; i < RG * G * 64; i += 512) {
+      for (int i = threadIdx.x; i < RG * G * 64; i += NT) {
         const int rg = i / (G * 64), rest = i % (G * 64);
         f32x4 s = red[rg * G * 64 + rest];
 #pragma unroll
@@ -626,13 +627,13 @@ void launch_split(const LinearArgs &A, hipStream_t stream) {
                      dim3(static_cast<unsigned>(64 * split_kw(A.nb) * rw)), 0, stream, A);
 }
 
-template <int F, int P, int C, int R, int KG>
+template <int F, int P, int C, int R, int KG, int RG>
 void launch_tile(const LinearArgs &A, hipStream_t stream) {
-  const int64_t rows = 8 / KG * 16 * R;
-  hipLaunchKernelGGL((linear_tile_kernel<F, P, C, R, KG>),
+  constexpr int rows = RG * 16 * R;
+  hipLaunchKernelGGL((linear_tile_kernel<F, P, C, R, KG, RG>),
                      dim3(static_cast<unsigned>((A.rows + rows - 1) / rows),
                           static_cast<unsigned>((A.X.ntile + C - 1) / C)),
-                     dim3(512), 0, stream, A);
+                     dim3(64 * KG * RG), 0, stream, A);
 }
 
 template <int F, int C, int R> void launch_prompt(const LinearArgs &A, hipStream_t stream) {
@@ -669,16 +670,18 @@ template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stre
   // token tiles would leave half of a tile empty.
   if (pairs <= 512) return launch_split<F, P, 2, 1>(A, stream);
   if (ntile == 2 || pairs <= 2048 * P) return launch_split<F, P, 2, 2>(A, stream);
-  const TileCost costs[2][5] = {{{64, 4, 37, 21}, {128, 4, 47, 31}, {128, 8, 56, 46}, {256, 8, 80, 74}, {256, 10, 92, 90}},
-                                {{128, 4, 70, 47}, {256, 4, 90, 76}}};
+  const TileCost costs[2][6] = {
+      {{64, 4, 37, 21}, {128, 4, 47, 31}, {96, 4, 40, 28}, {128, 8, 56, 46}, {256, 8, 80, 74}, {256, 10, 92, 90}},
+      {{128, 4, 70, 47}, {256, 4, 90, 76}}};
   int best = 0;
-  for (int i = 1; i < (P == 1 ? 5 : 2); ++i)
+  for (int i = 1; i < (P == 1 ? 6 : 2); ++i)
     if (tile_cost(costs[P - 1][i], A.rows, ntile) < tile_cost(costs[P - 1][best], A.rows, ntile)) best = i;
-  if (best == 0) return launch_tile<F, P, 4, 1, 2 / P>(A, stream);
-  if (best == 1) return launch_tile<F, P, 4, 2, 2 / P>(A, stream);
+  if (best == 0) return launch_tile<F, P, 4, 1, 2 / P, 4 * P>(A, stream);
+  if (best == 1) return launch_tile<F, P, 4, 2, 2 / P, 4 * P>(A, stream);
   if constexpr (P == 1) {
-    if (best == 2) return launch_prompt<F, 8, 1>(A, stream);
-    if (best == 3) return launch_prompt<F, 8, 2>(A, stream);
+    if (best == 2) return launch_tile<F, P, 4, 1, 2, 6>(A, stream);
+    if (best == 3) return launch_prompt<F, 8, 1>(A, stream);
+    if (best == 4) return launch_prompt<F, 8, 2>(A, stream);
     launch_prompt<F, 10, 2>(A, stream);
   }
 }
