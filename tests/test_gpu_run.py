@@ -288,6 +288,84 @@ def test_linear_views_guards_and_empty(api, T):
         api.linear(fmt, pay, grid.cpu(), x)
 
 
+# Row tiles times token tiles decide the kernel: rows, blocks, tokens, adapters, rank for each of those of many.
+MANY = {torch.bfloat16: [(1100, 3, 500, 3, 5), (1500, 2, 1000, 5, 24), (2000, 5, 1000, 0, 0), (2000, 3, 1100, 30, 17),
+                         (4000, 1, 1100, 2, 3), (8000, 2, 1100, 4, 16), (30000, 1, 33, 20, 8), (13000, 2, 9, 4, 6)],
+        torch.float32: [(300, 2, 1000, 3, 5), (1100, 3, 1000, 3, 5), (4000, 1, 600, 20, 17), (13000, 2, 9, 4, 6)]}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_many_exact(api, orc, fmt, dtype):
+    for i, (rows, nb, T, N, r) in enumerate(MANY[dtype]):
+        print("[case] linear many", fmt, dtype, rows, nb, T, N, r, flush=True)
+        grid, p, x, a, b, scale, ids, y, size = exact_linear(orc, fmt, rows, nb, T, N, r, 120 + i)
+        lora = dict(lora_a=dev(a, dtype), lora_b=dev(b, dtype), lora_scale=dev(scale), lora_ids=dev(ids)) if N else {}
+        st = api.new_status()
+        got = f64(api.linear(fmt, dev(p), dev(grid), dev(x, dtype), status=st, **lora))
+        # exact below 2^13, as above; adapters' sums beyond: 14 additions of exact terms
+        sure = size < 2.0 ** 13
+        assert sure.mean() > 0.5
+        assert np.array_equal(got[sure], round_to(y, dtype)[sure]), (rows, nb, T, N, r)
+        near = np.abs(got - y) <= 14 * U * size + np.abs(y) * (2.0 ** -8 if dtype == torch.bfloat16 else U)
+        assert near.all(), (rows, nb, T, N, r)
+        assert api.read_status(st) == 0
+
+
+@pytest.mark.parametrize("rows, T", [(60, 100), (1100, 500), (1500, 1000), (2000, 1000), (2000, 1100), (4000, 1100),
+                                     (8000, 1100)])
+def test_linear_block_scales(api, orc, rows, T):
+    """Scales of either sign from the smallest subnormal up to 2^6, blocks and whole rows of zero scale, and a token
+    with an infinity in a block that some rows scale by zero (0 * inf: NaN there)."""
+    print("[case] linear block scales", rows, T, flush=True)
+    for fmt in ("IQ2_S", "IQ1_M"):
+        nb = 4
+        g = inputs.rng(rows)
+        d = np.ldexp(1 + g.random((rows, nb)), g.integers(-24, 6, (rows, nb))).astype(np.float16)
+        d = np.where(g.random((rows, nb)) < 0.5, -d, d)
+        d[g.random((rows, nb)) < 0.3] = 0
+        d[rows // 2:rows // 2 + 3] = 0
+        d[0], d[-1, :2] = (0, 0, 0, 1), 0
+        grid, p = inputs.grid_for(fmt, 5), payload(fmt, rows, nb, 6, d16=d.astype(np.float16).view(np.uint16))
+        x = dev(inputs.activations(T, nb * 256, 7, 8)).bfloat16()
+        got = api.linear(fmt, dev(p), dev(grid), x)
+        xd, w = f64(x), decoded(orc, fmt, p, grid)
+        y, S = xd @ w.T, np.abs(xd) @ np.abs(w).T
+        # accumulated over the whole of K: K additions and a rescaling per block; sums in units of another block's
+        # scale stay between 2^-60 and 2^80, far from where float32 loses bits or overflows
+        tol = ((nb * 258 + 16) * 2 * U) * S + np.abs(y) * 2.0 ** -8 * 1.01
+        assert np.all(np.abs(f64(got) - y) <= tol), fmt
+        assert bool((got[:, rows // 2:rows // 2 + 3] == 0).all())
+        bad = x.clone()
+        bad[T // 2, 256 + 5] = float("inf")
+        out = api.linear(fmt, dev(p), dev(grid), bad)
+        keep = [t for t in range(T) if t != T // 2]
+        assert torch.equal(out[keep], got[keep])
+        row, zero = out[T // 2].float(), torch.from_numpy(d[:, 1] == 0).cuda()
+        assert bool(row[zero].isnan().all())
+        at = torch.from_numpy(w[:, 256 + 5]).cuda()
+        assert torch.equal(row[~zero], (torch.sign(at) * float("inf")).float()[~zero])
+
+
+@pytest.mark.parametrize("rows, T", [(1100, 500), (1500, 1000), (2000, 1000), (2000, 1100), (4000, 1100), (8000, 1100)])
+def test_linear_many_random(api, orc, rows, T):
+    print("[case] linear many random", rows, T, flush=True)
+    for fmt, dtype, nb in (("IQ2_XXS", torch.bfloat16, 5), ("IQ1_S", torch.bfloat16, 3), ("IQ2_XS", torch.float32, 3)):
+        grid, p = inputs.grid_for(fmt, 41), payload(fmt, rows, nb, rows + 1)
+        x = dev(inputs.activations(T, nb * 256, 42, 43, bf16=False), dtype)
+        base = api.linear(fmt, dev(p), dev(grid), x)
+        got, xd, w = f64(base), f64(x), decoded(orc, fmt, p, grid)
+        y, S = xd @ w.T, np.abs(xd) @ np.abs(w).T
+        # bf16 sums run through the whole of K, with a rescaling per block
+        assert np.all(np.abs(got - y) <= linear_tolerance(xd, w, dtype, y) + nb * 258 * 2 * U * S)
+        rel = np.linalg.norm(got - y) / np.linalg.norm(y)
+        assert rel < (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20)
+        # every token has a scale of its own
+        n = torch.arange(T, device="cuda") % 150 - 90
+        f = dev(np.ldexp(np.float32(1), n.cpu().numpy()))[:, None]
+        assert torch.equal(api.linear(fmt, dev(p), dev(grid), (x.float() * f).to(dtype)).float(), base.float() * f)
+
+
 # --------------------------------------------------------------------------
 # iq_moe
 # --------------------------------------------------------------------------
@@ -361,6 +439,49 @@ def test_moe_random(api, orc, fmt, dtype):
         y2, i2, w2 = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, ids=ids, weights=weights,
                              down_fmt=dfmt, down_grid=dev(dgrid))
         assert torch.equal(y, y2) and i2 is ids and w2 is weights
+
+
+# K of the router over four workgroups, each number of experts a lane holds, more than 256 of them, top_k of 64,
+# whole rows of few tokens, few tokens with the choice in a launch of its own
+MORE_MOE = [("IQ2_XS", 6, 2, 1024, 256, 6), ("IQ1_S", 5, 2, 1280, 256, 20), ("IQ2_S", 200, 9, 256, 256, 7),
+            ("IQ1_M", 200, 9, 256, 256, 13), ("IQ2_XXS", 300, 64, 256, 256, 3), ("IQ2_XS", 64, 64, 256, 256, 16),
+            ("IQ1_S", 64, 8, 512, 256, 8), ("IQ2_S", 30, 4, 256, 1024, 16), ("IQ2_XXS", 4, 2, 1536, 768, 2),
+            ("IQ1_M", 257, 1, 256, 256, 1), ("IQ1_S", 1, 1, 256, 256, 300), ("IQ1_M", 1100, 3, 256, 256, 40)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt, E, k, H, I, T", MORE_MOE)
+def test_moe_more_shapes(api, orc, fmt, E, k, H, I, T, dtype):
+    print("[case] moe more", fmt, dtype, E, k, H, I, T, flush=True)
+    grid, _, gate, up, down, x, router = moe_inputs(fmt, fmt, E, H, I, T, dtype, 1000 + E)
+    st = api.new_status()
+    y, ids, weights = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, router=router, top_k=k, status=st)
+    assert api.read_status(st) == 0
+    logits = f64(x) @ f64(router).T
+    want = np.argsort(-logits, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(ids.cpu().numpy(), want)
+    p = np.take_along_axis(np.exp(logits - logits.max(1, keepdims=True)), want, 1)
+    assert np.allclose(f64(weights), p / p.sum(1, keepdims=True), rtol=2.0 ** -17, atol=0)
+    ref, tol = moe_reference(orc, fmt, fmt, E, H, I, grid, grid, gate, up, down, f64(x), want, f64(weights), dtype)
+    assert np.all(np.abs(f64(y) - ref) <= tol)
+    rel = np.linalg.norm(f64(y) - ref) / np.linalg.norm(ref)
+    assert rel < (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20)
+
+
+def test_moe_most_experts(api):
+    """4,096 experts, the most there can be: ids, and the output against the same experts gathered into a small layer."""
+    print("[case] moe 4096 experts", flush=True)
+    fmt, E, k, H, I, T = "IQ1_S", 4096, 3, 256, 256, 20
+    grid, _, gate, up, down, x, router = moe_inputs(fmt, fmt, E, H, I, T, torch.bfloat16, 1300)
+    gate, up, down, grid = dev(gate), dev(up), dev(down), dev(grid)
+    y, ids, weights = api.moe(fmt, gate, up, down, grid, x, E, router=router, top_k=k)
+    want = np.argsort(-(f64(x) @ f64(router).T), axis=1, kind="stable")[:, :k]
+    assert np.array_equal(ids.cpu().numpy(), want)
+    some = ids.unique()
+    pick = lambda p, rows: p.view(E, rows, -1)[some.long()].reshape(-1, 1, p.shape[-1]).contiguous()
+    small = torch.searchsorted(some, ids).int()
+    y2, _, _ = api.moe(fmt, pick(gate, I), pick(up, I), pick(down, H), grid, x, len(some), ids=small, weights=weights)
+    assert torch.equal(y, y2)
 
 
 @pytest.mark.parametrize("T", [4, 40, 130])
@@ -530,5 +651,48 @@ def test_large_offsets(api, orc):
         y = api.linear(fmt, p, dev(grid), dev(x[:T]))
         got, want = f64(y[:, -64:]), x[:T].astype(np.float64) @ w.T
         assert np.all(np.abs(got - want) <= linear_tolerance(x[:T].astype(np.float64), w, torch.float32, want))
+        assert bool((y[:, :-64] == 0).all())
+        del y
+
+
+@pytest.mark.parametrize("T", [2, 16, 48, 400])
+def test_two_calls_at_once(api, T):
+    """Calls in flight on two streams, each with memory of its own, are the calls one after the other."""
+    print("[case] two calls at once", T, flush=True)
+    fmt, E, k, H, I = "IQ2_S", 16, 4, 512, 512
+    grid, _, gate, up, down, x, router = moe_inputs(fmt, fmt, E, H, I, T, torch.bfloat16, 1400)
+    grid, gate, up, down = dev(grid), dev(gate), dev(up), dev(down)
+    xs = [x, (x.float() * 0.5).roll(1, 0).bfloat16()]
+
+    def both(x):
+        return (api.linear(fmt, gate, grid, x), *api.moe(fmt, gate, up, down, grid, x, E, router=router, top_k=k))
+    want = [both(v) for v in xs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in xs], [[], []]
+    for _ in range(8):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(both(xs[n]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for g in got[n]:
+            assert all(torch.equal(p, q) for p, q in zip(g, want[n]))
+
+
+def test_large_offsets_in_prompts(api, orc):
+    """bf16 tokens over a payload of more than 2^31 bytes: the rows behind that offset, in the kernels for prompts."""
+    print("[case] large offsets, prompts", flush=True)
+    fmt, rows, nb = "IQ1_S", 1 << 22, 11
+    grid = inputs.grid_for(fmt, 5)
+    tail = payload(fmt, 64, nb, 6)
+    p = torch.zeros((rows, nb, 50), dtype=torch.uint8, device="cuda")
+    p[-64:] = dev(tail)
+    x = dev(inputs.activations(300, nb * 256, 7, 8)).bfloat16()
+    w = decoded(orc, fmt, tail, grid)
+    for T in (1, 20, 40, 300):  # 300 x 2^22 bf16 outputs: 2.5 GB
+        y = api.linear(fmt, p, dev(grid), x[:T])
+        got, xd = f64(y[:, -64:]), f64(x[:T])
+        want, S = xd @ w.T, np.abs(xd) @ np.abs(w).T
+        assert np.all(np.abs(got - want) <= linear_tolerance(xd, w, torch.bfloat16, want) + nb * 258 * 2 * U * S)
         assert bool((y[:, :-64] == 0).all())
         del y
