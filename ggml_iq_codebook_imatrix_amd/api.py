@@ -489,19 +489,34 @@ def _is(t, name: str, shape, dtype):
         _need(t, name, shape, dtype)
 
 
-def _addr(t, name: str, device):
+def _ends(t, name: str, shape, dtype):
+    """As _need, for a shape whose last entry alone is fixed; the shape."""
+    if not isinstance(t, torch.Tensor) or t.dim() != len(shape) or t.shape[-1] != shape[-1] or t.dtype is not dtype:
+        _need(t, name, shape, dtype)
+    return t.shape
+
+
+def _home(t: torch.Tensor) -> int:
+    """The index of the current device, on which t must be."""
+    index = t.get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        _device_of(t)
+    return index
+
+
+def _addr(t, name: str, index: int):
     if t is None:
         return None
-    if t.device != device or not t.is_contiguous():
-        _ptr(t, name, device)
+    if t.get_device() != index or not t.is_contiguous():
+        _ptr(t, name, torch.device("cuda", index))
     return t.data_ptr()
 
 
-def _scratch(nbytes: int, device, workspace):
+def _scratch(nbytes: int, x: torch.Tensor, workspace):
     if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = x.new_empty(nbytes, dtype=torch.uint8)
         return workspace, workspace.data_ptr(), nbytes
-    return _workspace(nbytes, device, workspace)
+    return _workspace(nbytes, x.device, workspace)
 
 
 def linear_workspace_size(fmt, rows: int, cols: int, dtype, T: int, rank: int = 0) -> int:
@@ -528,16 +543,16 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
     lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones)."""
     f = _fmt(fmt)
     entries, nbytes = _geometry(f)
-    _need(packed, "packed", (None, None, nbytes), torch.uint8)
-    rows, nb, _ = packed.shape
+    rows, nb, _ = _ends(packed, "packed", (None, None, nbytes), torch.uint8)
     cols = nb * 256
     _is(grid, "grid", (entries, 8), torch.float32)
-    _need(x, "x", (None, cols), tuple(DTYPE))
-    T, dtype = x.shape[0], x.dtype
+    if not isinstance(x, torch.Tensor) or x.dtype not in DTYPE:
+        _need(x, "x", (None, cols), tuple(DTYPE))
+    dtype = x.dtype
+    T = _ends(x, "x", (None, cols), dtype)[0]
     N = rank = 0
     if lora_a is not None:
-        _need(lora_a, "lora_a", (None, None, cols), dtype)
-        N, rank, _ = lora_a.shape
+        N, rank, _ = _ends(lora_a, "lora_a", (None, None, cols), dtype)
         if N < 1 or rank < 1:
             raise IQError("lora_a holds no adapter")
         _is(lora_b, "lora_b", (N, rows, rank), dtype)
@@ -550,16 +565,16 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
         _is(out, "out", (T, rows), dtype)
     if status is not None:
         _status_ok(status)
-    dev = _device_of(x)
+    dev = _home(x)
     if out is None:
-        out = torch.empty((T, rows), dtype=dtype, device=dev)
+        out = x.new_empty((T, rows))
     dt = DTYPE[dtype]
-    ws, wp, wn = _scratch(_run_size("iq_linear_workspace_size", f, rows, cols, dt, T, rank), dev, workspace)
+    ws, wp, wn = _scratch(_run_size("iq_linear_workspace_size", f, rows, cols, dt, T, rank), x, workspace)
     rc = lib().iq_linear(f, _addr(packed, "packed", dev), rows, cols, _addr(grid, "grid", dev), _addr(x, "x", dev),
                          dt, T, _addr(lora_a, "lora_a", dev), _addr(lora_b, "lora_b", dev),
                          _addr(lora_scale, "lora_scale", dev), _addr(lora_ids, "lora_ids", dev), N, rank,
                          _addr(out, "out", dev), wp, wn, _addr(status, "status", dev),
-                         torch._C._cuda_getCurrentRawStream(dev.index))
+                         torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, "iq_linear")
     return out
@@ -580,11 +595,13 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     E = int(num_experts)
     if E < 1:
         raise IQError("num_experts must be at least 1")
-    _need(x, "x", (None, None), tuple(DTYPE))
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in DTYPE:
+        _need(x, "x", (None, None), tuple(DTYPE))
     (T, hidden), dtype = x.shape, x.dtype
     if hidden % 256 or hidden == 0:
         raise IQError(f"x has {hidden} columns, not a multiple of 256")
-    _need(gate, "gate", (None, hidden // 256, nbytes), torch.uint8)
+    if not isinstance(gate, torch.Tensor) or gate.shape[1:] != (hidden // 256, nbytes) or gate.dtype is not torch.uint8:
+        _need(gate, "gate", (None, hidden // 256, nbytes), torch.uint8)
     if gate.shape[0] % E or gate.shape[0] // E % 256 or gate.shape[0] == 0:
         raise IQError(f"gate has {gate.shape[0]} rows, not a multiple of 256 for each of {E} experts")
     inter = gate.shape[0] // E
@@ -598,7 +615,8 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     else:
         _is(down_grid, "down_grid", (dentries, 8), torch.float32)
     if router is not None:
-        _need(router, "router", (E, hidden), tuple(DTYPE))
+        if not isinstance(router, torch.Tensor) or router.shape != (E, hidden) or router.dtype not in DTYPE:
+            _need(router, "router", (E, hidden), tuple(DTYPE))
         if top_k is None or not 1 <= int(top_k) <= E:
             raise IQError("top_k must lie in 1 .. num_experts with a router")
     elif ids is None or weights is None:
@@ -612,21 +630,21 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
         _is(out, "out", (T, hidden), dtype)
     if status is not None:
         _status_ok(status)
-    dev = _device_of(x)
+    dev = _home(x)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ids = x.new_empty((T, k), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        weights = x.new_empty((T, k), dtype=torch.float32)
     if out is None:
-        out = torch.empty((T, hidden), dtype=dtype, device=dev)
+        out = x.new_empty((T, hidden))
     dt = DTYPE[dtype]
-    ws, wp, wn = _scratch(_run_size("iq_moe_workspace_size", f, fd, hidden, inter, E, dt, T, k), dev, workspace)
+    ws, wp, wn = _scratch(_run_size("iq_moe_workspace_size", f, fd, hidden, inter, E, dt, T, k), x, workspace)
     rc = lib().iq_moe(f, fd, _addr(gate, "gate", dev), _addr(up, "up", dev), _addr(down, "down", dev), hidden, inter,
                       E, _addr(grid, "grid", dev), _addr(down_grid, "down_grid", dev), _addr(x, "x", dev), dt, T,
                       _addr(router, "router", dev), 0 if router is None else DTYPE[router.dtype], k,
                       int(bool(renormalize)), _addr(ids, "ids", dev), _addr(weights, "weights", dev),
                       _addr(out, "out", dev), wp, wn, _addr(status, "status", dev),
-                      torch._C._cuda_getCurrentRawStream(dev.index))
+                      torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, "iq_moe")
     return out, ids, weights
