@@ -503,7 +503,7 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
 // one, waiting for HBM was a third of the time).
 template <int F, int P, int C, int NW, bool FEW>
 __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KC = C * P == 4 ? 1 : 2, kUnits = 512 / (64 * NW), XU = KC * C * P * kUnits;
+  constexpr int N = 16 * C, KC = C * P >= 4 ? 1 : 2, kUnits = 512 / (64 * NW), XU = KC * C * P * kUnits;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ u32x4 s_x[2][XU * 64 * NW];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
 // workgroups.  z: one row per pair.
 template <int F, int P, int C, int NW, bool FEW>
 __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KB = 4 / P;
+  constexpr int N = 16 * C, KB = C == 4 ? 2 : 4 / P;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ _Float16 s_h[KB][C][P * 4096];
   __shared__ int s_ex[KB][N];
@@ -812,8 +812,16 @@ void launch_down_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
   hipLaunchKernelGGL((down_rows_kernel<F, P, C, NW, FEW>),
                      dim3(static_cast<unsigned>(experts * (A.hidden / (32 * NW)))), dim3(64 * NW), 0, stream, A);
 }
+// Tiles of 16 pairs that a workgroup multiplies at once, by an expert's pairs on
+// average: as many as most experts fill, since every pass decodes the rows again.
+// Measured (128 experts of 2,048 x 768, IQ1_M): 12.5 pairs with one tile 170 us and
+// 160 with two; 16 with two 168 and 190 with four; 31 with two 290 and 281 with
+// four; 250 with two 2,033 and 1,774 with four.  float32 has no room for four.
+int pair_tiles(int64_t npair, int64_t E) { return npair <= 8 * E ? 1 : npair <= 28 * E ? 2 : 4; }
+
 template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
   const int64_t experts = reached(A.npair, A.E);
+  const int pairs = pair_tiles(A.npair, A.E);
   if (split_up(A)) {
     const int64_t nb = A.hidden / 256, rows = split_rw(nb) * 16, per = (A.inter + rows - 1) / rows;
     hipLaunchKernelGGL((up_split_kernel<F, P>), dim3(static_cast<unsigned>(experts * per)),
@@ -822,13 +830,16 @@ template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
   }
   if (is_few(A.T, A.E))
     launch_up_rows<F, P, 1, 4, true>(A, experts, stream);
-  else if (A.npair <= 8 * static_cast<int64_t>(A.E))  // 8 pairs an expert on average: few have more than 16
+  else if (pairs == 1)
     launch_up_rows<F, P, 1, 8, false>(A, A.E, stream);
-  else
+  else if (P == 2 || pairs == 2)
     launch_up_rows<F, P, 2, 8, false>(A, A.E, stream);
+  else if constexpr (P == 1)
+    launch_up_rows<F, P, 4, 8, false>(A, A.E, stream);
 }
 
 template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
+  const int pairs = pair_tiles(A.npair, A.E);
   if (split_down(A.T, A.E)) {
     hipLaunchKernelGGL((down_split_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
                        dim3(64 * down_split_waves(P)), 0, stream, A);
@@ -836,10 +847,12 @@ template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
   }
   if (is_few(A.T, A.E))
     launch_down_rows<F, P, 1, 8, true>(A, reached(A.npair, A.E), stream);
-  else if (A.npair <= 8 * static_cast<int64_t>(A.E))
+  else if (pairs == 1)
     launch_down_rows<F, P, 1, 8, false>(A, A.E, stream);
-  else
+  else if (P == 2 || pairs == 2)
     launch_down_rows<F, P, 2, 8, false>(A, A.E, stream);
+  else if constexpr (P == 1)
+    launch_down_rows<F, P, 4, 8, false>(A, A.E, stream);
 }
 
 }  // namespace
