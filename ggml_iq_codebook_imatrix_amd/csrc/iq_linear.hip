@@ -523,6 +523,9 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[r][c] *= ratio;
     }
+    half8v w[2][R];  // the step in hand and the next, decoded while this one multiplies
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[0][r] = group_half8<F>(raw[r], 0, s_tab, keep[r]);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int64_t h = 2 * b + half;
@@ -535,16 +538,19 @@ __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
       __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below, not after it
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const int g = half * 4 + i;
         half8v x[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) x[c] = __builtin_bit_cast(half8v, s_x[half][c * 256 + i * 64 + lane]);
+        if (g < 7) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const half8v w = group_half8<F>(raw[r], half * 4 + i, s_tab, keep[r]);
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[c], w, acc[r][c], 0, 0, 0);
+          for (int r = 0; r < R; ++r) w[(g + 1) & 1][r] = group_half8<F>(raw[r], g + 1, s_tab, keep[r]);
         }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[c], w[g & 1][r], acc[r][c], 0, 0, 0);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // the next half is there, this one free
