@@ -664,7 +664,10 @@ inline int64_t tile_cost(const TileCost &k, int64_t rows, int64_t ntile) {
 template <int F, int P> void launch_linear(const LinearArgs &A, hipStream_t stream) {
   const int64_t ntile = A.X.ntile, rtiles = (A.rows + 15) / 16, pairs = rtiles * ntile;
   if (ntile == 1) {
-    if (rtiles / split_rw(A.nb) <= 768)
+    // Four row tiles a wave share its tokens and its workgroup's beginning and end
+    // (2,048 columns, 1 token: 8,192 rows 9.1 us with one and 10.6 with four, 12,288
+    // 11.3 and 10.7, 40,960 24.3 and 17.7).
+    if (rtiles / split_rw(A.nb) <= 640)
       launch_split<F, P, 1, 1>(A, stream);
     else
       launch_split<F, P, 1, 4>(A, stream);

@@ -756,15 +756,29 @@ __global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+// The rules below, measured with 128 experts of 2,048 x 768, eight a token, bf16,
+// unless another layer is named.
+//
+// Few tokens name few experts: a workgroup per chosen expert, not per expert (1
+// token 26 us and 49, 8 tokens 59 and 71, 16 tokens 73 and 84).
 bool is_few(int64_t T, int E) { return T <= kFewTokens && E <= kFewExperts; }
-// A wave picks a token's experts in 2 us (of 128), a launch for it takes 4 to 5:
-// picked in the next kernel while its eight waves do it in one go.
+// A wave picks a token's experts in 2 us, a launch for it takes 4 to 5 and as much
+// of the host's time: picked in the next kernel while its eight waves do it in one
+// go (8 tokens 59 us and 58, 9 tokens 63 and 58, 16 tokens 94 and 74).
 bool is_pick(int64_t T, int E) { return T <= 8 && E <= kFewExperts; }
 // Experts that np pairs reach at most.
 int64_t reached(int64_t np, int E) { return np < E ? np : E; }
-// K is split where whole rows would leave SIMDs without a wave (1,024 of them).
-bool split_up(const MoeArgs &A) { return is_few(A.T, A.E) && reached(A.npair, A.E) * (A.inter / 16) < 1024; }
-bool split_down(int64_t T, int E) { return T <= 2 && E <= kFewExperts; }
+// Gate and up with K split over the waves, where whole rows would leave half of
+// the 1,024 SIMDs without a wave: 384 row tiles 26 us and 30 with whole rows, 512
+// (16 experts of 1,024 x 512, 16 tokens) 28 and 30, 768 38 and 36.
+bool split_up(const MoeArgs &A) { return is_few(A.T, A.E) && reached(A.npair, A.E) * (A.inter / 16) <= 512; }
+// Down with the (expert, block) pairs split over the waves, no launch for the sums:
+// a wave converts every pair's block, so while these are few: 16 of them (16
+// experts of 1,024 x 512, 4 tokens) 21 us and 24 with whole rows, 24 26 and 31, 48
+// 38 and 38, 72 47 and 43; float32 has half the waves.
+bool split_down(int64_t T, int E, int top_k, int64_t inter, int dtype) {
+  return is_few(T, E) && T * top_k * (inter / 256) <= (dtype == IQ_DTYPE_F32 ? 24 : 48);
+}
 
 struct MoePlan {
   TokensPlan x;
@@ -780,10 +794,10 @@ MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, in
   p.xo = p.dtab + ws_up(static_cast<size_t>(kCodebook[down_fmt]) * 16);
   p.eo = p.xo + ws_up(p.x.xbytes);
   p.lo = p.eo + ws_up(p.x.ebytes);
-  p.ks = hidden >= 4 * 256 ? 4 : 1;  // 8 workgroups would route 16 tokens to 128 experts: 4 us more
+  p.ks = hidden >= 4 * 256 ? 4 : 1;  // eight workgroups alone would route 16 tokens to 128 experts: 3 to 5 us more
   p.ho = p.lo + ws_up(static_cast<size_t>(p.ks) * T * E * 8);
   p.zo = p.ho + ws_up(np * inter * 4);
-  p.bytes = p.zo + ws_up(split_down(T, E) ? 0 : np * hidden * 4) + kWsAlign;
+  p.bytes = p.zo + ws_up(split_down(T, E, top_k, inter, dtype) ? 0 : np * hidden * 4) + kWsAlign;
   return p;
 }
 
@@ -840,7 +854,7 @@ template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
 
 template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
   const int pairs = pair_tiles(A.npair, A.E);
-  if (split_down(A.T, A.E)) {
+  if (split_down(A.T, A.E, A.top_k, A.inter, A.dtype)) {
     hipLaunchKernelGGL((down_split_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
                        dim3(64 * down_split_waves(P)), 0, stream, A);
     return;
@@ -940,7 +954,7 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   IQ_BY_FMT(down_fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-  if (!split_down(T, num_experts)) {
+  if (!split_down(T, num_experts, top_k, inter, dtype)) {
     hipLaunchKernelGGL(sum_kernel, dim3(static_cast<unsigned>((T * (hidden / 4) + 255) / 256)), dim3(256), 0,
                        stream, A);
     if (!run_launched()) return IQ_ERR_HIP;

@@ -446,7 +446,8 @@ def test_moe_random(api, orc, fmt, dtype):
 MORE_MOE = [("IQ2_XS", 6, 2, 1024, 256, 6), ("IQ1_S", 5, 2, 1280, 256, 20), ("IQ2_S", 200, 9, 256, 256, 7),
             ("IQ1_M", 200, 9, 256, 256, 13), ("IQ2_XXS", 300, 64, 256, 256, 3), ("IQ2_XS", 64, 64, 256, 256, 16),
             ("IQ1_S", 64, 8, 512, 256, 8), ("IQ2_S", 30, 4, 256, 1024, 16), ("IQ2_XXS", 4, 2, 1536, 768, 2),
-            ("IQ1_M", 257, 1, 256, 256, 1), ("IQ1_S", 1, 1, 256, 256, 300), ("IQ1_M", 1100, 3, 256, 256, 40)]
+            ("IQ2_S", 16, 3, 512, 256, 16), ("IQ1_M", 257, 1, 256, 256, 1), ("IQ1_S", 1, 1, 256, 256, 300),
+            ("IQ1_M", 1100, 3, 256, 256, 40)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
