@@ -122,6 +122,9 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
   });
 }
 
+// 4,096 tokens of 5,120: 21 us without adapters (84 MB in and out, 4.0 TB/s: the
+// conversion is bound by memory, and its 16-byte pieces), 36 with eight adapters of
+// rank 16; 64 tokens of 2,048 with one 3 to 5 us, its loads' latency.
 template <int P>
 __global__ void __launch_bounds__(512) linear_prep_kernel(PrepArgs A) {
   __shared__ f32x4 s_red[8 * 64];
@@ -273,7 +276,11 @@ struct LinearArgs {
   void *y;
 };
 
-// Few tokens: waves split K (split_blocks), RT row tiles each by C token tiles.
+// Few tokens, or few tiles: the waves split K (split_blocks), RT row tiles each by
+// C token tiles.  Latency bounds it: a wave has one or two blocks, whose payload
+// and tokens it waits for once, and then the sums' way through LDS.  5,632 x 2,048,
+// IQ2_XS: one token 6.5 us (3.3 MB of payload, 0.5 TB/s), 16 tokens with 16 adapters
+// 8.5 us.
 template <int F, int P, int C, int RT>
 __global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
   constexpr int G = RT * C < 4 ? RT * C : 4;
@@ -326,9 +333,12 @@ __global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
 }
 
 // More tokens: the waves are KG groups that take every KG-th block and RG groups
-// that take 16 R rows each; the C token tiles of a chunk of KG
-// blocks lie in LDS for all of them (64 KiB), the next chunk's on their way in
-// registers.
+// that take 16 R rows each; the C token tiles of a chunk of KG blocks lie in LDS for
+// all of them (64 KiB), the next chunk's on their way in registers.  64 tokens
+// through 17,408 x 5,120, IQ1_M, 48 adapters of rank 32: 46 us (0.25 PFLOP/s),
+// about 34 without the adapters.  Its decode alone would take a third of that; the
+// waves (three a SIMD) wait at each chunk for its tokens and for one another.  One row tile a wave
+// (R = 1) in six groups fills 182 CUs, two in four groups 136 CUs (58 us).
 template <int F, int P, int C, int R, int KG, int RG>
 __global__ void __launch_bounds__(64 * KG * RG, KG * RG / 4) linear_tile_kernel(LinearArgs A) {
   constexpr int NT = 64 * KG * RG, kX = KG * C * P * 512, XU = (kX + NT - 1) / NT, G = 4, kTab = Geo<F>::N;
@@ -460,14 +470,19 @@ __global__ void __launch_bounds__(64 * KG * RG, KG * RG / 4) linear_tile_kernel(
   }
 }
 
-// Prompts (bf16): eight waves of 64 rows each by C token tiles.  What bounds it is
-// balanced: a step of a wave is four codebook entries and C token operands from
-// LDS, 80 vector instructions and 4 C matrix instructions.  Registers decide the
-// tile, so there are no sums apart from the accumulators: these are kept in units
-// of the block's d, and rescaled by the ratio of two blocks' d in between (one
+// Prompts (bf16): eight waves of 16 R rows each by C token tiles.  Registers decide
+// the tile, so there are no sums apart from the accumulators: these are kept in
+// units of the block's d, and rescaled by the ratio of two blocks' d in between (one
 // more rounding of 2^-24 a block, bf16 outputs round by 2^-9).  A block of d = 0
 // counts with zero weights instead.  Token operands go from memory to LDS
 // directly, half a block ahead.
+// 4,096 tokens through 17,408 x 5,120, IQ1_S: 0.74 ms, 0.98 PFLOP/s; the matrix cores
+// are busy 44 % of it, LDS 36 %.  What bounds it is the issue of the decode's vector
+// instructions (25 a step and row tile, at 5 to 8 cycles with two waves a SIMD)
+// beside 2 C matrix instructions of 16 cycles.  R = 4, C = 6 spilled registers (0.77
+// at 4,096 columns, against 0.62 with R = 2, C = 10); a third buffer, so that no half
+// waits for its tokens, made it 9 % slower, and four waves a SIMD would be bound by
+// their LDS reads.
 template <int F, int C, int R>
 __global__ void __launch_bounds__(512, 2) linear_prompt_kernel(LinearArgs A) {
   constexpr int kHalf = C * 256;  // 16-byte units of half a block: C tiles of 4 KiB

@@ -8,6 +8,10 @@
 // 16 tokens a workgroup takes the expert of its rank among the chosen ones; for
 // more it is given an expert, whose pairs it gathers from the ids.
 //
+// One token through 128 experts of 2,048 x 768 (eight of them, 9.7 MB of payload)
+// takes 27 us: routing 5.5, gate and up 13 (2 of them the choice), down 8.  Each is
+// a chain of waits: the launch, the logits, the payload, the sums.
+//
 // Gate and up (h in fp32, one row per pair):
 //  up_split_kernel  16 rows of gate and up, the blocks of K split over the waves:
 //                   where the chosen experts' rows alone would not fill the chip.
@@ -55,8 +59,9 @@ struct MoeArgs {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 // The logits of 16 tokens and 16 experts on the fp64 matrix cores, K split over
-// ks workgroups (whose sums the choice adds) and each one's eight waves.  In fp64, so that no order of summation can swap neighbours in
-// the ranking.  v_mfma_f64_16x16x4: lane l holds k = l / 16 of token (A) and
+// ks workgroups (whose sums the choice adds) and each one's eight waves.  In fp64,
+// so that no order of summation can swap neighbours in the ranking (5.5 us for up to
+// 64 tokens by 128 experts of 2,048, 8 for 200: latency).  v_mfma_f64_16x16x4: lane l holds k = l / 16 of token (A) and
 // expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
 template <int P>
 __device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w, double *s_red) {
@@ -294,7 +299,8 @@ __device__ __forceinline__ int few_expert(const MoeArgs &A, FewPairs &S, int slo
 }
 
 // 16 rows of gate and up of one expert a row group, K split over its waves
-// (split_blocks); h of its pairs.  For few pairs.
+// (split_blocks); h of its pairs.  For few experts' rows: the small layer (8 experts
+// of 512 x 256, 5 tokens, float32) 9 us, with whole rows 11.
 template <int F, int P>
 __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
   constexpr int C = 1, RT = 1, N = 16;
@@ -363,7 +369,8 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
 }
 
 // Waves split (expert, block of inter): each stages its tokens' h of that block
-// as the A operand (rows: tokens; absent ones zero) in LDS of its own.
+// as the A operand (rows: tokens; absent ones zero) in LDS of its own.  One token
+// through eight experts of 2,048 x 768: 8 us, latency.
 constexpr int down_split_waves(int parts) { return parts == 2 ? 4 : 8; }  // 8 KiB of LDS a part and wave
 template <int F, int P>
 __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(MoeArgs A) {
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
 }
 
 // Walks the pairs of one expert in ascending order, N at a time: f(list, count).
-// Few tokens: they are in LDS already; otherwise the ids are searched, a workgroup's width at a time.
+// The ids are searched, a workgroup's width at a time.
 template <int N> struct PairWalk {
   int list[512 + N], cnt[8];  // up to eight waves
 };
@@ -500,14 +507,19 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
 // 16 NW rows of gate and up of one expert: NW waves, 16 rows each over the whole
 // of K.  The pairs' tokens come through LDS, KC blocks at a time for all waves;
 // a wave keeps the payload of the next two blocks on its way in registers (with
-// one, waiting for HBM was a third of the time).
+// one, waiting for HBM was a third of the time).  64 tokens through 128 experts of
+// 2,048 x 768, IQ2_XXS: 51 us for 50 MB of payload (1.0 TB/s).  The decode bounds it:
+// 19,400 vector instructions a SIMD at 4.9 cycles are 0.85 of its time, LDS is busy
+// 0.45 of it.  Sharing the blocks of K between the waves instead took 119 us: every
+// wave then reads all tokens from memory.
 template <int F, int P, int C, int NW, bool FEW>
-__global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
+__global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 / P : P * C == 1 ? 4 : 2) up_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C, KC = C * P >= 4 ? 1 : 2, kUnits = 512 / (64 * NW), XU = KC * C * P * kUnits;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ u32x4 s_x[2][XU * 64 * NW];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, q = lane >> 4;
   const int64_t nb = A.hidden >> 8, per = A.inter / (16 * NW), part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
   load_table<F>(s_tab, A.tab);
@@ -618,7 +630,7 @@ __global__ void __launch_bounds__(64 * NW, P * C == 1 ? 4 : 2) up_rows_kernel(Mo
 // 32 NW columns of y of one expert: NW waves, 32 columns each.  The pairs' h
 // goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
 // block, so the conversion is repeated only by an expert's hidden / (32 NW)
-// workgroups.  z: one row per pair.
+// workgroups.  z: one row per pair.  64 tokens as above: 29 us, the decode 0.9 of it.
 template <int F, int P, int C, int NW, bool FEW>
 __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
   constexpr int N = 16 * C, KB = C == 4 ? 2 : 4 / P;
@@ -627,7 +639,8 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
   __shared__ int s_ex[KB][N];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.dtab);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, q = lane >> 4;
   const int nb = static_cast<int>(A.inter >> 8);
   const int64_t per = A.hidden / (32 * NW), part = blockIdx.x % per;
   int e = static_cast<int>(blockIdx.x / per);
@@ -723,7 +736,8 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
   }
 }
 
-// y[t] = the sum of its pairs' rows, in the order of its ids
+// y[t] = the sum of its pairs' rows, in the order of its ids: no atomics, so that
+// a call repeats bit for bit (4 to 5 us, a launch).
 __global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
   const int64_t per = A.hidden / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= A.T * per) return;
@@ -842,7 +856,7 @@ template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
                        dim3(static_cast<unsigned>(64 * split_kw(nb) * split_rw(nb))), 0, stream, A);
     return;
   }
-  if (is_few(A.T, A.E))
+  if (is_few(A.T, A.E))  // four waves: 8 tokens 59 us and 62 with eight, 9 tokens 58 and 64, 16 tokens 73 and 73
     launch_up_rows<F, P, 1, 4, true>(A, experts, stream);
   else if (pairs == 1)
     launch_up_rows<F, P, 1, 8, false>(A, A.E, stream);
