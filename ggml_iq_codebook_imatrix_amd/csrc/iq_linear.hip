@@ -630,11 +630,12 @@ int check_linear(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int 
   if (run_bad_fmt(fmt)) return IQ_ERR_FMT;
   if (run_bad_dtype(dtype)) return IQ_ERR_DTYPE;
   if (rows < 0 || T < 0 || cols <= 0 || cols % 256 != 0) return IQ_ERR_SHAPE;
-  if (rows > (int64_t(1) << 31) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
+  // rows: 512 threads take at least 32 where there are many
+  if (rows > (int64_t(1) << 27) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   if (rank < 0 || rank > 1024) return IQ_ERR_ARG;
   const int64_t ntile = (T + 15) / 16;
   // the preparing launch: conversion, codebook, adapters
-  if ((T + 7) / 8 + 8 + ntile * 16 * ((rank + 15) / 16) >= kMaxWG) return IQ_ERR_SHAPE;
+  if ((T + 7) / 8 + 8 + 1024 + ntile * ((rank + 15) / 16) >= kMaxWG) return IQ_ERR_SHAPE;
   if (ntile > 4 * 65535) return IQ_ERR_SHAPE;
   return IQ_OK;
 }

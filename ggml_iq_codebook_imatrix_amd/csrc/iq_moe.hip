@@ -823,9 +823,9 @@ int check_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, int d
   if (E < 1 || E > 4096 || top_k < 1 || top_k > kMaxTopK) return IQ_ERR_ARG;
   const int64_t ntile = (T + 15) / 16, np = T * top_k;
   if (T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
-  // the launches: routing, up, down, sum (pairs are counted in 32 bits)
-  if ((T + 7) / 8 + 8 + ((E + 15) / 16) * ntile * 4 >= kMaxWG ||
-      np >= kMaxWG || E * (inter / 16) >= kMaxWG || E * (hidden / 16) >= kMaxWG || T * (hidden / 4) / 256 >= kMaxWG)
+  // pairs are counted in 32 bits; then the launches: routing, up, down, sum
+  if (np >= (int64_t(1) << 31) - 1 || (T + 7) / 8 + 8 + ((E + 15) / 16) * ntile * 4 >= kMaxWG ||
+      E * (inter / 128) >= kMaxWG || E * (hidden / 256) >= kMaxWG || T * (hidden / 4) / 512 >= kMaxWG)
     return IQ_ERR_SHAPE;
   return IQ_OK;
 }

@@ -35,7 +35,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // arrays of it sta
 
 constexpr int ST_ROUNDED = IQ_STATUS_ROUNDED;
 constexpr int kCodebook[5] = {256, 512, 1024, 2048, 2048};
-constexpr int64_t kMaxWG = (int64_t(1) << 31) - 1;  // workgroups in one grid dimension
+// A dimension of a grid holds fewer than 2^32 threads: this many workgroups of 512.
+constexpr int64_t kMaxWG = (int64_t(1) << 23) - 1;
 
 inline bool run_launched() { return hipGetLastError() == hipSuccess; }
 inline bool run_bad_fmt(int f) { return f < 0 || f > 4; }

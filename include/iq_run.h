@@ -22,7 +22,9 @@
  *    fp32 tokens are held as the sum of two fp16 values (relative 2^-22 of the
  *    value).
  *  - the block scale d is applied in fp32 to each 256-column block's fp32 sum,
- *    blocks are added in fp32, and the power of two is taken back at the end.
+ *    blocks are added in fp32, and the power of two is taken back at the end (bf16
+ *    prompts keep the running sum in units of the block's d instead, and rescale it
+ *    in fp32 from block to block).
  * Infinities and NaN in a token reach that token's outputs only.
  */
 #ifndef IQ_RUN_H
@@ -65,8 +67,8 @@ extern "C" {
  * T == 0 or rows == 0 enqueues nothing and returns IQ_OK.
  * Errors: IQ_ERR_FMT, IQ_ERR_DTYPE, IQ_ERR_NULL (grid, packed, x, y; with
  * adapters lora_a, lora_b, lora_ids; a needed workspace), IQ_ERR_SHAPE (rows or
- * T negative, cols <= 0 or % 256, sizes whose launches would not fit a grid),
- * IQ_ERR_ARG (rank outside [0, 1024], num_adapters < 1 with a rank, packed at an
+ * T negative, cols <= 0 or % 256, rows above 2^27, sizes whose launches would not
+ * fit a grid), IQ_ERR_ARG (rank outside [0, 1024], num_adapters < 1 with a rank, packed at an
  * odd address),
  * IQ_ERR_WORKSPACE, IQ_ERR_HIP. */
 int iq_linear(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const float *grid, const void *x,

@@ -184,3 +184,76 @@ def base_moe():
 def test_moe_binding_refuses(api, kw):
     with pytest.raises(api.IQError):
         api.moe(**{**base_moe(), **kw})
+
+
+@pytest.fixture(scope="module")
+def measured(api, tmp_path_factory):
+    """The stand-in, which also keeps the largest dimensions that it was asked to launch."""
+    objs = sorted(glob.glob(os.path.join(ROOT, "ggml_iq_codebook_imatrix_amd", "_build", "iq_*.hip.o")))
+    d = tmp_path_factory.mktemp("measured")
+    src, so = d / "measured.c", str(d / "libiq_measured.so")
+    src.write_text(f"""
+#define hipLaunchKernel base_launch
+#include "{os.path.join(ROOT, 'tests', 'hip_launch_stub.c')}"
+#undef hipLaunchKernel
+static unsigned long long threads, rows, empty;
+hipError_t hipLaunchKernel(const void *fn, dim3 grid, dim3 block, void **args, size_t shared, void *stream) {{
+  unsigned long long n = (unsigned long long)grid.x * block.x;
+  if (n > threads) threads = n;
+  if (grid.y > rows) rows = grid.y;
+  if (!grid.x || !grid.y || !block.x || block.x > 1024 || block.x % 64) empty = 1;
+  return base_launch(fn, grid, block, args, shared, stream);
+}}
+void sizes_reset(void) {{ threads = rows = empty = 0; }}
+unsigned long long most_threads(void) {{ return threads; }}
+unsigned long long most_rows(void) {{ return rows; }}
+unsigned long long bad_shape(void) {{ return empty; }}
+""")
+    subprocess.run(["gcc", "-O1", "-fPIC", "-c", str(src), "-o", str(d / "m.o")], check=True)
+    subprocess.run(["gcc", "-shared", "-o", so, *objs, str(d / "m.o"), "-L/opt/rocm/lib", "-lamdhip64",
+                    "-Wl,-Bsymbolic", "-Wl,-rpath,/opt/rocm/lib"], check=True)
+    L = ctypes.CDLL(so)
+    for name, (args, res) in api.SIGNATURES.items():
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = res
+    for n in ("most_threads", "most_rows", "bad_shape"):
+        getattr(L, n).restype = ctypes.c_ulonglong
+    return L
+
+
+def launches_fit(L, call):
+    """call() either refuses the sizes before any launch, or launches what the hardware takes."""
+    L.stub_reset(0)
+    L.sizes_reset()
+    rc = call()
+    assert rc in (0, -4), rc
+    if rc:
+        assert L.stub_launches() == 0
+    else:
+        assert L.most_threads() < 1 << 32 and L.most_rows() <= 65535 and not L.bad_shape()
+    return rc == 0
+
+
+def test_linear_launches_fit_the_grid(measured):
+    done = 0
+    for rows in (1, 17, 640 * 16, 1 << 20, 1 << 27, (1 << 27) + 1, 1 << 31):
+        for cols in (256, 1280, 2048, 1 << 24):
+            for T in (1, 16, 17, 32, 33, 64, 65, 700, 5000, 1 << 20, 4 * 65535 * 16, 4 * 65535 * 16 + 1):
+                for rank, dtype in ((0, 1), (1024, 1), (0, 0), (1024, 0)):
+                    done += launches_fit(measured, lambda: linear(measured, rows=rows, cols=cols, T=T, rank=rank, N=1,
+                                                                  dtype=dtype, wn=1 << 62))
+    assert done > 500
+    assert linear(measured, rows=1 << 27, wn=1 << 62) == 0 and linear(measured, rows=(1 << 27) + 1, wn=1 << 62) == -4
+
+
+def test_moe_launches_fit_the_grid(measured):
+    done = 0
+    for E, k in ((1, 1), (8, 2), (256, 8), (300, 64), (4096, 64)):
+        for hidden, inter in ((256, 256), (2048, 768), (1 << 18, 256), (256, 1 << 18), (1 << 24, 1 << 24)):
+            for T in (1, 2, 8, 9, 16, 17, 700, 1 << 20, 1 << 24):
+                for dtype in (0, 1):
+                    done += launches_fit(measured, lambda: moe(measured, E=E, k=k, hidden=hidden, inter=inter, T=T,
+                                                               dtype=dtype, wn=1 << 62))
+    assert done > 200
+    # 4,096 experts of 2^18 rows: 2^32 threads in a launch over whole rows
+    assert moe(measured, E=4096, inter=1 << 18, T=700, wn=1 << 62) == -4
