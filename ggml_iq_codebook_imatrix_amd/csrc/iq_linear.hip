@@ -113,7 +113,7 @@ __device__ __forceinline__ void lora_shrink(const PrepArgs &P, int64_t tt, int r
           const uint32_t top = __float_as_uint(f) & 0xffff0000u;
           v[k * 512] = static_cast<uint16_t>(top >> 16);
           if (pad) v[k * 512 + 256] = 0;
-          f -= __uint_as_float(top);
+          f = finite_f(f) ? f - __uint_as_float(top) : 0.0f;  // inf - inf would be NaN
         }
       } else {
         static_cast<float *>(L.v)[(tt * L.chunks + rt) * 256 + (((jj & 15) >> 2) * 16 + tok) * 4 + (jj & 3)] = f;

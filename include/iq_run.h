@@ -57,7 +57,8 @@ extern "C" {
  *           with zeros.  lora_scale (device, nullable: all ones) [num_adapters]
  *           f32.  lora_ids (device) [T] int32: the token's adapter, -1 for none;
  *           any other id outside [0, num_adapters) raises IQ_STATUS_BADID and
- *           adds nothing.  All are ignored when rank is 0.
+ *           adds nothing.  All are ignored when rank is 0.  An infinity in lora_b
+ *           gives NaN (bf16: its factor is held as a sum of three values).
  *  y        (device) [T, rows] OUT, of x's dtype: the fp32 sum, rounded once.
  *           Must not overlap any input.
  *  workspace, workspace_bytes  (device) scratch of at least

@@ -224,6 +224,30 @@ def test_linear_adapter_ids(api):
         assert torch.equal(api.linear(fmt, p, grid, x, a2, b, None, ids), got)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows, T", [(70, 5), (70, 40), (1100, 500), (2000, 1100)])
+def test_linear_infinities_through_the_adapters(api, rows, T, dtype):
+    """An infinity in a token passes through its adapter as plain arithmetic has it: inf, or NaN against an opposite one."""
+    print("[case] linear inf adapters", rows, T, dtype, flush=True)
+    fmt, nb = "IQ2_XS", 2
+    grid, p = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
+    x = dev(inputs.activations(T, nb * 256, 7, 8)).to(dtype)
+    x[1, 300], x[T - 2, 17] = float("inf"), float("-inf")
+    sign = torch.sign(api.dequantize(fmt, p, grid)).double()
+    for r in (1, 8, 9, 40):
+        g = torch.Generator(device="cuda").manual_seed(r)
+        a = (torch.rand((2, r, nb * 256), device="cuda", generator=g) + 0.5).to(dtype)
+        b = (torch.rand((2, rows, r), device="cuda", generator=g) + 0.5).to(dtype)
+        ids = (torch.arange(T, device="cuda") % 2).int()
+        got = api.linear(fmt, p, grid, x, a, b, None, ids).double()
+        # A and B are positive: the adapter gives the infinity's own sign in every row
+        inf = float("inf")
+        assert torch.equal(got[1].nan_to_num(7, inf, -inf), (sign[:, 300] * inf + inf).nan_to_num(7, inf, -inf)), r
+        assert torch.equal(got[T - 2].nan_to_num(7, inf, -inf), (sign[:, 17] * -inf - inf).nan_to_num(7, inf, -inf)), r
+        keep = [t for t in range(T) if t not in (1, T - 2)]
+        assert bool(got[keep].isfinite().all())
+
+
 def test_linear_codebook_rounding_is_reported(api, orc):
     """A codebook that fp16 does not hold is rounded (2^-11 twice per weight) and reported."""
     for fmt in FORMATS:
