@@ -20,7 +20,7 @@
  *    magnitude under 2^15 and held in fp16: exact for bf16 tokens (what lies 2^-29
  *    or more below the token's largest value is rounded by less than 2^-39 of it);
  *    fp32 tokens are held as the sum of two fp16 values (relative 2^-22 of the
- *    value).
+ *    value, or 2^-39 of the token's largest).
  *  - the block scale d is applied in fp32 to each 256-column block's fp32 sum,
  *    blocks are added in fp32, and the power of two is taken back at the end (bf16
  *    prompts keep the running sum in units of the block's d instead, and rescale it

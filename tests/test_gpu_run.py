@@ -469,7 +469,7 @@ def test_moe_random(api, orc, fmt, dtype):
 # whole rows of few tokens, few tokens with the choice in a launch of its own
 MORE_MOE = [("IQ2_XS", 6, 2, 1024, 256, 6), ("IQ1_S", 5, 2, 1280, 256, 20), ("IQ2_S", 200, 9, 256, 256, 7),
             ("IQ1_M", 200, 9, 256, 256, 13), ("IQ2_XXS", 300, 64, 256, 256, 3), ("IQ2_XS", 64, 64, 256, 256, 16),
-            ("IQ1_S", 64, 8, 512, 256, 8), ("IQ2_S", 30, 4, 256, 1024, 16), ("IQ2_XXS", 4, 2, 1536, 768, 2),
+            ("IQ1_S", 64, 8, 512, 256, 8), ("IQ2_S", 30, 4, 256, 1024, 16), ("IQ2_XXS", 5, 2, 1536, 768, 2),
             ("IQ2_S", 16, 3, 512, 256, 16), ("IQ1_M", 257, 1, 256, 256, 1), ("IQ1_S", 1, 1, 256, 256, 300),
             ("IQ1_M", 1100, 3, 256, 256, 40)]
 
@@ -514,10 +514,10 @@ def test_moe_callers_routing(api, orc, T):
     """Ids outside the range, ids repeated in a token, zero weights, a token with no expert at all, experts that
     every token names and experts that none does."""
     print("[case] moe routing", T, flush=True)
-    fmt, E, k, H, I, dtype = "IQ2_XS", 6, 4, 512, 256, torch.float32
+    fmt, E, k, H, I, dtype = "IQ2_XS", 7, 4, 512, 256, torch.float32
     grid, dgrid, gate, up, down, x, _ = moe_inputs(fmt, fmt, E, H, I, T, dtype, 500)
     g = inputs.rng(501)
-    ids = g.integers(0, 5, (T, k)).astype(np.int32)  # expert 5 idle; repeats are common
+    ids = g.integers(0, 5, (T, k)).astype(np.int32)  # experts 5 and 6 idle; repeats are common
     weights = g.random((T, k)).astype(np.float32)
     ids[:, 0] = 2
     ids[1] = (-1, E, 2 ** 31 - 1, -2 ** 31)
@@ -584,12 +584,12 @@ def test_moe_views_and_guards(api, T):
 # --------------------------------------------------------------------------
 # Streams, graphs, and a run of the calls together
 # --------------------------------------------------------------------------
-@pytest.mark.parametrize("T", [1, 24, 140])
+@pytest.mark.parametrize("T", [1, 24, 140, 1100])
 def test_streams_graphs_and_repeats(api, T):
     """The same bits on every call, on another stream, and from a captured graph on new inputs after each replay;
     two graphs with a workspace each, replayed in turn."""
     print("[case] streams graphs", T, flush=True)
-    fmt, E, k, H, I, N, r = "IQ2_XXS", 12, 4, 512, 256, 3, 8
+    fmt, E, k, H, I, N, r = "IQ2_XXS", 10, 4, 512, 256, 3, 8
     grid, _, gate, up, down, x, router = moe_inputs(fmt, fmt, E, H, I, T, torch.bfloat16, 800)
     grid, gate, up, down = dev(grid), dev(gate), dev(up), dev(down)
     g = torch.Generator(device="cuda").manual_seed(3)
@@ -636,7 +636,7 @@ def test_encode_then_run_then_collect(api, orc):
     """As they are used together: experts encoded with their importance, tokens through the layer, and the layer's
     ids fed to the collector; a projection encoded and run against its own decode."""
     print("[case] encode, run, collect", flush=True)
-    fmt, E, k, H, I, T = "IQ2_XS", 6, 2, 512, 256, 60
+    fmt, E, k, H, I, T = "IQ2_XS", 5, 2, 512, 256, 60
     grid = inputs.grid_for(fmt, 202)
     gd = dev(grid)
     x = dev(inputs.activations(T, H, 900, 901)).bfloat16()
