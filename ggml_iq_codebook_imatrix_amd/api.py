@@ -512,6 +512,13 @@ def _addr(t, name: str, index: int):
     return t.data_ptr()
 
 
+def _no_grad(*tensors):
+    """Encoded weights are frozen and the calls below have no backward pass: refused where one would be recorded."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise IQError("the call has no backward pass: tensors that require a gradient need torch.no_grad()")
+
+
 def _scratch(nbytes: int, x: torch.Tensor, workspace):
     if workspace is None and nbytes:
         workspace = x.new_empty(nbytes, dtype=torch.uint8)
@@ -540,7 +547,7 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
            status: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Tokens x [T, cols] through the encoded weight packed [rows, cols/256, block_bytes] -> [T, rows], of x's dtype.
     With lora_a [N, r, cols], lora_b [N, rows, r] (x's dtype) and lora_ids [T] int32 (-1: none), token t also gets
-    lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones)."""
+    lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones).  No backward pass."""
     f = _fmt(fmt)
     entries, nbytes = _geometry(f)
     rows, nb, _ = _ends(packed, "packed", (None, None, nbytes), torch.uint8)
@@ -565,6 +572,8 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
         _is(out, "out", (T, rows), dtype)
     if status is not None:
         _status_ok(status)
+    if torch.is_grad_enabled():
+        _no_grad(x, lora_a, lora_b, lora_scale)
     dev = _home(x)
     if out is None:
         out = x.new_empty((T, rows))
@@ -588,7 +597,8 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     """A mixture-of-experts layer on encoded experts: gate, up [E*inter, hidden/256, bytes], down
     [E*hidden, inter/256, bytes] (down_fmt and down_grid where they differ), x [T, hidden].
     With router [E, hidden] and top_k the layer routes its tokens (ids and weights, where given, are filled);
-    without, ids [T, top_k] int32 and weights [T, top_k] f32 are the caller's.  Returns (y, ids, weights)."""
+    without, ids [T, top_k] int32 and weights [T, top_k] f32 are the caller's.  Returns (y, ids, weights).
+    No backward pass."""
     f = _fmt(fmt)
     fd = f if down_fmt is None else _fmt(down_fmt)
     (entries, nbytes), (dentries, dbytes) = _geometry(f), _geometry(fd)
@@ -630,6 +640,8 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
         _is(out, "out", (T, hidden), dtype)
     if status is not None:
         _status_ok(status)
+    if torch.is_grad_enabled():
+        _no_grad(x, router, weights)
     dev = _home(x)
     if ids is None:
         ids = x.new_empty((T, k), dtype=torch.int32)

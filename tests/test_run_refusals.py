@@ -186,6 +186,26 @@ def test_moe_binding_refuses(api, kw):
         api.moe(**{**base_moe(), **kw})
 
 
+@pytest.mark.parametrize("name", ["x", "lora_a", "lora_b", "lora_scale"])
+def test_linear_has_no_backward_pass(api, name):
+    kw = base_linear()
+    kw[name].requires_grad_()
+    with pytest.raises(api.IQError, match="no backward pass"):
+        api.linear(**kw)
+    with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
+        api.linear(**kw)
+
+
+@pytest.mark.parametrize("name", ["x", "router"])
+def test_moe_has_no_backward_pass(api, name):
+    kw = base_moe()
+    kw[name].requires_grad_()
+    with pytest.raises(api.IQError, match="no backward pass"):
+        api.moe(**kw)
+    with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
+        api.moe(**kw)
+
+
 @pytest.fixture(scope="module")
 def measured(api, tmp_path_factory):
     """The stand-in, which also keeps the largest dimensions that it was asked to launch."""
