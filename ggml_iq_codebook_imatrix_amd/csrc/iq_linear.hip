@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(512) linear_split_kernel(LinearArgs A) {
         for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * stride;
         load_operand<P, C>(x, xp);
       },
-      [](f32x4 &a, const f32x4 &part, float d, int) { scale_add(a, part, d); }, acc);
+        acc);
   f32x4 sum[RT][C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -423,22 +423,7 @@ __global__ void __launch_bounds__(64 * KG * RG, KG * RG / 4) linear_tile_kernel(
       acc[r][c] = f32x4{ldexpf(acc[r][c][0], e.x), ldexpf(acc[r][c][1], e.y), ldexpf(acc[r][c][2], e.z),
                         ldexpf(acc[r][c][3], e.w)};
   }
-  if (A.L.rank) {  // four token tiles at a time: what a round fetches is held in registers
-    constexpr int CB = C < 4 ? C : 4;
-#pragma unroll
-    for (int c0 = 0; c0 < C; c0 += CB) {
-      f32x4 a[R][CB];
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) a[r][c] = acc[r][c0 + c];
-      lora_expand<P, CB, R>(A.L, tt0 + c0, A.T, A.rows, row0, kg, KG, a);
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) acc[r][c0 + c] = a[r][c];
-    }
-  }
+  if (A.L.rank) lora_expand<P, C, R>(A.L, tt0, A.T, A.rows, row0, kg, KG, acc);
   const auto put = [&](int64_t r0, int tile, int l, const f32x4 &s) {
     const int64_t row = r0 + (tile / C) * 16 + (l & 15);
     if (row >= A.rows) return;

@@ -303,65 +303,51 @@ __device__ __forceinline__ int few_expert(const MoeArgs &A, FewPairs &S, int slo
 // of 512 x 256, 5 tokens, float32) 9 us, with whole rows 11.
 template <int F, int P>
 __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
-  constexpr int C = 1, RT = 1, N = 16;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ f32x4 s_red[8 * 2 * C * 64];
+  __shared__ f32x4 s_red[8 * 2 * 64];
   __shared__ FewPairs S;
   load_table<F>(s_tab, A.tab);
   const int64_t nb = A.hidden >> 8, rowbytes = nb * Geo<F>::BYTES, stride = A.X.ntile * P * 4096;
   const Split W = split_of(nb);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4, tiles = static_cast<int>(A.inter >> 4);
-  const int per = (tiles + W.rw * RT - 1) / (W.rw * RT), tile0 = static_cast<int>(blockIdx.x % per) * W.rw * RT;
+  const int per = (tiles + W.rw - 1) / W.rw, tile0 = static_cast<int>(blockIdx.x % per) * W.rw;
   few_ids(A, S, A.pick);
   const int e = few_expert(A, S, static_cast<int>(blockIdx.x / per));
   if (e < 0) return;
-  for (int c0 = 0; c0 < S.n; c0 += N) {
+  const int64_t row = e * A.inter + min(tile0 + W.rg, tiles - 1) * 16 + n;
+  for (int c0 = 0; c0 < S.n; c0 += 16) {
     const int *list = S.list + c0;
-    const int count = min(N, S.n - c0);
-    const _Float16 *x0[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t t = list[min(c * 16 + n, count - 1)] / A.top_k;
-      x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
-    }
-    f32x4 acc[RT][2][C] = {};
-    split_blocks<F, P, C, RT, 2>(
-        nb, W, s_tab,
-        [&](int m, int rt) {
-          const int64_t row = e * A.inter + min(tile0 + W.rg * RT + rt, tiles - 1) * 16 + n;
-          return (m ? A.up : A.gate) + row * rowbytes;
+    const int count = min(16, S.n - c0);
+    const int64_t t = list[min(n, count - 1)] / A.top_k;
+    const _Float16 *x0 = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
+    f32x4 acc[1][2][1] = {};
+    split_blocks<F, P, 1, 1, 2>(
+        nb, W, s_tab, [&](int m, int) { return (m ? A.up : A.gate) + row * rowbytes; },
+        [&](int64_t b, Operand<P, 1> &x) __attribute__((always_inline)) {
+          const _Float16 *const xp[1] = {x0 + b * stride};
+          load_operand<P, 1>(x, xp);
         },
-        [&](int64_t b, Operand<P, C> &x) __attribute__((always_inline)) {
-          const _Float16 *xp[C];
+        acc);
+    // the sums over a row group's waves, then h
 #pragma unroll
-          for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * stride;
-          load_operand<P, C>(x, xp);
-        },
-        [](f32x4 &a, const f32x4 &part, float d, int) { scale_add(a, part, d); }, acc);
+    for (int j = 0; j < 2; ++j) s_red[((W.rg * W.kw + W.kg) * 2 + j) * 64 + lane] = acc[0][j][0];
+    __syncthreads();
+    for (int i = threadIdx.x; i < W.rw * 64; i += blockDim.x) {
+      const int rg = i / 64, l = i & 63, tile = tile0 + rg;
+      if (tile >= tiles) continue;
+      const f32x4 *p = s_red + rg * W.kw * 2 * 64 + l;
+      f32x4 g = p[0], u = p[64];
+      for (int k = 1; k < W.kw; ++k) {
+        g += p[k * 2 * 64];
+        u += p[(k * 2 + 1) * 64];
+      }
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {  // the sums over a row group's waves, then h
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 2 * C; ++j) s_red[((W.rg * W.kw + W.kg) * 2 * C + j) * 64 + lane] = acc[rt][j / C][j % C];
-      __syncthreads();
-      for (int i = threadIdx.x; i < W.rw * C * 64; i += blockDim.x) {
-        const int rg = i / (C * 64), c = i / 64 % C, l = i & 63, tile = tile0 + rg * RT + rt;
-        if (tile >= tiles) continue;
-        const f32x4 *p = s_red + (rg * W.kw * 2 * C + c) * 64 + l;
-        f32x4 g = p[0], u = p[C * 64];
-        for (int k = 1; k < W.kw; ++k) {
-          g += p[k * 2 * C * 64];
-          u += p[(k * 2 + 1) * C * 64];
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = c * 16 + (l >> 4) * 4 + k;
-          if (at >= count) continue;
-          const int64_t pair = list[at];
-          const float w = S.w[pair];
-          const int ex = A.X.ex[pair / A.top_k];
-          A.h[pair * A.inter + tile * 16 + (l & 15)] = gated(ldexpf(g[k], ex), ldexpf(u[k], ex), w);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int at = (l >> 4) * 4 + k;
+        if (at >= count) continue;
+        const int64_t pair = list[at];
+        const int ex = A.X.ex[pair / A.top_k];
+        A.h[pair * A.inter + tile * 16 + (l & 15)] = gated(ldexpf(g[k], ex), ldexpf(u[k], ex), S.w[pair]);
       }
     }
     __syncthreads();  // the sums' memory is free again

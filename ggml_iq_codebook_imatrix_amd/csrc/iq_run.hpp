@@ -104,9 +104,6 @@ template <class V> __device__ __forceinline__ V ldu(const void *p) {  // any ali
   return v;
 }
 
-__device__ __forceinline__ float load1(const void *x, int dtype, int64_t i) {
-  return dtype == 1 ? bf16_to_f32(static_cast<const uint16_t *>(x)[i]) : static_cast<const float *>(x)[i];
-}
 __device__ __forceinline__ void store1(void *y, int dtype, int64_t i, float v) {
   if (dtype == 1)
     static_cast<uint16_t *>(y)[i] = f32_to_bf16(v);
@@ -491,11 +488,10 @@ __device__ __forceinline__ void load_operand(Operand<P, C> &x, const _Float16 *c
 }
 
 // acc[rt][m][c] += the wave's blocks of M matrices.  rowp(m, rt): the lane's row;
-// loadx(b, x): the operand of block b; scale(c, f): applied to a block's sums
-// times d (a power of two of the block's own, or nothing).
-template <int F, int P, int C, int RT, int M, class RowP, class LoadX, class Add>
+// loadx(b, x): the operand of block b.
+template <int F, int P, int C, int RT, int M, class RowP, class LoadX>
 __device__ __forceinline__ void split_blocks(int64_t nb, const Split &S, const uint4 *tab, RowP rowp, LoadX loadx,
-                                             Add add, f32x4 (&acc)[RT][M][C]) {
+                                             f32x4 (&acc)[RT][M][C]) {
   const int q = (threadIdx.x & 63) >> 4;
   Operand<P, C> x;
   Words words[M];
@@ -533,7 +529,7 @@ __device__ __forceinline__ void split_blocks(int64_t nb, const Split &S, const u
       for (int m = 0; m < M; ++m) {
         const float d = block_scale<F>(raw[m]);
 #pragma unroll
-        for (int c = 0; c < C; ++c) add(acc[rt][m][c], part[m][c], d, c);
+        for (int c = 0; c < C; ++c) scale_add(acc[rt][m][c], part[m][c], d);
         words[m] = next[m];
       }
     }
