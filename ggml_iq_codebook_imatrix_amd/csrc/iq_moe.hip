@@ -9,7 +9,7 @@
 // more it is given an expert, whose pairs it gathers from the ids.
 //
 // One token through 128 experts of 2,048 x 768 (eight of them, 9.7 MB of payload)
-// takes 27 us: routing 5.5, gate and up 13 (2 of them the choice), down 8.  Each is
+// takes 29 us: routing 5.5, gate and up 13 (2 of them the choice), down 10.  Each is
 // a chain of waits: the launch, the logits, the payload, the sums.
 //
 // Gate and up (h in fp32, one row per pair):
@@ -30,6 +30,11 @@
 namespace iq {
 namespace {
 
+// h is held as the sum of two fp16 values, for tokens of either type: one value's
+// 2^-12 would change one bf16 output in twenty by a step.  The second costs matrix
+// instructions beside the same decode: bf16, 1 token 28.7 us and 26.9 with one
+// value, 64 tokens 106 and 101, 200 tokens 162 and 153.
+constexpr int kHParts = 2;
 constexpr int kFewTokens = 16, kFewExperts = 256, kMaxTopK = 64;
 
 struct MoeArgs {
@@ -356,19 +361,19 @@ __global__ void __launch_bounds__(512) up_split_kernel(MoeArgs A) {
 
 // Waves split (expert, block of inter): each stages its tokens' h of that block
 // as the A operand (rows: tokens; absent ones zero) in LDS of its own.  One token
-// through eight experts of 2,048 x 768: 8 us, latency.
-constexpr int down_split_waves(int parts) { return parts == 2 ? 4 : 8; }  // 8 KiB of LDS a part and wave
-template <int F, int P>
-__global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(MoeArgs A) {
-  constexpr int NW = down_split_waves(P);
+// through eight experts of 2,048 x 768: 10 us, latency.
+constexpr int down_split_waves(int fmt) { return fmt >= IQ1_S ? 4 : 8; }  // 16 KiB of LDS a wave, beside the codebook
+template <int F>
+__global__ void __launch_bounds__(64 * down_split_waves(F)) down_split_kernel(MoeArgs A) {
+  constexpr int NW = down_split_waves(F);
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ uint4 s_x[NW][P * 512];  // also the sums over the waves
+  __shared__ uint4 s_x[NW][kHParts * 512];  // also the sums over the waves
   __shared__ int s_ex[NW][16], s_active[kFewExperts];
   __shared__ FewPairs S;
   load_table<F>(s_tab, A.dtab);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int np = static_cast<int>(A.npair), n = lane & 15, q = lane >> 4;
-  for (int i = lane; i < P * 512; i += 64) s_x[wave][i] = make_uint4(0, 0, 0, 0);
+  for (int i = lane; i < kHParts * 512; i += 64) s_x[wave][i] = make_uint4(0, 0, 0, 0);
   if (lane < 16) s_ex[wave][lane] = 0;
   few_ids(A, S, false);
   int na = 0;
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
 #pragma unroll
       for (int j = 0; j < 4; ++j) to_parts(v[j], up, hi[j], lo[j]);
       *reinterpret_cast<uint2 *>(xs + at + t * 8) = __builtin_bit_cast(uint2, hi);
-      if (P == 2) *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = __builtin_bit_cast(uint2, lo);
+      *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = __builtin_bit_cast(uint2, lo);
       if (lane == 0) s_ex[wave][t] = -up;
       present |= 1u << t;
     };
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
     Raw raw[1];
     raw[0] = unpack<F>(words, q);
     f32x4 part[1][1];
-    block_mma<F, P, 1, 1>(raw, s_tab, xp, part);
+    block_mma<F, kHParts, 1, 1>(raw, s_tab, xp, part);
     const float d = block_scale<F>(raw[0]);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
     for (uint32_t m = present; m; m &= m - 1) {  // leave the rows zero again
       const int t = __builtin_ctz(m);
       *reinterpret_cast<uint2 *>(xs + at + t * 8) = make_uint2(0, 0);
-      if (P == 2) *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = make_uint2(0, 0);
+      *reinterpret_cast<uint2 *>(xs + 4096 + at + t * 8) = make_uint2(0, 0);
     }
   }
   const Split W{NW, 1, wave, 0};
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(64 * down_split_waves(P)) down_split_kernel(Mo
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int t = (l >> 4) * 4 + k;
-      if (t < A.T) store1(A.y, P == 1, t * A.hidden + col0 + (l & 15), s[k]);
+      if (t < A.T) store1(A.y, A.dtype, t * A.hidden + col0 + (l & 15), s[k]);
     }
   });
 }
@@ -616,12 +621,12 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 2 / P : P * C == 1 ? 4 : 2)
 // 32 NW columns of y of one expert: NW waves, 32 columns each.  The pairs' h
 // goes to LDS as the A operand, KB blocks at a time: a wave converts one pair's
 // block, so the conversion is repeated only by an expert's hidden / (32 NW)
-// workgroups.  z: one row per pair.  64 tokens as above: 29 us, the decode 0.9 of it.
-template <int F, int P, int C, int NW, bool FEW>
+// workgroups.  z: one row per pair.  64 tokens as above: 36 us, the decode 0.75 of it.
+template <int F, int C, int NW, bool FEW>
 __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeArgs A) {
-  constexpr int N = 16 * C, KB = C == 4 ? 2 : 4 / P;
+  constexpr int N = 16 * C, KB = C == 4 ? 1 : 2;
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ _Float16 s_h[KB][C][P * 4096];
+  __shared__ _Float16 s_h[KB][C][kHParts * 4096];
   __shared__ int s_ex[KB][N];
   __shared__ typename std::conditional<FEW, FewPairs, PairWalk<N>>::type S;
   load_table<F>(s_tab, A.dtab);
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
         for (int k = 0; k < 4; ++k) to_parts(v[k], up, hi[k], lo[k]);
         _Float16 *o = &s_h[j][m >> 4][((n >> 1) * 64 + q * 16 + (m & 15)) * 8 + (n & 1) * 4];
         *reinterpret_cast<uint2 *>(o) = __builtin_bit_cast(uint2, hi);
-        if (P == 2) *reinterpret_cast<uint2 *>(o + 4096) = __builtin_bit_cast(uint2, lo);
+        *reinterpret_cast<uint2 *>(o + 4096) = __builtin_bit_cast(uint2, lo);
         if (lane == 0) s_ex[j][m] = -up;
       }
       __syncthreads();
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(64 * NW, C == 1 ? 4 : 2) down_rows_kernel(MoeA
         Raw raw[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) raw[r] = unpack<F>(words[0][r], q);
-        block_mma<F, P, C, 2>(raw, s_tab, xp, sum);
+        block_mma<F, kHParts, C, 2>(raw, s_tab, xp, sum);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -774,10 +779,11 @@ int64_t reached(int64_t np, int E) { return np < E ? np : E; }
 bool split_up(const MoeArgs &A) { return is_few(A.T, A.E) && reached(A.npair, A.E) * (A.inter / 16) <= 512; }
 // Down with the (expert, block) pairs split over the waves, no launch for the sums:
 // a wave converts every pair's block, so while these are few: 16 of them (16
-// experts of 1,024 x 512, 4 tokens) 21 us and 24 with whole rows, 24 26 and 31, 48
-// 38 and 38, 72 47 and 43; float32 has half the waves.
-bool split_down(int64_t T, int E, int top_k, int64_t inter, int dtype) {
-  return is_few(T, E) && T * top_k * (inter / 256) <= (dtype == IQ_DTYPE_F32 ? 24 : 48);
+// experts of 1,024 x 512, 4 tokens) 23 us and 26 with whole rows, 24 29 and 34, 48
+// 41 and 40, 72 52 and 46.  The IQ1 codebooks leave LDS for half the waves: 16 of
+// them 27 and 27, 24 34 and 35, 48 48 and 41.
+bool split_down(int64_t T, int E, int top_k, int64_t inter, int down_fmt) {
+  return is_few(T, E) && T * top_k * (inter / 256) <= (down_split_waves(down_fmt) == 4 ? 24 : 48);
 }
 
 struct MoePlan {
@@ -797,7 +803,7 @@ MoePlan plan_moe(int fmt, int down_fmt, int64_t hidden, int64_t inter, int E, in
   p.ks = hidden >= 4 * 256 ? 4 : 1;  // eight workgroups alone would route 16 tokens to 128 experts: 3 to 5 us more
   p.ho = p.lo + ws_up(static_cast<size_t>(p.ks) * T * E * 8);
   p.zo = p.ho + ws_up(np * inter * 4);
-  p.bytes = p.zo + ws_up(split_down(T, E, top_k, inter, dtype) ? 0 : np * hidden * 4) + kWsAlign;
+  p.bytes = p.zo + ws_up(split_down(T, E, top_k, inter, down_fmt) ? 0 : np * hidden * 4) + kWsAlign;
   return p;
 }
 
@@ -821,16 +827,17 @@ void launch_up_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
   hipLaunchKernelGGL((up_rows_kernel<F, P, C, NW, FEW>), dim3(static_cast<unsigned>(experts * (A.inter / (16 * NW)))),
                      dim3(64 * NW), 0, stream, A);
 }
-template <int F, int P, int C, int NW, bool FEW>
+template <int F, int C, int NW, bool FEW>
 void launch_down_rows(const MoeArgs &A, int64_t experts, hipStream_t stream) {
-  hipLaunchKernelGGL((down_rows_kernel<F, P, C, NW, FEW>),
+  hipLaunchKernelGGL((down_rows_kernel<F, C, NW, FEW>),
                      dim3(static_cast<unsigned>(experts * (A.hidden / (32 * NW)))), dim3(64 * NW), 0, stream, A);
 }
 // Tiles of 16 pairs that a workgroup multiplies at once, by an expert's pairs on
 // average: as many as most experts fill, since every pass decodes the rows again.
-// Measured (128 experts of 2,048 x 768, IQ1_M): 12.5 pairs with one tile 170 us and
-// 160 with two; 16 with two 168 and 190 with four; 31 with two 290 and 281 with
-// four; 250 with two 2,033 and 1,774 with four.  float32 has no room for four.
+// Measured (128 experts of 2,048 x 768, IQ1_M): 12.5 pairs with one tile 173 us and
+// 164 with two; 16 with two 200 and 204 with four; 31 with two 313 and 300 with
+// four; 250 with two 2,152 and 1,822 with four.  Gate and up of float32 have no room
+// for four.
 int pair_tiles(int64_t npair, int64_t E) { return npair <= 8 * E ? 1 : npair <= 28 * E ? 2 : 4; }
 
 template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
@@ -852,21 +859,21 @@ template <int F, int P> void launch_up(const MoeArgs &A, hipStream_t stream) {
     launch_up_rows<F, P, 4, 8, false>(A, A.E, stream);
 }
 
-template <int F, int P> void launch_down(const MoeArgs &A, hipStream_t stream) {
+template <int F> void launch_down(const MoeArgs &A, hipStream_t stream) {
   const int pairs = pair_tiles(A.npair, A.E);
-  if (split_down(A.T, A.E, A.top_k, A.inter, A.dtype)) {
-    hipLaunchKernelGGL((down_split_kernel<F, P>), dim3(static_cast<unsigned>(A.hidden / 16)),
-                       dim3(64 * down_split_waves(P)), 0, stream, A);
+  if (split_down(A.T, A.E, A.top_k, A.inter, F)) {
+    hipLaunchKernelGGL((down_split_kernel<F>), dim3(static_cast<unsigned>(A.hidden / 16)),
+                       dim3(64 * down_split_waves(F)), 0, stream, A);
     return;
   }
   if (is_few(A.T, A.E))
-    launch_down_rows<F, P, 1, 8, true>(A, reached(A.npair, A.E), stream);
+    launch_down_rows<F, 1, 8, true>(A, reached(A.npair, A.E), stream);
   else if (pairs == 1)
-    launch_down_rows<F, P, 1, 8, false>(A, A.E, stream);
-  else if (P == 2 || pairs == 2)
-    launch_down_rows<F, P, 2, 8, false>(A, A.E, stream);
-  else if constexpr (P == 1)
-    launch_down_rows<F, P, 4, 8, false>(A, A.E, stream);
+    launch_down_rows<F, 1, 8, false>(A, A.E, stream);
+  else if (pairs == 2)
+    launch_down_rows<F, 2, 8, false>(A, A.E, stream);
+  else
+    launch_down_rows<F, 4, 8, false>(A, A.E, stream);
 }
 
 }  // namespace
@@ -950,11 +957,11 @@ int iq_moe(int fmt, int down_fmt, const uint8_t *gate, const uint8_t *up, const 
   IQ_BY_FMT(fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-#define CALL(F) dtype == IQ_DTYPE_F32 ? launch_down<F, 2>(A, stream) : launch_down<F, 1>(A, stream)
+#define CALL(F) launch_down<F>(A, stream)
   IQ_BY_FMT(down_fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-  if (!split_down(T, num_experts, top_k, inter, dtype)) {
+  if (!split_down(T, num_experts, top_k, inter, down_fmt)) {
     hipLaunchKernelGGL(sum_kernel, dim3(static_cast<unsigned>((T * (hidden / 4) + 255) / 256)), dim3(256), 0,
                        stream, A);
     if (!run_launched()) return IQ_ERR_HIP;

@@ -104,9 +104,9 @@ int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int
  *           id repeated in one token counts per occurrence.
  *  ids      (device) [T, top_k] int32, weights (device) [T, top_k] f32.
  *  y        (device) [T, hidden] OUT, of x's dtype.  Must not overlap any input.
- *  h is held between the two products as the tokens are (fp16 under a
- *  power-of-two block scale: bf16 tokens one value, relative 2^-12, an eighth of
- *  the output's own rounding; fp32 tokens two values).
+ *  h is held between the two products in fp32, and enters the second one as the
+ *  sum of two fp16 values under a power of two per 256 columns, for tokens of
+ *  either type (relative 2^-22 of the value, or 2^-39 of the block's largest).
  *  workspace, workspace_bytes  (device) at least iq_moe_workspace_size(...).
  *  status   (device, nullable): IQ_STATUS_BADID, IQ_STATUS_ROUNDED.
  * T == 0 enqueues nothing and returns IQ_OK.

@@ -721,3 +721,61 @@ def test_large_offsets_in_prompts(api, orc):
         assert np.all(np.abs(got - want) <= linear_tolerance(xd, w, torch.bfloat16, want) + nb * 258 * 2 * U * S)
         assert bool((y[:, :-64] == 0).all())
         del y
+
+
+# (experts, top_k, hidden, inter, tokens): the waves that share an expert's blocks, whole rows of few tokens, and one,
+# two and four tiles of pairs; more blocks than a stage of h holds
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("down_fmt", ["IQ2_XXS", "IQ2_S", "IQ1_S"])
+@pytest.mark.parametrize("E, k, H, I, T", [(4, 2, 512, 256, 1), (4, 2, 512, 768, 5), (4, 2, 512, 768, 12),
+                                           (6, 2, 512, 768, 24), (4, 2, 256, 768, 40), (3, 1, 512, 1280, 120)])
+def test_moe_keeps_the_bits_of_h(api, orc, E, k, H, I, T, down_fmt, dtype):
+    """h of 12 and 13 bits beside sums that float32 holds exactly: the layer rounds nothing but its output."""
+    print("[case] moe bits of h", E, k, H, I, T, down_fmt, dtype, flush=True)
+    g = inputs.rng(1500 + T)
+    fmt = "IQ2_XXS"
+    grid = inputs.grid_for(fmt, 5)
+    grid[0] = 1
+
+    def rows_of(m, signs):
+        """Rows whose weights at columns 0 and 32 are +-m[:, 0] and +-m[:, 1] (odd, 1 to 31)."""
+        p = np.zeros((len(m), H // 256, 66), dtype=np.uint8)
+        p[..., 0], p[..., 1] = 0x00, 0x48  # d = 8, and a weight is d / 8 times its integers
+        for n in range(2):
+            p[:, 0, 2 + 8 * n + 7] = (m[:, n] // 2) << 4
+            p[:, 0, 2 + 8 * n + 4] = signs[n] & 127  # the eighth sign is the seven's parity, of a column that is zero
+        return p
+
+    # x = 2^n at column 0 and 2^n 32 at column 32: g = 2^n (m0 + 32 m1) >= 33, where silu(g) = g in float32, and
+    # u = 2^n (m0 - 32) with m0 of 27 to 31
+    gate = rows_of(2 * g.integers(0, 16, (E * I, 2)) + 1, (0, 0))
+    up = rows_of(np.stack((2 * g.integers(13, 16, E * I) + 1, np.ones(E * I, dtype=np.int64)), 1), (0, 1))
+    dgrid = grid if down_fmt == fmt else inputs.grid_for(down_fmt, 51)
+    down = payload(down_fmt, E * H, I // 256, 1501 + T, d16=0x4800)
+    if down_fmt == fmt:
+        down.reshape(-1, I // 256, 66)[..., 9::8] &= 15  # multipliers of one: weights of +-1, 3, 5
+    elif down_fmt == "IQ2_S":
+        down[..., 74:] = 0
+    else:
+        down[..., 35::2] &= 0x8f  # and here eighths: 1, 7 and 9 of them
+    x = np.zeros((T, H), dtype=np.float32)
+    x[:, 0] = 2.0 ** g.integers(0, 3, T)
+    x[:, 32] = 32 * x[:, 0]
+    ids = np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    weights = g.choice([-1.0, 1.0], (T, k)).astype(np.float32)
+    wg, wu, wd = decoded(orc, fmt, gate, grid), decoded(orc, fmt, up, grid), decoded(orc, down_fmt, down, dgrid)
+    y, size = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(E):
+        t, s = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        a, b = x[t] @ wg[e * I:(e + 1) * I].T, x[t] @ wu[e * I:(e + 1) * I].T
+        assert a.min() >= 33 and np.array_equal(a, a.astype(np.int64)) and np.abs(b).max() <= 4 * 5
+        h = a * b * weights[t, s, None]
+        np.add.at(y, t, h @ wd[e * H:(e + 1) * H].T)
+        np.add.at(size, t, np.abs(h) @ np.abs(wd[e * H:(e + 1) * H]).T / x[t, :1] ** 2)
+    assert size.max() < 2.0 ** 24  # in units of the token's own step: every partial sum, in any order, is exact
+    assert np.array_equal(y, y.astype(np.float32))
+    got, _, _ = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), dev(x, dtype), E, ids=dev(ids),
+                        weights=dev(weights), down_fmt=down_fmt, down_grid=dev(dgrid))
+    assert np.array_equal(f64(got), round_to(y, dtype))
