@@ -573,7 +573,7 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
     if status is not None:
         _status_ok(status)
     if torch.is_grad_enabled():
-        _no_grad(x, lora_a, lora_b, lora_scale)
+        _no_grad(grid, x, lora_a, lora_b, lora_scale)
     dev = _home(x)
     if out is None:
         out = x.new_empty((T, rows))
@@ -641,7 +641,7 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     if status is not None:
         _status_ok(status)
     if torch.is_grad_enabled():
-        _no_grad(x, router, weights)
+        _no_grad(grid, down_grid, x, router, weights)
     dev = _home(x)
     if ids is None:
         ids = x.new_empty((T, k), dtype=torch.int32)

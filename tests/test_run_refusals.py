@@ -277,3 +277,24 @@ def test_moe_launches_fit_the_grid(measured):
     assert done > 200
     # 4,096 experts of 2^18 rows: 2^32 threads in a launch over whole rows
     assert moe(measured, E=4096, inter=1 << 18, T=700, wn=1 << 62) == -4
+
+
+@pytest.mark.parametrize("name", ["grid", "down_grid", "weights"])
+def test_codebooks_and_weights_have_no_backward_pass(api, name):
+    """The output depends on the codebooks as well: a gradient through them is refused, not dropped."""
+    kw = base_moe()
+    kw.update(down_grid=torch.zeros((256, 8)))
+    if name == "weights":
+        kw.update(router=None, top_k=None, ids=torch.zeros((3, 2), dtype=torch.int32), weights=torch.zeros((3, 2)))
+    kw[name].requires_grad_()
+    with pytest.raises(api.IQError, match="no backward pass"):
+        api.moe(**kw)
+    with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
+        api.moe(**kw)
+    if name == "grid":
+        kw = base_linear()
+        kw["grid"].requires_grad_()
+        with pytest.raises(api.IQError, match="no backward pass"):
+            api.linear(**kw)
+        with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
+            api.linear(**kw)
