@@ -14,6 +14,7 @@ import functools
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libiq.so")
@@ -513,10 +514,16 @@ def _addr(t, name: str, index: int):
 
 
 def _no_grad(*tensors):
-    """Encoded weights are frozen and the calls below have no backward pass: refused where one would be recorded."""
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise IQError("the call has no backward pass: tensors that require a gradient need torch.no_grad()")
+    """Encoded weights are frozen and the calls below have no derivatives: refused where one would be recorded, or
+    carried along in forward mode (which torch.no_grad() does not stop)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise IQError("the call has no backward pass: tensors that require a gradient need torch.no_grad()")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise IQError("the call has no forward-mode derivative: a tensor carries a tangent")
 
 
 def _scratch(nbytes: int, x: torch.Tensor, workspace):
@@ -572,8 +579,7 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
         _is(out, "out", (T, rows), dtype)
     if status is not None:
         _status_ok(status)
-    if torch.is_grad_enabled():
-        _no_grad(grid, x, lora_a, lora_b, lora_scale)
+    _no_grad(grid, x, lora_a, lora_b, lora_scale)
     dev = _home(x)
     if out is None:
         out = x.new_empty((T, rows))
@@ -640,8 +646,7 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
         _is(out, "out", (T, hidden), dtype)
     if status is not None:
         _status_ok(status)
-    if torch.is_grad_enabled():
-        _no_grad(grid, down_grid, x, router, weights)
+    _no_grad(grid, down_grid, x, router, weights)
     dev = _home(x)
     if ids is None:
         ids = x.new_empty((T, k), dtype=torch.int32)

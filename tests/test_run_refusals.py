@@ -298,3 +298,23 @@ def test_codebooks_and_weights_have_no_backward_pass(api, name):
             api.linear(**kw)
         with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
             api.linear(**kw)
+
+
+@pytest.mark.parametrize("call, name", [("linear", n) for n in ("grid", "x", "lora_a", "lora_b", "lora_scale")] +
+                         [("moe", n) for n in ("grid", "down_grid", "x", "router")])
+def test_forward_mode_tangents_are_refused(api, call, name):
+    """A dual tensor's tangent would be dropped: refused, under no_grad as well (which does not stop forward mode)."""
+    kw = base_linear() if call == "linear" else {**base_moe(), "down_grid": torch.zeros((256, 8))}
+    run = getattr(api, call)
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises(api.IQError, match="device tensors"):
+            run(**kw)
+        kw[name] = torch.autograd.forward_ad.make_dual(kw[name], torch.ones_like(kw[name]))
+        with pytest.raises(api.IQError, match="tangent"):
+            run(**kw)
+        with torch.no_grad(), pytest.raises(api.IQError, match="tangent"):
+            run(**kw)
+    if call == "linear":
+        kw = base_linear()
+        with pytest.raises(api.IQError, match="tangent"):
+            torch.func.jvp(lambda t: run(**{**kw, name: t}), (kw[name],), (torch.ones_like(kw[name]),))
