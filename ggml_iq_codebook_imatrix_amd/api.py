@@ -637,7 +637,7 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
             raise IQError("top_k must lie in 1 .. num_experts with a router")
     elif ids is None or weights is None:
         raise IQError("either router or ids and weights must be given")
-    k = int(ids.shape[1] if top_k is None and ids is not None and ids.dim() == 2 else top_k or 0)
+    k = int(top_k) if top_k is not None else _need(ids, "ids", (T, None)).shape[1]
     if ids is not None:
         _is(ids, "ids", (T, k), torch.int32)
     if weights is not None:

@@ -318,3 +318,13 @@ def test_forward_mode_tangents_are_refused(api, call, name):
         kw = base_linear()
         with pytest.raises(api.IQError, match="tangent"):
             torch.func.jvp(lambda t: run(**{**kw, name: t}), (kw[name],), (torch.ones_like(kw[name]),))
+
+
+@pytest.mark.parametrize("router", [True, False])
+def test_moe_ids_that_are_no_tensor(api, router):
+    for ids in ([[0, 1]] * 3, 7, torch.zeros((3, 2), dtype=torch.int32).numpy()):
+        kw = {**base_moe(), "ids": ids}
+        if not router:
+            kw.update(router=None, top_k=None, weights=torch.zeros((3, 2)))
+        with pytest.raises(api.IQError, match="ids must be a tensor"):
+            api.moe(**kw)
