@@ -579,7 +579,7 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
         _is(out, "out", (T, rows), dtype)
     if status is not None:
         _status_ok(status)
-    _no_grad(grid, x, lora_a, lora_b, lora_scale)
+    _no_grad(grid, x, lora_a, lora_b, lora_scale, out)
     dev = _home(x)
     if out is None:
         out = x.new_empty((T, rows))
@@ -646,7 +646,7 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
         _is(out, "out", (T, hidden), dtype)
     if status is not None:
         _status_ok(status)
-    _no_grad(grid, down_grid, x, router, weights)
+    _no_grad(grid, down_grid, x, router, weights, out)
     dev = _home(x)
     if ids is None:
         ids = x.new_empty((T, k), dtype=torch.int32)

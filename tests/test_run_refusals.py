@@ -328,3 +328,14 @@ def test_moe_ids_that_are_no_tensor(api, router):
             kw.update(router=None, top_k=None, weights=torch.zeros((3, 2)))
         with pytest.raises(api.IQError, match="ids must be a tensor"):
             api.moe(**kw)
+
+
+@pytest.mark.parametrize("call", ["linear", "moe"])
+def test_out_that_requires_a_gradient(api, call):
+    """A call into a tensor of a recorded graph would change it behind the graph's back."""
+    kw = base_linear() if call == "linear" else base_moe()
+    kw["out"] = torch.zeros((3, 48 if call == "linear" else 512), requires_grad=True)
+    with pytest.raises(api.IQError, match="no backward pass"):
+        getattr(api, call)(**kw)
+    with torch.no_grad(), pytest.raises(api.IQError, match="device tensors"):
+        getattr(api, call)(**kw)
