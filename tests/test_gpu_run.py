@@ -779,3 +779,77 @@ def test_moe_keeps_the_bits_of_h(api, orc, E, k, H, I, T, down_fmt, dtype):
     got, _, _ = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), dev(x, dtype), E, ids=dev(ids),
                         weights=dev(weights), down_fmt=down_fmt, down_grid=dev(dgrid))
     assert np.array_equal(f64(got), round_to(y, dtype))
+
+
+@pytest.mark.parametrize("T", [1, 20, 40, 300])
+def test_linear_wide_tokens(api, orc, T):
+    """bf16 tokens of more than 6,144 columns (float32: 2,048), which the conversion reads twice; the largest value in
+    each part of a row in turn."""
+    print("[case] linear wide", T, flush=True)
+    for fmt, dtype, nb in (("IQ2_XXS", torch.bfloat16, 25), ("IQ1_M", torch.bfloat16, 49), ("IQ2_S", torch.float32, 25)):
+        grid, p = inputs.grid_for(fmt, 41), payload(fmt, 40, nb, 1600 + nb)
+        x = dev(inputs.activations(T, nb * 256, 42, 43, bf16=False), dtype)
+        at = torch.arange(T, device="cuda") * 911 % (nb * 256)
+        at[0] = nb * 256 - 1
+        x[torch.arange(T, device="cuda"), at] = 1000.0
+        got, xd, w = f64(api.linear(fmt, dev(p), dev(grid), x)), f64(x), decoded(orc, fmt, p, grid)
+        y = xd @ w.T
+        assert np.all(np.abs(got - y) <= linear_tolerance(xd, w, dtype, y)), (fmt, dtype)
+        rel = np.linalg.norm(got - y) / np.linalg.norm(y)
+        assert rel < (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20)
+
+
+# Blocks of K as real layers have them.  Gate and up with K split over eight waves, some with a second block (1 and 16
+# tokens), whole rows of few tokens; down in more than one stage of h with one, two and four tiles of pairs
+DEEP_MOE = [("IQ2_XXS", 4, 2, 2304, 256, 1), ("IQ2_S", 4, 2, 4096, 512, 1), ("IQ1_M", 3, 2, 2304, 1280, 16),
+            ("IQ2_XS", 8, 2, 2304, 1280, 16), ("IQ1_S", 4, 1, 512, 2304, 20), ("IQ2_XS", 3, 2, 512, 1280, 25),
+            ("IQ2_XXS", 2, 2, 512, 2304, 60), ("IQ1_M", 2, 1, 4096, 512, 70)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt, E, k, H, I, T", DEEP_MOE)
+def test_moe_deep(api, orc, fmt, E, k, H, I, T, dtype):
+    test_moe_more_shapes(api, orc, fmt, E, k, H, I, T, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_moe_large_offsets(api, T):
+    """256 experts in payloads of more than 2^31 bytes each: the last one, against the same expert in a small layer."""
+    print("[case] moe large offsets", T, flush=True)
+    fmt, E, H, I = "IQ1_S", 256, 16384, 4096  # 3.4 GB each of gate, up and down
+    grid = dev(inputs.grid_for(fmt, 5))
+    one = [dev(payload(fmt, rows, nb, 1700 + n)) for n, (rows, nb) in enumerate([(I, H // 256), (I, H // 256), (H, I // 256)])]
+
+    def layer(experts):
+        out = []
+        for p in one:
+            full = torch.zeros((experts * p.shape[0], *p.shape[1:]), dtype=torch.uint8, device="cuda")
+            full[-p.shape[0]:] = p
+            out.append(full)
+        return out
+    big, small = layer(E), layer(5)
+    assert min(p.numel() for p in big) > 2 ** 31
+    x = dev(inputs.activations(T, H, 7, 8)).bfloat16()
+    ids = torch.full((T, 1), E - 1, dtype=torch.int32, device="cuda")
+    if T > 2:
+        ids[1] = 3  # an expert of zeros
+    weights = torch.full((T, 1), 0.5, device="cuda")
+    y, _, _ = api.moe(fmt, *big, grid, x, E, ids=ids, weights=weights)
+    want, _, _ = api.moe(fmt, *small, grid, x, 5, ids=torch.where(ids == E - 1, 4, ids), weights=weights)
+    assert torch.equal(y, want) and bool(y[0].isfinite().all()) and bool((y[0] != 0).any())
+    if T > 2:
+        assert bool((y[1] == 0).all())
+
+
+@pytest.mark.parametrize("rows, T", [(1100, 500), (2000, 1000), (4000, 1100), (8000, 1100)])
+def test_linear_wide_prompts(api, orc, rows, T):
+    """The kernels for prompts over 25 blocks of K."""
+    print("[case] linear wide prompts", rows, T, flush=True)
+    fmt, nb = "IQ2_XS", 25
+    grid, p = inputs.grid_for(fmt, 41), payload(fmt, rows, nb, 1800 + rows)
+    x = dev(inputs.activations(T, nb * 256, 42, 43, bf16=False), torch.bfloat16)
+    got, xd, w = f64(api.linear(fmt, dev(p), dev(grid), x)), f64(x), decoded(orc, fmt, p, grid)
+    y, S = xd @ w.T, np.abs(xd) @ np.abs(w).T
+    # sums that run through the whole of K, with a rescaling per block
+    assert np.all(np.abs(got - y) <= linear_tolerance(xd, w, torch.bfloat16, y) + nb * 258 * 2 * U * S)
+    assert np.linalg.norm(got - y) / np.linalg.norm(y) < 2.0 ** -8
