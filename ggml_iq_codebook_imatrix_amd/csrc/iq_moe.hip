@@ -65,9 +65,10 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 // The logits of 16 tokens and 16 experts on the fp64 matrix cores, K split over
 // ks workgroups (whose sums the choice adds) and each one's eight waves.  In fp64,
-// so that no order of summation can swap neighbours in the ranking (5.5 us for up to
-// 64 tokens by 128 experts of 2,048, 8 for 200: latency).  v_mfma_f64_16x16x4: lane l holds k = l / 16 of token (A) and
-// expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
+// so that the order of summation, which is the same for every expert, decides between
+// logits within some 2^-52 of their terms only (5.5 us for up to 64 tokens by 128
+// experts of 2,048, 8 for 200: latency).  v_mfma_f64_16x16x4: lane l holds k = l / 16
+// of token (A) and expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
 template <int P>
 __device__ __forceinline__ void route_logits(const MoeArgs &A, int64_t w, double *s_red) {
   constexpr int U = 4;  // loads in flight
@@ -499,7 +500,7 @@ __device__ __forceinline__ void for_pairs(const MoeArgs &A, int e, PairWalk<N> &
 // of K.  The pairs' tokens come through LDS, KC blocks at a time for all waves;
 // a wave keeps the payload of the next two blocks on its way in registers (with
 // one, waiting for HBM was a third of the time).  64 tokens through 128 experts of
-// 2,048 x 768, IQ2_XXS: 51 us for 50 MB of payload (1.0 TB/s).  The decode bounds it:
+// 2,048 x 768, IQ2_XXS: 51 us for 102 MB of payload (2.0 TB/s).  The decode bounds it:
 // 19,400 vector instructions a SIMD at 4.9 cycles are 0.85 of its time, LDS is busy
 // 0.45 of it.  Sharing the blocks of K between the waves instead took 119 us: every
 // wave then reads all tokens from memory.
@@ -765,7 +766,8 @@ __global__ void __launch_bounds__(256) sum_kernel(MoeArgs A) {
 // unless another layer is named.
 //
 // Few tokens name few experts: a workgroup per chosen expert, not per expert (1
-// token 26 us and 49, 8 tokens 59 and 71, 16 tokens 73 and 84).
+// token 26 us and 49, 8 tokens 59 and 71, 16 tokens 73 and 84).  Past 256 experts a
+// launch takes all of them (1 token: 256 experts 32 us, 512 127).
 bool is_few(int64_t T, int E) { return T <= kFewTokens && E <= kFewExperts; }
 // A wave picks a token's experts in 2 us, a launch for it takes 4 to 5 and as much
 // of the host's time: picked in the next kernel while its eight waves do it in one
@@ -781,7 +783,9 @@ bool split_up(const MoeArgs &A) { return is_few(A.T, A.E) && reached(A.npair, A.
 // a wave converts every pair's block, so while these are few: 16 of them (16
 // experts of 1,024 x 512, 4 tokens) 23 us and 26 with whole rows, 24 29 and 34, 48
 // 41 and 40, 72 52 and 46.  The IQ1 codebooks leave LDS for half the waves: 16 of
-// them 27 and 27, 24 34 and 35, 48 48 and 41.
+// them 27 and 27, 24 34 and 35, 48 48 and 41.  Whole rows of few large experts leave
+// CUs without work: two of eight experts of 4,096 x 14,336, one token, are 32
+// workgroups, and the layer takes 174 us for 90 MB of payload.
 bool split_down(int64_t T, int E, int top_k, int64_t inter, int down_fmt) {
   return is_few(T, E) && T * top_k * (inter / 256) <= (down_split_waves(down_fmt) == 4 ? 24 : 48);
 }

@@ -48,8 +48,9 @@ inline int run_check_ws(size_t need, const void *ws, size_t have) {
 
 // Tokens in fp16: x16 [block][tile of 16 tokens][part][step 0..7][lane][8], the
 // A operand of a step as 1 KiB of consecutive memory; ex [tokens]: the power of
-// two that undoes a token's scaling.  What lies past the last token is left
-// unwritten and not read.
+// two that undoes a token's scaling.  Rows past the last token are left unwritten;
+// kernels that take whole tiles read them, and since a row of A gives a row of D, they
+// reach only outputs that are not stored.
 struct Tokens {
   _Float16 *x16;
   int32_t *ex;

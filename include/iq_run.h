@@ -15,7 +15,8 @@
  *  - m * (codebook value) is formed in fp16.  It is exact when the value has at
  *    most 6 significant bits (IQ2; IQ1: value +- 1/8 at most 7), as {1,3,5} and
  *    {-1,0,1} have; any other codebook is rounded to fp16, and the product again
- *    (relative 2^-11 each), and IQ_STATUS_ROUNDED is raised.
+ *    (relative 2^-11 each; in steps of 2^-24 below 2^-14, infinite past 65,504),
+ *    and IQ_STATUS_ROUNDED is raised.
  *  - each token is scaled by the power of two that brings its largest finite
  *    magnitude under 2^15 and held in fp16: exact for bf16 tokens (what lies 2^-29
  *    or more below the token's largest value is rounded by less than 2^-39 of it);
@@ -96,9 +97,11 @@ int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int
  *           where both are the same).
  *  x        (device) [T, hidden] tokens, dtype f32 or bf16.
  *  router   (device, nullable) [num_experts, hidden], router_dtype f32 or bf16.
- *           Given: ids and weights are OUT.  Logits are accumulated in fp64, so
- *           the choice does not depend on an order of summation; equal logits
- *           take the lower id first, NaN logits come after all others.
+ *           Given: ids and weights are OUT.  Logits are accumulated in fp64, in
+ *           the same order for every expert: those further apart than that
+ *           rounds (some 2^-52 of their terms' sum) are ranked as exact ones are,
+ *           equal rows of the router tie.  Equal logits take the lower id first,
+ *           NaN logits come after all others.
  *           NULL: ids and weights are the caller's (any other routing); an id
  *           outside [0, num_experts) raises IQ_STATUS_BADID and adds nothing, an
  *           id repeated in one token counts per occurrence.
