@@ -853,3 +853,81 @@ def test_linear_wide_prompts(api, orc, rows, T):
     # sums that run through the whole of K, with a rescaling per block
     assert np.all(np.abs(got - y) <= linear_tolerance(xd, w, torch.bfloat16, y) + nb * 258 * 2 * U * S)
     assert np.linalg.norm(got - y) / np.linalg.norm(y) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("r", [100, 513, 1024])
+def test_linear_large_ranks(api, orc, r, dtype):
+    fmt, nb, N = "IQ2_XXS", 3, 2
+    for rows, T in ((40, 1), (70, 45), (1100, 500)):
+        print("[case] linear large ranks", r, dtype, rows, T, flush=True)
+        g = inputs.rng(r + T)
+        grid, p = inputs.grid_for(fmt, 41), payload(fmt, rows, nb, 1900 + r)
+        x = dev(inputs.activations(T, nb * 256, 42, 43, bf16=False), dtype)
+        a = dev(g.standard_normal((N, r, nb * 256), dtype=np.float32) * 0.02, dtype)
+        b = dev(g.standard_normal((N, rows, r), dtype=np.float32) * 0.02, dtype)
+        ids = g.integers(-1, N, T).astype(np.int32)
+        ids[0] = 1
+        got = f64(api.linear(fmt, dev(p), dev(grid), x, lora_a=a, lora_b=b, lora_ids=dev(ids)))
+        xd, w = f64(x), decoded(orc, fmt, p, grid)
+        y, more = xd @ w.T, nb * 258 * 2 * U * (np.abs(xd) @ np.abs(w).T)
+        for n in range(N):
+            at = ids == n
+            y[at] += (xd[at] @ f64(a)[n].T) @ f64(b)[n].T
+            # K additions for v; r more for its product with B, each of three parts
+            more[at] += (nb * 256 + 3 * r + 8) * 2 * U * ((np.abs(xd[at]) @ np.abs(f64(a)[n]).T) @ np.abs(f64(b)[n]).T)
+        assert np.all(np.abs(got - y) <= linear_tolerance(xd, w, dtype, y) + more), (rows, T)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows, T", [(50, 3), (50, 40), (1100, 500), (2000, 1000), (4000, 1100)])
+def test_linear_small_values_beside_a_large_one(api, orc, rows, T, dtype):
+    """A token's largest value meets a block of zero scale; the rest, 2^-30 and 2^-38 of it, are integers whose sums
+    float32 holds exactly: multiples of 2^-24 in fp16 under the token's power of two, subnormal ones included."""
+    print("[case] linear small beside large", rows, T, dtype, flush=True)
+    for fmt in ("IQ2_XS", "IQ1_M"):
+        nb = 3
+        g = inputs.rng(rows + T)
+        grid = inputs.grid_for(fmt, 5)
+        d = np.full((rows, nb), 0x2000)  # 2^-7
+        d[:, 0] = 0
+        p = payload(fmt, rows, nb, 2000 + rows, d16=d)
+        x = g.integers(-8, 9, (T, nb * 256)).astype(np.float32)
+        x[:, 17] = np.where(np.arange(T) % 2, np.float32(2.0 ** 30), np.float32(2.0 ** 38))
+        w = decoded(orc, fmt, p, grid)
+        y, size = x.astype(np.float64) @ w.T, np.abs(x[:, 256:]).astype(np.float64) @ np.abs(w[:, 256:]).T
+        assert size.max() < 2.0 ** 13  # in steps of 2^-10: every partial sum is exact
+        got = api.linear(fmt, dev(p), dev(grid), dev(x, dtype))
+        assert np.array_equal(f64(got), round_to(y, dtype)), fmt
+
+
+@pytest.mark.parametrize("T", [7, 16, 40])
+def test_moe_more_choices_than_experts(api, orc, T):
+    """The caller's routing may name 64 experts a token of a layer of two."""
+    print("[case] moe repeats", T, flush=True)
+    for fmt, dtype in (("IQ2_S", torch.bfloat16), ("IQ1_S", torch.float32)):
+        E, k, H, I = 2, 64, 512, 256
+        grid, _, gate, up, down, x, _ = moe_inputs(fmt, fmt, E, H, I, T, dtype, 2100)
+        g = inputs.rng(2101)
+        ids = g.integers(0, E, (T, k)).astype(np.int32)
+        ids[0] = 1
+        weights = (g.random((T, k)) / k).astype(np.float32)
+        y, _, _ = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, ids=dev(ids), weights=dev(weights))
+        ref, tol = moe_reference(orc, fmt, fmt, E, H, I, grid, grid, gate, up, down, f64(x), ids, weights, dtype)
+        assert np.all(np.abs(f64(y) - ref) <= tol)
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_moe_router_of_another_type(api, T):
+    """float32 tokens with a bf16 router: the choice and its weights as 64 bits have them."""
+    print("[case] moe router type", T, flush=True)
+    fmt, E, k, H, I = "IQ2_XXS", 30, 4, 1024, 256
+    grid, _, gate, up, down, x, router = moe_inputs(fmt, fmt, E, H, I, T, torch.float32, 2200, torch.bfloat16)
+    y, ids, weights = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, router=router, top_k=k)
+    logits = f64(x) @ f64(router).T
+    want = np.argsort(-logits, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(ids.cpu().numpy(), want)
+    p = np.take_along_axis(np.exp(logits - logits.max(1, keepdims=True)), want, 1)
+    assert np.allclose(f64(weights), p / p.sum(1, keepdims=True), rtol=2.0 ** -17, atol=0)
+    y2, _, _ = api.moe(fmt, dev(gate), dev(up), dev(down), dev(grid), x, E, ids=ids, weights=weights)
+    assert torch.equal(y, y2)
