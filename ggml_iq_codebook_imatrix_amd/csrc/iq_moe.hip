@@ -65,8 +65,8 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 // The logits of 16 tokens and 16 experts on the fp64 matrix cores, K split over
 // ks workgroups (whose sums the choice adds) and each one's eight waves.  In fp64,
-// so that the order of summation, which is the same for every expert, decides between
-// logits within some 2^-52 of their terms only (5.5 us for up to 64 tokens by 128
+// so that the order of summation, which is the same for every expert, decides only
+// between logits within 2 hidden 2^-53 of their terms' sum (5.5 us for up to 64 tokens by 128
 // experts of 2,048, 8 for 200: latency).  v_mfma_f64_16x16x4: lane l holds k = l / 16
 // of token (A) and expert (B) l % 16; D has lane l hold expert l % 16 and tokens l / 16 + 4 i.
 template <int P>

@@ -98,10 +98,10 @@ int iq_linear_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int
  *  x        (device) [T, hidden] tokens, dtype f32 or bf16.
  *  router   (device, nullable) [num_experts, hidden], router_dtype f32 or bf16.
  *           Given: ids and weights are OUT.  Logits are accumulated in fp64, in
- *           the same order for every expert: those further apart than that
- *           rounds (some 2^-52 of their terms' sum) are ranked as exact ones are,
- *           equal rows of the router tie.  Equal logits take the lower id first,
- *           NaN logits come after all others.
+ *           the same order for every expert: those further apart than that can
+ *           round (2 hidden 2^-53 of the sum of |x R|) are ranked as exact ones
+ *           are, equal rows of the router tie.  Equal logits take the lower id
+ *           first, NaN logits come after all others.
  *           NULL: ids and weights are the caller's (any other routing); an id
  *           outside [0, num_experts) raises IQ_STATUS_BADID and adds nothing, an
  *           id repeated in one token counts per occurrence.
