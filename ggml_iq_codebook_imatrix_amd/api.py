@@ -1,4 +1,4 @@
-"""Thin Python binding of libiq.so (see include/iq.h and include/iq_run.h).
+"""Thin Python binding of libiq.so (see include/iq.h, include/iq_run.h and include/iq_train.h).
 
 Argument marshalling only: every step runs in the HIP library.  Each wrapper
 checks the shape, dtype and device of every tensor it is given (IQError before
@@ -53,6 +53,16 @@ SIGNATURES = {
     "iq_moe_workspace_size": ([_I, _I, _I64, _I64, _I, _I, _I64, _I, _P], _I),
     "iq_moe": ([_I, _I, _P, _P, _P, _I64, _I64, _I, _P, _P, _P, _I, _I64, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P,
                 _P], _I),
+    # include/iq_train.h
+    "iq_checkpoint": ([_P, _I, _I64, _I64, _P, _P, _P, _P], _I),
+    "iq_restore": ([_P, _P, _I64, _I64, _P, _I, _P], _I),
+    "iq_glu_workspace_size": ([_I, _I64, _I64, _I, _I64, _P], _I),
+    "iq_glu": ([_I, _P, _P, _I64, _I64, _P, _P, _I, _I64, _I, _P, _P, _SZ, _P, _P], _I),
+    "iq_glu_backward_workspace_size": ([_I, _I64, _I64, _I, _I64, _P], _I),
+    "iq_glu_backward": ([_I, _P, _P, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I, _P, _P, _SZ, _P, _P], _I),
+    "iq_linear_backward_workspace_size": ([_I, _I64, _I64, _I, _I64, _I, _I, _P], _I),
+    "iq_linear_backward": ([_I, _P, _I64, _I64, _P, _P, _P, _P, _I, _I64, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _SZ,
+                            _P, _P], _I),
 }
 
 
@@ -514,8 +524,9 @@ def _addr(t, name: str, index: int):
 
 
 def _no_grad(*tensors):
-    """Encoded weights are frozen and the calls below have no derivatives: refused where one would be recorded, or
-    carried along in forward mode (which torch.no_grad() does not stop)."""
+    """Encoded weights are frozen and the calls below record no derivatives (their backward passes are calls of their
+    own): refused where one would be recorded, or carried along in forward mode (which torch.no_grad() does not
+    stop)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -665,3 +676,227 @@ def moe(fmt, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, grid: tor
     if rc:
         _check(rc, "iq_moe")
     return out, ids, weights
+
+
+# --------------------------------------------------------------------------
+# Adapting a model whose weights stay encoded (include/iq_train.h)
+# --------------------------------------------------------------------------
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _activation(name) -> int:
+    act = ACTIVATIONS.get(name) if isinstance(name, str) else None
+    if act is None:
+        raise IQError(f"unknown activation {name!r}")
+    return act
+
+
+def _tokens(x, name: str, cols):
+    """Shape (T, cols) and dtype of a tensor of tokens; cols None: any."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in DTYPE or x.shape[1] != cols:
+        _need(x, name, (None, cols), tuple(DTYPE))
+    return x.shape[0], x.shape[1], x.dtype
+
+
+def _kept(x, T: int, cols: int, dtype):
+    """The data and exponents of tokens kept for the backward pass: a tensor [T, cols] of dtype, or the
+    (codes, exponents) that checkpoint() returned for one."""
+    if isinstance(x, (tuple, list)):
+        if len(x) != 2:
+            raise IQError("a checkpoint is a pair of codes and exponents")
+        _is(x[0], "codes", (T, cols), torch.int8)
+        _is(x[1], "exponents", (T, -(-cols // 32)), torch.uint8)
+        return x[0], x[1]
+    _is(x, "x", (T, cols), dtype)
+    return x, None
+
+
+def checkpoint(x: torch.Tensor, codes: torch.Tensor | None = None, exponents: torch.Tensor | None = None,
+               status: torch.Tensor | None = None):
+    """Activations x [T, cols] in 8 bits: (codes [T, cols] int8, exponents [T, ceil(cols/32)] uint8), a value being
+    code * 2^(exponent - 133).  Code -128 stands for an infinity or NaN."""
+    T, cols, dtype = _tokens(x, "x", None)
+    if codes is not None:
+        _is(codes, "codes", (T, cols), torch.int8)
+    if exponents is not None:
+        _is(exponents, "exponents", (T, -(-cols // 32)), torch.uint8)
+    if status is not None:
+        _status_ok(status)
+    _no_grad(x)
+    dev = _home(x)
+    if codes is None:
+        codes = x.new_empty((T, cols), dtype=torch.int8)
+    if exponents is None:
+        exponents = x.new_empty((T, -(-cols // 32)), dtype=torch.uint8)
+    rc = lib().iq_checkpoint(_addr(x, "x", dev), DTYPE[dtype], T, cols, _addr(codes, "codes", dev),
+                             _addr(exponents, "exponents", dev), _addr(status, "status", dev),
+                             torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "iq_checkpoint")
+    return codes, exponents
+
+
+def restore(codes: torch.Tensor, exponents: torch.Tensor, dtype=torch.float32,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of a checkpoint, [T, cols] of dtype (or of out's); exact in either."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2 or codes.dtype is not torch.int8:
+        _need(codes, "codes", (None, None), torch.int8)
+    T, cols = codes.shape
+    _is(exponents, "exponents", (T, -(-cols // 32)), torch.uint8)
+    if out is not None:
+        _need(out, "out", (T, cols), tuple(DTYPE))
+    elif dtype not in DTYPE:
+        raise IQError(f"unsupported output dtype {dtype}")
+    _no_grad(out)
+    dev = _home(codes)
+    if out is None:
+        out = codes.new_empty((T, cols), dtype=dtype)
+    rc = lib().iq_restore(_addr(codes, "codes", dev), _addr(exponents, "exponents", dev), T, cols,
+                          _addr(out, "out", dev), DTYPE[out.dtype], torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "iq_restore")
+    return out
+
+
+def glu_workspace_size(fmt, inter: int, hidden: int, dtype, T: int) -> int:
+    if dtype not in DTYPE:
+        raise IQError(f"unsupported dtype {dtype}")
+    return _run_size("iq_glu_workspace_size", _fmt(fmt), int(inter), int(hidden), DTYPE[dtype], int(T))
+
+
+def glu_backward_workspace_size(fmt, inter: int, hidden: int, dtype, T: int) -> int:
+    if dtype not in DTYPE:
+        raise IQError(f"unsupported dtype {dtype}")
+    return _run_size("iq_glu_backward_workspace_size", _fmt(fmt), int(inter), int(hidden), DTYPE[dtype], int(T))
+
+
+def _glu_args(fmt, gate, up, grid, activation):
+    f = _fmt(fmt)
+    entries, nbytes = _geometry(f)
+    inter, nb, _ = _ends(gate, "gate", (None, None, nbytes), torch.uint8)
+    _is(up, "up", (inter, nb, nbytes), torch.uint8)
+    _is(grid, "grid", (entries, 8), torch.float32)
+    return f, inter, nb * 256, _activation(activation)
+
+
+def glu(fmt, gate: torch.Tensor, up: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, activation: str = "silu",
+        out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A gated feed-forward block's first half on encoded weights gate, up [inter, hidden/256, block_bytes]:
+    act(x gate^T) * (x up^T) for tokens x [T, hidden] -> [T, inter], of x's dtype.  activation: "silu", "gelu" or
+    "gelu_tanh".  linear() is the second half; glu_backward() the backward pass."""
+    f, inter, hidden, act = _glu_args(fmt, gate, up, grid, activation)
+    T, _, dtype = _tokens(x, "x", hidden)
+    if out is not None:
+        _is(out, "out", (T, inter), dtype)
+    if status is not None:
+        _status_ok(status)
+    _no_grad(grid, x, out)
+    dev = _home(x)
+    if out is None:
+        out = x.new_empty((T, inter))
+    dt = DTYPE[dtype]
+    ws, wp, wn = _scratch(_run_size("iq_glu_workspace_size", f, inter, hidden, dt, T), x, workspace)
+    rc = lib().iq_glu(f, _addr(gate, "gate", dev), _addr(up, "up", dev), inter, hidden, _addr(grid, "grid", dev),
+                      _addr(x, "x", dev), dt, T, act, _addr(out, "out", dev), wp, wn, _addr(status, "status", dev),
+                      torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "iq_glu")
+    return out
+
+
+def glu_backward(fmt, gate: torch.Tensor, up: torch.Tensor, grid: torch.Tensor, x, dh: torch.Tensor,
+                 activation: str = "silu", out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient [T, hidden] by glu()'s x, from dh [T, inter], the gradient by its result.  x: the tokens, or the
+    (codes, exponents) that checkpoint() made of them."""
+    f, inter, hidden, act = _glu_args(fmt, gate, up, grid, activation)
+    T, _, dtype = _tokens(dh, "dh", inter)
+    x, exponents = _kept(x, T, hidden, dtype)
+    if out is not None:
+        _is(out, "out", (T, hidden), dtype)
+    if status is not None:
+        _status_ok(status)
+    _no_grad(grid, x, dh, out)
+    dev = _home(dh)
+    if out is None:
+        out = dh.new_empty((T, hidden))
+    dt = DTYPE[dtype]
+    ws, wp, wn = _scratch(_run_size("iq_glu_backward_workspace_size", f, inter, hidden, dt, T), dh, workspace)
+    rc = lib().iq_glu_backward(f, _addr(gate, "gate", dev), _addr(up, "up", dev), inter, hidden,
+                               _addr(grid, "grid", dev), _addr(x, "x", dev), _addr(exponents, "exponents", dev),
+                               _addr(dh, "dh", dev), dt, T, act, _addr(out, "out", dev), wp, wn,
+                               _addr(status, "status", dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "iq_glu_backward")
+    return out
+
+
+def linear_backward_workspace_size(fmt, rows: int, cols: int, dtype, T: int, num_adapters: int = 0,
+                                   rank: int = 0) -> int:
+    if dtype not in DTYPE:
+        raise IQError(f"unsupported dtype {dtype}")
+    return _run_size("iq_linear_backward_workspace_size", _fmt(fmt), int(rows), int(cols), DTYPE[dtype], int(T),
+                     int(num_adapters), int(rank))
+
+
+def linear_backward(fmt, packed: torch.Tensor, grid: torch.Tensor, dy: torch.Tensor, x=None,
+                    lora_a: torch.Tensor | None = None, lora_b: torch.Tensor | None = None,
+                    lora_scale: torch.Tensor | None = None, lora_ids: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, grad_a: torch.Tensor | None = None,
+                    grad_b: torch.Tensor | None = None, need_dx: bool = True, status: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None):
+    """The backward pass of linear(): from dy [T, rows], the gradient by its result, the gradient dx [T, cols] by its
+    tokens; with adapters (as linear() takes them, and x, the tokens or the (codes, exponents) that checkpoint() made
+    of them) the tuple (dx, gradient by lora_a, gradient by lora_b).  need_dx=False leaves dx out (None)."""
+    f = _fmt(fmt)
+    entries, nbytes = _geometry(f)
+    rows, nb, _ = _ends(packed, "packed", (None, None, nbytes), torch.uint8)
+    cols = nb * 256
+    _is(grid, "grid", (entries, 8), torch.float32)
+    T, _, dtype = _tokens(dy, "dy", rows)
+    N = rank = 0
+    exponents = None
+    if lora_a is not None:
+        N, rank, _ = _ends(lora_a, "lora_a", (None, None, cols), dtype)
+        if N < 1 or rank < 1:
+            raise IQError("lora_a holds no adapter")
+        _is(lora_b, "lora_b", (N, rows, rank), dtype)
+        if lora_scale is not None:
+            _is(lora_scale, "lora_scale", (N,), torch.float32)
+        _is(lora_ids, "lora_ids", (T,), torch.int32)
+        x, exponents = _kept(x, T, cols, dtype)
+        if grad_a is not None:
+            _is(grad_a, "grad_a", (N, rank, cols), dtype)
+        if grad_b is not None:
+            _is(grad_b, "grad_b", (N, rows, rank), dtype)
+    else:
+        if any(t is not None for t in (lora_b, lora_scale, lora_ids, grad_a, grad_b)):
+            raise IQError("lora_b, lora_scale, lora_ids, grad_a and grad_b need lora_a")
+        x = None
+    if out is not None:
+        if not need_dx:
+            raise IQError("out is given, but dx is not wanted")
+        _is(out, "out", (T, cols), dtype)
+    if status is not None:
+        _status_ok(status)
+    _no_grad(grid, dy, x, lora_a, lora_b, lora_scale, out, grad_a, grad_b)
+    dev = _home(dy)
+    if out is None and need_dx:
+        out = dy.new_empty((T, cols))
+    if N:
+        if grad_a is None:
+            grad_a = torch.empty_like(lora_a)
+        if grad_b is None:
+            grad_b = torch.empty_like(lora_b)
+    dt = DTYPE[dtype]
+    ws, wp, wn = _scratch(_run_size("iq_linear_backward_workspace_size", f, rows, cols, dt, T, N, rank), dy, workspace)
+    rc = lib().iq_linear_backward(f, _addr(packed, "packed", dev), rows, cols, _addr(grid, "grid", dev),
+                                  _addr(dy, "dy", dev), _addr(x, "x", dev), _addr(exponents, "exponents", dev), dt, T,
+                                  _addr(lora_a, "lora_a", dev), _addr(lora_b, "lora_b", dev),
+                                  _addr(lora_scale, "lora_scale", dev), _addr(lora_ids, "lora_ids", dev), N, rank,
+                                  _addr(out, "out", dev), _addr(grad_a, "grad_a", dev), _addr(grad_b, "grad_b", dev),
+                                  wp, wn, _addr(status, "status", dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "iq_linear_backward")
+    return (out, grad_a, grad_b) if N else out

@@ -1,0 +1,506 @@
+// iq_backward.hip -- iq_linear_backward: the gradients by an encoded projection's
+// tokens and by its low-rank adapters (include/iq_train.h).
+//
+// Launches: dy into operand order, with the bound on the weights and B with its rows
+// in line; the rank-wide products p = s dy B and v = s x A^T; dx (iq_rows.hip, with
+// p A added to its sums); and dA, dB as sums over the tokens.
+
+#include "iq_train.hpp"
+
+namespace iq {
+namespace {
+
+struct Adapters {
+  const void *a, *b;
+  const float *scale;
+  const int32_t *ids;
+  int n, rank;
+};
+
+struct BackPrepArgs {
+  const void *dy;
+  int dtype, fmt, bytes;
+  int64_t T, rows, nb, nconv;
+  const uint8_t *packed;
+  Grads G;
+  Bound B;
+  Codebooks books;
+  int convert;  // dx is wanted
+  Adapters L;
+  void *bt;      // B [adapter][rank][rowpad], of dtype
+  int64_t rowpad;
+};
+
+// One wave brings one token's gradient into the order of Grads.
+template <int P>
+__device__ __forceinline__ void convert_grad(const BackPrepArgs &A, int64_t t, int lane) {
+  const int n = 141 - static_cast<int>(row_exponent(A.dy, A.dtype, A.rows, t, lane));
+  const int64_t all = row_chunks(A.rows) * 64;
+  for (int64_t r = lane * 8; r < all; r += 512) {
+    float v[8];
+    if (r + 8 <= A.rows) {
+      load8u(A.dy, A.dtype, t * A.rows + r, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = r + j < A.rows ? load1(A.dy, A.dtype, t * A.rows + r + j) : 0.0f;
+    }
+    half8v hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      _Float16 x, y;
+      to_parts(v[j], n, x, y);
+      hi[j] = x;
+      lo[j] = y;
+    }
+    const int in = static_cast<int>(r & 63);
+    _Float16 *to = A.G.g16 + ((r >> 6) * A.G.ntile + (t >> 4)) * P * 1024 +
+                   ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8;
+    *reinterpret_cast<half8v *>(to) = hi;
+    if (P == 2) *reinterpret_cast<half8v *>(to + 1024) = lo;
+  }
+  if (lane == 0) A.G.ex[t] = -n;
+}
+
+template <int P> __global__ void __launch_bounds__(512) back_prep_kernel(BackPrepArgs A) {
+  __shared__ uint32_t s_red[8];
+  int64_t w = blockIdx.x;
+  if (A.convert) {
+    if (w < kScaleSlots) {
+      const uint8_t *const packed[2] = {A.packed, A.packed};
+      bound_scales(A.fmt, A.bytes, packed, 1, A.rows * A.nb, A.B, static_cast<int>(w), s_red);
+      return;
+    }
+    w -= kScaleSlots;
+    if (w < A.nconv) {
+      const int64_t t = w * 8 + (threadIdx.x >> 6);
+      if (t < A.T) convert_grad<P>(A, t, threadIdx.x & 63);
+      return;
+    }
+    w -= A.nconv;
+    if (w < A.books.wg[0]) {
+      convert_codebook(A.books, static_cast<int>(w));
+      bound_codebook(A.books, A.B, static_cast<int>(w), s_red);
+      return;
+    }
+    w -= A.books.wg[0];
+  }
+  // 512 rows of one adapter's B, turned; zeros past the last row
+  const int64_t per = (A.rowpad + 511) / 512, a = w / per, row = w % per * 512 + threadIdx.x;
+  if (row >= A.rowpad) return;
+  const int64_t from = (a * A.rows + min(row, A.rows - 1)) * A.L.rank, to = a * A.L.rank * A.rowpad + row;
+  for (int j = 0; j < A.L.rank; ++j) {
+    if (P == 1)
+      static_cast<uint16_t *>(A.bt)[to + j * A.rowpad] =
+          row < A.rows ? static_cast<const uint16_t *>(A.L.b)[from + j] : static_cast<uint16_t>(0);
+    else
+      static_cast<float *>(A.bt)[to + j * A.rowpad] = row < A.rows ? static_cast<const float *>(A.L.b)[from + j] : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rank-wide products
+// ---------------------------------------------------------------------------
+struct Shrink {
+  Source s;         // tokens [T, k]
+  int64_t k;
+  const void *w;    // [adapter][rank][kpad], of dtype; zeros past k
+  int64_t kpad;     // a multiple of 256
+  float *out;       // [ranks, in sixteens][tpad]
+};
+struct ShrinkArgs {
+  Shrink of[2];  // dy by B, x by A
+  int dtype;
+  int64_t T, tpad;
+  Adapters L;
+  int rtiles, slots;
+  int32_t *ids;  // OUT [tpad]: the tokens' adapters, -1 for none or another id
+  int32_t *status;
+};
+
+// Eight values of a source from column k on; past the row's end zeros.
+__device__ __forceinline__ void source8(const Source &s, int64_t cols, int64_t t, int64_t k, float v[8]) {
+  const int64_t at = t * cols + k;
+  if (s.ex) {  // whole blocks of 32
+    decode_codes(ldu<uint2>(static_cast<const int8_t *>(s.x) + at), s.ex[t * (cols >> 5) + (k >> 5)], v);
+  } else if (k + 8 <= cols) {
+    load8u(s.x, s.dtype, at, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k + j < cols ? load1(s.x, s.dtype, at + j) : 0.0f;
+  }
+}
+// The same in bf16, exact for bf16 tokens and checkpoints.
+__device__ __forceinline__ bf16x8 source8_bf16(const Source &s, int64_t cols, int64_t t, int64_t k) {
+  if (!s.ex && k + 8 <= cols) return ldu<bf16x8>(static_cast<const uint16_t *>(s.x) + t * cols + k);
+  float v[8];
+  source8(s, cols, t, k, v);
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+// 16 tokens (A) by 16 ranks (B) of the adapter of token `slot`, K split over the
+// eight waves; results of tokens with other adapters are dropped.
+__global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
+  __shared__ f32x4 s_red[8 * 64];
+  const int64_t tiles = (A.tpad >> 4) * A.rtiles;
+  int64_t w = blockIdx.x;
+  const int first = static_cast<int>(w / (2 * tiles));
+  w -= first * 2 * tiles;
+  const Shrink &S = A.of[w >= tiles ? 1 : 0];
+  const bool of_x = w >= tiles;
+  if (of_x) w -= tiles;
+  const int64_t tt = w / A.rtiles;
+  const int rt = static_cast<int>(w % A.rtiles);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, q = lane >> 4;
+  const int64_t mytok = tt * 16 + n;
+  int mine = -1;
+  if (mytok < A.T) {
+    const int id = A.L.ids[mytok];
+    if (id >= 0 && id < A.L.n)
+      mine = id;
+    else if (id != -1 && first == 0 && rt == 0 && !of_x && threadIdx.x < 16)
+      raise_status(A.status, ST_BADID);
+  }
+  if (first == 0 && rt == 0 && !of_x && threadIdx.x < 16) A.ids[mytok] = mine;
+  if (first == 0 && threadIdx.x < 256) {  // zeros for tokens without an adapter
+    const int tok = threadIdx.x & 15;
+    const uint32_t with = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xffffu;
+    if (!((with >> tok) & 1u)) S.out[(rt * 16 + (threadIdx.x >> 4)) * A.tpad + tt * 16 + tok] = 0.0f;
+  }
+  for (int slot = first; slot < 16; slot += A.slots) {
+    const int a = __builtin_amdgcn_readlane(mine, slot);
+    const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
+    if (a < 0 || (group & ((1u << slot) - 1u))) continue;  // done with an earlier token
+    const int64_t t = tt * 16 + (((group >> n) & 1u) ? n : slot);  // rows of other tokens read this one's
+    const int64_t wr = (static_cast<int64_t>(a) * A.L.rank + min(rt * 16 + n, A.L.rank - 1)) * S.kpad;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t k = wave * 32 + q * 8; k < S.kpad; k += 256) {
+      if (A.dtype == 1) {
+        const bf16x8 x = source8_bf16(S.s, S.k, t, k);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ldu<bf16x8>(static_cast<const uint16_t *>(S.w) + wr + k), acc,
+                                                      0, 0, 0);
+      } else {
+        float x[8], b[8];
+        source8(S.s, S.k, t, k, x);
+        load8u(S.w, 0, wr + k, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], b[i], acc, 0, 0, 0);
+      }
+    }
+    const float scale = A.L.scale ? A.L.scale[a] : 1.0f;
+    const Split P{8, 1, wave, 0};
+    reduce_split<1, 1>(&acc, s_red, P, [&](int, int, int l, const f32x4 &s) {
+      const int j = rt * 16 + (l & 15);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (l >> 4) * 4 + i;
+        if ((group >> tok) & 1u) S.out[j * A.tpad + tt * 16 + tok] = j < A.L.rank ? s[i] * scale : 0.0f;
+      }
+    });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients by the adapters: sums over the tokens
+// ---------------------------------------------------------------------------
+struct Outer {
+  Source s;        // [T, k]
+  int64_t k, blocks;  // workgroups' columns: 128 each
+  const float *w;  // [ranks, in sixteens][tpad]
+  void *out;       // by rank: [adapter][rank][k]; else [adapter][k][rank]
+  int by_rank;
+};
+struct OuterArgs {
+  Outer of[2];
+  int64_t T, tpad;
+  int dtype, rank;
+  const int32_t *ids;  // [tpad]
+};
+
+// The first of a lane's eight columns: the last lanes of a row overlap, so that every load is whole.
+__device__ __forceinline__ int64_t outer_col(const Outer &O, int64_t blk, int m) {
+  return max(min(blk * 128 + m * 8, O.k - 8), static_cast<int64_t>(0));
+}
+
+// out[j][c] = sum of w[j][t] s[t][c] over adapter n's tokens: 128 columns (A, eight a
+// lane, brought from eight tokens each into operands by byte permutations) by 16 RT
+// ranks (B), the tokens in steps of 32 dealt to eight waves.  w is the sum of three
+// bf16 values.  f32 tokens go through the fp32 cores.
+template <int RT>
+__global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
+  __shared__ f32x4 s_red[8 * 4 * 64];
+  __shared__ float s_out[16][132];
+  const bool second = blockIdx.x >= A.of[0].blocks;
+  const Outer &O = A.of[second ? 1 : 0];
+  const int64_t blk = blockIdx.x - (second ? A.of[0].blocks : 0);
+  const int a = blockIdx.y, rt0 = blockIdx.z * RT;
+  const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = outer_col(O, blk, m);
+  const bool plain = !O.s.ex && O.s.dtype == IQ_DTYPE_F32;
+  f32x4 acc[RT][8];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[r][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const float *wr[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) wr[r] = O.w + (static_cast<int64_t>(rt0 + r) * 16 + m) * A.tpad;
+  for (int64_t t0 = wave * 32; t0 < A.tpad; t0 += 256) {
+    if (!__ballot(A.ids[t0 + (lane & 31)] == a)) continue;
+    if (plain) {
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int64_t t = t0 + 4 * s + q;
+        const bool mine = A.ids[t] == a;  // false past the last token
+        float x[8];
+        if (O.k >= 8) {
+          load8u(O.s.x, 0, (mine ? t : 0) * O.k + c0, x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = j < O.k ? load1(O.s.x, 0, (mine ? t : 0) * O.k + j) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = mine ? x[j] : 0.0f;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float w = mine ? wr[r][t] : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], w, acc[r][j], 0, 0, 0);
+        }
+      }
+      continue;
+    }
+    u32x4 x[8];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t t = t0 + 8 * q + i;
+      const bool is = A.ids[t] == a;
+      mine |= static_cast<uint32_t>(is) << i;
+      if (O.k >= 8) {
+        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, is ? t : 0, c0));
+      } else {
+        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, is ? t : 0, 0));
+      }
+      if (!is) x[i] = u32x4{0, 0, 0, 0};
+    }
+    bf16x8 w[RT][3];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float f[8];
+      load8u(wr[r], 0, t0 + 8 * q, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v = (mine >> i) & 1u ? f[i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+          w[r][k][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
+          v = finite_f(v) ? v - __uint_as_float(top) : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_perm(x[2 * i + 1][j >> 1], x[2 * i][j >> 1], sel);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, o), w[r][k], acc[r][j], 0, 0, 0);
+    }
+  }
+  const Split P{8, 1, wave, 0};
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    // lane l: rank l % 16, columns j of lanes 4 (l / 16) + 0..3
+    reduce_split<8, 4>(acc[r], s_red, P, [&](int, int j, int l, const f32x4 &s) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s_out[l & 15][((l >> 4) * 4 + k) * 8 + j] = s[k];
+    });
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2048; i += 512) {
+      const int col = O.by_rank ? i & 127 : i >> 4, j = O.by_rank ? i >> 7 : i & 15, rank = (rt0 + r) * 16 + j;
+      const int64_t c = outer_col(O, blk, col >> 3) + (col & 7);
+      if (rank >= A.rank || c >= O.k) continue;
+      const int64_t at = O.by_rank ? (static_cast<int64_t>(a) * A.rank + rank) * O.k + c
+                                   : (static_cast<int64_t>(a) * O.k + c) * A.rank + rank;
+      store1(O.out, A.dtype, at, s_out[j][col]);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+struct BackPlan {
+  int64_t ntile, chunks, tpad, rowpad;
+  int rpad, splits;
+  size_t bo, go, geo, po, bto, pto, vto, ido, bytes;
+};
+BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n, int rank) {
+  BackPlan p{};
+  const size_t size = dtype == IQ_DTYPE_F32 ? 4 : 2;
+  p.ntile = (T + 15) / 16;
+  p.chunks = row_chunks(rows);
+  p.splits = rows_splits(T, cols, p.chunks, dtype);
+  p.bo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
+  p.go = p.bo + ws_up(kBoundBytes);
+  p.geo = p.go + ws_up(grads_bytes(p.chunks, p.ntile, dtype));
+  p.po = p.geo + ws_up(static_cast<size_t>(p.ntile) * 64);
+  p.bto = p.po + ws_up(rows_partial_bytes(T, cols, p.splits));
+  p.bytes = p.bto + kWsAlign;
+  if (!rank) return p;
+  p.tpad = (T + 31) / 32 * 32;
+  p.rowpad = (rows + 255) / 256 * 256;
+  p.rpad = (rank + 31) / 32 * 32;
+  p.pto = p.bto + ws_up(static_cast<size_t>(n) * rank * p.rowpad * size);
+  p.vto = p.pto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
+  p.ido = p.vto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
+  p.bytes = p.ido + ws_up(static_cast<size_t>(p.tpad) * 4) + kWsAlign;
+  return p;
+}
+
+int check_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n, int rank) {
+  if (run_bad_fmt(fmt)) return IQ_ERR_FMT;
+  if (run_bad_dtype(dtype)) return IQ_ERR_DTYPE;
+  if (rows < 0 || T < 0 || cols <= 0 || cols % 256 != 0) return IQ_ERR_SHAPE;
+  if (rows > (int64_t(1) << 24) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
+  if (rank < 0 || rank > 1024 || (rank && n < 1)) return IQ_ERR_ARG;
+  const int64_t ntile = (T + 15) / 16;
+  if (ntile > 4 * 65535 || (rank && n > 65535)) return IQ_ERR_SHAPE;  // grids of dx, of the adapters' gradients
+  if (T * (cols / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;    // the joining launch
+  if (rank && (ntile + 1) * 2 * ((rank + 15) / 16) >= kMaxWG) return IQ_ERR_SHAPE;
+  if (rank && (T + 7) / 8 + n * ((rows + 767) / 512) + 128 >= kMaxWG) return IQ_ERR_SHAPE;
+  return IQ_OK;
+}
+
+}  // namespace
+}  // namespace iq
+
+extern "C" {
+
+int iq_linear_backward_workspace_size(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int num_adapters,
+                                      int rank, size_t *bytes) {
+  const int rc = iq::check_back(fmt, rows, cols, dtype, T, num_adapters, rank);
+  if (rc != IQ_OK) return rc;
+  if (!bytes) return IQ_ERR_NULL;
+  *bytes = rows && T ? iq::plan_back(fmt, rows, cols, dtype, T, num_adapters, rank).bytes : 0;
+  return IQ_OK;
+}
+
+int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t cols, const float *grid,
+                       const void *dy, const void *x, const uint8_t *exponents, int dtype, int64_t T,
+                       const void *lora_a, const void *lora_b, const float *lora_scale, const int32_t *lora_ids,
+                       int num_adapters, int rank, void *dx, void *da, void *db, void *workspace,
+                       size_t workspace_bytes, int32_t *status, hipStream_t stream) {
+  using namespace iq;
+  int rc = check_back(fmt, rows, cols, dtype, T, num_adapters, rank);
+  if (rc != IQ_OK) return rc;
+  const bool empty = rows == 0 || T == 0;
+  const size_t size = dtype == IQ_DTYPE_F32 ? 4 : 2;
+  if (!grid || (rank && (!da || (rows && !db)))) return IQ_ERR_NULL;
+  if (!empty && (!packed || !dy || (rank && (!x || !lora_a || !lora_b || !lora_ids)))) return IQ_ERR_NULL;
+  if (empty) {
+    if (dx && (rc = launch_zero(dx, static_cast<size_t>(T) * cols * size, stream)) != IQ_OK) return rc;
+    if (!rank) return IQ_OK;
+    if ((rc = launch_zero(da, static_cast<size_t>(num_adapters) * rank * cols * size, stream)) != IQ_OK) return rc;
+    return launch_zero(db, static_cast<size_t>(num_adapters) * rank * rows * size, stream);
+  }
+  if (reinterpret_cast<uintptr_t>(packed) & 1) return IQ_ERR_ARG;
+  if (!dx && !rank) return IQ_OK;
+  const BackPlan P = plan_back(fmt, rows, cols, dtype, T, num_adapters, rank);
+  if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
+  char *base = ws_base(workspace);
+  _Float16 *tab = reinterpret_cast<_Float16 *>(base);
+  const Adapters L{lora_a, lora_b, lora_scale, lora_ids, rank ? num_adapters : 0, rank};
+  float *pt = reinterpret_cast<float *>(base + P.pto), *vt = reinterpret_cast<float *>(base + P.vto);
+  int32_t *ids = reinterpret_cast<int32_t *>(base + P.ido);
+  BackPrepArgs A{};
+  A.dy = dy;
+  A.dtype = dtype;
+  A.fmt = fmt;
+  A.bytes = block_bytes(fmt);
+  A.T = T;
+  A.rows = rows;
+  A.nb = cols / 256;
+  A.nconv = (T + 7) / 8;
+  A.packed = packed;
+  A.G = Grads{reinterpret_cast<_Float16 *>(base + P.go), reinterpret_cast<int32_t *>(base + P.geo), P.ntile};
+  A.books = one_codebook(fmt, grid, tab, status);
+  A.B = Bound{reinterpret_cast<uint32_t *>(base + P.bo), reinterpret_cast<uint32_t *>(base + P.bo) + kScaleSlots,
+              A.books.wg[0], fmt >= IQ1_S};
+  A.convert = dx != nullptr;
+  A.L = L;
+  A.bt = base + P.bto;
+  A.rowpad = P.rowpad;
+  const int64_t wgs = (dx ? kScaleSlots + A.nconv + A.books.wg[0] : 0) + L.n * ((P.rowpad + 511) / 512);
+  if (dtype == IQ_DTYPE_F32)
+    hipLaunchKernelGGL(back_prep_kernel<2>, dim3(static_cast<unsigned>(wgs)), dim3(512), 0, stream, A);
+  else
+    hipLaunchKernelGGL(back_prep_kernel<1>, dim3(static_cast<unsigned>(wgs)), dim3(512), 0, stream, A);
+  if (!run_launched()) return IQ_ERR_HIP;
+  if (rank) {
+    ShrinkArgs S{};
+    S.of[0] = Shrink{Source{dy, nullptr, dtype}, rows, A.bt, P.rowpad, pt};
+    S.of[1] = Shrink{Source{x, exponents, dtype}, cols, lora_a, cols, vt};
+    S.dtype = dtype;
+    S.T = T;
+    S.tpad = P.tpad;
+    S.L = L;
+    S.rtiles = (rank + 15) / 16;
+    S.slots = 16;  // as many as are at work at once
+    while (S.slots > 1 && (P.tpad >> 4) * 2 * S.rtiles * S.slots > 1024) S.slots /= 2;
+    S.ids = ids;
+    S.status = status;
+    hipLaunchKernelGGL(back_shrink_kernel, dim3(static_cast<unsigned>((P.tpad >> 4) * 2 * S.rtiles * S.slots)),
+                       dim3(512), 0, stream, S);
+    if (!run_launched()) return IQ_ERR_HIP;
+  }
+  if (dx) {
+    RowsArgs D{};
+    D.packed[0] = D.packed[1] = packed;
+    D.nmat = 1;
+    D.rows = rows;
+    D.nb = cols / 256;
+    D.T = T;
+    D.tab = tab;
+    D.G = A.G;
+    D.B = A.B;
+    D.out = dx;
+    D.partial = reinterpret_cast<float *>(base + P.po);
+    D.splits = P.splits;
+    D.a = lora_a;
+    D.p = pt;
+    D.ids = ids;
+    D.rank = rank;
+    D.tpad = P.tpad;
+    if ((rc = launch_rows(fmt, dtype, D, stream)) != IQ_OK) return rc;
+  }
+  if (rank) {
+    OuterArgs O{};
+    O.of[0] = Outer{Source{dy, nullptr, dtype}, rows, (rows + 127) / 128, vt, db, 0};
+    O.of[1] = Outer{Source{x, exponents, dtype}, cols, cols / 128, pt, da, 1};
+    O.T = T;
+    O.tpad = P.tpad;
+    O.dtype = dtype;
+    O.rank = rank;
+    O.ids = ids;
+    const unsigned across = static_cast<unsigned>(O.of[0].blocks + O.of[1].blocks);
+    if (rank <= 16)
+      hipLaunchKernelGGL(back_outer_kernel<1>, dim3(across, num_adapters, 1), dim3(512), 0, stream, O);
+    else
+      hipLaunchKernelGGL(back_outer_kernel<2>, dim3(across, num_adapters, (rank + 31) / 32), dim3(512), 0, stream, O);
+    if (!run_launched()) return IQ_ERR_HIP;
+  }
+  return IQ_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,597 @@
+// iq_glu.hip -- iq_glu and iq_glu_backward: a gated feed-forward block's two
+// projections, activation and product on encoded weights (include/iq_train.h).
+//
+// Forward, two launches: tokens and codebook into operand order, then both
+// products, whose sums meet in registers and leave as h.  Backward, three (four
+// where few tokens split the rows): the same product, whose sums leave as the
+// gradients by g and u in the operand order of the product over rows (iq_rows.hip)
+// that gives dx.
+
+#include "iq_train.hpp"
+
+namespace iq {
+namespace {
+
+struct GluArgs {
+  const uint8_t *packed[2];  // gate, up
+  int64_t rows, nb, T;
+  const _Float16 *tab;
+  Tokens X;
+  int act, dtype;
+  void *h;
+  // backward (dh not null)
+  const void *dh;
+  const int32_t *dhe;  // exponent field of each token's dh
+  Grads G;
+  int parts;  // of the gradients
+  Bound B;
+  int lh;  // 2^lh >= hidden
+};
+
+struct GluPrepArgs {
+  Source S;
+  int64_t T, cols, nconv;
+  Tokens X;
+  Codebooks books;
+  // backward: the bound on the weights, and the exponents of dh
+  int fmt, bytes, backward;
+  const uint8_t *packed[2];
+  int64_t rows;
+  Bound B;
+  const void *dh;
+  int dtype;
+  int32_t *dhe;
+};
+
+__global__ void __launch_bounds__(512) glu_prep_kernel(GluPrepArgs A) {
+  __shared__ uint32_t s_red[8];
+  int64_t w = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (A.backward) {
+    if (w < kScaleSlots) {
+      bound_scales(A.fmt, A.bytes, A.packed, 2, A.rows * (A.cols >> 8), A.B, static_cast<int>(w), s_red);
+      return;
+    }
+    w -= kScaleSlots;
+    if (w < A.nconv) {
+      const int64_t t = w * 8 + wave;
+      if (t < A.T) {
+        const uint32_t e = row_exponent(A.dh, A.dtype, A.rows, t, lane);
+        if (lane == 0) A.dhe[t] = static_cast<int32_t>(e);
+      }
+      return;
+    }
+    w -= A.nconv;
+  }
+  if (w < A.nconv) {
+    const int64_t t = w * 8 + wave;
+    if (t >= A.T) return;
+    if (A.S.ex)
+      convert_checkpoint(static_cast<const int8_t *>(A.S.x), A.S.ex, A.cols, A.X, t, lane);
+    else if (A.S.dtype == IQ_DTYPE_F32)
+      convert_token<2>(A.S.x, A.cols, A.X, t, lane);
+    else
+      convert_token<1>(A.S.x, A.cols, A.X, t, lane);
+    return;
+  }
+  w -= A.nconv;
+  convert_codebook(A.books, static_cast<int>(w));
+  if (A.backward) bound_codebook(A.books, A.B, static_cast<int>(w), s_red);
+}
+
+// ---------------------------------------------------------------------------
+// Activations
+// ---------------------------------------------------------------------------
+// act(g), and its derivative in slope.  A sigmoid of 0 or 1 leaves no 0 * inf.
+__device__ __forceinline__ float activation(int act, float g, float &slope) {
+  if (act == IQ_ACT_GELU) {
+    const float phi = 0.5f * erfcf(-0.70710678f * g);
+    slope = phi + g * (0.39894228f * expf(-0.5f * g * g));
+    return g * phi;
+  }
+  float z = g, dz = 1.0f;
+  if (act == IQ_ACT_GELU_TANH) {  // (1 + tanh(y)) / 2 is the sigmoid of 2 y
+    constexpr float c = 1.5957691f, a = 0.044715f;
+    const float g2 = g * g;
+    z = c * (g + a * g * g2);
+    dz = c * (1.0f + 3.0f * a * g2);
+  }
+  const float s = 1.0f / (1.0f + expf(-z)), r = s * (1.0f - s);
+  slope = s + (r == 0.0f ? 0.0f : g * r * dz);
+  return g * s;
+}
+
+// The power of two of a token's gradients by g and u: |dh| < 2^(field - 126),
+// |g| and |u| < hidden |x| |w|, slopes below 1.13, and one more for the roundings.
+__device__ __forceinline__ int grad_exponent(const GluArgs &A, int ew, int64_t t) {
+  return 15 - ((A.dhe[t] - 126) + (15 + A.X.ex[t]) + A.lh + ew + 2);
+}
+
+// ---------------------------------------------------------------------------
+// Results
+// ---------------------------------------------------------------------------
+// One value of h, or of both gradients.
+__device__ __forceinline__ void put1(const GluArgs &A, int n, int64_t t, int64_t row, float g, float u) {
+  if (t >= A.T) return;
+  float slope;
+  const float a = activation(A.act, g, slope);
+  if (!A.dh) {
+    if (row < A.rows) store1(A.h, A.dtype, t * A.rows + row, a * u);
+    return;
+  }
+  const int64_t chunks = row_chunks(A.rows);
+  if (row >= chunks * 64) return;
+  float v[2] = {0.0f, 0.0f};
+  if (row < A.rows) {
+    const float d = load1(A.dh, A.dtype, t * A.rows + row);
+    v[0] = d * u * slope;
+    v[1] = d * a;
+  }
+  const int in = static_cast<int>(row & 63);
+  _Float16 *to = A.G.g16 + ((row >> 6) * A.G.ntile + (t >> 4)) * A.parts * 1024 +
+                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8 + (in & 7);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    _Float16 hi, lo;
+    to_parts(v[m], n, hi, lo);
+    to[m * chunks * A.G.ntile * A.parts * 1024] = hi;
+    if (A.parts == 2) to[m * chunks * A.G.ntile * A.parts * 1024 + 1024] = lo;
+  }
+}
+
+// Four rows of one token from row on (row a multiple of four).
+__device__ __forceinline__ void put4(const GluArgs &A, int n, int64_t t, int64_t row, const f32x4 &g, const f32x4 &u) {
+  if (t >= A.T) return;
+  const int64_t chunks = row_chunks(A.rows);
+  if (row >= (A.dh ? chunks * 64 : A.rows)) return;
+  const bool whole = row + 4 <= A.rows;
+  float a[4], slope[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) a[k] = activation(A.act, g[k], slope[k]);
+  const int64_t at = t * A.rows + row;
+  if (!A.dh) {
+    if (whole && A.dtype == IQ_DTYPE_BF16) {
+      const uint2 o = make_uint2(f32_to_bf16(a[0] * u[0]) | (static_cast<uint32_t>(f32_to_bf16(a[1] * u[1])) << 16),
+                                 f32_to_bf16(a[2] * u[2]) | (static_cast<uint32_t>(f32_to_bf16(a[3] * u[3])) << 16));
+      __builtin_memcpy(static_cast<uint16_t *>(A.h) + at, &o, 8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < A.rows) store1(A.h, A.dtype, at + k, a[k] * u[k]);
+    }
+    return;
+  }
+  float d[4];
+  if (whole && A.dtype == IQ_DTYPE_BF16) {
+    const uint2 w = ldu<uint2>(static_cast<const uint16_t *>(A.dh) + at);
+    d[0] = __uint_as_float(w.x << 16);
+    d[1] = __uint_as_float(w.x & 0xffff0000u);
+    d[2] = __uint_as_float(w.y << 16);
+    d[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = row + k < A.rows ? load1(A.dh, A.dtype, at + k) : 0.0f;
+  }
+  const int in = static_cast<int>(row & 63);
+  _Float16 *to = A.G.g16 + ((row >> 6) * A.G.ntile + (t >> 4)) * A.parts * 1024 +
+                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8 + (in & 7);
+  typedef _Float16 half4v __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    half4v hi, lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      _Float16 x, y;
+      to_parts(row + k < A.rows ? (m ? d[k] * a[k] : d[k] * u[k] * slope[k]) : 0.0f, n, x, y);
+      hi[k] = x;
+      lo[k] = y;
+    }
+    *reinterpret_cast<half4v *>(to + m * chunks * A.G.ntile * A.parts * 1024) = hi;
+    if (A.parts == 2) *reinterpret_cast<half4v *>(to + m * chunks * A.G.ntile * A.parts * 1024 + 1024) = lo;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the waves split K (split_blocks), a row tile of both weights each.
+// ---------------------------------------------------------------------------
+template <int F, int P, int C>
+__global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
+  constexpr int kTab = Geo<F>::N, kRed = 8 * 2 * 64;
+  __shared__ uint4 s_mem[kTab > kRed ? kTab : kRed];
+  load_table<F>(s_mem, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const Split S = split_of(A.nb);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * S.rw + S.rg) * 16;
+  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * C;
+  const int64_t rowbytes = A.nb * Geo<F>::BYTES, stride = A.X.ntile * P * 4096;
+  const int64_t at = min(row0 + n, A.rows - 1) * rowbytes;
+  const _Float16 *x0[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t t = min((tt0 + c) * 16 + n, A.T - 1);
+    x0[c] = A.X.x16 + (t >> 4) * P * 4096 + (q * 16 + (t & 15)) * 8;
+  }
+  f32x4 acc[1][2][C] = {};
+  __syncthreads();
+  split_blocks<F, P, C, 1, 2>(
+      A.nb, S, s_mem, [&](int m, int) { return A.packed[m] + at; },
+      [&](int64_t b, Operand<P, C> &x) __attribute__((always_inline)) {
+        const _Float16 *xp[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) xp[c] = x0[c] + b * stride;
+        load_operand<P, C>(x, xp);
+      },
+      acc);
+  const int ew = A.dh ? weight_exponent(A.B) : 0;
+  f32x4 *red = reinterpret_cast<f32x4 *>(s_mem);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    __syncthreads();  // what the memory held before is read
+#pragma unroll
+    for (int m = 0; m < 2; ++m) red[((S.rg * S.kw + S.kg) * 2 + m) * 64 + lane] = acc[0][m][c];
+    __syncthreads();
+    for (int i = threadIdx.x; i < S.rw * 64; i += blockDim.x) {
+      const int rg = i >> 6, l = i & 63;
+      f32x4 s[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const f32x4 *p = red + (rg * S.kw * 2 + m) * 64 + l;
+        s[m] = p[0];
+        for (int k = 1; k < S.kw; ++k) s[m] += p[k * 128];
+      }
+      const int64_t row = (static_cast<int64_t>(blockIdx.x) * S.rw + rg) * 16 + (l & 15);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t t = (tt0 + c) * 16 + (l >> 4) * 4 + k;
+        if (t >= A.T) continue;
+        const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
+        put1(A, ng, t, row, ldexpf(s[0][k], e), ldexpf(s[1][k], e));
+        if (A.dh && row == 0) A.G.ex[t] = -ng;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: a workgroup's weights are decoded once and reach its waves through
+// LDS.  WT token groups of C tiles by WR row groups of R row tiles, half of them of
+// the gate and half of the up projection, so that a wave's registers end up with
+// both sums of an output.  A stage is KS steps of 32 columns; each wave decodes
+// R / WT row tiles of the next stage while the matrix cores work on this one.
+// Weights are the A operand here: a lane has four consecutive rows of one token.
+// Sums are kept in units of the block's d, as in iq_linear's prompts (P == 1); for
+// f32 tokens a block has sums of its own, which are scaled and added (kept in one sum,
+// 5,120 columns came to 1e-6 of h in the norm, near twice 32-bit arithmetic's).
+// ---------------------------------------------------------------------------
+template <int F, int P, int WT, int WR, int C, int R>
+__global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(GluArgs A) {
+  constexpr int NW = WT * WR, KS = 2 / P, NS = 8 / KS, DR = R / WT, TA = WT * C, TB = WR * R;
+  static_assert(R % WT == 0 && R % 2 == 0, "whole row tiles to decode, as many of either weight");
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ u32x4 s_a[2][TA * P * KS * 64];  // tokens [tile][part][step][lane]
+  __shared__ u32x4 s_b[2][TB * KS * 64];      // weights [tile][step][lane]
+  __shared__ f32x4 s_ratio[2][TB * 4], s_unit[TB * 4];
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / WR, wr = wave % WR;
+  const int64_t rblk = static_cast<int64_t>(blockIdx.x) * (TB / 2) * 16;  // first row of the workgroup
+  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * TA, rowbytes = A.nb * Geo<F>::BYTES;
+  // Tile i of the workgroup: row group i / R, within it R / 2 tiles of the gate, then of the up projection.
+  const auto tile_row = [&](int i) { return rblk + ((i / R) * (R / 2) + i % R % (R / 2)) * 16; };
+  const uint8_t *rp[DR];
+#pragma unroll
+  for (int i = 0; i < DR; ++i) {
+    const int ti = wave * DR + i;
+    rp[i] = A.packed[ti % R / (R / 2)] + min(tile_row(ti) + n, A.rows - 1) * rowbytes;
+  }
+  const auto fetch = [&](int64_t b, int sub, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i0 = 0; i0 < TA * P * KS; i0 += NW) {
+      const int i = i0 + wave;
+      if (TA * P * KS % NW && i >= TA * P * KS) break;
+      const int64_t tile = min(tt0 + i / (P * KS), A.X.ntile - 1);
+      const u32x4 *from = reinterpret_cast<const u32x4 *>(A.X.x16) +
+                          ((b * A.X.ntile + tile) * P + i / KS % P) * 512 + (sub * KS + i % KS) * 64 + lane;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                       (__attribute__((address_space(3))) void *)&s_a[buf][i * 64], 16, 0, 0);
+    }
+  };
+  Words words[DR];
+  Raw raw[DR];
+  float unit[DR];
+  uint32_t keep[DR];
+  // The block whose words are there becomes the one to decode; its d against the one before.
+  const auto open_block = [&](int par) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < DR; ++i) {
+      raw[i] = unpack<F>(words[i], q);
+      const float d = block_scale<F>(raw[i]);
+      keep[i] = d != 0.0f ? ~0u : 0u;
+      const float ratio = P == 2 ? d : keep[i] ? unit[i] / d : 1.0f;
+      unit[i] = P == 2 ? 1.0f : keep[i] ? d : unit[i];
+      if (q == 0) reinterpret_cast<float *>(s_ratio[par])[(wave * DR + i) * 16 + n] = ratio;
+    }
+  };
+  const auto decode = [&](int sub, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < DR; ++i)
+        s_b[buf][((wave * DR + i) * KS + k) * 64 + lane] =
+            __builtin_bit_cast(u32x4, group_half8<F>(raw[i], sub * KS + k, s_tab, keep[i]));
+  };
+  f32x4 acc[R][C], part[P == 2 ? R : 1][C];  // part: a block's sums
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < DR; ++i) {
+    unit[i] = 0.0f;
+    words[i] = load_words<F>(rp[i], q);
+  }
+  fetch(0, 0, 0);
+  __syncthreads();  // the codebook
+  open_block(0);
+  decode(0, 0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the barrier does not wait for loads into LDS
+  __syncthreads();
+  for (int64_t b = 0; b < A.nb; ++b) {
+    const int par = static_cast<int>(b) & 1;
+    f32x4 ratio[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      ratio[r] = s_ratio[par][(wr * R + r) * 4 + q];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (P == 2)
+          part[r % (P == 2 ? R : 1)][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        else
+          acc[r][c] *= ratio[r];
+      }
+    }
+#pragma unroll
+    for (int sub = 0; sub < NS; ++sub) {
+      const int cur = sub & 1;
+      const bool last = b + 1 == A.nb && sub + 1 == NS;
+      if (!last) fetch(sub + 1 == NS ? b + 1 : b, (sub + 1) % NS, cur ^ 1);
+      if (sub == 0) {
+        const int64_t bn = min(b + 1, A.nb - 1);
+#pragma unroll
+        for (int i = 0; i < DR; ++i) words[i] = load_words<F>(rp[i] + bn * Geo<F>::BYTES, q);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below
+      if (!last) {
+        if (sub + 1 == NS) open_block(par ^ 1);
+        decode((sub + 1) % NS, cur ^ 1);
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        half8v x[C][P];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            x[c][p] = __builtin_bit_cast(half8v, s_a[cur][(((wt * C + c) * P + p) * KS + k) * 64 + lane]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const half8v w = __builtin_bit_cast(half8v, s_b[cur][((wr * R + r) * KS + k) * 64 + lane]);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              f32x4 &to = P == 2 ? part[r % (P == 2 ? R : 1)][c] : acc[r][c];
+              to = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x[c][p], to, 0, 0, 0);
+            }
+        }
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // the next stage is there, this one free
+    }
+    if (P == 2)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[r][c][k] = fmaf(ratio[r][k], part[r % (P == 2 ? R : 1)][c][k], acc[r][c][k]);
+  }
+#pragma unroll
+  for (int i = 0; i < DR; ++i)
+    if (q == 0) reinterpret_cast<float *>(s_unit)[(wave * DR + i) * 16 + n] = unit[i];
+  __syncthreads();
+  const int ew = A.dh ? weight_exponent(A.B) : 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t t = (tt0 + wt * C + c) * 16 + n;
+    if (t >= A.T) continue;
+    const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
+    if (A.dh && rblk == 0 && wr == 0 && q == 0) A.G.ex[t] = -ng;
+#pragma unroll
+    for (int r = 0; r < R / 2; ++r) {
+      f32x4 g = acc[r][c] * s_unit[(wr * R + r) * 4 + q], u = acc[R / 2 + r][c] * s_unit[(wr * R + R / 2 + r) * 4 + q];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        g[k] = ldexpf(g[k], e);
+        u[k] = ldexpf(u[k], e);
+      }
+      put4(A, ng, t, tile_row(wr * R + r) + 4 * q, g, u);
+    }
+  }
+}
+
+template <int F, int P, int C> void launch_split(const GluArgs &A, hipStream_t stream) {
+  const int64_t rw = split_rw(A.nb), rows = rw * 16, all = A.dh ? row_chunks(A.rows) * 64 : A.rows;
+  hipLaunchKernelGGL((glu_split_kernel<F, P, C>),
+                     dim3(static_cast<unsigned>((all + rows - 1) / rows),
+                          static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+                     dim3(static_cast<unsigned>(64 * split_kw(A.nb) * rw)), 0, stream, A);
+}
+
+template <int F, int P, int WT, int WR, int C, int R>
+void launch_tile(const GluArgs &A, hipStream_t stream) {
+  constexpr int rows = WR * R / 2 * 16;
+  const int64_t all = A.dh ? row_chunks(A.rows) * 64 : A.rows;
+  hipLaunchKernelGGL((glu_tile_kernel<F, P, WT, WR, C, R>),
+                     dim3(static_cast<unsigned>((all + rows - 1) / rows),
+                          static_cast<unsigned>((A.X.ntile + WT * C - 1) / (WT * C))),
+                     dim3(64 * WT * WR), 0, stream, A);
+}
+
+template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
+  if (A.X.ntile == 1) return launch_split<F, P, 1>(A, stream);
+  if (A.X.ntile <= 8) return launch_tile<F, P, 1, 8, 4, 2>(A, stream);
+  constexpr int C = P == 2 ? 2 : Geo<F>::N > 1024 ? 3 : 4;
+  launch_tile<F, P, 4, 2, C, 8>(A, stream);
+}
+
+struct GluPlan {
+  TokensPlan x;
+  int splits;
+  size_t xo, eo, bo, do_, go, geo, po, bytes;
+};
+GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, bool backward) {
+  GluPlan p{};
+  p.x = plan_tokens(T, hidden, dtype);  // a checkpoint of f32 tokens needs half of it
+  p.xo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
+  p.eo = p.xo + ws_up(p.x.xbytes);
+  p.bo = p.eo + ws_up(p.x.ebytes);
+  p.bytes = p.bo + kWsAlign;
+  if (!backward) return p;
+  const int64_t chunks = 2 * row_chunks(inter);
+  p.splits = rows_splits(T, hidden, chunks, dtype);
+  p.do_ = p.bo + ws_up(kBoundBytes);
+  p.go = p.do_ + ws_up(static_cast<size_t>(T) * 4);
+  p.geo = p.go + ws_up(grads_bytes(chunks, p.x.ntile, dtype));
+  p.po = p.geo + ws_up(p.x.ebytes);
+  p.bytes = p.po + ws_up(rows_partial_bytes(T, hidden, p.splits)) + kWsAlign;
+  return p;
+}
+
+int check_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T) {
+  if (run_bad_fmt(fmt)) return IQ_ERR_FMT;
+  if (run_bad_dtype(dtype)) return IQ_ERR_DTYPE;
+  if (inter < 0 || T < 0 || hidden <= 0 || hidden % 256 != 0) return IQ_ERR_SHAPE;
+  if (inter > (int64_t(1) << 24) || hidden > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
+  const int64_t ntile = (T + 15) / 16;
+  if (ntile > 4 * 65535) return IQ_ERR_SHAPE;  // token tiles of the second and third launch
+  // the joining launch
+  if (T * (hidden / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;
+  return IQ_OK;
+}
+
+int run_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int64_t hidden, const float *grid,
+            const void *x, const uint8_t *exponents, const void *dh, int dtype, int64_t T, int act, void *out,
+            bool backward, void *workspace, size_t workspace_bytes, int32_t *status, hipStream_t stream) {
+  int rc = check_glu(fmt, inter, hidden, dtype, T);
+  if (rc != IQ_OK) return rc;
+  if (act < IQ_ACT_SILU || act > IQ_ACT_GELU_TANH) return IQ_ERR_ARG;
+  const bool nothing = T == 0 || (inter == 0 && !backward), zeros = !nothing && inter == 0;
+  if (!grid || (!nothing && !zeros && (!gate || !up || !x || (backward && !dh))) || (!nothing && !out))
+    return IQ_ERR_NULL;
+  if (nothing) return IQ_OK;
+  if (zeros) return launch_zero(out, static_cast<size_t>(T) * hidden * (dtype == IQ_DTYPE_F32 ? 4 : 2), stream);
+  if ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up)) & 1) return IQ_ERR_ARG;
+  const GluPlan P = plan_glu(fmt, inter, hidden, dtype, T, backward);
+  if ((rc = run_check_ws(P.bytes, workspace, workspace_bytes)) != IQ_OK) return rc;
+  char *base = ws_base(workspace);
+  _Float16 *tab = reinterpret_cast<_Float16 *>(base);
+  const Tokens X{reinterpret_cast<_Float16 *>(base + P.xo), reinterpret_cast<int32_t *>(base + P.eo), P.x.ntile};
+  GluPrepArgs A{};
+  A.S = Source{x, exponents, dtype};
+  A.T = T;
+  A.cols = hidden;
+  A.nconv = (T + 7) / 8;
+  A.X = X;
+  A.books = one_codebook(fmt, grid, tab, status);
+  A.fmt = fmt;
+  A.bytes = block_bytes(fmt);
+  A.backward = backward;
+  A.packed[0] = gate;
+  A.packed[1] = up;
+  A.rows = inter;
+  A.dh = dh;
+  A.dtype = dtype;
+  GluArgs M{};
+  M.packed[0] = gate;
+  M.packed[1] = up;
+  M.rows = inter;
+  M.nb = hidden / 256;
+  M.T = T;
+  M.tab = tab;
+  M.X = X;
+  M.act = act;
+  M.dtype = dtype;
+  M.h = out;
+  if (backward) {
+    A.B = Bound{reinterpret_cast<uint32_t *>(base + P.bo), reinterpret_cast<uint32_t *>(base + P.bo) + kScaleSlots,
+                A.books.wg[0], fmt >= IQ1_S};
+    A.dhe = reinterpret_cast<int32_t *>(base + P.do_);
+    M.B = A.B;
+    M.dh = dh;
+    M.dhe = A.dhe;
+    M.parts = dtype == IQ_DTYPE_F32 ? 2 : 1;
+    M.G = Grads{reinterpret_cast<_Float16 *>(base + P.go), reinterpret_cast<int32_t *>(base + P.geo), P.x.ntile};
+    while ((int64_t(1) << M.lh) < hidden) ++M.lh;
+  }
+  const int64_t wgs = A.nconv + A.books.wg[0] + (backward ? kScaleSlots + A.nconv : 0);
+  hipLaunchKernelGGL(glu_prep_kernel, dim3(static_cast<unsigned>(wgs)), dim3(512), 0, stream, A);
+  if (!run_launched()) return IQ_ERR_HIP;
+#define CALL(F) source_parts(A.S) == 2 ? launch_glu<F, 2>(M, stream) : launch_glu<F, 1>(M, stream)
+  IQ_BY_FMT(fmt, CALL)
+#undef CALL
+  if (!run_launched()) return IQ_ERR_HIP;
+  if (!backward) return IQ_OK;
+  RowsArgs D{};
+  D.packed[0] = gate;
+  D.packed[1] = up;
+  D.nmat = 2;
+  D.rows = inter;
+  D.nb = hidden / 256;
+  D.T = T;
+  D.tab = tab;
+  D.G = M.G;
+  D.B = M.B;
+  D.out = out;
+  D.partial = reinterpret_cast<float *>(base + P.po);
+  D.splits = P.splits;
+  return launch_rows(fmt, dtype, D, stream);
+}
+
+int glu_size(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, bool backward, size_t *bytes) {
+  const int rc = check_glu(fmt, inter, hidden, dtype, T);
+  if (rc != IQ_OK) return rc;
+  if (!bytes) return IQ_ERR_NULL;
+  *bytes = inter && T ? plan_glu(fmt, inter, hidden, dtype, T, backward).bytes : 0;
+  return IQ_OK;
+}
+
+}  // namespace
+}  // namespace iq
+
+extern "C" {
+
+int iq_glu_workspace_size(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, size_t *bytes) {
+  return iq::glu_size(fmt, inter, hidden, dtype, T, false, bytes);
+}
+
+int iq_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int64_t hidden, const float *grid,
+           const void *x, int dtype, int64_t T, int act, void *h, void *workspace, size_t workspace_bytes,
+           int32_t *status, hipStream_t stream) {
+  return iq::run_glu(fmt, gate, up, inter, hidden, grid, x, nullptr, nullptr, dtype, T, act, h, false, workspace,
+                     workspace_bytes, status, stream);
+}
+
+int iq_glu_backward_workspace_size(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, size_t *bytes) {
+  return iq::glu_size(fmt, inter, hidden, dtype, T, true, bytes);
+}
+
+int iq_glu_backward(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int64_t hidden,
+                    const float *grid, const void *x, const uint8_t *exponents, const void *dh, int dtype,
+                    int64_t T, int act, void *dx, void *workspace, size_t workspace_bytes, int32_t *status,
+                    hipStream_t stream) {
+  return iq::run_glu(fmt, gate, up, inter, hidden, grid, x, exponents, dh, dtype, T, act, dx, true, workspace,
+                     workspace_bytes, status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,314 @@
+// iq_train.hpp -- what the calls of include/iq_train.h share: checkpoints as
+// tokens, the bound on a payload's weights, gradients in operand order, and the
+// product of gradients with encoded weights over the weights' rows.
+#pragma once
+
+#include "iq_run.hpp"
+#include "iq_train.h"
+
+namespace iq {
+
+// Gradients in fp16, for products over rows: g16 [chunk of 64 rows][tile of 16
+// tokens][part][step of 32 rows][lane][8], the A operand of a step (rows in their
+// order) as 1 KiB of consecutive memory; ex [tokens] as in Tokens.  Rows past the
+// last of a weight are zeros, tokens past the last are left unwritten.
+struct Grads {
+  _Float16 *g16;
+  int32_t *ex;
+  int64_t ntile;
+};
+__host__ __device__ inline int64_t row_chunks(int64_t rows) { return (rows + 63) / 64; }
+inline size_t grads_bytes(int64_t chunks, int64_t ntile, int dtype) {
+  return static_cast<size_t>(chunks) * ntile * (dtype == IQ_DTYPE_F32 ? 2 : 1) * 2048;
+}
+
+// What bounds a payload's weights, found by a preparing launch: the largest finite
+// block scale (fp16 bits) of each of kScaleSlots workgroups' shares, and the largest
+// finite magnitude (fp32 bits) of each 512 codebook entries.
+constexpr int kScaleSlots = 64, kGridSlots = 4;
+struct Bound {
+  uint32_t *scale, *grid;
+  int ngrid;
+  int iq1;
+};
+constexpr size_t kBoundBytes = (kScaleSlots + kGridSlots) * 4;
+
+// Tokens to bring into operand order: as they are, or a checkpoint.
+struct Source {
+  const void *x;
+  const uint8_t *ex;  // a checkpoint's exponents; null: x is of `dtype`
+  int dtype;
+};
+
+// Tokens of the forward product: of a checkpoint, one part serves (its values have
+// seven bits).
+inline int source_parts(const Source &s) { return s.ex || s.dtype == IQ_DTYPE_BF16 ? 1 : 2; }
+
+// dx of gradients G with one or two encoded weights of the same size (see
+// iq_rows.hip).
+struct RowsArgs {
+  const uint8_t *packed[2];
+  int nmat;
+  int64_t rows, nb, T;
+  const _Float16 *tab;
+  Grads G;
+  Bound B;
+  void *out;       // dx, or null where only partial sums are wanted
+  float *partial;  // [split][T][cols], used where the launch splits
+  int splits;
+  // adapters (rank 0: none): A, p of the tokens [rank][tpad] in fp32, their adapters (-1: none)
+  const void *a;
+  const float *p;
+  const int32_t *ids;
+  int rank;
+  int64_t tpad;
+};
+int rows_splits(int64_t T, int64_t cols, int64_t chunks, int dtype);
+inline size_t rows_partial_bytes(int64_t T, int64_t cols, int splits) {
+  return splits > 1 ? static_cast<size_t>(splits) * T * cols * 4 : 0;
+}
+inline int block_bytes(int fmt) {
+  constexpr int bytes[5] = {Geo<IQ2_XXS>::BYTES, Geo<IQ2_XS>::BYTES, Geo<IQ2_S>::BYTES, Geo<IQ1_S>::BYTES,
+                            Geo<IQ1_M>::BYTES};
+  return bytes[fmt];
+}
+int launch_zero(void *p, size_t bytes, hipStream_t stream);  // bytes: a multiple of two
+int launch_rows(int fmt, int dtype, const RowsArgs &A, hipStream_t stream);
+
+#ifdef __HIPCC__
+
+__device__ __forceinline__ float load1(const void *x, int dtype, int64_t i) {
+  return dtype == 1 ? bf16_to_f32(static_cast<const uint16_t *>(x)[i]) : static_cast<const float *>(x)[i];
+}
+
+// Eight consecutive values to any address.
+__device__ __forceinline__ void store8u(void *y, int dtype, int64_t i, const float v[8]) {
+  if (dtype == 1) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = f32_to_bf16(v[2 * j]) | (static_cast<uint32_t>(f32_to_bf16(v[2 * j + 1])) << 16);
+    const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
+    __builtin_memcpy(static_cast<uint16_t *>(y) + i, &o, 16);
+  } else {
+    __builtin_memcpy(static_cast<float *>(y) + i, v, 32);
+  }
+}
+
+// Eight codes of one block to their values; -128 to NaN.
+__device__ __forceinline__ void decode_codes(uint2 w, int e, float v[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int code = static_cast<int8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    v[j] = code == -128 ? __uint_as_float(0x7fc00000u) : ldexpf(static_cast<float>(code), e - 133);
+  }
+}
+
+// As convert_token, of a checkpoint: the largest block exponent takes the place of
+// the largest magnitude's, so that codes become at most 127 * 2^8.
+__device__ __forceinline__ void convert_checkpoint(const int8_t *codes, const uint8_t *ex, int64_t cols,
+                                                   const Tokens &X, int64_t t, int lane) {
+  const int64_t blocks = cols >> 5;
+  const uint8_t *er = ex + t * blocks;
+  uint32_t most = 1;
+  for (int64_t b = lane; b < blocks; b += 64) most = max(most, static_cast<uint32_t>(er[b]));
+  const int n = 141 - static_cast<int>(wave_max_u32(most));
+  constexpr int U = 4;
+  for (int64_t k = 0; k < cols; k += 512 * U) {
+    uint2 w[U];
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = min(k + u * 512 + lane * 8, cols - 8);
+      w[u] = ldu<uint2>(codes + t * cols + col);
+      e[u] = er[col >> 5];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = k + u * 512 + lane * 8;
+      if (col >= cols) break;
+      const int g = static_cast<int>(col & 255) >> 3;
+      half8v hi;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const int j = kept_at(h), code = static_cast<int8_t>((j < 4 ? w[u].x : w[u].y) >> (8 * (j & 3)));
+        const float f = ldexpf(static_cast<float>(code), e[u] - 133 + n);
+        hi[h] = static_cast<_Float16>(code == -128 ? __uint_as_float(0x7fc00000u) : f);
+      }
+      *reinterpret_cast<half8v *>(X.x16 + ((col >> 8) * X.ntile + (t >> 4)) * 4096 +
+                                  ((g & 7) * 64 + (g >> 3) * 16 + (t & 15)) * 8) = hi;
+    }
+  }
+  if (lane == 0) X.ex[t] = -n;
+}
+
+// The largest exponent field of a row's finite magnitudes (at least 1), by one wave.
+__device__ __forceinline__ uint32_t row_exponent(const void *x, int dtype, int64_t n, int64_t t, int lane) {
+  uint32_t e = 1;
+  const int64_t base = t * n, whole = n & ~int64_t(7);
+  for (int64_t k = lane * 8; k < whole; k += 512) {
+    float v[8];
+    load8u(x, dtype, base + k, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e = max_exponent(e, v[j]);
+  }
+  if (whole + lane < n) e = max_exponent(e, load1(x, dtype, base + whole + lane));
+  return wave_max_u32(e);
+}
+
+// A wave's maximum into LDS, the workgroup's into *out (NW waves).
+template <int NW> __device__ __forceinline__ void workgroup_max(uint32_t v, uint32_t *red, uint32_t *out) {
+  const uint32_t m = wave_max_u32(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t r = red[0];
+    for (int w = 1; w < NW; ++w) r = max(r, red[w]);
+    *out = r;
+  }
+}
+
+// Workgroup s of kScaleSlots (512 threads): the largest finite block scale of its
+// share of `blocks` blocks of `count` payloads.
+__device__ __forceinline__ void bound_scales(int fmt, int bytes, const uint8_t *const (&packed)[2], int count,
+                                             int64_t blocks, const Bound &B, int s, uint32_t *red) {
+  uint32_t most = 0;
+  for (int m = 0; m < count; ++m)
+    for (int64_t b = s * 512 + static_cast<int>(threadIdx.x); b < blocks; b += kScaleSlots * 512) {
+      const uint8_t *blk = packed[m] + b * bytes;
+      uint32_t d;
+      if (fmt == IQ1_M) {
+        const uint2 w = ldu<uint2>(blk + 48);
+        d = ((w.x >> 12) & 15u) | ((w.x >> 28) << 4) | (((w.y >> 12) & 15u) << 8) | ((w.y >> 28) << 12);
+      } else {
+        d = *reinterpret_cast<const uint16_t *>(blk);
+      }
+      d &= 0x7fffu;
+      if (d < 0x7c00u) most = max(most, d);
+    }
+  workgroup_max<8>(most, red, B.scale + s);
+}
+
+// With the workgroup that converts 512 codebook entries.
+__device__ __forceinline__ void bound_codebook(const Codebooks &C, const Bound &B, int wg, uint32_t *red) {
+  uint32_t most = 0;
+  const int i = wg * 512 + static_cast<int>(threadIdx.x);
+  if (i < C.n[0]) {
+    float g[8];
+    load8u(C.grid[0], 0, static_cast<int64_t>(i) * 8, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (finite_f(g[j])) most = max(most, __float_as_uint(g[j]) & 0x7fffffffu);
+  }
+  workgroup_max<8>(most, red, B.grid + wg);
+}
+
+// An e with |weight| < 2^e for every finite weight the payloads can hold, and d * m
+// under it as well (a codebook below one does not lower it).
+__device__ __forceinline__ int weight_exponent(const Bound &B) {
+  const int lane = threadIdx.x & 63;
+  static_assert(kScaleSlots == 64, "one a lane");
+  const uint32_t d = wave_max_u32(B.scale[lane]);
+  const uint32_t g = wave_max_u32(lane < B.ngrid ? B.grid[lane] : 0u);
+  const float df = f16_bits_to_f32(static_cast<uint16_t>(d));
+  const float v = fmaxf(__uint_as_float(g) + (B.iq1 ? 0.125f : 0.0f), 1.0f), m = (B.iq1 ? 15.0f : 31.0f * 0.125f) * v;
+  // a codebook near the end of fp32 would pass it: fp16 operands end long before
+  const float w = fminf(df * fminf(m, 1e30f), 1e30f);
+  return w > 0.0f ? static_cast<int>(__float_as_uint(w * 1.0001f) >> 23) - 126 : 0;
+}
+
+// The fields of group g, from a block in LDS (at an even address).
+struct Fields {
+  uint32_t k, ls, mask, h, d16;
+};
+template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *blk, int g) {
+  const auto u16 = [&](int at) -> uint32_t { return *reinterpret_cast<const uint16_t *>(blk + at); };
+  Fields f;
+  f.mask = f.h = 0;
+  if (F == IQ1_M) {
+    const uint32_t w0 = u16(48), w1 = u16(50), w2 = u16(52), w3 = u16(54);
+    f.d16 = (w0 >> 12) | ((w1 >> 12) << 4) | ((w2 >> 12) << 8) | ((w3 >> 12) << 12);
+    const uint32_t nib = (blk[32 + (g >> 1)] >> (4 * (g & 1))) & 15u;
+    f.k = blk[g] | ((nib & 7u) << 8);
+    f.h = nib >> 3;
+    f.ls = (u16(48 + 2 * (g >> 3)) >> (3 * ((g >> 1) & 3))) & 7u;
+    return f;
+  }
+  f.d16 = u16(0);
+  if (F == IQ2_XXS) {
+    const int at = 2 + 8 * (g >> 2);
+    f.k = blk[at + (g & 3)];
+    const uint32_t word = u16(at + 4) | (u16(at + 6) << 16);
+    f.mask = (word >> (7 * (g & 3))) & 127u;
+    f.ls = word >> 28;
+  } else if (F == IQ2_XS) {
+    const uint32_t v = u16(2 + 2 * g);
+    f.k = v & 511u;
+    f.mask = v >> 9;
+    f.ls = (blk[66 + (g >> 2)] >> (4 * ((g >> 1) & 1))) & 15u;
+  } else if (F == IQ2_S) {
+    f.k = blk[2 + g] | (((blk[66 + (g >> 2)] >> (2 * (g & 3))) & 3u) << 8);
+    f.mask = blk[34 + g];
+    f.ls = (blk[74 + (g >> 2)] >> (4 * ((g >> 1) & 1))) & 15u;
+  } else {
+    const uint32_t w = u16(34 + 2 * (g >> 2));
+    f.k = blk[2 + g] | (((w >> (3 * (g & 3))) & 7u) << 8);
+    f.ls = (w >> 12) & 7u;
+    f.h = w >> 15;
+  }
+  return f;
+}
+
+// Whole weights of a group times 2^s as fp16: hi[p] holds values p (low half) and
+// p + 4; lo (P == 2) what they leave.  unit: 2^s (IQ2: 2^s / 8).
+template <int F, int P>
+__device__ __forceinline__ void whole_weights(const Fields &f, float unit, const uint4 *tab, uint32_t (&hi)[4],
+                                              uint32_t (&lo)[4]) {
+  const uint4 e = tab[f.k];
+  const float dm = f16_bits_to_f32(static_cast<uint16_t>(f.d16)) * unit * static_cast<float>(2 * f.ls + 1);
+  const uint32_t o[4] = {e.x, e.y, e.z, e.w};
+  uint32_t t = 0;
+  if (!Geo<F>::IQ1) {  // signs of pair p: bits p and p + 4 to 15 and 31
+    uint32_t mask = f.mask;
+    if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
+    t = mask * 0x1001000u;
+  }
+  if (P == 1) {
+    const _Float16 m = static_cast<_Float16>(dm);
+    const half2v m2 = {m, m};
+    if (Geo<F>::IQ1) {
+      const half2v up = m2 * static_cast<_Float16>(0.125f);
+      const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (f.h * 0x80008000u));
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        hi[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
+    } else {
+#pragma unroll
+      for (int p = 3; p >= 0; --p) {
+        const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
+        hi[p] = __builtin_bit_cast(uint32_t, v) ^ (t & 0x80008000u);
+        asm("v_add_u32 %0, %0, %0" : "+v"(t));
+      }
+    }
+  } else {
+    const float c = Geo<F>::IQ1 ? (f.h ? -0.125f : 0.125f) : 0.0f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const half2v v = __builtin_bit_cast(half2v, o[p]);
+      half2v a, b;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float w = (static_cast<float>(v[k]) + c) * dm;
+        if (!Geo<F>::IQ1) w = __uint_as_float(__float_as_uint(w) ^ (((t >> (12 + p + 4 * k)) & 1u) << 31));
+        a[k] = static_cast<_Float16>(w);
+        b[k] = finite_f(w) ? static_cast<_Float16>(w - static_cast<float>(a[k])) : static_cast<_Float16>(0.0f);
+      }
+      hi[p] = __builtin_bit_cast(uint32_t, a);
+      lo[p] = __builtin_bit_cast(uint32_t, b);
+    }
+  }
+}
+
+#endif  // __HIPCC__
+
+}  // namespace iq

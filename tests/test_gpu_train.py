@@ -1,0 +1,547 @@
+"""Adapting encoded weights on the GPU (include/iq_train.h) against plain 64-bit arithmetic on the oracle's decoded
+weights.
+
+Exact cases: gradients, adapters and block scales are small integers or powers of two, so that every operand is exact
+in fp16 and every sum in any order a float32 number: results must be equal bit for bit.  Random cases: the tolerances
+add up the roundings that the header states (u = 2^-24 a half step of float32, h = 2^-11 of fp16):
+  g, u       each fp32 addition is off by at most 2u of a partial sum that is at most S = sum |x w|: no output passes
+             through more than 256 additions in a block, one per block and 16 of waves; float32 tokens to 2^-22
+  act, slope the activations stay within |g| 2^-20 and their slopes (below 1.13, changing by at most 1 per unit of g)
+             within 2^-17: exp to 2^-22 of an argument that is itself off by 2^-22 of its value
+  dg, du     held to h (bf16) or 2^-22 (f32), in steps of 2^-39 of a bound on them
+  dx         weights 2.01 h (bf16: two roundings) or 2^-21 (f32: 2^-22 for the product of the two low parts that is
+             left out, and as much again); one addition a row and 32 more
+  outputs    bf16 2^-8 of the value, float32 2^-24"""
+import numpy as np
+import pytest
+
+from ggml_iq_codebook_imatrix_amd import inputs
+from test_gpu_run import FORMATS, U, decoded, dev, f64, odd, payload, round_to, shifted
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+H16 = 2.0 ** -11
+DTYPES = [torch.bfloat16, torch.float32]
+ACTS = ["silu", "gelu", "gelu_tanh"]
+OUT = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from ggml_iq_codebook_imatrix_amd import api as a
+    a.lib()
+    return a
+
+
+# --------------------------------------------------------------------------
+# Checkpoints
+# --------------------------------------------------------------------------
+def kept(x):
+    """codes, exponents and values of a checkpoint, from the definition."""
+    T, cols = x.shape
+    codes, ex, vals = np.zeros((T, cols), np.int8), np.zeros((T, -(-cols // 32)), np.uint8), np.zeros((T, cols))
+    for b in range(ex.shape[1]):
+        at = slice(32 * b, min(32 * b + 32, cols))
+        v = x[:, at].astype(np.float64)
+        fine = np.isfinite(v)
+        most = np.where(fine, np.abs(v), 0).max(1)
+        e = np.where(most > 0, np.maximum(np.frexp(most)[1] + 126, 1), 1)
+        e = np.where((np.round(np.ldexp(most, 133 - e)) > 127) & (e < 254), e + 1, e)
+        c = np.clip(np.round(np.ldexp(np.where(fine, v, 0), 133 - e[:, None])), -127, 127)
+        codes[:, at] = np.where(fine, c, -128)
+        ex[:, b] = e
+        vals[:, at] = np.where(fine, np.ldexp(c, e[:, None] - 133), np.nan)
+    return codes, ex, vals
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,cols", [(1, 1), (3, 31), (5, 32), (2, 33), (7, 1001), (4, 8192), (3, 8200), (130, 2048),
+                                    (1, 20000), (300, 7)])
+def test_checkpoint(api, T, cols, dtype):
+    print("[case] checkpoint", T, cols, dtype, flush=True)
+    g = inputs.rng(T * cols)
+    x = dev(g.standard_normal((T, cols)).astype(np.float32) * np.exp(4 * g.standard_normal((T, cols))), dtype)
+    x[:, ::7] = 0
+    codes, ex, vals = kept(f64(x))
+    for t in (x, odd(x)):
+        st = api.new_status()
+        c, e = api.checkpoint(t, status=st)
+        assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(e.cpu().numpy(), ex)
+        assert api.read_status(st) == 0
+    for out in DTYPES:
+        assert np.array_equal(f64(api.restore(c, e, out)), vals)
+    assert np.array_equal(f64(api.restore(shifted(c, 3), shifted(e, 1), torch.float32)), vals)
+    # off by half a unit at most, and a unit is at most 2^-6 of the block's largest value
+    unit = np.repeat(np.ldexp(1.0, ex.astype(int) - 133), 32, 1)[:, :cols]
+    assert np.all(np.abs(vals - f64(x)) <= unit / 2)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_checkpoint_of_extreme_values(api, dtype):
+    print("[case] checkpoint extremes", dtype, flush=True)
+    top = torch.finfo(dtype).max
+    x = torch.zeros((6, 96), dtype=torch.float64)
+    x[0, :4] = torch.tensor([top, -top, top / 3, 1.0])
+    x[1, 5] = 2.0 ** -133
+    x[1, 40] = 2.0 ** -126
+    x[2, 1], x[2, 2], x[2, 3] = 127.0, 127.5, -0.5  # rounds to 128: one exponent more
+    x[3, 0], x[3, 1], x[3, 70] = float("inf"), 3.0, float("nan")
+    x[4] = float("nan")
+    x[5, 33], x[5, 95] = -1e-30, float("-inf")
+    x = x.to(dtype).cuda()
+    codes, ex, vals = kept(f64(x))
+    st = api.new_status()
+    c, e = api.checkpoint(x, status=st)
+    assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(e.cpu().numpy(), ex)
+    assert api.read_status(st) == api.STATUS_NONFINITE
+    for out in DTYPES:
+        assert np.array_equal(f64(api.restore(c, e, out)), vals, equal_nan=True)
+
+
+# --------------------------------------------------------------------------
+# The gated block
+# --------------------------------------------------------------------------
+def act_of(name, g):
+    """The activation and its derivative in 64 bits."""
+    from scipy.special import erf, expit
+    if name == "silu":
+        s = expit(g)
+        return g * s, s * (1 + g * (1 - s))
+    if name == "gelu":
+        phi = 0.5 * (1 + erf(g / np.sqrt(2)))
+        return g * phi, phi + g * np.exp(-g * g / 2) / np.sqrt(2 * np.pi)
+    k = np.sqrt(2 / np.pi)
+    t = np.tanh(k * (g + 0.044715 * g ** 3))
+    return g / 2 * (1 + t), (1 + t) / 2 + g / 2 * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
+
+
+class Block:
+    """Weights of a gated block, and what its sums may be off by."""
+
+    def __init__(self, orc, fmt, inter, nb, seed):
+        self.fmt, self.nb, self.inter = fmt, nb, inter
+        self.grid = inputs.grid_for(fmt, 70 + seed)
+        self.gate, self.up = payload(fmt, inter, nb, seed), payload(fmt, inter, nb, seed + 1)
+        self.wg, self.wu = decoded(orc, fmt, self.gate, self.grid), decoded(orc, fmt, self.up, self.grid)
+
+    def args(self):
+        return self.fmt, dev(self.gate), dev(self.up), dev(self.grid)
+
+    def sums(self, x, parts2):
+        off = (276 + self.nb) * 2 * U + (2.0 ** -22 if parts2 else 0)
+        return [(x @ w.T, off * (np.abs(x) @ np.abs(w).T)) for w in (self.wg, self.wu)]
+
+    def forward(self, x, act, dtype):
+        (g, og), (u, ou) = self.sums(x, dtype == torch.float32)
+        a, _ = act_of(act, g)
+        oa = 1.13 * og + np.abs(g) * 2.0 ** -20
+        h = a * u
+        return h, oa * np.abs(u) + np.abs(a) * ou + oa * ou + np.abs(h) * OUT[dtype] * 1.01
+
+    def backward(self, x, dh, act, dtype, x_parts2):
+        (g, og), (u, ou) = self.sums(x, x_parts2)
+        a, slope = act_of(act, g)
+        oa, os_ = 1.13 * og + np.abs(g) * 2.0 ** -20, og + 2.0 ** -17
+        dg, du = dh * u * slope, dh * a
+        bound = np.abs(dh).max(1) * np.abs(x).max(1) * max(np.abs(self.wg).max(), np.abs(self.wu).max()) * x.shape[1]
+        step = (64 * bound * 2.0 ** -39)[:, None]
+        hold = H16 if dtype == torch.bfloat16 else 2.0 ** -22
+        odg = np.abs(dh) * ((np.abs(u) + ou) * os_ + 1.2 * ou) + np.abs(dg) * hold + step
+        odu = np.abs(dh) * oa + np.abs(du) * hold + step
+        dx = dg @ self.wg + du @ self.wu
+        S = (np.abs(dg) + odg) @ np.abs(self.wg) + (np.abs(du) + odu) @ np.abs(self.wu)
+        w = 2.01 * H16 if dtype == torch.bfloat16 else 2.0 ** -21
+        off = odg @ np.abs(self.wg) + odu @ np.abs(self.wu) + (w + (2 * self.inter + 160) * 2 * U) * S
+        return dx, off + np.abs(dx) * OUT[dtype] * 1.01
+
+
+# inter, blocks, tokens: one row and token, ends inside every tile, each kernel's range of tokens
+SHAPES = [(1, 1, 1), (15, 1, 2), (33, 2, 16), (64, 9, 17), (130, 3, 40), (257, 2, 100), (40, 20, 129), (300, 4, 150),
+          (129, 2, 300)]
+
+
+def tokens(T, nb, seed, dtype):
+    return dev(inputs.activations(T, nb * 256, seed, seed + 1, bf16=False), dtype)
+
+
+def upstream(T, cols, seed, dtype):
+    g = inputs.rng(seed)
+    d = g.standard_normal((T, cols)) * np.exp(g.standard_normal((T, 1))) * 1e-3
+    d[g.random(T) < 0.1] = 0
+    return dev(d.astype(np.float32), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_glu(api, orc, fmt, dtype):
+    for i, (inter, nb, T) in enumerate(SHAPES):
+        act = ACTS[i % 3]
+        print("[case] glu", fmt, dtype, inter, nb, T, act, flush=True)
+        b = Block(orc, fmt, inter, nb, 11 * i)
+        x = tokens(T, nb, i, dtype)
+        st = api.new_status()
+        got = api.glu(*b.args(), x, activation=act, status=st)
+        assert got.dtype == dtype and got.shape == (T, inter) and api.read_status(st) == 0
+        h, off = b.forward(f64(x), act, dtype)
+        assert np.all(np.abs(f64(got) - h) <= off), (inter, nb, T)
+        if inter * T >= 500:  # fewer sums may all be ones that nearly cancel
+            assert np.linalg.norm(f64(got) - h) <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20) * \
+                np.linalg.norm(h)
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_glu_backward(api, orc, fmt, dtype, keep):
+    for i, (inter, nb, T) in enumerate(SHAPES):
+        act = ACTS[(i + 1) % 3]
+        print("[case] glu backward", fmt, dtype, keep, inter, nb, T, act, flush=True)
+        b = Block(orc, fmt, inter, nb, 11 * i)
+        x = tokens(T, nb, i, dtype)
+        given, value = x, f64(x)
+        if keep:
+            given = api.checkpoint(x)
+            value = f64(api.restore(*given))
+        dh = upstream(T, inter, 5 + i, dtype)
+        st = api.new_status()
+        got = api.glu_backward(*b.args(), given, dh, activation=act, status=st)
+        assert got.dtype == dtype and got.shape == (T, nb * 256) and api.read_status(st) == 0
+        dx, off = b.backward(value, f64(dh), act, dtype, dtype == torch.float32 and not keep)
+        assert np.all(np.abs(f64(got) - dx) <= off), (inter, nb, T)
+        if inter * T >= 500:  # every output has a factor of each sum: fewer may all be ones that nearly cancel
+            assert np.linalg.norm(f64(got) - dx) <= (2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -19) * \
+                np.linalg.norm(dx)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_glu_backward_against_differences(api, orc, act):
+    """Central differences of sum(dh * h) in 64 bits: off by the third derivative times step^2 / 6, well below 2^-20
+    of a gradient at a step of 2^-16, and by 2^-53 / 2^-16 of the sum."""
+    inter, nb, T = 70, 1, 5
+    print("[case] glu differences", act, flush=True)
+    b = Block(orc, "IQ2_S", inter, nb, 3)
+    x, dh = tokens(T, nb, 1, torch.float32), upstream(T, inter, 2, torch.float32)
+    got = f64(api.glu_backward(*b.args(), x, dh, activation=act))
+    xd, dd = f64(x), f64(dh)
+
+    def loss(v):
+        return (dd * act_of(act, v @ b.wg.T)[0] * (v @ b.wu.T)).sum(1)
+    _, off = b.backward(xd, dd, act, torch.float32, True)
+    for c in (0, 1, 77, 128, 255):
+        step = np.zeros_like(xd)
+        step[:, c] = 2.0 ** -16
+        slope = (loss(xd + step) - loss(xd - step)) / 2.0 ** -15
+        assert np.all(np.abs(got[:, c] - slope) <= off[:, c] + 2.0 ** -20 * np.abs(got).max(1) + 1e-9)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_glu_at_large_sums(api, act):
+    """Activations past their saturation: no NaN out of 0 * inf, exact limits."""
+    print("[case] glu large", act, flush=True)
+    fmt, T = "IQ2_XS", 20
+    grid, gate = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, 48, 1, 6))
+    up = dev(payload(fmt, 48, 1, 7, d16=1))  # 2^-24: the products stay finite
+    x = dev(inputs.activations(T, 256, 7, 8))
+    wg, wu = (api.dequantize(fmt, p, grid, torch.float32).double() for p in (gate, up))
+    for scale in (1e4, 1e15, 2e19):
+        h = api.glu(fmt, gate, up, grid, x * scale, activation=act)
+        g, u = (x * scale).double() @ wg.T, (x * scale).double() @ wu.T
+        near = torch.where(g > 0, g, 0) * u
+        # past 50 the activation is g or 0 to 50 e^-50 of g; the sums to 2^-10 of themselves where they do not cancel
+        sure = (g.abs() > 50) & (g.abs() > (x * scale).double().abs() @ wg.abs().T / 64) & \
+            (u.abs() > (x * scale).double().abs() @ wu.abs().T / 64)
+        assert bool(sure.any())
+        assert bool((((h.double() - near).abs() <= 2.0 ** -7 * near.abs() + 1e-20 * (g * u).abs()) | ~sure).all())
+        dx = api.glu_backward(fmt, gate, up, grid, x * scale, torch.ones_like(h), activation=act)
+        assert bool(dx.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [6, 50, 200])
+def test_glu_infinities_stay_in_their_token(api, T, dtype):
+    print("[case] glu inf nan", T, dtype, flush=True)
+    fmt, inter, nb = "IQ1_S", 100, 3
+    grid, gate, up = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, inter, nb, 6)), dev(payload(fmt, inter, nb, 7))
+    x, dh = tokens(T, nb, 3, dtype), upstream(T, inter, 4, dtype)
+    clean, dclean = api.glu(fmt, gate, up, grid, x), api.glu_backward(fmt, gate, up, grid, x, dh)
+    bad, dbad = x.clone(), dh.clone()
+    bad[1, 300], bad[T - 2, 17] = float("inf"), float("nan")
+    dbad[3, 5], dbad[T - 1, 7] = float("-inf"), float("nan")
+    keep = [t for t in range(T) if t not in (1, T - 2)]
+    dkeep = [t for t in keep if t not in (3, T - 1)]
+    got, dgot = api.glu(fmt, gate, up, grid, bad), api.glu_backward(fmt, gate, up, grid, bad, dbad)
+    assert torch.equal(got[keep], clean[keep]) and torch.equal(dgot[dkeep], dclean[dkeep])
+    assert bool(got[T - 2].isnan().all()) and bool(dgot[T - 2].isnan().all()) and bool(dgot[T - 1].isnan().all())
+    assert not bool(dgot[3].isfinite().any()) and not bool(got[1].isfinite().all())
+    st = api.new_status()
+    ck = api.checkpoint(bad, status=st)
+    assert api.read_status(st) == api.STATUS_NONFINITE
+    assert bool(api.glu_backward(fmt, gate, up, grid, ck, dh)[[1, T - 2]].isnan().all())
+
+
+# --------------------------------------------------------------------------
+# The projection's backward pass
+# --------------------------------------------------------------------------
+# rows, blocks, tokens, adapters, rank
+BACK = [(1, 1, 1, 0, 0), (1, 1, 1, 1, 1), (7, 2, 3, 2, 2), (16, 2, 16, 1, 16), (33, 1, 17, 3, 5), (64, 3, 33, 2, 17),
+        (130, 2, 70, 4, 32), (257, 1, 130, 2, 40), (1001, 2, 64, 1, 3), (300, 2, 300, 12, 4), (65, 5, 260, 3, 64),
+        (200, 1, 40, 0, 0)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_backward_exact(api, orc, fmt, dtype):
+    for i, (rows, nb, T, N, r) in enumerate(BACK):
+        print("[case] linear backward exact", fmt, dtype, rows, nb, T, N, r, flush=True)
+        g = inputs.rng(40 + i)
+        cols = nb * 256
+        grid = inputs.grid_for(fmt, 300 + i)
+        p = payload(fmt, rows, nb, i, d16=g.choice([0x2000, 0x2400, 0x1c00], (rows, nb)))  # 2^-7, 2^-6, 2^-8
+        w = decoded(orc, fmt, p, grid)
+        dy = g.integers(-4, 5, (T, rows)).astype(np.float32)
+        x = g.integers(-4, 5, (T, cols)).astype(np.float32)
+        a, b = g.integers(-1, 2, (N, r, cols)).astype(np.float32), g.integers(-1, 2, (N, rows, r)).astype(np.float32)
+        scale = 2.0 ** g.integers(-2, 3, N).astype(np.float32)
+        ids = g.integers(-1, max(N, 1), T).astype(np.int32)
+        if N > 2:
+            ids[ids == 1] = 0  # an adapter without tokens
+        dx, size = dy.astype(np.float64) @ w, np.abs(dy) @ np.abs(w)
+        da, db = np.zeros(a.shape), np.zeros(b.shape)
+        sa, sb = np.zeros(a.shape), np.zeros(b.shape)
+        for n in range(N):
+            at = ids == n
+            back, v = scale[n] * (dy[at] @ b[n]).astype(np.float64), scale[n] * (x[at] @ a[n].T).astype(np.float64)
+            dx[at] += back @ a[n]
+            size[at] += np.abs(back) @ np.abs(a[n])
+            da[n], db[n] = back.T @ x[at], dy[at].T @ v
+            sa[n], sb[n] = np.abs(back).T @ np.abs(x[at]), np.abs(dy[at]).T @ np.abs(v)
+        # Partial sums in any order are exact below 2^24 steps: 2^-11, the weights', for dx, and 2^-2, the adapters'
+        # products', for their gradients.
+        st = api.new_status()
+        if not N:
+            got = [api.linear_backward(fmt, dev(p), dev(grid), dev(dy, dtype), status=st)]
+            want = [(dx, size)]
+        else:
+            want = [(dx, size), (da, sa), (db, sb)]
+            xs = dev(x, dtype)
+            got = api.linear_backward(fmt, dev(p), dev(grid), dev(dy, dtype), x=xs, lora_a=dev(a, dtype),
+                                      lora_b=dev(b, dtype), lora_scale=dev(scale), lora_ids=dev(ids), status=st)
+            again = api.linear_backward(fmt, dev(p), dev(grid), dev(dy, dtype), x=api.checkpoint(xs),
+                                        lora_a=dev(a, dtype), lora_b=dev(b, dtype), lora_scale=dev(scale),
+                                        lora_ids=dev(ids), need_dx=False)
+            assert again[0] is None  # integers up to 4 are exact in 8 bits
+            assert torch.equal(again[1], got[1]) and torch.equal(again[2], got[2])
+        for k, (t, (v, s)) in enumerate(zip(got, want)):
+            assert t.dtype == dtype and t.shape == v.shape
+            sure = s < (2.0 ** 22 if k else 2.0 ** 13)
+            assert sure.mean() > 0.5, (k, rows, nb, T, N, r)
+            assert np.array_equal(f64(t)[sure], round_to(v, dtype)[sure]), (k, rows, nb, T, N, r)
+        assert api.read_status(st) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_backward_random(api, orc, fmt, dtype):
+    for rows, nb, T, N, r in ((129, 8, 5, 2, 16), (500, 3, 45, 4, 9), (96, 20, 200, 3, 24)):
+        print("[case] linear backward random", fmt, dtype, rows, nb, T, N, r, flush=True)
+        g = inputs.rng(rows)
+        cols = nb * 256
+        grid = inputs.grid_for(fmt, 41)
+        p = payload(fmt, rows, nb, rows + 1)
+        w = decoded(orc, fmt, p, grid)
+        x, dy = tokens(T, nb, 42, dtype), upstream(T, rows, 43, dtype)
+        a = dev(g.standard_normal((N, r, cols), dtype=np.float32) * 0.02, dtype)
+        b = dev(g.standard_normal((N, rows, r), dtype=np.float32) * 0.02, dtype)
+        ids = g.integers(-1, N, T).astype(np.int32)
+        got = api.linear_backward(fmt, dev(p), dev(grid), dy, x=x, lora_a=a, lora_b=b, lora_ids=dev(ids))
+        xd, dd, ad, bd = f64(x), f64(dy), f64(a), f64(b)
+        parts = 2.01 * H16 if dtype == torch.bfloat16 else 2.0 ** -21 + 2.0 ** -22
+        dx, off = dd @ w, (parts + (rows + 96) * 2 * U) * (np.abs(dd) @ np.abs(w))
+        off += 2.0 ** -38 * np.abs(dd).max(1, keepdims=True) * np.abs(w).max() * rows
+        want = [dx, np.zeros(ad.shape), np.zeros(bd.shape)]
+        offs = [off, np.zeros(ad.shape), np.zeros(bd.shape)]
+        for n in range(N):
+            at = ids == n
+            back, v = dd[at] @ bd[n], xd[at] @ ad[n].T
+            oback = (rows + 16) * 2 * U * (np.abs(dd[at]) @ np.abs(bd[n]))
+            ov = (cols + 16) * 2 * U * (np.abs(xd[at]) @ np.abs(ad[n]).T)
+            dx[at] += back @ ad[n]
+            off[at] += oback @ np.abs(ad[n]) + (r + 16) * 2 * U * (np.abs(back) @ np.abs(ad[n]))
+            want[1][n], want[2][n] = back.T @ xd[at], dd[at].T @ v
+            offs[1][n] = oback.T @ np.abs(xd[at]) + (3 * T + 32) * 2 * U * (np.abs(back).T @ np.abs(xd[at]))
+            offs[2][n] = np.abs(dd[at]).T @ ov + (3 * T + 32) * 2 * U * (np.abs(dd[at]).T @ np.abs(v))
+        for k in range(3):
+            assert np.all(np.abs(f64(got[k]) - want[k]) <= offs[k] + np.abs(want[k]) * OUT[dtype] * 1.01), k
+            rel = np.linalg.norm(f64(got[k]) - want[k]) / np.linalg.norm(want[k])
+            assert rel <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_backward_adapters_and_bad_tokens(api, dtype):
+    """Ids that name no adapter, NaN in one token: they reach that token and its adapter only."""
+    print("[case] linear backward bad tokens", dtype, flush=True)
+    fmt, rows, nb, T, N, r = "IQ2_XXS", 90, 2, 77, 3, 6
+    g = inputs.rng(8)
+    grid, p = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
+    x, dy = tokens(T, nb, 3, dtype), upstream(T, rows, 4, dtype)
+    a = dev(g.standard_normal((N, r, nb * 256), dtype=np.float32), dtype)
+    b = dev(g.standard_normal((N, rows, r), dtype=np.float32), dtype)
+    ids = dev(g.integers(0, 2, T).astype(np.int32))
+    ids[10], ids[20] = -1, -1
+    ids[30:36] = 2
+    st = api.new_status()
+    run = lambda i, x, dy: api.linear_backward(fmt, p, grid, dy, x=x, lora_a=a, lora_b=b, lora_ids=i, status=st)  # noqa
+    clean = run(ids, x, dy)
+    assert api.read_status(st) == 0
+    wild = ids.clone()
+    wild[10], wild[20] = N, -2
+    got = run(wild, x, dy)
+    assert api.read_status(st) == api.STATUS_BADID
+    assert all(torch.equal(m, n) for m, n in zip(got, clean))
+    bad_x, bad_dy = x.clone(), dy.clone()
+    bad_x[31, 3], bad_dy[33, 4], bad_dy[10, 1] = float("nan"), float("inf"), float("nan")
+    dx, da, db = run(ids, bad_x, bad_dy)
+    rest = [t for t in range(T) if t not in (33, 10)]
+    assert torch.equal(dx[rest], clean[0][rest]) and torch.equal(da[:2], clean[1][:2]) and torch.equal(db[:2], clean[2][:2])
+    assert not bool(dx[33].isfinite().any()) and bool(dx[10].isnan().all())
+    assert bool(da[2, :, 3].isnan().all()) and bool(db[2].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_nothing_to_do(api, dtype):
+    print("[case] empty", dtype, flush=True)
+    fmt, nb = "IQ1_M", 2
+    grid = dev(inputs.grid_for(fmt, 5))
+    p, none = dev(payload(fmt, 40, nb, 6)), torch.empty((0, nb, 56), dtype=torch.uint8, device="cuda")
+    x0, x = torch.empty((0, nb * 256), dtype=dtype, device="cuda"), tokens(3, nb, 1, dtype)
+    full = lambda *s: torch.full(s, 7.0, dtype=dtype, device="cuda")  # noqa: E731
+    assert api.glu(fmt, p, p, grid, x0).shape == (0, 40) and api.glu(fmt, none, none, grid, x).shape == (3, 0)
+    assert api.glu_backward(fmt, p, p, grid, x0, full(0, 40)).shape == (0, 512)
+    assert bool((api.glu_backward(fmt, none, none, grid, x, full(3, 0), out=full(3, 512)) == 0).all())
+    assert bool((api.linear_backward(fmt, none, grid, full(3, 0), out=full(3, 512)) == 0).all())
+    a, b = full(2, 4, 512), full(2, 40, 4)
+    got = api.linear_backward(fmt, p, grid, full(0, 40), x=x0, lora_a=a, lora_b=b,
+                              lora_ids=torch.empty(0, dtype=torch.int32, device="cuda"), grad_a=full(2, 4, 512),
+                              grad_b=full(2, 40, 4))
+    assert got[0].shape == (0, 512) and bool((got[1] == 0).all()) and bool((got[2] == 0).all())
+    c, e = api.checkpoint(x0)
+    assert c.shape == (0, 512) and e.shape == (0, 16) and api.restore(c, e, dtype).shape == (0, 512)
+
+
+# --------------------------------------------------------------------------
+# All of them together, as one layer's training step
+# --------------------------------------------------------------------------
+def step(api, gate, up, down, grid, x, dy, lora, act="silu"):
+    """Forward with checkpoints, and back: y, dx and the adapters' gradients."""
+    kx = api.checkpoint(x)
+    h = api.glu(*gate, *up, grid[0], x, activation=act)
+    y = api.linear(*down, grid[1], h, **lora)
+    kh = api.checkpoint(h)
+    dh, da, db = api.linear_backward(*down, grid[1], dy, x=kh, **lora)
+    return y, api.glu_backward(*gate, *up, grid[0], kx, dh, activation=act), da, db
+
+
+def layer(dtype, T, seed=0):
+    g = inputs.rng(seed)
+    hidden, inter, N, r = 512, 768, 2, 8
+    f, fd = "IQ2_XS", "IQ1_S"
+    gate, up = dev(payload(f, inter, hidden // 256, 1)), dev(payload(f, inter, hidden // 256, 2))
+    down = dev(payload(fd, hidden, inter // 256, 3))
+    grid = dev(inputs.grid_for(f, 5)), dev(inputs.grid_for(fd, 6))
+    lora = dict(lora_a=dev(g.standard_normal((N, r, inter), dtype=np.float32) * 0.05, dtype),
+                lora_b=dev(g.standard_normal((N, hidden, r), dtype=np.float32) * 0.05, dtype),
+                lora_scale=dev(np.array([1.0, 0.5], np.float32)),
+                lora_ids=dev(np.sort(g.integers(-1, N, T)).astype(np.int32)))
+    return (f, gate), (up,), (fd, down), grid, tokens(T, hidden // 256, 7, dtype), upstream(T, hidden, 8, dtype), lora
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [5, 60, 200])
+def test_training_step(api, T, dtype):
+    """Against the same step in 64 bits on the values that the checkpoints hold.  Forward results differ by roundings of
+    h and y; gradients by those of dh, and of the operands that the tests above bound one by one: in the norm a few
+    roundings of the type, each 2^-9 (bf16) or 2^-25 on the average, and the products' own."""
+    print("[case] step", T, dtype, flush=True)
+    L = layer(dtype, T)
+    (f, gate), (up,), (fd, down), grid, x, dy, lora = L
+    y, dx, da, db = step(api, *L)
+    wg, wu = (api.dequantize(f, w, grid[0]).double().cpu() for w in (gate, up))
+    wd = api.dequantize(fd, down, grid[1]).double().cpu()
+    a, b, s = (lora[k].double().cpu() for k in ("lora_a", "lora_b", "lora_scale"))
+    ids = lora["lora_ids"].cpu()
+    mine = torch.nn.functional.one_hot(ids.long() + 1, 3)[:, 1:].double() * s
+
+    def forward(x):
+        h = torch.nn.functional.silu(x @ wg.T) * (x @ wu.T)
+        return h, h @ wd.T + torch.einsum("tn,tnr,nor->to", mine, torch.einsum("ti,nri->tnr", h, a), b)
+    want_y = forward(x.double().cpu())[1]
+    xr = api.restore(*api.checkpoint(x)).double().cpu().requires_grad_()
+    h, out = forward(xr)
+    (h64,) = torch.autograd.grad(out, h, dy.double().cpu(), retain_graph=True)
+    (dx64,) = torch.autograd.grad(out, xr, dy.double().cpu())
+    hk = api.restore(*api.checkpoint(api.glu(f, gate, up, grid[0], x))).double().cpu()
+    back = torch.einsum("to,nor->tnr", dy.double().cpu(), b) * mine[..., None]
+    da64 = torch.einsum("tnr,ti->nri", back, hk)
+    db64 = torch.einsum("to,tnr->nor", dy.double().cpu(), torch.einsum("ti,nri->tnr", hk, a) * mine[..., None])
+    off = 2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -19
+    for got, want in ((y, want_y), (dx, dx64), (da, da64), (db, db64)):
+        assert torch.linalg.norm(got.double().cpu() - want) <= off * torch.linalg.norm(want)
+
+
+def test_calls_do_not_disturb_each_other(api):
+    """Repeats are equal bit for bit, on two streams at once as well, from a captured graph with the program's own work
+    between the replays, with shared workspaces and buffers at any element; what lies around the outputs stays."""
+    print("[case] streams and graphs", flush=True)
+    L = layer(torch.bfloat16, 90)
+    (f, gate), (up,), (fd, down), grid, x, dy, lora = L
+    want = step(api, *L)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(step(api, *L))
+    torch.cuda.synchronize()
+    assert all(torch.equal(m, n) for g in got for m, n in zip(g, want))
+    moved = (f, shifted(gate, 2)), (shifted(up, 2),), (fd, shifted(down, 2)), grid, odd(x), odd(dy), \
+        {k: odd(v) for k, v in lora.items()}
+    assert all(torch.equal(m, n) for m, n in zip(step(api, *moved), want))
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.zeros(n + 128, dtype=dtype, device="cuda")
+        return buf, buf[64:64 + n].view(shape)
+    bd, dx = guarded(x.shape, x.dtype)
+    ba, da = guarded(lora["lora_a"].shape, x.dtype)
+    bb, db = guarded(lora["lora_b"].shape, x.dtype)
+    bh, h = guarded((90, 768), x.dtype)
+    bdh, dh = guarded((90, 768), x.dtype)
+    bc, c = guarded((90, 768), torch.int8)
+    be, e = guarded((90, 24), torch.uint8)
+    api.glu(f, gate, up, grid[0], x, out=h)
+    api.checkpoint(h, codes=c, exponents=e)
+    api.linear_backward(fd, down, grid[1], dy, x=(c, e), out=dh, grad_a=da, grad_b=db, **lora)
+    api.glu_backward(f, gate, up, grid[0], api.checkpoint(x), dh, out=dx)
+    assert torch.equal(dx, want[1]) and torch.equal(da, want[2]) and torch.equal(db, want[3])
+    for buf in (bd, ba, bb, bh, bdh, bc, be):
+        assert bool((buf[:64] == 0).all()) and bool((buf[-64:] == 0).all())
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = step(api, *L)
+    for k in range(3):
+        for t in held:
+            t.fill_(5)
+        x2 = x * (k + 1)
+        saved = x.clone()
+        x.copy_(x2)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for m, n in zip(held, step(api, *L)))
+        x.copy_(saved)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(m, n) for m, n in zip(held, want))
