@@ -7,6 +7,8 @@
 // gradients by g and u in the operand order of the product over rows (iq_rows.hip)
 // that gives dx.
 
+#include <type_traits>
+
 #include "iq_train.hpp"
 
 namespace iq {
@@ -82,11 +84,13 @@ __global__ void __launch_bounds__(512) glu_prep_kernel(GluPrepArgs A) {
 // ---------------------------------------------------------------------------
 // Activations
 // ---------------------------------------------------------------------------
-// act(g), and its derivative in slope.  A sigmoid of 0 or 1 leaves no 0 * inf.
-__device__ __forceinline__ float activation(int act, float g, float &slope) {
+// act(g), and with `back` its derivative in slope.  exp as a power of two (2^-23 |z| of its value) and one reciprocal
+// (an ulp) leave a sigmoid s within 2^-24 |z| s (1 - s) and an ulp.  A sigmoid of 0 or 1 leaves no 0 * inf.
+__device__ __forceinline__ float activation(int act, float g, bool back, float &slope) {
+  slope = 0.0f;
   if (act == IQ_ACT_GELU) {
     const float phi = 0.5f * erfcf(-0.70710678f * g);
-    slope = phi + g * (0.39894228f * expf(-0.5f * g * g));
+    if (back) slope = phi + g * (0.39894228f * expf(-0.5f * g * g));
     return g * phi;
   }
   float z = g, dz = 1.0f;
@@ -96,8 +100,11 @@ __device__ __forceinline__ float activation(int act, float g, float &slope) {
     z = c * (g + a * g * g2);
     dz = c * (1.0f + 3.0f * a * g2);
   }
-  const float s = 1.0f / (1.0f + expf(-z)), r = s * (1.0f - s);
-  slope = s + (r == 0.0f ? 0.0f : g * r * dz);
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+  if (back) {
+    const float r = s * (1.0f - s);
+    slope = s + (r == 0.0f ? 0.0f : g * r * dz);
+  }
   return g * s;
 }
 
@@ -114,7 +121,7 @@ __device__ __forceinline__ int grad_exponent(const GluArgs &A, int ew, int64_t t
 __device__ __forceinline__ void put1(const GluArgs &A, int n, int64_t t, int64_t row, float g, float u) {
   if (t >= A.T) return;
   float slope;
-  const float a = activation(A.act, g, slope);
+  const float a = activation(A.act, g, A.dh, slope);
   if (!A.dh) {
     if (row < A.rows) store1(A.h, A.dtype, t * A.rows + row, a * u);
     return;
@@ -139,55 +146,50 @@ __device__ __forceinline__ void put1(const GluArgs &A, int n, int64_t t, int64_t
   }
 }
 
-// Four rows of one token from row on (row a multiple of four).
-__device__ __forceinline__ void put4(const GluArgs &A, int n, int64_t t, int64_t row, const f32x4 &g, const f32x4 &u) {
-  if (t >= A.T) return;
-  const int64_t chunks = row_chunks(A.rows);
-  if (row >= (A.dh ? chunks * 64 : A.rows)) return;
-  const bool whole = row + 4 <= A.rows;
-  float a[4], slope[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) a[k] = activation(A.act, g[k], slope[k]);
-  const int64_t at = t * A.rows + row;
-  if (!A.dh) {
-    if (whole && A.dtype == IQ_DTYPE_BF16) {
-      const uint2 o = make_uint2(f32_to_bf16(a[0] * u[0]) | (static_cast<uint32_t>(f32_to_bf16(a[1] * u[1])) << 16),
-                                 f32_to_bf16(a[2] * u[2]) | (static_cast<uint32_t>(f32_to_bf16(a[3] * u[3])) << 16));
-      __builtin_memcpy(static_cast<uint16_t *>(A.h) + at, &o, 8);
+// Eight rows of one token from row on (row a multiple of eight).
+__device__ __forceinline__ void put8(const GluArgs &A, int n, int64_t t, int64_t row, const float (&g)[8],
+                                     const float (&u)[8]) {
+  const int64_t chunks = row_chunks(A.rows), at = t * A.rows + row;
+  const bool whole = row + 8 <= A.rows;
+  float a[8], slope[8], d[8];
+  if (A.dh) {
+    if (row >= chunks * 64) return;
+    if (whole) {
+      load8u(A.dh, A.dtype, at, d);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row + k < A.rows) store1(A.h, A.dtype, at + k, a[k] * u[k]);
+      for (int k = 0; k < 8; ++k) d[k] = row + k < A.rows ? load1(A.dh, A.dtype, at + k) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = activation(A.act, g[k], A.dh, slope[k]);
+  if (!A.dh) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] *= u[k];
+    if (whole) {
+      store8u(A.h, A.dtype, at, a);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (row + k < A.rows) store1(A.h, A.dtype, at + k, a[k]);
     }
     return;
   }
-  float d[4];
-  if (whole && A.dtype == IQ_DTYPE_BF16) {
-    const uint2 w = ldu<uint2>(static_cast<const uint16_t *>(A.dh) + at);
-    d[0] = __uint_as_float(w.x << 16);
-    d[1] = __uint_as_float(w.x & 0xffff0000u);
-    d[2] = __uint_as_float(w.y << 16);
-    d[3] = __uint_as_float(w.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) d[k] = row + k < A.rows ? load1(A.dh, A.dtype, at + k) : 0.0f;
-  }
   const int in = static_cast<int>(row & 63);
   _Float16 *to = A.G.g16 + ((row >> 6) * A.G.ntile + (t >> 4)) * A.parts * 1024 +
-                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8 + (in & 7);
-  typedef _Float16 half4v __attribute__((ext_vector_type(4)));
+                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    half4v hi, lo;
+    half8v hi, lo;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      _Float16 x, y;
+    for (int k = 0; k < 8; ++k) {
+      _Float16 x, y;  // rows past the last: zeros, whatever was summed there
       to_parts(row + k < A.rows ? (m ? d[k] * a[k] : d[k] * u[k] * slope[k]) : 0.0f, n, x, y);
       hi[k] = x;
       lo[k] = y;
     }
-    *reinterpret_cast<half4v *>(to + m * chunks * A.G.ntile * A.parts * 1024) = hi;
-    if (A.parts == 2) *reinterpret_cast<half4v *>(to + m * chunks * A.G.ntile * A.parts * 1024 + 1024) = lo;
+    *reinterpret_cast<half8v *>(to + m * chunks * A.G.ntile * A.parts * 1024) = hi;
+    if (A.parts == 2) *reinterpret_cast<half8v *>(to + m * chunks * A.G.ntile * A.parts * 1024 + 1024) = lo;
   }
 }
 
@@ -252,30 +254,79 @@ __global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
   }
 }
 
+// weights_half8 begun: the fields of group i, which is the same in all lanes but not known to the compiler, and its
+// codebook entry, which comes from LDS some time later.
+struct Entry {
+  uint4 e;
+  GroupFields g;
+  uint32_t keep;
+};
+template <int F> __device__ __forceinline__ Entry lookup(const Raw &r, int i, const uint4 *tab, uint32_t keep) {
+  Raw s = r;  // the words that hold it, where group_fields looks for those of groups 0 .. 3
+  if (i & 4) {
+    s.a[0] = F == IQ2_XXS || F == IQ2_XS ? r.a[2] : r.a[1];
+    s.a[1] = r.a[3];
+    if (F == IQ2_S) s.a[2] = r.a[3];
+    if (F == IQ1_S || F == IQ1_M) s.a[2] = r.a[2] >> 16;
+  }
+  const int lo = i & 3;
+  if (F == IQ2_XS) {
+    s.a[0] = (lo & 2 ? s.a[1] : s.a[0]) >> (16 * (lo & 1));
+    s.s = r.s >> (4 * (i >> 1));
+  } else {
+    s.a[0] >>= 8 * lo;
+    if (F == IQ2_XXS) s.a[1] = ((s.a[1] >> (7 * lo)) & 127u) | (s.a[1] & 0xf0000000u);
+    if (F == IQ2_S) {
+      s.a[2] >>= 8 * lo;
+      s.s = ((r.s >> (2 * i)) & 3u) | ((r.s >> (4 * (i >> 1))) & 0xffff0000u);
+    }
+    if (F == IQ1_S) s.a[2] = ((s.a[2] >> (3 * lo)) & 7u) | (s.a[2] & 0xf000u);
+    if (F == IQ1_M) {
+      s.a[2] >>= 4 * lo;
+      s.s = r.s >> (3 * (i >> 1));
+    }
+  }
+  Entry t;
+  t.g = group_fields<F>(s, 0);
+  t.e = tab[t.g.k];
+  t.keep = keep;
+  return t;
+}
+
 // ---------------------------------------------------------------------------
 // Many tokens: a workgroup's weights are decoded once and reach its waves through
 // LDS.  WT token groups of C tiles by WR row groups of R row tiles, half of them of
 // the gate and half of the up projection, so that a wave's registers end up with
-// both sums of an output.  A stage is KS steps of 32 columns; each wave decodes
-// R / WT row tiles of the next stage while the matrix cores work on this one.
-// Weights are the A operand here: a lane has four consecutive rows of one token.
+// both sums of an output.  Weights are the A operand here: a lane has four
+// consecutive rows of one token.
+//
+// A stage is a step of 32 columns.  While the matrix cores work on stage s, the wave
+// decodes its R / WT row tiles of stage s + 2 between their instructions and the
+// tokens of stage s + 3 are on their way to LDS; its operands are read a group of W
+// row tiles ahead, the first of a stage before the barrier that opens it (its buffers
+// were full a barrier earlier), so that no wave waits for LDS at a barrier.
+//
 // Sums are kept in units of the block's d, as in iq_linear's prompts (P == 1); for
 // f32 tokens a block has sums of its own, which are scaled and added (kept in one sum,
 // 5,120 columns came to 1e-6 of h in the norm, near twice 32-bit arithmetic's).
 // ---------------------------------------------------------------------------
 template <int F, int P, int WT, int WR, int C, int R>
 __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(GluArgs A) {
-  constexpr int NW = WT * WR, KS = 2 / P, NS = 8 / KS, DR = R / WT, TA = WT * C, TB = WR * R;
-  static_assert(R % WT == 0 && R % 2 == 0, "whole row tiles to decode, as many of either weight");
+  constexpr int NW = WT * WR, DR = R / WT, TA = WT * C, TB = WR * R;
+  constexpr int W = R < 4 ? R : 4, NG = R / W;               // groups of row tiles whose operands are read together
+  constexpr int NP = TA * P, NPW = (NP + NW - 1) / NW;       // pieces of 1 KiB of a stage's tokens, a wave's share
+  static_assert(R % WT == 0 && R % 2 == 0 && R % W == 0, "whole row tiles to decode, as many of either weight");
+  static_assert(NP % NW == 0 || NP < NW, "waves wait for the same number of loads, or have none");
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ u32x4 s_a[2][TA * P * KS * 64];  // tokens [tile][part][step][lane]
-  __shared__ u32x4 s_b[2][TB * KS * 64];      // weights [tile][step][lane]
+  __shared__ u32x4 s_a[4][NP * 64];  // tokens [stage % 4][tile][part][lane]
+  __shared__ u32x4 s_b[3][TB * 64];  // weights [stage % 3][tile][lane]
   __shared__ f32x4 s_ratio[2][TB * 4], s_unit[TB * 4];
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / WR, wr = wave % WR;
   const int64_t rblk = static_cast<int64_t>(blockIdx.x) * (TB / 2) * 16;  // first row of the workgroup
   const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * TA, rowbytes = A.nb * Geo<F>::BYTES;
+  const int stages = static_cast<int>(A.nb) * 8;
   // Tile i of the workgroup: row group i / R, within it R / 2 tiles of the gate, then of the up projection.
   const auto tile_row = [&](int i) { return rblk + ((i / R) * (R / 2) + i % R % (R / 2)) * 16; };
   const uint8_t *rp[DR];
@@ -284,23 +335,30 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
     const int ti = wave * DR + i;
     rp[i] = A.packed[ti % R / (R / 2)] + min(tile_row(ti) + n, A.rows - 1) * rowbytes;
   }
-  const auto fetch = [&](int64_t b, int sub, int buf) __attribute__((always_inline)) {
+  const char *xbase = reinterpret_cast<const char *>(A.X.x16) + tt0 * P * 8192;
+  const int64_t xblock = A.X.ntile * P * 8192;  // bytes of a block of columns
+  uint32_t xoff[NPW];
 #pragma unroll
-    for (int i0 = 0; i0 < TA * P * KS; i0 += NW) {
-      const int i = i0 + wave;
-      if (TA * P * KS % NW && i >= TA * P * KS) break;
-      const int64_t tile = min(tt0 + i / (P * KS), A.X.ntile - 1);
-      const u32x4 *from = reinterpret_cast<const u32x4 *>(A.X.x16) +
-                          ((b * A.X.ntile + tile) * P + i / KS % P) * 512 + (sub * KS + i % KS) * 64 + lane;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                       (__attribute__((address_space(3))) void *)&s_a[buf][i * 64], 16, 0, 0);
-    }
+  for (int i = 0; i < NPW; ++i) {
+    const int p = i * NW + wave, most = static_cast<int>(min(A.X.ntile - tt0, static_cast<int64_t>(TA))) - 1;
+    xoff[i] = static_cast<uint32_t>((min(p / P, most) * P + p % P) * 8192 + lane * 16);
+  }
+  const auto fetch = [&](int s) __attribute__((always_inline)) {
+    const char *from = xbase + (s >> 3) * xblock + (s & 7) * 1024;
+#pragma unroll
+    for (int i = 0; i < NPW; ++i)
+      if (NP % NW == 0 || i * NW + wave < NP) load_to_lds(from, xoff[i], &s_a[s & 3][(i * NW + wave) * 64]);
   };
   Words words[DR];
   Raw raw[DR];
   float unit[DR];
   uint32_t keep[DR];
-  // The block whose words are there becomes the one to decode; its d against the one before.
+  const auto load_block = [&](int64_t b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < DR; ++i) words[i] = load_words<F>(rp[i] + min(b, A.nb - 1) * Geo<F>::BYTES, q);
+  };
+  // The block whose words are there becomes the one to decode; its d against the one before.  (Past the last block
+  // the last comes again, which changes nothing that is read.)
   const auto open_block = [&](int par) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < DR; ++i) {
@@ -312,110 +370,157 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
       if (q == 0) reinterpret_cast<float *>(s_ratio[par])[(wave * DR + i) * 16 + n] = ratio;
     }
   };
-  const auto decode = [&](int sub, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int i = 0; i < DR; ++i)
-        s_b[buf][((wave * DR + i) * KS + k) * 64 + lane] =
-            __builtin_bit_cast(u32x4, group_half8<F>(raw[i], sub * KS + k, s_tab, keep[i]));
+  const auto put_weights = [&](const Entry &t, int i, int buf) __attribute__((always_inline)) {
+    s_b[buf][(wave * DR + i) * 64 + lane] = __builtin_bit_cast(u32x4, weights_half8<F>(t.g, t.e, t.keep));
   };
+  half8v x[2][C][P], w[2][W];
+  const auto read_x = [&](int u, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int p = 0; p < P; ++p) x[u][c][p] = __builtin_bit_cast(half8v, s_a[s & 3][((wt * C + c) * P + p) * 64 + lane]);
+  };
+  const auto read_w = [&](int u, int g, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[u][i] = __builtin_bit_cast(half8v, s_b[buf][(wr * R + g * W + i) * 64 + lane]);
+  };
+
   f32x4 acc[R][C], part[P == 2 ? R : 1][C];  // part: a block's sums
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < DR; ++i) {
-    unit[i] = 0.0f;
-    words[i] = load_words<F>(rp[i], q);
-  }
-  fetch(0, 0, 0);
+  for (int i = 0; i < DR; ++i) unit[i] = 0.0f;
+  load_block(0);
+  fetch(0);
+  fetch(1);
+  fetch(2);
   __syncthreads();  // the codebook
   open_block(0);
-  decode(0, 0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the barrier does not wait for loads into LDS
+  load_block(1);
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int i = 0; i < DR; ++i) put_weights(lookup<F>(raw[i], d, s_tab, keep[i]), i, d);
+  Entry t[DR];  // begun: the row tiles of stage s + 2
+#pragma unroll
+  for (int i = 0; i < DR; ++i) t[i] = lookup<F>(raw[i], 2, s_tab, keep[i]);
+  wait_loads<0>();
   __syncthreads();
-  for (int64_t b = 0; b < A.nb; ++b) {
-    const int par = static_cast<int>(b) & 1;
-    f32x4 ratio[R];
+  read_x(0, 0);
+  read_w(0, 0, 0);
+  // Of a SIMD's two waves the first goes first: while it works on its addresses the other has the matrix cores.
+  if (wave < NW / 2) __builtin_amdgcn_s_setprio(1);
+  int b0 = 0, b1 = 1, b2 = 2;  // buffers of the weights of stages s, s + 1, s + 2
+  const auto stage = [&](auto parity, int s) __attribute__((always_inline)) {
+    constexpr int U = decltype(parity)::value;
+    const int d = s + 2;
+    if ((s & 7) == 0) {
+      const int par = (s >> 3) & 1;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      ratio[r] = s_ratio[par][(wr * R + r) * 4 + q];
+      for (int r = 0; r < R; ++r) {
+        const f32x4 f = s_ratio[par][(wr * R + r) * 4 + q];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (P == 2)
-          part[r % (P == 2 ? R : 1)][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        else
-          acc[r][c] *= ratio[r];
-      }
-    }
-#pragma unroll
-    for (int sub = 0; sub < NS; ++sub) {
-      const int cur = sub & 1;
-      const bool last = b + 1 == A.nb && sub + 1 == NS;
-      if (!last) fetch(sub + 1 == NS ? b + 1 : b, (sub + 1) % NS, cur ^ 1);
-      if (sub == 0) {
-        const int64_t bn = min(b + 1, A.nb - 1);
-#pragma unroll
-        for (int i = 0; i < DR; ++i) words[i] = load_words<F>(rp[i] + bn * Geo<F>::BYTES, q);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below
-      if (!last) {
-        if (sub + 1 == NS) open_block(par ^ 1);
-        decode((sub + 1) % NS, cur ^ 1);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        half8v x[C][P];
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            x[c][p] = __builtin_bit_cast(half8v, s_a[cur][(((wt * C + c) * P + p) * KS + k) * 64 + lane]);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const half8v w = __builtin_bit_cast(half8v, s_b[cur][((wr * R + r) * KS + k) * 64 + lane]);
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              f32x4 &to = P == 2 ? part[r % (P == 2 ? R : 1)][c] : acc[r][c];
-              to = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x[c][p], to, 0, 0, 0);
-            }
+        for (int c = 0; c < C; ++c) {
+          if (P == 2)
+            part[r % (P == 2 ? R : 1)][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          else
+            acc[r][c] *= f;
         }
       }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();  // the next stage is there, this one free
     }
-    if (P == 2)
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int g = 0; g < NG; ++g) {
+      constexpr int first = U * NG;  // groups alternate between two sets of registers
+      // Before the last group's products the next stage's first operands and entries are requested.
+      if (g + 1 < NG) {
+        read_w((first + g + 1) & 1, g + 1, b0);
+      } else {
+        read_x(U ^ 1, s + 1);
+        read_w((first + g + 1) & 1, 0, b1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < DR; ++i)
+        if (i * NG / DR == g) put_weights(t[i], i, b2);
+#pragma unroll
+      for (int i = 0; i < W; ++i)
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[r][c][k] = fmaf(ratio[r][k], part[r % (P == 2 ? R : 1)][c][k], acc[r][c][k]);
+          for (int p = 0; p < P; ++p) {
+            f32x4 &to = P == 2 ? part[(g * W + i) % (P == 2 ? R : 1)][c] : acc[g * W + i][c];
+            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[(first + g) & 1][i], x[U][c][p], to, 0, 0, 0);
+          }
+      __builtin_amdgcn_sched_barrier(0);
+      if (g == 0) {
+        if ((d & 7) == 1 && s > 0) load_block((d >> 3) + 1);
+        if (s + 3 < stages) fetch(s + 3);
+      }
+    }
+    if (((d + 1) & 7) == 0) open_block(((d + 1) >> 3) & 1);
+#pragma unroll
+    for (int i = 0; i < DR; ++i) t[i] = lookup<F>(raw[i], (d + 1) & 7, s_tab, keep[i]);
+    if (P == 2 && (s & 7) == 7) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const f32x4 f = s_ratio[(s >> 3) & 1][(wr * R + r) * 4 + q];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[r][c][k] = fmaf(f[k], part[r % (P == 2 ? R : 1)][c][k], acc[r][c][k]);
+      }
+    }
+    if (s + 3 < stages)
+      wait_loads<NPW>();
+    else
+      wait_loads<0>();
+    __syncthreads();
+    const int old = b0;
+    b0 = b1;
+    b1 = b2;
+    b2 = old;
+  };
+  for (int s = 0; s < stages; s += 2) {
+    stage(std::integral_constant<int, 0>{}, s);
+    stage(std::integral_constant<int, 1>{}, s + 1);
   }
 #pragma unroll
   for (int i = 0; i < DR; ++i)
     if (q == 0) reinterpret_cast<float *>(s_unit)[(wave * DR + i) * 16 + n] = unit[i];
   __syncthreads();
+  // A token tile's sums at a time through LDS, in which a lane finds eight rows of one token; one copy of the code
+  // for all of them (16 in a row were 160 KB of instructions, and took as long as twelve stages).
+  static_assert(4 * NP >= NW * R, "a wave's sums of a token tile fit");
   const int ew = A.dh ? weight_exponent(A.B) : 0;
-#pragma unroll
+  f32x4 *own = reinterpret_cast<f32x4 *>(s_a) + wave * R * 64;
+#pragma unroll 1
   for (int c = 0; c < C; ++c) {
-    const int64_t t = (tt0 + wt * C + c) * 16 + n;
-    if (t >= A.T) continue;
-    const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
-    if (A.dh && rblk == 0 && wr == 0 && q == 0) A.G.ex[t] = -ng;
 #pragma unroll
-    for (int r = 0; r < R / 2; ++r) {
-      f32x4 g = acc[r][c] * s_unit[(wr * R + r) * 4 + q], u = acc[R / 2 + r][c] * s_unit[(wr * R + R / 2 + r) * 4 + q];
+    for (int k = 0; k < C; ++k) {
+      if (k != c) continue;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        g[k] = ldexpf(g[k], e);
-        u[k] = ldexpf(u[k], e);
+      for (int r = 0; r < R; ++r) own[r * 64 + lane] = acc[r][k] * s_unit[(wr * R + r) * 4 + q];
+    }
+#pragma unroll 1
+    for (int i = lane; i < 16 * R; i += 64) {
+      const int m = i & 15, o = i >> 4;  // token, and its eight rows
+      const int64_t t = (tt0 + wt * C + c) * 16 + m, row = tile_row(wr * R) + o * 8;
+      if (t >= A.T || row >= (A.dh ? row_chunks(A.rows) * 64 : A.rows)) continue;
+      const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
+      if (A.dh && row == 0) A.G.ex[t] = -ng;
+      float g[8], u[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // row tile o / 2, quarters 2 (o % 2) + h
+        const f32x4 *at = own + (o >> 1) * 64 + ((o & 1) * 2 + h) * 16 + m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          g[h * 4 + k] = ldexpf(at[0][k], e);
+          u[h * 4 + k] = ldexpf(at[R / 2 * 64][k], e);
+        }
       }
-      put4(A, ng, t, tile_row(wr * R + r) + 4 * q, g, u);
+      put8(A, ng, t, row, g, u);
     }
   }
 }
@@ -441,7 +546,7 @@ void launch_tile(const GluArgs &A, hipStream_t stream) {
 template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
   if (A.X.ntile == 1) return launch_split<F, P, 1>(A, stream);
   if (A.X.ntile <= 8) return launch_tile<F, P, 1, 8, 4, 2>(A, stream);
-  constexpr int C = P == 2 ? 2 : Geo<F>::N > 1024 ? 3 : 4;
+  constexpr int C = P == 2 ? 2 : 4;
   launch_tile<F, P, 4, 2, C, 8>(A, stream);
 }
 

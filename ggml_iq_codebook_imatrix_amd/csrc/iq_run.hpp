@@ -240,43 +240,51 @@ template <int F> __device__ __forceinline__ float block_scale(const Raw &r) {
 // Which of a group's eight values the operands' element h holds.
 __device__ constexpr int kept_at(int h) { return (h >> 1) + 4 * (h & 1); }
 
-// m * v of group 8q + i as eight fp16 values (tab: the codebook in fp16); zeros
-// where keep is 0 instead of all ones.
-template <int F>
-__device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab, uint32_t keep = ~0u) {
-  uint32_t k, ls, mask = 0, h = 0;
+// The fields of one group: codebook entry, multiplier, signs (IQ2) or shift (IQ1).
+struct GroupFields {
+  uint32_t k, ls, mask, h;
+};
+template <int F> __device__ __forceinline__ GroupFields group_fields(const Raw &r, int i) {
+  GroupFields g{};
   if (F == IQ2_XXS) {
     const uint32_t word = r.a[2 * (i >> 2) + 1];
-    k = (r.a[2 * (i >> 2)] >> (8 * (i & 3))) & 255u;
-    mask = (word >> (7 * (i & 3))) & 127u;
-    ls = word >> 28;
+    g.k = (r.a[2 * (i >> 2)] >> (8 * (i & 3))) & 255u;
+    g.mask = (word >> (7 * (i & 3))) & 127u;
+    g.ls = word >> 28;
   } else if (F == IQ2_XS) {
     const uint32_t v = r.a[i >> 1] >> (16 * (i & 1));
-    k = v & 511u;
-    mask = (v >> 9) & 127u;
-    ls = (r.s >> (4 * (i >> 1))) & 15u;
+    g.k = v & 511u;
+    g.mask = (v >> 9) & 127u;
+    g.ls = (r.s >> (4 * (i >> 1))) & 15u;
   } else if (F == IQ2_S) {
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((r.s >> (2 * i)) & 3u) << 8);
-    mask = (r.a[2 + (i >> 2)] >> (8 * (i & 3))) & 255u;
-    ls = (r.s >> (16 + 4 * (i >> 1))) & 15u;
+    g.k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((r.s >> (2 * i)) & 3u) << 8);
+    g.mask = (r.a[2 + (i >> 2)] >> (8 * (i & 3))) & 255u;
+    g.ls = (r.s >> (16 + 4 * (i >> 1))) & 15u;
   } else if (F == IQ1_S) {
     const uint32_t w = r.a[2] >> (16 * (i >> 2));
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((w >> (3 * (i & 3))) & 7u) << 8);
-    ls = (w >> 12) & 7u;
-    h = (w >> 15) & 1u;
+    g.k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | (((w >> (3 * (i & 3))) & 7u) << 8);
+    g.ls = (w >> 12) & 7u;
+    g.h = (w >> 15) & 1u;
   } else {
     const uint32_t nib = r.a[2] >> (4 * i);
-    k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | ((nib & 7u) << 8);
-    h = (nib >> 3) & 1u;
-    ls = (r.s >> (3 * (i >> 1))) & 7u;
+    g.k = ((r.a[i >> 2] >> (8 * (i & 3))) & 255u) | ((nib & 7u) << 8);
+    g.h = (nib >> 3) & 1u;
+    g.ls = (r.s >> (3 * (i >> 1))) & 7u;
   }
-  const uint4 e = tab[k];
-  const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * ls + 1));
+  return g;
+}
+
+// m * v of a group as eight fp16 values (e: its codebook entry in fp16); zeros
+// where keep is 0 instead of all ones.
+template <int F>
+__device__ __forceinline__ half8v weights_half8(const GroupFields &g, const uint4 &e, uint32_t keep) {
+  uint32_t mask = g.mask;
+  const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * g.ls + 1));
   const half2v m2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, half2v{m, m}) & keep);
   uint32_t o[4] = {e.x, e.y, e.z, e.w};
   if (Geo<F>::IQ1) {
     const half2v up = m2 * static_cast<_Float16>(0.125f);
-    const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (h * 0x80008000u));
+    const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (g.h * 0x80008000u));
 #pragma unroll
     for (int p = 0; p < 4; ++p)  // m g + m delta, rounded once
       o[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
@@ -294,6 +302,13 @@ __device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *
     }
   }
   return __builtin_bit_cast(half8v, make_uint4(o[0], o[1], o[2], o[3]));
+}
+
+// The same of group 8q + i (tab: the codebook).
+template <int F>
+__device__ __forceinline__ half8v group_half8(const Raw &r, int i, const uint4 *tab, uint32_t keep = ~0u) {
+  const GroupFields g = group_fields<F>(r, i);
+  return weights_half8<F>(g, tab[g.k], keep);
 }
 
 template <int F> __device__ __forceinline__ void load_table(uint4 *s_tab, const _Float16 *tab) {

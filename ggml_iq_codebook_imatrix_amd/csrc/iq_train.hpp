@@ -156,6 +156,18 @@ __device__ __forceinline__ uint32_t row_exponent(const void *x, int dtype, int64
   return wave_max_u32(e);
 }
 
+// 64 lanes' 16 bytes each, from base + off on, to 1 KiB of LDS (base and `to` the same in all lanes).  The compiler
+// takes every later read of LDS for one of these bytes and waits for them, which is a memory's latency lost in each
+// round of a buffer; written out, they are waited for where the buffers change (wait_loads), and by nothing before.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, void *to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)to)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(at)
+               : "memory");
+}
+// All loads but the wave's last N (in the order of their issue).
+template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
 // A wave's maximum into LDS, the workgroup's into *out (NW waves).
 template <int NW> __device__ __forceinline__ void workgroup_max(uint32_t v, uint32_t *red, uint32_t *out) {
   const uint32_t m = wave_max_u32(v);
