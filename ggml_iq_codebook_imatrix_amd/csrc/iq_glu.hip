@@ -254,6 +254,116 @@ __global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
   }
 }
 
+// load_words loads at least so many times.
+constexpr int kWordLoads = 2;
+
+// ---------------------------------------------------------------------------
+// A batch of tokens: a wave has one row tile of one weight, RT row tiles of both are
+// a workgroup, and all its C token tiles meet a weight in the registers of the wave
+// that decoded it.  The tokens of half a block lie in LDS for all waves, the next
+// half's on their way.  d scales a block's sums.
+// ---------------------------------------------------------------------------
+template <int F, int P, int C, int RT>
+__global__ void __launch_bounds__(128 * RT, RT < 4 ? 2 : RT / 2) glu_batch_kernel(GluArgs A) {
+  constexpr int NW = 2 * RT, NP = C * P * 4, NPW = (NP + NW - 1) / NW;  // pieces of 1 KiB of half a block's tokens
+  constexpr int kX = 2 * NP * 64, kRed = NW * C * 64;
+  __shared__ uint4 s_tab[Geo<F>::N];
+  __shared__ u32x4 s_x[kX > kRed ? kX : kRed];  // [half % 2][tile][part][step][lane]
+  const uint32_t x_at = IQ_LDS_ADDRESS(s_x);
+  load_table<F>(s_tab, A.tab);
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = wave & 1, rt = wave >> 1;
+  const int64_t rblk = static_cast<int64_t>(blockIdx.x) * (16 * RT), tt0 = static_cast<int64_t>(blockIdx.y) * C;
+  const uint8_t *rp = A.packed[m] + min(rblk + rt * 16 + n, A.rows - 1) * A.nb * Geo<F>::BYTES;
+  const char *xbase = reinterpret_cast<const char *>(A.X.x16) + tt0 * P * 8192;
+  const int64_t xblock = A.X.ntile * P * 8192;
+  uint32_t xoff[NPW];
+#pragma unroll
+  for (int i = 0; i < NPW; ++i) {
+    const int p = i * NW + wave, most = static_cast<int>(min(A.X.ntile - tt0, static_cast<int64_t>(C))) - 1;
+    xoff[i] = static_cast<uint32_t>((min(p / (P * 4), most) * P + p / 4 % P) * 8192 + p % 4 * 1024 + lane * 16);
+  }
+  const auto fetch = [&](int64_t b, int half) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NPW; ++i)
+      if (NP % NW == 0 || i * NW + wave < NP)
+        load_to_lds(xbase + b * xblock + half * 4096, xoff[i], x_at + (half * NP + i * NW + wave) * 1024);
+  };
+  f32x4 acc[C], part[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = part[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  Words words = load_words<F>(rp, q);
+  fetch(0, 0);
+  wait_loads<0>();
+  __syncthreads();
+  for (int64_t b = 0; b < A.nb; ++b) {
+    const Raw raw = unpack<F>(words, q);
+    half8v w[2];
+    w[0] = group_half8<F>(raw, 0, s_tab);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half == 0)
+        fetch(b, 1);
+      else if (b + 1 < A.nb)
+        fetch(b + 1, 0);
+      // after the tokens, which are waited for first: the payload comes from further away
+      if (half == 0) words = load_words<F>(rp + min(b + 1, A.nb - 1) * Geo<F>::BYTES, q);
+      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below
+      const u32x4 *xs = s_x + half * NP * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int g = half * 4 + i;
+        half8v x[C][P];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int p = 0; p < P; ++p) x[c][p] = __builtin_bit_cast(half8v, xs[((c * P + p) * 4 + i) * 64]);
+        if (g < 7) w[(g + 1) & 1] = group_half8<F>(raw, g + 1, s_tab);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            part[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[c][p], w[g & 1], part[c], 0, 0, 0);
+      }
+      if (half == 1) {
+        const float d = block_scale<F>(raw);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          scale_add(acc[c], part[c], d);
+          part[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
+      if (half == 0)
+        wait_loads<kWordLoads>();
+      else
+        wait_loads<0>();
+      __syncthreads();  // the next half is there, this one free
+    }
+  }
+  // both sums of an output in one lane: tile [row tile][weight][token tile], lane l's row l % 16, tokens 4 (l / 16) + k
+  const float *all = reinterpret_cast<const float *>(s_x);
+#pragma unroll
+  for (int c = 0; c < C; ++c) s_x[((rt * 2 + m) * C + c) * 64 + lane] = __builtin_bit_cast(u32x4, acc[c]);
+  __syncthreads();
+  const int ew = A.dh ? weight_exponent(A.B) : 0;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 32 * RT * C; i += 64 * NW) {
+    const int o = i % (2 * RT), tok = i / (2 * RT) & 15, c = i / (32 * RT);  // eight rows, token, token tile
+    const int64_t t = (tt0 + c) * 16 + tok, row = rblk + o * 8;
+    if (t >= A.T || row >= (A.dh ? row_chunks(A.rows) * 64 : A.rows)) continue;
+    const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
+    if (A.dh && row == 0) A.G.ex[t] = -ng;
+    const float *at = all + (((o >> 1) * 2 * C + c) * 64 + (tok >> 2) * 16 + (o & 1) * 8) * 4 + (tok & 3);
+    float g[8], u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[k] = ldexpf(at[k * 4], e);
+      u[k] = ldexpf(at[C * 256 + k * 4], e);
+    }
+    put8(A, ng, t, row, g, u);
+  }
+}
+
 // weights_half8 begun: the fields of group i, which is the same in all lanes but not known to the compiler, and its
 // codebook entry, which comes from LDS some time later.
 struct Entry {
@@ -321,6 +431,7 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
   __shared__ u32x4 s_a[4][NP * 64];  // tokens [stage % 4][tile][part][lane]
   __shared__ u32x4 s_b[3][TB * 64];  // weights [stage % 3][tile][lane]
   __shared__ f32x4 s_ratio[2][TB * 4], s_unit[TB * 4];
+  const uint32_t x_at = IQ_LDS_ADDRESS(s_a);
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / WR, wr = wave % WR;
@@ -343,11 +454,17 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
     const int p = i * NW + wave, most = static_cast<int>(min(A.X.ntile - tt0, static_cast<int64_t>(TA))) - 1;
     xoff[i] = static_cast<uint32_t>((min(p / P, most) * P + p % P) * 8192 + lane * 16);
   }
-  const auto fetch = [&](int s) __attribute__((always_inline)) {
-    const char *from = xbase + (s >> 3) * xblock + (s & 7) * 1024;
+  // Stages in turn, each call the next (past the last some bytes that are not read).
+  const char *xnext = xbase;
+  int fetched = 0;
+  const auto fetch = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NPW; ++i)
-      if (NP % NW == 0 || i * NW + wave < NP) load_to_lds(from, xoff[i], &s_a[s & 3][(i * NW + wave) * 64]);
+      if (NP % NW == 0 || i * NW + wave < NP)
+        load_to_lds(xnext, xoff[i], x_at + ((fetched & 3) * NP + i * NW + wave) * 1024);
+    ++fetched;
+    xnext += 1024;
+    if ((fetched & 7) == 0) xnext += fetched < stages ? xblock - 8192 : -8192;
   };
   Words words[DR];
   Raw raw[DR];
@@ -393,9 +510,9 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
 #pragma unroll
   for (int i = 0; i < DR; ++i) unit[i] = 0.0f;
   load_block(0);
-  fetch(0);
-  fetch(1);
-  fetch(2);
+  fetch();
+  fetch();
+  fetch();
   __syncthreads();  // the codebook
   open_block(0);
   load_block(1);
@@ -456,7 +573,7 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
       __builtin_amdgcn_sched_barrier(0);
       if (g == 0) {
         if ((d & 7) == 1 && s > 0) load_block((d >> 3) + 1);
-        if (s + 3 < stages) fetch(s + 3);
+        fetch();
       }
     }
     if (((d + 1) & 7) == 0) open_block(((d + 1) >> 3) & 1);
@@ -472,10 +589,12 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
           for (int k = 0; k < 4; ++k) acc[r][c][k] = fmaf(f[k], part[r % (P == 2 ? R : 1)][c][k], acc[r][c][k]);
       }
     }
-    if (s + 3 < stages)
-      wait_loads<NPW>();
+    // The tokens of stage s + 2 have to be there; what was requested after them may be on its way: those of stage
+    // s + 3, and in one stage of eight the next block's payload, which comes from further away.
+    if (s > 0 && (d & 7) == 1)
+      wait_loads<NPW + DR * kWordLoads>();
     else
-      wait_loads<0>();
+      wait_loads<NPW>();
     __syncthreads();
     const int old = b0;
     b0 = b1;
@@ -486,6 +605,7 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
     stage(std::integral_constant<int, 0>{}, s);
     stage(std::integral_constant<int, 1>{}, s + 1);
   }
+  wait_loads<0>();  // the memory is used again below
 #pragma unroll
   for (int i = 0; i < DR; ++i)
     if (q == 0) reinterpret_cast<float *>(s_unit)[(wave * DR + i) * 16 + n] = unit[i];
@@ -543,10 +663,46 @@ void launch_tile(const GluArgs &A, hipStream_t stream) {
                      dim3(64 * WT * WR), 0, stream, A);
 }
 
+template <int F, int P, int C, int RT> void launch_batch(const GluArgs &A, hipStream_t stream) {
+  const int64_t all = A.dh ? row_chunks(A.rows) * 64 : A.rows;
+  hipLaunchKernelGGL((glu_batch_kernel<F, P, C, RT>),
+                     dim3(static_cast<unsigned>((all + 16 * RT - 1) / (16 * RT)),
+                          static_cast<unsigned>((A.X.ntile + C - 1) / C)),
+                     dim3(128 * RT), 0, stream, A);
+}
+
+// What a batch costs with RT row tiles a workgroup: the rounds of its workgroups over 256 CUs times a workgroup's
+// waves on a SIMD, in eighths.  Measured at 17,408 x 5,120 (IQ1_M) with RT = 2, 4, 6, us: 64 tokens 67, 59, 50 (3, 4 and
+// 3 waves on the fullest CU's SIMDs); 128 tokens 97, 89, 91; 256 tokens 158, 138, 132; at 5,632 x 2,048 (IQ2_S): 64
+// tokens 20, 23, 27; 128 tokens 25, 24, 27; 256 tokens 32, 35, 31.  So workgroups of two row tiles, which bring as many
+// tokens to LDS as others, count a quarter more where several share a CU (with two token tiles they do not: 39, 47,
+// 44 at 32 tokens), six a tenth.
+inline int64_t batch_cost(const GluArgs &A, int C, int RT) {
+  const int64_t rounds = ((A.rows + 16 * RT - 1) / (16 * RT) * ((A.X.ntile + C - 1) / C) + 255) / 256;
+  return rounds * (RT == 2 ? (rounds > 1 && C > 2 ? 10 : 8) : RT == 4 ? 16 : 26);
+}
+
+template <int F, int P, int C> void launch_batches(const GluArgs &A, hipStream_t stream) {
+  const int64_t two = batch_cost(A, C, 2), four = batch_cost(A, C, 4), six = batch_cost(A, C, 6);
+  if (two < four && two <= six) return launch_batch<F, P, C, 2>(A, stream);
+  if (four <= six) return launch_batch<F, P, C, 4>(A, stream);
+  launch_batch<F, P, C, 6>(A, stream);
+}
+
 template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
-  if (A.X.ntile == 1) return launch_split<F, P, 1>(A, stream);
-  if (A.X.ntile <= 8) return launch_tile<F, P, 1, 8, 4, 2>(A, stream);
+  const int64_t ntile = A.X.ntile;
+  if (ntile == 1) return launch_split<F, P, 1>(A, stream);
+  if (ntile == 2) return launch_batches<F, P, 2>(A, stream);
+  if (ntile == 3 || ntile == 5 || ntile == 6) return launch_batches<F, P, 3>(A, stream);
+  // Tiles, a workgroup a CU, take 16 us a round and 7.2 more for each block of columns; batches 0.08 and 0.09 (f32
+  // 0.155) of their cost.  5,632 x 2,048 (IQ2_S), batches and tiles, us: 500 tokens 49 and 83, 2,048 tokens 150 and
+  // 167, 4,096 tokens 286 and 244 (f32: 512 tokens 70 and 84, 2,048 tokens 228 and 236); 17,408 x 5,120 (IQ1_M): 512
+  // tokens 255 and 335, 1,024 tokens 493 and 522.
   constexpr int C = P == 2 ? 2 : 4;
+  int64_t batch = batch_cost(A, 4, 2);
+  for (int RT = 4; RT <= 6; RT += 2) batch = min(batch, batch_cost(A, 4, RT));
+  const int64_t rounds = ((A.rows + 127) / 128 * ((ntile + 4 * C - 1) / (4 * C)) + 255) / 256;
+  if (batch * (16 + (P == 2 ? 31 : 18) * A.nb) <= rounds * (3200 + 1440 * A.nb)) return launch_batches<F, P, 4>(A, stream);
   launch_tile<F, P, 4, 2, C, 8>(A, stream);
 }
 

@@ -16,6 +16,8 @@
 // two fp16 values (f32, three products; the sums of four chunks are added to the whole
 // ones, so that fewer additions round at a whole sum's size).
 
+#include <type_traits>
+
 #include "iq_train.hpp"
 
 namespace iq {
@@ -91,14 +93,23 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
 }
 
 // Waves: 4 token groups (of C tiles) by H halves of a block's columns.  LORA: with adapters.
+//
+// A stage is a step of 32 rows, a chunk two.  Chunk c + 1 is decoded in the odd stage of chunk c - 1 (a thread's first
+// two rows) and the even stage of chunk c (the others, and both pairs to LDS).  Its payload is requested in an odd
+// stage NA chunks before chunk c + 1's, and the gradients NA - 1 stages ahead.  As in iq_glu's tiles the work stands between the matrix instructions, and
+// operands are read a group of four ahead, a stage's first before the barrier that opens it.
 template <int F, int P, int C, int H, bool LORA>
 __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
-  constexpr int NW = 4 * H, NT = 64 * NW, TA = 4 * C;
+  constexpr int NW = 4 * H, NT = 64 * NW, TA = 4 * C, NP = TA * P, NPW = (NP + NW - 1) / NW;
+  constexpr int NA = Geo<F>::N > 512 ? 3 : 4;  // stages of gradients in LDS, beside a large codebook one fewer
   constexpr int W = (Geo<F>::BYTES + 5) / 4, NR = (64 * W + NT - 1) / NT;  // words of a row's block, a thread's share
+  constexpr int NB = NA - 1;                    // chunks of payload in LDS
+  static_assert(NP % NW == 0 || NP < NW, "waves wait for the same number of loads, or have none");
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ u32x4 s_a[2][TA * P * 2 * 64];   // [tile][part][step][lane]
-  __shared__ u32x4 s_b[2][H * 8 * P * 2 * 64];  // [half][column j][part][step][lane]
-  __shared__ uint32_t s_raw[2][64 * W];
+  __shared__ u32x4 s_a[NA][NP * 64];            // [stage % NA][tile][part][lane]
+  __shared__ u32x4 s_b[2][2][H * 8 * P * 64];   // [chunk % 2][step][half][column j][part][lane]
+  __shared__ uint32_t s_raw[NB][NR * NT];       // [chunk % NB][row][word]
+  const uint32_t grad_at = IQ_LDS_ADDRESS(s_a), raw_at = IQ_LDS_ADDRESS(s_raw);
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / H, wh = wave % H;
@@ -106,63 +117,72 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   const int half0 = H == 2 ? 0 : static_cast<int>(blockIdx.x & 1);  // the first half that the workgroup takes
   const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * TA;
   const int64_t per = (A.rows + 63) / 64, chunks = per * A.nmat;
-  const int64_t share = (chunks + A.splits - 1) / A.splits, ch0 = blockIdx.z * share, ch1 = min(ch0 + share, chunks);
+  const int64_t share = (chunks + A.splits - 1) / A.splits, ch0 = blockIdx.z * share;
+  const int count = static_cast<int>(max(min(share, chunks - ch0), static_cast<int64_t>(0)));
   const int ew = weight_exponent(A.B);
-  const float unit = ldexpf(1.0f, 15 - ew - (Geo<F>::IQ1 ? 0 : 3));
+  const int unit = 15 - ew - (Geo<F>::IQ1 ? 0 : 3);
   const uint8_t *const p0 = A.packed[0] + cb * Geo<F>::BYTES, *const p1 = A.packed[A.nmat - 1] + cb * Geo<F>::BYTES;
 
-  // Chunk ch's blocks, whole aligned words; rows past the last read the last's.
-  uint32_t raw[NR];
-  const auto load_raw = [&](int64_t ch) __attribute__((always_inline)) {
-    const bool second = ch >= per;
-    const uint8_t *base = second ? p1 : p0;
-    const int64_t row0 = (second ? ch - per : ch) * 64;
+  // The first row of chunk c of the workgroup's, and its weight's payload; past the last chunk the last.
+  const auto chunk_of = [&](int c, const uint8_t *&base) __attribute__((always_inline)) {
+    const int64_t ch = ch0 + min(c, count - 1);
+    base = ch >= per ? p1 : p0;
+    return (ch >= per ? ch - per : ch) * 64;
+  };
+  // Its blocks, whole aligned words (rows past the last read the last's) into buffer `buf`.
+  const auto fetch_raw = [&](int c, int buf) __attribute__((always_inline)) {
+    const uint8_t *base;
+    const int64_t row0 = chunk_of(c, base);
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int u = i * NT + static_cast<int>(threadIdx.x);
-      if (64 * W % NT && u >= 64 * W) break;
-      const int r = u / W, w = u % W;
+      const int u = i * NT + static_cast<int>(threadIdx.x), r = min(u / W, 63), w = u % W;
       const uintptr_t at = reinterpret_cast<uintptr_t>(base + min(row0 + r, A.rows - 1) * rowbytes);
       const int last = (static_cast<int>(at & 2) + Geo<F>::BYTES - 1) >> 2;
-      raw[i] = ldw<uint32_t>((at & ~uintptr_t(3)) + 4 * min(w, last));
+      load_words_to_lds((at & ~uintptr_t(3)) + 4 * min(w, last), raw_at + ((buf * NR + i) * NT + wave * 64) * 4);
     }
   };
-  const auto store_raw = [&](int buf) __attribute__((always_inline)) {
+  // Stage s of the gradients into buffer `buf`.
+  const char *gbase = reinterpret_cast<const char *>(A.G.g16) + (ch0 * A.G.ntile + tt0) * P * 2048;
+  const int64_t gchunk = A.G.ntile * P * 2048;
+  uint32_t goff[NPW];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int u = i * NT + static_cast<int>(threadIdx.x);
-      if (64 * W % NT && u >= 64 * W) break;
-      s_raw[buf][u] = raw[i];
-    }
-  };
-  const auto fetch = [&](int64_t ch, int buf) __attribute__((always_inline)) {
+  for (int i = 0; i < NPW; ++i) {
+    const int p = i * NW + wave, most = static_cast<int>(min(A.G.ntile - tt0, static_cast<int64_t>(TA))) - 1;
+    goff[i] = static_cast<uint32_t>((min(p / P, most) * P + p % P) * 2048 + lane * 16);
+  }
+  const auto fetch = [&](int s, int buf) __attribute__((always_inline)) {
+    const char *from = gbase + (s >> 1) * gchunk + (s & 1) * 1024;
 #pragma unroll
-    for (int i0 = 0; i0 < TA * P * 2; i0 += NW) {
-      const int i = i0 + wave;
-      const int64_t tile = min(tt0 + i / (2 * P), A.G.ntile - 1);
-      const u32x4 *from = reinterpret_cast<const u32x4 *>(A.G.g16) + (ch * A.G.ntile + tile) * (P * 128) +
-                          (i % (2 * P)) * 64 + lane;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                       (__attribute__((address_space(3))) void *)&s_a[buf][i * 64], 16, 0, 0);
-    }
+    for (int i = 0; i < NPW; ++i)
+      if (NP % NW == 0 || i * NW + wave < NP) load_to_lds(from, goff[i], grad_at + (buf * NP + i * NW + wave) * 1024);
   };
-  // The thread's group and four rows of each chunk.
+  // The thread's group and four rows of each chunk: fields and entries of two rows at a time, weights, and both pairs
+  // of rows to operand [quad / 8][wave % H][column], lane 16 ((quad % 8) / 2) + n, half quad % 2.
   const int group = (half0 + wave % H) * 16 + n, quad = (wave / H) * 4 + q;
-  const auto decode = [&](int64_t ch, int buf) __attribute__((always_inline)) {
-    const bool second = ch >= per;
-    const uintptr_t base = reinterpret_cast<uintptr_t>(second ? p1 : p0);
-    const int64_t row0 = (second ? ch - per : ch) * 64;
-    uint32_t hi[4][4], lo[4][4];
+  Fields f[2];
+  uint4 e[2];
+  uint32_t hi[4][4], lo[4][4];
+  const auto read_rows = [&](int c, int j0, int buf) __attribute__((always_inline)) {
+    const uint8_t *base;
+    const int64_t row0 = chunk_of(c, base);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = min(row0 + quad * 4 + j, A.rows - 1);
-      const uint32_t off = static_cast<uint32_t>(base + r * rowbytes) & 2u;
-      const uint8_t *blk = reinterpret_cast<const uint8_t *>(&s_raw[buf][(quad * 4 + j) * W]) + off;
-      whole_weights<F, P>(read_fields<F>(blk, group), unit, s_tab, hi[j], lo[j]);
+    for (int j = 0; j < 2; ++j) {
+      const int r = quad * 4 + j0 + j;
+      const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base) + min(row0 + r, A.rows - 1) * rowbytes) & 2u;
+      f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + odd, group);
     }
-    // operand [wave % H][column][part][quad / 8], lane 16 ((quad % 8) / 2) + n, half quad % 2
-    uint2 *to = reinterpret_cast<uint2 *>(s_b[buf]) +
-                (((wave % H) * 8 * P * 2 + quad / 8) * 64 + (quad % 8) / 2 * 16 + n) * 2 + quad % 2;
+  };
+  const auto look_up = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) e[j] = s_tab[f[j].k];
+  };
+  const auto weigh = [&](int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) whole_weights<F, P>(f[j], e[j], unit, hi[j0 + j], lo[j0 + j]);
+  };
+  const auto put = [&](int c) __attribute__((always_inline)) {
+    uint2 *to = reinterpret_cast<uint2 *>(s_b[c & 1][quad / 8]) +
+                ((wave % H) * 8 * P * 64 + (quad % 8) / 2 * 16 + n) * 2 + quad % 2;
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -171,10 +191,25 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
         for (int part = 0; part < P; ++part) {
           const uint32_t(&v)[4][4] = part ? lo : hi;
-          to[((p + 4 * k) * P + part) * 256] = make_uint2(__builtin_amdgcn_perm(v[1][p], v[0][p], sel),
+          to[((p + 4 * k) * P + part) * 128] = make_uint2(__builtin_amdgcn_perm(v[1][p], v[0][p], sel),
                                                           __builtin_amdgcn_perm(v[3][p], v[2][p], sel));
         }
       }
+  };
+  constexpr int G = P == 1 ? 4 : 2, NG = 8 / G;  // columns whose operands are read together
+  half8v x[2][C][P], w[2][G][P];
+  const auto read_x = [&](int u, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int p = 0; p < P; ++p) x[u][c][p] = __builtin_bit_cast(half8v, s_a[buf][((wt * C + c) * P + p) * 64 + lane]);
+  };
+  const auto read_w = [&](int u, int g, int c, int step) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        w[u][j][p] = __builtin_bit_cast(half8v, s_b[c & 1][step][((wh * 8 + g * G + j) * P + p) * 64 + lane]);
   };
 
   f32x4 acc[8][C], part[P == 2 ? 8 : 1][C];
@@ -182,64 +217,106 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[j][c] = part[j % (P == 2 ? 8 : 1)][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (ch0 < ch1) {
-    load_raw(ch0);
-    fetch(ch0, 0);
-    store_raw(0);
-    load_raw(min(ch0 + 1, ch1 - 1));
-    __syncthreads();
-    decode(ch0, 0);
-    store_raw(1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the barrier does not wait for loads into LDS
-    __syncthreads();
-  }
-  for (int64_t ch = ch0; ch < ch1; ++ch) {
-    const int cur = static_cast<int>(ch - ch0) & 1;
-    if (ch + 1 < ch1) {
-      fetch(ch + 1, cur ^ 1);
-      load_raw(min(ch + 2, ch1 - 1));
-      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the work below
-      decode(ch + 1, cur ^ 1);
-    }
+  int a0 = 0;  // the buffer of the stage's gradients
+  const auto buffer = [&](int ahead) __attribute__((always_inline)) {
+    const int b = a0 + ahead;
+    return b >= NA ? b - NA : b;
+  };
+  int r1 = 1 % NB, r2 = 2 % NB;  // the buffers of the payload of chunks c + 1 and c + 2
+  const auto stage = [&](auto step, int c) __attribute__((always_inline)) {
+    constexpr int U = decltype(step)::value;
+    const int s = 2 * c + U, next = c + 1 + U;  // the chunk whose rows are decoded in this stage
+    read_rows(next, U ? 0 : 2, U ? r2 : r1);
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      half8v a[C][P];
+    for (int g = 0; g < NG; ++g) {
+      constexpr int first = U * NG;  // groups alternate between two sets of registers
+      if (g + 1 < NG) {
+        read_w((first + g + 1) & 1, g + 1, c, U);
+      } else {  // the next stage's first
+        read_x(U ^ 1, buffer(1));
+        read_w((first + g + 1) & 1, 0, c + U, U ^ 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (g + 1 == NG) {
+        weigh(U ? 0 : 2);
+        if (U == 0) put(next);
+      }
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int j = 0; j < G; ++j)
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          a[c][p] = __builtin_bit_cast(half8v, s_a[cur][(((wt * C + c) * P + p) * 2 + step) * 64 + lane]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        half8v b[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          b[p] = __builtin_bit_cast(half8v, s_b[cur][(((wh * 8 + j) * P + p) * 2 + step) * 64 + lane]);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          f32x4 &to = P == 2 ? part[j % (P == 2 ? 8 : 1)][c] : acc[j][c];
-          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[c][0], b[0], to, 0, 0, 0);
+        for (int cc = 0; cc < C; ++cc) {
+          f32x4 &to = P == 2 ? part[(g * G + j) % (P == 2 ? 8 : 1)][cc] : acc[g * G + j][cc];
+          const half8v(&ww)[P] = w[(first + g) & 1][j];
+          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][0], ww[0], to, 0, 0, 0);
           if (P == 2) {
-            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[c][P - 1], b[0], to, 0, 0, 0);
-            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[c][0], b[P - 1], to, 0, 0, 0);
+            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][P - 1], ww[0], to, 0, 0, 0);
+            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][0], ww[P - 1], to, 0, 0, 0);
           }
         }
+      __builtin_amdgcn_sched_barrier(0);
+      if (g == 0) {
+        look_up();
+        if (s + NA - 1 < 2 * count) fetch(s + NA - 1, buffer(NA - 1));
+        if (U == 1) fetch_raw(c + NA, r1);  // chunk c + 1's is decoded
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (P == 2 && (((ch - ch0) & 3) == 3 || ch + 1 == ch1)) {
+    if (P == 2 && U == 1 && ((c & 3) == 3 || c + 1 == count)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          f32x4 &p = part[j % (P == 2 ? 8 : 1)][c];
-          acc[j][c] += p;
+        for (int cc = 0; cc < C; ++cc) {
+          f32x4 &p = part[j % (P == 2 ? 8 : 1)][cc];
+          acc[j][cc] += p;
           p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
     }
-    if (ch + 1 < ch1) {
-      store_raw(cur);  // read by the decode before the last barrier
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
+    // What the stage after the next needs has to be there.  Four buffers: the gradients requested a stage ago, so that
+    // those of this stage and a payload requested since may be on their way; three: the gradients of this stage, but
+    // not a payload requested after them.
+    if (s + NA - 1 >= 2 * count)
+      wait_loads<0>();
+    else if (NA == 4)
+      wait_loads<NPW + NR>();
+    else if (U == 1)
+      wait_loads<NR>();
+    else
+      wait_loads<0>();
+    __syncthreads();
+    a0 = buffer(1);
+    if (U == 1) {
+      const int next2 = r2 + 1 == NB ? 0 : r2 + 1;
+      r1 = r2;
+      r2 = next2;
+    }
+  };
+  if (count) {
+    fetch_raw(0, 0);
+    fetch_raw(1, 1 % NB);
+#pragma unroll
+    for (int s = 0; s < NA - 1; ++s)
+      if (s < 2 * count) fetch(s, s);
+    wait_loads<0>();
+    __syncthreads();
+    read_rows(0, 0, 0);
+    look_up();
+    weigh(0);
+    read_rows(0, 2, 0);
+    look_up();
+    weigh(2);
+    put(0);
+    read_rows(1, 0, 1 % NB);
+    look_up();
+    weigh(0);
+    __syncthreads();  // chunk 0 is there, its payload read
+    for (int c = 2; c < NA; ++c) fetch_raw(c, c % NB);
+    wait_loads<0>();
+    __syncthreads();
+    read_x(0, 0);
+    read_w(0, 0, 0, 0);
+    for (int c = 0; c < count; ++c) {
+      stage(std::integral_constant<int, 0>{}, c);
+      stage(std::integral_constant<int, 1>{}, c);
     }
   }
   // tokens 4 q + k of tile c, columns 8 n + j of the wave's half
@@ -247,11 +324,11 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int4 e4 = *reinterpret_cast<const int4 *>(A.G.ex + min((tw + c) * 16 + q * 4, A.G.ntile * 16 - 4));
-    const int e[4] = {e4.x, e4.y, e4.z, e4.w};
+    const int ex[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[j][c][k] = ldexpf(acc[j][c][k], e[k] + ew - 15);
+      for (int k = 0; k < 4; ++k) acc[j][c][k] = ldexpf(acc[j][c][k], ex[k] + ew - 15);
   }
   if (LORA && blockIdx.z == 0) add_adapters<P, C>(A, tw, col, acc);
 #pragma unroll
@@ -300,9 +377,9 @@ template <int F, int P, int C, int H, bool LORA> void launch_tile(const RowsArgs
 }
 
 template <int F, bool LORA> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t stream) {
-  constexpr bool big = Geo<F>::N > 1024;  // 32 KiB of codebook
-  if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, big ? 1 : 2, 1, LORA>(A, stream);
-  launch_tile<F, 1, big ? 3 : 4, 2, LORA>(A, stream);
+  if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, (Geo<F>::N > 1024 ? 1 : 2), 1, LORA>(A, stream);
+  if (A.G.ntile <= 8) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
+  launch_tile<F, 1, 4, 2, LORA>(A, stream);
 }
 
 }  // namespace

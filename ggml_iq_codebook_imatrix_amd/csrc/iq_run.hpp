@@ -31,6 +31,7 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // arrays of it stay in registers, of uint4 they did not
 
 constexpr int ST_ROUNDED = IQ_STATUS_ROUNDED;
@@ -152,14 +153,21 @@ struct Words {
   uint32_t sel;  // the permutation: bytes 2.. or 4.. of a pair of words
 };
 
-template <class V> __device__ __forceinline__ V ldw(uintptr_t p) {  // 4-byte aligned
-  V v;
-  __builtin_memcpy(&v, __builtin_assume_aligned(reinterpret_cast<const void *>(p), 4), sizeof(V));
-  return v;
+// Payload comes from global memory, which the compiler cannot see of an address that was rounded or chosen: told so, it
+// does not make flat loads, which a barrier waits for as for LDS.
+template <class V, int ALIGN> __device__ __forceinline__ V ld_global(uintptr_t p) {
+  struct __attribute__((packed, aligned(ALIGN))) At {
+    V v;
+  };
+  return reinterpret_cast<const __attribute__((address_space(1))) At *>(p)->v;
 }
+template <class V> __device__ __forceinline__ V ldw(uintptr_t p) { return ld_global<V, 4>(p); }  // 4-byte aligned
 struct Words3 {
   uint32_t x, y, z;
 };
+__device__ __forceinline__ Words3 ldw3(uintptr_t p) {
+  return Words3{ldw<uint32_t>(p), ldw<uint32_t>(p + 4), ldw<uint32_t>(p + 8)};
+}
 
 template <int F> __device__ __forceinline__ Words load_words(const uint8_t *blk, int q) {
   Words r;
@@ -171,25 +179,26 @@ template <int F> __device__ __forceinline__ Words load_words(const uint8_t *blk,
     if (F == IQ2_XXS) {
       r.w[4] = ldw<uint32_t>(a + 16 * q + 16);
     } else {  // the last fields and the scales; the fifth word of other quarters is their neighbour's first
-      const Words3 t = ldw<Words3>(a + 64);
+      const Words3 t = ldw3(a + 64);
       r.w[4] = t.x; r.w[5] = t.y; r.w[6] = t.z;
     }
   } else if (F == IQ2_S) {
-    const Words3 k = ldw<Words3>(a + 8 * q), m = ldw<Words3>(a + 32 + 8 * q);
+    const Words3 k = ldw3(a + 8 * q), m = ldw3(a + 32 + 8 * q);
     const uintptr_t t = reinterpret_cast<uintptr_t>(blk) + 66 + 2 * q;
-    const Words3 e = ldw<Words3>(t & ~uintptr_t(3));
+    const Words3 e = ldw3(t & ~uintptr_t(3));
     r.w[0] = k.x; r.w[1] = k.y; r.w[2] = k.z;
     r.w[3] = m.x; r.w[4] = m.y; r.w[5] = m.z;
     r.w[6] = e.x; r.w[8] = e.z;
     r.w[7] = (t & 2) ? 0x07060302u : 0x05040100u;
   } else if (F == IQ1_S) {
-    const Words3 k = ldw<Words3>(a + 8 * q);
+    const Words3 k = ldw3(a + 8 * q);
     r.w[0] = k.x; r.w[1] = k.y; r.w[2] = k.z;
-    r.w[3] = ldu<uint32_t>(blk + 34 + 4 * q);
+    r.w[3] = ld_global<uint32_t, 2>(reinterpret_cast<uintptr_t>(blk) + 34 + 4 * q);
   } else {
-    const uint2 k = ldu<uint2>(blk + 8 * q), w = ldu<uint2>(blk + 48);
-    r.w[0] = k.x; r.w[1] = k.y; r.w[2] = ldu<uint32_t>(blk + 32 + 4 * q);
-    r.w[3] = w.x; r.w[4] = w.y;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(blk);
+    const u32x2 k = ld_global<u32x2, 2>(b + 8 * q), w = ld_global<u32x2, 2>(b + 48);
+    r.w[0] = k[0]; r.w[1] = k[1]; r.w[2] = ld_global<uint32_t, 2>(b + 32 + 4 * q);
+    r.w[3] = w[0]; r.w[4] = w[1];
   }
   return r;
 }
@@ -274,13 +283,26 @@ template <int F> __device__ __forceinline__ GroupFields group_fields(const Raw &
   return g;
 }
 
+// 2 ls + 1 twice in fp16: added to 1,024 in its last bits, and 1,024 taken off (exact).
+__device__ __forceinline__ half2v multiplier2(uint32_t ls) {
+  const uint32_t sum = ls * 0x20002u + 0x64016401u;
+  return __builtin_bit_cast(half2v, sum) - half2v{static_cast<_Float16>(1024.0f), static_cast<_Float16>(1024.0f)};
+}
+
+// The signs of IQ2's eight values where doubling brings pair after pair: those of
+// values 3 and 7 in bits 15 and 31, those of p and p + 4 after 3 - p doublings.  The
+// eighth sign is the parity of the seven (IQ2_S holds it).
+template <int F> __device__ __forceinline__ uint32_t sign_places(uint32_t mask) {
+  uint32_t twice = mask << 1;
+  if (Geo<F>::PARITY) twice |= __builtin_popcount(twice) << 8;
+  return twice * 0x800800u;  // the signs in bits 12.. and 24..; a product of 24 bits, one of 32 has a quarter of the rate
+}
+
 // m * v of a group as eight fp16 values (e: its codebook entry in fp16); zeros
 // where keep is 0 instead of all ones.
 template <int F>
 __device__ __forceinline__ half8v weights_half8(const GroupFields &g, const uint4 &e, uint32_t keep) {
-  uint32_t mask = g.mask;
-  const _Float16 m = static_cast<_Float16>(static_cast<uint16_t>(2 * g.ls + 1));
-  const half2v m2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, half2v{m, m}) & keep);
+  const half2v m2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, multiplier2(g.ls)) & keep);
   uint32_t o[4] = {e.x, e.y, e.z, e.w};
   if (Geo<F>::IQ1) {
     const half2v up = m2 * static_cast<_Float16>(0.125f);
@@ -289,11 +311,7 @@ __device__ __forceinline__ half8v weights_half8(const GroupFields &g, const uint
     for (int p = 0; p < 4; ++p)  // m g + m delta, rounded once
       o[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
   } else {
-    // The eighth sign is the parity of the seven (IQ2_S holds it).  Signs 3 and
-    // 7 to bits 15 and 31, the places of the last register's pair; each doubling
-    // brings the pair before it there.
-    if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
-    uint32_t t = mask * 0x1001000u;
+    uint32_t t = sign_places<F>(g.mask);
 #pragma unroll
     for (int p = 3; p >= 0; --p) {
       const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;

@@ -156,14 +156,19 @@ __device__ __forceinline__ uint32_t row_exponent(const void *x, int dtype, int64
   return wave_max_u32(e);
 }
 
-// 64 lanes' 16 bytes each, from base + off on, to 1 KiB of LDS (base and `to` the same in all lanes).  The compiler
-// takes every later read of LDS for one of these bytes and waits for them, which is a memory's latency lost in each
-// round of a buffer; written out, they are waited for where the buffers change (wait_loads), and by nothing before.
-__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, void *to) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)to)));
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(at)
+// Where an array in LDS begins, for the two loads below.
+#define IQ_LDS_ADDRESS(array) \
+  static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)(array)))
+// 64 lanes' 16 bytes each, from base + off on, to 1 KiB of LDS at `to` (base and `to` the same in all lanes).  The
+// compiler takes every later read of LDS for one of these bytes and waits for them, which is a memory's latency lost in
+// each round of a buffer; written out, they are waited for where the buffers change (wait_loads), and by nothing before.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
                : "memory");
+}
+// 64 lanes' 4 bytes each, from any 4-byte aligned addresses, to 256 bytes of LDS.
+__device__ __forceinline__ void load_words_to_lds(uintptr_t from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
 }
 // All loads but the wave's last N (in the order of their issue).
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
@@ -271,23 +276,18 @@ template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *bl
   return f;
 }
 
-// Whole weights of a group times 2^s as fp16: hi[p] holds values p (low half) and
-// p + 4; lo (P == 2) what they leave.  unit: 2^s (IQ2: 2^s / 8).
+// Whole weights of a group times 2^s as fp16, e its codebook entry: hi[p] holds values p (low half) and p + 4; lo
+// (P == 2) what they leave.  s: for IQ2 without the 2^-3 of its weights.
 template <int F, int P>
-__device__ __forceinline__ void whole_weights(const Fields &f, float unit, const uint4 *tab, uint32_t (&hi)[4],
+__device__ __forceinline__ void whole_weights(const Fields &f, const uint4 &e, int s, uint32_t (&hi)[4],
                                               uint32_t (&lo)[4]) {
-  const uint4 e = tab[f.k];
-  const float dm = f16_bits_to_f32(static_cast<uint16_t>(f.d16)) * unit * static_cast<float>(2 * f.ls + 1);
   const uint32_t o[4] = {e.x, e.y, e.z, e.w};
   uint32_t t = 0;
-  if (!Geo<F>::IQ1) {  // signs of pair p: bits p and p + 4 to 15 and 31
-    uint32_t mask = f.mask;
-    if (Geo<F>::PARITY) mask |= __builtin_popcount(mask) << 7;
-    t = mask * 0x1001000u;
-  }
+  if (!Geo<F>::IQ1) t = sign_places<F>(f.mask);
   if (P == 1) {
-    const _Float16 m = static_cast<_Float16>(dm);
-    const half2v m2 = {m, m};
+    // d 2^s has d's bits (steps of 2^-24 below 2^-14), d m is rounded to fp16
+    const _Float16 d = __builtin_amdgcn_ldexph(__builtin_bit_cast(_Float16, static_cast<uint16_t>(f.d16)), s);
+    const half2v m2 = multiplier2(f.ls) * half2v{d, d};
     if (Geo<F>::IQ1) {
       const half2v up = m2 * static_cast<_Float16>(0.125f);
       const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (f.h * 0x80008000u));
@@ -303,6 +303,7 @@ __device__ __forceinline__ void whole_weights(const Fields &f, float unit, const
       }
     }
   } else {
+    const float dm = ldexpf(f16_bits_to_f32(static_cast<uint16_t>(f.d16)), s) * static_cast<float>(2 * f.ls + 1);
     const float c = Geo<F>::IQ1 ? (f.h ? -0.125f : 0.125f) : 0.0f;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
