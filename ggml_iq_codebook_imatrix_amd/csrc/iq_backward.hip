@@ -112,8 +112,9 @@ struct ShrinkArgs {
   int dtype;
   int64_t T, tpad;
   Adapters L;
-  int rtiles, slots;
+  int rgroups, slots;  // 32 ranks a workgroup
   int32_t *ids;  // OUT [tpad]: the tokens' adapters, -1 for none or another id
+  int2 *range;   // OUT [tpad / 16]: the least and the largest of a tile's
   int32_t *status;
 };
 
@@ -121,7 +122,7 @@ struct ShrinkArgs {
 __device__ __forceinline__ void source8(const Source &s, int64_t cols, int64_t t, int64_t k, float v[8]) {
   const int64_t at = t * cols + k;
   if (s.ex) {  // whole blocks of 32
-    decode_codes(ldu<uint2>(static_cast<const int8_t *>(s.x) + at), s.ex[t * (cols >> 5) + (k >> 5)], v);
+    decode_codes(ldu<uint2>(static_cast<const int8_t *>(s.x) + at), s.ex[t * (cols >> 5) + (k >> 5)] - 133, v);
   } else if (k + 8 <= cols) {
     load8u(s.x, s.dtype, at, v);
   } else {
@@ -141,19 +142,22 @@ __device__ __forceinline__ bf16x8 source8_bf16(const Source &s, int64_t cols, in
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// 16 tokens (A) by 16 ranks (B) of the adapter of token `slot`, K split over the
-// eight waves; results of tokens with other adapters are dropped.
+// 16 tokens (A) by 32 ranks (B) of the adapter of token `slot`, K split over the
+// eight waves, U loads of each in flight; results of tokens with other adapters are
+// dropped.
+template <bool BF16>
 __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
-  __shared__ f32x4 s_red[8 * 64];
-  const int64_t tiles = (A.tpad >> 4) * A.rtiles;
+  constexpr int U = BF16 ? 4 : 2;
+  __shared__ f32x4 s_red[8 * 2 * 64];
+  const int64_t tiles = (A.tpad >> 4) * A.rgroups;
   int64_t w = blockIdx.x;
   const int first = static_cast<int>(w / (2 * tiles));
   w -= first * 2 * tiles;
-  const Shrink &S = A.of[w >= tiles ? 1 : 0];
   const bool of_x = w >= tiles;
+  const Shrink S = of_x ? A.of[1] : A.of[0];
   if (of_x) w -= tiles;
-  const int64_t tt = w / A.rtiles;
-  const int rt = static_cast<int>(w % A.rtiles);
+  const int64_t tt = w / A.rgroups;
+  const int r0 = static_cast<int>(w % A.rgroups) * 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, q = lane >> 4;
   const int64_t mytok = tt * 16 + n;
@@ -162,39 +166,72 @@ __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
     const int id = A.L.ids[mytok];
     if (id >= 0 && id < A.L.n)
       mine = id;
-    else if (id != -1 && first == 0 && rt == 0 && !of_x && threadIdx.x < 16)
+    else if (id != -1 && first == 0 && r0 == 0 && !of_x && threadIdx.x < 16)
       raise_status(A.status, ST_BADID);
   }
-  if (first == 0 && rt == 0 && !of_x && threadIdx.x < 16) A.ids[mytok] = mine;
-  if (first == 0 && threadIdx.x < 256) {  // zeros for tokens without an adapter
+  if (first == 0 && r0 == 0 && !of_x && threadIdx.x < 64) {
+    int least = mine, most = mine;
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+      least = min(least, __shfl_xor(least, d, 64));
+      most = max(most, __shfl_xor(most, d, 64));
+    }
+    if (threadIdx.x < 16) A.ids[mytok] = mine;
+    if (threadIdx.x == 0) A.range[tt] = make_int2(least, most);
+  }
+  if (first == 0) {  // zeros for tokens without an adapter
     const int tok = threadIdx.x & 15;
     const uint32_t with = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xffffu;
-    if (!((with >> tok) & 1u)) S.out[(rt * 16 + (threadIdx.x >> 4)) * A.tpad + tt * 16 + tok] = 0.0f;
+    if (!((with >> tok) & 1u)) S.out[(r0 + (threadIdx.x >> 4)) * A.tpad + tt * 16 + tok] = 0.0f;
   }
   for (int slot = first; slot < 16; slot += A.slots) {
     const int a = __builtin_amdgcn_readlane(mine, slot);
     const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
     if (a < 0 || (group & ((1u << slot) - 1u))) continue;  // done with an earlier token
     const int64_t t = tt * 16 + (((group >> n) & 1u) ? n : slot);  // rows of other tokens read this one's
-    const int64_t wr = (static_cast<int64_t>(a) * A.L.rank + min(rt * 16 + n, A.L.rank - 1)) * S.kpad;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k = wave * 32 + q * 8; k < S.kpad; k += 256) {
-      if (A.dtype == 1) {
-        const bf16x8 x = source8_bf16(S.s, S.k, t, k);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ldu<bf16x8>(static_cast<const uint16_t *>(S.w) + wr + k), acc,
-                                                      0, 0, 0);
-      } else {
-        float x[8], b[8];
-        source8(S.s, S.k, t, k, x);
-        load8u(S.w, 0, wr + k, b);
+    int64_t wr[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], b[i], acc, 0, 0, 0);
+    for (int r = 0; r < 2; ++r) wr[r] = (static_cast<int64_t>(a) * A.L.rank + min(r0 + r * 16 + n, A.L.rank - 1)) * S.kpad;
+    f32x4 acc[2] = {};
+    for (int64_t k0 = wave * 32; k0 < S.kpad; k0 += 256 * U) {
+      // past the end the last columns again, whose products are left out
+      if constexpr (BF16) {
+        bf16x8 x[U], b[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t k = min(k0 + 256 * u, S.kpad - 32) + q * 8;
+          x[u] = source8_bf16(S.s, S.k, t, k);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) b[u][r] = ldu<bf16x8>(static_cast<const uint16_t *>(S.w) + wr[r] + k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k0 + 256 * u < S.kpad)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[u], b[u][r], acc[r], 0, 0, 0);
+      } else {
+        float x[U][8], b[U][2][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t k = min(k0 + 256 * u, S.kpad - 32) + q * 8;
+          source8(S.s, S.k, t, k, x[u]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) load8u(S.w, 0, wr[r] + k, b[u][r]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k0 + 256 * u < S.kpad)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[u][i], b[u][r][i], acc[r], 0, 0, 0);
       }
     }
     const float scale = A.L.scale ? A.L.scale[a] : 1.0f;
     const Split P{8, 1, wave, 0};
-    reduce_split<1, 1>(&acc, s_red, P, [&](int, int, int l, const f32x4 &s) {
-      const int j = rt * 16 + (l & 15);
+    reduce_split<2, 2>(acc, s_red, P, [&](int, int r, int l, const f32x4 &s) {
+      const int j = r0 + r * 16 + (l & 15);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = (l >> 4) * 4 + i;
@@ -218,7 +255,11 @@ struct OuterArgs {
   Outer of[2];
   int64_t T, tpad;
   int dtype, rank;
-  const int32_t *ids;  // [tpad]
+  const int32_t *ids;   // [tpad]
+  const int2 *range;    // [tpad / 16]
+  int splits;           // of the tokens
+  float *partial;       // [split][both gradients], where there are several
+  int64_t before[2], all;  // where each gradient begins in a split's, and its size
 };
 
 // The first of a lane's eight columns: the last lanes of a row overlap, so that every load is whole.
@@ -226,18 +267,20 @@ __device__ __forceinline__ int64_t outer_col(const Outer &O, int64_t blk, int m)
   return max(min(blk * 128 + m * 8, O.k - 8), static_cast<int64_t>(0));
 }
 
-// out[j][c] = sum of w[j][t] s[t][c] over adapter n's tokens: 128 columns (A, eight a
+// out[j][c] = sum of w[j][t] s[t][c] over adapter a's tokens: 128 columns (A, eight a
 // lane, brought from eight tokens each into operands by byte permutations) by 16 RT
-// ranks (B), the tokens in steps of 32 dealt to eight waves.  w is the sum of three
-// bf16 values.  f32 tokens go through the fp32 cores.
+// ranks (B).  The tokens in steps of 32 are dealt to the splits and their eight
+// waves; a step whose tokens' adapters cannot be a is passed over, and where all
+// are a none is masked out.  w is the sum of three bf16 values.  f32 tokens go through
+// the fp32 cores.
 template <int RT>
 __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
   __shared__ f32x4 s_red[8 * 4 * 64];
   __shared__ float s_out[16][132];
   const bool second = blockIdx.x >= A.of[0].blocks;
-  const Outer &O = A.of[second ? 1 : 0];
+  const Outer O = second ? A.of[1] : A.of[0];
   const int64_t blk = blockIdx.x - (second ? A.of[0].blocks : 0);
-  const int a = blockIdx.y, rt0 = blockIdx.z * RT;
+  const int a = blockIdx.y, rt0 = static_cast<int>(blockIdx.z / A.splits) * RT, split = blockIdx.z % A.splits;
   const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t c0 = outer_col(O, blk, m);
@@ -250,13 +293,12 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
   const float *wr[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) wr[r] = O.w + (static_cast<int64_t>(rt0 + r) * 16 + m) * A.tpad;
-  for (int64_t t0 = wave * 32; t0 < A.tpad; t0 += 256) {
-    if (!__ballot(A.ids[t0 + (lane & 31)] == a)) continue;
+  const auto one_step = [&](int64_t t0, bool all) __attribute__((always_inline)) {
     if (plain) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const int64_t t = t0 + 4 * s + q;
-        const bool mine = A.ids[t] == a;  // false past the last token
+        const bool mine = all || A.ids[t] == a;  // false past the last token
         float x[8];
         if (O.k >= 8) {
           load8u(O.s.x, 0, (mine ? t : 0) * O.k + c0, x);
@@ -273,30 +315,36 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
           for (int j = 0; j < 8; ++j) acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], w, acc[r][j], 0, 0, 0);
         }
       }
-      continue;
+      return;
+    }
+    uint32_t mine = 255u;
+    if (!all) {
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine |= static_cast<uint32_t>(A.ids[t0 + 8 * q + i] == a) << i;
     }
     u32x4 x[8];
-    uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t t = t0 + 8 * q + i;
-      const bool is = A.ids[t] == a;
-      mine |= static_cast<uint32_t>(is) << i;
-      if (O.k >= 8) {
-        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, is ? t : 0, c0));
-      } else {
-        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, is ? t : 0, 0));
-      }
-      if (!is) x[i] = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i)
+      x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, (mine >> i) & 1u ? t0 + 8 * q + i : 0, O.k >= 8 ? c0 : 0));
+    float f[RT][8];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load8u(wr[r], 0, t0 + 8 * q, f[r]);
+    if (!all) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!((mine >> i) & 1u)) {
+          x[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) f[r][i] = 0.0f;
+        }
     }
     bf16x8 w[RT][3];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float f[8];
-      load8u(wr[r], 0, t0 + 8 * q, f);
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float v = (mine >> i) & 1u ? f[i] : 0.0f;
+        float v = f[r][i];
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const uint32_t top = __float_as_uint(v) & 0xffff0000u;
@@ -304,7 +352,6 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
           v = finite_f(v) ? v - __uint_as_float(top) : 0.0f;
         }
       }
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
@@ -316,6 +363,23 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
 #pragma unroll
         for (int k = 0; k < 3; ++k)
           acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, o), w[r][k], acc[r][j], 0, 0, 0);
+    }
+  };
+  // The wave's steps, 64 looked at together: step i is tokens 32 (i dealt + its place) on.
+  const int64_t steps = A.tpad >> 5, dealt = 8 * A.splits, place = split * 8 + wave;
+  for (int64_t i0 = 0; i0 * dealt + place < steps; i0 += 64) {
+    const int64_t s = (i0 + lane) * dealt + place;
+    int2 r = make_int2(-1, -1);
+    if (s < steps) {
+      const int4 both = *reinterpret_cast<const int4 *>(A.range + 2 * s);
+      r = make_int2(min(both.x, both.z), max(both.y, both.w));
+    }
+    uint64_t some = __ballot(r.x <= a && a <= r.y);
+    const uint64_t all = __ballot(r.x == a && a == r.y);
+    while (some) {
+      const int i = __builtin_ctzll(some);
+      some &= some - 1;
+      one_step(((i0 + i) * dealt + place) * 32, (all >> i) & 1u);
     }
   }
   const Split P{8, 1, wave, 0};
@@ -333,24 +397,45 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
       if (rank >= A.rank || c >= O.k) continue;
       const int64_t at = O.by_rank ? (static_cast<int64_t>(a) * A.rank + rank) * O.k + c
                                    : (static_cast<int64_t>(a) * O.k + c) * A.rank + rank;
-      store1(O.out, A.dtype, at, s_out[j][col]);
+      if (A.splits > 1)
+        A.partial[split * A.all + A.before[second ? 1 : 0] + at] = s_out[j][col];
+      else
+        store1(O.out, A.dtype, at, s_out[j][col]);
     }
     __syncthreads();
   }
 }
 
+// The splits' sums, in their order.
+__global__ void __launch_bounds__(256) back_join_kernel(OuterArgs A) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= A.all) return;
+  float s = A.partial[i];
+  for (int k = 1; k < A.splits; ++k) s += A.partial[k * A.all + i];
+  const int which = i >= A.before[1] ? 1 : 0;
+  store1(A.of[which].out, A.dtype, i - A.before[which], s);
+}
+
 // ---------------------------------------------------------------------------
 struct BackPlan {
   int64_t ntile, chunks, tpad, rowpad;
-  int rpad, splits;
-  size_t bo, go, geo, po, bto, pto, vto, ido, bytes;
+  int rpad, splits, osplits;
+  int64_t grads;  // values of both adapters' gradients
+  size_t bo, go, geo, po, bto, pto, vto, ido, rgo, oo, bytes;
 };
+// Splits of the tokens for the adapters' gradients: as long as workgroups are fewer than CUs and each wave keeps a step.
+int outer_splits(int64_t rows, int64_t cols, int64_t T, int n, int rank) {
+  const int64_t wgs = ((rows + 127) / 128 + cols / 128) * n * ((rank + 31) / 32);
+  int s = 1;
+  while (s < 16 && wgs * s < 256 && s * 256 < T) s *= 2;
+  return s;
+}
 BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n, int rank) {
   BackPlan p{};
   const size_t size = dtype == IQ_DTYPE_F32 ? 4 : 2;
   p.ntile = (T + 15) / 16;
   p.chunks = row_chunks(rows);
-  p.splits = rows_splits(T, cols, p.chunks, dtype);
+  p.splits = rows_splits(fmt, T, cols, p.chunks, dtype);
   p.bo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
   p.go = p.bo + ws_up(kBoundBytes);
   p.geo = p.go + ws_up(grads_bytes(p.chunks, p.ntile, dtype));
@@ -364,7 +449,11 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   p.pto = p.bto + ws_up(static_cast<size_t>(n) * rank * p.rowpad * size);
   p.vto = p.pto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
   p.ido = p.vto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
-  p.bytes = p.ido + ws_up(static_cast<size_t>(p.tpad) * 4) + kWsAlign;
+  p.rgo = p.ido + ws_up(static_cast<size_t>(p.tpad) * 4);
+  p.oo = p.rgo + ws_up(static_cast<size_t>(p.tpad) / 2);
+  p.grads = static_cast<int64_t>(n) * rank * (rows + cols);
+  p.osplits = outer_splits(rows, cols, T, n, rank);
+  p.bytes = p.oo + (p.osplits > 1 ? ws_up(static_cast<size_t>(p.osplits) * p.grads * 4) : 0) + kWsAlign;
   return p;
 }
 
@@ -377,7 +466,7 @@ int check_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n,
   const int64_t ntile = (T + 15) / 16;
   if (ntile > 4 * 65535 || (rank && n > 65535)) return IQ_ERR_SHAPE;  // grids of dx, of the adapters' gradients
   if (T * (cols / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;    // the joining launch
-  if (rank && (ntile + 1) * 2 * ((rank + 15) / 16) >= kMaxWG) return IQ_ERR_SHAPE;
+  if (rank && (ntile + 1) * 2 * ((rank + 31) / 32) >= kMaxWG) return IQ_ERR_SHAPE;
   if (rank && (T + 7) / 8 + n * ((rows + 767) / 512) + 128 >= kMaxWG) return IQ_ERR_SHAPE;
   return IQ_OK;
 }
@@ -423,6 +512,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   const Adapters L{lora_a, lora_b, lora_scale, lora_ids, rank ? num_adapters : 0, rank};
   float *pt = reinterpret_cast<float *>(base + P.pto), *vt = reinterpret_cast<float *>(base + P.vto);
   int32_t *ids = reinterpret_cast<int32_t *>(base + P.ido);
+  int2 *range = reinterpret_cast<int2 *>(base + P.rgo);
   BackPrepArgs A{};
   A.dy = dy;
   A.dtype = dtype;
@@ -455,13 +545,17 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     S.T = T;
     S.tpad = P.tpad;
     S.L = L;
-    S.rtiles = (rank + 15) / 16;
+    S.rgroups = (rank + 31) / 32;
     S.slots = 16;  // as many as are at work at once
-    while (S.slots > 1 && (P.tpad >> 4) * 2 * S.rtiles * S.slots > 1024) S.slots /= 2;
+    while (S.slots > 1 && (P.tpad >> 4) * 2 * S.rgroups * S.slots > 1024) S.slots /= 2;
     S.ids = ids;
+    S.range = range;
     S.status = status;
-    hipLaunchKernelGGL(back_shrink_kernel, dim3(static_cast<unsigned>((P.tpad >> 4) * 2 * S.rtiles * S.slots)),
-                       dim3(512), 0, stream, S);
+    const dim3 shrinks(static_cast<unsigned>((P.tpad >> 4) * 2 * S.rgroups * S.slots));
+    if (dtype == IQ_DTYPE_F32)
+      hipLaunchKernelGGL(back_shrink_kernel<false>, shrinks, dim3(512), 0, stream, S);
+    else
+      hipLaunchKernelGGL(back_shrink_kernel<true>, shrinks, dim3(512), 0, stream, S);
     if (!run_launched()) return IQ_ERR_HIP;
   }
   if (dx) {
@@ -493,12 +587,21 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     O.dtype = dtype;
     O.rank = rank;
     O.ids = ids;
-    const unsigned across = static_cast<unsigned>(O.of[0].blocks + O.of[1].blocks);
+    O.range = range;
+    O.splits = P.osplits;
+    O.partial = reinterpret_cast<float *>(base + P.oo);
+    O.before[1] = static_cast<int64_t>(num_adapters) * rank * rows;
+    O.all = P.grads;
+    const unsigned across = static_cast<unsigned>(O.of[0].blocks + O.of[1].blocks), z = P.osplits;
     if (rank <= 16)
-      hipLaunchKernelGGL(back_outer_kernel<1>, dim3(across, num_adapters, 1), dim3(512), 0, stream, O);
+      hipLaunchKernelGGL(back_outer_kernel<1>, dim3(across, num_adapters, z), dim3(512), 0, stream, O);
     else
-      hipLaunchKernelGGL(back_outer_kernel<2>, dim3(across, num_adapters, (rank + 31) / 32), dim3(512), 0, stream, O);
+      hipLaunchKernelGGL(back_outer_kernel<2>, dim3(across, num_adapters, (rank + 31) / 32 * z), dim3(512), 0, stream, O);
     if (!run_launched()) return IQ_ERR_HIP;
+    if (z > 1) {
+      hipLaunchKernelGGL(back_join_kernel, dim3(static_cast<unsigned>((P.grads + 255) / 256)), dim3(256), 0, stream, O);
+      if (!run_launched()) return IQ_ERR_HIP;
+    }
   }
   return IQ_OK;
 }

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) restore_kernel(CheckpointArgs A) {
     unit_of(A, u, row, col);
     const int64_t at = row * A.cols + col;
     float v[8];
-    decode_codes(w[u], e[u], v);
+    decode_codes(w[u], e[u] - 133, v);
     if (col + 8 <= A.cols) {
       store8u(A.y, A.dtype, at, v);
     } else {

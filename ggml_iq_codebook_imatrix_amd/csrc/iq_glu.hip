@@ -720,7 +720,7 @@ GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, b
   p.bytes = p.bo + kWsAlign;
   if (!backward) return p;
   const int64_t chunks = 2 * row_chunks(inter);
-  p.splits = rows_splits(T, hidden, chunks, dtype);
+  p.splits = rows_splits(fmt, T, hidden, chunks, dtype);
   p.do_ = p.bo + ws_up(kBoundBytes);
   p.go = p.do_ + ws_up(static_cast<size_t>(T) * 4);
   p.geo = p.go + ws_up(grads_bytes(chunks, p.x.ntile, dtype));

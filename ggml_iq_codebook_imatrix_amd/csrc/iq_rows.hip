@@ -123,25 +123,35 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   const int unit = 15 - ew - (Geo<F>::IQ1 ? 0 : 3);
   const uint8_t *const p0 = A.packed[0] + cb * Geo<F>::BYTES, *const p1 = A.packed[A.nmat - 1] + cb * Geo<F>::BYTES;
 
-  // The first row of chunk c of the workgroup's, and its weight's payload; past the last chunk the last.
-  const auto chunk_of = [&](int c, const uint8_t *&base) __attribute__((always_inline)) {
+  // The first row of chunk c of the workgroup's, and whether it is the second weight's; past the last chunk the last.
+  const auto chunk_of = [&](int c, bool &second) __attribute__((always_inline)) {
     const int64_t ch = ch0 + min(c, count - 1);
-    base = ch >= per ? p1 : p0;
-    return (ch >= per ? ch - per : ch) * 64;
+    second = ch >= per;
+    return (second ? ch - per : ch) * 64;
   };
-  // Its blocks, whole aligned words (rows past the last read the last's) into buffer `buf`.
+  // Its blocks, whole aligned words (rows past the last read the last's) into buffer `buf`.  64 rows are a multiple of
+  // four bytes, so a lane's offsets are the same for all whole chunks of a weight.
+  uint32_t roff[NR];
+  int rkey = -1;
   const auto fetch_raw = [&](int c, int buf) __attribute__((always_inline)) {
-    const uint8_t *base;
-    const int64_t row0 = chunk_of(c, base);
+    bool second;
+    const int64_t row0 = chunk_of(c, second);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(second ? p1 : p0);
+    const int most = static_cast<int>(min(A.rows - 1 - row0, static_cast<int64_t>(63))), key = most * 2 + second;
+    if (key != rkey) {
+      rkey = key;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int u = i * NT + static_cast<int>(threadIdx.x), r = min(u / W, 63), w = u % W;
-      const uintptr_t at = reinterpret_cast<uintptr_t>(base + min(row0 + r, A.rows - 1) * rowbytes);
-      const int last = (static_cast<int>(at & 2) + Geo<F>::BYTES - 1) >> 2;
-      load_words_to_lds((at & ~uintptr_t(3)) + 4 * min(w, last), raw_at + ((buf * NR + i) * NT + wave * 64) * 4);
+      for (int i = 0; i < NR; ++i) {
+        const int u = i * NT + static_cast<int>(threadIdx.x), r = min(u / W, most), w = u % W;
+        const uint32_t at = static_cast<uint32_t>(base & 2) + static_cast<uint32_t>(r) * static_cast<uint32_t>(rowbytes);
+        roff[i] = (at & ~3u) + 4 * min(w, static_cast<int>(((at & 2) + Geo<F>::BYTES - 1) >> 2));
+      }
     }
+    const char *from = reinterpret_cast<const char *>(base & ~uintptr_t(3)) + row0 * rowbytes;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) load_words_to_lds(from, roff[i], raw_at + ((buf * NR + i) * NT + wave * 64) * 4);
   };
-  // Stage s of the gradients into buffer `buf`.
+  // Step `step` of the gradients of the chunk at `from` into buffer `buf`.
   const char *gbase = reinterpret_cast<const char *>(A.G.g16) + (ch0 * A.G.ntile + tt0) * P * 2048;
   const int64_t gchunk = A.G.ntile * P * 2048;
   uint32_t goff[NPW];
@@ -150,11 +160,11 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
     const int p = i * NW + wave, most = static_cast<int>(min(A.G.ntile - tt0, static_cast<int64_t>(TA))) - 1;
     goff[i] = static_cast<uint32_t>((min(p / P, most) * P + p % P) * 2048 + lane * 16);
   }
-  const auto fetch = [&](int s, int buf) __attribute__((always_inline)) {
-    const char *from = gbase + (s >> 1) * gchunk + (s & 1) * 1024;
+  const auto fetch = [&](const char *from, int step, int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NPW; ++i)
-      if (NP % NW == 0 || i * NW + wave < NP) load_to_lds(from, goff[i], grad_at + (buf * NP + i * NW + wave) * 1024);
+      if (NP % NW == 0 || i * NW + wave < NP)
+        load_to_lds(from + step * 1024, goff[i], grad_at + (buf * NP + i * NW + wave) * 1024);
   };
   // The thread's group and four rows of each chunk: fields and entries of two rows at a time, weights, and both pairs
   // of rows to operand [quad / 8][wave % H][column], lane 16 ((quad % 8) / 2) + n, half quad % 2.
@@ -162,14 +172,16 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   Fields f[2];
   uint4 e[2];
   uint32_t hi[4][4], lo[4][4];
+  const int odd0 = static_cast<int>(reinterpret_cast<uintptr_t>(p0)) & 2, odd1 = static_cast<int>(reinterpret_cast<uintptr_t>(p1)) & 2;
   const auto read_rows = [&](int c, int j0, int buf) __attribute__((always_inline)) {
-    const uint8_t *base;
-    const int64_t row0 = chunk_of(c, base);
+    bool second;
+    const int64_t row0 = chunk_of(c, second);
+    const int most = static_cast<int>(min(A.rows - 1 - row0, static_cast<int64_t>(63)));
+    const int step = static_cast<int>(rowbytes) & 2, odd = second ? odd1 : odd0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = quad * 4 + j0 + j;
-      const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base) + min(row0 + r, A.rows - 1) * rowbytes) & 2u;
-      f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + odd, group);
+      const int r = quad * 4 + j0 + j, half = ((min(r, most) << 1) & step) ^ odd;  // the block's address modulo four
+      f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + half, group);
     }
   };
   const auto look_up = [&]() __attribute__((always_inline)) {
@@ -223,9 +235,10 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
     return b >= NA ? b - NA : b;
   };
   int r1 = 1 % NB, r2 = 2 % NB;  // the buffers of the payload of chunks c + 1 and c + 2
+  const char *g1 = gbase + (count > 1 ? gchunk : 0), *g2 = g1 + (count > 2 ? gchunk : 0);  // their gradients; past the last its
   const auto stage = [&](auto step, int c) __attribute__((always_inline)) {
     constexpr int U = decltype(step)::value;
-    const int s = 2 * c + U, next = c + 1 + U;  // the chunk whose rows are decoded in this stage
+    const int next = c + 1 + U;  // the chunk whose rows are decoded in this stage
     read_rows(next, U ? 0 : 2, U ? r2 : r1);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
       __builtin_amdgcn_sched_barrier(0);
       if (g == 0) {
         look_up();
-        if (s + NA - 1 < 2 * count) fetch(s + NA - 1, buffer(NA - 1));
+        fetch(NA == 3 || U == 0 ? g1 : g2, NA == 3 ? U : U ^ 1, buffer(NA - 1));
         if (U == 1) fetch_raw(c + NA, r1);  // chunk c + 1's is decoded
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -274,9 +287,7 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
     // What the stage after the next needs has to be there.  Four buffers: the gradients requested a stage ago, so that
     // those of this stage and a payload requested since may be on their way; three: the gradients of this stage, but
     // not a payload requested after them.
-    if (s + NA - 1 >= 2 * count)
-      wait_loads<0>();
-    else if (NA == 4)
+    if (NA == 4)
       wait_loads<NPW + NR>();
     else if (U == 1)
       wait_loads<NR>();
@@ -288,14 +299,15 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
       const int next2 = r2 + 1 == NB ? 0 : r2 + 1;
       r1 = r2;
       r2 = next2;
+      g1 = g2;
+      if (c + 3 < count) g2 += gchunk;
     }
   };
   if (count) {
     fetch_raw(0, 0);
     fetch_raw(1, 1 % NB);
 #pragma unroll
-    for (int s = 0; s < NA - 1; ++s)
-      if (s < 2 * count) fetch(s, s);
+    for (int s = 0; s < NA - 1; ++s) fetch(s < 2 ? gbase : g1, s & 1, s);
     wait_loads<0>();
     __syncthreads();
     read_rows(0, 0, 0);
@@ -314,10 +326,13 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
     __syncthreads();
     read_x(0, 0);
     read_w(0, 0, 0, 0);
+    // Of a SIMD's two waves the first goes first: while it works on its addresses the other has the matrix cores.
+    if (wave < NW / 2) __builtin_amdgcn_s_setprio(1);
     for (int c = 0; c < count; ++c) {
       stage(std::integral_constant<int, 0>{}, c);
       stage(std::integral_constant<int, 1>{}, c);
     }
+    wait_loads<0>();  // none is on its way to memory that another workgroup may be given
   }
   // tokens 4 q + k of tile c, columns 8 n + j of the wave's half
   const int64_t col = cb * 256 + (half0 + wh) * 128 + 8 * n, tw = tt0 + wt * C;
@@ -376,20 +391,39 @@ template <int F, int P, int C, int H, bool LORA> void launch_tile(const RowsArgs
                      dim3(256 * H), 0, stream, A);
 }
 
+// Token tiles of a workgroup.
+int rows_tiles(int fmt, int dtype, int64_t ntile) {
+  if (dtype == IQ_DTYPE_F32) return kCodebook[fmt] > 1024 ? 4 : 8;
+  return ntile <= 8 ? 4 : 16;
+}
+
 template <int F, bool LORA> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t stream) {
+  const int tiles = rows_tiles(F, dtype, A.G.ntile);
   if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, (Geo<F>::N > 1024 ? 1 : 2), 1, LORA>(A, stream);
-  if (A.G.ntile <= 8) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
+  if (tiles == 4) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
   launch_tile<F, 1, 4, 2, LORA>(A, stream);
 }
 
 }  // namespace
 
-int rows_splits(int64_t T, int64_t cols, int64_t chunks, int dtype) {
-  const int64_t wgs = (cols / 128) * ((T + 127) / 128);
-  int64_t s = 512 / (wgs < 1 ? 1 : wgs);
-  if (s > chunks / 4) s = chunks / 4;
-  (void)dtype;
-  return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
+// Splits of the rows: rounds of the workgroups over 256 CUs, each 8 us and 1.6 for a chunk (64 rows; 0.8 with tiles of 64
+// tokens), against 3 us of the joining launch and the way of the partial sums there and back (4 TB/s).
+int rows_splits(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) {
+  const int64_t ntile = (T + 15) / 16;
+  const int tiles = rows_tiles(fmt, dtype, ntile);
+  const int64_t wgs = cols / (dtype == IQ_DTYPE_F32 ? 128 : 256) * ((ntile + tiles - 1) / tiles);
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 64 && s <= chunks; ++s) {
+    const double rounds = static_cast<double>((wgs * s + 255) / 256), length = static_cast<double>((chunks + s - 1) / s);
+    double us = rounds * (8.0 + length * (tiles == 4 ? 0.8 : 1.6));
+    if (s > 1) us += 3.0 + static_cast<double>(s) * static_cast<double>(T) * static_cast<double>(cols) * 8.0 / 4e6;
+    if (s == 1 || us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 int launch_zero(void *p, size_t bytes, hipStream_t stream) {

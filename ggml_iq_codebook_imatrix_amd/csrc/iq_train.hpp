@@ -63,7 +63,7 @@ struct RowsArgs {
   int rank;
   int64_t tpad;
 };
-int rows_splits(int64_t T, int64_t cols, int64_t chunks, int dtype);
+int rows_splits(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype);
 inline size_t rows_partial_bytes(int64_t T, int64_t cols, int splits) {
   return splits > 1 ? static_cast<size_t>(splits) * T * cols * 4 : 0;
 }
@@ -95,12 +95,17 @@ __device__ __forceinline__ void store8u(void *y, int dtype, int64_t i, const flo
   }
 }
 
-// Eight codes of one block to their values; -128 to NaN.
-__device__ __forceinline__ void decode_codes(uint2 w, int e, float v[8]) {
+// Eight codes of one block times 2^n; -128 to NaN.  A code plus 128 is a byte, which converts in one instruction.
+__device__ __forceinline__ void decode_codes(uint2 w, int n, float v[8]) {
+  const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+  const float unit = ldexpf(1.0f, n);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int code = static_cast<int8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-    v[j] = code == -128 ? __uint_as_float(0x7fc00000u) : ldexpf(static_cast<float>(code), e - 133);
+  for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((u[j >> 2] >> (8 * (j & 3))) & 255u) - 128.0f) * unit;
+  const auto zero_byte = [](uint32_t x) { return (x - 0x01010101u) & ~x & 0x80808080u; };
+  if (zero_byte(u[0]) | zero_byte(u[1])) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!((u[j >> 2] >> (8 * (j & 3))) & 255u)) v[j] = __uint_as_float(0x7fc00000u);
   }
 }
 
@@ -128,13 +133,11 @@ __device__ __forceinline__ void convert_checkpoint(const int8_t *codes, const ui
       const int64_t col = k + u * 512 + lane * 8;
       if (col >= cols) break;
       const int g = static_cast<int>(col & 255) >> 3;
+      float v[8];
+      decode_codes(w[u], e[u] - 133 + n, v);
       half8v hi;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        const int j = kept_at(h), code = static_cast<int8_t>((j < 4 ? w[u].x : w[u].y) >> (8 * (j & 3)));
-        const float f = ldexpf(static_cast<float>(code), e[u] - 133 + n);
-        hi[h] = static_cast<_Float16>(code == -128 ? __uint_as_float(0x7fc00000u) : f);
-      }
+      for (int h = 0; h < 8; ++h) hi[h] = static_cast<_Float16>(v[kept_at(h)]);
       *reinterpret_cast<half8v *>(X.x16 + ((col >> 8) * X.ntile + (t >> 4)) * 4096 +
                                   ((g & 7) * 64 + (g >> 3) * 16 + (t & 15)) * 8) = hi;
     }
@@ -166,9 +169,9 @@ __device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
                : "memory");
 }
-// 64 lanes' 4 bytes each, from any 4-byte aligned addresses, to 256 bytes of LDS.
-__device__ __forceinline__ void load_words_to_lds(uintptr_t from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+// The same of 4 bytes each, to 256 bytes of LDS.
+__device__ __forceinline__ void load_words_to_lds(const char *base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
 }
 // All loads but the wave's last N (in the order of their issue).
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
