@@ -105,7 +105,8 @@ struct Shrink {
   int64_t k;
   const void *w;    // [adapter][rank][kpad], of dtype; zeros past k
   int64_t kpad;     // a multiple of 256
-  float *out;       // [ranks, in sixteens][tpad]
+  float *out;       // f32: [ranks, in 32s][tpad]
+  uint16_t *parts;  // three bf16 values each [32 tokens][16 ranks, 32s of them][3][lane][8]
 };
 struct ShrinkArgs {
   Shrink of[2];  // dy by B, x by A
@@ -114,7 +115,8 @@ struct ShrinkArgs {
   Adapters L;
   int rgroups, slots;  // 32 ranks a workgroup
   int32_t *ids;  // OUT [tpad]: the tokens' adapters, -1 for none or another id
-  int2 *range;   // OUT [tpad / 16]: the least and the largest of a tile's
+  int2 *range;   // OUT [tpad / 32]: the least and the largest of 32 tokens'
+  uint16_t *parts;  // OUT, bf16: p [tile of 16 tokens][32 ranks][3][lane][8]
   int32_t *status;
 };
 
@@ -142,103 +144,172 @@ __device__ __forceinline__ bf16x8 source8_bf16(const Source &s, int64_t cols, in
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// 16 tokens (A) by 32 ranks (B) of the adapter of token `slot`, K split over the
-// eight waves, U loads of each in flight; results of tokens with other adapters are
-// dropped.
+// Sixteen values as they are loaded, and in bf16.
+struct Sixteen {
+  u32x4 w[2];
+  int e;
+};
+__device__ __forceinline__ Sixteen load_sixteen(const Source &s, int64_t cols, int64_t t, int64_t k) {
+  Sixteen x;
+  x.e = 0;
+  if (s.ex) {
+    x.w[0] = ldu<u32x4>(static_cast<const int8_t *>(s.x) + t * cols + k);
+    x.w[1] = x.w[0];
+    x.e = s.ex[t * (cols >> 5) + (k >> 5)];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x.w[h] = __builtin_bit_cast(u32x4, source8_bf16(s, cols, t, k + 8 * h));
+  }
+  return x;
+}
+__device__ __forceinline__ bf16x8 eight_of(const Source &s, const Sixteen &x, int h) {
+  if (!s.ex) return __builtin_bit_cast(bf16x8, x.w[h]);
+  float v[8];
+  decode_codes(make_uint2(x.w[0][2 * h], x.w[0][2 * h + 1]), x.e - 133, v);
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+// 32 tokens (A, two tiles) by 32 ranks (B) of the adapter of token `slot`, K split
+// over the eight waves, each lane 16 columns at a time (64 bytes of a row a load);
+// results of tokens with other adapters are dropped.
+// (Each product is a call of its own: of a chosen one the compiler would not see that its pointers are to global memory.)
 template <bool BF16>
-__global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
-  constexpr int U = BF16 ? 4 : 2;
-  __shared__ f32x4 s_red[8 * 2 * 64];
-  const int64_t tiles = (A.tpad >> 4) * A.rgroups;
-  int64_t w = blockIdx.x;
-  const int first = static_cast<int>(w / (2 * tiles));
-  w -= first * 2 * tiles;
-  const bool of_x = w >= tiles;
-  const Shrink S = of_x ? A.of[1] : A.of[0];
-  if (of_x) w -= tiles;
+__device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, bool of_x, int first, int64_t w, f32x4 *s_red) {
   const int64_t tt = w / A.rgroups;
-  const int r0 = static_cast<int>(w % A.rgroups) * 32;
+  const int rg = static_cast<int>(w % A.rgroups), r0 = rg * 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, q = lane >> 4;
-  const int64_t mytok = tt * 16 + n;
+  const int64_t mytok = tt * 32 + (lane & 31);
+  const bool once = first == 0 && rg == 0 && !of_x && threadIdx.x < 64;
   int mine = -1;
   if (mytok < A.T) {
     const int id = A.L.ids[mytok];
     if (id >= 0 && id < A.L.n)
       mine = id;
-    else if (id != -1 && first == 0 && r0 == 0 && !of_x && threadIdx.x < 16)
+    else if (id != -1 && once)
       raise_status(A.status, ST_BADID);
   }
-  if (first == 0 && r0 == 0 && !of_x && threadIdx.x < 64) {
+  if (once) {
     int least = mine, most = mine;
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
+    for (int d = 1; d < 32; d *= 2) {
       least = min(least, __shfl_xor(least, d, 64));
       most = max(most, __shfl_xor(most, d, 64));
     }
-    if (threadIdx.x < 16) A.ids[mytok] = mine;
-    if (threadIdx.x == 0) A.range[tt] = make_int2(least, most);
+    if (lane < 32) A.ids[mytok] = mine;
+    if (lane == 0) A.range[tt] = make_int2(least, most);
   }
+  const uint32_t with = static_cast<uint32_t>(__ballot(mine >= 0));  // the tokens twice, once in either half of the wave
+  // Value r of token tok's 32 in fp32, and as the three bf16 values that add up to it: in the order of the operands of
+  // the sums over tokens, and of p for dx.
+  const auto put_ranks = [&](int64_t step, int tok, int r, float f) __attribute__((always_inline)) {
+    if (S.out) S.out[(r0 + r) * A.tpad + step * 32 + tok] = f;
+    uint16_t *u = S.parts + ((step * A.rgroups + rg) * 2 + (r >> 4)) * 1536 + ((tok >> 3) * 16 + (r & 15)) * 8 + (tok & 7);
+    uint16_t *v = A.parts + ((2 * step + (tok >> 4)) * A.rgroups + rg) * 1536 + ((r >> 3) * 16 + (tok & 15)) * 8 + (r & 7);
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      const uint32_t top = __float_as_uint(f) & 0xffff0000u;
+      u[d * 512] = static_cast<uint16_t>(top >> 16);
+      if (BF16 && !of_x) v[d * 512] = static_cast<uint16_t>(top >> 16);
+      f = finite_f(f) ? f - __uint_as_float(top) : 0.0f;  // inf - inf would be NaN
+    }
+  };
   if (first == 0) {  // zeros for tokens without an adapter
-    const int tok = threadIdx.x & 15;
-    const uint32_t with = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xffffu;
-    if (!((with >> tok) & 1u)) S.out[(r0 + (threadIdx.x >> 4)) * A.tpad + tt * 16 + tok] = 0.0f;
+    const int tok = threadIdx.x & 31;
+    if (!((with >> tok) & 1u))
+      for (int r = threadIdx.x >> 5; r < 32; r += 16) put_ranks(tt, tok, r, 0.0f);
   }
-  for (int slot = first; slot < 16; slot += A.slots) {
+  for (int slot = first; slot < 32; slot += A.slots) {
     const int a = __builtin_amdgcn_readlane(mine, slot);
-    const uint32_t group = static_cast<uint32_t>(__ballot(mine == a)) & 0xffffu;
+    const uint32_t group = static_cast<uint32_t>(__ballot(mine == a));
     if (a < 0 || (group & ((1u << slot) - 1u))) continue;  // done with an earlier token
-    const int64_t t = tt * 16 + (((group >> n) & 1u) ? n : slot);  // rows of other tokens read this one's
-    int64_t wr[2];
+    const bool tile[2] = {(group & 0xffffu) != 0, (group >> 16) != 0};
+    int64_t t[2], wr[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) wr[r] = (static_cast<int64_t>(a) * A.L.rank + min(r0 + r * 16 + n, A.L.rank - 1)) * S.kpad;
-    f32x4 acc[2] = {};
-    for (int64_t k0 = wave * 32; k0 < S.kpad; k0 += 256 * U) {
-      // past the end the last columns again, whose products are left out
-      if constexpr (BF16) {
-        bf16x8 x[U], b[U][2];
+    for (int r = 0; r < 2; ++r) {  // rows of other tokens read this one's
+      t[r] = tt * 32 + (((group >> (16 * r + n)) & 1u) ? 16 * r + n : slot);
+      wr[r] = (static_cast<int64_t>(a) * A.L.rank + min(r0 + r * 16 + n, A.L.rank - 1)) * S.kpad;
+    }
+    f32x4 acc[4] = {};  // [token tile][rank tile]
+    if constexpr (BF16) {
+      // a round of the waves is 512 columns; two rounds are on their way while one multiplies (past the end the last
+      // columns again)
+      Sixteen x[3][2];
+      u32x4 b[3][2][2];
+      const auto load = [&](int u, int64_t k0) __attribute__((always_inline)) {
+        const int64_t k = min(k0, S.kpad - 64) + q * 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t k = min(k0 + 256 * u, S.kpad - 32) + q * 8;
-          x[u] = source8_bf16(S.s, S.k, t, k);
+        for (int r = 0; r < 2; ++r) {
+          if (tile[r]) x[u][r] = load_sixteen(S.s, S.k, t[r], k);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) b[u][r] = ldu<bf16x8>(static_cast<const uint16_t *>(S.w) + wr[r] + k);
+          for (int h = 0; h < 2; ++h) b[u][r][h] = ldu<u32x4>(static_cast<const uint16_t *>(S.w) + wr[r] + k + 8 * h);
         }
+      };
+      load(0, wave * 64);
+      load(1, wave * 64 + 512);
+      for (int64_t k0 = wave * 64; k0 < S.kpad; k0 += 3 * 512)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (k0 + 256 * u < S.kpad)
+        for (int u = 0; u < 3; ++u) {
+          if (k0 + u * 512 >= S.kpad) break;
+          load((u + 2) % 3, k0 + (u + 2) * 512);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[u], b[u][r], acc[r], 0, 0, 0);
-      } else {
-        float x[U][8], b[U][2][8];
+          for (int r = 0; r < 2; ++r)
+            if (tile[r])
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t k = min(k0 + 256 * u, S.kpad - 32) + q * 8;
-          source8(S.s, S.k, t, k, x[u]);
+              for (int h = 0; h < 2; ++h) {
+                const bf16x8 v = eight_of(S.s, x[u][r], h);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) load8u(S.w, 0, wr[r] + k, b[u][r]);
+                for (int i = 0; i < 2; ++i)
+                  acc[2 * r + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, b[u][i][h]),
+                                                                          acc[2 * r + i], 0, 0, 0);
+              }
         }
+    } else {
+      for (int64_t k0 = wave * 64; k0 < S.kpad; k0 += 512)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (k0 + 256 * u < S.kpad)
+        for (int h = 0; h < 2; ++h) {
+          const int64_t k = k0 + q * 16 + 8 * h;
+          float x[2][8], b[2][8];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < 2; ++r) {
+            if (tile[r]) source8(S.s, S.k, t[r], k, x[r]);
+            load8u(S.w, 0, wr[r] + k, b[r]);
+          }
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[u][i], b[u][r][i], acc[r], 0, 0, 0);
-      }
+          for (int i = 0; i < 4; ++i)
+            if (tile[i >> 1])
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i >> 1][j], b[i & 1][j], acc[i], 0, 0, 0);
+        }
     }
     const float scale = A.L.scale ? A.L.scale[a] : 1.0f;
     const Split P{8, 1, wave, 0};
-    reduce_split<2, 2>(acc, s_red, P, [&](int, int r, int l, const f32x4 &s) {
-      const int j = r0 + r * 16 + (l & 15);
+    reduce_split<4, 4>(acc, s_red, P, [&](int, int i, int l, const f32x4 &s) {
+      const int r = (i & 1) * 16 + (l & 15), j = r0 + r;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (l >> 4) * 4 + i;
-        if ((group >> tok) & 1u) S.out[j * A.tpad + tt * 16 + tok] = j < A.L.rank ? s[i] * scale : 0.0f;
+      for (int k = 0; k < 4; ++k) {
+        const int tok = (i >> 1) * 16 + (l >> 4) * 4 + k;
+        if (!((group >> tok) & 1u)) continue;
+        put_ranks(tt, tok, r, j < A.L.rank ? s[k] * scale : 0.0f);
       }
     });
   }
+}
+
+template <bool BF16> __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
+  __shared__ f32x4 s_red[8 * 4 * 64];
+  const int64_t steps = (A.tpad >> 5) * A.rgroups, w = blockIdx.x % (2 * steps);
+  const int first = static_cast<int>(blockIdx.x / (2 * steps));
+  if (w < steps)
+    shrink<BF16>(A, A.of[0], false, first, w, s_red);
+  else
+    shrink<BF16>(A, A.of[1], true, first, w - steps, s_red);
 }
 
 // ---------------------------------------------------------------------------
@@ -247,16 +318,17 @@ __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
 struct Outer {
   Source s;        // [T, k]
   int64_t k, blocks;  // workgroups' columns: 128 each
-  const float *w;  // [ranks, in sixteens][tpad]
+  const float *w;         // f32: [ranks, in 32s][tpad]
+  const uint16_t *parts;  // Shrink's
   void *out;       // by rank: [adapter][rank][k]; else [adapter][k][rank]
   int by_rank;
 };
 struct OuterArgs {
   Outer of[2];
   int64_t T, tpad;
-  int dtype, rank;
+  int dtype, rank, rgroups;
   const int32_t *ids;   // [tpad]
-  const int2 *range;    // [tpad / 16]
+  const int2 *range;    // [tpad / 32]
   int splits;           // of the tokens
   float *partial;       // [split][both gradients], where there are several
   int64_t before[2], all;  // where each gradient begins in a split's, and its size
@@ -269,32 +341,27 @@ __device__ __forceinline__ int64_t outer_col(const Outer &O, int64_t blk, int m)
 
 // out[j][c] = sum of w[j][t] s[t][c] over adapter a's tokens: 128 columns (A, eight a
 // lane, brought from eight tokens each into operands by byte permutations) by 16 RT
-// ranks (B).  The tokens in steps of 32 are dealt to the splits and their eight
+// ranks (B; three bf16 values each).  The tokens in steps of 32 are dealt to the splits and their eight
 // waves; a step whose tokens' adapters cannot be a is passed over, and where all
-// are a none is masked out.  w is the sum of three bf16 values.  f32 tokens go through
-// the fp32 cores.
-template <int RT>
-__global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
-  __shared__ f32x4 s_red[8 * 4 * 64];
-  __shared__ float s_out[16][132];
-  const bool second = blockIdx.x >= A.of[0].blocks;
-  const Outer O = second ? A.of[1] : A.of[0];
-  const int64_t blk = blockIdx.x - (second ? A.of[0].blocks : 0);
+// are a none is masked out.  f32 tokens go through the fp32 cores.
+enum SourceKind { FROM_F32, FROM_BF16, FROM_CHECKPOINT };
+struct OuterMemory {
+  f32x4 red[8 * 4 * 64];
+  float out[16][132];
+};
+template <int RT, int KIND>
+__device__ __forceinline__ void outer_sums(const OuterArgs &A, const Outer &O, int which, int64_t blk, OuterMemory &mem) {
   const int a = blockIdx.y, rt0 = static_cast<int>(blockIdx.z / A.splits) * RT, split = blockIdx.z % A.splits;
   const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t c0 = outer_col(O, blk, m);
-  const bool plain = !O.s.ex && O.s.dtype == IQ_DTYPE_F32;
   f32x4 acc[RT][8];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[r][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const float *wr[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) wr[r] = O.w + (static_cast<int64_t>(rt0 + r) * 16 + m) * A.tpad;
   const auto one_step = [&](int64_t t0, bool all) __attribute__((always_inline)) {
-    if (plain) {
+    if constexpr (KIND == FROM_F32) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const int64_t t = t0 + 4 * s + q;
@@ -310,7 +377,7 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
         for (int j = 0; j < 8; ++j) x[j] = mine ? x[j] : 0.0f;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float w = mine ? wr[r][t] : 0.0f;
+          const float w = mine ? O.w[(static_cast<int64_t>(rt0 + r) * 16 + m) * A.tpad + t] : 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], w, acc[r][j], 0, 0, 0);
         }
@@ -324,34 +391,47 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
       for (int i = 0; i < 8; ++i) mine |= static_cast<uint32_t>(A.ids[t0 + 8 * q + i] == a) << i;
     }
     u32x4 x[8];
+    if constexpr (KIND == FROM_CHECKPOINT) {
+      uint2 codes[8];
+      int e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, (mine >> i) & 1u ? t0 + 8 * q + i : 0, O.k >= 8 ? c0 : 0));
-    float f[RT][8];
+      for (int i = 0; i < 8; ++i) {
+        const int64_t t = (mine >> i) & 1u ? t0 + 8 * q + i : 0;
+        codes[i] = ldu<uint2>(static_cast<const int8_t *>(O.s.x) + t * O.k + c0);
+        e[i] = O.s.ex[t * (O.k >> 5) + (c0 >> 5)];
+      }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) load8u(wr[r], 0, t0 + 8 * q, f[r]);
-    if (!all) {
+      for (int i = 0; i < 8; ++i) {
+        float v[8];
+        decode_codes(codes[i], e[i] - 133, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[i][j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!((mine >> i) & 1u)) {
-          x[i] = u32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int r = 0; r < RT; ++r) f[r][i] = 0.0f;
-        }
+        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, (mine >> i) & 1u ? t0 + 8 * q + i : 0, O.k >= 8 ? c0 : 0));
     }
-    bf16x8 w[RT][3];
+    u32x4 w[RT][3];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = f[r][i];
+      for (int k = 0; k < 3; ++k)
+        w[r][k] = ldu<u32x4>(O.parts + ((t0 >> 5) * 2 * A.rgroups + rt0 + r) * 1536 + k * 512 + lane * 8);
+    if (!all) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-          w[r][k][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
-          v = finite_f(v) ? v - __uint_as_float(top) : 0.0f;
-        }
+      for (int i = 0; i < 8; ++i)
+        if (!((mine >> i) & 1u)) x[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t keep = ((mine >> (2 * i)) & 1u ? 0xffffu : 0u) | ((mine >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) w[r][k][i] &= keep;
       }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
@@ -362,7 +442,8 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, o), w[r][k], acc[r][j], 0, 0, 0);
+          acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, o),
+                                                              __builtin_bit_cast(bf16x8, w[r][k]), acc[r][j], 0, 0, 0);
     }
   };
   // The wave's steps, 64 looked at together: step i is tokens 32 (i dealt + its place) on.
@@ -370,10 +451,7 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
   for (int64_t i0 = 0; i0 * dealt + place < steps; i0 += 64) {
     const int64_t s = (i0 + lane) * dealt + place;
     int2 r = make_int2(-1, -1);
-    if (s < steps) {
-      const int4 both = *reinterpret_cast<const int4 *>(A.range + 2 * s);
-      r = make_int2(min(both.x, both.z), max(both.y, both.w));
-    }
+    if (s < steps) r = A.range[s];
     uint64_t some = __ballot(r.x <= a && a <= r.y);
     const uint64_t all = __ballot(r.x == a && a == r.y);
     while (some) {
@@ -386,9 +464,9 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     // lane l: rank l % 16, columns j of lanes 4 (l / 16) + 0..3
-    reduce_split<8, 4>(acc[r], s_red, P, [&](int, int j, int l, const f32x4 &s) {
+    reduce_split<8, 4>(acc[r], mem.red, P, [&](int, int j, int l, const f32x4 &s) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s_out[l & 15][((l >> 4) * 4 + k) * 8 + j] = s[k];
+      for (int k = 0; k < 4; ++k) mem.out[l & 15][((l >> 4) * 4 + k) * 8 + j] = s[k];
     });
     __syncthreads();
     for (int i = threadIdx.x; i < 2048; i += 512) {
@@ -398,12 +476,29 @@ __global__ void __launch_bounds__(512) back_outer_kernel(OuterArgs A) {
       const int64_t at = O.by_rank ? (static_cast<int64_t>(a) * A.rank + rank) * O.k + c
                                    : (static_cast<int64_t>(a) * O.k + c) * A.rank + rank;
       if (A.splits > 1)
-        A.partial[split * A.all + A.before[second ? 1 : 0] + at] = s_out[j][col];
+        A.partial[split * A.all + A.before[which] + at] = mem.out[j][col];
       else
-        store1(O.out, A.dtype, at, s_out[j][col]);
+        store1(O.out, A.dtype, at, mem.out[j][col]);
     }
     __syncthreads();
   }
+}
+
+// KIND of x; dy is of its tensors' type (BF16).
+template <int RT, int KIND, bool BF16>
+__global__ void __launch_bounds__(512, 2) back_outer_kernel(OuterArgs A) {
+  __shared__ OuterMemory s_mem;
+  if (blockIdx.x < A.of[0].blocks)
+    outer_sums<RT, BF16 ? FROM_BF16 : FROM_F32>(A, A.of[0], 0, blockIdx.x, s_mem);
+  else
+    outer_sums<RT, KIND>(A, A.of[1], 1, blockIdx.x - A.of[0].blocks, s_mem);
+}
+
+template <int KIND, bool BF16> void launch_outer(const OuterArgs &O, dim3 wgs, hipStream_t stream) {
+  if (O.rank <= 16)
+    hipLaunchKernelGGL((back_outer_kernel<1, KIND, BF16>), wgs, dim3(512), 0, stream, O);
+  else
+    hipLaunchKernelGGL((back_outer_kernel<2, KIND, BF16>), wgs, dim3(512), 0, stream, O);
 }
 
 // The splits' sums, in their order.
@@ -421,7 +516,7 @@ struct BackPlan {
   int64_t ntile, chunks, tpad, rowpad;
   int rpad, splits, osplits;
   int64_t grads;  // values of both adapters' gradients
-  size_t bo, go, geo, po, bto, pto, vto, ido, rgo, oo, bytes;
+  size_t bo, go, geo, po, bto, pto, vto, ppo, vpo, ido, rgo, pao, oo, bytes;
 };
 // Splits of the tokens for the adapters' gradients: as long as workgroups are fewer than CUs and each wave keeps a step.
 int outer_splits(int64_t rows, int64_t cols, int64_t T, int n, int rank) {
@@ -447,10 +542,15 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   p.rowpad = (rows + 255) / 256 * 256;
   p.rpad = (rank + 31) / 32 * 32;
   p.pto = p.bto + ws_up(static_cast<size_t>(n) * rank * p.rowpad * size);
-  p.vto = p.pto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
-  p.ido = p.vto + ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4);
+  const size_t whole = dtype == IQ_DTYPE_F32 ? ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4) : 0;
+  const size_t parts = ws_up(static_cast<size_t>(p.rpad) * p.tpad * 6);
+  p.vto = p.pto + whole;
+  p.ppo = p.vto + whole;
+  p.vpo = p.ppo + parts;
+  p.ido = p.vpo + parts;
   p.rgo = p.ido + ws_up(static_cast<size_t>(p.tpad) * 4);
-  p.oo = p.rgo + ws_up(static_cast<size_t>(p.tpad) / 2);
+  p.pao = p.rgo + ws_up(static_cast<size_t>(p.tpad) / 4);
+  p.oo = p.pao + (dtype == IQ_DTYPE_BF16 ? parts : 0);
   p.grads = static_cast<int64_t>(n) * rank * (rows + cols);
   p.osplits = outer_splits(rows, cols, T, n, rank);
   p.bytes = p.oo + (p.osplits > 1 ? ws_up(static_cast<size_t>(p.osplits) * p.grads * 4) : 0) + kWsAlign;
@@ -510,7 +610,9 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   char *base = ws_base(workspace);
   _Float16 *tab = reinterpret_cast<_Float16 *>(base);
   const Adapters L{lora_a, lora_b, lora_scale, lora_ids, rank ? num_adapters : 0, rank};
-  float *pt = reinterpret_cast<float *>(base + P.pto), *vt = reinterpret_cast<float *>(base + P.vto);
+  float *pt = dtype == IQ_DTYPE_F32 ? reinterpret_cast<float *>(base + P.pto) : nullptr;
+  float *vt = dtype == IQ_DTYPE_F32 ? reinterpret_cast<float *>(base + P.vto) : nullptr;
+  uint16_t *pp = reinterpret_cast<uint16_t *>(base + P.ppo), *vp = reinterpret_cast<uint16_t *>(base + P.vpo);
   int32_t *ids = reinterpret_cast<int32_t *>(base + P.ido);
   int2 *range = reinterpret_cast<int2 *>(base + P.rgo);
   BackPrepArgs A{};
@@ -539,19 +641,20 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   if (!run_launched()) return IQ_ERR_HIP;
   if (rank) {
     ShrinkArgs S{};
-    S.of[0] = Shrink{Source{dy, nullptr, dtype}, rows, A.bt, P.rowpad, pt};
-    S.of[1] = Shrink{Source{x, exponents, dtype}, cols, lora_a, cols, vt};
+    S.of[0] = Shrink{Source{dy, nullptr, dtype}, rows, A.bt, P.rowpad, pt, pp};
+    S.of[1] = Shrink{Source{x, exponents, dtype}, cols, lora_a, cols, vt, vp};
     S.dtype = dtype;
     S.T = T;
     S.tpad = P.tpad;
     S.L = L;
     S.rgroups = (rank + 31) / 32;
-    S.slots = 16;  // as many as are at work at once
-    while (S.slots > 1 && (P.tpad >> 4) * 2 * S.rgroups * S.slots > 1024) S.slots /= 2;
+    S.slots = 32;  // as many as are at work at once
+    while (S.slots > 1 && (P.tpad >> 5) * 2 * S.rgroups * S.slots > 1024) S.slots /= 2;
     S.ids = ids;
     S.range = range;
+    S.parts = reinterpret_cast<uint16_t *>(base + P.pao);
     S.status = status;
-    const dim3 shrinks(static_cast<unsigned>((P.tpad >> 4) * 2 * S.rgroups * S.slots));
+    const dim3 shrinks(static_cast<unsigned>((P.tpad >> 5) * 2 * S.rgroups * S.slots));
     if (dtype == IQ_DTYPE_F32)
       hipLaunchKernelGGL(back_shrink_kernel<false>, shrinks, dim3(512), 0, stream, S);
     else
@@ -573,6 +676,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     D.splits = P.splits;
     D.a = lora_a;
     D.p = pt;
+    D.parts = reinterpret_cast<const uint16_t *>(base + P.pao);
     D.ids = ids;
     D.rank = rank;
     D.tpad = P.tpad;
@@ -580,12 +684,13 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   }
   if (rank) {
     OuterArgs O{};
-    O.of[0] = Outer{Source{dy, nullptr, dtype}, rows, (rows + 127) / 128, vt, db, 0};
-    O.of[1] = Outer{Source{x, exponents, dtype}, cols, cols / 128, pt, da, 1};
+    O.of[0] = Outer{Source{dy, nullptr, dtype}, rows, (rows + 127) / 128, vt, vp, db, 0};
+    O.of[1] = Outer{Source{x, exponents, dtype}, cols, cols / 128, pt, pp, da, 1};
     O.T = T;
     O.tpad = P.tpad;
     O.dtype = dtype;
     O.rank = rank;
+    O.rgroups = (rank + 31) / 32;
     O.ids = ids;
     O.range = range;
     O.splits = P.osplits;
@@ -593,10 +698,11 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     O.before[1] = static_cast<int64_t>(num_adapters) * rank * rows;
     O.all = P.grads;
     const unsigned across = static_cast<unsigned>(O.of[0].blocks + O.of[1].blocks), z = P.osplits;
-    if (rank <= 16)
-      hipLaunchKernelGGL(back_outer_kernel<1>, dim3(across, num_adapters, z), dim3(512), 0, stream, O);
+    const dim3 wgo(across, num_adapters, rank <= 16 ? z : (rank + 31) / 32 * z);
+    if (dtype == IQ_DTYPE_F32)
+      exponents ? launch_outer<FROM_CHECKPOINT, false>(O, wgo, stream) : launch_outer<FROM_F32, false>(O, wgo, stream);
     else
-      hipLaunchKernelGGL(back_outer_kernel<2>, dim3(across, num_adapters, (rank + 31) / 32 * z), dim3(512), 0, stream, O);
+      exponents ? launch_outer<FROM_CHECKPOINT, true>(O, wgo, stream) : launch_outer<FROM_BF16, true>(O, wgo, stream);
     if (!run_launched()) return IQ_ERR_HIP;
     if (z > 1) {
       hipLaunchKernelGGL(back_join_kernel, dim3(static_cast<unsigned>((P.grads + 255) / 256)), dim3(256), 0, stream, O);

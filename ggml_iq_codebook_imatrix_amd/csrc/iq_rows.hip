@@ -45,31 +45,31 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
         for (int i = 0; i < 8; ++i) w[i] = ldu<u32x4>(from + min(r0 + 8 * q + i, A.rank - 1) * cols);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          if (!((group >> (16 * c)) & 0xffffu)) continue;
+          const uint32_t tokens = static_cast<uint32_t>(group >> (16 * c)) & 0xffffu;
+          if (!tokens) continue;
+          const uint16_t *p = A.parts + ((tt + c) * ((A.rank + 31) >> 5) + (r0 >> 5)) * 1536 + lane * 8;
           bf16x8 v[3];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float f = r0 + 8 * q + i < A.rank ? A.p[(r0 + 8 * q + i) * A.tpad + (tt + c) * 16 + n] : 0.0f;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const uint32_t top = __float_as_uint(f) & 0xffff0000u;
-              v[k][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
-              f = finite_f(f) ? f - __uint_as_float(top) : 0.0f;
-            }
-          }
+          for (int k = 0; k < 3; ++k) v[k] = ldu<bf16x8>(p + k * 512);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
             u32x4 o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_perm(w[2 * i + 1][j >> 1], w[2 * i][j >> 1], sel);
+            if (tokens == 0xffffu) {
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[k], __builtin_bit_cast(bf16x8, o), acc[j][c], 0, 0, 0);
+              continue;
+            }
             f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < 3; ++k)
               d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[k], __builtin_bit_cast(bf16x8, o), d, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if ((group >> (16 * c + 4 * q + k)) & 1u) acc[j][c][k] += d[k];
+              if ((tokens >> (4 * q + k)) & 1u) acc[j][c][k] += d[k];
           }
         }
       } else {

@@ -56,9 +56,11 @@ struct RowsArgs {
   void *out;       // dx, or null where only partial sums are wanted
   float *partial;  // [split][T][cols], used where the launch splits
   int splits;
-  // adapters (rank 0: none): A, p of the tokens [rank][tpad] in fp32, their adapters (-1: none)
+  // adapters (rank 0: none): A, p of the tokens (f32: [rank][tpad]; bf16: three values that add up to it, [tile of 16
+  // tokens][32 ranks][3][lane][8]), their adapters (-1: none)
   const void *a;
   const float *p;
+  const uint16_t *parts;
   const int32_t *ids;
   int rank;
   int64_t tpad;
