@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(256) back_join_kernel(OuterArgs A) {
 // ---------------------------------------------------------------------------
 struct BackPlan {
   int64_t ntile, chunks, tpad, rowpad;
-  int rpad, splits, osplits;
+  RowsPlan dx;
+  int rpad, osplits;
   int64_t grads;  // values of both adapters' gradients
   size_t bo, go, geo, po, bto, pto, vto, ppo, vpo, ido, rgo, pao, oo, bytes;
 };
@@ -530,12 +531,12 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   const size_t size = dtype == IQ_DTYPE_F32 ? 4 : 2;
   p.ntile = (T + 15) / 16;
   p.chunks = row_chunks(rows);
-  p.splits = rows_splits(fmt, T, cols, p.chunks, dtype);
+  p.dx = plan_rows(fmt, T, cols, p.chunks, dtype);
   p.bo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
   p.go = p.bo + ws_up(kBoundBytes);
   p.geo = p.go + ws_up(grads_bytes(p.chunks, p.ntile, dtype));
   p.po = p.geo + ws_up(static_cast<size_t>(p.ntile) * 64);
-  p.bto = p.po + ws_up(rows_partial_bytes(T, cols, p.splits));
+  p.bto = p.po + ws_up(p.dx.bytes);
   p.bytes = p.bto + kWsAlign;
   if (!rank) return p;
   p.tpad = (T + 31) / 32 * 32;
@@ -673,7 +674,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     D.B = A.B;
     D.out = dx;
     D.partial = reinterpret_cast<float *>(base + P.po);
-    D.splits = P.splits;
+    D.plan = P.dx;
     D.a = lora_a;
     D.p = pt;
     D.parts = reinterpret_cast<const uint16_t *>(base + P.pao);

@@ -708,7 +708,7 @@ template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
 
 struct GluPlan {
   TokensPlan x;
-  int splits;
+  RowsPlan rows;
   size_t xo, eo, bo, do_, go, geo, po, bytes;
 };
 GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, bool backward) {
@@ -720,12 +720,12 @@ GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, b
   p.bytes = p.bo + kWsAlign;
   if (!backward) return p;
   const int64_t chunks = 2 * row_chunks(inter);
-  p.splits = rows_splits(fmt, T, hidden, chunks, dtype);
+  p.rows = plan_rows(fmt, T, hidden, chunks, dtype);
   p.do_ = p.bo + ws_up(kBoundBytes);
   p.go = p.do_ + ws_up(static_cast<size_t>(T) * 4);
   p.geo = p.go + ws_up(grads_bytes(chunks, p.x.ntile, dtype));
   p.po = p.geo + ws_up(p.x.ebytes);
-  p.bytes = p.po + ws_up(rows_partial_bytes(T, hidden, p.splits)) + kWsAlign;
+  p.bytes = p.po + ws_up(p.rows.bytes) + kWsAlign;
   return p;
 }
 
@@ -815,7 +815,7 @@ int run_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int6
   D.B = M.B;
   D.out = out;
   D.partial = reinterpret_cast<float *>(base + P.po);
-  D.splits = P.splits;
+  D.plan = P.rows;
   return launch_rows(fmt, dtype, D, stream);
 }
 

@@ -113,11 +113,14 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / H, wh = wave % H;
-  const int64_t cb = blockIdx.x / (2 / H), cols = A.nb * 256, rowbytes = A.nb * Geo<F>::BYTES;
-  const int half0 = H == 2 ? 0 : static_cast<int>(blockIdx.x & 1);  // the first half that the workgroup takes
-  const int64_t tt0 = static_cast<int64_t>(blockIdx.y) * TA;
+  const bool whole = blockIdx.x < A.plan.full;
+  const int64_t rest = blockIdx.x - A.plan.full, place = whole ? blockIdx.x : A.plan.full + rest / A.plan.splits;
+  const int splits = whole ? 1 : A.plan.splits, split = whole ? 0 : static_cast<int>(rest % A.plan.splits);
+  const int64_t across = place % A.plan.across, tt0 = place / A.plan.across * TA;
+  const int64_t cb = across / (2 / H), cols = A.nb * 256, rowbytes = A.nb * Geo<F>::BYTES;
+  const int half0 = H == 2 ? 0 : static_cast<int>(across & 1);  // the first half that the workgroup takes
   const int64_t per = (A.rows + 63) / 64, chunks = per * A.nmat;
-  const int64_t share = (chunks + A.splits - 1) / A.splits, ch0 = blockIdx.z * share;
+  const int64_t share = (chunks + splits - 1) / splits, ch0 = split * share;
   const int count = static_cast<int>(max(min(share, chunks - ch0), static_cast<int64_t>(0)));
   const int ew = weight_exponent(A.B);
   const int unit = 15 - ew - (Geo<F>::IQ1 ? 0 : 3);
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[j][c][k] = ldexpf(acc[j][c][k], ex[k] + ew - 15);
   }
-  if (LORA && blockIdx.z == 0) add_adapters<P, C>(A, tw, col, acc);
+  if (LORA && split == 0) add_adapters<P, C>(A, tw, col, acc);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t t0 = (tw + c) * 16 + q * 4;
@@ -355,27 +358,31 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = acc[j][c][k];
-      if (A.splits > 1)
-        store8u(A.partial + (blockIdx.z * A.T + t0 + k) * cols, 0, col, v);
-      else
+      if (whole)
         store8u(A.out, P == 1, (t0 + k) * cols + col, v);
+      else
+        store8u(A.partial + (rest * TA * 16 + t0 + k - tt0 * 16) * (128 * H), 0, wh * 128 + 8 * n, v);
     }
   }
 }
 
-// The splits' sums, in their order.
+// The splits' sums, in their order: a workgroup has 2,048 values of one tile of the rest.
 template <int P> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs A) {
-  const int64_t n = A.T * A.nb * 256, i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
+  constexpr int width = P == 2 ? 128 : 256;
+  const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * width, per = size / 2048;
+  const int64_t rest = blockIdx.x / per, i = blockIdx.x % per * 2048 + threadIdx.x * 8;
+  const int64_t place = A.plan.full + rest, t = place / A.plan.across * A.plan.tiles * 16 + i / width;
+  if (t >= A.T) return;
+  const float *from = A.partial + rest * A.plan.splits * size + i;
   float v[8];
-  load8u(A.partial, 0, i, v);
-  for (int s = 1; s < A.splits; ++s) {
+  load8u(from, 0, 0, v);
+  for (int s = 1; s < A.plan.splits; ++s) {
     float w[8];
-    load8u(A.partial, 0, s * n + i, w);
+    load8u(from, 0, s * size, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += w[j];
   }
-  store8u(A.out, P == 1, i, v);
+  store8u(A.out, P == 1, t * A.nb * 256 + place % A.plan.across * width + i % width, v);
 }
 
 // An empty sum's result (a fill by the runtime is no kernel, and would enter a captured graph as another node).
@@ -386,41 +393,48 @@ __global__ void __launch_bounds__(256) zero_kernel(uint16_t *p, size_t n) {
 
 template <int F, int P, int C, int H, bool LORA> void launch_tile(const RowsArgs &A, hipStream_t stream) {
   hipLaunchKernelGGL((rows_kernel<F, P, C, H, LORA>),
-                     dim3(static_cast<unsigned>(A.nb * (2 / H)), static_cast<unsigned>((A.G.ntile + 4 * C - 1) / (4 * C)),
-                          static_cast<unsigned>(A.splits)),
-                     dim3(256 * H), 0, stream, A);
-}
-
-// Token tiles of a workgroup.
-int rows_tiles(int fmt, int dtype, int64_t ntile) {
-  if (dtype == IQ_DTYPE_F32) return kCodebook[fmt] > 1024 ? 4 : 8;
-  return ntile <= 8 ? 4 : 16;
+                     dim3(static_cast<unsigned>(A.plan.full + A.plan.rest * A.plan.splits)), dim3(256 * H), 0, stream, A);
 }
 
 template <int F, bool LORA> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t stream) {
-  const int tiles = rows_tiles(F, dtype, A.G.ntile);
   if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, (Geo<F>::N > 1024 ? 1 : 2), 1, LORA>(A, stream);
-  if (tiles == 4) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
+  if (A.plan.tiles == 4) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
+  if (A.plan.tiles == 8) return launch_tile<F, 1, 2, 2, LORA>(A, stream);
   launch_tile<F, 1, 4, 2, LORA>(A, stream);
 }
 
 }  // namespace
 
-// Splits of the rows: rounds of the workgroups over 256 CUs, each 8 us and 1.6 for a chunk (64 rows; 0.8 with tiles of 64
-// tokens), against 3 us of the joining launch and the way of the partial sums there and back (4 TB/s).
-int rows_splits(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) {
+// The tiles of 16 c tokens that cost least: whole rounds of them over 256 CUs, and the rest in as many splits of the
+// rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below; a split rest also
+// costs the joining launch's 3 us and the way of its sums there and back (4 TB/s).
+RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) {
+  struct Tile {
+    int tiles;
+    double chunk;
+  };
+  const bool f32 = dtype == IQ_DTYPE_F32;
+  constexpr Tile bf16s[3] = {{4, 1.55}, {8, 1.6}, {16, 2.3}};
+  const Tile single = {kCodebook[fmt] > 1024 ? 4 : 8, kCodebook[fmt] > 1024 ? 2.0 : 2.7};
   const int64_t ntile = (T + 15) / 16;
-  const int tiles = rows_tiles(fmt, dtype, ntile);
-  const int64_t wgs = cols / (dtype == IQ_DTYPE_F32 ? 128 : 256) * ((ntile + tiles - 1) / tiles);
-  int best = 1;
+  RowsPlan best{};
   double least = 0.0;
-  for (int s = 1; s <= 64 && s <= chunks; ++s) {
-    const double rounds = static_cast<double>((wgs * s + 255) / 256), length = static_cast<double>((chunks + s - 1) / s);
-    double us = rounds * (8.0 + length * (tiles == 4 ? 0.8 : 1.6));
-    if (s > 1) us += 3.0 + static_cast<double>(s) * static_cast<double>(T) * static_cast<double>(cols) * 8.0 / 4e6;
-    if (s == 1 || us < least) {
-      least = us;
-      best = s;
+  for (int k = 0; k < (f32 ? 1 : 3); ++k) {
+    const Tile &tile = f32 ? single : bf16s[k];
+    const int64_t across = cols / (f32 ? 128 : 256), all = across * ((ntile + tile.tiles - 1) / tile.tiles);
+    const int64_t full = all / 256 * 256, rest = all - full, size = static_cast<int64_t>(tile.tiles) * 16 * (f32 ? 128 : 256) * 4;
+    const double whole = static_cast<double>(full / 256) * (8.0 + static_cast<double>(chunks) * tile.chunk);
+    for (int s = 1; s <= 64 && s <= chunks; ++s) {
+      if (s > 1 && !rest) break;
+      double us = whole;
+      if (rest)
+        us += static_cast<double>((rest * s + 255) / 256) * (8.0 + static_cast<double>((chunks + s - 1) / s) * tile.chunk);
+      if (s > 1) us += 3.0 + static_cast<double>(s * rest * size) * 2.0 / 4e6;
+      if (!best.tiles || us < least) {
+        least = us;
+        best = RowsPlan{tile.tiles, across, s > 1 ? full : all, s > 1 ? rest : 0, s,
+                        s > 1 ? static_cast<size_t>(s * rest * size) : 0};
+      }
     }
   }
   return best;
@@ -439,9 +453,9 @@ int launch_rows(int fmt, int dtype, const RowsArgs &A, hipStream_t stream) {
   IQ_BY_FMT(fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-  if (A.splits > 1) {
-    const int64_t units = A.T * A.nb * 32;
-    const dim3 wgs(static_cast<unsigned>((units + 255) / 256));
+  if (A.plan.rest) {
+    const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * (dtype == IQ_DTYPE_F32 ? 128 : 256);
+    const dim3 wgs(static_cast<unsigned>(A.plan.rest * (size / 2048)));
     if (dtype == IQ_DTYPE_F32)
       hipLaunchKernelGGL(rows_join_kernel<2>, wgs, dim3(256), 0, stream, A);
     else

@@ -44,8 +44,16 @@ struct Source {
 // seven bits).
 inline int source_parts(const Source &s) { return s.ex || s.dtype == IQ_DTYPE_BF16 ? 1 : 2; }
 
-// dx of gradients G with one or two encoded weights of the same size (see
-// iq_rows.hip).
+// dx of gradients G with one or two encoded weights of the same size (see iq_rows.hip).  The workgroups' tiles of dx:
+// the first `full` whole, of the others the rows split, whose sums a second launch adds.
+struct RowsPlan {
+  int tiles;       // of 16 tokens, in a workgroup's tile
+  int64_t across;  // tiles of dx beside each other
+  int64_t full, rest;
+  int splits;
+  size_t bytes;    // of the rest's partial sums
+};
+RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype);
 struct RowsArgs {
   const uint8_t *packed[2];
   int nmat;
@@ -53,9 +61,9 @@ struct RowsArgs {
   const _Float16 *tab;
   Grads G;
   Bound B;
-  void *out;       // dx, or null where only partial sums are wanted
-  float *partial;  // [split][T][cols], used where the launch splits
-  int splits;
+  void *out;
+  float *partial;  // [tile of the rest][split][16 tiles tokens][128 or 256 columns]
+  RowsPlan plan;
   // adapters (rank 0: none): A, p of the tokens (f32: [rank][tpad]; bf16: three values that add up to it, [tile of 16
   // tokens][32 ranks][3][lane][8]), their adapters (-1: none)
   const void *a;
@@ -65,10 +73,6 @@ struct RowsArgs {
   int rank;
   int64_t tpad;
 };
-int rows_splits(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype);
-inline size_t rows_partial_bytes(int64_t T, int64_t cols, int splits) {
-  return splits > 1 ? static_cast<size_t>(splits) * T * cols * 4 : 0;
-}
 inline int block_bytes(int fmt) {
   constexpr int bytes[5] = {Geo<IQ2_XXS>::BYTES, Geo<IQ2_XS>::BYTES, Geo<IQ2_S>::BYTES, Geo<IQ1_S>::BYTES,
                             Geo<IQ1_M>::BYTES};
