@@ -565,8 +565,8 @@ int check_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n,
   if (rows > (int64_t(1) << 24) || cols > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   if (rank < 0 || rank > 1024 || (rank && n < 1)) return IQ_ERR_ARG;
   const int64_t ntile = (T + 15) / 16;
-  if (ntile > 4 * 65535 || (rank && n > 65535)) return IQ_ERR_SHAPE;  // grids of dx, of the adapters' gradients
-  if (T * (cols / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;    // the joining launch
+  if (ntile > 4 * 65535 || (rank && n > 65535)) return IQ_ERR_SHAPE;  // the adapters' gradients' grid
+  if (T * (cols / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;    // the tiles of dx
   if (rank && (ntile + 1) * 2 * ((rank + 31) / 32) >= kMaxWG) return IQ_ERR_SHAPE;
   if (rank && (T + 7) / 8 + n * ((rows + 767) / 512) + 128 >= kMaxWG) return IQ_ERR_SHAPE;
   return IQ_OK;

@@ -735,9 +735,8 @@ int check_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T) {
   if (inter < 0 || T < 0 || hidden <= 0 || hidden % 256 != 0) return IQ_ERR_SHAPE;
   if (inter > (int64_t(1) << 24) || hidden > (int64_t(1) << 24) || T > (int64_t(1) << 24)) return IQ_ERR_SHAPE;
   const int64_t ntile = (T + 15) / 16;
-  if (ntile > 4 * 65535) return IQ_ERR_SHAPE;  // token tiles of the second and third launch
-  // the joining launch
-  if (T * (hidden / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;
+  if (ntile > 4 * 65535) return IQ_ERR_SHAPE;  // token tiles of the products
+  if (T * (hidden / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;  // the tiles of dx
   return IQ_OK;
 }
 

@@ -288,11 +288,12 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
         }
     }
     // What the stage after the next needs has to be there.  Four buffers: the gradients requested a stage ago, so that
-    // those of this stage and a payload requested since may be on their way; three: the gradients of this stage, but
-    // not a payload requested after them.
-    if (NA == 4)
+    // those of this stage and a payload requested since may be on their way (of a wave without gradients to request only
+    // a payload: with more allowed, the end of the one before it could be among them); three: the gradients of this
+    // stage, but not a payload requested after them.
+    if (NA == 4 && (NP % NW == 0 || wave < NP))
       wait_loads<NPW + NR>();
-    else if (U == 1)
+    else if (NA == 4 || U == 1)
       wait_loads<NR>();
     else
       wait_loads<0>();

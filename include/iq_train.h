@@ -105,7 +105,7 @@ int iq_glu_workspace_size(int fmt, int64_t inter, int64_t hidden, int dtype, int
  * values) under one power of two per token that bounds both: 2^31 or less above
  * the largest of them for any weights whose rows and tokens are not concentrated
  * in single values, which leaves 2^-39 of that bound as the step.
- * Otherwise as iq_glu. */
+ * inter == 0: dx is zeros.  Otherwise as iq_glu. */
 int iq_glu_backward(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int64_t hidden,
                     const float *grid, const void *x, const uint8_t *exponents, const void *dh, int dtype,
                     int64_t T, int act, void *dx, void *workspace, size_t workspace_bytes, int32_t *status,

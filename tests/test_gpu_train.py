@@ -122,7 +122,7 @@ class Block:
     """Weights of a gated block, and what its sums may be off by."""
 
     def __init__(self, orc, fmt, inter, nb, seed):
-        self.fmt, self.nb, self.inter = fmt, nb, inter
+        self.fmt, self.nb, self.inter, self.adds = fmt, nb, inter, 276 + nb
         self.grid = inputs.grid_for(fmt, 70 + seed)
         self.gate, self.up = payload(fmt, inter, nb, seed), payload(fmt, inter, nb, seed + 1)
         self.wg, self.wu = decoded(orc, fmt, self.gate, self.grid), decoded(orc, fmt, self.up, self.grid)
@@ -131,7 +131,7 @@ class Block:
         return self.fmt, dev(self.gate), dev(self.up), dev(self.grid)
 
     def sums(self, x, parts2):
-        off = (276 + self.nb) * 2 * U + (2.0 ** -22 if parts2 else 0)
+        off = self.adds * 2 * U + (2.0 ** -22 if parts2 else 0)
         return [(x @ w.T, off * (np.abs(x) @ np.abs(w).T)) for w in (self.wg, self.wu)]
 
     def forward(self, x, act, dtype):
@@ -214,6 +214,33 @@ def test_glu_backward(api, orc, fmt, dtype, keep):
         if inter * T >= 500:  # every output has a factor of each sum: fewer may all be ones that nearly cancel
             assert np.linalg.norm(f64(got) - dx) <= (2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -19) * \
                 np.linalg.norm(dx)
+
+
+def some_of(T):
+    """Tokens of a large call that are checked, each output row being its token's alone: the ends, those beside the
+    edges of tiles, others at random."""
+    return np.unique(np.r_[0, 1, 15, 16, 63, 64, 255, 256, T // 2, T - 5:T, inputs.rng(T).integers(0, T, 50)])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_glu_of_many_tokens(api, orc, fmt, dtype):
+    """Sizes at which workgroups take tiles of both weights, the last rows and tokens ending inside one."""
+    inter, nb, T, act = 1500, 8, 4100, "silu"
+    print("[case] glu of many tokens", fmt, dtype, flush=True)
+    b = Block(orc, fmt, inter, nb, 11)
+    b.adds = 257 * nb + 16  # a sum goes through all blocks
+    x, dh, at = tokens(T, nb, 12, dtype), upstream(T, inter, 13, dtype), some_of(T)
+    got = f64(api.glu(*b.args(), x, activation=act))[at]
+    want, off = b.forward(f64(x)[at], act, dtype)
+    assert np.all(np.abs(got - want) <= off)
+    for keep in (False, True):
+        k = api.checkpoint(x) if keep else x
+        got = f64(api.glu_backward(*b.args(), k, dh, activation=act))[at]
+        want, off = b.backward(f64(api.restore(*k) if keep else x)[at], f64(dh)[at], act, dtype,
+                               dtype == torch.float32 and not keep)
+        assert np.all(np.abs(got - want) <= off), keep
+        assert np.linalg.norm(got - want) <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20) * np.linalg.norm(want)
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -377,6 +404,46 @@ def test_linear_backward_random(api, orc, fmt, dtype):
             assert np.all(np.abs(f64(got[k]) - want[k]) <= offs[k] + np.abs(want[k]) * OUT[dtype] * 1.01), k
             rel = np.linalg.norm(f64(got[k]) - want[k]) / np.linalg.norm(want[k])
             assert rel <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_backward_of_many_tokens(api, orc, fmt, dtype):
+    """Sizes at which workgroups take wide tiles of dx, in whole rounds with a rest that is split over the rows, and
+    ranks in several groups; all adapters in any 32 tokens."""
+    for rows, nb, T, N, r in ((333, 16, 1100, 5, 20), (1001, 16, 4100, 2, 40), (700, 8, 4100, 3, 3), (1001, 16, 4100, 0, 0)):
+        print("[case] linear backward of many tokens", fmt, dtype, rows, nb, T, N, r, flush=True)
+        g = inputs.rng(rows + T)
+        cols = nb * 256
+        grid = inputs.grid_for(fmt, 500)
+        p = payload(fmt, rows, nb, 7, d16=g.choice([0x2000, 0x2400, 0x1c00], (rows, nb)))  # 2^-7, 2^-6, 2^-8
+        w, at = decoded(orc, fmt, p, grid), some_of(T)
+        dy = g.integers(-1, 2, (T, rows)).astype(np.float32) * (g.random((T, rows)) < 0.25)
+        x = g.integers(-1, 2, (T, cols)).astype(np.float32)
+        a, b = g.integers(-1, 2, (N, r, cols)).astype(np.float32), g.integers(-1, 2, (N, rows, r)).astype(np.float32)
+        ids = g.integers(-1, max(N, 1), T).astype(np.int32)
+        dx, size = dy[at].astype(np.float64) @ w, np.abs(dy[at]) @ np.abs(w)
+        want = [(dx, size), (np.zeros(a.shape), np.zeros(a.shape)), (np.zeros(b.shape), np.zeros(b.shape))]
+        for n in range(N):
+            m = ids == n
+            back, v = (dy[m] @ b[n]).astype(np.float64), (x[m] @ a[n].T).astype(np.float64)
+            all_back = np.zeros((T, r))
+            all_back[m] = back
+            dx += all_back[at] @ a[n]
+            size += np.abs(all_back[at]) @ np.abs(a[n])
+            want[1][0][n], want[1][1][n] = back.T @ x[m], np.abs(back).T @ np.abs(x[m])
+            want[2][0][n], want[2][1][n] = dy[m].T @ v, np.abs(dy[m]).T @ np.abs(v)
+        if N:
+            got = api.linear_backward(fmt, dev(p), dev(grid), dev(dy, dtype), x=dev(x, dtype), lora_a=dev(a, dtype),
+                                      lora_b=dev(b, dtype), lora_ids=dev(ids))
+        else:
+            got = [api.linear_backward(fmt, dev(p), dev(grid), dev(dy, dtype))]
+        for k, t in enumerate(got):  # partial sums are exact below 2^24 steps, of 2^-11 for dx, of one for the others
+            v, s = want[k]
+            sure = s < (2.0 ** 24 if k else 2.0 ** 13)
+            assert sure.mean() > 0.5, (k, rows, nb, T, N, r)
+            t = f64(t)[at] if k == 0 else f64(t)
+            assert np.array_equal(t[sure], round_to(v, dtype)[sure]), (k, rows, nb, T, N, r)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
