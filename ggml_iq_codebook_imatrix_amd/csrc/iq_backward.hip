@@ -1,8 +1,7 @@
 // iq_backward.hip -- iq_linear_backward: the gradients by an encoded projection's
 // tokens and by its low-rank adapters (include/iq_train.h).
 //
-// Launches: dy into operand order, with the bound on the weights and B with its rows
-// in line; the rank-wide products p = s dy B and v = s x A^T; dx (iq_rows.hip, with
+// Launches: dy and the adapters into operand order, with the bound on the weights; the rank-wide products p = s dy B and v = s x A^T; dx (iq_rows.hip, with
 // p A added to its sums); and dA, dB as sums over the tokens.
 
 #include "iq_train.hpp"
@@ -27,8 +26,11 @@ struct BackPrepArgs {
   Codebooks books;
   int convert;  // dx is wanted
   Adapters L;
-  void *bt;      // B [adapter][rank][rowpad], of dtype
-  int64_t rowpad;
+  // OUT, A and B for the rank-wide products [adapter][tile of 16 ranks][64 of k][half][lane][8], of dtype: lane 16 q + n
+  // of half h holds rank n, k = 16 q + 8 h on; zeros past the last rank and row
+  void *ao, *bo;
+  int tiles;
+  int64_t cols, rowpad;
 };
 
 // One wave brings one token's gradient into the order of Grads.
@@ -84,16 +86,33 @@ template <int P> __global__ void __launch_bounds__(512) back_prep_kernel(BackPre
     }
     w -= A.books.wg[0];
   }
-  // 512 rows of one adapter's B, turned; zeros past the last row
-  const int64_t per = (A.rowpad + 511) / 512, a = w / per, row = w % per * 512 + threadIdx.x;
-  if (row >= A.rowpad) return;
-  const int64_t from = (a * A.rows + min(row, A.rows - 1)) * A.L.rank, to = a * A.L.rank * A.rowpad + row;
-  for (int j = 0; j < A.L.rank; ++j) {
-    if (P == 1)
-      static_cast<uint16_t *>(A.bt)[to + j * A.rowpad] =
-          row < A.rows ? static_cast<const uint16_t *>(A.L.b)[from + j] : static_cast<uint16_t>(0);
-    else
-      static_cast<float *>(A.bt)[to + j * A.rowpad] = row < A.rows ? static_cast<const float *>(A.L.b)[from + j] : 0.0f;
+  // 256 rows of B or columns of A, of a tile of 16 ranks
+  int64_t per = A.rowpad >> 8;
+  const bool of_a = w >= A.L.n * A.tiles * per;
+  if (of_a) {
+    w -= A.L.n * A.tiles * per;
+    per = A.cols >> 8;
+  }
+  const int64_t tile = w / per, a = tile / A.tiles;
+  const int lane = threadIdx.x & 63, h = (threadIdx.x >> 6) & 1, rank = static_cast<int>(tile % A.tiles) * 16 + (lane & 15);
+  const int64_t block = w % per * 4 + (threadIdx.x >> 7), k = block * 64 + (lane >> 4) * 16 + h * 8;
+  float v[8];
+  if (of_a && rank < A.L.rank) {
+    load8u(A.L.a, P == 1, (a * A.L.rank + rank) * A.cols + k, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = !of_a && rank < A.L.rank && k + j < A.rows ? load1(A.L.b, P == 1, (a * A.rows + k + j) * A.L.rank + rank) : 0.0f;
+  }
+  const int64_t to = ((tile * per * 4 + block) * 2 + h) * 512 + lane * 8;
+  if (P == 1) {  // as they were: a NaN keeps its bits' top half
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(of_a ? A.ao : A.bo) + to) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    __builtin_memcpy(static_cast<float *>(of_a ? A.ao : A.bo) + to, v, 32);
   }
 }
 
@@ -103,7 +122,7 @@ template <int P> __global__ void __launch_bounds__(512) back_prep_kernel(BackPre
 struct Shrink {
   Source s;         // tokens [T, k]
   int64_t k;
-  const void *w;    // [adapter][rank][kpad], of dtype; zeros past k
+  const void *w;    // adapters as BackPrepArgs has them
   int64_t kpad;     // a multiple of 256
   float *out;       // f32: [ranks, in 32s][tpad]
   uint16_t *parts;  // three bf16 values each [32 tokens][16 ranks, 32s of them][3][lane][8]
@@ -228,11 +247,12 @@ __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, boo
     const uint32_t group = static_cast<uint32_t>(__ballot(mine == a));
     if (a < 0 || (group & ((1u << slot) - 1u))) continue;  // done with an earlier token
     const bool tile[2] = {(group & 0xffffu) != 0, (group >> 16) != 0};
+    const int tiles = (A.L.rank + 15) >> 4;
     int64_t t[2], wr[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {  // rows of other tokens read this one's
       t[r] = tt * 32 + (((group >> (16 * r + n)) & 1u) ? 16 * r + n : slot);
-      wr[r] = (static_cast<int64_t>(a) * A.L.rank + min(r0 + r * 16 + n, A.L.rank - 1)) * S.kpad;
+      wr[r] = (static_cast<int64_t>(a) * tiles + min(2 * rg + r, tiles - 1)) * S.kpad * 16 + lane * 8;
     }
     f32x4 acc[4] = {};  // [token tile][rank tile]
     if constexpr (BF16) {
@@ -241,12 +261,12 @@ __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, boo
       Sixteen x[3][2];
       u32x4 b[3][2][2];
       const auto load = [&](int u, int64_t k0) __attribute__((always_inline)) {
-        const int64_t k = min(k0, S.kpad - 64) + q * 16;
+        const int64_t block = min(k0, S.kpad - 64), k = block + q * 16;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if (tile[r]) x[u][r] = load_sixteen(S.s, S.k, t[r], k);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) b[u][r][h] = ldu<u32x4>(static_cast<const uint16_t *>(S.w) + wr[r] + k + 8 * h);
+          for (int h = 0; h < 2; ++h) b[u][r][h] = ldu<u32x4>(static_cast<const uint16_t *>(S.w) + wr[r] + block * 16 + 512 * h);
         }
       };
       load(0, wave * 64);
@@ -278,7 +298,7 @@ __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, boo
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             if (tile[r]) source8(S.s, S.k, t[r], k, x[r]);
-            load8u(S.w, 0, wr[r] + k, b[r]);
+            load8u(S.w, 0, wr[r] + k0 * 16 + 512 * h, b[r]);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -515,9 +535,9 @@ __global__ void __launch_bounds__(256) back_join_kernel(OuterArgs A) {
 struct BackPlan {
   int64_t ntile, chunks, tpad, rowpad;
   RowsPlan dx;
-  int rpad, osplits;
+  int rpad, tiles, osplits;
   int64_t grads;  // values of both adapters' gradients
-  size_t bo, go, geo, po, bto, pto, vto, ppo, vpo, ido, rgo, pao, oo, bytes;
+  size_t bo, go, geo, po, bto, pto, ato, vto, ppo, vpo, ido, rgo, pao, oo, bytes;
 };
 // Splits of the tokens for the adapters' gradients: as long as workgroups are fewer than CUs and each wave keeps a step.
 int outer_splits(int64_t rows, int64_t cols, int64_t T, int n, int rank) {
@@ -542,7 +562,9 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   p.tpad = (T + 31) / 32 * 32;
   p.rowpad = (rows + 255) / 256 * 256;
   p.rpad = (rank + 31) / 32 * 32;
-  p.pto = p.bto + ws_up(static_cast<size_t>(n) * rank * p.rowpad * size);
+  p.tiles = (rank + 15) / 16;
+  p.ato = p.bto + ws_up(static_cast<size_t>(n) * p.tiles * 16 * p.rowpad * size);
+  p.pto = p.ato + ws_up(static_cast<size_t>(n) * p.tiles * 16 * cols * size);
   const size_t whole = dtype == IQ_DTYPE_F32 ? ws_up(static_cast<size_t>(p.rpad) * p.tpad * 4) : 0;
   const size_t parts = ws_up(static_cast<size_t>(p.rpad) * p.tpad * 6);
   p.vto = p.pto + whole;
@@ -568,7 +590,8 @@ int check_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, int n,
   if (ntile > 4 * 65535 || (rank && n > 65535)) return IQ_ERR_SHAPE;  // the adapters' gradients' grid
   if (T * (cols / 256) >= (int64_t(1) << 26)) return IQ_ERR_SHAPE;    // the tiles of dx
   if (rank && (ntile + 1) * 2 * ((rank + 31) / 32) >= kMaxWG) return IQ_ERR_SHAPE;
-  if (rank && (T + 7) / 8 + n * ((rows + 767) / 512) + 128 >= kMaxWG) return IQ_ERR_SHAPE;
+  if (rank && (T + 7) / 8 + n * static_cast<int64_t>((rank + 15) / 16) * ((rows + 255) / 256 + cols / 256) + 128 >= kMaxWG)
+    return IQ_ERR_SHAPE;
   return IQ_OK;
 }
 
@@ -632,9 +655,13 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
               A.books.wg[0], fmt >= IQ1_S};
   A.convert = dx != nullptr;
   A.L = L;
-  A.bt = base + P.bto;
+  A.ao = base + P.ato;
+  A.bo = base + P.bto;
+  A.tiles = P.tiles;
+  A.cols = cols;
   A.rowpad = P.rowpad;
-  const int64_t wgs = (dx ? kScaleSlots + A.nconv + A.books.wg[0] : 0) + L.n * ((P.rowpad + 511) / 512);
+  const int64_t wgs = (dx ? kScaleSlots + A.nconv + A.books.wg[0] : 0) +
+                      static_cast<int64_t>(L.n) * P.tiles * ((P.rowpad + cols) / 256);
   if (dtype == IQ_DTYPE_F32)
     hipLaunchKernelGGL(back_prep_kernel<2>, dim3(static_cast<unsigned>(wgs)), dim3(512), 0, stream, A);
   else
@@ -642,8 +669,8 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   if (!run_launched()) return IQ_ERR_HIP;
   if (rank) {
     ShrinkArgs S{};
-    S.of[0] = Shrink{Source{dy, nullptr, dtype}, rows, A.bt, P.rowpad, pt, pp};
-    S.of[1] = Shrink{Source{x, exponents, dtype}, cols, lora_a, cols, vt, vp};
+    S.of[0] = Shrink{Source{dy, nullptr, dtype}, rows, A.bo, P.rowpad, pt, pp};
+    S.of[1] = Shrink{Source{x, exponents, dtype}, cols, A.ao, cols, vt, vp};
     S.dtype = dtype;
     S.T = T;
     S.tpad = P.tpad;
