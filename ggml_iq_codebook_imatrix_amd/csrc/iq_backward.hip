@@ -31,6 +31,7 @@ struct BackPrepArgs {
   void *ao, *bo;
   int tiles;
   int64_t cols, rowpad;
+  uint32_t *wild;  // OUT [adapter][tile of 16 ranks][256 columns of A]: not all of them are finite
 };
 
 // One wave brings one token's gradient into the order of Grads.
@@ -103,6 +104,13 @@ template <int P> __global__ void __launch_bounds__(512) back_prep_kernel(BackPre
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       v[j] = !of_a && rank < A.L.rank && k + j < A.rows ? load1(A.L.b, P == 1, (a * A.rows + k + j) * A.L.rank + rank) : 0.0f;
+  }
+  if (of_a) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bad |= !finite_f(v[j]);
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) A.wild[w] = any;
   }
   const int64_t to = ((tile * per * 4 + block) * 2 + h) * 512 + lane * 8;
   if (P == 1) {  // as they were: a NaN keeps its bits' top half
@@ -537,7 +545,7 @@ struct BackPlan {
   RowsPlan dx;
   int rpad, tiles, osplits;
   int64_t grads;  // values of both adapters' gradients
-  size_t bo, go, geo, po, bto, pto, ato, vto, ppo, vpo, ido, rgo, pao, oo, bytes;
+  size_t bo, go, geo, po, bto, pto, ato, vto, ppo, vpo, ido, rgo, pao, wo, oo, bytes;
 };
 // Splits of the tokens for the adapters' gradients: as long as workgroups are fewer than CUs and each wave keeps a step.
 int outer_splits(int64_t rows, int64_t cols, int64_t T, int n, int rank) {
@@ -573,7 +581,8 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   p.ido = p.vpo + parts;
   p.rgo = p.ido + ws_up(static_cast<size_t>(p.tpad) * 4);
   p.pao = p.rgo + ws_up(static_cast<size_t>(p.tpad) / 4);
-  p.oo = p.pao + (dtype == IQ_DTYPE_BF16 ? parts : 0);
+  p.wo = p.pao + (dtype == IQ_DTYPE_BF16 ? parts : 0);
+  p.oo = p.wo + ws_up(static_cast<size_t>(n) * p.tiles * (cols / 256) * 4);
   p.grads = static_cast<int64_t>(n) * rank * (rows + cols);
   p.osplits = outer_splits(rows, cols, T, n, rank);
   p.bytes = p.oo + (p.osplits > 1 ? ws_up(static_cast<size_t>(p.osplits) * p.grads * 4) : 0) + kWsAlign;
@@ -657,6 +666,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   A.L = L;
   A.ao = base + P.ato;
   A.bo = base + P.bto;
+  A.wild = reinterpret_cast<uint32_t *>(base + P.wo);
   A.tiles = P.tiles;
   A.cols = cols;
   A.rowpad = P.rowpad;
@@ -705,6 +715,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     D.a = lora_a;
     D.p = pt;
     D.parts = reinterpret_cast<const uint16_t *>(base + P.pao);
+    D.wild = reinterpret_cast<const uint32_t *>(base + P.wo);
     D.ids = ids;
     D.rank = rank;
     D.tpad = P.tpad;

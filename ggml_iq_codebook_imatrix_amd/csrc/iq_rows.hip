@@ -25,19 +25,22 @@ namespace {
 
 // acc[j][c] += p A of the adapters that the wave's tokens (tiles tt .. tt + C - 1) name, columns col + j of the lane's
 // eight.  32 ranks at a time: a lane has eight ranks of its eight columns, which byte permutations make operands of
-// (bf16; p is the sum of three bf16 values, without a rounding), or four ranks at a time on the fp32 cores.  What
-// rows of tokens with other adapters give is dropped.
+// (bf16; p is the sum of three bf16 values, without a rounding), or four ranks at a time on the fp32 cores.  Rows of
+// tokens with other adapters are zeros; where A is not finite, 0 * A would reach them, and what they give is dropped.
 template <int P, int C>
 __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int64_t col, f32x4 (&acc)[8][C]) {
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int64_t cols = A.nb * 256, mytok = tt * 16 + lane;
+  const int64_t cols = A.nb * 256, mytok = tt * 16 + lane, cb = col >> 8;
   const int mine = lane < 16 * C && mytok < A.T ? A.ids[mytok] : -1;
+  const int tiles = (A.rank + 15) >> 4;
   uint64_t todo = __ballot(mine >= 0);
   while (todo) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
     const uint64_t group = __ballot(mine == a);
     todo &= ~group;
     for (int r0 = 0; r0 < A.rank; r0 += P == 1 ? 32 : 4) {
+      const uint32_t *wild = A.wild + (static_cast<int64_t>(a) * tiles + (r0 >> 4)) * A.nb + cb;
+      const bool drop = wild[0] | wild[P == 1 && r0 + 16 < A.rank ? A.nb : 0];
       if constexpr (P == 1) {
         const uint16_t *from = static_cast<const uint16_t *>(A.a) + static_cast<int64_t>(a) * A.rank * cols + col;
         u32x4 w[8];  // ranks r0 + 8 q + i; past the last p is zero
@@ -48,28 +51,31 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
           const uint32_t tokens = static_cast<uint32_t>(group >> (16 * c)) & 0xffffu;
           if (!tokens) continue;
           const uint16_t *p = A.parts + ((tt + c) * ((A.rank + 31) >> 5) + (r0 >> 5)) * 1536 + lane * 8;
+          const uint32_t keep = (tokens >> n) & 1u ? ~0u : 0u;
           bf16x8 v[3];
 #pragma unroll
-          for (int k = 0; k < 3; ++k) v[k] = ldu<bf16x8>(p + k * 512);
+          for (int k = 0; k < 3; ++k) {
+            u32x4 t = ldu<u32x4>(p + k * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] &= keep;
+            v[k] = __builtin_bit_cast(bf16x8, t);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
             u32x4 o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_perm(w[2 * i + 1][j >> 1], w[2 * i][j >> 1], sel);
-            if (tokens == 0xffffu) {
-#pragma unroll
-              for (int k = 0; k < 3; ++k)
-                acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[k], __builtin_bit_cast(bf16x8, o), acc[j][c], 0, 0, 0);
-              continue;
-            }
-            f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 d = acc[j][c];
 #pragma unroll
             for (int k = 0; k < 3; ++k)
               d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[k], __builtin_bit_cast(bf16x8, o), d, 0, 0, 0);
+            if (drop) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((tokens >> (4 * q + k)) & 1u) acc[j][c][k] += d[k];
+              for (int k = 0; k < 4; ++k)
+                if (!((tokens >> (4 * q + k)) & 1u)) d[k] = acc[j][c][k];
+            }
+            acc[j][c] = d;
           }
         }
       } else {
@@ -77,14 +83,18 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
         load8u(A.a, 0, (static_cast<int64_t>(a) * A.rank + min(r0 + q, A.rank - 1)) * cols + col, w);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          if (!((group >> (16 * c)) & 0xffffu)) continue;
-          const float v = r0 + q < A.rank ? A.p[(r0 + q) * A.tpad + (tt + c) * 16 + n] : 0.0f;
+          const uint32_t tokens = static_cast<uint32_t>(group >> (16 * c)) & 0xffffu;
+          if (!tokens) continue;
+          const float v = r0 + q < A.rank && ((tokens >> n) & 1u) ? A.p[(r0 + q) * A.tpad + (tt + c) * 16 + n] : 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            f32x4 d = __builtin_amdgcn_mfma_f32_16x16x4f32(v, w[j], acc[j][c], 0, 0, 0);
+            if (drop) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((group >> (16 * c + 4 * q + k)) & 1u) acc[j][c][k] += d[k];
+              for (int k = 0; k < 4; ++k)
+                if (!((tokens >> (4 * q + k)) & 1u)) d[k] = acc[j][c][k];
+            }
+            acc[j][c] = d;
           }
         }
       }

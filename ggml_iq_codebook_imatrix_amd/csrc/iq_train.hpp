@@ -65,10 +65,12 @@ struct RowsArgs {
   float *partial;  // [tile of the rest][split][16 tiles tokens][128 or 256 columns]
   RowsPlan plan;
   // adapters (rank 0: none): A, p of the tokens (f32: [rank][tpad]; bf16: three values that add up to it, [tile of 16
-  // tokens][32 ranks][3][lane][8]), their adapters (-1: none)
+  // tokens][32 ranks][3][lane][8]), their adapters (-1: none),
+  // and where A is not finite [adapter][tile of 16 ranks][256 columns]
   const void *a;
   const float *p;
   const uint16_t *parts;
+  const uint32_t *wild;
   const int32_t *ids;
   int rank;
   int64_t tpad;

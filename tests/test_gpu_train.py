@@ -478,6 +478,29 @@ def test_linear_backward_adapters_and_bad_tokens(api, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_backward_with_an_adapter_that_is_not_finite(api, dtype):
+    """An infinity in one adapter's A: what it reaches is dx of its tokens, in that column, and its gradient by B."""
+    print("[case] linear backward wild adapter", dtype, flush=True)
+    fmt, rows, nb, T, N, r = "IQ2_XS", 70, 3, 90, 3, 40
+    g = inputs.rng(9)
+    grid, p = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
+    x, dy = tokens(T, nb, 3, dtype), upstream(T, rows, 4, dtype)
+    a = dev(g.standard_normal((N, r, nb * 256), dtype=np.float32), dtype)
+    b = dev(g.standard_normal((N, rows, r), dtype=np.float32), dtype)
+    ids = g.integers(-1, N, T).astype(np.int32)
+    run = lambda a: api.linear_backward(fmt, p, grid, dy, x=x, lora_a=a, lora_b=b, lora_ids=dev(ids))  # noqa: E731
+    clean, wild = run(a), a.clone()
+    wild[1, 37, 300] = float("inf")
+    dx, da, db = run(wild)
+    keep = torch.ones_like(dx, dtype=torch.bool)
+    keep[torch.from_numpy(ids == 1).cuda(), 300] = False
+    assert torch.equal(dx[keep], clean[0][keep]) and not bool(dx[~keep].isfinite().any())
+    assert torch.equal(da, clean[1]) and torch.equal(db[[0, 2]], clean[2][[0, 2]])
+    assert torch.equal(db[1, :, :37], clean[2][1, :, :37]) and torch.equal(db[1, :, 38:], clean[2][1, :, 38:])
+    assert not bool(db[1, :, 37].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_nothing_to_do(api, dtype):
     print("[case] empty", dtype, flush=True)
     fmt, nb = "IQ1_M", 2
