@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
   constexpr int NA = Geo<F>::N > 512 ? 3 : 4;  // stages of gradients in LDS, beside a large codebook one fewer
   constexpr int W = (Geo<F>::BYTES + 5) / 4, NR = (64 * W + NT - 1) / NT;  // words of a row's block, a thread's share
   constexpr int NB = NA - 1;                    // chunks of payload in LDS
-  static_assert(NP % NW == 0 || NP < NW, "waves wait for the same number of loads, or have none");
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ u32x4 s_a[NA][NP * 64];            // [stage % NA][tile][part][lane]
   __shared__ u32x4 s_b[2][2][H * 8 * P * 64];   // [chunk % 2][step][half][column j][part][lane]
@@ -298,12 +297,14 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
         }
     }
     // What the stage after the next needs has to be there.  Four buffers: the gradients requested a stage ago, so that
-    // those of this stage and a payload requested since may be on their way (of a wave without gradients to request only
-    // a payload: with more allowed, the end of the one before it could be among them); three: the gradients of this
-    // stage, but not a payload requested after them.
-    if (NA == 4 && (NP % NW == 0 || wave < NP))
+    // those of this stage and a payload requested since may be on their way (as many as the wave has: with more allowed,
+    // the end of an earlier payload could be among them); three: the gradients of this stage, but not a payload requested
+    // after them.
+    if (NA == 4 && (NP % NW == 0 || wave < NP % NW))
       wait_loads<NPW + NR>();
-    else if (NA == 4 || U == 1)
+    else if (NA == 4)
+      wait_loads<NPW - 1 + NR>();
+    else if (U == 1)
       wait_loads<NR>();
     else
       wait_loads<0>();
@@ -411,26 +412,30 @@ template <int F, bool LORA> void launch_fmt(int dtype, const RowsArgs &A, hipStr
   if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, (Geo<F>::N > 1024 ? 1 : 2), 1, LORA>(A, stream);
   if (A.plan.tiles == 4) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
   if (A.plan.tiles == 8) return launch_tile<F, 1, 2, 2, LORA>(A, stream);
+  if (A.plan.tiles == 12) return launch_tile<F, 1, 3, 2, LORA>(A, stream);
   launch_tile<F, 1, 4, 2, LORA>(A, stream);
 }
 
 }  // namespace
 
-// The tiles of 16 c tokens that cost least: whole rounds of them over 256 CUs, and the rest in as many splits of the
-// rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below; a split rest also
-// costs the joining launch's 3 us and the way of its sums there and back (4 TB/s).
+// The tiles of 64 to 256 tokens that cost least: whole rounds of them over 256 CUs, and the rest in as many splits of
+// the rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below, from 256 tiles of
+// 88 and of 176 chunks (IQ2_XS; IQ1 within 15%): 155 and 294 us with 64 tokens, 153 and 292 with 128, 194 and 363 with
+// 192, 208 and 413 with 256 (f32: 458 for 176 chunks of 128 tokens by 128 columns, 383 of 64 beside a codebook of
+// 2,048 entries).  A split rest also costs the joining launch's 3 us and the way of its sums there and back (4 TB/s).
+// With 192 tokens as well 5,632 x 5,120 (IQ2_XS) by 1,500 tokens took 128 us, without 150.
 RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) {
   struct Tile {
     int tiles;
     double chunk;
   };
   const bool f32 = dtype == IQ_DTYPE_F32;
-  constexpr Tile bf16s[3] = {{4, 1.55}, {8, 1.6}, {16, 2.3}};
+  constexpr Tile bf16s[4] = {{4, 1.55}, {8, 1.6}, {12, 1.95}, {16, 2.3}};
   const Tile single = {kCodebook[fmt] > 1024 ? 4 : 8, kCodebook[fmt] > 1024 ? 2.0 : 2.7};
   const int64_t ntile = (T + 15) / 16;
   RowsPlan best{};
   double least = 0.0;
-  for (int k = 0; k < (f32 ? 1 : 3); ++k) {
+  for (int k = 0; k < (f32 ? 1 : 4); ++k) {
     const Tile &tile = f32 ? single : bf16s[k];
     const int64_t across = cols / (f32 ? 128 : 256), all = across * ((ntile + tile.tiles - 1) / tile.tiles);
     const int64_t full = all / 256 * 256, rest = all - full, size = static_cast<int64_t>(tile.tiles) * 16 * (f32 ? 128 : 256) * 4;
