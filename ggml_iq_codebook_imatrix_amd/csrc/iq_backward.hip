@@ -171,28 +171,10 @@ __device__ __forceinline__ bf16x8 source8_bf16(const Source &s, int64_t cols, in
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// Sixteen values as they are loaded, and in bf16.
-struct Sixteen {
-  u32x4 w[2];
-  int e;
-};
-__device__ __forceinline__ Sixteen load_sixteen(const Source &s, int64_t cols, int64_t t, int64_t k) {
-  Sixteen x;
-  x.e = 0;
-  if (s.ex) {
-    x.w[0] = ldu<u32x4>(static_cast<const int8_t *>(s.x) + t * cols + k);
-    x.w[1] = x.w[0];
-    x.e = s.ex[t * (cols >> 5) + (k >> 5)];
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) x.w[h] = __builtin_bit_cast(u32x4, source8_bf16(s, cols, t, k + 8 * h));
-  }
-  return x;
-}
-__device__ __forceinline__ bf16x8 eight_of(const Source &s, const Sixteen &x, int h) {
-  if (!s.ex) return __builtin_bit_cast(bf16x8, x.w[h]);
+// Eight values of a checkpoint in bf16 (exact).
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi, int e) {
   float v[8];
-  decode_codes(make_uint2(x.w[0][2 * h], x.w[0][2 * h + 1]), x.e - 133, v);
+  decode_codes(make_uint2(lo, hi), e - 133, v);
   u32x4 o;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -200,11 +182,13 @@ __device__ __forceinline__ bf16x8 eight_of(const Source &s, const Sixteen &x, in
   return __builtin_bit_cast(bf16x8, o);
 }
 
+enum SourceKind { FROM_F32, FROM_BF16, FROM_CHECKPOINT };
 // 32 tokens (A, two tiles) by 32 ranks (B) of the adapter of token `slot`, K split
 // over the eight waves, each lane 16 columns at a time (64 bytes of a row a load);
-// results of tokens with other adapters are dropped.
+// results of tokens with other adapters are dropped.  Nothing in the loop depends on the kind of tokens or on a row's
+// end: a value that one of two branches loads is waited for where they meet.
 // (Each product is a call of its own: of a chosen one the compiler would not see that its pointers are to global memory.)
-template <bool BF16>
+template <int KIND, bool BF16>
 __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, bool of_x, int first, int64_t w, f32x4 *s_red) {
   const int64_t tt = w / A.rgroups;
   const int rg = static_cast<int>(w % A.rgroups), r0 = rg * 32;
@@ -264,39 +248,63 @@ __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, boo
     }
     f32x4 acc[4] = {};  // [token tile][rank tile]
     if constexpr (BF16) {
-      // a round of the waves is 512 columns; two rounds are on their way while one multiplies (past the end the last
-      // columns again)
-      Sixteen x[3][2];
-      u32x4 b[3][2][2];
+      // A round of the waves is 512 columns; two rounds are on their way while one multiplies (past the end the last
+      // columns again).
+      constexpr int H = KIND == FROM_CHECKPOINT ? 1 : 2;  // loads of a lane's 16 columns
+      const int64_t whole = S.k & ~int64_t(63);
+      const uint8_t *row[2], *ex[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        row[r] = static_cast<const uint8_t *>(S.s.x) + t[r] * S.k * H;
+        ex[r] = S.s.ex + t[r] * (S.k >> 5);
+      }
+      u32x4 x[3][2][H], b[3][2][2];
+      int e[3][2];
       const auto load = [&](int u, int64_t k0) __attribute__((always_inline)) {
-        const int64_t block = min(k0, S.kpad - 64), k = block + q * 16;
+        const int64_t block = min(k0, whole - 64), k = block + q * 16;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          if (tile[r]) x[u][r] = load_sixteen(S.s, S.k, t[r], k);
+#pragma unroll
+          for (int h = 0; h < H; ++h) x[u][r][h] = ldu<u32x4>(row[r] + k * H + 16 * h);
+          if (KIND == FROM_CHECKPOINT) e[u][r] = ex[r][k >> 5];
 #pragma unroll
           for (int h = 0; h < 2; ++h) b[u][r][h] = ldu<u32x4>(static_cast<const uint16_t *>(S.w) + wr[r] + block * 16 + 512 * h);
         }
       };
-      load(0, wave * 64);
-      load(1, wave * 64 + 512);
-      for (int64_t k0 = wave * 64; k0 < S.kpad; k0 += 3 * 512)
+      const auto multiply = [&](int i, bf16x8 v, const u32x4 &w) __attribute__((always_inline)) {
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, w), acc[i], 0, 0, 0);
+      };
+      if (wave * 64 < whole) {
+        load(0, wave * 64);
+        load(1, wave * 64 + 512);
+      }
+      for (int64_t k0 = wave * 64; k0 < whole; k0 += 3 * 512)
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
-          if (k0 + u * 512 >= S.kpad) break;
+          if (k0 + u * 512 >= whole) break;
           load((u + 2) % 3, k0 + (u + 2) * 512);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (tile[r])
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const bf16x8 v = eight_of(S.s, x[u][r], h);
+            for (int h = 0; h < 2; ++h) {
+              const u32x4 &w = x[u][r][h % H];
+              const bf16x8 v = H == 1 ? codes_bf16(w[2 * h], w[2 * h + 1], e[u][r]) : __builtin_bit_cast(bf16x8, w);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  acc[2 * r + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, b[u][i][h]),
-                                                                          acc[2 * r + i], 0, 0, 0);
-              }
+              for (int i = 0; i < 2; ++i) multiply(2 * r + i, v, b[u][i][h]);
+            }
         }
+      if ((S.k & 63) && (whole >> 6) % 8 == wave) {  // the last columns (of dy: a checkpoint has whole blocks of 256)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bf16x8 v = source8_bf16(S.s, S.k, t[r], whole + q * 16 + 8 * h);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              multiply(2 * r + i, v, ldu<u32x4>(static_cast<const uint16_t *>(S.w) + wr[i] + whole * 16 + 512 * h));
+          }
+      }
     } else {
       for (int64_t k0 = wave * 64; k0 < S.kpad; k0 += 512)
 #pragma unroll
@@ -330,14 +338,15 @@ __device__ __forceinline__ void shrink(const ShrinkArgs &A, const Shrink &S, boo
   }
 }
 
-template <bool BF16> __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
+// KIND of x; dy is of its tensors' type (BF16).
+template <int KIND, bool BF16> __global__ void __launch_bounds__(512) back_shrink_kernel(ShrinkArgs A) {
   __shared__ f32x4 s_red[8 * 4 * 64];
   const int64_t steps = (A.tpad >> 5) * A.rgroups, w = blockIdx.x % (2 * steps);
   const int first = static_cast<int>(blockIdx.x / (2 * steps));
   if (w < steps)
-    shrink<BF16>(A, A.of[0], false, first, w, s_red);
+    shrink<BF16 ? FROM_BF16 : FROM_F32, BF16>(A, A.of[0], false, first, w, s_red);
   else
-    shrink<BF16>(A, A.of[1], true, first, w - steps, s_red);
+    shrink<KIND, BF16>(A, A.of[1], true, first, w - steps, s_red);
 }
 
 // ---------------------------------------------------------------------------
@@ -372,7 +381,6 @@ __device__ __forceinline__ int64_t outer_col(const Outer &O, int64_t blk, int m)
 // ranks (B; three bf16 values each).  The tokens in steps of 32 are dealt to the splits and their eight
 // waves; a step whose tokens' adapters cannot be a is passed over, and where all
 // are a none is masked out.  f32 tokens go through the fp32 cores.
-enum SourceKind { FROM_F32, FROM_BF16, FROM_CHECKPOINT };
 struct OuterMemory {
   f32x4 red[8 * 4 * 64];
   float out[16][132];
@@ -693,10 +701,12 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     S.parts = reinterpret_cast<uint16_t *>(base + P.pao);
     S.status = status;
     const dim3 shrinks(static_cast<unsigned>((P.tpad >> 5) * 2 * S.rgroups * S.slots));
-    if (dtype == IQ_DTYPE_F32)
-      hipLaunchKernelGGL(back_shrink_kernel<false>, shrinks, dim3(512), 0, stream, S);
+    if (dtype == IQ_DTYPE_F32)  // of either kind
+      hipLaunchKernelGGL((back_shrink_kernel<FROM_F32, false>), shrinks, dim3(512), 0, stream, S);
+    else if (exponents)
+      hipLaunchKernelGGL((back_shrink_kernel<FROM_CHECKPOINT, true>), shrinks, dim3(512), 0, stream, S);
     else
-      hipLaunchKernelGGL(back_shrink_kernel<true>, shrinks, dim3(512), 0, stream, S);
+      hipLaunchKernelGGL((back_shrink_kernel<FROM_BF16, true>), shrinks, dim3(512), 0, stream, S);
     if (!run_launched()) return IQ_ERR_HIP;
   }
   if (dx) {
