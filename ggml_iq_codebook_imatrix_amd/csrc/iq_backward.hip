@@ -537,12 +537,16 @@ template <int KIND, bool BF16> void launch_outer(const OuterArgs &O, dim3 wgs, h
     hipLaunchKernelGGL((back_outer_kernel<2, KIND, BF16>), wgs, dim3(512), 0, stream, O);
 }
 
-// The splits' sums, in their order.
+// The splits' sums (16 at most), in their order.
 __global__ void __launch_bounds__(256) back_join_kernel(OuterArgs A) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= A.all) return;
-  float s = A.partial[i];
-  for (int k = 1; k < A.splits; ++k) s += A.partial[k * A.all + i];
+  float w[16], s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = A.partial[min(k, A.splits - 1) * A.all + i];
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (k < A.splits) s += w[k];
   const int which = i >= A.before[1] ? 1 : 0;
   store1(A.of[which].out, A.dtype, i - A.before[which], s);
 }

@@ -386,13 +386,17 @@ template <int P> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArg
   const int64_t place = A.plan.full + rest, t = place / A.plan.across * A.plan.tiles * 16 + i / width;
   if (t >= A.T) return;
   const float *from = A.partial + rest * A.plan.splits * size + i;
-  float v[8];
-  load8u(from, 0, 0, v);
-  for (int s = 1; s < A.plan.splits; ++s) {
-    float w[8];
-    load8u(from, 0, s * size, w);
+  float v[8] = {};
+  for (int s0 = 0; s0 < A.plan.splits; s0 += 8) {
+    float w[8][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += w[j];
+    for (int s = 0; s < 8; ++s) load8u(from, 0, min(s0 + s, A.plan.splits - 1) * size, w[s]);
+    __builtin_amdgcn_sched_barrier(0);  // all of them on their way together
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (s0 + s < A.plan.splits) v[j] += w[s][j];
   }
   store8u(A.out, P == 1, t * A.nb * 256 + place % A.plan.across * width + i % width, v);
 }
