@@ -565,7 +565,8 @@ def linear(fmt, packed: torch.Tensor, grid: torch.Tensor, x: torch.Tensor, lora_
            status: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Tokens x [T, cols] through the encoded weight packed [rows, cols/256, block_bytes] -> [T, rows], of x's dtype.
     With lora_a [N, r, cols], lora_b [N, rows, r] (x's dtype) and lora_ids [T] int32 (-1: none), token t also gets
-    lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones).  No backward pass."""
+    lora_scale[a] * (x[t] A_a^T) B_a^T, a = lora_ids[t] (lora_scale [N] f32; None: ones).  linear_backward() is the
+    backward pass."""
     f = _fmt(fmt)
     entries, nbytes = _geometry(f)
     rows, nb, _ = _ends(packed, "packed", (None, None, nbytes), torch.uint8)
