@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = quad * 4 + j0 + j, half = ((min(r, most) << 1) & step) ^ odd;  // the block's address modulo four
-      f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + half, group);
+      f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + half, group, half);
     }
   };
   const auto look_up = [&]() __attribute__((always_inline)) {

@@ -245,21 +245,23 @@ __device__ __forceinline__ int weight_exponent(const Bound &B) {
   return w > 0.0f ? static_cast<int>(__float_as_uint(w * 1.0001f) >> 23) - 126 : 0;
 }
 
-// The fields of group g, from a block in LDS (at an even address).
+// The fields of group g, from a block in LDS, `half` bytes (0 or 2) behind an address that is a multiple of four.
 struct Fields {
   uint32_t k, ls, mask, h, d16;
 };
-template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *blk, int g) {
+template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *blk, int g, uint32_t half) {
   const auto u16 = [&](int at) -> uint32_t { return *reinterpret_cast<const uint16_t *>(blk + at); };
   Fields f;
   f.mask = f.h = 0;
   if (F == IQ1_M) {
-    const uint32_t w0 = u16(48), w1 = u16(50), w2 = u16(52), w3 = u16(54);
-    f.d16 = (w0 >> 12) | ((w1 >> 12) << 4) | ((w2 >> 12) << 8) | ((w3 >> 12) << 12);
+    // the scale and the shifts as words
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(blk - half + 48);
+    const uint32_t w0 = __builtin_amdgcn_alignbyte(w[1], w[0], half), w1 = __builtin_amdgcn_alignbyte(w[2], w[1], half);
+    f.d16 = ((w0 >> 12) & 15u) | ((w0 >> 28) << 4) | (((w1 >> 12) & 15u) << 8) | ((w1 >> 28) << 12);
     const uint32_t nib = (blk[32 + (g >> 1)] >> (4 * (g & 1))) & 15u;
     f.k = blk[g] | ((nib & 7u) << 8);
     f.h = nib >> 3;
-    f.ls = (u16(48 + 2 * (g >> 3)) >> (3 * ((g >> 1) & 3))) & 7u;
+    f.ls = ((g & 16 ? w1 : w0) >> (16 * ((g >> 3) & 1) + 3 * ((g >> 1) & 3))) & 7u;
     return f;
   }
   f.d16 = u16(0);
