@@ -1,8 +1,9 @@
 // iq_backward.hip -- iq_linear_backward: the gradients by an encoded projection's
 // tokens and by its low-rank adapters (include/iq_train.h).
 //
-// Launches: dy and the adapters into operand order, with the bound on the weights; the rank-wide products p = s dy B and v = s x A^T; dx (iq_rows.hip, with
-// p A added to its sums); and dA, dB as sums over the tokens.
+// Launches: dy and the adapters into operand order, with the bound on the weights;
+// the rank-wide products p = s dy B and v = s x A^T; dx (iq_rows.hip, with p A added
+// to its sums); and dA, dB as sums over the tokens.
 
 #include "iq_train.hpp"
 

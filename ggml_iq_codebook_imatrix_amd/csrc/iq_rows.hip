@@ -106,12 +106,14 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
 //
 // A stage is a step of 32 rows, a chunk two.  Chunk c + 1 is decoded in the odd stage of chunk c - 1 (a thread's first
 // two rows) and the even stage of chunk c (the others, and both pairs to LDS).  Its payload is requested in an odd
-// stage NA chunks before chunk c + 1's, and the gradients NA - 1 stages ahead.  As in iq_glu's tiles the work stands between the matrix instructions, and
-// operands are read a group of four ahead, a stage's first before the barrier that opens it.
+// stage NA chunks before chunk c + 1's, and the gradients NA - 1 stages ahead.  As in iq_glu's tiles the work stands
+// between the matrix instructions, and operands are read a group of four ahead, a stage's first before the barrier that
+// opens it.
 //
 // Two weights of 17,408 x 5,120 (IQ1_M), 4,096 tokens: 1,379 us, 1.06 PFLOP/s (a library's large product of fp16: 1.20),
 // matrix cores busy 0.46 of the time, LDS 0.45, waves waiting 0.28; 5,120 x 17,408 (IQ1_S) with four adapters 715, 1.02.
-// Without the decode a chunk of IQ1_S takes 1.65 us of its 2.3, with a quarter of the products 1.85: neither bounds it alone.
+// Without the decode a chunk of IQ1_S takes 1.65 us of its 2.3, with a quarter of the products 1.85: neither bounds it
+// alone.
 // Larger tiles would decode less for each product, but 512 tokens' gradients do not fit LDS beside a codebook.
 template <int F, int P, int C, int H, bool LORA>
 __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
