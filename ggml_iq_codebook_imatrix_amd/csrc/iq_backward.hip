@@ -437,6 +437,12 @@ __device__ __forceinline__ void outer_sums(const OuterArgs &A, const Outer &O, i
 #pragma unroll
       for (int i = 0; i < 8; ++i) mine |= static_cast<uint32_t>(A.ids[t0 + 8 * q + i] == a) << i;
     }
+    u32x4 w[RT][3];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        w[r][k] = ldu<u32x4>(O.parts + ((t0 >> 5) * 2 * A.rgroups + rt0 + r) * 1536 + k * 512 + lane * 8);
     u32x4 x[8];
     if constexpr (KIND == FROM_CHECKPOINT) {
       uint2 codes[8];
@@ -455,17 +461,15 @@ __device__ __forceinline__ void outer_sums(const OuterArgs &A, const Outer &O, i
         for (int j = 0; j < 4; ++j)
           x[i][j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
       }
+    } else if (O.k >= 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = ldu<u32x4>(static_cast<const uint16_t *>(O.s.x) + ((mine >> i) & 1u ? t0 + 8 * q + i : 0) * O.k + c0);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, (mine >> i) & 1u ? t0 + 8 * q + i : 0, O.k >= 8 ? c0 : 0));
+        x[i] = __builtin_bit_cast(u32x4, source8_bf16(O.s, O.k, (mine >> i) & 1u ? t0 + 8 * q + i : 0, 0));
     }
-    u32x4 w[RT][3];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        w[r][k] = ldu<u32x4>(O.parts + ((t0 >> 5) * 2 * A.rgroups + rt0 + r) * 1536 + k * 512 + lane * 8);
     if (!all) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
