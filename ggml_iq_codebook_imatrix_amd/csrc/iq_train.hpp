@@ -173,13 +173,21 @@ __device__ __forceinline__ uint32_t row_exponent(const void *x, int dtype, int64
 // 64 lanes' 16 bytes each, from base + off on, to 1 KiB of LDS at `to` (base and `to` the same in all lanes).  The
 // compiler takes every later read of LDS for one of these bytes and waits for them, which is a memory's latency lost in
 // each round of a buffer; written out, they are waited for where the buffers change (wait_loads), and by nothing before.
+// m0 leaves as an output, so that the compiler takes none it has set for one that is still there.
 __device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               : "={m0}"(m0)
+               : "v"(off), "s"(base), "s"(to)
                : "memory");
 }
 // The same of 4 bytes each, to 256 bytes of LDS.
 __device__ __forceinline__ void load_words_to_lds(const char *base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               : "={m0}"(m0)
+               : "v"(off), "s"(base), "s"(to)
+               : "memory");
 }
 // All loads but the wave's last N (in the order of their issue).
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
