@@ -38,31 +38,40 @@ struct BackPrepArgs {
 // One wave brings one token's gradient into the order of Grads.
 template <int P>
 __device__ __forceinline__ void convert_grad(const BackPrepArgs &A, int64_t t, int lane) {
-  const int n = 141 - static_cast<int>(row_exponent(A.dy, A.dtype, A.rows, t, lane));
   const int64_t all = row_chunks(A.rows) * 64;
-  for (int64_t r = lane * 8; r < all; r += 512) {
-    float v[8];
+  const auto load = [&](int64_t r, float (&v)[8]) __attribute__((always_inline)) {
     if (r + 8 <= A.rows) {
       load8u(A.dy, A.dtype, t * A.rows + r, v);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = r + j < A.rows ? load1(A.dy, A.dtype, t * A.rows + r + j) : 0.0f;
     }
-    half8v hi, lo;
+  };
+  uint32_t most = 0;
+  if (P == 1) {
+    most = row_exponent(A.dy, A.dtype, A.rows, t, lane) << 23;
+    const int n = grad_power(most, false);
+    for (int64_t r = lane * 8; r < all; r += 512) {
+      float v[8];
+      load(r, v);
+      half8v o;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      _Float16 x, y;
-      to_parts(v[j], n, x, y);
-      hi[j] = x;
-      lo[j] = y;
+      for (int j = 0; j < 8; ++j) o[j] = static_cast<_Float16>(ldexpf(v[j], n));
+      const int in = static_cast<int>(r & 63);
+      *reinterpret_cast<half8v *>(static_cast<_Float16 *>(A.G.g) + ((r >> 6) * A.G.ntile + (t >> 4)) * 1024 +
+                                  ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8) = o;
     }
-    const int in = static_cast<int>(r & 63);
-    _Float16 *to = A.G.g16 + ((r >> 6) * A.G.ntile + (t >> 4)) * P * 1024 +
-                   ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8;
-    *reinterpret_cast<half8v *>(to) = hi;
-    if (P == 2) *reinterpret_cast<half8v *>(to + 1024) = lo;
+  } else {
+    for (int64_t r = lane * 8; r < all; r += 512) {
+      float v[8];
+      load(r, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = max_bits(most, v[j]);
+      put_grads(A.G, 0, t, r, v);
+    }
+    most = wave_max_u32(most);
   }
-  if (lane == 0) A.G.ex[t] = -n;
+  if (lane == 0) A.G.most[t] = most;
 }
 
 // A wave a token of dy, which it goes through twice (the largest magnitude first).  4,096 tokens of 5,120 columns, four
@@ -586,10 +595,10 @@ BackPlan plan_back(int fmt, int64_t rows, int64_t cols, int dtype, int64_t T, in
   const size_t size = dtype == IQ_DTYPE_F32 ? 4 : 2;
   p.ntile = (T + 15) / 16;
   p.chunks = row_chunks(rows);
-  p.dx = plan_rows(fmt, T, cols, p.chunks, dtype);
+  p.dx = plan_rows(T, cols / 256, p.chunks, dtype, dtype == IQ_DTYPE_F32);
   p.bo = ws_up(static_cast<size_t>(kCodebook[fmt]) * 16);
   p.go = p.bo + ws_up(kBoundBytes);
-  p.geo = p.go + ws_up(grads_bytes(p.chunks, p.ntile, dtype));
+  p.geo = p.go + ws_up(grads_bytes(p.chunks, p.ntile, dtype == IQ_DTYPE_F32));
   p.po = p.geo + ws_up(static_cast<size_t>(p.ntile) * 64);
   p.bto = p.po + ws_up(p.dx.bytes);
   p.bytes = p.bto + kWsAlign;
@@ -685,7 +694,7 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
   A.nb = cols / 256;
   A.nconv = (T + 7) / 8;
   A.packed = packed;
-  A.G = Grads{reinterpret_cast<_Float16 *>(base + P.go), reinterpret_cast<int32_t *>(base + P.geo), P.ntile};
+  A.G = Grads{base + P.go, reinterpret_cast<uint32_t *>(base + P.geo), P.ntile};
   A.books = one_codebook(fmt, grid, tab, status);
   A.B = Bound{reinterpret_cast<uint32_t *>(base + P.bo), reinterpret_cast<uint32_t *>(base + P.bo) + kScaleSlots,
               A.books.wg[0], fmt >= IQ1_S};

@@ -23,11 +23,7 @@ struct GluArgs {
   void *h;
   // backward (dh not null)
   const void *dh;
-  const int32_t *dhe;  // exponent field of each token's dh
   Grads G;
-  int parts;  // of the gradients
-  Bound B;
-  int lh;  // 2^lh >= hidden
 };
 
 struct GluPrepArgs {
@@ -35,14 +31,12 @@ struct GluPrepArgs {
   int64_t T, cols, nconv;
   Tokens X;
   Codebooks books;
-  // backward: the bound on the weights, and the exponents of dh
+  // backward: the bound on the weights; the products find the largest of their gradients from zero on
   int fmt, bytes, backward;
   const uint8_t *packed[2];
   int64_t rows;
   Bound B;
-  const void *dh;
-  int dtype;
-  int32_t *dhe;
+  uint32_t *most;
 };
 
 // Everything the products want beforehand, a wave a token: 4,096 tokens x 5,120 in bf16 20 us (63 MB, 3.1 TB/s: a token's
@@ -58,19 +52,11 @@ __global__ void __launch_bounds__(512) glu_prep_kernel(GluPrepArgs A) {
       return;
     }
     w -= kScaleSlots;
-    if (w < A.nconv) {
-      const int64_t t = w * 8 + wave;
-      if (t < A.T) {
-        const uint32_t e = row_exponent(A.dh, A.dtype, A.rows, t, lane);
-        if (lane == 0) A.dhe[t] = static_cast<int32_t>(e);
-      }
-      return;
-    }
-    w -= A.nconv;
   }
   if (w < A.nconv) {
     const int64_t t = w * 8 + wave;
     if (t >= A.T) return;
+    if (A.backward && lane == 0) A.most[t] = 0;
     if (A.S.ex)
       convert_checkpoint(static_cast<const int8_t *>(A.S.x), A.S.ex, A.cols, A.X, t, lane);
     else if (A.S.dtype == IQ_DTYPE_F32)
@@ -111,52 +97,43 @@ __device__ __forceinline__ float activation(int act, float g, bool back, float &
   return g * s;
 }
 
-// The power of two of a token's gradients by g and u: |dh| < 2^(field - 126),
-// |g| and |u| < hidden |x| |w|, slopes below 1.13, and one more for the roundings.
-__device__ __forceinline__ int grad_exponent(const GluArgs &A, int ew, int64_t t) {
-  return 15 - ((A.dhe[t] - 126) + (15 + A.X.ex[t]) + A.lh + ew + 2);
-}
-
 // ---------------------------------------------------------------------------
 // Results
 // ---------------------------------------------------------------------------
-// One value of h, or of both gradients.
-__device__ __forceinline__ void put1(const GluArgs &A, int n, int64_t t, int64_t row, float g, float u) {
-  if (t >= A.T) return;
+// One value of h, or of both gradients, whose largest magnitude's bits are the result.  (dh meets u and the slope last: a
+// dh * u that is infinite would make NaN of a slope of zero.)
+__device__ __forceinline__ uint32_t put1(const GluArgs &A, int64_t t, int64_t row, float g, float u) {
+  if (t >= A.T) return 0;
   float slope;
   const float a = activation(A.act, g, A.dh, slope);
   if (!A.dh) {
     if (row < A.rows) store1(A.h, A.dtype, t * A.rows + row, a * u);
-    return;
+    return 0;
   }
   const int64_t chunks = row_chunks(A.rows);
-  if (row >= chunks * 64) return;
+  if (row >= chunks * 64) return 0;
   float v[2] = {0.0f, 0.0f};
   if (row < A.rows) {
     const float d = load1(A.dh, A.dtype, t * A.rows + row);
-    v[0] = d * u * slope;
+    v[0] = d * (u * slope);
     v[1] = d * a;
   }
   const int in = static_cast<int>(row & 63);
-  _Float16 *to = A.G.g16 + ((row >> 6) * A.G.ntile + (t >> 4)) * A.parts * 1024 +
-                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8 + (in & 7);
+  float *to = static_cast<float *>(A.G.g) + ((row >> 6) * A.G.ntile + (t >> 4)) * 1024 + (in >> 5) * 512 +
+              ((in & 7) >> 2) * 256 + (((in & 31) >> 3) * 16 + (t & 15)) * 4 + (in & 3);
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    _Float16 hi, lo;
-    to_parts(v[m], n, hi, lo);
-    to[m * chunks * A.G.ntile * A.parts * 1024] = hi;
-    if (A.parts == 2) to[m * chunks * A.G.ntile * A.parts * 1024 + 1024] = lo;
-  }
+  for (int m = 0; m < 2; ++m) to[m * chunks * A.G.ntile * 1024] = v[m];
+  return max_bits(max_bits(0, v[0]), v[1]);
 }
 
 // Eight rows of one token from row on (row a multiple of eight).
-__device__ __forceinline__ void put8(const GluArgs &A, int n, int64_t t, int64_t row, const float (&g)[8],
-                                     const float (&u)[8]) {
+__device__ __forceinline__ uint32_t put8(const GluArgs &A, int64_t t, int64_t row, const float (&g)[8],
+                                         const float (&u)[8]) {
   const int64_t chunks = row_chunks(A.rows), at = t * A.rows + row;
   const bool whole = row + 8 <= A.rows;
   float a[8], slope[8], d[8];
   if (A.dh) {
-    if (row >= chunks * 64) return;
+    if (row >= chunks * 64) return 0;
     if (whole) {
       load8u(A.dh, A.dtype, at, d);
     } else {
@@ -176,24 +153,27 @@ __device__ __forceinline__ void put8(const GluArgs &A, int n, int64_t t, int64_t
       for (int k = 0; k < 8; ++k)
         if (row + k < A.rows) store1(A.h, A.dtype, at + k, a[k]);
     }
-    return;
+    return 0;
   }
-  const int in = static_cast<int>(row & 63);
-  _Float16 *to = A.G.g16 + ((row >> 6) * A.G.ntile + (t >> 4)) * A.parts * 1024 +
-                 ((in >> 5) * 64 + ((in & 31) >> 3) * 16 + (t & 15)) * 8;
+  uint32_t most = 0;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    half8v hi, lo;
+    float v[8];  // rows past the last: zeros, whatever was summed there
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      _Float16 x, y;  // rows past the last: zeros, whatever was summed there
-      to_parts(row + k < A.rows ? (m ? d[k] * a[k] : d[k] * u[k] * slope[k]) : 0.0f, n, x, y);
-      hi[k] = x;
-      lo[k] = y;
+      v[k] = row + k < A.rows ? (m ? d[k] * a[k] : d[k] * (u[k] * slope[k])) : 0.0f;
+      most = max_bits(most, v[k]);
     }
-    *reinterpret_cast<half8v *>(to + m * chunks * A.G.ntile * A.parts * 1024) = hi;
-    if (A.parts == 2) *reinterpret_cast<half8v *>(to + m * chunks * A.G.ntile * A.parts * 1024 + 1024) = lo;
+    put_grads(A.G, m * chunks, t, row, v);
   }
+  return most;
+}
+
+// The largest magnitude of each of a workgroup's N tokens, collected in LDS, into A.G.most (maxima, in any order alike).
+template <int N> __device__ __forceinline__ void put_most(const GluArgs &A, int64_t t0, const uint32_t *s_most) {
+  __syncthreads();
+  const int64_t t = t0 + threadIdx.x;
+  if (A.dh && threadIdx.x < N && t < A.T && s_most[threadIdx.x]) atomicMax(A.G.most + t, s_most[threadIdx.x]);
 }
 
 // ---------------------------------------------------------------------------
@@ -206,7 +186,9 @@ template <int F, int P, int C>
 __global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
   constexpr int kTab = Geo<F>::N, kRed = 8 * 2 * 64;
   __shared__ uint4 s_mem[kTab > kRed ? kTab : kRed];
+  __shared__ uint32_t s_most[16 * C];
   load_table<F>(s_mem, A.tab);
+  if (threadIdx.x < 16 * C) s_most[threadIdx.x] = 0;
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const Split S = split_of(A.nb);
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * S.rw + S.rg) * 16;
@@ -230,7 +212,6 @@ __global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
         load_operand<P, C>(x, xp);
       },
       acc);
-  const int ew = A.dh ? weight_exponent(A.B) : 0;
   f32x4 *red = reinterpret_cast<f32x4 *>(s_mem);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -252,12 +233,13 @@ __global__ void __launch_bounds__(512) glu_split_kernel(GluArgs A) {
       for (int k = 0; k < 4; ++k) {
         const int64_t t = (tt0 + c) * 16 + (l >> 4) * 4 + k;
         if (t >= A.T) continue;
-        const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
-        put1(A, ng, t, row, ldexpf(s[0][k], e), ldexpf(s[1][k], e));
-        if (A.dh && row == 0) A.G.ex[t] = -ng;
+        const int e = A.X.ex[t];
+        const uint32_t most = put1(A, t, row, ldexpf(s[0][k], e), ldexpf(s[1][k], e));
+        if (most) atomicMax(s_most + c * 16 + (l >> 4) * 4 + k, most);
       }
     }
   }
+  put_most<16 * C>(A, tt0 * 16, s_most);
 }
 
 // load_words loads at least so many times.
@@ -278,6 +260,7 @@ __global__ void __launch_bounds__(128 * RT, RT < 4 ? 2 : RT / 2) glu_batch_kerne
   constexpr int kX = 2 * NP * 64, kRed = NW * C * 64;
   __shared__ uint4 s_tab[Geo<F>::N];
   __shared__ u32x4 s_x[kX > kRed ? kX : kRed];  // [half % 2][tile][part][step][lane]
+  static_assert(16 * C <= 64 * NW, "a thread a token");
   const uint32_t x_at = IQ_LDS_ADDRESS(s_x);
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
@@ -353,15 +336,15 @@ __global__ void __launch_bounds__(128 * RT, RT < 4 ? 2 : RT / 2) glu_batch_kerne
   const float *all = reinterpret_cast<const float *>(s_x);
 #pragma unroll
   for (int c = 0; c < C; ++c) s_x[((rt * 2 + m) * C + c) * 64 + lane] = __builtin_bit_cast(u32x4, acc[c]);
+  uint32_t *s_most = reinterpret_cast<uint32_t *>(s_tab);  // the codebook has done its work
+  if (threadIdx.x < 16 * C) s_most[threadIdx.x] = 0;
   __syncthreads();
-  const int ew = A.dh ? weight_exponent(A.B) : 0;
 #pragma unroll 1
   for (int i = threadIdx.x; i < 32 * RT * C; i += 64 * NW) {
     const int o = i % (2 * RT), tok = i / (2 * RT) & 15, c = i / (32 * RT);  // eight rows, token, token tile
     const int64_t t = (tt0 + c) * 16 + tok, row = rblk + o * 8;
     if (t >= A.T || row >= (A.dh ? row_chunks(A.rows) * 64 : A.rows)) continue;
-    const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
-    if (A.dh && row == 0) A.G.ex[t] = -ng;
+    const int e = A.X.ex[t];
     const float *at = all + (((o >> 1) * 2 * C + c) * 64 + (tok >> 2) * 16 + (o & 1) * 8) * 4 + (tok & 3);
     float g[8], u[8];
 #pragma unroll
@@ -369,8 +352,10 @@ __global__ void __launch_bounds__(128 * RT, RT < 4 ? 2 : RT / 2) glu_batch_kerne
       g[k] = ldexpf(at[k * 4], e);
       u[k] = ldexpf(at[C * 256 + k * 4], e);
     }
-    put8(A, ng, t, row, g, u);
+    const uint32_t most = put8(A, t, row, g, u);
+    if (most) atomicMax(s_most + c * 16 + tok, most);
   }
+  put_most<16 * C>(A, tt0 * 16, s_most);
 }
 
 // weights_half8 begun: the fields of group i, which is the same in all lanes but not known to the compiler, and its
@@ -446,6 +431,7 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
   __shared__ u32x4 s_a[4][NP * 64];  // tokens [stage % 4][tile][part][lane]
   __shared__ u32x4 s_b[3][TB * 64];  // weights [stage % 3][tile][lane]
   __shared__ f32x4 s_ratio[2][TB * 4], s_unit[TB * 4];
+  static_assert(16 * TA <= 64 * NW, "a thread a token");
   const uint32_t x_at = IQ_LDS_ADDRESS(s_a);
   load_table<F>(s_tab, A.tab);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
@@ -624,11 +610,12 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
 #pragma unroll
   for (int i = 0; i < DR; ++i)
     if (q == 0) reinterpret_cast<float *>(s_unit)[(wave * DR + i) * 16 + n] = unit[i];
+  uint32_t *s_most = reinterpret_cast<uint32_t *>(s_tab);  // the codebook has done its work
+  if (threadIdx.x < 16 * TA) s_most[threadIdx.x] = 0;
   __syncthreads();
   // A token tile's sums at a time through LDS, in which a lane finds eight rows of one token; one copy of the code
   // for all of them (16 in a row were 160 KB of instructions, and took as long as twelve stages).
   static_assert(4 * NP >= NW * R, "a wave's sums of a token tile fit");
-  const int ew = A.dh ? weight_exponent(A.B) : 0;
   f32x4 *own = reinterpret_cast<f32x4 *>(s_a) + wave * R * 64;
 #pragma unroll 1
   for (int c = 0; c < C; ++c) {
@@ -643,8 +630,7 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
       const int m = i & 15, o = i >> 4;  // token, and its eight rows
       const int64_t t = (tt0 + wt * C + c) * 16 + m, row = tile_row(wr * R) + o * 8;
       if (t >= A.T || row >= (A.dh ? row_chunks(A.rows) * 64 : A.rows)) continue;
-      const int e = A.X.ex[t], ng = A.dh ? grad_exponent(A, ew, t) : 0;
-      if (A.dh && row == 0) A.G.ex[t] = -ng;
+      const int e = A.X.ex[t];
       float g[8], u[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // row tile o / 2, quarters 2 (o % 2) + h
@@ -655,9 +641,11 @@ __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(Glu
           u[h * 4 + k] = ldexpf(at[R / 2 * 64][k], e);
         }
       }
-      put8(A, ng, t, row, g, u);
+      const uint32_t most = put8(A, t, row, g, u);
+      if (most) atomicMax(s_most + (wt * C + c) * 16 + m, most);
     }
   }
+  put_most<16 * TA>(A, tt0 * 16, s_most);
 }
 
 template <int F, int P, int C> void launch_split(const GluArgs &A, hipStream_t stream) {
@@ -724,7 +712,7 @@ template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
 struct GluPlan {
   TokensPlan x;
   RowsPlan rows;
-  size_t xo, eo, bo, do_, go, geo, po, bytes;
+  size_t xo, eo, bo, go, geo, po, bytes;
 };
 GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, bool backward) {
   GluPlan p{};
@@ -735,10 +723,9 @@ GluPlan plan_glu(int fmt, int64_t inter, int64_t hidden, int dtype, int64_t T, b
   p.bytes = p.bo + kWsAlign;
   if (!backward) return p;
   const int64_t chunks = 2 * row_chunks(inter);
-  p.rows = plan_rows(fmt, T, hidden, chunks, dtype);
-  p.do_ = p.bo + ws_up(kBoundBytes);
-  p.go = p.do_ + ws_up(static_cast<size_t>(T) * 4);
-  p.geo = p.go + ws_up(grads_bytes(chunks, p.x.ntile, dtype));
+  p.rows = plan_rows(T, hidden / 256, chunks, dtype, true);
+  p.go = p.bo + ws_up(kBoundBytes);
+  p.geo = p.go + ws_up(grads_bytes(chunks, p.x.ntile, true));
   p.po = p.geo + ws_up(p.x.ebytes);
   p.bytes = p.po + ws_up(p.rows.bytes) + kWsAlign;
   return p;
@@ -785,8 +772,6 @@ int run_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int6
   A.packed[0] = gate;
   A.packed[1] = up;
   A.rows = inter;
-  A.dh = dh;
-  A.dtype = dtype;
   GluArgs M{};
   M.packed[0] = gate;
   M.packed[1] = up;
@@ -801,15 +786,11 @@ int run_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int6
   if (backward) {
     A.B = Bound{reinterpret_cast<uint32_t *>(base + P.bo), reinterpret_cast<uint32_t *>(base + P.bo) + kScaleSlots,
                 A.books.wg[0], fmt >= IQ1_S};
-    A.dhe = reinterpret_cast<int32_t *>(base + P.do_);
-    M.B = A.B;
+    A.most = reinterpret_cast<uint32_t *>(base + P.geo);
     M.dh = dh;
-    M.dhe = A.dhe;
-    M.parts = dtype == IQ_DTYPE_F32 ? 2 : 1;
-    M.G = Grads{reinterpret_cast<_Float16 *>(base + P.go), reinterpret_cast<int32_t *>(base + P.geo), P.x.ntile};
-    while ((int64_t(1) << M.lh) < hidden) ++M.lh;
+    M.G = Grads{base + P.go, A.most, P.x.ntile};
   }
-  const int64_t wgs = A.nconv + A.books.wg[0] + (backward ? kScaleSlots + A.nconv : 0);
+  const int64_t wgs = A.nconv + A.books.wg[0] + (backward ? kScaleSlots : 0);
   hipLaunchKernelGGL(glu_prep_kernel, dim3(static_cast<unsigned>(wgs)), dim3(512), 0, stream, A);
   if (!run_launched()) return IQ_ERR_HIP;
 #define CALL(F) source_parts(A.S) == 2 ? launch_glu<F, 2>(M, stream) : launch_glu<F, 1>(M, stream)
@@ -826,7 +807,7 @@ int run_glu(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int6
   D.T = T;
   D.tab = tab;
   D.G = M.G;
-  D.B = M.B;
+  D.B = A.B;
   D.out = out;
   D.partial = reinterpret_cast<float *>(base + P.po);
   D.plan = P.rows;

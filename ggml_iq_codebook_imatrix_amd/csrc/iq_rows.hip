@@ -2,6 +2,14 @@
 // rows (iq_linear_backward, and iq_glu_backward for two weights one after the
 // other).
 //
+// A weight is d m v, d its block's scale.  m v is exact in fp16.  d differs from row to
+// row, so it cannot scale a sum; but a workgroup's columns are one block of each row,
+// so that d belongs to a row there, as the gradients do: G d is formed in fp32 for the
+// workgroup and enters as the sum of two fp16 values (2^-23 of the value), under
+// one power of two per token, of its largest gradient, and one for the payload's scales.  The weight as an fp16
+// operand in the place of m v would have been rounded twice; two values of it, beside
+// gradients of two values, take three products and twice the LDS.
+//
 // The matrix instruction wants eight consecutive rows of one column from a lane; a
 // payload gives eight consecutive columns of one row.  A thread therefore decodes
 // the same group of four consecutive rows, which makes two pairs of rows of each of
@@ -9,12 +17,9 @@
 // operands that a group's lane has in eight instructions: operand j of half h holds
 // columns 128 h + 8 n + j of a block, n the lane's place, so that its results are
 // eight consecutive columns of dx.  Decoded once for all tokens of a workgroup, the
-// weights reach the waves through LDS.
-//
-// d differs from row to row, so it cannot scale a sum: the operand is the whole
-// weight, d m v, in fp16 under one power of two for the payload (bf16), or the sum of
-// two fp16 values (f32, three products; the sums of four chunks are added to the whole
-// ones, so that fewer additions round at a whole sum's size).
+// weights reach the waves through LDS; a wave's gradients are its own tokens', and
+// come from memory to its registers.  For f32 the sums of four chunks are added to the
+// whole ones, so that fewer additions round at a whole sum's size.
 
 #include <type_traits>
 
@@ -27,7 +32,7 @@ namespace {
 // eight.  32 ranks at a time: a lane has eight ranks of its eight columns, which byte permutations make operands of
 // (bf16; p is the sum of three bf16 values, without a rounding), or four ranks at a time on the fp32 cores.  Rows of
 // tokens with other adapters are zeros; where A is not finite, 0 * A would reach them, and what they give is dropped.
-template <int P, int C>
+template <bool F32, int C>
 __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int64_t col, f32x4 (&acc)[8][C]) {
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int64_t cols = A.nb * 256, mytok = tt * 16 + lane, cb = col >> 8;
@@ -38,10 +43,10 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
     const uint64_t group = __ballot(mine == a);
     todo &= ~group;
-    for (int r0 = 0; r0 < A.rank; r0 += P == 1 ? 32 : 4) {
+    for (int r0 = 0; r0 < A.rank; r0 += F32 ? 4 : 32) {
       const uint32_t *wild = A.wild + (static_cast<int64_t>(a) * tiles + (r0 >> 4)) * A.nb + cb;
-      const bool drop = wild[0] | wild[P == 1 && r0 + 16 < A.rank ? A.nb : 0];
-      if constexpr (P == 1) {
+      const bool drop = wild[0] | wild[!F32 && r0 + 16 < A.rank ? A.nb : 0];
+      if constexpr (!F32) {
         const uint16_t *from = static_cast<const uint16_t *>(A.a) + static_cast<int64_t>(a) * A.rank * cols + col;
         u32x4 w[8];  // ranks r0 + 8 q + i; past the last p is zero
 #pragma unroll
@@ -102,44 +107,57 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
   }
 }
 
-// Waves: 4 token groups (of C tiles) by H halves of a block's columns.  LORA: with adapters.
+// Two gradients times their rows' scales, as the sums of two fp16 values each.  They leave 2^-23 of the product;
+// where it
+// is infinite the second part, inf - inf, becomes a number, which leaves the infinity.
+template <class V>
+__device__ __forceinline__ void scaled_parts(V g0, V g1, float d0, float d1, uint32_t &hi, uint32_t &lo) {
+  // written as fma, a product and its rounding are one instruction for each half of a register
+  const half2v h = {static_cast<_Float16>(__builtin_fmaf(static_cast<float>(g0), d0, 0.0f)),
+                    static_cast<_Float16>(__builtin_fmaf(static_cast<float>(g1), d1, 0.0f))};
+  hi = __builtin_bit_cast(uint32_t, h);
+  asm("" : "+v"(hi));  // both halves are taken from here
+  const half2v k = __builtin_bit_cast(half2v, hi);
+  const half2v l = {static_cast<_Float16>(__builtin_fmaf(static_cast<float>(g0), d0, -static_cast<float>(k[0]))),
+                    static_cast<_Float16>(__builtin_fmaf(static_cast<float>(g1), d1, -static_cast<float>(k[1])))};
+  const half2v most = {static_cast<_Float16>(65504.0f), static_cast<_Float16>(65504.0f)};
+  lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(l, most));
+}
+
+// Eight waves, each C tiles of 16 tokens and the block's 256 columns.  WIDE: the gradients are fp32, else fp16.  F32: dx
+// is.  LORA: with adapters.
 //
 // A stage is a step of 32 rows, a chunk two.  Chunk c + 1 is decoded in the odd stage of chunk c - 1 (a thread's first
-// two rows) and the even stage of chunk c (the others, and both pairs to LDS).  Its payload is requested in an odd
-// stage NA chunks before chunk c + 1's, and the gradients NA - 1 stages ahead.  As in iq_glu's tiles the work stands
-// between the matrix instructions, and operands are read a group of four ahead, a stage's first before the barrier that
-// opens it.
+// two rows) and the even stage of chunk c (the others, and both pairs to LDS); the next stage's gradients meet their
+// scales in each stage, and those of the stage after it are requested when that is done.  Payload is requested in the odd
+// stage four chunks before its own.  The work stands between the matrix instructions, and weights are read a group of G
+// columns ahead, a stage's first before the barrier that opens it.
 //
-// Two weights of 17,408 x 5,120 (IQ1_M), 4,096 tokens: 1,379 us, 1.06 PFLOP/s (a library's large product of fp16: 1.20),
-// matrix cores busy 0.46 of the time, LDS 0.45, waves waiting 0.28; 5,120 x 17,408 (IQ1_S) with four adapters 715, 1.02.
-// Without the decode a chunk of IQ1_S takes 1.65 us of its 2.3, with a quarter of the products 1.85: neither bounds it
-// alone.
-// Larger tiles would decode less for each product, but 512 tokens' gradients do not fit LDS beside a codebook.
-template <int F, int P, int C, int H, bool LORA>
-__global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
-  constexpr int NW = 4 * H, NT = 64 * NW, TA = 4 * C, NP = TA * P, NPW = (NP + NW - 1) / NW;
-  constexpr int NA = Geo<F>::N > 512 ? 3 : 4;  // stages of gradients in LDS, beside a large codebook one fewer
+// With 256 tokens bound by the matrix cores at the rate that a large product sustains here: 176 chunks by 256 tiles
+// (IQ2_XS, fp16 gradients) 638 us, 1.18 PFLOP/s of its two products (a library's product of fp16: 1.20).  With 128 tokens
+// the decode, which is the same for half the products, counts as much as they do: 455 us, 0.83.
+template <int F, bool WIDE, int C, bool F32, bool LORA>
+__global__ void __launch_bounds__(512, 2) rows_kernel(RowsArgs A) {
+  constexpr int NT = 512, TA = 8 * C;
   constexpr int W = (Geo<F>::BYTES + 5) / 4, NR = (64 * W + NT - 1) / NT;  // words of a row's block, a thread's share
-  constexpr int NB = NA - 1;                    // chunks of payload in LDS
+  constexpr int NB = 3;                                                    // chunks of payload in LDS
+  constexpr int GL = WIDE ? 2 : 1;                                         // a lane's loads of a tile's step
   __shared__ uint4 s_tab[Geo<F>::N];
-  __shared__ u32x4 s_a[NA][NP * 64];            // [stage % NA][tile][part][lane]
-  __shared__ u32x4 s_b[2][2][H * 8 * P * 64];   // [chunk % 2][step][half][column j][part][lane]
-  __shared__ uint32_t s_raw[NB][NR * NT];       // [chunk % NB][row][word]
-  const uint32_t grad_at = IQ_LDS_ADDRESS(s_a), raw_at = IQ_LDS_ADDRESS(s_raw);
-  load_table<F>(s_tab, A.tab);
+  __shared__ u32x4 s_b[2][2][16 * 64];     // m v [chunk % 2][step][column 8 half + j][lane]
+  __shared__ uint32_t s_raw[NB][NR * NT];  // [chunk % NB][row][word]
+  __shared__ f32x4 s_d[2][16];             // the rows' scales [chunk % 2][row / 4]
+  const uint32_t raw_at = IQ_LDS_ADDRESS(s_raw);
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wt = wave / H, wh = wave % H;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool whole = blockIdx.x < A.plan.full;
   const int64_t rest = blockIdx.x - A.plan.full, place = whole ? blockIdx.x : A.plan.full + rest / A.plan.splits;
   const int splits = whole ? 1 : A.plan.splits, split = whole ? 0 : static_cast<int>(rest % A.plan.splits);
-  const int64_t across = place % A.plan.across, tt0 = place / A.plan.across * TA;
-  const int64_t cb = across / (2 / H), cols = A.nb * 256, rowbytes = A.nb * Geo<F>::BYTES;
-  const int half0 = H == 2 ? 0 : static_cast<int>(across & 1);  // the first half that the workgroup takes
+  const int64_t cb = place % A.nb, tt0 = place / A.nb * TA;
+  const int64_t cols = A.nb * 256, rowbytes = A.nb * Geo<F>::BYTES;
   const int64_t per = (A.rows + 63) / 64, chunks = per * A.nmat;
   const int64_t share = (chunks + splits - 1) / splits, ch0 = split * share;
   const int count = static_cast<int>(max(min(share, chunks - ch0), static_cast<int64_t>(0)));
-  const int ew = weight_exponent(A.B);
-  const int unit = 15 - ew - (Geo<F>::IQ1 ? 0 : 3);
+  const bool more = count > NB;  // payload is requested in the loop as well
   const uint8_t *const p0 = A.packed[0] + cb * Geo<F>::BYTES, *const p1 = A.packed[A.nmat - 1] + cb * Geo<F>::BYTES;
 
   // The first row of chunk c of the workgroup's, and whether it is the second weight's; past the last chunk the last.
@@ -170,36 +188,69 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) load_words_to_lds(from, roff[i], raw_at + ((buf * NR + i) * NT + wave * 64) * 4);
   };
-  // Step `step` of the gradients of the chunk at `from` into buffer `buf`.
-  const char *gbase = reinterpret_cast<const char *>(A.G.g16) + (ch0 * A.G.ntile + tt0) * P * 2048;
-  const int64_t gchunk = A.G.ntile * P * 2048;
-  uint32_t goff[NPW];
+  // The wave's gradients of a step of the chunk at `from`, and with their scales as operands.
+  const int64_t gchunk = A.G.ntile * (GL * 2048);
+  const char *gbase = reinterpret_cast<const char *>(A.G.g) + (ch0 * A.G.ntile + tt0) * (GL * 2048);
+  uint32_t goff[C];
 #pragma unroll
-  for (int i = 0; i < NPW; ++i) {
-    const int p = i * NW + wave, most = static_cast<int>(min(A.G.ntile - tt0, static_cast<int64_t>(TA))) - 1;
-    goff[i] = static_cast<uint32_t>((min(p / P, most) * P + p % P) * 2048 + lane * 16);
+  for (int c = 0; c < C; ++c) {
+    const int most = static_cast<int>(min(A.G.ntile - tt0, static_cast<int64_t>(TA))) - 1;
+    goff[c] = static_cast<uint32_t>(min(wave * C + c, most) * (GL * 2048) + lane * 16);
   }
-  const auto fetch = [&](const char *from, int step, int buf) __attribute__((always_inline)) {
+  u32x4 grad[C][GL];
+  const auto load_grads = [&](const char *from, int step) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NPW; ++i)
-      if (NP % NW == 0 || i * NW + wave < NP)
-        load_to_lds(from + step * 1024, goff[i], grad_at + (buf * NP + i * NW + wave) * 1024);
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < GL; ++i)
+        grad[c][i] = ld_global<u32x4, 16>(reinterpret_cast<uintptr_t>(from) + (step * GL + i) * 1024 + goff[c]);
+  };
+  // of the lane's tokens, and of the payload
+  float power[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    power[c] = ldexpf(1.0f, grad_power(A.G.most[min(tt0 + wave * C + c, A.G.ntile - 1) * 16 + n], true));
+  half8v x[2][C][2];
+  f32x4 scale[2];
+  const auto read_scales = [&](int c, int step) __attribute__((always_inline)) {
+    scale[0] = s_d[c & 1][step * 8 + q * 2];
+    scale[1] = s_d[c & 1][step * 8 + q * 2 + 1];
+  };
+  const auto convert = [&](int u, int c) __attribute__((always_inline)) {
+    u32x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float d0 = scale[i >> 1][2 * (i & 1)], d1 = scale[i >> 1][2 * (i & 1) + 1];
+      uint32_t h, l;
+      if constexpr (WIDE) {
+        const u32x4 &g = grad[c][(i >> 1) % GL];
+        scaled_parts(__uint_as_float(g[2 * (i & 1)]) * power[c], __uint_as_float(g[2 * (i & 1) + 1]) * power[c], d0, d1, h, l);
+      } else {
+        const half2v g = __builtin_bit_cast(half2v, static_cast<uint32_t>(grad[c][0][i]));
+        scaled_parts(g[0], g[1], d0, d1, h, l);
+      }
+      hi[i] = h;
+      lo[i] = l;
+    }
+    x[u][c][0] = __builtin_bit_cast(half8v, hi);
+    x[u][c][1] = __builtin_bit_cast(half8v, lo);
   };
   // The thread's group and four rows of each chunk: fields and entries of two rows at a time, weights, and both pairs
-  // of rows to operand [quad / 8][wave % H][column], lane 16 ((quad % 8) / 2) + n, half quad % 2.
-  const int group = (half0 + wave % H) * 16 + n, quad = (wave / H) * 4 + q;
+  // of rows to operand [quad / 8][half][column], lane 16 ((quad % 8) / 2) + n, half quad % 2.
+  const int group = (wave & 1) * 16 + n, quad = (wave >> 1) * 4 + q;
   Fields f[2];
   uint4 e[2];
-  uint32_t hi[4][4], lo[4][4];
+  uint32_t wv[4][4];
+  int last = 0;  // of the rows in `f`'s chunk
   const int odd0 = static_cast<int>(reinterpret_cast<uintptr_t>(p0)) & 2, odd1 = static_cast<int>(reinterpret_cast<uintptr_t>(p1)) & 2;
   const auto read_rows = [&](int c, int j0, int buf) __attribute__((always_inline)) {
     bool second;
     const int64_t row0 = chunk_of(c, second);
-    const int most = static_cast<int>(min(A.rows - 1 - row0, static_cast<int64_t>(63)));
+    last = static_cast<int>(min(A.rows - 1 - row0, static_cast<int64_t>(63)));
     const int step = static_cast<int>(rowbytes) & 2, odd = second ? odd1 : odd0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = quad * 4 + j0 + j, half = ((min(r, most) << 1) & step) ^ odd;  // the block's address modulo four
+      const int r = quad * 4 + j0 + j, half = ((min(r, last) << 1) & step) ^ odd;  // the block's address modulo four
       f[j] = read_fields<F>(reinterpret_cast<const uint8_t *>(&s_raw[buf][r * W]) + half, group, half);
     }
   };
@@ -207,191 +258,171 @@ __global__ void __launch_bounds__(256 * H, H) rows_kernel(RowsArgs A) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) e[j] = s_tab[f[j].k];
   };
-  const auto weigh = [&](int j0) __attribute__((always_inline)) {
+  const int ed = scale_exponent(A.B), shift = codebook_shift(A.B);
+  const _Float16 shrink = static_cast<_Float16>(ldexpf(1.0f, -shift));
+  const auto weigh = [&](int c, int j0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) whole_weights<F, P>(f[j], e[j], unit, hi[j0 + j], lo[j0 + j]);
+    for (int j = 0; j < 2; ++j) row_weights<F>(f[j], e[j], half2v{shrink, shrink}, wv[j0 + j]);
+    if (group == 0) {  // zeros past the last row, whose scale need not be finite
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float d = f16_bits_to_f32(static_cast<uint16_t>(f[j].d16)) * (Geo<F>::IQ1 ? 1.0f : 0.125f);
+        reinterpret_cast<float *>(s_d[c & 1])[quad * 4 + j0 + j] = quad * 4 + j0 + j <= last ? ldexpf(d, -ed) : 0.0f;
+      }
+    }
   };
   const auto put = [&](int c) __attribute__((always_inline)) {
-    uint2 *to = reinterpret_cast<uint2 *>(s_b[c & 1][quad / 8]) +
-                ((wave % H) * 8 * P * 64 + (quad % 8) / 2 * 16 + n) * 2 + quad % 2;
+    uint2 *to = reinterpret_cast<uint2 *>(s_b[c & 1][quad / 8]) + ((wave & 1) * 8 * 64 + (quad % 8) / 2 * 16 + n) * 2 + quad % 2;
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // column p + 4 k
         const uint32_t sel = k ? 0x07060302u : 0x05040100u;
-#pragma unroll
-        for (int part = 0; part < P; ++part) {
-          const uint32_t(&v)[4][4] = part ? lo : hi;
-          to[((p + 4 * k) * P + part) * 128] = make_uint2(__builtin_amdgcn_perm(v[1][p], v[0][p], sel),
-                                                          __builtin_amdgcn_perm(v[3][p], v[2][p], sel));
-        }
+        to[(p + 4 * k) * 128] = make_uint2(__builtin_amdgcn_perm(wv[1][p], wv[0][p], sel),
+                                           __builtin_amdgcn_perm(wv[3][p], wv[2][p], sel));
       }
   };
-  constexpr int G = P == 1 ? 4 : 2, NG = 8 / G;  // columns whose operands are read together
-  half8v x[2][C][P], w[2][G][P];
-  const auto read_x = [&](int u, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int p = 0; p < P; ++p) x[u][c][p] = __builtin_bit_cast(half8v, s_a[buf][((wt * C + c) * P + p) * 64 + lane]);
-  };
+  constexpr int G = C == 1 && !F32 ? 4 : 2, NG = 16 / G;  // columns whose weights are read together
+  half8v w[2][G];
   const auto read_w = [&](int u, int g, int c, int step) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < G; ++j)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        w[u][j][p] = __builtin_bit_cast(half8v, s_b[c & 1][step][((wh * 8 + g * G + j) * P + p) * 64 + lane]);
+    for (int j = 0; j < G; ++j) w[u][j] = __builtin_bit_cast(half8v, s_b[c & 1][step][(g * G + j) * 64 + lane]);
   };
 
-  f32x4 acc[8][C], part[P == 2 ? 8 : 1][C];
+  f32x4 acc[2][8][C], part[F32 ? 16 : 1][C];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 16; ++j)
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[j][c] = part[j % (P == 2 ? 8 : 1)][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  int a0 = 0;  // the buffer of the stage's gradients
-  const auto buffer = [&](int ahead) __attribute__((always_inline)) {
-    const int b = a0 + ahead;
-    return b >= NA ? b - NA : b;
-  };
-  int r1 = 1 % NB, r2 = 2 % NB;  // the buffers of the payload of chunks c + 1 and c + 2
-  const char *g1 = gbase + (count > 1 ? gchunk : 0), *g2 = g1 + (count > 2 ? gchunk : 0);  // their gradients; past the last its
+    for (int c = 0; c < C; ++c) acc[j >> 3][j & 7][c] = part[F32 ? j : 0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int r1 = 1, r2 = 2;  // the buffers of the payload of chunks c + 1 and c + 2
+  const char *g1 = gbase + (count > 1 ? gchunk : 0);  // the gradients of chunk c + 1; past the last its
   const auto stage = [&](auto step, int c) __attribute__((always_inline)) {
     constexpr int U = decltype(step)::value;
     const int next = c + 1 + U;  // the chunk whose rows are decoded in this stage
     read_rows(next, U ? 0 : 2, U ? r2 : r1);
+    if (U == 1 && more) fetch_raw(c + 4, r1);  // chunk c + 1's is decoded
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      constexpr int first = U * NG;  // groups alternate between two sets of registers
-      if (g + 1 < NG) {
-        read_w((first + g + 1) & 1, g + 1, c, U);
-      } else {  // the next stage's first
-        read_x(U ^ 1, buffer(1));
-        read_w((first + g + 1) & 1, 0, c + U, U ^ 1);
-      }
+      if (g + 1 < NG)
+        read_w((g + 1) & 1, g + 1, c, U);
+      else  // the next stage's first
+        read_w(0, 0, c + U, U ^ 1);
       __builtin_amdgcn_sched_barrier(0);
-      if (g + 1 == NG) {
-        weigh(U ? 0 : 2);
-        if (U == 0) put(next);
-      }
+      if (g == NG / 4) weigh(next, U ? 0 : 2);
+      if (g == NG / 2 - 1 && U == 0) put(next);
+      if (g == NG - C - 1) read_scales(c + U, U ^ 1);
+      if (g >= NG - C) convert(U ^ 1, g - (NG - C));
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
         for (int cc = 0; cc < C; ++cc) {
-          f32x4 &to = P == 2 ? part[(g * G + j) % (P == 2 ? 8 : 1)][cc] : acc[g * G + j][cc];
-          const half8v(&ww)[P] = w[(first + g) & 1][j];
-          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][0], ww[0], to, 0, 0, 0);
-          if (P == 2) {
-            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][P - 1], ww[0], to, 0, 0, 0);
-            to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][0], ww[P - 1], to, 0, 0, 0);
-          }
+          const int col = g * G + j;
+          f32x4 &to = F32 ? part[F32 ? col : 0][cc] : acc[col >> 3][col & 7][cc];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) to = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[U][cc][p], w[g & 1][j], to, 0, 0, 0);
         }
       __builtin_amdgcn_sched_barrier(0);
       if (g == 0) {
         look_up();
-        fetch(NA == 3 || U == 0 ? g1 : g2, NA == 3 ? U : U ^ 1, buffer(NA - 1));
-        if (U == 1) fetch_raw(c + NA, r1);  // chunk c + 1's is decoded
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (P == 2 && U == 1 && ((c & 3) == 3 || c + 1 == count)) {
+    load_grads(g1, U);
+    if (F32 && U == 1 && ((c & 3) == 3 || c + 1 == count)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 16; ++j)
 #pragma unroll
         for (int cc = 0; cc < C; ++cc) {
-          f32x4 &p = part[j % (P == 2 ? 8 : 1)][cc];
-          acc[j][cc] += p;
+          f32x4 &p = part[F32 ? j : 0][cc];
+          acc[j >> 3][j & 7][cc] += p;
           p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
     }
-    // What the stage after the next needs has to be there.  Four buffers: the gradients requested a stage ago, so that
-    // those of this stage and a payload requested since may be on their way (as many as the wave has: with more allowed,
-    // the end of an earlier payload could be among them); three: the gradients of this stage, but not a payload requested
-    // after them.
-    if (NA == 4 && (NP % NW == 0 || wave < NP % NW))
-      wait_loads<NPW + NR>();
-    else if (NA == 4)
-      wait_loads<NPW - 1 + NR>();
-    else if (U == 1)
-      wait_loads<NR>();
-    else
-      wait_loads<0>();
+    // The payload of chunk c + 2, which the next stage reads, has to be there; of what was requested after it the newest
+    // may be on its way: chunk c + 3's payload and this stage's gradients.
+    if (U == 0 && more) wait_loads<C * GL + NR>();
     __syncthreads();
-    a0 = buffer(1);
     if (U == 1) {
-      const int next2 = r2 + 1 == NB ? 0 : r2 + 1;
       r1 = r2;
-      r2 = next2;
-      g1 = g2;
-      if (c + 3 < count) g2 += gchunk;
+      r2 = r2 + 1 == NB ? 0 : r2 + 1;
+      if (c + 2 < count) g1 += gchunk;
     }
   };
   if (count) {
     fetch_raw(0, 0);
-    fetch_raw(1, 1 % NB);
-#pragma unroll
-    for (int s = 0; s < NA - 1; ++s) fetch(s < 2 ? gbase : g1, s & 1, s);
+    if (count > 1) fetch_raw(1, 1);
+    if (count > 2) fetch_raw(2, 2);
+    load_grads(gbase, 0);
+  }
+  load_table<F>(s_tab, A.tab);
+  if (count) {
     wait_loads<0>();
     __syncthreads();
     read_rows(0, 0, 0);
     look_up();
-    weigh(0);
+    weigh(0, 0);
     read_rows(0, 2, 0);
     look_up();
-    weigh(2);
+    weigh(0, 2);
     put(0);
-    read_rows(1, 0, 1 % NB);
+    read_rows(1, 0, 1);  // of a single chunk there is none: what lies there is decoded, and not used
     look_up();
-    weigh(0);
+    weigh(1, 0);
     __syncthreads();  // chunk 0 is there, its payload read
-    for (int c = 2; c < NA; ++c) fetch_raw(c, c % NB);
-    wait_loads<0>();
-    __syncthreads();
-    read_x(0, 0);
+    if (more) fetch_raw(3, 0);
+    read_scales(0, 0);
+#pragma unroll
+    for (int c = 0; c < C; ++c) convert(0, c);
+    load_grads(gbase, 1);
     read_w(0, 0, 0, 0);
     // Of a SIMD's two waves the first goes first: while it works on its addresses the other has the matrix cores.
-    if (wave < NW / 2) __builtin_amdgcn_s_setprio(1);
+    if (wave < 4) __builtin_amdgcn_s_setprio(1);
     for (int c = 0; c < count; ++c) {
       stage(std::integral_constant<int, 0>{}, c);
       stage(std::integral_constant<int, 1>{}, c);
     }
     wait_loads<0>();  // none is on its way to memory that another workgroup may be given
   }
-  // tokens 4 q + k of tile c, columns 8 n + j of the wave's half
-  const int64_t col = cb * 256 + (half0 + wh) * 128 + 8 * n, tw = tt0 + wt * C;
+  // tokens 4 q + k of tile c, columns 8 n + j of either half
+  const int64_t tw = tt0 + wave * C;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int4 e4 = *reinterpret_cast<const int4 *>(A.G.ex + min((tw + c) * 16 + q * 4, A.G.ntile * 16 - 4));
-    const int ex[4] = {e4.x, e4.y, e4.z, e4.w};
+    const uint4 e4 = *reinterpret_cast<const uint4 *>(A.G.most + min((tw + c) * 16 + q * 4, A.G.ntile * 16 - 4));
+    const uint32_t most[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 16; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[j][c][k] = ldexpf(acc[j][c][k], ex[k] + ew - 15);
+      for (int k = 0; k < 4; ++k) acc[j >> 3][j & 7][c][k] = ldexpf(acc[j >> 3][j & 7][c][k], ed + shift - grad_power(most[k], WIDE));
   }
-  if (LORA && split == 0) add_adapters<P, C>(A, tw, col, acc);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int64_t t0 = (tw + c) * 16 + q * 4;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t col = cb * 256 + h * 128 + 8 * n;
+    if (LORA && split == 0) add_adapters<F32, C>(A, tw, col, acc[h]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (t0 + k >= A.T) continue;
-      float v[8];
+    for (int c = 0; c < C; ++c) {
+      const int64_t t0 = (tw + c) * 16 + q * 4;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[j][c][k];
-      if (whole)
-        store8u(A.out, P == 1, (t0 + k) * cols + col, v);
-      else
-        store8u(A.partial + (rest * TA * 16 + t0 + k - tt0 * 16) * (128 * H), 0, wh * 128 + 8 * n, v);
+      for (int k = 0; k < 4; ++k) {
+        if (t0 + k >= A.T) continue;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = acc[h][j][c][k];
+        if (whole)
+          store8u(A.out, !F32, (t0 + k) * cols + col, v);
+        else
+          store8u(A.partial + (rest * TA * 16 + t0 + k - tt0 * 16) * 256, 0, h * 128 + 8 * n, v);
+      }
     }
   }
 }
 
 // The splits' sums, in their order: a workgroup has 2,048 values of one tile of the rest.  Bound by memory: 64 tiles in 4
 // splits 13 us (67 MB read, half of it from caches), 26 splits of 19 tokens' 5, a load's latency four times.
-template <int P> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs A) {
-  constexpr int width = P == 2 ? 128 : 256;
+template <bool F32> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs A) {
+  constexpr int width = 256;
   const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * width, per = size / 2048;
   const int64_t rest = blockIdx.x / per, i = blockIdx.x % per * 2048 + threadIdx.x * 8;
-  const int64_t place = A.plan.full + rest, t = place / A.plan.across * A.plan.tiles * 16 + i / width;
+  const int64_t place = A.plan.full + rest, t = place / A.nb * A.plan.tiles * 16 + i / width;
   if (t >= A.T) return;
   const float *from = A.partial + rest * A.plan.splits * size + i;
   float v[8] = {};
@@ -406,7 +437,7 @@ template <int P> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArg
       for (int j = 0; j < 8; ++j)
         if (s0 + s < A.plan.splits) v[j] += w[s][j];
   }
-  store8u(A.out, P == 1, t * A.nb * 256 + place % A.plan.across * width + i % width, v);
+  store8u(A.out, !F32, t * A.nb * 256 + place % A.nb * width + i % width, v);
 }
 
 // An empty sum's result (a fill by the runtime is no kernel, and would enter a captured graph as another node).
@@ -415,42 +446,42 @@ __global__ void __launch_bounds__(256) zero_kernel(uint16_t *p, size_t n) {
     p[i] = 0;
 }
 
-template <int F, int P, int C, int H, bool LORA> void launch_tile(const RowsArgs &A, hipStream_t stream) {
-  hipLaunchKernelGGL((rows_kernel<F, P, C, H, LORA>),
-                     dim3(static_cast<unsigned>(A.plan.full + A.plan.rest * A.plan.splits)), dim3(256 * H), 0, stream, A);
+template <int F, bool WIDE, int C, bool F32, bool LORA> void launch_tile(const RowsArgs &A, hipStream_t stream) {
+  hipLaunchKernelGGL((rows_kernel<F, WIDE, C, F32, LORA>),
+                     dim3(static_cast<unsigned>(A.plan.full + A.plan.rest * A.plan.splits)), dim3(512), 0, stream, A);
 }
 
-template <int F, bool LORA> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t stream) {
-  if (dtype == IQ_DTYPE_F32) return launch_tile<F, 2, (Geo<F>::N > 1024 ? 1 : 2), 1, LORA>(A, stream);
-  if (A.plan.tiles == 4) return launch_tile<F, 1, 1, 2, LORA>(A, stream);
-  if (A.plan.tiles == 8) return launch_tile<F, 1, 2, 2, LORA>(A, stream);
-  if (A.plan.tiles == 12) return launch_tile<F, 1, 3, 2, LORA>(A, stream);
-  launch_tile<F, 1, 4, 2, LORA>(A, stream);
+template <int F> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t stream) {
+  if (dtype == IQ_DTYPE_F32)
+    return A.rank ? launch_tile<F, true, 1, true, true>(A, stream) : launch_tile<F, true, 1, true, false>(A, stream);
+  if (A.nmat == 2)  // a gated block's
+    return A.plan.tiles == 8 ? launch_tile<F, true, 1, false, false>(A, stream) : launch_tile<F, true, 2, false, false>(A, stream);
+  if (A.plan.tiles == 8)
+    return A.rank ? launch_tile<F, false, 1, false, true>(A, stream) : launch_tile<F, false, 1, false, false>(A, stream);
+  A.rank ? launch_tile<F, false, 2, false, true>(A, stream) : launch_tile<F, false, 2, false, false>(A, stream);
 }
 
 }  // namespace
 
-// The tiles of 64 to 256 tokens that cost least: whole rounds of them over 256 CUs, and the rest in as many splits of
+// The tiles of 128 or 256 tokens that cost least: whole rounds of them over 256 CUs, and the rest in as many splits of
 // the rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below, from 256 tiles of
-// 88 and of 176 chunks (IQ2_XS; IQ1 within 15%): 155 and 294 us with 64 tokens, 153 and 292 with 128, 194 and 363 with
-// 192, 208 and 413 with 256 (f32: 458 for 176 chunks of 128 tokens by 128 columns, 383 of 64 beside a codebook of
-// 2,048 entries).  A split rest also costs the joining launch's 3 us and the way of its sums there and back (4 TB/s).
-// With 192 tokens as well 5,632 x 5,120 (IQ2_XS) by 1,500 tokens took 128 us, without 150.
-RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) {
+// 88 and of 176 chunks (IQ2_XS; IQ1_S up to 9% less): 241 and 455 us with 128 tokens of fp16 gradients, 253 and 464 of
+// fp32, 267 and 473 for dx in f32; with 256 tokens 317 and 638, and 333 and 686.  A split rest also costs the joining
+// launch's 3 us and the way of its sums there and back (4 TB/s).
+RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide) {
   struct Tile {
     int tiles;
     double chunk;
   };
   const bool f32 = dtype == IQ_DTYPE_F32;
-  constexpr Tile bf16s[4] = {{4, 1.55}, {8, 1.6}, {12, 1.95}, {16, 2.3}};
-  const Tile single = {kCodebook[fmt] > 1024 ? 4 : 8, kCodebook[fmt] > 1024 ? 2.0 : 2.7};
+  const Tile kinds[2] = {{8, f32 ? 2.6 : 2.5}, {16, wide ? 3.9 : 3.6}};
   const int64_t ntile = (T + 15) / 16;
   RowsPlan best{};
   double least = 0.0;
-  for (int k = 0; k < (f32 ? 1 : 4); ++k) {
-    const Tile &tile = f32 ? single : bf16s[k];
-    const int64_t across = cols / (f32 ? 128 : 256), all = across * ((ntile + tile.tiles - 1) / tile.tiles);
-    const int64_t full = all / 256 * 256, rest = all - full, size = static_cast<int64_t>(tile.tiles) * 16 * (f32 ? 128 : 256) * 4;
+  for (int k = 0; k < (f32 ? 1 : 2); ++k) {
+    const Tile &tile = kinds[k];
+    const int64_t all = nb * ((ntile + tile.tiles - 1) / tile.tiles);
+    const int64_t full = all / 256 * 256, rest = all - full, size = static_cast<int64_t>(tile.tiles) * 16 * 256 * 4;
     const double whole = static_cast<double>(full / 256) * (8.0 + static_cast<double>(chunks) * tile.chunk);
     for (int s = 1; s <= 64 && s <= chunks; ++s) {
       if (s > 1 && !rest) break;
@@ -460,7 +491,7 @@ RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype) 
       if (s > 1) us += 3.0 + static_cast<double>(s * rest * size) * 2.0 / 4e6;
       if (!best.tiles || us < least) {
         least = us;
-        best = RowsPlan{tile.tiles, across, s > 1 ? full : all, s > 1 ? rest : 0, s,
+        best = RowsPlan{tile.tiles, s > 1 ? full : all, s > 1 ? rest : 0, s,
                         s > 1 ? static_cast<size_t>(s * rest * size) : 0};
       }
     }
@@ -477,17 +508,17 @@ int launch_zero(void *p, size_t bytes, hipStream_t stream) {
 }
 
 int launch_rows(int fmt, int dtype, const RowsArgs &A, hipStream_t stream) {
-#define CALL(F) A.rank ? launch_fmt<F, true>(dtype, A, stream) : launch_fmt<F, false>(dtype, A, stream)
+#define CALL(F) launch_fmt<F>(dtype, A, stream)
   IQ_BY_FMT(fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
   if (A.plan.rest) {
-    const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * (dtype == IQ_DTYPE_F32 ? 128 : 256);
+    const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * 256;
     const dim3 wgs(static_cast<unsigned>(A.plan.rest * (size / 2048)));
     if (dtype == IQ_DTYPE_F32)
-      hipLaunchKernelGGL(rows_join_kernel<2>, wgs, dim3(256), 0, stream, A);
+      hipLaunchKernelGGL(rows_join_kernel<true>, wgs, dim3(256), 0, stream, A);
     else
-      hipLaunchKernelGGL(rows_join_kernel<1>, wgs, dim3(256), 0, stream, A);
+      hipLaunchKernelGGL(rows_join_kernel<false>, wgs, dim3(256), 0, stream, A);
     if (!run_launched()) return IQ_ERR_HIP;
   }
   return IQ_OK;

@@ -8,18 +8,24 @@
 
 namespace iq {
 
-// Gradients in fp16, for products over rows: g16 [chunk of 64 rows][tile of 16
-// tokens][part][step of 32 rows][lane][8], the A operand of a step (rows in their
-// order) as 1 KiB of consecutive memory; ex [tokens] as in Tokens.  Rows past the
-// last of a weight are zeros, tokens past the last are left unwritten.
+// Gradients for products over rows: g [chunk of 64 rows][tile of 16 tokens][step of 32 rows][lane][8], rows in their
+// order, lane 16 q + n with token n and rows 8 q on.  bf16 gradients of a caller are fp16 under a power of two a token
+// (grad_power; exact, in steps of 2^-39 of a token's largest), others fp32 as they are, whose lanes' first four rows come
+// before all lanes' other four: a lane's loads of 16 bytes are 1 KiB in a row for the wave.  most [tokens]: the fp32 bits
+// of the largest finite magnitude.  Rows past the last of a weight are zeros, tokens past the last are left unwritten.
 struct Grads {
-  _Float16 *g16;
-  int32_t *ex;
+  void *g;
+  uint32_t *most;
   int64_t ntile;
 };
+// The power of two that brings a token's gradients under 2^15 (wide: as a factor, which has to be a number).
+__host__ __device__ inline int grad_power(uint32_t most, bool wide) {
+  const int n = 141 - (static_cast<int>(most >> 23) > 1 ? static_cast<int>(most >> 23) : 1);
+  return wide && n > 126 ? 126 : n;
+}
 __host__ __device__ inline int64_t row_chunks(int64_t rows) { return (rows + 63) / 64; }
-inline size_t grads_bytes(int64_t chunks, int64_t ntile, int dtype) {
-  return static_cast<size_t>(chunks) * ntile * (dtype == IQ_DTYPE_F32 ? 2 : 1) * 2048;
+inline size_t grads_bytes(int64_t chunks, int64_t ntile, bool wide) {
+  return static_cast<size_t>(chunks) * ntile * (wide ? 4096 : 2048);
 }
 
 // What bounds a payload's weights, found by a preparing launch: the largest finite
@@ -47,13 +53,12 @@ inline int source_parts(const Source &s) { return s.ex || s.dtype == IQ_DTYPE_BF
 // dx of gradients G with one or two encoded weights of the same size (see iq_rows.hip).  The workgroups' tiles of dx:
 // the first `full` whole, of the others the rows split, whose sums a second launch adds.
 struct RowsPlan {
-  int tiles;       // of 16 tokens, in a workgroup's tile
-  int64_t across;  // tiles of dx beside each other
+  int tiles;  // of 16 tokens, in a workgroup's tile, which is a block of columns wide
   int64_t full, rest;
   int splits;
-  size_t bytes;    // of the rest's partial sums
+  size_t bytes;  // of the rest's partial sums
 };
-RowsPlan plan_rows(int fmt, int64_t T, int64_t cols, int64_t chunks, int dtype);
+RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide);
 struct RowsArgs {
   const uint8_t *packed[2];
   int nmat;
@@ -62,7 +67,7 @@ struct RowsArgs {
   Grads G;
   Bound B;
   void *out;
-  float *partial;  // [tile of the rest][split][16 tiles tokens][128 or 256 columns]
+  float *partial;  // [tile of the rest][split][16 tiles tokens][256 columns]
   RowsPlan plan;
   // adapters (rank 0: none): A, p of the tokens (f32: [rank][tpad]; bf16: three values that add up to it, [tile of 16
   // tokens][32 ranks][3][lane][8]), their adapters (-1: none),
@@ -101,6 +106,21 @@ __device__ __forceinline__ void store8u(void *y, int dtype, int64_t i, const flo
   } else {
     __builtin_memcpy(static_cast<float *>(y) + i, v, 32);
   }
+}
+
+// The larger of `most` and a value's magnitude, as fp32 bits; infinities and NaN are passed over.
+__device__ __forceinline__ uint32_t max_bits(uint32_t most, float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? max(most, b) : most;
+}
+
+// Eight rows of one token's gradients (fp32), chunk0 chunks into G; row a multiple of eight.
+__device__ __forceinline__ void put_grads(const Grads &G, int64_t chunk0, int64_t t, int64_t row, const float (&v)[8]) {
+  const int in = static_cast<int>(row & 63);
+  float *to = static_cast<float *>(G.g) + ((chunk0 + (row >> 6)) * G.ntile + (t >> 4)) * 1024 + (in >> 5) * 512 +
+              (((in & 31) >> 3) * 16 + (t & 15)) * 4;
+  *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4 *>(to + 256) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
 // Eight codes of one block times 2^n; -128 to NaN.  A code plus 128 is a byte, which converts in one instruction.
@@ -239,18 +259,20 @@ __device__ __forceinline__ void bound_codebook(const Codebooks &C, const Bound &
   workgroup_max<8>(most, red, B.grid + wg);
 }
 
-// An e with |weight| < 2^e for every finite weight the payloads can hold, and d * m
-// under it as well (a codebook below one does not lower it).
-__device__ __forceinline__ int weight_exponent(const Bound &B) {
+// An e with |d| < 2^e for every finite block scale (with IQ2's 2^-3) of the payloads.
+__device__ __forceinline__ int scale_exponent(const Bound &B) {
+  const uint32_t d = wave_max_u32(B.scale[threadIdx.x & 63]);
+  const float f = f16_bits_to_f32(static_cast<uint16_t>(d)) * (B.iq1 ? 1.0f : 0.125f);
+  return f > 0.0f ? static_cast<int>(__float_as_uint(f) >> 23) - 126 : 0;
+}
+
+// The power of two to take off m v so that the largest a codebook can form stays under 2^15: 0 for all that fp16 holds
+// with a bit to spare, which the layouts' own are far below.
+__device__ __forceinline__ int codebook_shift(const Bound &B) {
   const int lane = threadIdx.x & 63;
-  static_assert(kScaleSlots == 64, "one a lane");
-  const uint32_t d = wave_max_u32(B.scale[lane]);
-  const uint32_t g = wave_max_u32(lane < B.ngrid ? B.grid[lane] : 0u);
-  const float df = f16_bits_to_f32(static_cast<uint16_t>(d));
-  const float v = fmaxf(__uint_as_float(g) + (B.iq1 ? 0.125f : 0.0f), 1.0f), m = (B.iq1 ? 15.0f : 31.0f * 0.125f) * v;
-  // a codebook near the end of fp32 would pass it: fp16 operands end long before
-  const float w = fminf(df * fminf(m, 1e30f), 1e30f);
-  return w > 0.0f ? static_cast<int>(__float_as_uint(w * 1.0001f) >> 23) - 126 : 0;
+  const float g = __uint_as_float(wave_max_u32(lane < B.ngrid ? B.grid[lane] : 0u));
+  const float most = B.iq1 ? 15.0f * (g + 0.125f) : 31.0f * g;
+  return min(max(static_cast<int>(__float_as_uint(most) >> 23) - 126 - 15, 0), 10);
 }
 
 // The fields of group g, from a block in LDS, `half` bytes (0 or 2) behind an address that is a multiple of four.
@@ -298,48 +320,24 @@ template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *bl
   return f;
 }
 
-// Whole weights of a group times 2^s as fp16, e its codebook entry: hi[p] holds values p (low half) and p + 4; lo
-// (P == 2) what they leave.  s: for IQ2 without the 2^-3 of its weights.
-template <int F, int P>
-__device__ __forceinline__ void whole_weights(const Fields &f, const uint4 &e, int s, uint32_t (&hi)[4],
-                                              uint32_t (&lo)[4]) {
-  const uint32_t o[4] = {e.x, e.y, e.z, e.w};
-  uint32_t t = 0;
-  if (!Geo<F>::IQ1) t = sign_places<F>(f.mask);
-  if (P == 1) {
-    // d 2^s has d's bits (steps of 2^-24 below 2^-14), d m is rounded to fp16
-    const _Float16 d = __builtin_amdgcn_ldexph(__builtin_bit_cast(_Float16, static_cast<uint16_t>(f.d16)), s);
-    const half2v m2 = multiplier2(f.ls) * half2v{d, d};
-    if (Geo<F>::IQ1) {
-      const half2v up = m2 * static_cast<_Float16>(0.125f);
-      const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (f.h * 0x80008000u));
+// m v of a group, e its codebook entry, times `shrink` (a power of two): w[p] holds values p (low half) and p + 4.
+template <int F>
+__device__ __forceinline__ void row_weights(const Fields &f, const uint4 &e, half2v shrink, uint32_t (&w)[4]) {
+  const uint32_t o[4] = {e.x, e.y, e.z, e.w}, sum = f.ls * 0x20002u + 0x64016401u;  // as in multiplier2
+  const half2v m2 = __builtin_elementwise_fma(__builtin_bit_cast(half2v, sum), shrink, shrink * static_cast<_Float16>(-1024.0f));
+  if (Geo<F>::IQ1) {
+    const half2v up = m2 * static_cast<_Float16>(0.125f);
+    const half2v c2 = __builtin_bit_cast(half2v, __builtin_bit_cast(uint32_t, up) ^ (f.h * 0x80008000u));
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        hi[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
-    } else {
-#pragma unroll
-      for (int p = 3; p >= 0; --p) {
-        const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
-        hi[p] = __builtin_bit_cast(uint32_t, v) ^ (t & 0x80008000u);
-        asm("v_add_u32 %0, %0, %0" : "+v"(t));
-      }
-    }
+    for (int p = 0; p < 4; ++p)
+      w[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, o[p]), m2, c2));
   } else {
-    const float dm = ldexpf(f16_bits_to_f32(static_cast<uint16_t>(f.d16)), s) * static_cast<float>(2 * f.ls + 1);
-    const float c = Geo<F>::IQ1 ? (f.h ? -0.125f : 0.125f) : 0.0f;
+    uint32_t t = sign_places<F>(f.mask);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const half2v v = __builtin_bit_cast(half2v, o[p]);
-      half2v a, b;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float w = (static_cast<float>(v[k]) + c) * dm;
-        if (!Geo<F>::IQ1) w = __uint_as_float(__float_as_uint(w) ^ (((t >> (12 + p + 4 * k)) & 1u) << 31));
-        a[k] = static_cast<_Float16>(w);
-        b[k] = finite_f(w) ? static_cast<_Float16>(w - static_cast<float>(a[k])) : static_cast<_Float16>(0.0f);
-      }
-      hi[p] = __builtin_bit_cast(uint32_t, a);
-      lo[p] = __builtin_bit_cast(uint32_t, b);
+    for (int p = 3; p >= 0; --p) {
+      const half2v v = __builtin_bit_cast(half2v, o[p]) * m2;
+      w[p] = __builtin_bit_cast(uint32_t, v) ^ (t & 0x80008000u);
+      asm("v_add_u32 %0, %0, %0" : "+v"(t));
     }
   }
 }

@@ -13,19 +13,13 @@
  *
  * Arithmetic.  Products over a weight's columns (g, u below) are iq_linear's:
  * exact fp16 operands, fp32 sums, the block scale applied in fp32.  Products
- * over its rows (dx) cannot take a block's scale out of the sum, so there the
- * whole weight d * m * v is an fp16 operand, under one power of two that brings
- * the largest weight a codebook and the payload's block scales can form under
- * 2^15:
- *  - bf16: d * m is rounded to fp16, its product with v again (relative 2^-11
- *    each at most; weights 2^-29 and more below the largest in steps of 2^-39
- *    of it);
- *  - f32: the weight is the sum of two fp16 values (exact for d * m * v of up
- *    to 22 bits, as the layouts' codebooks form).
- * A gradient is scaled by a power of two per token and held in fp16 (bf16
- * gradients given by the caller exactly; what the calls form themselves to
- * 2^-11), f32 gradients as the sum of two fp16 values (2^-22 of the value), both
- * in steps of 2^-39 of the token's bound at least.  Sums are fp32.
+ * over its rows (dx) cannot take a block's scale d out of the sum, so there d
+ * meets the gradient of its row: their fp32 product is held as the sum of two fp16
+ * values (2^-23 of it, in steps of 2^-39 of the token's largest gradient times the
+ * payload's largest finite scale), and m v is exact in fp16 (a codebook that fp16
+ * does not hold raises IQ_STATUS_ROUNDED).  That holds for bf16 calls as for f32
+ * ones: what a call forms on the way (g, u, the gradients by them, p and v) is fp32,
+ * and bf16 outputs are rounded once.  Sums are fp32.
  * Infinities and NaN in a token reach that token's rows of the outputs, and the
  * gradients of its adapter.
  */
@@ -52,9 +46,10 @@ enum {
  *
  * The exponent is the biased fp32 exponent of the block's largest finite
  * magnitude (at least 1), one more where that magnitude would round to more than
- * 127 (then 127 at the largest exponent, 254); codes are rounded to nearest even, so a value is off by half a unit at
- * most.  An infinity or NaN gets code -128, which iq_restore returns as NaN, and
- * raises IQ_STATUS_NONFINITE.
+ * 127, and codes are rounded to nearest even, so a value is off by half a unit at
+ * most.  The largest exponent, 254, has no further one: there codes end at 127, a
+ * unit from a magnitude that would round to 128.  An infinity or NaN gets code
+ * -128, which iq_restore returns as NaN, and raises IQ_STATUS_NONFINITE.
  *
  *  x          (device) [T, cols] f32 or bf16.
  *  codes      (device) [T, cols] int8 OUT.
@@ -101,10 +96,6 @@ int iq_glu_workspace_size(int fmt, int64_t inter, int64_t hidden, int dtype, int
  *           codes [T, hidden] int8 and exponents [T, hidden/32] of a checkpoint.
  *  dh       (device) [T, inter] of `dtype` (f32 or bf16): the gradient by h.
  *  dx       (device) [T, hidden] OUT, of `dtype`, rounded once.
- * Between the two products dh act'(g) u and dh act(g) are held in fp16 (f32: two
- * values) under one power of two per token that bounds both: 2^31 or less above
- * the largest of them for any weights whose rows and tokens are not concentrated
- * in single values, which leaves 2^-39 of that bound as the step.
  * inter == 0: dx is zeros.  Otherwise as iq_glu. */
 int iq_glu_backward(int fmt, const uint8_t *gate, const uint8_t *up, int64_t inter, int64_t hidden,
                     const float *grid, const void *x, const uint8_t *exponents, const void *dh, int dtype,
