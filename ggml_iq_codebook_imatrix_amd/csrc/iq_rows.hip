@@ -21,6 +21,7 @@
 // come from memory to its registers.  For f32 the sums of four chunks are added to the
 // whole ones, so that fewer additions round at a whole sum's size.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "iq_train.hpp"
@@ -410,19 +411,18 @@ __global__ void __launch_bounds__(512, 2) rows_kernel(RowsArgs A) {
         if (whole)
           store8u(A.out, !F32, (t0 + k) * cols + col, v);
         else
-          store8u(A.partial + (rest * TA * 16 + t0 + k - tt0 * 16) * 256, 0, h * 128 + 8 * n, v);
+          store8u(A.partial + (rest * min(A.T, static_cast<int64_t>(TA * 16)) + t0 + k - tt0 * 16) * 256, 0, h * 128 + 8 * n, v);
       }
     }
   }
 }
 
-// The splits' sums, in their order: a workgroup has 2,048 values of one tile of the rest.  Bound by memory: 64 tiles in 4
+// The splits' sums, in their order: a workgroup has eight tokens of one tile of the rest.  Bound by memory: 64 tiles in 4
 // splits 13 us (67 MB read, half of it from caches), 26 splits of 19 tokens' 5, a load's latency four times.
 template <bool F32> __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs A) {
-  constexpr int width = 256;
-  const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * width, per = size / 2048;
+  const int64_t held = min(A.T, static_cast<int64_t>(A.plan.tiles) * 16), per = (held + 7) / 8, size = held * 256;
   const int64_t rest = blockIdx.x / per, i = blockIdx.x % per * 2048 + threadIdx.x * 8;
-  const int64_t place = A.plan.full + rest, t = place / A.nb * A.plan.tiles * 16 + i / width;
+  const int64_t place = A.plan.full + rest, t = place / A.nb * A.plan.tiles * 16 + i / 256;
   if (t >= A.T) return;
   const float *from = A.partial + rest * A.plan.splits * size + i;
   float v[8] = {};
@@ -437,7 +437,7 @@ template <bool F32> __global__ void __launch_bounds__(256) rows_join_kernel(Rows
       for (int j = 0; j < 8; ++j)
         if (s0 + s < A.plan.splits) v[j] += w[s][j];
   }
-  store8u(A.out, !F32, t * A.nb * 256 + place % A.nb * width + i % width, v);
+  store8u(A.out, !F32, (t * A.nb + place % A.nb) * 256 + i % 256, v);
 }
 
 // An empty sum's result (a fill by the runtime is no kernel, and would enter a captured graph as another node).
@@ -467,35 +467,41 @@ template <int F> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t strea
 // the rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below, from 256 tiles of
 // 88 and of 176 chunks (IQ2_XS; IQ1_S up to 9% less): 241 and 455 us with 128 tokens of fp16 gradients, 253 and 464 of
 // fp32, 267 and 473 for dx in f32; with 256 tokens 317 and 638, and 333 and 686.  A split rest also costs the joining
-// launch's 3 us and the way of its sums there and back (4 TB/s).
+// launch's 3 us and the way of its sums there and back (4 TB/s).  At most kMostSplit workgroups share a rest, two rounds:
+// more would pay in places, and take up to 16,000 tiles of sums.
 RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide) {
   struct Tile {
     int tiles;
     double chunk;
   };
+  constexpr int64_t kMostSplit = 512;
   const bool f32 = dtype == IQ_DTYPE_F32;
   const Tile kinds[2] = {{8, f32 ? 2.6 : 2.5}, {16, wide ? 3.9 : 3.6}};
   const int64_t ntile = (T + 15) / 16;
   RowsPlan best{};
+  size_t most = 0;
   double least = 0.0;
   for (int k = 0; k < (f32 ? 1 : 2); ++k) {
     const Tile &tile = kinds[k];
     const int64_t all = nb * ((ntile + tile.tiles - 1) / tile.tiles);
-    const int64_t full = all / 256 * 256, rest = all - full, size = static_cast<int64_t>(tile.tiles) * 16 * 256 * 4;
+    const int64_t full = all / 256 * 256, rest = all - full, size = std::min(T, static_cast<int64_t>(tile.tiles) * 16) * 256 * 4;
+    const int64_t splits = std::min(chunks, static_cast<int64_t>(64));
+    // what any smaller T could take, so that a workspace for more tokens serves fewer
+    most = std::max(most, static_cast<size_t>(std::min(all * splits, kMostSplit) * size));
     const double whole = static_cast<double>(full / 256) * (8.0 + static_cast<double>(chunks) * tile.chunk);
-    for (int s = 1; s <= 64 && s <= chunks; ++s) {
-      if (s > 1 && !rest) break;
+    for (int s = 1; s <= splits; ++s) {
+      if (s > 1 && (!rest || rest * s > kMostSplit)) break;
       double us = whole;
       if (rest)
         us += static_cast<double>((rest * s + 255) / 256) * (8.0 + static_cast<double>((chunks + s - 1) / s) * tile.chunk);
       if (s > 1) us += 3.0 + static_cast<double>(s * rest * size) * 2.0 / 4e6;
       if (!best.tiles || us < least) {
         least = us;
-        best = RowsPlan{tile.tiles, s > 1 ? full : all, s > 1 ? rest : 0, s,
-                        s > 1 ? static_cast<size_t>(s * rest * size) : 0};
+        best = RowsPlan{tile.tiles, s > 1 ? full : all, s > 1 ? rest : 0, s, 0};
       }
     }
   }
+  best.bytes = most;
   return best;
 }
 
@@ -512,9 +518,9 @@ int launch_rows(int fmt, int dtype, const RowsArgs &A, hipStream_t stream) {
   IQ_BY_FMT(fmt, CALL)
 #undef CALL
   if (!run_launched()) return IQ_ERR_HIP;
-  if (A.plan.rest) {
-    const int64_t size = static_cast<int64_t>(A.plan.tiles) * 16 * 256;
-    const dim3 wgs(static_cast<unsigned>(A.plan.rest * (size / 2048)));
+  if (A.plan.splits > 1) {
+    const int64_t held = std::min(A.T, static_cast<int64_t>(A.plan.tiles) * 16);
+    const dim3 wgs(static_cast<unsigned>(A.plan.rest * ((held + 7) / 8)));
     if (dtype == IQ_DTYPE_F32)
       hipLaunchKernelGGL(rows_join_kernel<true>, wgs, dim3(256), 0, stream, A);
     else

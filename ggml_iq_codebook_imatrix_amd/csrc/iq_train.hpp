@@ -56,7 +56,7 @@ struct RowsPlan {
   int tiles;  // of 16 tokens, in a workgroup's tile, which is a block of columns wide
   int64_t full, rest;
   int splits;
-  size_t bytes;  // of the rest's partial sums
+  size_t bytes;  // at least those of the rest's partial sums; never less for more tokens
 };
 RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide);
 struct RowsArgs {
@@ -67,7 +67,7 @@ struct RowsArgs {
   Grads G;
   Bound B;
   void *out;
-  float *partial;  // [tile of the rest][split][16 tiles tokens][256 columns]
+  float *partial;  // [tile of the rest][split][16 tiles or all tokens, if fewer][256 columns]
   RowsPlan plan;
   // adapters (rank 0: none): A, p of the tokens (f32: [rank][tpad]; bf16: three values that add up to it, [tile of 16
   // tokens][32 ranks][3][lane][8]), their adapters (-1: none),

@@ -8,8 +8,9 @@
  * bits, caller-owned device buffers and workspaces, errors that the host can
  * see before anything is enqueued, asynchronous work on `stream`, payloads at
  * even addresses of which whole aligned 4-byte words are read, outputs that
- * must not overlap inputs, and results that repeat bit for bit (no atomics on
- * results).
+ * must not overlap inputs, and results that repeat bit for bit (no atomics but
+ * for maxima).  A workspace for T tokens serves every smaller T: the sizes that the
+ * queries give do not fall as T grows.
  *
  * Arithmetic.  Products over a weight's columns (g, u below) are iq_linear's:
  * exact fp16 operands, fp32 sums, the block scale applied in fp32.  Products
