@@ -1,9 +1,10 @@
-"""Calls of include/iq_train.h that a training loop makes in passing: one workspace for batches of all sizes."""
+"""Calls of include/iq_train.h that a training loop makes in passing: one workspace for batches of all sizes, weights
+with a scale that is not finite, infinite gradients."""
 import numpy as np
 import pytest
 
 from ggml_iq_codebook_imatrix_amd import inputs
-from test_gpu_run import dev, payload
+from test_gpu_run import FORMATS, decoded, dev, f64, payload
 from test_gpu_train import DTYPES, tokens, upstream
 
 torch = pytest.importorskip("torch")
@@ -44,3 +45,37 @@ def test_one_workspace_serves_smaller_batches(api, dtype):
         for m, w in zip(api.linear_backward(fmt, down, grid, d, workspace=ws, **lora),
                         api.linear_backward(fmt, down, grid, d, **lora)):
             assert torch.equal(m, w) and bool(m.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_an_infinite_scale_stays_infinite(api, orc, fmt, dtype):
+    """An infinite block scale in the last row, which ends inside a chunk: its columns of dx become infinities of the
+    weights' signs, the others keep their values."""
+    print("[case] infinite scale", fmt, dtype, flush=True)
+    rows, nb, T = 70, 3, 9
+    grid, g = inputs.grid_for(fmt, 5), inputs.rng(4)
+    d16 = np.full((rows, nb), 0x2000, np.uint16)
+    clean = payload(fmt, rows, nb, 6, d16=d16)
+    d16[-1, 1] = 0x7c00
+    wild = payload(fmt, rows, nb, 6, d16=d16)
+    dy = g.integers(-3, 4, (T, rows)).astype(np.float32)
+    dy[:, -1] = 1 + np.arange(T) % 2
+    want = f64(api.linear_backward(fmt, dev(clean), dev(grid), dev(dy, dtype)))
+    got = f64(api.linear_backward(fmt, dev(wild), dev(grid), dev(dy, dtype)))
+    sign = np.sign(decoded(orc, fmt, clean, grid)[-1, 256:512])
+    assert np.array_equal(got[:, :256], want[:, :256]) and np.array_equal(got[:, 512:], want[:, 512:])
+    assert np.all(sign != 0) and np.array_equal(got[:, 256:512], np.broadcast_to(sign * np.inf, (T, 256)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_an_infinite_gradient_stays_infinite(api, orc, dtype):
+    print("[case] infinite gradient", dtype, flush=True)
+    fmt, rows, nb, T = "IQ2_XS", 70, 3, 9
+    grid, p = inputs.grid_for(fmt, 5), payload(fmt, rows, nb, 6)
+    dy = upstream(T, rows, 3, dtype)
+    dy[4, 20] = float("-inf")
+    got = f64(api.linear_backward(fmt, dev(p), dev(grid), dy))
+    w = decoded(orc, fmt, p, grid)[20]
+    assert np.all(w != 0) and np.array_equal(got[4], -np.sign(w) * np.inf)
+    assert np.isfinite(np.delete(got, 4, 0)).all()
