@@ -416,9 +416,10 @@ template <int F> __device__ __forceinline__ Entry lookup(const Raw &r, int i, co
 // the decode and the operands' reads in the stage that needs them a call took 1,648 us
 // instead of 1,433.
 //
-// Sums are kept in units of the block's d, as in iq_linear's prompts (P == 1); for
-// f32 tokens a block has sums of its own, which are scaled and added (kept in one sum,
-// 5,120 columns came to 1e-6 of h in the norm, near twice 32-bit arithmetic's).
+// Sums are kept in units of the block's d, as in iq_linear's prompts (P == 1, bf16
+// calls); for f32 tokens a block has sums of its own, which are scaled and added (kept
+// in one sum, 5,120 columns came to 1e-6 of h in the norm, near twice 32-bit
+// arithmetic's).
 // ---------------------------------------------------------------------------
 template <int F, int P, int WT, int WR, int C, int R>
 __global__ void __launch_bounds__(64 * WT * WR, WT * WR / 4) glu_tile_kernel(GluArgs A) {
@@ -702,6 +703,10 @@ template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
   // 167, 4,096 tokens 286 and 244 (f32: 512 tokens 70 and 84, 2,048 tokens 228 and 236); 17,408 x 5,120 (IQ1_M): 512
   // tokens 255 and 335, 1,024 tokens 493 and 522.
   constexpr int C = P == 2 ? 2 : 4;
+  // A checkpoint's tokens in an f32 call want a block's own sums as well.  Tiles of 128 of them took 67 and 410 us for 512
+  // and 4,096 tokens of 5,632 x 2,048 (IQ2_S) where batches, which have them, take 48 and 328; 17,408 x 5,120 (IQ1_M),
+  // 2,048 tokens 1,220 and 975.
+  if (P == 1 && A.dtype == IQ_DTYPE_F32) return launch_batches<F, P, 4>(A, stream);
   int64_t batch = batch_cost(A, 4, 2);
   for (int RT = 4; RT <= 6; RT += 2) batch = min(batch, batch_cost(A, 4, RT));
   const int64_t rounds = ((A.rows + 127) / 128 * ((ntile + 4 * C - 1) / (4 * C)) + 255) / 256;

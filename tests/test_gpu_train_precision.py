@@ -164,3 +164,18 @@ def test_gradients_past_float32_on_the_way(api, act):
         far = api.glu_backward(fmt, gate, up, grid, x, dh * 2.0 ** n, activation=act)
         scaled = torch.linalg.norm(far.double() * 2.0 ** -n - near.double())
         assert bool(scaled <= 2.0 ** -22 * torch.linalg.norm(near.double()))
+
+
+@pytest.mark.parametrize("fmt,inter,nb,T", [("IQ2_XS", 33, 2, 9), ("IQ2_S", 130, 3, 40), ("IQ1_M", 300, 4, 150),
+                                            ("IQ1_S", 1500, 8, 4100), ("IQ2_XXS", 1500, 20, 4100)])
+def test_float32_glu_backward_sums_a_checkpoint_as_its_values(api, fmt, inter, nb, T):
+    """A checkpoint's values have seven bits, so that a call's sums are those of the float32 tokens it stands for, bit
+    for bit, in any kernel: few tokens, batches, tiles."""
+    print("[case] float32 checkpoint", fmt, inter, nb, T, flush=True)
+    grid = dev(inputs.grid_for(fmt, 5))
+    gate, up = dev(payload(fmt, inter, nb, 6)), dev(payload(fmt, inter, nb, 7))
+    x = dev(inputs.activations(T, nb * 256, 1, 2, bf16=False))
+    dh = dev((1e-3 * inputs.rng(3).standard_normal((T, inter))).astype(np.float32))
+    kept = api.checkpoint(x)
+    assert torch.equal(api.glu_backward(fmt, gate, up, grid, kept, dh),
+                       api.glu_backward(fmt, gate, up, grid, api.restore(*kept), dh))
