@@ -195,10 +195,11 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi, int e) {
 }
 
 enum SourceKind { FROM_F32, FROM_BF16, FROM_CHECKPOINT };
-// Bound by the lines its loads touch: tokens' rows lie apart, so that each lane of a load has a line of its own, where the
-// factors in operand order are 1 KiB in a row (when they were not, 108 us instead of 84); and once for each adapter among
-// 32 tokens.  4,096 tokens, 5,120 and 17,408 columns, four adapters of rank 32 in no order: 63 us, where each token's
-// values once, from memory, would take 22.  Sorted by adapter first, which needs a launch's 25 us, it gained nothing.
+// 4,096 tokens, 5,120 and 17,408 columns, four adapters of rank 32: 63 us with an adapter's tokens together, 130 in random
+// order; 2,048 tokens, 2,048 and 5,632 columns, eight adapters of rank 16 24 and 53.  Each token's values once, from
+// memory, would take 22 of the 63.  With the tokens together one slot of eight finds work, 256 workgroups of 2,048, of
+// which the 128 of x A^T are 3.4 times as long as those of dy B; in random order each adapter among 32 tokens goes through
+// their rows again.  Factors in operand order, 1 KiB in a row, made 84 us of 108.
 //
 // 32 tokens (A, two tiles) by 32 ranks (B) of the adapter of token `slot`, K split
 // over the eight waves, each lane 16 columns at a time (64 bytes of a row a load);
@@ -398,9 +399,10 @@ __device__ __forceinline__ int64_t outer_col(const Outer &O, int64_t blk, int m)
 // ranks (B; three bf16 values each).  The tokens in steps of 32 are dealt to the splits and their eight
 // waves; a step whose tokens' adapters cannot be a is passed over, and where all
 // are a none is masked out.  f32 tokens go through the fp32 cores.  4,096 tokens, 5,120
-// and 17,408 columns, four adapters in no order: 49 us, every adapter's workgroups going
-// through all tokens (450 MB, 58 of them from memory); 2,048 tokens, 2,048 and 5,632
-// columns, one adapter 13.  With the next step's loads ahead registers spill: 88 us.
+// and 17,408 columns, four adapters: 47 us with an adapter's tokens together, 149 in
+// random order, where every adapter's workgroups go through all tokens; 2,048 tokens,
+// 2,048 and 5,632 columns, one adapter 13, eight 14 and 45.  With the next step's loads
+// ahead registers spill: 88 us.
 struct OuterMemory {
   f32x4 red[8 * 4 * 64];
   float out[16][132];
@@ -722,7 +724,10 @@ int iq_linear_backward(int fmt, const uint8_t *packed, int64_t rows, int64_t col
     S.tpad = P.tpad;
     S.L = L;
     S.rgroups = (rank + 31) / 32;
-    S.slots = 32;  // as many as are at work at once
+    // Slots as long as workgroups are 1,024 at most, as many as are at work at once.  With 512, 1,024, 2,048 and 4,096, us:
+    // 4,096 tokens, four adapters of rank 32, together 68, 63, 63, 66, in random order 145, 130, 130, 148; 2,048 tokens,
+    // one adapter of rank 16 16, 16, 17, 26, eight in random order 60, 61, 56, 67.
+    S.slots = 32;
     while (S.slots > 1 && (P.tpad >> 5) * 2 * S.rgroups * S.slots > 1024) S.slots /= 2;
     S.ids = ids;
     S.range = range;

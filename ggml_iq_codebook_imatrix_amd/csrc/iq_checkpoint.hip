@@ -3,9 +3,11 @@
 //
 // Bound by memory: a thread takes eight columns, four neighbouring ones a block
 // of 32, whose largest magnitude goes through two lane exchanges.  A tensor
-// whose rows are whole blocks is one long row.  8,192 x 17,408 in bf16: 101 us to
-// keep (432 MB, 4.3 TB/s) and 78 to restore (5.5 TB/s), where a copy reaches 5.1;
-// 37 x 1,001 in f32 6 and 5, a launch's latency.
+// whose rows are whole blocks is one long row.  8,192 x 17,408 in bf16: 97 us to
+// keep (432 MB, 4.4 TB/s) and 72 to restore (5.9 TB/s), f32 161 and 145 (4.5 and 5.0),
+// with six tensors in turn, more than the caches hold, where a copy reaches 5.1 (a
+// restore's codes are fresh from the keeping); the same tensor each time takes as
+// long.  37 x 1,001 in f32 6 and 5, a launch's latency.
 
 #include "iq_train.hpp"
 

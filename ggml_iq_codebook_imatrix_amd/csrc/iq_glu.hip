@@ -40,8 +40,8 @@ struct GluPrepArgs {
 };
 
 // Everything the products want beforehand, a wave a token: 4,096 tokens x 5,120 in bf16 20 us (63 MB, 3.1 TB/s: a token's
-// largest magnitude has to be known before its first value is written); backward 66, which reads dh (143 MB) and the
-// payloads' block scales for their bounds as well.
+// largest magnitude has to be known before its first value is written); backward, of a checkpoint, 36, which reads the
+// payloads' block scales for their bound as well.
 __global__ void __launch_bounds__(512) glu_prep_kernel(GluPrepArgs A) {
   __shared__ uint32_t s_red[8];
   int64_t w = blockIdx.x;
@@ -414,7 +414,7 @@ template <int F> __device__ __forceinline__ Entry lookup(const Raw &r, int i, co
 // product of fp16 reaches 1.20.  Matrix cores are busy 0.43 of the time, LDS 0.33, and
 // the decode issues 297,000 vector instructions a SIMD (0.37); waves wait 0.28.  With
 // the decode and the operands' reads in the stage that needs them a call took 1,648 us
-// instead of 1,433.
+// instead of 1,433.  Backward (IQ1_M) 1,630 to 1,710: it writes both gradients in fp32, 560 MB where h is 140.
 //
 // Sums are kept in units of the block's d, as in iq_linear's prompts (P == 1, bf16
 // calls); for f32 tokens a block has sums of its own, which are scaled and added (kept
@@ -697,6 +697,9 @@ template <int F, int P> void launch_glu(const GluArgs &A, hipStream_t stream) {
   const int64_t ntile = A.X.ntile;
   if (ntile == 1) return launch_split<F, P, 1>(A, stream);
   if (ntile == 2) return launch_batches<F, P, 2>(A, stream);
+  // Three token tiles a workgroup where they leave less of it empty than four, us with two, three and four: 17,408 x
+  // 5,120 (IQ1_M), 48 tokens 57, 42, 46 (f32 91, 55, 65), 80 tokens 82, 73, 82 (122, 101, 139), 96 tokens 81, 72, 80 (119,
+  // 101, 135); 5,632 x 2,048 (IQ2_S) 16, 14, 15, 20, 18, 20 and 20, 18, 21.
   if (ntile == 3 || ntile == 5 || ntile == 6) return launch_batches<F, P, 3>(A, stream);
   // Tiles, a workgroup a CU, take 16 us a round and 7.2 more for each block of columns; batches 0.08 and 0.09 (f32
   // 0.155) of their cost.  5,632 x 2,048 (IQ2_S), batches and tiles, us: 500 tokens 49 and 83, 2,048 tokens 150 and

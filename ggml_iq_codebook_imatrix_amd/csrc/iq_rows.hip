@@ -477,7 +477,7 @@ template <int F> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t strea
 // 88 and of 176 chunks (IQ2_XS; IQ1_S up to 9% less): 241 and 455 us with 128 tokens of fp16 gradients, 253 and 464 of
 // fp32, 267 and 473 for dx in f32; with 256 tokens 317 and 638, and 333 and 686.  A split rest also costs the joining
 // launch's 3 us and the way of its sums there and back (4 TB/s).  At most kMostSplit workgroups share a rest, two rounds:
-// more would pay in places, and take up to 16,000 tiles of sums.
+// beyond that a split rest gains a few percent of a round by this reckoning and would take thousands of tiles of sums.
 RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide) {
   struct Tile {
     int tiles;

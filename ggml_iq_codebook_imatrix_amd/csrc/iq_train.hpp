@@ -285,7 +285,7 @@ template <int F> __device__ __forceinline__ Fields read_fields(const uint8_t *bl
   f.mask = f.h = 0;
   if (F == IQ1_M) {
     // the scale and the shifts as words: with narrow reads, five more, the product of two weights of 17,408 x 5,120 and
-    // 4,096 tokens took 1,555 us instead of 1,370 (the other layouts' fields as words changed nothing)
+    // 4,096 tokens took 2,680 us instead of 2,620 (the other layouts' fields as words changed nothing)
     const uint32_t *w = reinterpret_cast<const uint32_t *>(blk - half + 48);
     const uint32_t w0 = __builtin_amdgcn_alignbyte(w[1], w[0], half), w1 = __builtin_amdgcn_alignbyte(w[2], w[1], half);
     f.d16 = ((w0 >> 12) & 15u) | ((w0 >> 28) << 4) | (((w1 >> 12) & 15u) << 8) | ((w1 >> 28) << 12);
