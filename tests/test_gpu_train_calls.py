@@ -1,11 +1,11 @@
 """Calls of include/iq_train.h that a training loop makes in passing: one workspace for batches of all sizes, weights
-with a scale that is not finite, infinite gradients."""
+with a scale that is not finite, infinite gradients, large codebooks and workspaces."""
 import numpy as np
 import pytest
 
 from ggml_iq_codebook_imatrix_amd import inputs
 from test_gpu_run import FORMATS, decoded, dev, f64, payload
-from test_gpu_train import DTYPES, tokens, upstream
+from test_gpu_train import DTYPES, Block, tokens, upstream
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,34 @@ def test_an_infinite_gradient_stays_infinite(api, orc, dtype):
     w = decoded(orc, fmt, p, grid)[20]
     assert np.all(w != 0) and np.array_equal(got[4], -np.sign(w) * np.inf)
     assert np.isfinite(np.delete(got, 4, 0)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", ["IQ2_XXS", "IQ2_XS", "IQ2_S"])
+def test_a_codebook_of_large_values(api, fmt, dtype):
+    """2,048 times the codebook is 2,048 times the gradient, though its products with the largest multiplier pass fp16."""
+    print("[case] large codebook", fmt, dtype, flush=True)
+    rows, nb, T = 90, 2, 40
+    grid, p = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6, d16=0x1400))
+    dy = upstream(T, rows, 3, dtype)
+    want = api.linear_backward(fmt, p, grid, dy)
+    st = api.new_status()
+    got = api.linear_backward(fmt, p, grid * 2048, dy, status=st)
+    assert float(grid.max()) * 2048 * 31 > 65504 and torch.equal(got, want * 2048)
+    assert api.read_status(st) == api.STATUS_ROUNDED
+
+
+def test_gradients_past_four_gigabytes(api, orc):
+    """A gated block's gradients wait in more than 2^32 bytes of workspace."""
+    fmt, inter, nb, T = "IQ2_XS", 33000, 1, 16400
+    print("[case] gradients past 4 GiB", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    b = Block(orc, fmt, inter, nb, 3)
+    x = torch.randn((T, nb * 256), device="cuda", generator=gen).bfloat16()
+    dh = (torch.randn((T, inter), device="cuda", generator=gen) * 1e-3).bfloat16()
+    assert api.glu_backward_workspace_size(fmt, inter, nb * 256, torch.bfloat16, T) > 1 << 32
+    at = np.r_[0, 17, 8191, 16128, T - 17:T]
+    got = f64(api.glu_backward(*b.args(), x, dh)[at])
+    want, off = b.backward(f64(x[at]), f64(dh[at]), "silu", torch.bfloat16, False)
+    assert np.all(np.abs(got - want) <= off)
+    assert np.linalg.norm(got - want) <= 2.0 ** -8 * np.linalg.norm(want)
