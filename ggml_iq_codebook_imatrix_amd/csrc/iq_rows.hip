@@ -32,7 +32,7 @@ namespace {
 // acc[j][c] += p A of the adapters that the wave's tokens (tiles tt .. tt + C - 1) name, columns col + j of the lane's
 // eight.  32 ranks at a time: a lane has eight ranks of its eight columns, which byte permutations make operands of
 // (bf16; p is the sum of three bf16 values, without a rounding), or four ranks at a time on the fp32 cores.  Rows of
-// tokens with other adapters are zeros; where A is not finite, 0 * A would reach them, and what they give is dropped.
+// tokens with other adapters are zeros; where A is not finite (wild), 0 * A would reach them, and what they give is dropped.
 template <bool F32, int C>
 __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int64_t col, f32x4 (&acc)[8][C]) {
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
@@ -49,9 +49,14 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
       const bool drop = wild[0] | wild[!F32 && r0 + 16 < A.rank ? A.nb : 0];
       if constexpr (!F32) {
         const uint16_t *from = static_cast<const uint16_t *>(A.a) + static_cast<int64_t>(a) * A.rank * cols + col;
-        u32x4 w[8];  // ranks r0 + 8 q + i; past the last p is zero
+        u32x4 w[8];  // ranks r0 + 8 q + i; zeros past the last, as p is there
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = ldu<u32x4>(from + min(r0 + 8 * q + i, A.rank - 1) * cols);
+        if (r0 + 32 > A.rank) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (r0 + 8 * q + i >= A.rank) w[i] = u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const uint32_t tokens = static_cast<uint32_t>(group >> (16 * c)) & 0xffffu;
@@ -72,9 +77,16 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
             u32x4 o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_perm(w[2 * i + 1][j >> 1], w[2 * i][j >> 1], sel);
-            f32x4 d = acc[j][c];
+            f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], __builtin_bit_cast(bf16x8, o), acc[j][c], 0, 0, 0);
+            if (drop) {  // the first part of p has met what is not finite; the others may be zeros
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
+              for (int i = 0; i < 4; ++i) {
+                if ((o[i] & 0x7f80u) == 0x7f80u) o[i] &= 0xffff0000u;
+                if ((o[i] & 0x7f800000u) == 0x7f800000u) o[i] &= 0xffffu;
+              }
+            }
+#pragma unroll
+            for (int k = 1; k < 3; ++k)
               d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[k], __builtin_bit_cast(bf16x8, o), d, 0, 0, 0);
             if (drop) {
 #pragma unroll
@@ -87,6 +99,8 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
       } else {
         float w[8];
         load8u(A.a, 0, (static_cast<int64_t>(a) * A.rank + min(r0 + q, A.rank - 1)) * cols + col, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = r0 + q < A.rank ? w[j] : 0.0f;  // as v is there
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const uint32_t tokens = static_cast<uint32_t>(group >> (16 * c)) & 0xffffu;

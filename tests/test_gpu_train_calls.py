@@ -110,3 +110,33 @@ def test_gradients_past_four_gigabytes(api, orc):
     want, off = b.backward(f64(x[at]), f64(dh[at]), "silu", torch.bfloat16, False)
     assert np.all(np.abs(got - want) <= off)
     assert np.linalg.norm(got - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("r,at", [(5, 4), (5, 1), (40, 39), (40, 32), (64, 63)])
+def test_an_infinity_of_an_adapter_stays_infinite(api, orc, dtype, r, at):
+    """An infinity in A, in the last rank as well: dx of its tokens is infinite in that column with the sign of p A,
+    where p is one bfloat16 value as where it takes three."""
+    print("[case] infinite adapter", dtype, r, at, flush=True)
+    fmt, rows, nb, T, N = "IQ2_XS", 70, 2, 50, 2
+    g = inputs.rng(9)
+    grid, p = dev(inputs.grid_for(fmt, 5)), dev(payload(fmt, rows, nb, 6))
+    x, dy = tokens(T, nb, 3, dtype), g.integers(-3, 4, (T, rows)).astype(np.float32)
+    dy[::2] *= np.float32(1.001)  # more than eight bits, in float32 calls
+    dy = dev(dy, dtype)
+    a = g.standard_normal((N, r, nb * 256), dtype=np.float32)
+    b = g.integers(-1, 2, (N, rows, r)).astype(np.float32)
+    b[1, :, at] = g.standard_normal(rows) if r == 40 else b[1, :, at]
+    a, b = dev(a, dtype), dev(b, dtype)
+    ids = g.integers(-1, N, T).astype(np.int32)
+    run = lambda a: f64(api.linear_backward(fmt, p, grid, dy, x=x, lora_a=a, lora_b=b, lora_ids=dev(ids))[0])  # noqa: E731
+    clean, wild = run(a), a.clone()
+    wild[1, at, 300] = float("-inf")
+    got = run(wild)
+    pr = f64(dy) @ f64(b)[1][:, at]
+    hit = (ids == 1) & (np.abs(pr) > 1e-4)
+    assert hit.sum() > 5
+    assert np.array_equal(got[hit, 300], -np.sign(pr[hit]) * np.inf)
+    keep = np.ones_like(got, bool)
+    keep[ids == 1, 300] = False
+    assert np.array_equal(got[keep], clean[keep])
