@@ -122,9 +122,8 @@ __device__ __forceinline__ void add_adapters(const RowsArgs &A, int64_t tt, int6
   }
 }
 
-// Two gradients times their rows' scales, as the sums of two fp16 values each.  They leave 2^-23 of the product;
-// where it
-// is infinite the second part, inf - inf, becomes a number, which leaves the infinity.
+// Two gradients times their rows' scales, as the sums of two fp16 values each, to 2^-23 of the product; where it is
+// infinite the second value, inf - inf, becomes a number, which leaves the infinity.
 template <class V>
 __device__ __forceinline__ void scaled_parts(V g0, V g1, float d0, float d1, uint32_t &hi, uint32_t &lo) {
   // written as fma, a product and its rounding are one instruction for each half of a register
@@ -490,14 +489,14 @@ template <int F> void launch_fmt(int dtype, const RowsArgs &A, hipStream_t strea
 // the rows as fill a round or do better.  A round is 8 us and per chunk of 64 rows what stands below, from 256 tiles of
 // 88 and of 176 chunks (IQ2_XS; IQ1_S up to 9% less): 241 and 455 us with 128 tokens of fp16 gradients, 253 and 464 of
 // fp32, 267 and 473 for dx in f32; with 256 tokens 317 and 638, and 333 and 686.  A split rest also costs the joining
-// launch's 3 us and the way of its sums there and back (4 TB/s).  At most kMostSplit workgroups share a rest, two rounds:
-// beyond that a split rest gains a few percent of a round by this reckoning and would take thousands of tiles of sums.
+// launch's 3 us and the way of its sums there and back (4 TB/s).  Its sums take 128 MiB at most: over six sizes of weights
+// and up to 9,000 tokens that costs 0.1% of a call by this reckoning (64 MiB 0.7, none would take 327 MB in places).
 RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide) {
   struct Tile {
     int tiles;
     double chunk;
   };
-  constexpr int64_t kMostSplit = 512;
+  constexpr int64_t kMostBytes = int64_t(1) << 27;
   const bool f32 = dtype == IQ_DTYPE_F32;
   const Tile kinds[2] = {{8, f32 ? 2.6 : 2.5}, {16, wide ? 3.9 : 3.6}};
   const int64_t ntile = (T + 15) / 16;
@@ -510,10 +509,10 @@ RowsPlan plan_rows(int64_t T, int64_t nb, int64_t chunks, int dtype, bool wide) 
     const int64_t full = all / 256 * 256, rest = all - full, size = std::min(T, static_cast<int64_t>(tile.tiles) * 16) * 256 * 4;
     const int64_t splits = std::min(chunks, static_cast<int64_t>(64));
     // what any smaller T could take, so that a workspace for more tokens serves fewer
-    most = std::max(most, static_cast<size_t>(std::min(all * splits, kMostSplit) * size));
+    most = std::max(most, static_cast<size_t>(std::min(all * splits * size, kMostBytes)));
     const double whole = static_cast<double>(full / 256) * (8.0 + static_cast<double>(chunks) * tile.chunk);
     for (int s = 1; s <= splits; ++s) {
-      if (s > 1 && (!rest || rest * s > kMostSplit)) break;
+      if (s > 1 && (!rest || rest * s * size > kMostBytes)) break;
       double us = whole;
       if (rest)
         us += static_cast<double>((rest * s + 255) / 256) * (8.0 + static_cast<double>((chunks + s - 1) / s) * tile.chunk);
